@@ -296,10 +296,10 @@ def plain_scale(amax, codes):
 
 
 def plain_codes(y, codes):
-    """Values in units of the scale, as the codes' values (NaN: 0 in int8)."""
+    """Values in units of the scale, as codes (NaN: 0)."""
     if codes == "int8":
         return torch.round(y).nan_to_num(0.0, 127.0, -127.0).clamp(-127, 127).to(torch.int8)
-    return y.clamp(-448, 448).to(torch.float8_e4m3fn)
+    return y.nan_to_num(0.0, 448.0, -448.0).clamp(-448, 448).to(torch.float8_e4m3fn)
 
 
 def plain_write(pool, scale, x, case, s):
@@ -399,7 +399,8 @@ def run_own(s, case):
     import causal_attention_score_gb300 as csa
     if case["op"] == "rotary":
         call = csa.rotary_backward if case["backward"] else csa.rotary_forward
-        call(s["out"], s["x"], s["rotary"], s["positions"], start=case["far"], period=case["period"], interleaved=case["interleaved"])
+        start = case["far"] if s["positions"] is None else 0
+        call(s["out"], s["x"], s["rotary"], s["positions"], start=start, period=case["period"], interleaved=case["interleaved"])
         return s["out"]
     if case["op"] == "cache":
         csa.kv_cache_write(s["cache"], s["batch"], s["k_new"], s["v_new"])
