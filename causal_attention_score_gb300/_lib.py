@@ -23,6 +23,7 @@ CSA_ERR_CUDA = -8
 CSA_ERR_CHECK = -9
 CSA_ERR_WORKSPACE = -10
 CSA_ERR_BUSY = -11
+CSA_ERR_INDEX = -12
 
 CSA_MASK_NAN = 0x7FC00000
 CSA_MASK_NEG_INF = 0xFF800000
@@ -33,6 +34,10 @@ CSA_TRIMUL_LOWER_ONLY = 1
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _u32 = ctypes.c_uint32
+_i64 = ctypes.c_int64
+_f = ctypes.c_float
+_d = ctypes.c_double
+_rotary = [_vp, _vp, _i, _i64, _i, _i, _i, _i64, _i64, _i64, _i64, _vp, _f, _vp, _i, _i, _i, _vp]
 SIGNATURES = {
     "trimul_forward": (_i, [_vp, _vp, _i, _i, _i, _i]),
     "trimul_forward_ex": (_i, [_vp, _vp, _i, _i, _i, _i, _u32, _u32, _vp]),
@@ -48,6 +53,14 @@ SIGNATURES = {
     "dense_xwt_grouped_workspace_size": (_i, [_vp, _vp, _vp, _i, _i, _i,
                                               ctypes.POINTER(ctypes.c_size_t)]),
     "dense_xwt_grouped_ws": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _vp, ctypes.c_size_t, _vp]),
+    "rotary_forward": (_i, _rotary),
+    "rotary_backward": (_i, _rotary),
+    "csa_rotary_turns": (_i, [_vp, _i, _d, _i, _d, _d, _d, _d]),
+    "kv_cache_write": (_i, [_vp, _vp, _vp, _vp, _i, _i64, _i64, _i64, _i64, _vp]),
+    "kv_cache_read": (_i, [_vp, _vp, _i, _i64, _i64, _i64, _i64, _vp, _vp, _vp]),
+    "cache_attention_forward": (_i, [_vp, _vp, _i, _i, _i64, _i64, _i64, _i64, _vp, _vp, _f, _i,
+                                     _i, _vp, ctypes.c_size_t, _vp]),
+    "cache_attention_workspace_size": (_i, [_vp, _i, ctypes.POINTER(ctypes.c_size_t)]),
     "csa_get_status": (_i, [_vp]),
     "csa_status_string": (ctypes.c_char_p, [_i]),
     "csa_last_error": (ctypes.c_char_p, []),

@@ -1,7 +1,6 @@
 // C ABI of libcsa_gb300.so: argument validation, per-device facts, tensor-map
 // encoding through the runtime's driver entry point, and the device status
-// word that bounded waits report into. The compute lives in
-// trimul_sm103a.cu and dense_sm103a.cu.
+// word that bounded waits report into. The compute lives in the *_sm103a.cu files.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -9,6 +8,7 @@
 #include <algorithm>
 #include <atomic>
 #include <chrono>
+#include <cmath>
 #include <condition_variable>
 #include <cstdint>
 #include <cstdlib>
@@ -675,7 +675,9 @@ csa_status csa_get_status(void* stream) {
     const int zero[2] = {0, 0};
     e = cudaMemcpy(dev.status_word, zero, sizeof zero, cudaMemcpyHostToDevice);
     if (e != cudaSuccess) return cuda_error("csa_get_status: clear status", e);
-    t_last_error = "device wait ran out at site " + std::to_string(host[1]);
+    t_last_error = (host[0] == CSA_ERR_INDEX ? "index out of range on the device, site "
+                                             : "device wait ran out at site ") +
+                   std::to_string(host[1]);
     return host[0];
   }
   return CSA_OK;
@@ -695,6 +697,7 @@ const char* csa_status_string(csa_status s) {
     case CSA_ERR_CHECK: return "device-side index check failed (debug build)";
     case CSA_ERR_WORKSPACE: return "workspace missing or too small";
     case CSA_ERR_BUSY: return "work-list counter sets exhausted";
+    case CSA_ERR_INDEX: return "index in device memory out of range";
     default: return "unknown status";
   }
 }
@@ -803,6 +806,284 @@ csa_status csa_set_dense_fetch(int mode) {
     return set_error(CSA_ERR_SHAPE, "csa_set_dense_fetch: unknown mode " + std::to_string(mode));
   g_dense_fetch.store(mode);
   return CSA_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// Elements from the first to the last of [tokens][heads][size] with these strides, or -1
+// where strides are negative or the span overflows.
+long long span_of(long long tokens, int heads, int size, long long token, long long head) {
+  if (token < 0 || head < 0) return -1;
+  const __int128 n = static_cast<__int128>(tokens - 1) * token +
+                     static_cast<__int128>(heads - 1) * head + size;
+  return n > (static_cast<__int128>(1) << 60) ? -1 : static_cast<long long>(n);
+}
+
+// Whether no two rows of [tokens][heads][size] share an element: heads within a token's
+// stride, or tokens within a head's.
+bool rows_apart(long long tokens, int heads, int size, long long token, long long head) {
+  const bool heads_ok = heads == 1 || head >= size, tokens_ok = tokens == 1 || token >= size;
+  if (!heads_ok || !tokens_ok) return false;
+  return tokens == 1 || heads == 1 ||
+         token >= static_cast<long long>(heads - 1) * head + size ||
+         static_cast<__int128>(head) >= static_cast<__int128>(tokens - 1) * token + size;
+}
+
+int rotary(const char* who, const RotaryCall& c, void* stream) {
+  t_last_error.clear();
+  const std::string w(who);
+  if (!c.out || !c.x || !c.turns) return set_error(CSA_ERR_NULL, w + ": null pointer");
+  if (c.dtype != CSA_BF16 && c.dtype != CSA_F16 && c.dtype != CSA_F32)
+    return set_error(CSA_ERR_UNSUPPORTED, w + ": unknown dtype");
+  if (c.tokens <= 0 || c.heads <= 0 || c.head_size < 2)
+    return set_error(CSA_ERR_SHAPE, w + ": tokens, heads must be >= 1, head_size >= 2");
+  if (c.rot_dim < 2 || c.rot_dim % 2 != 0 || c.rot_dim > c.head_size)
+    return set_error(CSA_ERR_SHAPE, w + ": rot_dim must be even, in [2, head_size]");
+  if (!std::isfinite(c.amplitude)) return set_error(CSA_ERR_SHAPE, w + ": amplitude not finite");
+  if (!c.positions) {
+    const long long last = (c.period > 0 ? std::min<long long>(c.tokens, c.period) : c.tokens) - 1;
+    if (c.start < 0 || c.period < 0 || c.start + last > 0x7FFFFFFFll)
+      return set_error(CSA_ERR_SHAPE, w + ": positions must be within [0, 2^31)");
+  } else if (c.start != 0 || c.period != 0) {
+    return set_error(CSA_ERR_UNSUPPORTED, w + ": start and period go with positions = NULL");
+  }
+  const int esize = c.dtype == CSA_F32 ? 4 : 2;
+  if (!aligned(c.out, esize) || !aligned(c.x, esize) || !aligned(c.turns, 8) ||
+      !aligned(c.positions, 4))
+    return set_error(CSA_ERR_ALIGN, w + ": a pointer breaks its type's alignment");
+  const long long nx = span_of(c.tokens, c.heads, c.head_size, c.x_token, c.x_head);
+  const long long no = span_of(c.tokens, c.heads, c.head_size, c.out_token, c.out_head);
+  if (nx < 0 || no < 0) return set_error(CSA_ERR_SHAPE, w + ": bad strides");
+  if (!rows_apart(c.tokens, c.heads, c.head_size, c.out_token, c.out_head))
+    return set_error(CSA_ERR_SHAPE, w + ": rows of the output overlap");
+  if (c.out == c.x) {
+    if ((c.tokens > 1 && c.x_token != c.out_token) || (c.heads > 1 && c.x_head != c.out_head))
+      return set_error(CSA_ERR_UNSUPPORTED, w + ": in place needs equal strides");
+  } else {
+    const uintptr_t x0 = reinterpret_cast<uintptr_t>(c.x), o0 = reinterpret_cast<uintptr_t>(c.out);
+    if (x0 < o0 + static_cast<uintptr_t>(no) * esize && o0 < x0 + static_cast<uintptr_t>(nx) * esize)
+      return set_error(CSA_ERR_UNSUPPORTED, w + ": input and output overlap in part");
+  }
+  DeviceInfo dev;
+  std::string err;
+  int rc = current_device(dev, err);
+  if (rc != CSA_OK) return set_error(rc, err);
+  apply_stream_sm_limit(dev, static_cast<cudaStream_t>(stream));
+  rc = rotary_launch(c, static_cast<cudaStream_t>(stream), dev, err);
+  return rc == CSA_OK ? CSA_OK : set_error(rc, err);
+}
+
+// Checks shared by the cache calls; CSA_OK or the status to return.
+int cache_args_ok(const std::string& w, const csa_kv_cache* c) {
+  if (!c) return set_error(CSA_ERR_NULL, w + ": null cache");
+  if (!c->k || !c->v || !c->k_scale || !c->v_scale)
+    return set_error(CSA_ERR_NULL, w + ": null pointer in the cache");
+  if (c->pages <= 0 || c->heads <= 0 || c->head_size <= 0)
+    return set_error(CSA_ERR_SHAPE, w + ": pages, heads, head_size must be >= 1");
+  if (c->page_tokens != 16 && c->page_tokens != 32 && c->page_tokens != 64 &&
+      c->page_tokens != 128)
+    return set_error(CSA_ERR_UNSUPPORTED, w + ": page_tokens must be 16, 32, 64 or 128");
+  if (c->head_size % 16 != 0)
+    return set_error(CSA_ERR_ALIGN, w + ": head_size must be a multiple of 16");
+  if (c->head_size > 128) return set_error(CSA_ERR_UNSUPPORTED, w + ": head_size > 128");
+  if (c->format != CSA_KV_INT8 && c->format != CSA_KV_E4M3)
+    return set_error(CSA_ERR_UNSUPPORTED, w + ": unknown format");
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) ||
+      !aligned(c->v_scale, 4))
+    return set_error(CSA_ERR_ALIGN, w + ": codes must be 16-byte aligned, scales 4-byte");
+  return CSA_OK;
+}
+
+int batch_args_ok(const std::string& w, const csa_kv_batch* b) {
+  if (!b) return set_error(CSA_ERR_NULL, w + ": null batch");
+  if (!b->offsets || !b->lengths || !b->table)
+    return set_error(CSA_ERR_NULL, w + ": null pointer in the batch");
+  if (b->sequences <= 0 || b->table_width <= 0 || b->rows <= 0 || b->max_new <= 0)
+    return set_error(CSA_ERR_SHAPE, w + ": sequences, table_width, rows, max_new must be >= 1");
+  if (!aligned(b->offsets, 4) || !aligned(b->lengths, 4) || !aligned(b->table, 4))
+    return set_error(CSA_ERR_ALIGN, w + ": the batch's arrays must be 4-byte aligned");
+  return CSA_OK;
+}
+
+// Rows of 16-byte multiples: pointer, strides; and their span.
+int rows_ok(const std::string& w, const void* p, int dtype, long long rows, int heads, int size,
+            long long token, long long head, bool written) {
+  const int per16 = dtype == CSA_F32 ? 4 : 8;
+  if (!aligned(p, 16) || token % per16 != 0 || head % per16 != 0)
+    return set_error(CSA_ERR_ALIGN, w + ": rows must start on 16-byte boundaries");
+  if (span_of(rows, heads, size, token, head) < 0)
+    return set_error(CSA_ERR_SHAPE, w + ": bad strides");
+  if (written && !rows_apart(rows, heads, size, token, head))
+    return set_error(CSA_ERR_SHAPE, w + ": rows of the output overlap");
+  return CSA_OK;
+}
+
+int kv_rows(const char* who, const csa_kv_cache* cache, const csa_kv_batch* batch, KvRows r,
+            bool write, void* stream) {
+  t_last_error.clear();
+  const std::string w(who);
+  int rc = cache_args_ok(w, cache);
+  if (rc == CSA_OK) rc = batch_args_ok(w, batch);
+  if (rc != CSA_OK) return rc;
+  if (!r.x[0] || !r.x[1]) return set_error(CSA_ERR_NULL, w + ": null pointer");
+  if (r.dtype != CSA_BF16 && r.dtype != CSA_F16 && (write || r.dtype != CSA_F32))
+    return set_error(CSA_ERR_UNSUPPORTED, w + ": unknown dtype");
+  for (int i = 0; i < 2; ++i) {
+    rc = rows_ok(w, r.x[i], r.dtype, batch->rows, cache->heads, cache->head_size, r.token[i],
+                 r.head[i], !write);
+    if (rc != CSA_OK) return rc;
+  }
+  DeviceInfo dev;
+  std::string err;
+  rc = current_device(dev, err);
+  if (rc != CSA_OK) return set_error(rc, err);
+  apply_stream_sm_limit(dev, static_cast<cudaStream_t>(stream));
+  rc = kv_cache_launch(*cache, *batch, r, write, static_cast<cudaStream_t>(stream), dev, err);
+  return rc == CSA_OK ? CSA_OK : set_error(rc, err);
+}
+
+int attention_heads_ok(const std::string& w, const csa_kv_cache* cache, int q_heads) {
+  const int rc = cache_args_ok(w, cache);
+  if (rc != CSA_OK) return rc;
+  if (q_heads <= 0 || q_heads % cache->heads != 0)
+    return set_error(CSA_ERR_SHAPE, w + ": q_heads must be a multiple of the cache's heads");
+  return CSA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+csa_status rotary_forward(void* out, const void* x, int dtype, int64_t tokens, int heads,
+                          int head_size, int rot_dim, int64_t out_token_stride,
+                          int64_t out_head_stride, int64_t x_token_stride, int64_t x_head_stride,
+                          const uint64_t* turns, float amplitude, const int32_t* positions,
+                          int start, int period, int interleaved, void* stream) {
+  return rotary("rotary_forward",
+                {x, out, dtype, tokens, heads, head_size, rot_dim, x_token_stride, x_head_stride,
+                 out_token_stride, out_head_stride, turns, positions, start, period, amplitude,
+                 interleaved != 0, 0},
+                stream);
+}
+
+csa_status rotary_backward(void* dx, const void* dy, int dtype, int64_t tokens, int heads,
+                           int head_size, int rot_dim, int64_t dx_token_stride,
+                           int64_t dx_head_stride, int64_t dy_token_stride,
+                           int64_t dy_head_stride, const uint64_t* turns, float amplitude,
+                           const int32_t* positions, int start, int period, int interleaved,
+                           void* stream) {
+  return rotary("rotary_backward",
+                {dy, dx, dtype, tokens, heads, head_size, rot_dim, dy_token_stride, dy_head_stride,
+                 dx_token_stride, dx_head_stride, turns, positions, start, period, amplitude,
+                 interleaved != 0, 1},
+                stream);
+}
+
+csa_status csa_rotary_turns(uint64_t* turns, int rot_dim, double base, int scaling, double factor,
+                            double original_length, double slow, double fast) {
+  t_last_error.clear();
+  if (!turns) return set_error(CSA_ERR_NULL, "csa_rotary_turns: null pointer");
+  if (scaling < CSA_ROTARY_NONE || scaling > CSA_ROTARY_BY_PARTS)
+    return set_error(CSA_ERR_UNSUPPORTED, "csa_rotary_turns: unknown scaling");
+  if (rot_dim < 2 || rot_dim % 2 != 0 || !(base > 1.0) || !std::isfinite(base))
+    return set_error(CSA_ERR_SHAPE, "csa_rotary_turns: rot_dim must be even and >= 2, base > 1");
+  if (scaling != CSA_ROTARY_NONE && !(factor >= 1.0 && std::isfinite(factor)))
+    return set_error(CSA_ERR_SHAPE, "csa_rotary_turns: factor must be >= 1");
+  if (scaling == CSA_ROTARY_BY_PARTS &&
+      !(original_length > 0.0 && std::isfinite(original_length) && fast > slow &&
+        std::isfinite(fast) && std::isfinite(slow)))
+    return set_error(CSA_ERR_SHAPE,
+                     "csa_rotary_turns: original_length must be > 0, fast > slow");
+  const double two_pi = 6.283185307179586476925286766559;
+  if (scaling == CSA_ROTARY_NTK && rot_dim > 2)
+    base *= std::pow(factor, static_cast<double>(rot_dim) / (rot_dim - 2));
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    double f = std::pow(base, -2.0 * i / rot_dim);
+    if (scaling == CSA_ROTARY_LINEAR) f /= factor;
+    if (scaling == CSA_ROTARY_BY_PARTS) {
+      const double g =
+          std::min(1.0, std::max(0.0, (original_length * f / two_pi - slow) / (fast - slow)));
+      f *= g + (1.0 - g) / factor;
+    }
+    turns[i] = static_cast<uint64_t>(std::nearbyint(std::ldexp(f / two_pi, 64)));
+  }
+  return CSA_OK;
+}
+
+csa_status kv_cache_write(const csa_kv_cache* cache, const csa_kv_batch* batch, const void* k,
+                          const void* v, int dtype, int64_t k_token_stride, int64_t k_head_stride,
+                          int64_t v_token_stride, int64_t v_head_stride, void* stream) {
+  return kv_rows("kv_cache_write", cache, batch,
+                 {{const_cast<void*>(k), const_cast<void*>(v)},
+                  dtype,
+                  {k_token_stride, v_token_stride},
+                  {k_head_stride, v_head_stride}},
+                 true, stream);
+}
+
+csa_status kv_cache_read(void* k, void* v, int dtype, int64_t k_token_stride,
+                         int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                         const csa_kv_cache* cache, const csa_kv_batch* batch, void* stream) {
+  return kv_rows("kv_cache_read", cache, batch,
+                 {{k, v}, dtype, {k_token_stride, v_token_stride}, {k_head_stride, v_head_stride}},
+                 false, stream);
+}
+
+csa_status cache_attention_workspace_size(const csa_kv_cache* cache, int q_heads, size_t* bytes) {
+  t_last_error.clear();
+  if (!bytes) return set_error(CSA_ERR_NULL, "cache_attention_workspace_size: null pointer");
+  *bytes = 0;
+  const int rc = attention_heads_ok("cache_attention_workspace_size", cache, q_heads);
+  if (rc != CSA_OK) return rc;
+  *bytes = cache_attention_workspace_bytes(cache->head_size);
+  return CSA_OK;
+}
+
+csa_status cache_attention_forward(void* out, const void* q, int dtype, int q_heads,
+                                   int64_t out_token_stride, int64_t out_head_stride,
+                                   int64_t q_token_stride, int64_t q_head_stride,
+                                   const csa_kv_cache* cache, const csa_kv_batch* batch,
+                                   float scale, int window, int sinks, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+  t_last_error.clear();
+  const std::string w("cache_attention_forward");
+  int rc = attention_heads_ok(w, cache, q_heads);
+  if (rc == CSA_OK) rc = batch_args_ok(w, batch);
+  if (rc != CSA_OK) return rc;
+  if (!out || !q) return set_error(CSA_ERR_NULL, w + ": null pointer");
+  if (dtype != CSA_BF16 && dtype != CSA_F16)
+    return set_error(CSA_ERR_UNSUPPORTED, w + ": unknown dtype");
+  if (!std::isfinite(scale)) return set_error(CSA_ERR_SHAPE, w + ": scale not finite");
+  if (window < 0 || sinks < 0)
+    return set_error(CSA_ERR_SHAPE, w + ": window and sinks must be >= 0");
+  rc = rows_ok(w, q, dtype, batch->rows, q_heads, cache->head_size, q_token_stride, q_head_stride,
+               false);
+  if (rc == CSA_OK)
+    rc = rows_ok(w, out, dtype, batch->rows, q_heads, cache->head_size, out_token_stride,
+                 out_head_stride, true);
+  if (rc != CSA_OK) return rc;
+  const size_t need = cache_attention_workspace_bytes(cache->head_size);
+  if (!workspace || workspace_bytes < need)
+    return set_error(CSA_ERR_WORKSPACE, w + ": " + std::to_string(need) +
+                                            " bytes of workspace needed, " +
+                                            std::to_string(workspace ? workspace_bytes : 0) +
+                                            " given");
+  if (!aligned(workspace, 16))
+    return set_error(CSA_ERR_ALIGN, w + ": workspace must be 16-byte aligned");
+  DeviceInfo dev;
+  std::string err;
+  rc = current_device(dev, err);
+  if (rc != CSA_OK) return set_error(rc, err);
+  apply_stream_sm_limit(dev, static_cast<cudaStream_t>(stream));
+  rc = cache_attention_launch(*cache, *batch,
+                              {q, out, dtype, q_heads, q_token_stride, q_head_stride,
+                               out_token_stride, out_head_stride, scale, window, sinks, workspace},
+                              static_cast<cudaStream_t>(stream), dev, err);
+  return rc == CSA_OK ? CSA_OK : set_error(rc, err);
 }
 
 }  // extern "C"

@@ -159,4 +159,48 @@ int dense_grouped_launch(float* const* Y, const void* const* X, const void* W, c
 size_t dense_grouped_workspace_bytes(const void* const* X, const void* W, const int* M, int n,
                                      int I, int H);
 
+// Rotary positions: one call, strides in elements, `turns` as csa_rotary_turns fills it.
+struct RotaryCall {
+  const void* x;
+  void* out;
+  int dtype;
+  long long tokens;
+  int heads, head_size, rot_dim;
+  long long x_token, x_head, out_token, out_head;
+  const uint64_t* turns;
+  const int* positions;
+  int start, period;
+  float amplitude;
+  int interleaved, backward;
+};
+int rotary_launch(const RotaryCall& call, cudaStream_t stream, const DeviceInfo& dev,
+                  std::string& err);
+
+// Rows of K and V beside a cache (written from, or read into), strides in elements.
+struct KvRows {
+  void* x[2];
+  int dtype;
+  long long token[2], head[2];
+};
+int kv_cache_launch(const csa_kv_cache& cache, const csa_kv_batch& batch, const KvRows& rows,
+                    bool write, cudaStream_t stream, const DeviceInfo& dev, std::string& err);
+
+struct AttendCall {
+  const void* q;
+  void* out;
+  int dtype, q_heads;
+  long long q_token, q_head, out_token, out_head;
+  float scale;
+  int window, sinks;  // window 0: none
+  void* workspace;    // cache_attention_workspace_bytes
+};
+size_t cache_attention_workspace_bytes(int head_size);
+int cache_attention_launch(const csa_kv_cache& cache, const csa_kv_batch& batch,
+                           const AttendCall& call, cudaStream_t stream, const DeviceInfo& dev,
+                           std::string& err);
+
+// The device's view of a cache and a batch (kv_cache.cuh).
+struct KvView;
+KvView kv_view(const csa_kv_cache& cache, const csa_kv_batch& batch, const DeviceInfo& dev);
+
 }  // namespace csa

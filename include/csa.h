@@ -35,7 +35,8 @@
  *    status word, the kernels' work-list counters and the scratch of
  *    trimul_forward_noalloc (plus the page-locked completion words below).
  *  - bf16 inputs are passed as `const void*` to raw 16-bit bfloat16 values.
- *  - Outputs are fp32 and fully overwritten (no read-modify-write).
+ *  - Outputs are fp32 and fully overwritten (no read-modify-write), but for the rotary,
+ *    cache and cache-attention calls, which name their types and what they leave.
  *  - `stream` is a cudaStream_t passed as void*; NULL is the legacy default
  *    stream. Calls are asynchronous on that stream; argument errors are
  *    returned synchronously before anything is launched.
@@ -89,6 +90,9 @@ typedef int csa_status;
 #define CSA_ERR_BUSY         -11  /* no work-list counter set free: score or softmax
                                      launches in flight on 256 other streams, or more
                                      than 1024 of them captured into CUDA graphs */
+#define CSA_ERR_INDEX        -12  /* a page number, row range or length in device memory was
+                                     out of range; what it named was skipped (reported by
+                                     csa_get_status) */
 
 /* Causal mask bit patterns for the upper triangle (t2 > t). The page writes
  * NAN (the float quiet NaN, 0x7FC00000) and notes -inf would also do. */
@@ -360,10 +364,171 @@ csa_status causal_softmax_forward(float* att, const void* qkv, int B, int T, int
 csa_status batch_matmul_nt(float* Y, const void* X, const void* W, int batch, int T1, int T2,
                            int D, void* stream);
 
+/* Element types of the calls below (rows of 16- or 32-bit values). */
+#define CSA_BF16 0
+#define CSA_F16  1
+#define CSA_F32  2
+
+/*
+ * rotary_forward -- rotary positions: every head's first rot_dim elements are turned,
+ * pair by pair, by the angle p * f[i] of their token's position p:
+ *   y0 = a (x0 cos - x1 sin),   y1 = a (x1 cos + x0 sin),
+ * pairs (i, i + rot_dim/2), or (2i, 2i + 1) when `interleaved`; elements from rot_dim on
+ * are copied. Computed in fp32 and rounded once.
+ *   out, x       device, [tokens][heads][head_size] of `dtype`, head elements contiguous,
+ *                tokens and heads *_token_stride and *_head_stride elements apart (so the
+ *                Q and K parts of a packed (B,T,3,NH,HS) tensor are rotated in one call
+ *                with heads = 2 NH and token stride 3C). out == x with equal strides
+ *                rotates in place (elements from rot_dim on are then not touched); memory
+ *                ranges that overlap otherwise are refused (CSA_ERR_UNSUPPORTED), as are
+ *                strides with which rows of `out` would overlap (CSA_ERR_SHAPE).
+ *   turns        device, rot_dim/2 values of csa_rotary_turns.
+ *   amplitude    a, finite.
+ *   positions    device, int32 [tokens]; a negative one marks padding, whose rows of out
+ *                are left as they were. Or NULL: token t has position
+ *                start + (period > 0 ? t % period : t), start >= 0.
+ * Any head_size >= 2, rot_dim even, 2 <= rot_dim <= head_size. Pointers and strides need
+ * only the type's alignment; rows of 16-byte multiples take 16-byte loads. Angles come
+ * from 64-bit fixed-point turns: no precision is lost at any 32-bit position.
+ * Asynchronous on `stream`.
+ *
+ * rotary_backward -- the gradient: dx = a R(-p f) dy, same arguments (dx for out, dy for x).
+ */
+csa_status rotary_forward(void* out, const void* x, int dtype, int64_t tokens, int heads,
+                          int head_size, int rot_dim, int64_t out_token_stride,
+                          int64_t out_head_stride, int64_t x_token_stride, int64_t x_head_stride,
+                          const uint64_t* turns, float amplitude, const int32_t* positions,
+                          int start, int period, int interleaved, void* stream);
+csa_status rotary_backward(void* dx, const void* dy, int dtype, int64_t tokens, int heads,
+                           int head_size, int rot_dim, int64_t dx_token_stride,
+                           int64_t dx_head_stride, int64_t dy_token_stride,
+                           int64_t dy_head_stride, const uint64_t* turns, float amplitude,
+                           const int32_t* positions, int start, int period, int interleaved,
+                           void* stream);
+
+/*
+ * csa_rotary_turns -- fills turns[0 .. rot_dim/2 - 1] (host memory) with
+ * round(f[i] / 2pi * 2^64), the frequencies f[i] = base^(-2i/rot_dim) scaled for contexts
+ * longer than a model was trained on:
+ *   CSA_ROTARY_NONE      as they are;
+ *   CSA_ROTARY_LINEAR    f / factor (positions interpolated);
+ *   CSA_ROTARY_NTK       base * factor^(rot_dim / (rot_dim - 2)) in place of base;
+ *   CSA_ROTARY_BY_PARTS  f (g + (1 - g) / factor) with g = clip((r - slow) / (fast - slow), 0, 1)
+ *                        and r = original_length f / 2pi, the turns a frequency makes over the
+ *                        trained length (Peng et al., 2023): fast pairs kept, slow ones
+ *                        interpolated.
+ * Host only. CSA_ERR_NULL; CSA_ERR_SHAPE for rot_dim odd or < 2, base <= 1, factor < 1, or
+ * (BY_PARTS) original_length <= 0 or fast <= slow; CSA_ERR_UNSUPPORTED for another scaling.
+ */
+#define CSA_ROTARY_NONE     0
+#define CSA_ROTARY_LINEAR   1
+#define CSA_ROTARY_NTK      2
+#define CSA_ROTARY_BY_PARTS 3
+csa_status csa_rotary_turns(uint64_t* turns, int rot_dim, double base, int scaling, double factor,
+                            double original_length, double slow, double fast);
+
+/*
+ * csa_kv_cache -- a paged cache of keys and values in 8 bits. A page holds page_tokens
+ * tokens of one sequence; each (page, head) is a block with one fp32 scale for K and one
+ * for V, and its values are code * scale.
+ *   k, v              device, 8-bit codes [pages][heads][page_tokens][head_size], 16-byte aligned;
+ *   k_scale, v_scale  device, fp32 [pages][heads];
+ *   page_tokens       16, 32, 64 or 128;
+ *   head_size         a multiple of 16, at most 128;
+ *   format            CSA_KV_INT8 (codes -127 .. 127) or CSA_KV_E4M3 (the 8-bit float of 4
+ *                     exponent and 3 fraction bits, no infinities).
+ * Nothing needs clearing: pages and slots no token was written to are never interpreted.
+ */
+#define CSA_KV_INT8 0
+#define CSA_KV_E4M3 1
+typedef struct csa_kv_cache {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int pages, heads, page_tokens, head_size, format;
+} csa_kv_cache;
+
+/*
+ * csa_kv_batch -- which rows of a call are which tokens of which sequence. Sequence s has
+ * rows [offsets[s], offsets[s + 1]) of the call's `rows` rows; they are its last tokens, the
+ * final one at position lengths[s] - 1. Block b of the sequence (tokens b * page_tokens on)
+ * is page table[s][b].
+ *   offsets      device, int32 [sequences + 1], not decreasing, within [0, rows];
+ *   lengths      device, int32 [sequences], tokens INCLUDING the rows of this call, within
+ *                [0, table_width * page_tokens];
+ *   table        device, int32 [sequences][table_width]; entries past a length are not read;
+ *   max_new      at least every offsets[s + 1] - offsets[s] (it sizes the launch).
+ * Rows past offsets[sequences] are left as they were. Rows before a sequence's beginning
+ * (more rows than its length) are neither written nor read; attention gives zeros there.
+ * These arrays are read on the device: a sequence whose entries break the rules is skipped,
+ * as is a block whose page number is outside [0, pages), and csa_get_status reports
+ * CSA_ERR_INDEX. Pages that a call writes belong to one sequence each (prefix pages that
+ * several sequences share are full, and only read).
+ */
+typedef struct csa_kv_batch {
+  const int32_t* offsets;
+  const int32_t* lengths;
+  const int32_t* table;
+  int sequences, table_width, rows, max_new;
+} csa_kv_batch;
+
+/*
+ * kv_cache_write -- quantises the rows of K and V into the cache.
+ *   k, v   device, CSA_BF16 or CSA_F16 rows [rows][heads][head_size], head elements contiguous,
+ *          strides in elements; pointers 16-byte aligned, strides multiples of 8 elements.
+ * A block's scale is s = max(scale of what it held, s(m)), m its new rows' largest finite
+ * magnitude: for int8 s(m) is the smallest value of 8 significant bits with 127 s >= m, for
+ * e4m3 the smallest power of two with 448 s >= m, and at least 2^-100. Codes are x / s
+ * rounded to nearest even (NaN: 0; infinities: the largest code); when a block's scale
+ * grows, its older codes become code * s_old / s, rounded again. The codes are those of
+ * this definition in real numbers (no fp32 rounding shows). Asynchronous on `stream`.
+ *
+ * kv_cache_read -- the values code * scale of the batch's rows, rounded once to `dtype`
+ * (CSA_BF16, CSA_F16 or CSA_F32), into k and v. The batch may name other rows than those of
+ * a write: any sequence's last offsets[s + 1] - offsets[s] tokens.
+ */
+csa_status kv_cache_write(const csa_kv_cache* cache, const csa_kv_batch* batch, const void* k,
+                          const void* v, int dtype, int64_t k_token_stride, int64_t k_head_stride,
+                          int64_t v_token_stride, int64_t v_head_stride, void* stream);
+csa_status kv_cache_read(void* k, void* v, int dtype, int64_t k_token_stride,
+                         int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
+                         const csa_kv_cache* cache, const csa_kv_batch* batch, void* stream);
+
+/*
+ * cache_attention_forward -- attention of the batch's rows over the cache (their own K and V
+ * written before): row j of sequence s at position p = lengths[s] - n + j, query head h
+ *   out = sum_t w_t v_t / sum_t w_t,   w_t = exp(scale * q . k_t)
+ * over the visible t: t <= p, and with window > 0 also p - t < window or t < sinks. Query
+ * heads h share kv head h / (q_heads / heads). A row that sees nothing gives zeros.
+ *   out, q     device, [rows][q_heads][head_size] of CSA_BF16 or CSA_F16, strides as above;
+ *   q_heads    a multiple of cache->heads;
+ *   scale      finite (the framework's score uses 1/sqrt(head_size));
+ *   window     0: none; sinks >= 0 (used with a window);
+ *   workspace  device, 16-byte aligned, cache_attention_workspace_size bytes; needs no
+ *              clearing, in use until the call's kernels complete: calls that may overlap on
+ *              the GPU, replays of captured ones too, need separate workspaces.
+ * Codes enter the tensor cores as exact fp16 values; scores, the running maximum, sums and
+ * the output accumulate in fp32; weights are rounded to fp16 (11 bits) for the product with
+ * V; the result is rounded once. Visible codes must not be NaN (kv_cache_write stores none).
+ * The order of every sum is fixed: same inputs and SM limit, same bits. Asynchronous on
+ * `stream`; nothing is allocated.
+ */
+csa_status cache_attention_forward(void* out, const void* q, int dtype, int q_heads,
+                                   int64_t out_token_stride, int64_t out_head_stride,
+                                   int64_t q_token_stride, int64_t q_head_stride,
+                                   const csa_kv_cache* cache, const csa_kv_batch* batch,
+                                   float scale, int window, int sinks, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/* cache_attention_workspace_size -- bytes of workspace cache_attention_forward needs, into
+ * *bytes. Depends on cache and q_heads only (checked as there). Host only. */
+csa_status cache_attention_workspace_size(const csa_kv_cache* cache, int q_heads, size_t* bytes);
+
 /*
  * csa_get_status -- synchronises `stream`, then returns and clears the current
  * device's status word: CSA_OK, or CSA_ERR_TIMEOUT if a kernel's bounded wait
- * ran out since the last call. Returns CSA_ERR_CUDA if synchronisation fails.
+ * ran out since the last call, or CSA_ERR_INDEX (see csa_kv_batch). Returns CSA_ERR_CUDA if synchronisation fails.
  */
 csa_status csa_get_status(void* stream);
 
