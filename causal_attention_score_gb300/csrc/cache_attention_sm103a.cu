@@ -4,13 +4,19 @@
 //   out = sum_t w_t v_t / sum_t w_t,  w_t = exp(c q.k_t),  over the visible t:
 //   t <= p, and p - t < window or t < sinks where there is a window.
 //
-// G = q_heads / heads query heads share a kv head, so a unit of work is up to
-// 16 rows (tokens x G) of one sequence and kv head: the M of one
-// mma.m16n8k16, whatever G is. The step is bound by reading the codes of K and
-// V once from HBM; the tensor cores are far from busy (8 useful flops a byte
-// at G = 1), so mma.sync, whose operands are registers, is the right
-// instruction here: codes go from HBM to registers to the tensor core with no
-// trip through shared memory.
+// G = q_heads / heads query heads share a kv head, so a unit of work is a block
+// of 8 (or 16) rows (tokens x G) of one sequence and kv head. The step is bound
+// by reading the codes of K and V once from HBM; the tensor cores are far from
+// busy (8 useful flops a byte at G = 1), so mma.sync, whose operands are
+// registers, is the right instruction here: codes go from HBM to registers to
+// the tensor core with no trip through shared memory.
+//
+// Roles: mma.m16n8k16 with the cache as its A operand: scores are S^T = K Q^T
+// (16 tokens x 8 rows) and the output O^T = V^T P^T (16 elements x 8 rows), so
+// that 8 rows fill the instruction (with Q as A, 16 would be needed) and the
+// accumulator of a 128-element head takes 32 registers. P^T comes out of the
+// first product as an accumulator and goes into the second as a B operand: one
+// movmatrix (an 8 x 8 transposition) per 8 tokens in between.
 //
 // Codes and scales. Codes become fp16 exactly (|int8| <= 127; e4m3 has 4
 // significant bits). Q becomes fp16 after a power-of-two scale per row that
@@ -26,8 +32,8 @@
 //
 // Layout trick: a dot product may run over the elements in any order, so lane
 // (g, t) of a warp loads 16 contiguous bytes of token g's K row and uses its
-// four words as four k-steps (Q's fragments are laid out to match), and the 16
-// contiguous bytes of a V row that a lane loads are 16 of its n-tiles.
+// four words as four k-steps (Q's fragments are loaded to match), and the 16
+// contiguous bytes of a V row that a lane loads are 16 rows of V^T.
 //
 // Work split: all (sequence, head, row block) units in a row, each of as many
 // 64-token tiles as its rows see; every group of four warps takes an equal run
@@ -51,20 +57,25 @@
 namespace csa {
 namespace {
 
-constexpr int kGroups = 3;                  // groups of four warps per CTA
-constexpr int kThreads = kGroups * 128;
-constexpr int kRows = 16;
+// Groups of four warps per CTA (one CTA per SM): 512 threads of 128 registers
+// with one 8-row block, 384 of 168 with two.
+template <int NB>
+constexpr int kGroups = NB == 1 ? 4 : 3;
 constexpr int kTileTokens = 64;             // per group and step: 16 a warp
 constexpr int kMaxSms = 152;
-constexpr int kMaxWorkers = kMaxSms * kGroups;
+constexpr int kMaxWorkers = kMaxSms * 4;
+constexpr int kMaxRows = 16;
 constexpr float kRaise = 8.0f;              // the running maximum is raised past this
-constexpr float kNegInf = -INFINITY;
+// The running maximum of a row that has seen nothing: finite, so that
+// differences of two of them are 0.
+constexpr float kNothing = -1e30f;
 
 struct AttendArgs {
   KvView v;
   const void* q;
   void* out;
   long long q_token, q_head, out_token, out_head;
+  int half;        // rows are fp16 (else bf16)
   int group;       // query heads per kv head
   int window, sinks;
   float scale_log2;
@@ -78,12 +89,21 @@ struct AttendArgs {
 // A piece that begins a unit but does not end it: what the join needs.
 enum HeaderWord { kHeadPieces = 0, kHeadRow0, kHeadFirst, kHeadHead, kHeadRows };
 
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The transposed 8 x 8 matrix of 16-bit elements (lane (g, t): row g, columns
+// 2t and 2t + 1).
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
 }
 
 __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
@@ -96,6 +116,13 @@ __device__ __forceinline__ void group_sync(int group) {
   asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory");
 }
 
+__device__ __forceinline__ void store_out(const AttendArgs& a, long long at, float v) {
+  if (a.half)
+    static_cast<__half*>(a.out)[at] = __float2half_rn(v);
+  else
+    static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
+}
+
 // What a sequence asks for: rows (tokens x group), their 64-token tiles (the
 // first `sink_tiles`, then those from `window_tile` on).
 struct SeqWork {
@@ -103,6 +130,7 @@ struct SeqWork {
   int rows, blocks, tiles, sink_tiles, window_tile;
 };
 
+template <int NB>
 __device__ __forceinline__ SeqWork seq_work(const AttendArgs& a, int s) {
   SeqWork w;
   w.q = kv_sequence(a.v, s);
@@ -112,7 +140,7 @@ __device__ __forceinline__ SeqWork seq_work(const AttendArgs& a, int s) {
     return w;
   }
   w.rows = static_cast<int>(rows);
-  w.blocks = (w.rows + kRows - 1) / kRows;
+  w.blocks = (w.rows + 8 * NB - 1) / (8 * NB);
   w.sink_tiles = w.window_tile = 0;
   const int all = (w.q.length + kTileTokens - 1) / kTileTokens;
   if (a.window > 0) {
@@ -125,37 +153,67 @@ __device__ __forceinline__ SeqWork seq_work(const AttendArgs& a, int s) {
   return w;
 }
 
-template <int HSP>
-struct GroupSmem {
-  static constexpr int kColStride = HSP / 8 + 4;             // floats per n column, padded
-  static constexpr int kRowStride = 8 * kColStride + 4;
-  uint4 q[HSP / 16][32];
-  float o[4][kRows][kRowStride];
-  float factor[kRows];
-  int pos[kRows];
-  float m[4][kRows], l[4][kRows];
+// A group's place in the work list and the piece of a unit that it is at. Kept
+// in shared memory: the main loop needs the registers.
+struct Piece {
+  long long at, end;  // the group's run of tiles still to do
+  long long base;     // where sequence s begins in the list
+  SeqWork w;
+  int s;
+  int head, row_first, rows;  // the unit
+  int tile0, count;           // its tiles [tile0, tile0 + count); count 0: no more pieces
 };
 
-template <typename T>
-__device__ __forceinline__ T to_out(float v);
-template <>
-__device__ __forceinline__ __nv_bfloat16 to_out<__nv_bfloat16>(float v) {
-  return __float2bfloat16_rn(v);
-}
-template <>
-__device__ __forceinline__ __half to_out<__half>(float v) {
-  return __float2half_rn(v);
+template <int NB>
+__device__ __forceinline__ void next_piece(const AttendArgs& a, Piece& p) {
+  p.count = 0;
+  if (p.at >= p.end) return;
+  long long units;
+  for (;;) {
+    units = static_cast<long long>(p.w.blocks) * a.v.heads;
+    if (p.at < p.base + units * p.w.tiles) break;
+    p.base += units * p.w.tiles;
+    p.w = seq_work<NB>(a, ++p.s);
+  }
+  const long long off = p.at - p.base;
+  const int unit = static_cast<int>(off / p.w.tiles);
+  p.tile0 = static_cast<int>(off - static_cast<long long>(unit) * p.w.tiles);
+  p.head = unit / p.w.blocks;
+  p.row_first = (unit - p.head * p.w.blocks) * (8 * NB);
+  p.rows = min(p.w.rows - p.row_first, 8 * NB);
+  p.count = static_cast<int>(min(static_cast<long long>(p.w.tiles - p.tile0), p.end - p.at));
+  p.at += p.count;
 }
 
-template <int HSP, int kFormat, typename T>
-__global__ void __launch_bounds__(kThreads, 1) attend_rows_sm103a_kernel(const AttendArgs a) {
+template <int HSP, int NB>
+struct GroupSmem {
+  // Floats per lane column and row, padded so that the float4 accesses of eight
+  // lanes (two g, four t) fall into different banks.
+  static constexpr int kColStride = HSP / 8 + 4;
+  static constexpr int kRowStride = 8 * kColStride + 4;
+  // Q's fragments stay in registers with one row block; two take this.
+  static constexpr bool kSharedQ = NB == 2 && HSP == 128;
+  float o[4][8 * NB][kRowStride];
+  uint4 q[kSharedQ ? NB * HSP / 32 : 1][32];
+  float m[4][8 * NB], l[4][8 * NB];
+  Piece piece;
+};
+
+// HSP: head size padded to 64 or 128; kFull: head_size == HSP (no bounds on the
+// element loads).
+template <int HSP, int NB, int kFormat, bool kFull>
+__global__ void __launch_bounds__(128 * kGroups<NB>, 1)
+    attend_rows_sm103a_kernel(const AttendArgs a) {
+  constexpr int kThreads = 128 * kGroups<NB>;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   __shared__ long long s_prefix[kThreads + 1];
   __shared__ long long s_warp[kThreads / 32];
-  GroupSmem<HSP>* groups = reinterpret_cast<GroupSmem<HSP>*>(smem_raw);
+  using Smem = GroupSmem<HSP, NB>;
+  Smem* groups = reinterpret_cast<Smem*>(smem_raw);
   constexpr int kChunks = HSP / 64;       // 16-byte chunks of a K row per lane
-  constexpr int kVWords = HSP / 32;       // words of a V row per lane
-  constexpr int kTilesN = HSP / 8;        // n-tiles of the output
+  constexpr int kVBytes = HSP / 8;        // bytes of a V row per lane
+  constexpr int kVWords = kVBytes / 4;
+  constexpr int kTilesM = HSP / 16;       // m-tiles of the output
 
   grid_dependency_wait();
 
@@ -167,8 +225,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_rows_sm103a_kernel(const A
   const int lane = threadIdx.x & 31, warp_id = threadIdx.x >> 5;
   {
     long long mine = 0;
-    for (int s = threadIdx.x * c; s < min(S, (static_cast<int>(threadIdx.x) + 1) * c); ++s) {
-      const SeqWork w = seq_work(a, s);
+    const long long from = static_cast<long long>(threadIdx.x) * c;
+    for (long long s = from; s < min(static_cast<long long>(S), from + c); ++s) {
+      const SeqWork w = seq_work<NB>(a, static_cast<int>(s));
       mine += static_cast<long long>(w.blocks) * w.tiles * a.v.heads;
     }
     long long sum = mine;
@@ -189,154 +248,170 @@ __global__ void __launch_bounds__(kThreads, 1) attend_rows_sm103a_kernel(const A
   const int gi = warp_id >> 2;       // group in the CTA
   const int warp = warp_id & 3;      // warp in the group
   const int gtid = threadIdx.x & 127;
-  const int worker = blockIdx.x * kGroups + gi;
+  const int worker = blockIdx.x * kGroups<NB> + gi;
   const long long share = (total + a.workers - 1) / a.workers;
-  long long at = share * worker;
-  const long long end = min(at + share, total);
-  GroupSmem<HSP>& sm = groups[gi];
+  Smem& sm = groups[gi];
   const int g = lane >> 2, t = lane & 3;
-  const int D = a.v.head_size;
+  const int D = kFull ? HSP : a.v.head_size;
   int* header = a.headers + worker * 8;
   bool left_open = false;
 
-  int s = 0;
-  long long base = 0;
-  SeqWork w{};
-  if (at < end) {
-    int lo = 0, hi = kThreads;  // s_prefix[lo] <= at < s_prefix[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (s_prefix[mid] <= at) lo = mid;
-      else hi = mid;
+  if (gtid == 0) {
+    Piece& p = sm.piece;
+    p.at = min(share * worker, total);
+    p.end = min(p.at + share, total);
+    if (p.at < p.end) {
+      int lo = 0, hi = kThreads;  // s_prefix[lo] <= at < s_prefix[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (s_prefix[mid] <= p.at) lo = mid;
+        else hi = mid;
+      }
+      p.s = lo * c;
+      p.base = s_prefix[lo];
+      p.w = seq_work<NB>(a, p.s);
     }
-    s = lo * c;
-    base = s_prefix[lo];
-    w = seq_work(a, s);
   }
-  while (at < end) {
-    const long long units = static_cast<long long>(w.blocks) * a.v.heads;
-    if (at >= base + units * w.tiles) {
-      base += units * w.tiles;
-      w = seq_work(a, ++s);
-      continue;
-    }
-    const long long off = at - base;
-    const int unit = static_cast<int>(off / w.tiles);
-    const int tile0 = static_cast<int>(off - static_cast<long long>(unit) * w.tiles);
-    const int head = unit / w.blocks;
-    const int row_first = (unit - head * w.blocks) * kRows;
-    const int rows = min(w.rows - row_first, kRows);
-    const int count = static_cast<int>(min(static_cast<long long>(w.tiles - tile0), end - at));
-    at += count;
+  for (;;) {
+    if (gtid == 0) next_piece<NB>(a, sm.piece);
+    group_sync(gi);
+    const volatile Piece& piece = sm.piece;
+    const int count = piece.count;
+    if (count == 0) break;
+    const int s = piece.s, head = piece.head, tile0 = piece.tile0;
+    const int length = piece.w.q.length;
 
     // ------------------------------------------------------ Q's fragments --
+    // Lane (g, t): row g (and g + 8), the 16 elements of chunks t and t + 4.
+    uint32_t qf[NB][kChunks][8];
+    float fr[NB][2];  // of rows 2t, 2t + 1 (this lane's columns of S^T)
+    int pr[NB][2];
+    int pos_low, pos_high;
     {
-      const int r = gtid >> 3, part = gtid & 7;  // 16 elements of a row
-      const int rr = row_first + r;
-      const int j = rr / a.group;
-      const bool live = r < rows;
-      uint4 raw[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-      if (live && part * 16 < D) {
-        const uint4* from = reinterpret_cast<const uint4*>(
-            static_cast<const T*>(a.q) + (w.q.row0 + j) * a.q_token +
-            (head * a.group + (rr - j * a.group)) * a.q_head + part * 16);
-        raw[0] = from[0];
-        raw[1] = from[1];
-      }
-      const uint32_t* word = reinterpret_cast<const uint32_t*>(raw);
-      uint32_t h[8];
-      float back = 1.0f;
-      if constexpr (std::is_same<T, __half>::value) {
+      const int row_first = piece.row_first, rows = piece.rows;
+      const int first = piece.w.q.first, row0 = piece.w.q.row0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] = word[i];
-      } else {
-        float x[16], most = 0.0f;
+      for (int b = 0; b < NB; ++b) {
+        const int rr = row_first + 8 * b + g;
+        const int j = rr / a.group;
+        const bool live = 8 * b + g < rows;
+        float back = 1.0f, most = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[2 * i] = __uint_as_float(word[i] << 16);
-          x[2 * i + 1] = __uint_as_float(word[i] & 0xFFFF0000u);
-          most = fmaxf(most, fmaxf(fabsf(x[2 * i]), fabsf(x[2 * i + 1])));
+        for (int h = 0; h < kChunks; ++h) {
+          const int d = (4 * h + t) * 16;
+          uint4 raw[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+          if (live && (kFull || d < D)) {
+            const uint4* from = reinterpret_cast<const uint4*>(
+                static_cast<const uint16_t*>(a.q) + (row0 + j) * a.q_token +
+                (head * a.group + (rr - j * a.group)) * a.q_head + d);
+            raw[0] = from[0];
+            raw[1] = from[1];
+          }
+          const uint32_t* word = reinterpret_cast<const uint32_t*>(raw);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            qf[b][h][i] = word[i];
+            most = fmaxf(most, fmaxf(fabsf(__uint_as_float(word[i] << 16)),
+                                     fabsf(__uint_as_float(word[i] & 0xFFFF0000u))));
+          }
         }
+        if (!a.half) {  // bf16 rows: to fp16, scaled
+          most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+          most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+          const uint32_t e = max(__float_as_uint(most) >> 23, 15u);
+          const float up = __uint_as_float((268u - e) << 23);  // 2^(14 - exponent)
+          back = __uint_as_float((e - 14u) << 23);
 #pragma unroll
-        for (int d = 1; d < 8; d *= 2) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
-        const uint32_t e = max(__float_as_uint(most) >> 23, 15u);
-        const float up = __uint_as_float((268u - e) << 23);  // 2^(14 - exponent)
-        back = __uint_as_float((e - 14u) << 23);
+          for (int h = 0; h < kChunks; ++h)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] = half2_of(x[2 * i] * up, x[2 * i + 1] * up);
-      }
-      if (part * 16 < HSP) {
-        // chunk `part` is lane (r % 8, part % 4)'s, in k-steps 4 (part / 4) + 0..3
-        const int to = (r & 7) * 4 + (part & 3);
+            for (int i = 0; i < 8; ++i)
+              qf[b][h][i] = half2_of(__uint_as_float(qf[b][h][i] << 16) * up,
+                                     __uint_as_float(qf[b][h][i] & 0xFFFF0000u) * up);
+        }
+        if constexpr (Smem::kSharedQ) {
+          if (warp == 0)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t* f = reinterpret_cast<uint32_t*>(&sm.q[(part >> 2) * 4 + i][to]);
-          f[r >> 3] = h[2 * i];
-          f[2 + (r >> 3)] = h[2 * i + 1];
+            for (int h = 0; h < kChunks; ++h)
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+                sm.q[(b * kChunks + h) * 2 + k][lane] =
+                    make_uint4(qf[b][h][4 * k], qf[b][h][4 * k + 1], qf[b][h][4 * k + 2],
+                               qf[b][h][4 * k + 3]);
+        }
+        const float f = a.scale_log2 * back;
+        const int pos = live ? first + j : -1;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          fr[b][e] = __shfl_sync(0xFFFFFFFFu, f, (2 * t + e) * 4);
+          pr[b][e] = __shfl_sync(0xFFFFFFFFu, pos, (2 * t + e) * 4);
         }
       }
-      if (part == 0) {
-        sm.factor[r] = a.scale_log2 * back;
-        sm.pos[r] = live ? w.q.first + j : -1;
-      }
+      pos_low = first + row_first / a.group;
+      pos_high = first + (row_first + rows - 1) / a.group;
     }
-    group_sync(gi);
-    const float f0 = sm.factor[g], f1 = sm.factor[g + 8];
-    const int pos0 = sm.pos[g], pos1 = sm.pos[g + 8];
-    const int pos_low = sm.pos[0], pos_high = sm.pos[rows - 1];
+    if constexpr (Smem::kSharedQ) group_sync(gi);
 
-    float o[kTilesN][4];
+    float o[NB][kTilesM][4];
 #pragma unroll
-    for (int i = 0; i < kTilesN; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-    float m0 = kNegInf, m1 = kNegInf, l0 = 0.0f, l1 = 0.0f;
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int i = 0; i < kTilesM; ++i) o[b][i][0] = o[b][i][1] = o[b][i][2] = o[b][i][3] = 0.0f;
+    float m[NB][2], l[NB][2];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      m[b][0] = m[b][1] = kNothing;
+      l[b][0] = l[b][1] = 0.0f;
+    }
 
     uint4 kr[2][kChunks];
     uint32_t vr[4][kVWords];
     float ks = 0.0f, vs = 1.0f;
+    const int sink_tiles = piece.w.sink_tiles, window_skip = piece.w.window_tile - sink_tiles;
     // First token of this warp's 16 in step i, and its page (-1: nothing there).
     auto token_of = [&](int i) {
       const int tile = tile0 + i;
-      return (tile < w.sink_tiles ? tile : tile - w.sink_tiles + w.window_tile) * kTileTokens +
-             warp * 16;
+      return (tile < sink_tiles ? tile : tile + window_skip) * kTileTokens + warp * 16;
     };
     auto page_of = [&](int i) {
       if (i >= count) return -1;
       const int tb = token_of(i);
-      return tb < w.q.length ? kv_page(a.v, s, tb >> a.v.page_shift) : -1;
+      return tb < length ? kv_page(a.v, s, tb >> a.v.page_shift) : -1;
     };
+    // Lane (g, t): tokens g and g + 8, chunks t and t + 4 of their K rows; tokens
+    // 2t, 2t + 1, 2t + 8, 2t + 9, chunk g of their V rows.
+    const int k_lane = g * D + t * 16, v_lane = 2 * t * D + g * kVBytes;
     auto load_k = [&](int tb, int page) {
       const uint8_t* from = a.v.codes[0] + kv_page_offset(a.v, page, head) +
-                            (tb & (a.v.page_tokens - 1)) * D;
+                            ((tb & (a.v.page_tokens - 1)) * D + k_lane);
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int h = 0; h < kChunks; ++h) {
-          const int d = (h * 4 + t) * 16;
-          kr[n][h] = d < D ? *reinterpret_cast<const uint4*>(from + (8 * n + g) * D + d)
-                           : make_uint4(0, 0, 0, 0);
-        }
-      ks = a.v.scale[0][static_cast<long long>(page) * a.v.heads + head];
+        for (int h = 0; h < kChunks; ++h)
+          kr[n][h] = kFull || (4 * h + t) * 16 < D
+                         ? __ldg(reinterpret_cast<const uint4*>(from + 8 * n * D + 64 * h))
+                         : make_uint4(0, 0, 0, 0);
+      ks = __ldg(a.v.scale[0] + (static_cast<long long>(page) * a.v.heads + head));
     };
     auto load_v = [&](int tb, int page) {
       const uint8_t* from = a.v.codes[1] + kv_page_offset(a.v, page, head) +
-                            (tb & (a.v.page_tokens - 1)) * D + g * (HSP / 8);
+                            ((tb & (a.v.page_tokens - 1)) * D + v_lane);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint8_t* row = from + (2 * t + (i & 1) + 8 * (i >> 1)) * D;
-        const bool in = g * (HSP / 8) < D;
+        const uint8_t* row = from + ((i & 1) + 8 * (i >> 1)) * D;
+        const bool in = kFull || g * kVBytes < D;
         if constexpr (kVWords == 4) {
-          const uint4 x = in ? *reinterpret_cast<const uint4*>(row) : make_uint4(0, 0, 0, 0);
+          const uint4 x = in ? __ldg(reinterpret_cast<const uint4*>(row)) : make_uint4(0, 0, 0, 0);
           vr[i][0] = x.x;
           vr[i][1] = x.y;
           vr[i][2] = x.z;
           vr[i][3] = x.w;
         } else {
-          const uint2 x = in ? *reinterpret_cast<const uint2*>(row) : make_uint2(0, 0);
+          const uint2 x = in ? __ldg(reinterpret_cast<const uint2*>(row)) : make_uint2(0, 0);
           vr[i][0] = x.x;
           vr[i][1] = x.y;
         }
       }
-      vs = a.v.scale[1][static_cast<long long>(page) * a.v.heads + head];
+      vs = __ldg(a.v.scale[1] + (static_cast<long long>(page) * a.v.heads + head));
     };
 
     int page = page_of(0), page_next = page_of(1);
@@ -347,86 +422,108 @@ __global__ void __launch_bounds__(kThreads, 1) attend_rows_sm103a_kernel(const A
     for (int i = 0; i < count; ++i) {
       const int tb = token_of(i);
       const int page_after = page_of(i + 2);
-      const bool here = page >= 0;
-      uint4 pa = make_uint4(0, 0, 0, 0);
-      if (here) {
-        float sc[2][4] = {};
+      if (page >= 0) {
+        float sc[NB][4] = {};
 #pragma unroll
-        for (int h = 0; h < kChunks; ++h)
+        for (int h = 0; h < kChunks; ++h) {
+          const uint32_t* k0 = reinterpret_cast<const uint32_t*>(&kr[0][h]);
+          const uint32_t* k1 = reinterpret_cast<const uint32_t*>(&kr[1][h]);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint4 qa = sm.q[h * 4 + k][lane];
+          for (int k2 = 0; k2 < 2; ++k2) {
+            uint32_t q4[NB][4];
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              const uint32_t word = k == 0   ? kr[n][h].x
-                                    : k == 1 ? kr[n][h].y
-                                    : k == 2 ? kr[n][h].z
-                                             : kr[n][h].w;
-              uint32_t b0, b1;
-              codes4_to_half2x2<kFormat>(word, b0, b1);
-              mma_f16(sc[n], qa, b0, b1);
+            for (int b = 0; b < NB; ++b) {
+              if constexpr (Smem::kSharedQ) {
+                const uint4 x = sm.q[(b * kChunks + h) * 2 + k2][lane];
+                q4[b][0] = x.x;
+                q4[b][1] = x.y;
+                q4[b][2] = x.z;
+                q4[b][3] = x.w;
+              } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) q4[b][i] = qf[b][h][4 * k2 + i];
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              uint32_t a0, a1, a2, a3;
+              codes4_to_half2x2<kFormat>(k0[2 * k2 + k], a0, a2);
+              codes4_to_half2x2<kFormat>(k1[2 * k2 + k], a1, a3);
+#pragma unroll
+              for (int b = 0; b < NB; ++b)
+                mma_f16(sc[b], a0, a1, a2, a3, q4[b][2 * k], q4[b][2 * k + 1]);
             }
           }
-        const float fk0 = f0 * ks, fk1 = f1 * ks;
+        }
         const float lv = __log2f(vs), inv = __fdividef(1.0f, vs);
+        float fk[NB][2];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          fk[b][0] = fr[b][0] * ks;
+          fk[b][1] = fr[b][1] * ks;
+        }
         if (page_next >= 0) load_k(token_of(i + 1), page_next);
-        float x[2][4];
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[n][e] = fmaf(sc[n][e], e < 2 ? fk0 : fk1, lv);
+        // sc element e: token g + 8 (e / 2), row 2t + e % 2
         const bool open = tb + 15 <= pos_low &&
                           (a.window == 0 || pos_high - tb < a.window || tb + 15 < a.sinks);
-        if (!open) {
+        float x[NB][4];
+        bool raise = false;
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int tok = tb + 8 * n + 2 * t + (e & 1);
-              const int p = e < 2 ? pos0 : pos1;
+          for (int e = 0; e < 4; ++e) {
+            if (!open) {
+              const int tok = tb + g + 8 * (e >> 1), p = pr[b][e & 1];
               if (tok > p || (a.window != 0 && p - tok >= a.window && tok >= a.sinks))
-                x[n][e] = kNegInf;
+                sc[b][e] = -INFINITY;
+            }
+            // a masked score stays -inf through the scale, whatever its sign or value
+            x[b][e] = sc[b][e] == -INFINITY ? -INFINITY
+                                            : fmaf(sc[b][e], fk[b][e & 1], lv - m[b][e & 1]);
+            raise |= x[b][e] > kRaise;
+          }
+        if (__any_sync(0xFFFFFFFFu, raise)) {
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              float y[2], most;
+#pragma unroll
+              for (int n = 0; n < 2; ++n)
+                y[n] = sc[b][2 * n + r] == -INFINITY ? -INFINITY
+                                                     : fmaf(sc[b][2 * n + r], fk[b][r], lv);
+              most = fmaxf(y[0], y[1]);
+              most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 4));
+              most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 8));
+              most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 16));
+              const float n = fmaxf(m[b][r], most);
+              const float corr = ex2_approx(m[b][r] - n);
+              m[b][r] = n;
+              l[b][r] *= corr;
+#pragma unroll
+              for (int j = 0; j < kTilesM; ++j) {
+                o[b][j][r] *= corr;
+                o[b][j][2 + r] *= corr;
+              }
+              x[b][r] = y[0] - n;
+              x[b][2 + r] = y[1] - n;
             }
         }
-        float mx0 = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
-        float mx1 = fmaxf(fmaxf(x[0][2], x[0][3]), fmaxf(x[1][2], x[1][3]));
-        if (__any_sync(0xFFFFFFFFu, mx0 > m0 + kRaise || mx1 > m1 + kRaise)) {
+        uint32_t pb[NB][2];
 #pragma unroll
-          for (int d = 1; d < 4; d *= 2) {
-            mx0 = fmaxf(mx0, __shfl_xor_sync(0xFFFFFFFFu, mx0, d));
-            mx1 = fmaxf(mx1, __shfl_xor_sync(0xFFFFFFFFu, mx1, d));
-          }
-          const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
-          const float c0 = n0 == kNegInf ? 1.0f : ex2_approx(m0 - n0);
-          const float c1 = n1 == kNegInf ? 1.0f : ex2_approx(m1 - n1);
-          m0 = n0;
-          m1 = n1;
-          l0 *= c0;
-          l1 *= c1;
+        for (int b = 0; b < NB; ++b) {
 #pragma unroll
-          for (int j = 0; j < kTilesN; ++j) {
-            o[j][0] *= c0;
-            o[j][1] *= c0;
-            o[j][2] *= c1;
-            o[j][3] *= c1;
-          }
+          for (int e = 0; e < 4; ++e) x[b][e] = ex2_approx(x[b][e]);
+          l[b][0] = fmaf(x[b][0] + x[b][2], inv, l[b][0]);
+          l[b][1] = fmaf(x[b][1] + x[b][3], inv, l[b][1]);
+          pb[b][0] = transpose_8x8(half2_of(x[b][0], x[b][1]));
+          pb[b][1] = transpose_8x8(half2_of(x[b][2], x[b][3]));
         }
-        const float z0 = m0 == kNegInf ? 0.0f : m0, z1 = m1 == kNegInf ? 0.0f : m1;
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[n][e] = ex2_approx(x[n][e] - (e < 2 ? z0 : z1));
-        l0 = fmaf((x[0][0] + x[0][1]) + (x[1][0] + x[1][1]), inv, l0);
-        l1 = fmaf((x[0][2] + x[0][3]) + (x[1][2] + x[1][3]), inv, l1);
-        pa.x = half2_of(x[0][0], x[0][1]);
-        pa.y = half2_of(x[0][2], x[0][3]);
-        pa.z = half2_of(x[1][0], x[1][1]);
-        pa.w = half2_of(x[1][2], x[1][3]);
-        if (tb + 16 > w.q.length) {
+        if (tb + 16 > length) {
           // slots past the sequence's end may hold the codes of no number
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            if (tb + 2 * t + (k & 1) + 8 * (k >> 1) >= w.q.length) {
+            if (tb + 2 * t + (k & 1) + 8 * (k >> 1) >= length) {
 #pragma unroll
               for (int j = 0; j < kVWords; ++j) vr[k][j] = 0;
             }
@@ -434,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_rows_sm103a_kernel(const A
 #pragma unroll
         for (int j = 0; j < kVWords; ++j) {
           // four elements of two token pairs: bytes to (token, token + 1) pairs
-          uint32_t lo[2], hi[2];
+          uint32_t f[4][2];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             uint32_t u = vr[2 * k][j], v = vr[2 * k + 1][j];
@@ -442,26 +539,25 @@ __global__ void __launch_bounds__(kThreads, 1) attend_rows_sm103a_kernel(const A
               u ^= 0x80808080u;
               v ^= 0x80808080u;
             }
-            lo[k] = byte_perm(u, v, 0x5140);
-            hi[k] = byte_perm(u, v, 0x7362);
-          }
-          uint32_t b[4][2];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
+            const uint32_t lo = byte_perm(u, v, 0x5140), hi = byte_perm(u, v, 0x7362);
             if (kFormat == CSA_KV_INT8) {
-              b[0][k] = flipped_pair_to_half2<0x4140>(lo[k]);
-              b[1][k] = flipped_pair_to_half2<0x4342>(lo[k]);
-              b[2][k] = flipped_pair_to_half2<0x4140>(hi[k]);
-              b[3][k] = flipped_pair_to_half2<0x4342>(hi[k]);
+              f[0][k] = flipped_pair_to_half2<0x4140>(lo);
+              f[1][k] = flipped_pair_to_half2<0x4342>(lo);
+              f[2][k] = flipped_pair_to_half2<0x4140>(hi);
+              f[3][k] = flipped_pair_to_half2<0x4342>(hi);
             } else {
-              b[0][k] = e4m3x2_to_half2(lo[k] & 0xFFFFu);
-              b[1][k] = e4m3x2_to_half2(lo[k] >> 16);
-              b[2][k] = e4m3x2_to_half2(hi[k] & 0xFFFFu);
-              b[3][k] = e4m3x2_to_half2(hi[k] >> 16);
+              f[0][k] = e4m3x2_to_half2(lo & 0xFFFFu);
+              f[1][k] = e4m3x2_to_half2(lo >> 16);
+              f[2][k] = e4m3x2_to_half2(hi & 0xFFFFu);
+              f[3][k] = e4m3x2_to_half2(hi >> 16);
             }
           }
+          // m-tile 2j: elements 4j (rows g) and 4j + 1 (rows g + 8) of the chunk
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma_f16(o[4 * j + k], pa, b[k][0], b[k][1]);
+          for (int b = 0; b < NB; ++b) {
+            mma_f16(o[b][2 * j], f[0][0], f[1][0], f[0][1], f[1][1], pb[b][0], pb[b][1]);
+            mma_f16(o[b][2 * j + 1], f[2][0], f[3][0], f[2][1], f[3][1], pb[b][0], pb[b][1]);
+          }
         }
       } else if (page_next >= 0) {
         load_k(token_of(i + 1), page_next);
@@ -473,73 +569,73 @@ __global__ void __launch_bounds__(kThreads, 1) attend_rows_sm103a_kernel(const A
 
     // ------------------------------------------- the four warps' results --
 #pragma unroll
-    for (int d = 1; d < 4; d *= 2) {
-      l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, d);
-      l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, d);
-    }
-    if (t == 0) {
-      sm.m[warp][g] = m0;
-      sm.m[warp][g + 8] = m1;
-      sm.l[warp][g] = l0;
-      sm.l[warp][g + 8] = l1;
-    }
-    group_sync(gi);
-    {
-      const float n0 = fmaxf(fmaxf(sm.m[0][g], sm.m[1][g]), fmaxf(sm.m[2][g], sm.m[3][g]));
-      const float n1 =
-          fmaxf(fmaxf(sm.m[0][g + 8], sm.m[1][g + 8]), fmaxf(sm.m[2][g + 8], sm.m[3][g + 8]));
-      const float c0 = n0 == kNegInf ? 1.0f : ex2_approx(m0 - n0);
-      const float c1 = n1 == kNegInf ? 1.0f : ex2_approx(m1 - n1);
-      // element (n-tile j, column n) is dimension n * HSP / 8 + j
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int r = g + (e >> 1) * 8;
-        if (r >= rows) continue;
-        float* to = &sm.o[warp][r][(2 * t + (e & 1)) * GroupSmem<HSP>::kColStride];
-        const float cc = e < 2 ? c0 : c1;
+      for (int r = 0; r < 2; ++r) {
 #pragma unroll
-        for (int j = 0; j < kTilesN; j += 4)
-          *reinterpret_cast<float4*>(to + j) = make_float4(o[j][e] * cc, o[j + 1][e] * cc,
-                                                           o[j + 2][e] * cc, o[j + 3][e] * cc);
+        for (int d = 4; d < 32; d *= 2) l[b][r] += __shfl_xor_sync(0xFFFFFFFFu, l[b][r], d);
+        if (g == 0) {
+          sm.m[warp][8 * b + 2 * t + r] = m[b][r];
+          sm.l[warp][8 * b + 2 * t + r] = l[b][r];
+        }
       }
-    }
     group_sync(gi);
-    const bool whole = tile0 == 0 && count == w.tiles;
-    const int slot = 2 * worker + (tile0 == 0 ? 1 : 0);
+    const int rows = piece.rows;
+    auto row_max = [&](int r) {
+      return fmaxf(fmaxf(sm.m[0][r], sm.m[1][r]), fmaxf(sm.m[2][r], sm.m[3][r]));
+    };
+    // lane (g, t) holds elements g * kVBytes .. of rows 2t and 2t + 1: element 2j of
+    // a chunk in o[j][0..1], 2j + 1 in o[j][2..3]
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * b + 2 * t + e;
+        if (r >= rows) continue;
+        const float corr = ex2_approx(m[b][e] - row_max(r));
+        float* to = &sm.o[warp][r][g * Smem::kColStride];
+#pragma unroll
+        for (int j = 0; j < kTilesM; j += 2)
+          *reinterpret_cast<float4*>(to + 2 * j) =
+              make_float4(o[b][j][e] * corr, o[b][j][2 + e] * corr, o[b][j + 1][e] * corr,
+                          o[b][j + 1][2 + e] * corr);
+      }
+    group_sync(gi);
+    const bool begins = piece.tile0 == 0, whole = begins && piece.count == piece.w.tiles;
+    const int row_first = piece.row_first, row0 = piece.w.q.row0, out_head = piece.head * a.group;
+    const int slot = 2 * worker + (begins ? 1 : 0);
     float* part = a.parts + static_cast<long long>(slot) * a.part_floats;
-    // 128 threads over rows x HSP
     for (int e = gtid; e < rows * HSP; e += 128) {
       const int r = e / HSP, d = e % HSP;
-      const int idx = (d / (HSP / 8)) * GroupSmem<HSP>::kColStride + d % (HSP / 8);
-      const float mm = fmaxf(fmaxf(sm.m[0][r], sm.m[1][r]), fmaxf(sm.m[2][r], sm.m[3][r]));
+      const int idx = (d / kVBytes) * Smem::kColStride + d % kVBytes;
+      const float mm = row_max(r);
       const float acc = (sm.o[0][r][idx] + sm.o[1][r][idx]) + (sm.o[2][r][idx] + sm.o[3][r][idx]);
-      float l = 0.0f;
+      float lt = 0.0f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        l += sm.l[k][r] * (mm == kNegInf ? 1.0f : ex2_approx(sm.m[k][r] - mm));
+      for (int k = 0; k < 4; ++k) lt += sm.l[k][r] * ex2_approx(sm.m[k][r] - mm);
       if (whole) {
         const int rr = row_first + r;
         const int j = rr / a.group;
-        if (d < D)
-          static_cast<T*>(a.out)[(w.q.row0 + j) * a.out_token +
-                                 (head * a.group + (rr - j * a.group)) * a.out_head + d] =
-              to_out<T>(l == 0.0f ? 0.0f : acc / l);
+        if (kFull || d < D)
+          store_out(a,
+                    (row0 + j) * a.out_token + (out_head + (rr - j * a.group)) * a.out_head + d,
+                    lt == 0.0f ? 0.0f : acc / lt);
       } else {
-        part[2 * kRows + r * HSP + d] = acc;
+        part[2 * kMaxRows + r * HSP + d] = acc;
         if (d == 0) {
           part[r] = mm;
-          part[kRows + r] = l;
+          part[kMaxRows + r] = lt;
         }
       }
     }
-    if (!whole && tile0 == 0) {
+    if (!whole && begins) {
       left_open = true;
       if (gtid == 0) {
         header[kHeadPieces] =
-            1 + static_cast<int>((w.tiles - count + share - 1) / share);
-        header[kHeadRow0] = w.q.row0;
+            1 + static_cast<int>((piece.w.tiles - piece.count + share - 1) / share);
+        header[kHeadRow0] = row0;
         header[kHeadFirst] = row_first;
-        header[kHeadHead] = head;
+        header[kHeadHead] = piece.head;
         header[kHeadRows] = rows;
       }
     }
@@ -552,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_rows_sm103a_kernel(const A
 // last piece begins the unit. Piece 0 is that worker's second slot, piece i the
 // first slot of worker + i. Warp w takes pieces w, w + 4, ...; the four sums
 // are added in order.
-template <int HSP, typename T>
+template <int HSP>
 __global__ void __launch_bounds__(128) attend_join_sm103a_kernel(const AttendArgs a) {
   __shared__ float s_o[4][HSP];
   __shared__ float s_l[4], s_m[4];
@@ -570,7 +666,7 @@ __global__ void __launch_bounds__(128) attend_join_sm103a_kernel(const AttendArg
     return a.parts + static_cast<long long>(slot) * a.part_floats;
   };
   for (int r = 0; r < rows; ++r) {
-    float m = kNegInf;
+    float m = kNothing;
     for (int i = threadIdx.x; i < pieces; i += 128) m = fmaxf(m, part_of(i)[r]);
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
@@ -581,11 +677,11 @@ __global__ void __launch_bounds__(128) attend_join_sm103a_kernel(const AttendArg
 #pragma unroll 4
     for (int i = warp; i < pieces; i += 4) {
       const float* p = part_of(i);
-      const float c = m == kNegInf ? 1.0f : ex2_approx(p[r] - m);
-      l = fmaf(p[kRows + r], c, l);
+      const float c = ex2_approx(p[r] - m);
+      l = fmaf(p[kMaxRows + r], c, l);
 #pragma unroll
       for (int k = 0; k < E; ++k)
-        acc[k] = fmaf(p[2 * kRows + r * HSP + lane * E + k], c, acc[k]);
+        acc[k] = fmaf(p[2 * kMaxRows + r * HSP + lane * E + k], c, acc[k]);
     }
 #pragma unroll
     for (int k = 0; k < E; ++k) s_o[warp][lane * E + k] = acc[k];
@@ -596,35 +692,39 @@ __global__ void __launch_bounds__(128) attend_join_sm103a_kernel(const AttendArg
     const int j = rr / a.group;
     const int d = threadIdx.x;
     if (d < a.v.head_size)
-      static_cast<T*>(a.out)[(row0 + j) * a.out_token +
-                             (head * a.group + (rr - j * a.group)) * a.out_head + d] =
-          to_out<T>(lt == 0.0f
-                        ? 0.0f
-                        : ((s_o[0][d] + s_o[1][d]) + (s_o[2][d] + s_o[3][d])) / lt);
+      store_out(a, (row0 + j) * a.out_token + (head * a.group + (rr - j * a.group)) * a.out_head + d,
+                lt == 0.0f ? 0.0f
+                           : ((s_o[0][d] + s_o[1][d]) + (s_o[2][d] + s_o[3][d])) / lt);
     __syncthreads();
   }
 }
 
-template <int HSP, int kFormat, typename T>
-cudaError_t launch_rows(const AttendArgs& a, int sms, const DeviceInfo& dev, cudaStream_t stream,
-                        int& rc, std::string& err) {
-  const int smem = static_cast<int>(sizeof(GroupSmem<HSP>)) * kGroups;
+template <int HSP, int NB, int kFormat, bool kFull>
+cudaError_t launch_rows(AttendArgs a, int sms, const DeviceInfo& dev, cudaStream_t stream, int& rc,
+                        std::string& err) {
+  const int smem = static_cast<int>(sizeof(GroupSmem<HSP, NB>)) * kGroups<NB>;
+  a.workers = sms * kGroups<NB>;
   rc = set_max_dynamic_smem(
-      reinterpret_cast<const void*>(attend_rows_sm103a_kernel<HSP, kFormat, T>), smem, dev.device,
-      err);
+      reinterpret_cast<const void*>(attend_rows_sm103a_kernel<HSP, NB, kFormat, kFull>), smem,
+      dev.device, err);
   if (rc != CSA_OK) return cudaSuccess;
-  cudaError_t e = launch_programmatic(attend_rows_sm103a_kernel<HSP, kFormat, T>,
-                                      static_cast<unsigned>(sms), kThreads, smem, stream, a);
+  cudaError_t e = launch_programmatic(attend_rows_sm103a_kernel<HSP, NB, kFormat, kFull>,
+                                      static_cast<unsigned>(sms), 128 * kGroups<NB>, smem, stream,
+                                      a);
   if (e != cudaSuccess) return e;
-  return launch_programmatic(attend_join_sm103a_kernel<HSP, T>, static_cast<unsigned>(a.workers),
-                             128, 0, stream, a);
+  return launch_programmatic(attend_join_sm103a_kernel<HSP>, static_cast<unsigned>(a.workers), 128,
+                             0, stream, a);
 }
 
-template <int HSP, int kFormat>
-cudaError_t launch_rows_t(int dtype, const AttendArgs& a, int sms, const DeviceInfo& dev,
-                          cudaStream_t stream, int& rc, std::string& err) {
-  return dtype == CSA_F16 ? launch_rows<HSP, kFormat, __half>(a, sms, dev, stream, rc, err)
-                          : launch_rows<HSP, kFormat, __nv_bfloat16>(a, sms, dev, stream, rc, err);
+template <int HSP, int NB>
+cudaError_t launch_rows(const AttendArgs& a, int format, int sms, const DeviceInfo& dev,
+                        cudaStream_t stream, int& rc, std::string& err) {
+  const bool full = a.v.head_size == HSP;
+  if (format == CSA_KV_INT8)
+    return full ? launch_rows<HSP, NB, CSA_KV_INT8, true>(a, sms, dev, stream, rc, err)
+                : launch_rows<HSP, NB, CSA_KV_INT8, false>(a, sms, dev, stream, rc, err);
+  return full ? launch_rows<HSP, NB, CSA_KV_E4M3, true>(a, sms, dev, stream, rc, err)
+              : launch_rows<HSP, NB, CSA_KV_E4M3, false>(a, sms, dev, stream, rc, err);
 }
 
 int padded_head(int head_size) { return head_size <= 64 ? 64 : 128; }
@@ -634,7 +734,8 @@ int padded_head(int head_size) { return head_size <= 64 ? 64 : 128; }
 size_t cache_attention_workspace_bytes(int head_size) {
   return static_cast<size_t>(kMaxWorkers) * 8 * sizeof(int) +
          static_cast<size_t>(2 * kMaxWorkers) *
-             (2 * kRows + kRows * static_cast<size_t>(padded_head(head_size))) * sizeof(float);
+             (2 * kMaxRows + kMaxRows * static_cast<size_t>(padded_head(head_size))) *
+             sizeof(float);
 }
 
 int cache_attention_launch(const csa_kv_cache& cache, const csa_kv_batch& batch,
@@ -648,27 +749,27 @@ int cache_attention_launch(const csa_kv_cache& cache, const csa_kv_batch& batch,
   a.q_head = call.q_head;
   a.out_token = call.out_token;
   a.out_head = call.out_head;
+  a.half = call.dtype == CSA_F16;
   a.group = call.q_heads / cache.heads;
   a.window = call.window;
   a.sinks = call.window > 0 ? call.sinks : 0;
   a.scale_log2 = static_cast<float>(static_cast<double>(call.scale) * 1.4426950408889634);
   const int sms = std::min(dev.sm_count, kMaxSms);
-  a.workers = sms * kGroups;
+  a.workers = 0;
   a.row_limit = 0x7FFFFFFF;
   const int hsp = padded_head(cache.head_size);
   a.headers = static_cast<int*>(call.workspace);
   a.parts = reinterpret_cast<float*>(a.headers + kMaxWorkers * 8);
-  a.part_floats = 2 * kRows + kRows * hsp;
+  a.part_floats = 2 * kMaxRows + kMaxRows * hsp;
+  const bool one = static_cast<long long>(batch.max_new) * a.group <= 8;
   int rc = CSA_OK;
   cudaError_t e;
   if (hsp == 64)
-    e = cache.format == CSA_KV_INT8
-            ? launch_rows_t<64, CSA_KV_INT8>(call.dtype, a, sms, dev, stream, rc, err)
-            : launch_rows_t<64, CSA_KV_E4M3>(call.dtype, a, sms, dev, stream, rc, err);
+    e = one ? launch_rows<64, 1>(a, cache.format, sms, dev, stream, rc, err)
+            : launch_rows<64, 2>(a, cache.format, sms, dev, stream, rc, err);
   else
-    e = cache.format == CSA_KV_INT8
-            ? launch_rows_t<128, CSA_KV_INT8>(call.dtype, a, sms, dev, stream, rc, err)
-            : launch_rows_t<128, CSA_KV_E4M3>(call.dtype, a, sms, dev, stream, rc, err);
+    e = one ? launch_rows<128, 1>(a, cache.format, sms, dev, stream, rc, err)
+            : launch_rows<128, 2>(a, cache.format, sms, dev, stream, rc, err);
   if (rc != CSA_OK) {
     err = "cache_attention_forward: " + err;
     return rc;

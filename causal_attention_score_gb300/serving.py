@@ -12,7 +12,7 @@ import math
 import torch
 
 from . import _lib
-from .ops import _need, _stream_ptr
+from .ops import _need
 
 CSA_BF16, CSA_F16, CSA_F32 = 0, 1, 2
 CSA_KV_INT8, CSA_KV_E4M3 = 0, 1
@@ -22,13 +22,19 @@ _FORMAT = {torch.int8: CSA_KV_INT8, torch.float8_e4m3fn: CSA_KV_E4M3}
 _SCALING = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
 
 
-def _on_device(t: torch.Tensor, name: str) -> int:
-    """The tensor's device index: the current device, on which every call works."""
-    i = t.device.index
-    if i != torch.cuda.current_device():
-        raise ValueError(f"{name} is on cuda:{i}, but calls work on the current device "
+def _on_device(t: torch.Tensor, name: str) -> None:
+    """Every call works on the current device: its tensors must be there."""
+    if t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on {t.device}, but calls work on the current device "
                          f"cuda:{torch.cuda.current_device()}")
-    return i
+
+
+def _stream_ptr(stream) -> int:
+    """The raw handle of ``stream``, by default of the current device's current stream
+    (asked for directly: building a torch.cuda.Stream takes as long as a launch)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _rows(t: torch.Tensor, name: str, shape, dtypes) -> tuple[int, int]:
@@ -52,9 +58,10 @@ def _rows(t: torch.Tensor, name: str, shape, dtypes) -> tuple[int, int]:
 
 
 def _same_storage(tensors, ptrs, what: str) -> None:
-    if [t.data_ptr() for t in tensors] != ptrs:
-        raise ValueError(f"a tensor of this {what} no longer has the storage it was made with; "
-                         f"make a new {what}")
+    for t, p in zip(tensors, ptrs):
+        if t.data_ptr() != p:
+            raise ValueError(f"a tensor of this {what} no longer has the storage it was made "
+                             f"with; make a new {what}")
 
 
 class RotaryTable:
