@@ -36,7 +36,7 @@
 // contiguous bytes of a V row that a lane loads are 16 rows of V^T.
 //
 // Work split: all (sequence, head, row block) units in a row, each of as many
-// 64-token tiles as its rows see; every group of four warps takes an equal run
+// tiles of tokens as its rows see; every group of four warps takes an equal run
 // of tiles, wherever it begins and ends, so ragged batches and few sequences
 // alike use every SM. A group that covers a unit writes its rows; the others
 // leave (m, l, O) in the workspace, and a second kernel joins them in a fixed
@@ -57,13 +57,16 @@
 namespace csa {
 namespace {
 
-// Groups of four warps per CTA (one CTA per SM): 512 threads of 128 registers
-// with one 8-row block, 384 of 168 with two.
+// Groups of four warps per CTA (one CTA per SM): 384 threads of 168 registers
+// with one 8-row block, 256 of up to 255 with two.
 template <int NB>
-constexpr int kGroups = NB == 1 ? 4 : 3;
-constexpr int kTileTokens = 64;             // per group and step: 16 a warp
+constexpr int kGroups = NB == 1 ? 3 : 2;
+// A warp takes kSub blocks of 16 tokens per step, all in one page: two where pages hold 32
+// tokens or more. A tile is what a group's four warps take.
+template <int kSub>
+constexpr int kTileTokens = 64 * kSub;
 constexpr int kMaxSms = 152;
-constexpr int kMaxWorkers = kMaxSms * 4;
+constexpr int kMaxWorkers = kMaxSms * 3;
 constexpr int kMaxRows = 16;
 constexpr float kRaise = 8.0f;              // the running maximum is raised past this
 // The running maximum of a row that has seen nothing: finite, so that
@@ -123,14 +126,14 @@ __device__ __forceinline__ void store_out(const AttendArgs& a, long long at, flo
     static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
 }
 
-// What a sequence asks for: rows (tokens x group), their 64-token tiles (the
+// What a sequence asks for: rows (tokens x group), their tiles of tokens (the
 // first `sink_tiles`, then those from `window_tile` on).
 struct SeqWork {
   KvSequence q;
   int rows, blocks, tiles, sink_tiles, window_tile;
 };
 
-template <int NB>
+template <int NB, int kSub>
 __device__ __forceinline__ SeqWork seq_work(const AttendArgs& a, int s) {
   SeqWork w;
   w.q = kv_sequence(a.v, s);
@@ -142,12 +145,13 @@ __device__ __forceinline__ SeqWork seq_work(const AttendArgs& a, int s) {
   w.rows = static_cast<int>(rows);
   w.blocks = (w.rows + 8 * NB - 1) / (8 * NB);
   w.sink_tiles = w.window_tile = 0;
-  const int all = (w.q.length + kTileTokens - 1) / kTileTokens;
+  constexpr int T = kTileTokens<kSub>;
+  const int all = (w.q.length + T - 1) / T;
   if (a.window > 0) {
     const int from = max(max(w.q.first, 0) - a.window + 1, 0);  // first key any row's window has
-    w.window_tile = from / kTileTokens;
+    w.window_tile = from / T;
     const int sinks = min(a.sinks, from);
-    w.sink_tiles = min((sinks + kTileTokens - 1) / kTileTokens, w.window_tile);
+    w.sink_tiles = min((sinks + T - 1) / T, w.window_tile);
   }
   w.tiles = max(1, w.sink_tiles + all - w.window_tile);  // rows that see nothing: one, for their zeros
   return w;
@@ -164,7 +168,7 @@ struct Piece {
   int tile0, count;           // its tiles [tile0, tile0 + count); count 0: no more pieces
 };
 
-template <int NB>
+template <int NB, int kSub>
 __device__ __forceinline__ void next_piece(const AttendArgs& a, Piece& p) {
   p.count = 0;
   if (p.at >= p.end) return;
@@ -173,7 +177,7 @@ __device__ __forceinline__ void next_piece(const AttendArgs& a, Piece& p) {
     units = static_cast<long long>(p.w.blocks) * a.v.heads;
     if (p.at < p.base + units * p.w.tiles) break;
     p.base += units * p.w.tiles;
-    p.w = seq_work<NB>(a, ++p.s);
+    p.w = seq_work<NB, kSub>(a, ++p.s);
   }
   const long long off = p.at - p.base;
   const int unit = static_cast<int>(off / p.w.tiles);
@@ -201,7 +205,7 @@ struct GroupSmem {
 
 // HSP: head size padded to 64 or 128; kFull: head_size == HSP (no bounds on the
 // element loads).
-template <int HSP, int NB, int kFormat, bool kFull>
+template <int HSP, int NB, int kSub, int kFormat, bool kFull>
 __global__ void __launch_bounds__(128 * kGroups<NB>, 1)
     attend_rows_sm103a_kernel(const AttendArgs a) {
   constexpr int kThreads = 128 * kGroups<NB>;
@@ -227,7 +231,7 @@ __global__ void __launch_bounds__(128 * kGroups<NB>, 1)
     long long mine = 0;
     const long long from = static_cast<long long>(threadIdx.x) * c;
     for (long long s = from; s < min(static_cast<long long>(S), from + c); ++s) {
-      const SeqWork w = seq_work<NB>(a, static_cast<int>(s));
+      const SeqWork w = seq_work<NB, kSub>(a, static_cast<int>(s));
       mine += static_cast<long long>(w.blocks) * w.tiles * a.v.heads;
     }
     long long sum = mine;
@@ -269,17 +273,82 @@ __global__ void __launch_bounds__(128 * kGroups<NB>, 1)
       }
       p.s = lo * c;
       p.base = s_prefix[lo];
-      p.w = seq_work<NB>(a, p.s);
+      p.w = seq_work<NB, kSub>(a, p.s);
     }
   }
   for (;;) {
-    if (gtid == 0) next_piece<NB>(a, sm.piece);
+    if (gtid == 0) next_piece<NB, kSub>(a, sm.piece);
     group_sync(gi);
     const volatile Piece& piece = sm.piece;
     const int count = piece.count;
     if (count == 0) break;
     const int s = piece.s, head = piece.head, tile0 = piece.tile0;
     const int length = piece.w.q.length;
+
+    // K's chunks and V's of the step's blocks as they come from HBM, their page's scales.
+    uint4 kr[kSub][2][kChunks];
+    uint32_t vr[kSub][4][kVWords];
+    float ks = 1.0f, vs = 1.0f;
+    const int sink_tiles = piece.w.sink_tiles, window_skip = piece.w.window_tile - sink_tiles;
+    // First token of this warp's in step i, and its page (-1: nothing there).
+    auto token_of = [&](int i) {
+      const int tile = tile0 + i;
+      return (tile < sink_tiles ? tile : tile + window_skip) * kTileTokens<kSub> +
+             warp * (16 * kSub);
+    };
+    auto page_of = [&](int i) {
+      if (i >= count) return -1;
+      const int tb = token_of(i);
+      return tb < length ? kv_page(a.v, s, tb >> a.v.page_shift) : -1;
+    };
+    // Lane (g, t): tokens g and g + 8, chunks t and t + 4 of their K rows; tokens
+    // 2t, 2t + 1, 2t + 8, 2t + 9, chunk g of their V rows.
+    const uint8_t* k_lane = a.v.codes[0] + (g * D + t * 16);
+    const uint8_t* v_lane = a.v.codes[1] + (2 * t * D + g * kVBytes);
+    const int page_bytes = a.v.page_tokens * D;
+    auto load_k = [&](int tb, int page) {
+      const long long unit = static_cast<long long>(page) * a.v.heads + head;
+      const uint8_t* from = k_lane + (unit * page_bytes + (tb & (a.v.page_tokens - 1)) * D);
+#pragma unroll
+      for (int u = 0; u < kSub; ++u)
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int h = 0; h < kChunks; ++h)
+            kr[u][n][h] = kFull || (4 * h + t) * 16 < D
+                              ? __ldg(reinterpret_cast<const uint4*>(from + (16 * u + 8 * n) * D +
+                                                                     64 * h))
+                              : make_uint4(0, 0, 0, 0);
+      ks = __ldg(a.v.scale[0] + unit);
+    };
+    auto load_v = [&](int tb, int page) {
+      const long long unit = static_cast<long long>(page) * a.v.heads + head;
+      const uint8_t* from = v_lane + (unit * page_bytes + (tb & (a.v.page_tokens - 1)) * D);
+      const bool in = kFull || g * kVBytes < D;
+#pragma unroll
+      for (int u = 0; u < kSub; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint8_t* row = from + (16 * u + (i & 1) + 8 * (i >> 1)) * D;
+          if constexpr (kVWords == 4) {
+            const uint4 x = in ? __ldg(reinterpret_cast<const uint4*>(row)) : make_uint4(0, 0, 0, 0);
+            vr[u][i][0] = x.x;
+            vr[u][i][1] = x.y;
+            vr[u][i][2] = x.z;
+            vr[u][i][3] = x.w;
+          } else {
+            const uint2 x = in ? __ldg(reinterpret_cast<const uint2*>(row)) : make_uint2(0, 0);
+            vr[u][i][0] = x.x;
+            vr[u][i][1] = x.y;
+          }
+        }
+      vs = __ldg(a.v.scale[1] + unit);
+    };
+    int page = page_of(0), page_next = page_of(1);
+    if (page >= 0) {
+      load_k(token_of(0), page);
+      load_v(token_of(0), page);
+    }
 
     // ------------------------------------------------------ Q's fragments --
     // Lane (g, t): row g (and g + 8), the 16 elements of chunks t and t + 4.
@@ -363,71 +432,17 @@ __global__ void __launch_bounds__(128 * kGroups<NB>, 1)
       l[b][0] = l[b][1] = 0.0f;
     }
 
-    uint4 kr[2][kChunks];
-    uint32_t vr[4][kVWords];
-    float ks = 0.0f, vs = 1.0f;
-    const int sink_tiles = piece.w.sink_tiles, window_skip = piece.w.window_tile - sink_tiles;
-    // First token of this warp's 16 in step i, and its page (-1: nothing there).
-    auto token_of = [&](int i) {
-      const int tile = tile0 + i;
-      return (tile < sink_tiles ? tile : tile + window_skip) * kTileTokens + warp * 16;
-    };
-    auto page_of = [&](int i) {
-      if (i >= count) return -1;
-      const int tb = token_of(i);
-      return tb < length ? kv_page(a.v, s, tb >> a.v.page_shift) : -1;
-    };
-    // Lane (g, t): tokens g and g + 8, chunks t and t + 4 of their K rows; tokens
-    // 2t, 2t + 1, 2t + 8, 2t + 9, chunk g of their V rows.
-    const int k_lane = g * D + t * 16, v_lane = 2 * t * D + g * kVBytes;
-    auto load_k = [&](int tb, int page) {
-      const uint8_t* from = a.v.codes[0] + kv_page_offset(a.v, page, head) +
-                            ((tb & (a.v.page_tokens - 1)) * D + k_lane);
-#pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int h = 0; h < kChunks; ++h)
-          kr[n][h] = kFull || (4 * h + t) * 16 < D
-                         ? __ldg(reinterpret_cast<const uint4*>(from + 8 * n * D + 64 * h))
-                         : make_uint4(0, 0, 0, 0);
-      ks = __ldg(a.v.scale[0] + (static_cast<long long>(page) * a.v.heads + head));
-    };
-    auto load_v = [&](int tb, int page) {
-      const uint8_t* from = a.v.codes[1] + kv_page_offset(a.v, page, head) +
-                            ((tb & (a.v.page_tokens - 1)) * D + v_lane);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint8_t* row = from + ((i & 1) + 8 * (i >> 1)) * D;
-        const bool in = kFull || g * kVBytes < D;
-        if constexpr (kVWords == 4) {
-          const uint4 x = in ? __ldg(reinterpret_cast<const uint4*>(row)) : make_uint4(0, 0, 0, 0);
-          vr[i][0] = x.x;
-          vr[i][1] = x.y;
-          vr[i][2] = x.z;
-          vr[i][3] = x.w;
-        } else {
-          const uint2 x = in ? __ldg(reinterpret_cast<const uint2*>(row)) : make_uint2(0, 0);
-          vr[i][0] = x.x;
-          vr[i][1] = x.y;
-        }
-      }
-      vs = __ldg(a.v.scale[1] + (static_cast<long long>(page) * a.v.heads + head));
-    };
-
-    int page = page_of(0), page_next = page_of(1);
-    if (page >= 0) {
-      load_k(token_of(0), page);
-      load_v(token_of(0), page);
-    }
     for (int i = 0; i < count; ++i) {
       const int tb = token_of(i);
       const int page_after = page_of(i + 2);
       if (page >= 0) {
-        float sc[NB][4] = {};
+        float sc[kSub][NB][4];
 #pragma unroll
-        for (int h = 0; h < kChunks; ++h) {
-          const uint32_t* k0 = reinterpret_cast<const uint32_t*>(&kr[0][h]);
-          const uint32_t* k1 = reinterpret_cast<const uint32_t*>(&kr[1][h]);
+        for (int u = 0; u < kSub; ++u)
+#pragma unroll
+          for (int b = 0; b < NB; ++b) sc[u][b][0] = sc[u][b][1] = sc[u][b][2] = sc[u][b][3] = 0.0f;
+#pragma unroll
+        for (int h = 0; h < kChunks; ++h)
 #pragma unroll
           for (int k2 = 0; k2 < 2; ++k2) {
             uint32_t q4[NB][4];
@@ -441,20 +456,23 @@ __global__ void __launch_bounds__(128 * kGroups<NB>, 1)
                 q4[b][3] = x.w;
               } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) q4[b][i] = qf[b][h][4 * k2 + i];
+                for (int e = 0; e < 4; ++e) q4[b][e] = qf[b][h][4 * k2 + e];
               }
             }
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              uint32_t a0, a1, a2, a3;
-              codes4_to_half2x2<kFormat>(k0[2 * k2 + k], a0, a2);
-              codes4_to_half2x2<kFormat>(k1[2 * k2 + k], a1, a3);
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
-              for (int b = 0; b < NB; ++b)
-                mma_f16(sc[b], a0, a1, a2, a3, q4[b][2 * k], q4[b][2 * k + 1]);
-            }
+              for (int u = 0; u < kSub; ++u) {
+                const uint32_t* k0 = reinterpret_cast<const uint32_t*>(&kr[u][0][h]);
+                const uint32_t* k1 = reinterpret_cast<const uint32_t*>(&kr[u][1][h]);
+                uint32_t a0, a1, a2, a3;
+                codes4_to_half2x2<kFormat>(k0[2 * k2 + k], a0, a2);
+                codes4_to_half2x2<kFormat>(k1[2 * k2 + k], a1, a3);
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+                  mma_f16(sc[u][b], a0, a1, a2, a3, q4[b][2 * k], q4[b][2 * k + 1]);
+              }
           }
-        }
         const float lv = __log2f(vs), inv = __fdividef(1.0f, vs);
         float fk[NB][2];
 #pragma unroll
@@ -463,102 +481,119 @@ __global__ void __launch_bounds__(128 * kGroups<NB>, 1)
           fk[b][1] = fr[b][1] * ks;
         }
         if (page_next >= 0) load_k(token_of(i + 1), page_next);
-        // sc element e: token g + 8 (e / 2), row 2t + e % 2
-        const bool open = tb + 15 <= pos_low &&
-                          (a.window == 0 || pos_high - tb < a.window || tb + 15 < a.sinks);
-        float x[NB][4];
+        // sc element e: token g + 8 (e / 2), row 2t + e % 2. A masked score is -inf, and
+        // stays so whatever the scales.
+        const int last = tb + 16 * kSub - 1;
+        const bool open = last <= pos_low &&
+                          (a.window == 0 || pos_high - tb < a.window || last < a.sinks);
+        float x[kSub][NB][4];
         bool raise = false;
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+        for (int u = 0; u < kSub; ++u)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (!open) {
-              const int tok = tb + g + 8 * (e >> 1), p = pr[b][e & 1];
-              if (tok > p || (a.window != 0 && p - tok >= a.window && tok >= a.sinks))
-                sc[b][e] = -INFINITY;
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              x[u][b][e] = fmaf(sc[u][b][e], fk[b][e & 1], lv - m[b][e & 1]);
+              if (!open) {
+                const int tok = tb + 16 * u + g + 8 * (e >> 1), p = pr[b][e & 1];
+                if (tok > p || (a.window != 0 && p - tok >= a.window && tok >= a.sinks)) {
+                  sc[u][b][e] = -INFINITY;
+                  x[u][b][e] = -INFINITY;
+                }
+              }
+              raise |= x[u][b][e] > kRaise;
             }
-            // a masked score stays -inf through the scale, whatever its sign or value
-            x[b][e] = sc[b][e] == -INFINITY ? -INFINITY
-                                            : fmaf(sc[b][e], fk[b][e & 1], lv - m[b][e & 1]);
-            raise |= x[b][e] > kRaise;
-          }
         if (__any_sync(0xFFFFFFFFu, raise)) {
 #pragma unroll
           for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              float y[2], most;
+              float y[kSub][2], most = -INFINITY;
 #pragma unroll
-              for (int n = 0; n < 2; ++n)
-                y[n] = sc[b][2 * n + r] == -INFINITY ? -INFINITY
-                                                     : fmaf(sc[b][2 * n + r], fk[b][r], lv);
-              most = fmaxf(y[0], y[1]);
+              for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                  y[u][n] = sc[u][b][2 * n + r] == -INFINITY
+                                ? -INFINITY
+                                : fmaf(sc[u][b][2 * n + r], fk[b][r], lv);
+                  most = fmaxf(most, y[u][n]);
+                }
               most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 4));
               most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 8));
               most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 16));
-              const float n = fmaxf(m[b][r], most);
-              const float corr = ex2_approx(m[b][r] - n);
-              m[b][r] = n;
+              const float top = fmaxf(m[b][r], most);
+              const float corr = ex2_approx(m[b][r] - top);
+              m[b][r] = top;
               l[b][r] *= corr;
 #pragma unroll
               for (int j = 0; j < kTilesM; ++j) {
                 o[b][j][r] *= corr;
                 o[b][j][2 + r] *= corr;
               }
-              x[b][r] = y[0] - n;
-              x[b][2 + r] = y[1] - n;
+#pragma unroll
+              for (int u = 0; u < kSub; ++u)
+#pragma unroll
+                for (int n = 0; n < 2; ++n) x[u][b][2 * n + r] = y[u][n] - top;
             }
         }
-        uint32_t pb[NB][2];
+        uint32_t pb[kSub][NB][2];
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[b][e] = ex2_approx(x[b][e]);
-          l[b][0] = fmaf(x[b][0] + x[b][2], inv, l[b][0]);
-          l[b][1] = fmaf(x[b][1] + x[b][3], inv, l[b][1]);
-          pb[b][0] = transpose_8x8(half2_of(x[b][0], x[b][1]));
-          pb[b][1] = transpose_8x8(half2_of(x[b][2], x[b][3]));
-        }
-        if (tb + 16 > length) {
-          // slots past the sequence's end may hold the codes of no number
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (tb + 2 * t + (k & 1) + 8 * (k >> 1) >= length) {
-#pragma unroll
-              for (int j = 0; j < kVWords; ++j) vr[k][j] = 0;
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < kVWords; ++j) {
-          // four elements of two token pairs: bytes to (token, token + 1) pairs
-          uint32_t f[4][2];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            uint32_t u = vr[2 * k][j], v = vr[2 * k + 1][j];
-            if (kFormat == CSA_KV_INT8) {
-              u ^= 0x80808080u;
-              v ^= 0x80808080u;
-            }
-            const uint32_t lo = byte_perm(u, v, 0x5140), hi = byte_perm(u, v, 0x7362);
-            if (kFormat == CSA_KV_INT8) {
-              f[0][k] = flipped_pair_to_half2<0x4140>(lo);
-              f[1][k] = flipped_pair_to_half2<0x4342>(lo);
-              f[2][k] = flipped_pair_to_half2<0x4140>(hi);
-              f[3][k] = flipped_pair_to_half2<0x4342>(hi);
-            } else {
-              f[0][k] = e4m3x2_to_half2(lo & 0xFFFFu);
-              f[1][k] = e4m3x2_to_half2(lo >> 16);
-              f[2][k] = e4m3x2_to_half2(hi & 0xFFFFu);
-              f[3][k] = e4m3x2_to_half2(hi >> 16);
-            }
-          }
-          // m-tile 2j: elements 4j (rows g) and 4j + 1 (rows g + 8) of the chunk
+        for (int u = 0; u < kSub; ++u)
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
-            mma_f16(o[b][2 * j], f[0][0], f[1][0], f[0][1], f[1][1], pb[b][0], pb[b][1]);
-            mma_f16(o[b][2 * j + 1], f[2][0], f[3][0], f[2][1], f[3][1], pb[b][0], pb[b][1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[u][b][e] = ex2_approx(x[u][b][e]);
+            l[b][0] = fmaf(x[u][b][0] + x[u][b][2], inv, l[b][0]);
+            l[b][1] = fmaf(x[u][b][1] + x[u][b][3], inv, l[b][1]);
+            pb[u][b][0] = transpose_8x8(half2_of(x[u][b][0], x[u][b][1]));
+            pb[u][b][1] = transpose_8x8(half2_of(x[u][b][2], x[u][b][3]));
           }
+        if (last >= length) {
+          // slots past the sequence's end may hold the codes of no number
+#pragma unroll
+          for (int u = 0; u < kSub; ++u)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (tb + 16 * u + 2 * t + (k & 1) + 8 * (k >> 1) >= length) {
+#pragma unroll
+                for (int j = 0; j < kVWords; ++j) vr[u][k][j] = 0;
+              }
         }
+#pragma unroll
+        for (int u = 0; u < kSub; ++u)
+#pragma unroll
+          for (int j = 0; j < kVWords; ++j) {
+            // four elements of two token pairs: bytes to (token, token + 1) pairs
+            uint32_t f[4][2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              uint32_t v0 = vr[u][2 * k][j], v1 = vr[u][2 * k + 1][j];
+              if (kFormat == CSA_KV_INT8) {
+                v0 ^= 0x80808080u;
+                v1 ^= 0x80808080u;
+              }
+              const uint32_t lo = byte_perm(v0, v1, 0x5140), hi = byte_perm(v0, v1, 0x7362);
+              if (kFormat == CSA_KV_INT8) {
+                f[0][k] = flipped_pair_to_half2<0x4140>(lo);
+                f[1][k] = flipped_pair_to_half2<0x4342>(lo);
+                f[2][k] = flipped_pair_to_half2<0x4140>(hi);
+                f[3][k] = flipped_pair_to_half2<0x4342>(hi);
+              } else {
+                f[0][k] = e4m3x2_to_half2(lo & 0xFFFFu);
+                f[1][k] = e4m3x2_to_half2(lo >> 16);
+                f[2][k] = e4m3x2_to_half2(hi & 0xFFFFu);
+                f[3][k] = e4m3x2_to_half2(hi >> 16);
+              }
+            }
+            // m-tile 2j: elements 4j (rows g) and 4j + 1 (rows g + 8) of the chunk
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+              mma_f16(o[b][2 * j], f[0][0], f[1][0], f[0][1], f[1][1], pb[u][b][0], pb[u][b][1]);
+              mma_f16(o[b][2 * j + 1], f[2][0], f[3][0], f[2][1], f[3][1], pb[u][b][0],
+                      pb[u][b][1]);
+            }
+          }
       } else if (page_next >= 0) {
         load_k(token_of(i + 1), page_next);
       }
@@ -699,32 +734,37 @@ __global__ void __launch_bounds__(128) attend_join_sm103a_kernel(const AttendArg
   }
 }
 
-template <int HSP, int NB, int kFormat, bool kFull>
+template <int HSP, int NB, int kSub, int kFormat, bool kFull>
 cudaError_t launch_rows(AttendArgs a, int sms, const DeviceInfo& dev, cudaStream_t stream, int& rc,
                         std::string& err) {
+  const auto kernel = attend_rows_sm103a_kernel<HSP, NB, kSub, kFormat, kFull>;
   const int smem = static_cast<int>(sizeof(GroupSmem<HSP, NB>)) * kGroups<NB>;
   a.workers = sms * kGroups<NB>;
-  rc = set_max_dynamic_smem(
-      reinterpret_cast<const void*>(attend_rows_sm103a_kernel<HSP, NB, kFormat, kFull>), smem,
-      dev.device, err);
+  rc = set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), smem, dev.device, err);
   if (rc != CSA_OK) return cudaSuccess;
-  cudaError_t e = launch_programmatic(attend_rows_sm103a_kernel<HSP, NB, kFormat, kFull>,
-                                      static_cast<unsigned>(sms), 128 * kGroups<NB>, smem, stream,
-                                      a);
+  cudaError_t e = launch_programmatic(kernel, static_cast<unsigned>(sms), 128 * kGroups<NB>, smem,
+                                      stream, a);
   if (e != cudaSuccess) return e;
   return launch_programmatic(attend_join_sm103a_kernel<HSP>, static_cast<unsigned>(a.workers), 128,
                              0, stream, a);
 }
 
-template <int HSP, int NB>
+template <int HSP, int NB, int kSub>
 cudaError_t launch_rows(const AttendArgs& a, int format, int sms, const DeviceInfo& dev,
                         cudaStream_t stream, int& rc, std::string& err) {
   const bool full = a.v.head_size == HSP;
   if (format == CSA_KV_INT8)
-    return full ? launch_rows<HSP, NB, CSA_KV_INT8, true>(a, sms, dev, stream, rc, err)
-                : launch_rows<HSP, NB, CSA_KV_INT8, false>(a, sms, dev, stream, rc, err);
-  return full ? launch_rows<HSP, NB, CSA_KV_E4M3, true>(a, sms, dev, stream, rc, err)
-              : launch_rows<HSP, NB, CSA_KV_E4M3, false>(a, sms, dev, stream, rc, err);
+    return full ? launch_rows<HSP, NB, kSub, CSA_KV_INT8, true>(a, sms, dev, stream, rc, err)
+                : launch_rows<HSP, NB, kSub, CSA_KV_INT8, false>(a, sms, dev, stream, rc, err);
+  return full ? launch_rows<HSP, NB, kSub, CSA_KV_E4M3, true>(a, sms, dev, stream, rc, err)
+              : launch_rows<HSP, NB, kSub, CSA_KV_E4M3, false>(a, sms, dev, stream, rc, err);
+}
+
+template <int HSP, int NB>
+cudaError_t launch_rows(const AttendArgs& a, int format, int sms, const DeviceInfo& dev,
+                        cudaStream_t stream, int& rc, std::string& err) {
+  return a.v.page_tokens < 32 ? launch_rows<HSP, NB, 1>(a, format, sms, dev, stream, rc, err)
+                              : launch_rows<HSP, NB, 2>(a, format, sms, dev, stream, rc, err);
 }
 
 int padded_head(int head_size) { return head_size <= 64 ? 64 : 128; }
