@@ -68,6 +68,8 @@ constexpr int kTileTokens = 64 * kSub;
 constexpr int kMaxSms = 152;
 constexpr int kMaxWorkers = kMaxSms * 3;
 constexpr int kMaxRows = 16;
+// Sequences of more rows than this go to the prompt kernel.
+constexpr int kRowLimit = 64;
 constexpr float kRaise = 8.0f;              // the running maximum is raised past this
 // The running maximum of a row that has seen nothing: finite, so that
 // differences of two of them are 0.
@@ -796,13 +798,21 @@ int cache_attention_launch(const csa_kv_cache& cache, const csa_kv_batch& batch,
   a.scale_log2 = static_cast<float>(static_cast<double>(call.scale) * 1.4426950408889634);
   const int sms = std::min(dev.sm_count, kMaxSms);
   a.workers = 0;
-  a.row_limit = 0x7FFFFFFF;
+  a.row_limit = kRowLimit;
   const int hsp = padded_head(cache.head_size);
   a.headers = static_cast<int*>(call.workspace);
   a.parts = reinterpret_cast<float*>(a.headers + kMaxWorkers * 8);
   a.part_floats = 2 * kMaxRows + kMaxRows * hsp;
-  const bool one = static_cast<long long>(batch.max_new) * a.group <= 8;
+  const long long most_rows = static_cast<long long>(batch.max_new) * a.group;
+  const bool one = most_rows <= 8;
   int rc = CSA_OK;
+  if (most_rows > kRowLimit) {
+    rc = cache_prompt_launch(cache, batch, call, kRowLimit, stream, dev, err);
+    if (rc != CSA_OK) {
+      err = "cache_attention_forward: " + err;
+      return rc;
+    }
+  }
   cudaError_t e;
   if (hsp == 64)
     e = one ? launch_rows<64, 1>(a, cache.format, sms, dev, stream, rc, err)

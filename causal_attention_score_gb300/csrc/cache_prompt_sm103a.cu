@@ -1,0 +1,747 @@
+// Attention of many new tokens per sequence (prompts and their chunks) over the
+// paged 8-bit cache: the same function as the rows kernel of
+// cache_attention_sm103a.cu, on tcgen05.
+//
+// A unit of work is 256 rows (tokens x query heads of one kv head) of a
+// sequence: two groups A and B of 128, each a TMEM accumulator's lanes, which
+// share every tile of 128 keys. One CTA per SM walks a list of units (longest
+// first within a sequence), with 13 warps:
+//  - warps 0..7: softmax, warps 0..3 group A, 4..7 group B, a thread a row. Per
+//    tile: one pass over S in TMEM for the row's maximum, one that writes the
+//    weights exp2(x - m) as fp16 over S (P, the second product's A operand in
+//    TMEM). m is raised only when a value passes m + 8 (then the thread's O row
+//    is rescaled in TMEM). Before a unit they turn Q's rows into fp16 in shared
+//    memory; after it they write O / l.
+//  - warps 8..11: conversion. Codes come from HBM into registers a tile ahead,
+//    become fp16 exactly, and go to shared memory in the 128-byte-swizzle K-major
+//    layout: K as [token][element], V transposed in registers to
+//    [element][token]. Two stages each.
+//  - warp 12: one thread issues, per tile, O_A += P_A V, S_A = Q_A K^T of the next
+//    tile, and the same for B: while one group is in its softmax, the tensor core
+//    works for the other. MMAs run in issue order, so S_A may overwrite P_A.
+//
+// Scales (see cache_attention_sm103a.cu): with K's and V's scales per 16 tokens in
+// shared memory, x = s (c ks) + log2(vs) and the weight has V's scale in it; the
+// denominator sums w / vs.
+//
+// Bound: 4 HSP flops and one exp2 per row and key; per 256 x 128 tile 2048 cycles
+// of MMA at the dense rate and 2048 cycles of the 16-a-cycle exponential unit.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <string>
+
+#include "csa_internal.h"
+#include "kv_cache.cuh"
+#include "sm103a_ptx.cuh"
+
+namespace csa {
+namespace {
+
+constexpr int kSoftmaxWarps = 8;
+constexpr int kConvertWarps = 4;
+constexpr int kMmaWarp = kSoftmaxWarps + kConvertWarps;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kTile = 128;          // keys per tile, rows per group
+constexpr int kUnitRows = 2 * kTile;
+constexpr int kStages = 2;
+constexpr int kFactorSlots = 4;
+constexpr int kTmemCols = 512;      // S_A, S_B, O_A, O_B
+constexpr float kRaise = 8.0f;
+constexpr float kNothing = -1e30f;  // the running maximum of a row that has seen nothing
+
+struct PromptArgs {
+  KvView v;
+  const void* q;
+  void* out;
+  long long q_token, q_head, out_token, out_head;
+  int half;
+  int group;
+  int window, sinks;
+  int row_limit;        // sequences of at most this many rows are the rows kernel's
+  float scale_log2;     // its magnitude
+  uint32_t q_flip;      // sign bits flipped in Q's words where the scale is negative
+  int* status;
+  unsigned long long wait_limit_ns;
+  int inject;
+};
+
+// What 16 keys' scores are multiplied with, log2 of their V's scale, its inverse.
+struct Factor {
+  float k, log2v, inv, pad;
+};
+
+template <int HSP>
+struct Layout {
+  static constexpr int kQBytes = kTile * HSP * 2;  // per group: [HSP / 64][128 rows][128 B]
+  static constexpr int kKBytes = kTile * HSP * 2;  // per stage: the same
+  static constexpr int kVBytes = HSP * kTile * 2;  // per stage: [2][HSP rows][128 B]
+  static constexpr int kQ = 0, kK = 2 * kQBytes, kV = kK + kStages * kKBytes,
+                       kFactors = kV + kStages * kVBytes,
+                       kBars = kFactors + kFactorSlots * 8 * static_cast<int>(sizeof(Factor)),
+                       kMisc = kBars + 8 * 20, kTotal = kMisc + 16;
+};
+
+struct Unit {
+  KvSequence q;
+  int s, head, row0, rows;  // rows [row0, row0 + rows) of the sequence
+  int sink_tiles, window_tile;
+  int n[2];                 // tiles of each group
+};
+
+// The list's u-th unit: sequences in order, the last (longest) rows first.
+__device__ __forceinline__ long long units_of(const PromptArgs& a, const KvSequence& q) {
+  const long long rows = static_cast<long long>(q.n) * a.group;
+  return rows <= a.row_limit ? 0 : (rows + kUnitRows - 1) / kUnitRows * a.v.heads;
+}
+
+__device__ __forceinline__ Unit decode_unit(const PromptArgs& a, const long long* prefix, int per,
+                                            long long u) {
+  int lo = 0, hi = kThreads;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (prefix[mid] <= u) lo = mid;
+    else hi = mid;
+  }
+  Unit r;
+  long long base = prefix[lo];
+  r.s = lo * per;
+  for (;;) {
+    r.q = kv_sequence(a.v, r.s);
+    const long long n = units_of(a, r.q);
+    if (u < base + n) break;
+    base += n;
+    ++r.s;
+  }
+  const int all_rows = static_cast<int>(static_cast<long long>(r.q.n) * a.group);
+  const int blocks = (all_rows + kUnitRows - 1) / kUnitRows;
+  const int i = static_cast<int>(u - base);
+  const int back = i / a.v.heads;
+  r.head = i - back * a.v.heads;
+  r.row0 = (blocks - 1 - back) * kUnitRows;
+  r.rows = min(all_rows - r.row0, kUnitRows);
+  r.sink_tiles = r.window_tile = 0;
+  if (a.window > 0) {
+    const int from = max(max(r.q.first + r.row0 / a.group, 0) - a.window + 1, 0);
+    r.window_tile = from / kTile;
+    r.sink_tiles = min((min(a.sinks, from) + kTile - 1) / kTile, r.window_tile);
+  }
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    const int rows = min(r.rows - g * kTile, kTile);
+    r.n[g] = 0;
+    if (rows <= 0) continue;
+    const int last = r.q.first + (r.row0 + g * kTile + rows - 1) / a.group;  // position
+    if (last >= 0) r.n[g] = r.sink_tiles + max(last / kTile + 1 - r.window_tile, 0);
+  }
+  return r;
+}
+
+__device__ __forceinline__ int tile_token(const Unit& u, int j) {
+  return (j < u.sink_tiles ? j : j - u.sink_tiles + u.window_tile) * kTile;
+}
+
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Instruction descriptor, kind::f16: A = B = fp16, D = f32, both K-major.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]^T for 16-bit operands: A's 128 rows are TMEM
+// lanes, two K-elements to a 32-bit column.
+__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// 32 lanes x 16 consecutive 32-bit columns from 16 registers (no wait).
+__device__ __forceinline__ void tmem_st_16cols(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void st_shared16(uint32_t addr, const uint32_t* w) {
+  st_shared_v4(addr, w[0], w[1], w[2], w[3]);
+}
+
+template <int HSP, int kFormat>
+__global__ void __launch_bounds__(kThreads, 1)
+    attend_prompt_sm103a_kernel(const PromptArgs a) {
+  using L = Layout<HSP>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ long long s_prefix[kThreads + 1];
+  __shared__ long long s_warp[kThreads / 32];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw);
+  const uint32_t bars = base + L::kBars;
+  auto k_full = [&](uint32_t s) { return bars + 8u * s; };
+  auto k_empty = [&](uint32_t s) { return bars + 8u * (2 + s); };
+  auto v_full = [&](uint32_t s) { return bars + 8u * (4 + s); };
+  auto v_empty = [&](uint32_t s) { return bars + 8u * (6 + s); };
+  auto q_ready = [&](uint32_t g) { return bars + 8u * (8 + g); };
+  auto s_full = [&](uint32_t g) { return bars + 8u * (10 + g); };
+  auto p_ready = [&](uint32_t g) { return bars + 8u * (12 + g); };
+  auto o_full = [&](uint32_t g) { return bars + 8u * (14 + g); };
+  const uint32_t drain = bars + 8u * 16;
+  const uint32_t tmem_slot = base + L::kMisc;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::kMisc + 4);
+  Factor* factors = reinterpret_cast<Factor*>(gbase + L::kFactors);
+  const Watchdog wd{a.wait_limit_ns, a.status, abort_flag};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(k_full(s), kConvertWarps);
+      mbar_init(v_full(s), kConvertWarps);
+      mbar_init(k_empty(s), 1);
+      mbar_init(v_empty(s), 1);
+    }
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(q_ready(g), 4);
+      mbar_init(s_full(g), 1);
+      mbar_init(p_ready(g), 4);
+      mbar_init(o_full(g), 1);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_relinquish();
+    tc_fence_before_sync();
+  }
+  grid_dependency_wait();
+
+  // The work list: thread i counts the units of sequences [i per, (i + 1) per).
+  const int S = a.v.sequences;
+  const int per = (S + kThreads - 1) / kThreads;
+  {
+    long long mine = 0;
+    const long long from = static_cast<long long>(threadIdx.x) * per;
+    for (long long s = from; s < min(static_cast<long long>(S), from + per); ++s)
+      mine += units_of(a, kv_sequence(a.v, static_cast<int>(s)));
+    long long sum = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const long long up = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+      if (lane >= d) sum += up;
+    }
+    if (lane == 31) s_warp[warp] = sum;
+    __syncthreads();
+    long long before = 0;
+    for (int w = 0; w < warp; ++w) before += s_warp[w];
+    s_prefix[threadIdx.x + 1] = before + sum;
+    if (threadIdx.x == 0) s_prefix[0] = 0;
+  }
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = ld_shared_b32(tmem_slot);
+  const long long total = s_prefix[kThreads];
+  // The k-th unit of this CTA: forwards and backwards through the list in turn, so
+  // that a CTA with a long unit gets a short one next.
+  auto unit_index = [&](long long k) {
+    return k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+  };
+  const int D = a.v.head_size;
+
+  if (warp < kSoftmaxWarps) {
+    // ------------------------------------------------------------ softmax --
+    const uint32_t g = warp >> 2;
+    const int r = threadIdx.x & 127;                       // row of the group
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lane field
+    const uint32_t s_tmem = tmem + lanes + g * kTile;
+    const uint32_t o_tmem = tmem + lanes + 2 * kTile + g * HSP;
+    const uint32_t q_smem = base + L::kQ + g * L::kQBytes;
+    uint32_t tiles_done = 0, o_phase = 0;
+    uint32_t it = 0;  // tiles of the CTA so far (the factors' slots)
+    bool ok = true;
+    for (long long k = 0; ok && unit_index(k) < total; ++k) {
+      const Unit u = decode_unit(a, s_prefix, per, unit_index(k));
+      const int n = g == 0 ? u.n[0] : u.n[1], n_all = max(u.n[0], u.n[1]);
+      const int rr = u.row0 + static_cast<int>(g) * kTile + r;
+      const int j_tok = rr / a.group;
+      const bool live = static_cast<int>(g) * kTile + r < u.rows;
+      const int pos = live ? u.q.first + j_tok : -1;
+      const long long out_at = (u.q.row0 + j_tok) * a.out_token +
+                               (u.head * a.group + (rr - j_tok * a.group)) * a.out_head;
+      float l = 0.0f, m = kNothing, f = 0.0f;
+      if (n > 0) {
+        // Q's row to fp16 in shared memory (the group's last S product is complete:
+        // this thread has seen its o_full)
+        const uint32_t* from = reinterpret_cast<const uint32_t*>(
+            static_cast<const uint16_t*>(a.q) + (u.q.row0 + j_tok) * a.q_token +
+            (u.head * a.group + (rr - j_tok * a.group)) * a.q_head);
+        uint32_t w[HSP / 2];
+        float most = 0.0f;
+#pragma unroll
+        for (int i = 0; i < HSP / 8; ++i) {
+          const uint4 x = live && i * 8 < D ? reinterpret_cast<const uint4*>(from)[i]
+                                            : make_uint4(0, 0, 0, 0);
+          w[4 * i] = x.x ^ a.q_flip;
+          w[4 * i + 1] = x.y ^ a.q_flip;
+          w[4 * i + 2] = x.z ^ a.q_flip;
+          w[4 * i + 3] = x.w ^ a.q_flip;
+        }
+        float back = 1.0f;
+        if (!a.half) {
+#pragma unroll
+          for (int i = 0; i < HSP / 2; ++i)
+            most = fmaxf(most, fmaxf(fabsf(__uint_as_float(w[i] << 16)),
+                                     fabsf(__uint_as_float(w[i] & 0xFFFF0000u))));
+          const uint32_t e = max(__float_as_uint(most) >> 23, 15u);
+          const float up = __uint_as_float((268u - e) << 23);  // 2^(14 - exponent)
+          back = __uint_as_float((e - 14u) << 23);
+#pragma unroll
+          for (int i = 0; i < HSP / 2; ++i)
+            w[i] = half2_of(__uint_as_float(w[i] << 16) * up,
+                            __uint_as_float(w[i] & 0xFFFF0000u) * up);
+        }
+        f = a.scale_log2 * back;
+#pragma unroll
+        for (int i = 0; i < HSP / 8; ++i)
+          st_shared16(q_smem + (i >> 3) * (kTile * 128) + r * 128 + (((i & 7) ^ (r & 7)) << 4),
+                      w + 4 * i);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_ready(g));
+      }
+      const int pos_low = __reduce_min_sync(0xFFFFFFFFu, live ? pos : 0x7FFFFFFF);
+      const int pos_high = __reduce_max_sync(0xFFFFFFFFu, pos);
+      for (int j = 0; j < n; ++j) {
+        const int tb = tile_token(u, j);
+        if (!mbar_wait_warp(s_full(g), tiles_done & 1u, wd, kSiteEpilogueFull)) {
+          ok = false;
+          break;
+        }
+        ++tiles_done;
+        tc_fence_after_sync();
+        const Factor* fac = factors + ((it + j) % kFactorSlots) * 8;
+        const bool edge = !(tb + kTile - 1 <= pos_low &&
+                            (a.window == 0 || pos_high - tb < a.window || tb + kTile - 1 < a.sinks));
+        // columns 0 .. last are at or before this row; from first_window on, or below
+        // sink_cols, they are in its window or sinks
+        const int last = pos - tb;
+        const int first_window = a.window ? last - a.window + 1 : -kTile;
+        const int sink_cols = a.window ? a.sinks - tb : 0;
+        float top = kNothing;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t x[64];
+          tmem_ld_64cols(s_tmem + 64 * h, x);
+          if (edge) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) {
+              const int c = 64 * h + i;
+              if (c > last || (c < first_window && c >= sink_cols))
+                x[i] = __float_as_uint(-3e38f);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float y = __uint_as_float(x[16 * i]);
+#pragma unroll
+            for (int e = 1; e < 16; ++e) y = fmaxf(y, __uint_as_float(x[16 * i + e]));
+            const Factor c = fac[4 * h + i];
+            top = fmaxf(top, fmaf(y, f * c.k, c.log2v));
+          }
+        }
+        if (__any_sync(0xFFFFFFFFu, top > m + kRaise)) {
+          const float to = fmaxf(m, top);
+          const float corr = ex2_approx(m - to);
+          m = to;
+          l *= corr;
+          if (j > 0) {
+            // (the product that last added to O precedes this tile's S)
+#pragma unroll
+            for (int h = 0; h < HSP / 32; ++h) {
+              uint32_t x[32];
+              tmem_ld_32cols(o_tmem + 32 * h, x);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                x[i] = __float_as_uint(__uint_as_float(x[i]) * corr);
+              tmem_st_32cols(o_tmem + 32 * h, x);
+            }
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t x[64];
+          tmem_ld_64cols(s_tmem + 64 * h, x);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const Factor c = fac[4 * h + i];
+            const float fk = f * c.k, add = c.log2v - m;
+            const uint64_t fk2 = pack_f32x2(fk, fk), add2 = pack_f32x2(add, add);
+            uint64_t sum = 0;
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const int at = 16 * i + e;
+              float y0, y1;
+              fma_f32x2(y0, y1, __uint_as_float(x[at]), __uint_as_float(x[at + 1]), fk2, add2);
+              if (edge) {
+                const int c0 = 64 * h + at;
+                if (c0 > last || (c0 < first_window && c0 >= sink_cols)) y0 = -INFINITY;
+                if (c0 + 1 > last || (c0 + 1 < first_window && c0 + 1 >= sink_cols))
+                  y1 = -INFINITY;
+              }
+              y0 = ex2_approx(y0);
+              y1 = ex2_approx(y1);
+              sum = add_f32x2(sum, pack_f32x2(y0, y1));
+              x[at / 2] = half2_of(y0, y1);
+            }
+            float s0, s1;
+            unpack_f32x2(sum, s0, s1);
+            l = fmaf(s0 + s1, c.inv, l);
+          }
+          // P over S: columns 32 h .., whose scores have been read
+          uint32_t p0[16], p1[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            p0[i] = x[i];
+            p1[i] = x[16 + i];
+          }
+          tmem_st_16cols(s_tmem + 32 * h, p0);
+          tmem_st_16cols(s_tmem + 32 * h + 16, p1);
+        }
+        tmem_wait_st();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_ready(g));
+      }
+      it += n_all;
+      if (!ok) break;
+      if (n > 0) {
+        if (!mbar_wait_warp(o_full(g), o_phase, wd, kSiteEpilogueFull)) break;
+        o_phase ^= 1u;
+        tc_fence_after_sync();
+      }
+      const float inv_l = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+      for (int h = 0; h < HSP / 32; ++h) {
+        uint32_t x[32];
+        if (n > 0) {
+          tmem_ld_32cols(o_tmem + 32 * h, x);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = 0u;
+        }
+        if (!live) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (32 * h + 8 * i >= D) break;
+          uint32_t y[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float v0 = __uint_as_float(x[8 * i + 2 * e]) * inv_l;
+            float v1 = __uint_as_float(x[8 * i + 2 * e + 1]) * inv_l;
+            if (l == 0.0f) v0 = v1 = 0.0f;
+            if (a.half) {
+              y[e] = half2_of(v0, v1);
+            } else {
+              const __nv_bfloat162 b = __floats2bfloat162_rn(v0, v1);
+              y[e] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+          }
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + out_at + 32 * h + 8 * i) =
+              make_uint4(y[0], y[1], y[2], y[3]);
+        }
+      }
+      tc_fence_before_sync();  // O may be overwritten after the next unit's p_ready
+    }
+  } else if (warp < kMmaWarp) {
+    // --------------------------------------------------------- conversion --
+    const int w = warp - kSoftmaxWarps;
+    constexpr int kLaneVBytes = HSP / 8;  // V elements a lane transposes, for 8 tokens
+    constexpr int kKLoads = 4 * (HSP / 64);
+    // K: tokens 32 w + 8 o + lane % 8, elements 64 h + 16 (lane / 8) ..
+    // V: tokens 64 (w & 1) + 8 (lane % 8) .., elements (w >> 1) HSP / 2 + (lane / 8) kLaneVBytes ..
+    const int vt = 64 * (w & 1) + 8 * (lane & 7);
+    const int vd = (w >> 1) * (HSP / 2) + (lane >> 3) * kLaneVBytes;
+    uint32_t it = 0;
+    uint4 kx[kKLoads];
+    uint32_t vx[8][kLaneVBytes / 4];
+    bool ok = true, injected = false;
+
+    auto load_tile = [&](const Unit& u, int j) {
+      const int tb = tile_token(u, j);
+#pragma unroll
+      for (int o = 0; o < 4; ++o) {
+        const int tok = tb + 32 * w + 8 * o + (lane & 7);
+        int page = -1;
+        if (tok < u.q.length) page = kv_page(a.v, u.s, tok >> a.v.page_shift);
+        const uint8_t* from = a.v.codes[0] + kv_page_offset(a.v, max(page, 0), u.head) +
+                              (tok & (a.v.page_tokens - 1)) * D + 16 * (lane >> 3);
+#pragma unroll
+        for (int h = 0; h < HSP / 64; ++h)
+          kx[o * (HSP / 64) + h] = page >= 0 && 64 * h + 16 * (lane >> 3) < D
+                                       ? __ldg(reinterpret_cast<const uint4*>(from + 64 * h))
+                                       : make_uint4(0, 0, 0, 0);
+      }
+      const int tok = tb + vt;
+      int page = -1;
+      if (tok < u.q.length) page = kv_page(a.v, u.s, tok >> a.v.page_shift);
+      const uint8_t* from = a.v.codes[1] + kv_page_offset(a.v, max(page, 0), u.head) +
+                            (tok & (a.v.page_tokens - 1)) * D + vd;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bool in = page >= 0 && tok + i < u.q.length && vd < D;
+        if constexpr (kLaneVBytes == 16) {
+          const uint4 x = in ? __ldg(reinterpret_cast<const uint4*>(from + i * D))
+                             : make_uint4(0, 0, 0, 0);
+          vx[i][0] = x.x;
+          vx[i][1] = x.y;
+          vx[i][2] = x.z;
+          vx[i][3] = x.w;
+        } else {
+          const uint2 x = in ? __ldg(reinterpret_cast<const uint2*>(from + i * D)) : make_uint2(0, 0);
+          vx[i][0] = x.x;
+          vx[i][1] = x.y;
+        }
+      }
+    };
+    auto load_factor = [&](const Unit& u, int j) {
+      // scales of the 16 tokens 16 lane .. of the tile (lanes 0..7 of one warp)
+      Factor c{1.0f, -INFINITY, 0.0f, 0.0f};
+      const int tok = tile_token(u, j) + 16 * lane;
+      if (tok < u.q.length) {
+        const int page = kv_page(a.v, u.s, tok >> a.v.page_shift);
+        if (page >= 0) {
+          const long long unit = static_cast<long long>(page) * a.v.heads + u.head;
+          c.k = __ldg(a.v.scale[0] + unit);
+          const float vs = __ldg(a.v.scale[1] + unit);
+          c.log2v = __log2f(vs);
+          c.inv = __fdividef(1.0f, vs);
+        }
+      }
+      return c;
+    };
+
+    for (long long k = 0; ok && unit_index(k) < total; ++k) {
+      const Unit u = decode_unit(a, s_prefix, per, unit_index(k));
+      const int n = max(u.n[0], u.n[1]);
+      if (n > 0) load_tile(u, 0);
+      for (int j = 0; j < n; ++j, ++it) {
+        const uint32_t stage = it % kStages, phase = (it / kStages) & 1u;
+        Factor fac{};
+        if (w == 0 && lane < 8) fac = load_factor(u, j);
+        if (!mbar_wait_warp(k_empty(stage), phase ^ 1u, wd, kSiteLoaderEmpty)) {
+          ok = false;
+          break;
+        }
+        if (w == 0 && lane < 8) factors[(it % kFactorSlots) * 8 + lane] = fac;
+        const uint32_t ks = base + L::kK + stage * L::kKBytes;
+#pragma unroll
+        for (int o = 0; o < 4; ++o) {
+          const uint32_t row = 32 * w + 8 * o + (lane & 7);
+#pragma unroll
+          for (int h = 0; h < HSP / 64; ++h) {
+            const uint32_t* c = reinterpret_cast<const uint32_t*>(&kx[o * (HSP / 64) + h]);
+            uint32_t y[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) codes4_to_half2x2<kFormat>(c[i], y[2 * i], y[2 * i + 1]);
+            const uint32_t at = ks + h * (kTile * 128) + row * 128;
+            const uint32_t unit = 2 * (lane >> 3);
+            st_shared16(at + ((unit ^ (row & 7)) << 4), y);
+            st_shared16(at + (((unit + 1) ^ (row & 7)) << 4), y + 4);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (a.inject && !injected) {
+          injected = true;  // withhold the CTA's first K tile: the MMA warp's wait runs out
+        } else if (lane == 0) {
+          mbar_arrive(k_full(stage));
+        }
+        if (!mbar_wait_warp(v_empty(stage), phase ^ 1u, wd, kSiteLoaderEmpty)) {
+          ok = false;
+          break;
+        }
+        const uint32_t vs = base + L::kV + stage * L::kVBytes + (w & 1) * (HSP * 128);
+#pragma unroll
+        for (int c = 0; c < kLaneVBytes / 4; ++c) {
+          // eight tokens of four elements: pairs of tokens, then rows of V^T
+          uint32_t y[4][4];
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            uint32_t x0 = vx[2 * p][c], x1 = vx[2 * p + 1][c];
+            if (kFormat == CSA_KV_INT8) {
+              x0 ^= 0x80808080u;
+              x1 ^= 0x80808080u;
+            }
+            const uint32_t lo = byte_perm(x0, x1, 0x5140), hi = byte_perm(x0, x1, 0x7362);
+            if (kFormat == CSA_KV_INT8) {
+              y[0][p] = flipped_pair_to_half2<0x4140>(lo);
+              y[1][p] = flipped_pair_to_half2<0x4342>(lo);
+              y[2][p] = flipped_pair_to_half2<0x4140>(hi);
+              y[3][p] = flipped_pair_to_half2<0x4342>(hi);
+            } else {
+              y[0][p] = e4m3x2_to_half2(lo & 0xFFFFu);
+              y[1][p] = e4m3x2_to_half2(lo >> 16);
+              y[2][p] = e4m3x2_to_half2(hi & 0xFFFFu);
+              y[3][p] = e4m3x2_to_half2(hi >> 16);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t row = vd + 4 * c + e;
+            st_shared16(vs + row * 128 + (((lane & 7) ^ (row & 7)) << 4), y[e]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(v_full(stage));
+        if (j + 1 < n) load_tile(u, j + 1);
+      }
+    }
+  } else {
+    // --------------------------------------------------------- MMA issuer --
+    if (lane == 0) {
+      constexpr uint32_t kIdescS = idesc_f16_f32(kTile, kTile), kIdescO = idesc_f16_f32(kTile, HSP);
+      uint32_t it = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+      bool ok = true;
+      for (long long k = 0; ok && unit_index(k) < total; ++k) {
+        const Unit u = decode_unit(a, s_prefix, per, unit_index(k));
+        const int n = max(u.n[0], u.n[1]);
+        if (n == 0) continue;
+        for (int j = 0; ok && j <= n; ++j) {
+          const uint32_t stage = (it + j) % kStages, phase = ((it + j) / kStages) & 1u;
+          const uint32_t prev = (it + j - 1) % kStages, prev_phase = ((it + j - 1) / kStages) & 1u;
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            if (!ok) break;
+            const uint32_t s_tmem = tmem + g * kTile, o_tmem = tmem + 2 * kTile + g * HSP;
+            if (j >= 1 && j <= u.n[g]) {
+              if (!mbar_wait(v_full(prev), prev_phase, wd, kSiteMmaFull) ||
+                  !mbar_wait(p_ready(g), p_phase[g], wd, kSiteMmaTmemEmpty)) {
+                ok = false;
+                break;
+              }
+              p_phase[g] ^= 1u;
+              tc_fence_after_sync();
+              const uint32_t vs = base + L::kV + prev * L::kVBytes;
+#pragma unroll
+              for (int s = 0; s < kTile / 16; ++s)
+                umma_f16_ts(o_tmem, s_tmem + 8 * s,
+                            umma_desc_k_sw128(vs + (s >> 2) * (HSP * 128) + (s & 3) * 32), kIdescO,
+                            j > 1 || s > 0);
+              if (j == u.n[g]) umma_commit(o_full(g));
+            }
+            if (j < u.n[g]) {
+              if (j == 0) {
+                if (!mbar_wait(q_ready(g), q_phase[g], wd, kSiteMmaFull)) {
+                  ok = false;
+                  break;
+                }
+                q_phase[g] ^= 1u;
+              }
+              if (!mbar_wait(k_full(stage), phase, wd, kSiteMmaFull)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after_sync();
+              const uint32_t qs = base + L::kQ + g * L::kQBytes;
+              const uint32_t ks = base + L::kK + stage * L::kKBytes;
+#pragma unroll
+              for (int s = 0; s < HSP / 16; ++s)
+                umma_bf16(s_tmem,
+                          umma_desc_k_sw128(qs + (s >> 2) * (kTile * 128) + (s & 3) * 32),
+                          umma_desc_k_sw128(ks + (s >> 2) * (kTile * 128) + (s & 3) * 32), kIdescS,
+                          s > 0);
+              umma_commit(s_full(g));
+            }
+          }
+          if (!ok) break;
+          if (j < n) umma_commit(k_empty(stage));
+          if (j >= 1) umma_commit(v_empty(prev));
+        }
+        it += n;
+      }
+      // Every MMA must be complete before TMEM and shared memory go away.
+      umma_commit(drain);
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_test(drain, 0) && globaltimer_ns() - t0 < a.wait_limit_ns) {
+      }
+    }
+    __syncwarp();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+}
+
+template <int HSP, int kFormat>
+cudaError_t launch_prompt(const PromptArgs& a, const DeviceInfo& dev, cudaStream_t stream, int& rc,
+                          std::string& err) {
+  const auto kernel = attend_prompt_sm103a_kernel<HSP, kFormat>;
+  const int smem = Layout<HSP>::kTotal + 1024;
+  rc = set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), smem, dev.device, err);
+  if (rc != CSA_OK) return cudaSuccess;
+  return launch_programmatic(kernel, static_cast<unsigned>(dev.sm_count), kThreads, smem, stream, a);
+}
+
+}  // namespace
+
+int cache_prompt_launch(const csa_kv_cache& cache, const csa_kv_batch& batch,
+                        const AttendCall& call, int row_limit, cudaStream_t stream,
+                        const DeviceInfo& dev, std::string& err) {
+  PromptArgs a;
+  a.v = kv_view(cache, batch, dev);
+  a.q = call.q;
+  a.out = call.out;
+  a.q_token = call.q_token;
+  a.q_head = call.q_head;
+  a.out_token = call.out_token;
+  a.out_head = call.out_head;
+  a.half = call.dtype == CSA_F16;
+  a.group = call.q_heads / cache.heads;
+  a.window = call.window;
+  a.sinks = call.window > 0 ? call.sinks : 0;
+  a.row_limit = row_limit;
+  a.scale_log2 = static_cast<float>(std::fabs(static_cast<double>(call.scale)) * 1.4426950408889634);
+  a.q_flip = call.scale < 0 ? 0x80008000u : 0u;
+  a.status = dev.status_word;
+  a.wait_limit_ns = wait_limit_ns();
+  a.inject = take_inject() ? 1 : 0;
+  int rc = CSA_OK;
+  cudaError_t e;
+  if (cache.head_size <= 64)
+    e = cache.format == CSA_KV_INT8 ? launch_prompt<64, CSA_KV_INT8>(a, dev, stream, rc, err)
+                                    : launch_prompt<64, CSA_KV_E4M3>(a, dev, stream, rc, err);
+  else
+    e = cache.format == CSA_KV_INT8 ? launch_prompt<128, CSA_KV_INT8>(a, dev, stream, rc, err)
+                                    : launch_prompt<128, CSA_KV_E4M3>(a, dev, stream, rc, err);
+  if (rc != CSA_OK) return rc;
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e != cudaSuccess) {
+    err = std::string("launch: ") + cudaGetErrorString(e);
+    return CSA_ERR_LAUNCH;
+  }
+  return CSA_OK;
+}
+
+}  // namespace csa
