@@ -87,6 +87,7 @@ struct AttendArgs {
   int workers;
   int row_limit;   // sequences of more rows (tokens x group) are left to another kernel
   int* headers;    // [workers][8]
+  unsigned int* counter;  // the prompt kernel's, cleared here
   float* parts;    // [2 * workers][part_floats]
   int part_floats;
 };
@@ -222,6 +223,7 @@ __global__ void __launch_bounds__(128 * kGroups<NB>, 1)
   constexpr int kTilesM = HSP / 16;       // m-tiles of the output
 
   grid_dependency_wait();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.counter = 0;
 
   // -------------------------------------------------------- the work list --
   // Thread i sums the work of sequences [i c, (i + 1) c); a scan over the CTA
@@ -774,7 +776,7 @@ int padded_head(int head_size) { return head_size <= 64 ? 64 : 128; }
 }  // namespace
 
 size_t cache_attention_workspace_bytes(int head_size) {
-  return static_cast<size_t>(kMaxWorkers) * 8 * sizeof(int) +
+  return static_cast<size_t>(kMaxWorkers + 1) * 8 * sizeof(int) +
          static_cast<size_t>(2 * kMaxWorkers) *
              (2 * kMaxRows + kMaxRows * static_cast<size_t>(padded_head(head_size))) *
              sizeof(float);
@@ -801,18 +803,12 @@ int cache_attention_launch(const csa_kv_cache& cache, const csa_kv_batch& batch,
   a.row_limit = kRowLimit;
   const int hsp = padded_head(cache.head_size);
   a.headers = static_cast<int*>(call.workspace);
-  a.parts = reinterpret_cast<float*>(a.headers + kMaxWorkers * 8);
+  a.counter = reinterpret_cast<unsigned int*>(a.headers + kMaxWorkers * 8);
+  a.parts = reinterpret_cast<float*>(a.headers + (kMaxWorkers + 1) * 8);
   a.part_floats = 2 * kMaxRows + kMaxRows * hsp;
   const long long most_rows = static_cast<long long>(batch.max_new) * a.group;
   const bool one = most_rows <= 8;
   int rc = CSA_OK;
-  if (most_rows > kRowLimit) {
-    rc = cache_prompt_launch(cache, batch, call, kRowLimit, stream, dev, err);
-    if (rc != CSA_OK) {
-      err = "cache_attention_forward: " + err;
-      return rc;
-    }
-  }
   cudaError_t e;
   if (hsp == 64)
     e = one ? launch_rows<64, 1>(a, cache.format, sms, dev, stream, rc, err)
@@ -828,6 +824,13 @@ int cache_attention_launch(const csa_kv_cache& cache, const csa_kv_batch& batch,
   if (e != cudaSuccess) {
     err = std::string("cache_attention_forward: launch: ") + cudaGetErrorString(e);
     return CSA_ERR_LAUNCH;
+  }
+  if (most_rows > kRowLimit) {
+    rc = cache_prompt_launch(cache, batch, call, kRowLimit, a.counter, stream, dev, err);
+    if (rc != CSA_OK) {
+      err = "cache_attention_forward: " + err;
+      return rc;
+    }
   }
   return CSA_OK;
 }

@@ -4,21 +4,23 @@
 //
 // A unit of work is 256 rows (tokens x query heads of one kv head) of a
 // sequence: two groups A and B of 128, each a TMEM accumulator's lanes, which
-// share every tile of 128 keys. One CTA per SM walks a list of units (longest
-// first within a sequence), with 13 warps:
+// share every tile of 128 keys. One CTA per SM takes units from a counter
+// (longest first within a sequence), with 14 warps:
 //  - warps 0..7: softmax, warps 0..3 group A, 4..7 group B, a thread a row. Per
-//    tile: one pass over S in TMEM for the row's maximum, one that writes the
+//    half tile of 64 keys: scores from TMEM, x - m, their maximum, and the
 //    weights exp2(x - m) as fp16 over S (P, the second product's A operand in
-//    TMEM). m is raised only when a value passes m + 8 (then the thread's O row
-//    is rescaled in TMEM). Before a unit they turn Q's rows into fp16 in shared
-//    memory; after it they write O / l.
-//  - warps 8..11: conversion. Codes come from HBM into registers a tile ahead,
-//    become fp16 exactly, and go to shared memory in the 128-byte-swizzle K-major
-//    layout: K as [token][element], V transposed in registers to
-//    [element][token]. Two stages each.
+//    TMEM). m is raised only when a value passes m + 8; then the thread's O row,
+//    its l and the weights of the tile so far are rescaled. Before a unit they
+//    turn Q's rows into fp16 in shared memory; after it they write O / l.
+//  - warps 8..11: conversion. Codes come from HBM into registers a tile ahead
+//    (their page numbers two), become fp16 exactly, and go to shared memory in the
+//    128-byte-swizzle K-major layout: K as [token][element], V transposed in
+//    registers to [element][token]. Two stages each.
 //  - warp 12: one thread issues, per tile, O_A += P_A V, S_A = Q_A K^T of the next
 //    tile, and the same for B: while one group is in its softmax, the tensor core
 //    works for the other. MMAs run in issue order, so S_A may overwrite P_A.
+//  - warp 13: takes units from the counter (workspace, cleared by the rows kernel
+//    ahead in the stream) and passes them on a unit ahead.
 //
 // Scales (see cache_attention_sm103a.cu): with K's and V's scales per 16 tokens in
 // shared memory, x = s (c ks) + log2(vs) and the weight has V's scale in it; the
@@ -34,6 +36,7 @@
 #include <cmath>
 #include <cstdint>
 #include <string>
+#include <type_traits>
 
 #include "csa_internal.h"
 #include "kv_cache.cuh"
@@ -45,11 +48,13 @@ namespace {
 constexpr int kSoftmaxWarps = 8;
 constexpr int kConvertWarps = 4;
 constexpr int kMmaWarp = kSoftmaxWarps + kConvertWarps;
-constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kListWarp = kMmaWarp + 1;
+constexpr int kThreads = 32 * (kListWarp + 1);
 constexpr int kTile = 128;          // keys per tile, rows per group
 constexpr int kUnitRows = 2 * kTile;
 constexpr int kStages = 2;
 constexpr int kFactorSlots = 4;
+constexpr int kUnitSlots = 2;
 constexpr int kTmemCols = 512;      // S_A, S_B, O_A, O_B
 constexpr float kRaise = 8.0f;
 constexpr float kNothing = -1e30f;  // the running maximum of a row that has seen nothing
@@ -65,6 +70,7 @@ struct PromptArgs {
   int row_limit;        // sequences of at most this many rows are the rows kernel's
   float scale_log2;     // its magnitude
   uint32_t q_flip;      // sign bits flipped in Q's words where the scale is negative
+  unsigned int* counter;  // units taken, zero at launch
   int* status;
   unsigned long long wait_limit_ns;
   int inject;
@@ -75,6 +81,13 @@ struct Factor {
   float k, log2v, inv, pad;
 };
 
+struct Unit {
+  KvSequence q;
+  int s, head, row0, rows;  // rows [row0, row0 + rows) of the sequence
+  int sink_tiles, window_tile;
+  int n[2];                 // tiles of each group; n[0] < 0: the list has ended
+};
+
 template <int HSP>
 struct Layout {
   static constexpr int kQBytes = kTile * HSP * 2;  // per group: [HSP / 64][128 rows][128 B]
@@ -83,14 +96,8 @@ struct Layout {
   static constexpr int kQ = 0, kK = 2 * kQBytes, kV = kK + kStages * kKBytes,
                        kFactors = kV + kStages * kVBytes,
                        kBars = kFactors + kFactorSlots * 8 * static_cast<int>(sizeof(Factor)),
-                       kMisc = kBars + 8 * 20, kTotal = kMisc + 16;
-};
-
-struct Unit {
-  KvSequence q;
-  int s, head, row0, rows;  // rows [row0, row0 + rows) of the sequence
-  int sink_tiles, window_tile;
-  int n[2];                 // tiles of each group
+                       kMisc = kBars + 8 * 22, kUnits = kMisc + 16,
+                       kTotal = kUnits + kUnitSlots * static_cast<int>(sizeof(Unit));
 };
 
 // The list's u-th unit: sequences in order, the last (longest) rows first.
@@ -99,7 +106,7 @@ __device__ __forceinline__ long long units_of(const PromptArgs& a, const KvSeque
   return rows <= a.row_limit ? 0 : (rows + kUnitRows - 1) / kUnitRows * a.v.heads;
 }
 
-__device__ __forceinline__ Unit decode_unit(const PromptArgs& a, const long long* prefix, int per,
+__device__ Unit decode_unit(const PromptArgs& a, const long long* prefix, int per,
                                             long long u) {
   int lo = 0, hi = kThreads;
   while (hi - lo > 1) {
@@ -168,14 +175,17 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       : "memory");
 }
 
-// 32 lanes x 16 consecutive 32-bit columns from 16 registers (no wait).
-__device__ __forceinline__ void tmem_st_16cols(uint32_t taddr, const uint32_t (&r)[16]) {
+// 32 lanes x 32 consecutive 32-bit columns from 32 registers, without the wait.
+__device__ __forceinline__ void tmem_st_32cols_async(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, "
+      "%21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15])
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() {
@@ -206,6 +216,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto p_ready = [&](uint32_t g) { return bars + 8u * (12 + g); };
   auto o_full = [&](uint32_t g) { return bars + 8u * (14 + g); };
   const uint32_t drain = bars + 8u * 16;
+  auto u_full = [&](uint32_t s) { return bars + 8u * (17 + s); };
+  auto u_empty = [&](uint32_t s) { return bars + 8u * (19 + s); };
   const uint32_t tmem_slot = base + L::kMisc;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::kMisc + 4);
   Factor* factors = reinterpret_cast<Factor*>(gbase + L::kFactors);
@@ -226,6 +238,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(o_full(g), 1);
     }
     mbar_init(drain, 1);
+    for (int s = 0; s < kUnitSlots; ++s) {
+      mbar_init(u_full(s), 1);
+      mbar_init(u_empty(s), kMmaWarp + 1);  // every warp but the list's
+    }
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -261,10 +277,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after_sync();
   const uint32_t tmem = ld_shared_b32(tmem_slot);
   const long long total = s_prefix[kThreads];
-  // The k-th unit of this CTA: forwards and backwards through the list in turn, so
-  // that a CTA with a long unit gets a short one next.
-  auto unit_index = [&](long long k) {
-    return k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+  // The k-th unit that this CTA works on, for a whole warp; false: a wait ran out.
+  auto take_unit = [&](uint32_t k, Unit& u) {
+    const uint32_t slot = k % kUnitSlots;
+    if (!mbar_wait_warp(u_full(slot), (k / kUnitSlots) & 1u, wd, kSiteSched)) return false;
+    u = reinterpret_cast<const Unit*>(gbase + L::kUnits)[slot];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(u_empty(slot));
+    return true;
   };
   const int D = a.v.head_size;
 
@@ -279,8 +299,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t tiles_done = 0, o_phase = 0;
     uint32_t it = 0;  // tiles of the CTA so far (the factors' slots)
     bool ok = true;
-    for (long long k = 0; ok && unit_index(k) < total; ++k) {
-      const Unit u = decode_unit(a, s_prefix, per, unit_index(k));
+    for (uint32_t k = 0; ok; ++k) {
+      Unit u;
+      if (!take_unit(k, u) || u.n[0] < 0) break;
       const int n = g == 0 ? u.n[0] : u.n[1], n_all = max(u.n[0], u.n[1]);
       const int rr = u.row0 + static_cast<int>(g) * kTile + r;
       const int j_tok = rr / a.group;
@@ -347,86 +368,94 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int last = pos - tb;
         const int first_window = a.window ? last - a.window + 1 : -kTile;
         const int sink_cols = a.window ? a.sinks - tb : 0;
-        float top = kNothing;
+        auto softmax = [&](auto edge_tile) {
+          constexpr bool kEdge = decltype(edge_tile)::value;
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            uint32_t x[64];
+            // x = score * f * c.k + c.log2v - less, masked: -inf; returns the maximum
+            auto scores = [&](float less) {
+              tmem_ld_64cols(s_tmem + 64 * h, x);
+              float top = -INFINITY;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t x[64];
-          tmem_ld_64cols(s_tmem + 64 * h, x);
-          if (edge) {
+              for (int i = 0; i < 4; ++i) {
+                const Factor c = fac[4 * h + i];
+                const float fk = f * c.k, add = c.log2v - less;
+                const uint64_t fk2 = pack_f32x2(fk, fk), add2 = pack_f32x2(add, add);
 #pragma unroll
-            for (int i = 0; i < 64; ++i) {
-              const int c = 64 * h + i;
-              if (c > last || (c < first_window && c >= sink_cols))
-                x[i] = __float_as_uint(-3e38f);
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float y = __uint_as_float(x[16 * i]);
-#pragma unroll
-            for (int e = 1; e < 16; ++e) y = fmaxf(y, __uint_as_float(x[16 * i + e]));
-            const Factor c = fac[4 * h + i];
-            top = fmaxf(top, fmaf(y, f * c.k, c.log2v));
-          }
-        }
-        if (__any_sync(0xFFFFFFFFu, top > m + kRaise)) {
-          const float to = fmaxf(m, top);
-          const float corr = ex2_approx(m - to);
-          m = to;
-          l *= corr;
-          if (j > 0) {
-            // (the product that last added to O precedes this tile's S)
-#pragma unroll
-            for (int h = 0; h < HSP / 32; ++h) {
-              uint32_t x[32];
-              tmem_ld_32cols(o_tmem + 32 * h, x);
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                x[i] = __float_as_uint(__uint_as_float(x[i]) * corr);
-              tmem_st_32cols(o_tmem + 32 * h, x);
-            }
-          }
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t x[64];
-          tmem_ld_64cols(s_tmem + 64 * h, x);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const Factor c = fac[4 * h + i];
-            const float fk = f * c.k, add = c.log2v - m;
-            const uint64_t fk2 = pack_f32x2(fk, fk), add2 = pack_f32x2(add, add);
-            uint64_t sum = 0;
-#pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              const int at = 16 * i + e;
-              float y0, y1;
-              fma_f32x2(y0, y1, __uint_as_float(x[at]), __uint_as_float(x[at + 1]), fk2, add2);
-              if (edge) {
-                const int c0 = 64 * h + at;
-                if (c0 > last || (c0 < first_window && c0 >= sink_cols)) y0 = -INFINITY;
-                if (c0 + 1 > last || (c0 + 1 < first_window && c0 + 1 >= sink_cols))
-                  y1 = -INFINITY;
+                for (int e = 0; e < 16; e += 2) {
+                  const int at = 16 * i + e;
+                  float y0, y1;
+                  fma_f32x2(y0, y1, __uint_as_float(x[at]), __uint_as_float(x[at + 1]), fk2, add2);
+                  if (kEdge) {
+                    const int c0 = 64 * h + at;
+                    if (c0 > last || (c0 < first_window && c0 >= sink_cols)) y0 = -INFINITY;
+                    if (c0 + 1 > last || (c0 + 1 < first_window && c0 + 1 >= sink_cols))
+                      y1 = -INFINITY;
+                  }
+                  x[at] = __float_as_uint(y0);
+                  x[at + 1] = __float_as_uint(y1);
+                  top = fmaxf(top, fmaxf(y0, y1));
+                }
               }
-              y0 = ex2_approx(y0);
-              y1 = ex2_approx(y1);
-              sum = add_f32x2(sum, pack_f32x2(y0, y1));
-              x[at / 2] = half2_of(y0, y1);
-            }
-            float s0, s1;
-            unpack_f32x2(sum, s0, s1);
-            l = fmaf(s0 + s1, c.inv, l);
-          }
-          // P over S: columns 32 h .., whose scores have been read
-          uint32_t p0[16], p1[16];
+              return top;
+            };
+            const float top = scores(m);
+            if (__any_sync(0xFFFFFFFFu, top > kRaise)) {
+              const float to = fmaxf(m, scores(0.0f));
+              const float corr = ex2_approx(m - to);
+              m = to;
+              l *= corr;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            p0[i] = x[i];
-            p1[i] = x[16 + i];
+              for (int i = 0; i < 64; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) - m);
+              uint32_t y[32];
+              if (j > 0) {
+                // (the product that last added to O precedes this tile's S)
+#pragma unroll 1
+                for (int c = 0; c < HSP; c += 32) {
+                  tmem_ld_32cols(o_tmem + c, y);
+#pragma unroll
+                  for (int i = 0; i < 32; ++i)
+                    y[i] = __float_as_uint(__uint_as_float(y[i]) * corr);
+                  tmem_st_32cols(o_tmem + c, y);
+                }
+              }
+              if (h == 1) {
+                // the first half's weights; in fp32, as corr may be below fp16's range
+                tmem_wait_st();
+                tmem_ld_32cols(s_tmem, y);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                  const float2 w = __half22float2(*reinterpret_cast<__half2*>(&y[i]));
+                  y[i] = half2_of(w.x * corr, w.y * corr);
+                }
+                tmem_st_32cols(s_tmem, y);
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint64_t sum = 0;
+#pragma unroll
+              for (int e = 0; e < 16; e += 2) {
+                const int at = 16 * i + e;
+                const float y0 = ex2_approx(__uint_as_float(x[at]));
+                const float y1 = ex2_approx(__uint_as_float(x[at + 1]));
+                sum = add_f32x2(sum, pack_f32x2(y0, y1));
+                x[at / 2] = half2_of(y0, y1);
+              }
+              float s0, s1;
+              unpack_f32x2(sum, s0, s1);
+              l = fmaf(s0 + s1, fac[4 * h + i].inv, l);
+            }
+            // P over S: columns 32 h .., whose scores have been read
+            uint32_t p[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) p[i] = x[i];
+            tmem_st_32cols_async(s_tmem + 32 * h, p);
           }
-          tmem_st_16cols(s_tmem + 32 * h, p0);
-          tmem_st_16cols(s_tmem + 32 * h + 16, p1);
-        }
+        };
+        if (edge) softmax(std::true_type{});
+        else softmax(std::false_type{});
         tmem_wait_st();
         tc_fence_before_sync();
         __syncwarp();
@@ -486,29 +515,45 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t vx[8][kLaneVBytes / 4];
     bool ok = true, injected = false;
 
-    auto load_tile = [&](const Unit& u, int j) {
+    // Pages of a tile's tokens that this lane takes: four of K, one of V, and (lanes
+    // 0..7 of warp 0) that of the 16 tokens whose factors it makes. -1: none there.
+    struct Pages {
+      int k[4], v, f;
+    };
+    auto pages_of = [&](const Unit& u, int j) {
+      const int tb = tile_token(u, j);
+      auto page = [&](int tok) {
+        return tok < u.q.length ? kv_page(a.v, u.s, tok >> a.v.page_shift) : -1;
+      };
+      Pages p;
+#pragma unroll
+      for (int o = 0; o < 4; ++o) p.k[o] = page(tb + 32 * w + 8 * o + (lane & 7));
+      p.v = page(tb + vt);
+      p.f = w == 0 && lane < 8 ? page(tb + 16 * lane) : -1;
+      return p;
+    };
+    const int page_mask = a.v.page_tokens - 1;
+    auto load_k = [&](const Unit& u, int j, const Pages& p) {
       const int tb = tile_token(u, j);
 #pragma unroll
       for (int o = 0; o < 4; ++o) {
         const int tok = tb + 32 * w + 8 * o + (lane & 7);
-        int page = -1;
-        if (tok < u.q.length) page = kv_page(a.v, u.s, tok >> a.v.page_shift);
-        const uint8_t* from = a.v.codes[0] + kv_page_offset(a.v, max(page, 0), u.head) +
-                              (tok & (a.v.page_tokens - 1)) * D + 16 * (lane >> 3);
+        const uint8_t* from = a.v.codes[0] + kv_page_offset(a.v, max(p.k[o], 0), u.head) +
+                              (tok & page_mask) * D + 16 * (lane >> 3);
 #pragma unroll
         for (int h = 0; h < HSP / 64; ++h)
-          kx[o * (HSP / 64) + h] = page >= 0 && 64 * h + 16 * (lane >> 3) < D
+          kx[o * (HSP / 64) + h] = p.k[o] >= 0 && 64 * h + 16 * (lane >> 3) < D
                                        ? __ldg(reinterpret_cast<const uint4*>(from + 64 * h))
                                        : make_uint4(0, 0, 0, 0);
       }
-      const int tok = tb + vt;
-      int page = -1;
-      if (tok < u.q.length) page = kv_page(a.v, u.s, tok >> a.v.page_shift);
-      const uint8_t* from = a.v.codes[1] + kv_page_offset(a.v, max(page, 0), u.head) +
-                            (tok & (a.v.page_tokens - 1)) * D + vd;
+    };
+    auto load_v = [&](const Unit& u, int j, const Pages& p) {
+      const int tok = tile_token(u, j) + vt;
+      const uint8_t* from = a.v.codes[1] + kv_page_offset(a.v, max(p.v, 0), u.head) +
+                            (tok & page_mask) * D + vd;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const bool in = page >= 0 && tok + i < u.q.length && vd < D;
+        const bool in = p.v >= 0 && tok + i < u.q.length && vd < D;
         if constexpr (kLaneVBytes == 16) {
           const uint4 x = in ? __ldg(reinterpret_cast<const uint4*>(from + i * D))
                              : make_uint4(0, 0, 0, 0);
@@ -523,36 +568,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     };
-    auto load_factor = [&](const Unit& u, int j) {
-      // scales of the 16 tokens 16 lane .. of the tile (lanes 0..7 of one warp)
-      Factor c{1.0f, -INFINITY, 0.0f, 0.0f};
-      const int tok = tile_token(u, j) + 16 * lane;
-      if (tok < u.q.length) {
-        const int page = kv_page(a.v, u.s, tok >> a.v.page_shift);
-        if (page >= 0) {
-          const long long unit = static_cast<long long>(page) * a.v.heads + u.head;
-          c.k = __ldg(a.v.scale[0] + unit);
-          const float vs = __ldg(a.v.scale[1] + unit);
-          c.log2v = __log2f(vs);
-          c.inv = __fdividef(1.0f, vs);
-        }
+    float f_k = 1.0f, f_v = 0.0f;  // scales on their way
+    auto load_scales = [&](const Unit& u, const Pages& p) {
+      if (p.f >= 0) {
+        const long long unit = static_cast<long long>(p.f) * a.v.heads + u.head;
+        f_k = __ldg(a.v.scale[0] + unit);
+        f_v = __ldg(a.v.scale[1] + unit);
+      } else {
+        f_k = 1.0f;
+        f_v = 0.0f;  // log2: -inf, which masks the 16 tokens
       }
-      return c;
     };
 
-    for (long long k = 0; ok && unit_index(k) < total; ++k) {
-      const Unit u = decode_unit(a, s_prefix, per, unit_index(k));
+    for (uint32_t k = 0; ok; ++k) {
+      Unit u;
+      if (!take_unit(k, u) || u.n[0] < 0) break;
       const int n = max(u.n[0], u.n[1]);
-      if (n > 0) load_tile(u, 0);
+      if (n == 0) continue;
+      Pages next = pages_of(u, 0);
+      load_k(u, 0, next);
+      load_v(u, 0, next);
+      load_scales(u, next);
+      if (n > 1) next = pages_of(u, 1);
       for (int j = 0; j < n; ++j, ++it) {
         const uint32_t stage = it % kStages, phase = (it / kStages) & 1u;
-        Factor fac{};
-        if (w == 0 && lane < 8) fac = load_factor(u, j);
         if (!mbar_wait_warp(k_empty(stage), phase ^ 1u, wd, kSiteLoaderEmpty)) {
           ok = false;
           break;
         }
-        if (w == 0 && lane < 8) factors[(it % kFactorSlots) * 8 + lane] = fac;
+        if (w == 0 && lane < 8)
+          factors[(it % kFactorSlots) * 8 + lane] =
+              Factor{f_k, __log2f(f_v), f_v > 0.0f ? __fdividef(1.0f, f_v) : 0.0f, 0.0f};
         const uint32_t ks = base + L::kK + stage * L::kKBytes;
 #pragma unroll
         for (int o = 0; o < 4; ++o) {
@@ -575,6 +621,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           injected = true;  // withhold the CTA's first K tile: the MMA warp's wait runs out
         } else if (lane == 0) {
           mbar_arrive(k_full(stage));
+        }
+        if (j + 1 < n) {
+          load_k(u, j + 1, next);
+          load_scales(u, next);
         }
         if (!mbar_wait_warp(v_empty(stage), phase ^ 1u, wd, kSiteLoaderEmpty)) {
           ok = false;
@@ -614,20 +664,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(v_full(stage));
-        if (j + 1 < n) load_tile(u, j + 1);
+        if (j + 1 < n) load_v(u, j + 1, next);
+        if (j + 2 < n) next = pages_of(u, j + 2);
       }
     }
+  } else if (warp == kListWarp) {
+    // --------------------------------------------------------------- list --
+    if (lane == 0) {
+      for (uint32_t k = 0;; ++k) {
+        const uint32_t slot = k % kUnitSlots;
+        const long long at = atomicAdd(a.counter, 1u);
+        Unit u;
+        if (at < total) u = decode_unit(a, s_prefix, per, at);
+        else u.n[0] = -1;
+        if (!mbar_wait(u_empty(slot), ((k / kUnitSlots) & 1u) ^ 1u, wd, kSiteSched)) break;
+        reinterpret_cast<Unit*>(gbase + L::kUnits)[slot] = u;
+        mbar_arrive(u_full(slot));
+        if (at >= total) break;
+      }
+    }
+    __syncwarp();
   } else {
     // --------------------------------------------------------- MMA issuer --
-    if (lane == 0) {
+    {
       constexpr uint32_t kIdescS = idesc_f16_f32(kTile, kTile), kIdescO = idesc_f16_f32(kTile, HSP);
       uint32_t it = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
       bool ok = true;
-      for (long long k = 0; ok && unit_index(k) < total; ++k) {
-        const Unit u = decode_unit(a, s_prefix, per, unit_index(k));
+      for (uint32_t k = 0; ok; ++k) {
+        Unit u;
+        if (!take_unit(k, u) || u.n[0] < 0) break;
         const int n = max(u.n[0], u.n[1]);
         if (n == 0) continue;
-        for (int j = 0; ok && j <= n; ++j) {
+        if (lane == 0) for (int j = 0; ok && j <= n; ++j) {
           const uint32_t stage = (it + j) % kStages, phase = ((it + j) / kStages) & 1u;
           const uint32_t prev = (it + j - 1) % kStages, prev_phase = ((it + j - 1) / kStages) & 1u;
 #pragma unroll
@@ -679,11 +747,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (j >= 1) umma_commit(v_empty(prev));
         }
         it += n;
+        ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;  // lane 0's: the warp leaves together
       }
       // Every MMA must be complete before TMEM and shared memory go away.
-      umma_commit(drain);
-      const uint64_t t0 = globaltimer_ns();
-      while (!mbar_test(drain, 0) && globaltimer_ns() - t0 < a.wait_limit_ns) {
+      if (lane == 0) {
+        umma_commit(drain);
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_test(drain, 0) && globaltimer_ns() - t0 < a.wait_limit_ns) {
+        }
       }
     }
     __syncwarp();
@@ -707,8 +778,8 @@ cudaError_t launch_prompt(const PromptArgs& a, const DeviceInfo& dev, cudaStream
 }  // namespace
 
 int cache_prompt_launch(const csa_kv_cache& cache, const csa_kv_batch& batch,
-                        const AttendCall& call, int row_limit, cudaStream_t stream,
-                        const DeviceInfo& dev, std::string& err) {
+                        const AttendCall& call, int row_limit, unsigned int* counter,
+                        cudaStream_t stream, const DeviceInfo& dev, std::string& err) {
   PromptArgs a;
   a.v = kv_view(cache, batch, dev);
   a.q = call.q;
@@ -727,6 +798,7 @@ int cache_prompt_launch(const csa_kv_cache& cache, const csa_kv_batch& batch,
   a.status = dev.status_word;
   a.wait_limit_ns = wait_limit_ns();
   a.inject = take_inject() ? 1 : 0;
+  a.counter = counter;
   int rc = CSA_OK;
   cudaError_t e;
   if (cache.head_size <= 64)

@@ -200,10 +200,10 @@ int cache_attention_launch(const csa_kv_cache& cache, const csa_kv_batch& batch,
                            std::string& err);
 
 // The tcgen05 form, for the sequences of more than row_limit rows (tokens x query
-// heads of a kv head).
+// heads of a kv head). `counter` (device) must be zero when the kernel starts.
 int cache_prompt_launch(const csa_kv_cache& cache, const csa_kv_batch& batch,
-                        const AttendCall& call, int row_limit, cudaStream_t stream,
-                        const DeviceInfo& dev, std::string& err);
+                        const AttendCall& call, int row_limit, unsigned int* counter,
+                        cudaStream_t stream, const DeviceInfo& dev, std::string& err);
 
 // The device's view of a cache and a batch (kv_cache.cuh).
 struct KvView;
