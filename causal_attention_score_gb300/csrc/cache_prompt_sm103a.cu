@@ -175,18 +175,51 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       : "memory");
 }
 
-// 32 lanes x 32 consecutive 32-bit columns from 32 registers, without the wait.
-__device__ __forceinline__ void tmem_st_32cols_async(uint32_t taddr, const uint32_t (&r)[32]) {
+// 32 lanes x 16 consecutive 32-bit columns from 16 registers, without the wait.
+__device__ __forceinline__ void tmem_st_16cols(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, "
-      "%21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
-      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "r"(r[15])
       : "memory");
+}
+__device__ __forceinline__ void tmem_ld_16cols(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+// 32 columns without the wait: valid after tmem_wait_ld_32 on the same array.
+__device__ __forceinline__ void tmem_ld_32cols_async(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, "
+      "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld_32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -280,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The k-th unit that this CTA works on, for a whole warp; false: a wait ran out.
   auto take_unit = [&](uint32_t k, Unit& u) {
     const uint32_t slot = k % kUnitSlots;
-    if (!mbar_wait_warp(u_full(slot), (k / kUnitSlots) & 1u, wd, kSiteSched)) return false;
+    if (!mbar_wait_warp_inline(u_full(slot), (k / kUnitSlots) & 1u, wd, kSiteSched)) return false;
     u = reinterpret_cast<const Unit*>(gbase + L::kUnits)[slot];
     __syncwarp();
     if (lane == 0) mbar_arrive(u_empty(slot));
@@ -354,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int pos_high = __reduce_max_sync(0xFFFFFFFFu, pos);
       for (int j = 0; j < n; ++j) {
         const int tb = tile_token(u, j);
-        if (!mbar_wait_warp(s_full(g), tiles_done & 1u, wd, kSiteEpilogueFull)) {
+        if (!mbar_wait_warp_inline(s_full(g), tiles_done & 1u, wd, kSiteEpilogueFull)) {
           ok = false;
           break;
         }
@@ -370,70 +403,72 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int sink_cols = a.window ? a.sinks - tb : 0;
         auto softmax = [&](auto edge_tile) {
           constexpr bool kEdge = decltype(edge_tile)::value;
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            uint32_t x[64];
-            // x = score * f * c.k + c.log2v - less, masked: -inf; returns the maximum
-            auto scores = [&](float less) {
-              tmem_ld_64cols(s_tmem + 64 * h, x);
-              float top = -INFINITY;
+          // x = score * f * c.k + c.log2v - less of 32 keys, masked: -inf; returns the maximum
+          auto scores = [&](int h, uint32_t (&x)[32], float less) {
+            float top = -INFINITY;
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const Factor c = fac[4 * h + i];
-                const float fk = f * c.k, add = c.log2v - less;
-                const uint64_t fk2 = pack_f32x2(fk, fk), add2 = pack_f32x2(add, add);
+            for (int i = 0; i < 2; ++i) {
+              const Factor c = fac[2 * h + i];
+              const float fk = f * c.k, add = c.log2v - less;
+              const uint64_t fk2 = pack_f32x2(fk, fk), add2 = pack_f32x2(add, add);
 #pragma unroll
-                for (int e = 0; e < 16; e += 2) {
-                  const int at = 16 * i + e;
-                  float y0, y1;
-                  fma_f32x2(y0, y1, __uint_as_float(x[at]), __uint_as_float(x[at + 1]), fk2, add2);
-                  if (kEdge) {
-                    const int c0 = 64 * h + at;
-                    if (c0 > last || (c0 < first_window && c0 >= sink_cols)) y0 = -INFINITY;
-                    if (c0 + 1 > last || (c0 + 1 < first_window && c0 + 1 >= sink_cols))
-                      y1 = -INFINITY;
-                  }
-                  x[at] = __float_as_uint(y0);
-                  x[at + 1] = __float_as_uint(y1);
-                  top = fmaxf(top, fmaxf(y0, y1));
+              for (int e = 0; e < 16; e += 2) {
+                const int at = 16 * i + e;
+                float y0, y1;
+                fma_f32x2(y0, y1, __uint_as_float(x[at]), __uint_as_float(x[at + 1]), fk2, add2);
+                if (kEdge) {
+                  const int c0 = 32 * h + at;
+                  if (c0 > last || (c0 < first_window && c0 >= sink_cols)) y0 = -INFINITY;
+                  if (c0 + 1 > last || (c0 + 1 < first_window && c0 + 1 >= sink_cols))
+                    y1 = -INFINITY;
                 }
+                x[at] = __float_as_uint(y0);
+                x[at + 1] = __float_as_uint(y1);
+                top = fmaxf(top, fmaxf(y0, y1));
               }
-              return top;
-            };
-            const float top = scores(m);
+            }
+            return top;
+          };
+          // Weights of keys 32 h .. from their scores in x, to P.
+          auto quarter = [&](int h, uint32_t (&x)[32]) {
+            const float top = scores(h, x, m);
             if (__any_sync(0xFFFFFFFFu, top > kRaise)) {
-              const float to = fmaxf(m, scores(0.0f));
+              // (rare) the true values from S again, the new maximum, and what was
+              // computed with the old one: O, l, this tile's weights so far
+              tmem_ld_32cols(s_tmem + 32 * h, x);
+              const float to = fmaxf(m, scores(h, x, 0.0f));
               const float corr = ex2_approx(m - to);
               m = to;
               l *= corr;
 #pragma unroll
-              for (int i = 0; i < 64; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) - m);
-              uint32_t y[32];
+              for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) - m);
+              uint32_t y[16];
               if (j > 0) {
                 // (the product that last added to O precedes this tile's S)
 #pragma unroll 1
-                for (int c = 0; c < HSP; c += 32) {
-                  tmem_ld_32cols(o_tmem + c, y);
+                for (int c = 0; c < HSP; c += 16) {
+                  tmem_ld_16cols(o_tmem + c, y);
 #pragma unroll
-                  for (int i = 0; i < 32; ++i)
+                  for (int i = 0; i < 16; ++i)
                     y[i] = __float_as_uint(__uint_as_float(y[i]) * corr);
-                  tmem_st_32cols(o_tmem + c, y);
+                  tmem_st_16cols(o_tmem + c, y);
                 }
               }
-              if (h == 1) {
-                // the first half's weights; in fp32, as corr may be below fp16's range
-                tmem_wait_st();
-                tmem_ld_32cols(s_tmem, y);
+              tmem_wait_st();
+#pragma unroll 1
+              for (int c = 0; c < 16 * h; c += 16) {
+                tmem_ld_16cols(s_tmem + c, y);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
+                for (int i = 0; i < 16; ++i) {
                   const float2 w = __half22float2(*reinterpret_cast<__half2*>(&y[i]));
                   y[i] = half2_of(w.x * corr, w.y * corr);
                 }
-                tmem_st_32cols(s_tmem, y);
+                tmem_st_16cols(s_tmem + c, y);
               }
             }
+            uint32_t p[16];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 2; ++i) {
               uint64_t sum = 0;
 #pragma unroll
               for (int e = 0; e < 16; e += 2) {
@@ -441,17 +476,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float y0 = ex2_approx(__uint_as_float(x[at]));
                 const float y1 = ex2_approx(__uint_as_float(x[at + 1]));
                 sum = add_f32x2(sum, pack_f32x2(y0, y1));
-                x[at / 2] = half2_of(y0, y1);
+                p[at / 2] = half2_of(y0, y1);
               }
               float s0, s1;
               unpack_f32x2(sum, s0, s1);
-              l = fmaf(s0 + s1, fac[4 * h + i].inv, l);
+              l = fmaf(s0 + s1, fac[2 * h + i].inv, l);
             }
-            // P over S: columns 32 h .., whose scores have been read
-            uint32_t p[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) p[i] = x[i];
-            tmem_st_32cols_async(s_tmem + 32 * h, p);
+            // P over S: columns 16 h .., whose scores have been read
+            tmem_st_16cols(s_tmem + 16 * h, p);
+          };
+          // The next quarter's scores are on their way while one is worked on.
+          uint32_t xa[32], xb[32];
+          tmem_ld_32cols_async(s_tmem, xa);
+          tmem_wait_ld_32(xa);
+#pragma unroll 1
+          for (int h = 0; h < 4; h += 2) {
+            tmem_ld_32cols_async(s_tmem + 32 * (h + 1), xb);
+            quarter(h, xa);
+            tmem_wait_ld_32(xb);
+            if (h < 2) tmem_ld_32cols_async(s_tmem + 32 * (h + 2), xa);
+            quarter(h + 1, xb);
+            tmem_wait_ld_32(xa);
           }
         };
         if (edge) softmax(std::true_type{});
@@ -464,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       it += n_all;
       if (!ok) break;
       if (n > 0) {
-        if (!mbar_wait_warp(o_full(g), o_phase, wd, kSiteEpilogueFull)) break;
+        if (!mbar_wait_warp_inline(o_full(g), o_phase, wd, kSiteEpilogueFull)) break;
         o_phase ^= 1u;
         tc_fence_after_sync();
       }
@@ -515,45 +560,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t vx[8][kLaneVBytes / 4];
     bool ok = true, injected = false;
 
-    // Pages of a tile's tokens that this lane takes: four of K, one of V, and (lanes
-    // 0..7 of warp 0) that of the 16 tokens whose factors it makes. -1: none there.
-    struct Pages {
-      int k[4], v, f;
-    };
+    // The pages of a tile's eight groups of 16 tokens, in lanes 0..7 (-1: none there).
     auto pages_of = [&](const Unit& u, int j) {
-      const int tb = tile_token(u, j);
-      auto page = [&](int tok) {
-        return tok < u.q.length ? kv_page(a.v, u.s, tok >> a.v.page_shift) : -1;
-      };
-      Pages p;
-#pragma unroll
-      for (int o = 0; o < 4; ++o) p.k[o] = page(tb + 32 * w + 8 * o + (lane & 7));
-      p.v = page(tb + vt);
-      p.f = w == 0 && lane < 8 ? page(tb + 16 * lane) : -1;
-      return p;
+      const int tok = tile_token(u, j) + 16 * lane;
+      return lane < 8 && tok < u.q.length ? kv_page(a.v, u.s, tok >> a.v.page_shift) : -1;
     };
+    const long long page_bytes = static_cast<long long>(a.v.page_tokens) * D;
     const int page_mask = a.v.page_tokens - 1;
-    auto load_k = [&](const Unit& u, int j, const Pages& p) {
+    auto load_k = [&](const Unit& u, int j, int pages) {
       const int tb = tile_token(u, j);
 #pragma unroll
-      for (int o = 0; o < 4; ++o) {
-        const int tok = tb + 32 * w + 8 * o + (lane & 7);
-        const uint8_t* from = a.v.codes[0] + kv_page_offset(a.v, max(p.k[o], 0), u.head) +
-                              (tok & page_mask) * D + 16 * (lane >> 3);
+      for (int half = 0; half < 2; ++half) {  // 16 tokens each
+        const int page = __shfl_sync(0xFFFFFFFFu, pages, 2 * w + half);
+        const int tok = tb + 32 * w + 16 * half + (lane & 7);
+        const uint8_t* from =
+            a.v.codes[0] + (static_cast<long long>(page) * a.v.heads + u.head) * page_bytes +
+            ((tok & page_mask) * D + 16 * (lane >> 3));
 #pragma unroll
-        for (int h = 0; h < HSP / 64; ++h)
-          kx[o * (HSP / 64) + h] = p.k[o] >= 0 && 64 * h + 16 * (lane >> 3) < D
-                                       ? __ldg(reinterpret_cast<const uint4*>(from + 64 * h))
-                                       : make_uint4(0, 0, 0, 0);
+        for (int o = 0; o < 2; ++o)
+#pragma unroll
+          for (int h = 0; h < HSP / 64; ++h)
+            kx[(2 * half + o) * (HSP / 64) + h] =
+                page >= 0 && 64 * h + 16 * (lane >> 3) < D
+                    ? __ldg(reinterpret_cast<const uint4*>(from + 8 * o * D + 64 * h))
+                    : make_uint4(0, 0, 0, 0);
       }
     };
-    auto load_v = [&](const Unit& u, int j, const Pages& p) {
+    auto load_v = [&](const Unit& u, int j, int pages) {
       const int tok = tile_token(u, j) + vt;
-      const uint8_t* from = a.v.codes[1] + kv_page_offset(a.v, max(p.v, 0), u.head) +
-                            (tok & page_mask) * D + vd;
+      const int page = __shfl_sync(0xFFFFFFFFu, pages, vt >> 4);
+      const uint8_t* from =
+          a.v.codes[1] + (static_cast<long long>(page) * a.v.heads + u.head) * page_bytes +
+          ((tok & page_mask) * D + vd);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const bool in = p.v >= 0 && tok + i < u.q.length && vd < D;
+        const bool in = page >= 0 && tok + i < u.q.length && vd < D;
         if constexpr (kLaneVBytes == 16) {
           const uint4 x = in ? __ldg(reinterpret_cast<const uint4*>(from + i * D))
                              : make_uint4(0, 0, 0, 0);
@@ -569,9 +610,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     float f_k = 1.0f, f_v = 0.0f;  // scales on their way
-    auto load_scales = [&](const Unit& u, const Pages& p) {
-      if (p.f >= 0) {
-        const long long unit = static_cast<long long>(p.f) * a.v.heads + u.head;
+    auto load_scales = [&](const Unit& u, int pages) {
+      if (w != 0) return;
+      if (pages >= 0) {
+        const long long unit = static_cast<long long>(pages) * a.v.heads + u.head;
         f_k = __ldg(a.v.scale[0] + unit);
         f_v = __ldg(a.v.scale[1] + unit);
       } else {
@@ -585,14 +627,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!take_unit(k, u) || u.n[0] < 0) break;
       const int n = max(u.n[0], u.n[1]);
       if (n == 0) continue;
-      Pages next = pages_of(u, 0);
+      int next = pages_of(u, 0);
       load_k(u, 0, next);
       load_v(u, 0, next);
       load_scales(u, next);
       if (n > 1) next = pages_of(u, 1);
       for (int j = 0; j < n; ++j, ++it) {
         const uint32_t stage = it % kStages, phase = (it / kStages) & 1u;
-        if (!mbar_wait_warp(k_empty(stage), phase ^ 1u, wd, kSiteLoaderEmpty)) {
+        if (!mbar_wait_warp_inline(k_empty(stage), phase ^ 1u, wd, kSiteLoaderEmpty)) {
           ok = false;
           break;
         }
@@ -626,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           load_k(u, j + 1, next);
           load_scales(u, next);
         }
-        if (!mbar_wait_warp(v_empty(stage), phase ^ 1u, wd, kSiteLoaderEmpty)) {
+        if (!mbar_wait_warp_inline(v_empty(stage), phase ^ 1u, wd, kSiteLoaderEmpty)) {
           ok = false;
           break;
         }
