@@ -5,24 +5,27 @@
 // A unit of work is 256 rows (tokens x query heads of one kv head) of a
 // sequence: two groups A and B of 128, each a TMEM accumulator's lanes, which
 // share every tile of 128 keys. One CTA per SM takes units from a counter
-// (longest first within a sequence), with 14 warps:
+// (longest first within a sequence), with 15 warps:
 //  - warps 0..7: softmax, warps 0..3 group A, 4..7 group B, a thread a row. Per
 //    half tile of 64 keys: scores from TMEM, x - m, their maximum, and the
 //    weights exp2(x - m) as fp16 over S (P, the second product's A operand in
 //    TMEM). m is raised only when a value passes m + 8; then the thread's O row,
-//    its l and the weights of the tile so far are rescaled. Before a unit they
-//    turn Q's rows into fp16 in shared memory; after it they write O / l.
+//    its l and the half tile's weights so far are rescaled. Before a unit they
+//    copy Q's rows to shared memory; after it they write O / l.
 //  - warps 8..11: conversion. Codes come from HBM into registers a tile ahead
-//    (their page numbers two), become fp16 exactly, and go to shared memory in the
-//    128-byte-swizzle K-major layout: K as [token][element], V transposed in
-//    registers to [element][token]. Two stages each.
-//  - warp 12: one thread issues, per tile, O_A += P_A V, S_A = Q_A K^T of the next
-//    tile, and the same for B: while one group is in its softmax, the tensor core
-//    works for the other. MMAs run in issue order, so S_A may overwrite P_A.
-//  - warp 13: takes units from the counter (workspace, cleared by the rows kernel
+//    (their page numbers two) and go to shared memory in the 128-byte-swizzle
+//    K-major layout, K as [token][element] in Q's type, V transposed in registers
+//    to [element][token] in fp16 (both exact). Two stages each.
+//  - warps 12 and 13: one thread each issues a group's products: per half tile
+//    S = Q K^T of the next one, then O += P V of this one. S has two buffers of 64
+//    columns, so the softmax finds the next scores ready when it is done with the
+//    last. A thread's MMAs run in issue order, so S may overwrite the weights that
+//    the product issued before it reads. (With both groups on one warp the issue
+//    itself, some 90 cycles an MMA, was the longest path.)
+//  - warp 14: takes units from the counter (workspace, cleared by the rows kernel
 //    ahead in the stream) and passes them on a unit ahead.
 //
-// Scales (see cache_attention_sm103a.cu): with K's and V's scales per 16 tokens in
+// Scales (see cache_attention_sm103a.cu): with c ks and log2(vs) per 16 tokens in
 // shared memory, x = s (c ks) + log2(vs) and the weight has V's scale in it; the
 // denominator sums w / vs.
 //
@@ -48,14 +51,15 @@ namespace {
 constexpr int kSoftmaxWarps = 8;
 constexpr int kConvertWarps = 4;
 constexpr int kMmaWarp = kSoftmaxWarps + kConvertWarps;
-constexpr int kListWarp = kMmaWarp + 1;
+constexpr int kListWarp = kMmaWarp + 2;
 constexpr int kThreads = 32 * (kListWarp + 1);
 constexpr int kTile = 128;          // keys per tile, rows per group
 constexpr int kUnitRows = 2 * kTile;
 constexpr int kStages = 2;
 constexpr int kFactorSlots = 4;
 constexpr int kUnitSlots = 2;
-constexpr int kTmemCols = 512;      // S_A, S_B, O_A, O_B
+constexpr int kHalf = 64;           // keys per step of the products and the softmax
+constexpr int kTmemCols = 512;      // S_A (two buffers), S_B, O_A, O_B
 constexpr float kRaise = 8.0f;
 constexpr float kNothing = -1e30f;  // the running maximum of a row that has seen nothing
 
@@ -68,15 +72,15 @@ struct PromptArgs {
   int group;
   int window, sinks;
   int row_limit;        // sequences of at most this many rows are the rows kernel's
-  float scale_log2;     // its magnitude
-  uint32_t q_flip;      // sign bits flipped in Q's words where the scale is negative
+  float scale_log2;
   unsigned int* counter;  // units taken, zero at launch
   int* status;
   unsigned long long wait_limit_ns;
   int inject;
 };
 
-// What 16 keys' scores are multiplied with, log2 of their V's scale, its inverse.
+// What 16 keys' scores are multiplied with (to the base-2 exponent), log2 of their V's
+// scale, its inverse.
 struct Factor {
   float k, log2v, inv, pad;
 };
@@ -85,7 +89,8 @@ struct Unit {
   KvSequence q;
   int s, head, row0, rows;  // rows [row0, row0 + rows) of the sequence
   int sink_tiles, window_tile;
-  int n[2];                 // tiles of each group; n[0] < 0: the list has ended
+  int tiles;                // of 128 keys
+  int n[2];                 // half tiles of each group; n[0] < 0: the list has ended
 };
 
 template <int HSP>
@@ -96,7 +101,7 @@ struct Layout {
   static constexpr int kQ = 0, kK = 2 * kQBytes, kV = kK + kStages * kKBytes,
                        kFactors = kV + kStages * kVBytes,
                        kBars = kFactors + kFactorSlots * 8 * static_cast<int>(sizeof(Factor)),
-                       kMisc = kBars + 8 * 22, kUnits = kMisc + 16,
+                       kMisc = kBars + 8 * 30, kUnits = kMisc + 16,
                        kTotal = kUnits + kUnitSlots * static_cast<int>(sizeof(Unit));
 };
 
@@ -143,8 +148,10 @@ __device__ Unit decode_unit(const PromptArgs& a, const long long* prefix, int pe
     r.n[g] = 0;
     if (rows <= 0) continue;
     const int last = r.q.first + (r.row0 + g * kTile + rows - 1) / a.group;  // position
-    if (last >= 0) r.n[g] = r.sink_tiles + max(last / kTile + 1 - r.window_tile, 0);
+    if (last >= 0)
+      r.n[g] = 2 * r.sink_tiles + max(last / kHalf + 1 - 2 * r.window_tile, 0);
   }
+  r.tiles = (max(r.n[0], r.n[1]) + 1) / 2;
   return r;
 }
 
@@ -158,20 +165,41 @@ __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
   return r;
 }
 
+// One lane of a converged warp: its MMAs' operands may stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // Instruction descriptor, kind::f16: A = B = fp16, D = f32, both K-major.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// D[tmem] (+)= A[tmem] * B[smem]^T for 16-bit operands: A's 128 rows are TMEM
-// lanes, two K-elements to a 32-bit column.
-__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                            uint32_t idesc, uint32_t accumulate) {
+// D[tmem] (+)= A * B[smem]^T for 16-bit operands, A in shared memory (ss) or in TMEM
+// (ts: 128 rows are lanes, two K-elements to a 32-bit column). Shared-memory
+// descriptors as their low words and the high word that all of them share.
+__device__ __forceinline__ void umma_f16_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
+                                            uint32_t hi, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
+                                            uint32_t hi, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 
@@ -225,11 +253,17 @@ __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// 16-byte global -> shared copy past L1; zeros where bytes is 0.
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+
 __device__ __forceinline__ void st_shared16(uint32_t addr, const uint32_t* w) {
   st_shared_v4(addr, w[0], w[1], w[2], w[3]);
 }
 
-template <int HSP, int kFormat>
+template <int HSP, int kFormat, bool kBf16>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_prompt_sm103a_kernel(const PromptArgs a) {
   using L = Layout<HSP>;
@@ -245,35 +279,39 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto v_full = [&](uint32_t s) { return bars + 8u * (4 + s); };
   auto v_empty = [&](uint32_t s) { return bars + 8u * (6 + s); };
   auto q_ready = [&](uint32_t g) { return bars + 8u * (8 + g); };
-  auto s_full = [&](uint32_t g) { return bars + 8u * (10 + g); };
-  auto p_ready = [&](uint32_t g) { return bars + 8u * (12 + g); };
-  auto o_full = [&](uint32_t g) { return bars + 8u * (14 + g); };
-  const uint32_t drain = bars + 8u * 16;
-  auto u_full = [&](uint32_t s) { return bars + 8u * (17 + s); };
-  auto u_empty = [&](uint32_t s) { return bars + 8u * (19 + s); };
+  // (of a group's even and odd products: a parity tells only neighbouring phases apart,
+  // and a waiter may be up to two products behind)
+  auto pv_done = [&](uint32_t g, uint32_t b) { return bars + 8u * (25 + 2 * g + b); };
+  auto s_full = [&](uint32_t g, uint32_t b) { return bars + 8u * (12 + 2 * g + b); };
+  auto p_ready = [&](uint32_t g, uint32_t b) { return bars + 8u * (16 + 2 * g + b); };
+  auto u_full = [&](uint32_t s) { return bars + 8u * (20 + s); };
+  auto u_empty = [&](uint32_t s) { return bars + 8u * (22 + s); };
+  const uint32_t drain = bars + 8u * 24;
   const uint32_t tmem_slot = base + L::kMisc;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::kMisc + 4);
   Factor* factors = reinterpret_cast<Factor*>(gbase + L::kFactors);
   const Watchdog wd{a.wait_limit_ns, a.status, abort_flag};
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(k_full(s), kConvertWarps);
       mbar_init(v_full(s), kConvertWarps);
-      mbar_init(k_empty(s), 1);
-      mbar_init(v_empty(s), 1);
+      mbar_init(k_empty(s), 2);  // one commit of each group's issuer
+      mbar_init(v_empty(s), 2);
     }
     for (int g = 0; g < 2; ++g) {
       mbar_init(q_ready(g), 4);
-      mbar_init(s_full(g), 1);
-      mbar_init(p_ready(g), 4);
-      mbar_init(o_full(g), 1);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(pv_done(g, b), 1);
+        mbar_init(s_full(g, b), 1);
+        mbar_init(p_ready(g, b), 4);
+      }
     }
-    mbar_init(drain, 1);
+    mbar_init(drain, 2);
     for (int s = 0; s < kUnitSlots; ++s) {
       mbar_init(u_full(s), 1);
-      mbar_init(u_empty(s), kMmaWarp + 1);  // every warp but the list's
+      mbar_init(u_empty(s), kListWarp);  // every warp but the list's
     }
     *abort_flag = 0;
     fence_barrier_init();
@@ -308,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
   tc_fence_after_sync();
-  const uint32_t tmem = ld_shared_b32(tmem_slot);
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, ld_shared_b32(tmem_slot), 0);
   const long long total = s_prefix[kThreads];
   // The k-th unit that this CTA works on, for a whole warp; false: a wait ran out.
   auto take_unit = [&](uint32_t k, Unit& u) {
@@ -326,91 +364,78 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t g = warp >> 2;
     const int r = threadIdx.x & 127;                       // row of the group
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lane field
-    const uint32_t s_tmem = tmem + lanes + g * kTile;
     const uint32_t o_tmem = tmem + lanes + 2 * kTile + g * HSP;
     const uint32_t q_smem = base + L::kQ + g * L::kQBytes;
-    uint32_t tiles_done = 0, o_phase = 0;
-    uint32_t it = 0;  // tiles of the CTA so far (the factors' slots)
+    // Rows go between HBM and shared memory a warp's 32 at a time: kLanes lanes of 16
+    // bytes to a row.
+    constexpr int kLanes = HSP / 8, kRowsAtOnce = 32 / kLanes;
+    const int piece = lane % kLanes;  // this lane's 8 elements of such a row
+    uint32_t products = 0;            // of the group, before this unit
+    uint32_t tiles = 0;               // of the CTA, before this unit (the factors' slots)
     bool ok = true;
     for (uint32_t k = 0; ok; ++k) {
       Unit u;
       if (!take_unit(k, u) || u.n[0] < 0) break;
-      const int n = g == 0 ? u.n[0] : u.n[1], n_all = max(u.n[0], u.n[1]);
+      const int n = g == 0 ? u.n[0] : u.n[1];
       const int rr = u.row0 + static_cast<int>(g) * kTile + r;
       const int j_tok = rr / a.group;
+      const int q_row = u.q.row0 + j_tok, q_hd = u.head * a.group + (rr - j_tok * a.group);
       const bool live = static_cast<int>(g) * kTile + r < u.rows;
       const int pos = live ? u.q.first + j_tok : -1;
-      const long long out_at = (u.q.row0 + j_tok) * a.out_token +
-                               (u.head * a.group + (rr - j_tok * a.group)) * a.out_head;
-      float l = 0.0f, m = kNothing, f = 0.0f;
+      float l = 0.0f, m = kNothing;
       if (n > 0) {
-        // Q's row to fp16 in shared memory (the group's last S product is complete:
-        // this thread has seen its o_full)
-        const uint32_t* from = reinterpret_cast<const uint32_t*>(
-            static_cast<const uint16_t*>(a.q) + (u.q.row0 + j_tok) * a.q_token +
-            (u.head * a.group + (rr - j_tok * a.group)) * a.q_head);
-        uint32_t w[HSP / 2];
-        float most = 0.0f;
-#pragma unroll
-        for (int i = 0; i < HSP / 8; ++i) {
-          const uint4 x = live && i * 8 < D ? reinterpret_cast<const uint4*>(from)[i]
-                                            : make_uint4(0, 0, 0, 0);
-          w[4 * i] = x.x ^ a.q_flip;
-          w[4 * i + 1] = x.y ^ a.q_flip;
-          w[4 * i + 2] = x.z ^ a.q_flip;
-          w[4 * i + 3] = x.w ^ a.q_flip;
+        // Q's rows to shared memory (the group's last S product is complete: this thread
+        // has seen the end of the product after it)
+#pragma unroll 4
+        for (int i = 0; i < kLanes; ++i) {
+          const int from = i * kRowsAtOnce + lane / kLanes;  // row of the warp
+          const int row = __shfl_sync(0xFFFFFFFFu, live ? q_row : -1, from);
+          const int head = __shfl_sync(0xFFFFFFFFu, q_hd, from);
+          const bool in = row >= 0 && piece * 8 < D;
+          const uint32_t sr = static_cast<uint32_t>((warp & 3) * 32 + from);
+          cp_async_16(q_smem + (piece >> 3) * (kTile * 128) + sr * 128 +
+                          (((piece & 7) ^ (sr & 7)) << 4),
+                      static_cast<const uint16_t*>(a.q) +
+                          (in ? row * a.q_token + head * a.q_head + piece * 8 : 0),
+                      in ? 16u : 0u);
         }
-        float back = 1.0f;
-        if (!a.half) {
-#pragma unroll
-          for (int i = 0; i < HSP / 2; ++i)
-            most = fmaxf(most, fmaxf(fabsf(__uint_as_float(w[i] << 16)),
-                                     fabsf(__uint_as_float(w[i] & 0xFFFF0000u))));
-          const uint32_t e = max(__float_as_uint(most) >> 23, 15u);
-          const float up = __uint_as_float((268u - e) << 23);  // 2^(14 - exponent)
-          back = __uint_as_float((e - 14u) << 23);
-#pragma unroll
-          for (int i = 0; i < HSP / 2; ++i)
-            w[i] = half2_of(__uint_as_float(w[i] << 16) * up,
-                            __uint_as_float(w[i] & 0xFFFF0000u) * up);
-        }
-        f = a.scale_log2 * back;
-#pragma unroll
-        for (int i = 0; i < HSP / 8; ++i)
-          st_shared16(q_smem + (i >> 3) * (kTile * 128) + r * 128 + (((i & 7) ^ (r & 7)) << 4),
-                      w + 4 * i);
+        cp_async_commit();
+        cp_async_wait<0>();
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_ready(g));
       }
       const int pos_low = __reduce_min_sync(0xFFFFFFFFu, live ? pos : 0x7FFFFFFF);
       const int pos_high = __reduce_max_sync(0xFFFFFFFFu, pos);
-      for (int j = 0; j < n; ++j) {
-        const int tb = tile_token(u, j);
-        if (!mbar_wait_warp_inline(s_full(g), tiles_done & 1u, wd, kSiteEpilogueFull)) {
+      for (int step = 0; ok && step < n; ++step) {
+        const uint32_t buffer = (products + step) & 1u;
+        const uint32_t s_tmem = tmem + lanes + g * kTile + buffer * kHalf;
+        const int tb = tile_token(u, step >> 1) + (step & 1) * kHalf;
+        if (!mbar_wait_warp_inline(s_full(g, buffer), ((products + step) >> 1) & 1u, wd,
+                                   kSiteEpilogueFull)) {
           ok = false;
           break;
         }
-        ++tiles_done;
         tc_fence_after_sync();
-        const Factor* fac = factors + ((it + j) % kFactorSlots) * 8;
-        const bool edge = !(tb + kTile - 1 <= pos_low &&
-                            (a.window == 0 || pos_high - tb < a.window || tb + kTile - 1 < a.sinks));
+        const Factor* fac =
+            factors + ((tiles + (step >> 1)) % kFactorSlots) * 8 + (step & 1) * 4;
+        const bool edge = !(tb + kHalf - 1 <= pos_low &&
+                            (a.window == 0 || pos_high - tb < a.window || tb + kHalf - 1 < a.sinks));
         // columns 0 .. last are at or before this row; from first_window on, or below
         // sink_cols, they are in its window or sinks
         const int last = pos - tb;
-        const int first_window = a.window ? last - a.window + 1 : -kTile;
+        const int first_window = a.window ? last - a.window + 1 : -kHalf;
         const int sink_cols = a.window ? a.sinks - tb : 0;
         auto softmax = [&](auto edge_tile) {
           constexpr bool kEdge = decltype(edge_tile)::value;
-          // x = score * f * c.k + c.log2v - less of 32 keys, masked: -inf; returns the maximum
+          // x = score * c.k + c.log2v - less of 32 keys, masked: -inf; returns the maximum
           auto scores = [&](int h, uint32_t (&x)[32], float less) {
             float top = -INFINITY;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const Factor c = fac[2 * h + i];
-              const float fk = f * c.k, add = c.log2v - less;
-              const uint64_t fk2 = pack_f32x2(fk, fk), add2 = pack_f32x2(add, add);
+              const float add = c.log2v - less;
+              const uint64_t fk2 = pack_f32x2(c.k, c.k), add2 = pack_f32x2(add, add);
 #pragma unroll
               for (int e = 0; e < 16; e += 2) {
                 const int at = 16 * i + e;
@@ -429,12 +454,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             return top;
           };
-          // Weights of keys 32 h .. from their scores in x, to P.
-          auto quarter = [&](int h, uint32_t (&x)[32]) {
+          // Weights of keys 32 h .. from their scores in x, to P. `coming`: registers
+          // that a TMEM load may still be writing.
+          auto quarter = [&](int h, uint32_t (&x)[32], uint32_t (&coming)[32]) {
             const float top = scores(h, x, m);
             if (__any_sync(0xFFFFFFFFu, top > kRaise)) {
               // (rare) the true values from S again, the new maximum, and what was
-              // computed with the old one: O, l, this tile's weights so far
+              // computed with the old one: O, l, this half's weights so far
+              tmem_wait_ld_32(coming);
               tmem_ld_32cols(s_tmem + 32 * h, x);
               const float to = fmaxf(m, scores(h, x, 0.0f));
               const float corr = ex2_approx(m - to);
@@ -443,8 +470,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) - m);
               uint32_t y[16];
-              if (j > 0) {
-                // (the product that last added to O precedes this tile's S)
+              if (step > 0) {
+                // O is the product issued last's until that is complete (the one before
+                // it is: this half tile's scores were issued later)
+                const uint32_t before = products + step - 1;
+                if (!mbar_wait_warp_inline(pv_done(g, before & 1u), (before >> 1) & 1u, wd,
+                                           kSiteEpilogueFull))
+                  ok = false;
+                tc_fence_after_sync();
 #pragma unroll 1
                 for (int c = 0; c < HSP; c += 16) {
                   tmem_ld_16cols(o_tmem + c, y);
@@ -485,36 +518,35 @@ __global__ void __launch_bounds__(kThreads, 1)
             // P over S: columns 16 h .., whose scores have been read
             tmem_st_16cols(s_tmem + 16 * h, p);
           };
-          // The next quarter's scores are on their way while one is worked on.
+          // The second quarter's scores are on their way while the first is worked on.
           uint32_t xa[32], xb[32];
           tmem_ld_32cols_async(s_tmem, xa);
           tmem_wait_ld_32(xa);
-#pragma unroll 1
-          for (int h = 0; h < 4; h += 2) {
-            tmem_ld_32cols_async(s_tmem + 32 * (h + 1), xb);
-            quarter(h, xa);
-            tmem_wait_ld_32(xb);
-            if (h < 2) tmem_ld_32cols_async(s_tmem + 32 * (h + 2), xa);
-            quarter(h + 1, xb);
-            tmem_wait_ld_32(xa);
-          }
+          tmem_ld_32cols_async(s_tmem + 32, xb);
+          quarter(0, xa, xb);
+          tmem_wait_ld_32(xb);
+          quarter(1, xb, xa);
         };
         if (edge) softmax(std::true_type{});
         else softmax(std::false_type{});
         tmem_wait_st();
         tc_fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_ready(g));
+        if (lane == 0) mbar_arrive(p_ready(g, buffer));
       }
-      it += n_all;
       if (!ok) break;
+      products += n;
+      tiles += u.tiles;
       if (n > 0) {
-        if (!mbar_wait_warp_inline(o_full(g), o_phase, wd, kSiteEpilogueFull)) break;
-        o_phase ^= 1u;
+        const uint32_t final = products - 1;
+        if (!mbar_wait_warp_inline(pv_done(g, final & 1u), (final >> 1) & 1u, wd,
+                                   kSiteEpilogueFull))
+          break;
         tc_fence_after_sync();
       }
+      // O / l, through Q's place in shared memory (no product reads that any more)
       const float inv_l = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
+#pragma unroll 1
       for (int h = 0; h < HSP / 32; ++h) {
         uint32_t x[32];
         if (n > 0) {
@@ -523,10 +555,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) x[i] = 0u;
         }
-        if (!live) continue;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if (32 * h + 8 * i >= D) break;
           uint32_t y[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -540,11 +570,28 @@ __global__ void __launch_bounds__(kThreads, 1)
               y[e] = *reinterpret_cast<const uint32_t*>(&b);
             }
           }
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + out_at + 32 * h + 8 * i) =
-              make_uint4(y[0], y[1], y[2], y[3]);
+          const int unit = 4 * h + i;
+          st_shared16(q_smem + (unit >> 3) * (kTile * 128) + r * 128 +
+                          (((unit & 7) ^ (r & 7)) << 4),
+                      y);
         }
       }
       tc_fence_before_sync();  // O may be overwritten after the next unit's p_ready
+      __syncwarp();
+#pragma unroll 4
+      for (int i = 0; i < kLanes; ++i) {
+        const int from = i * kRowsAtOnce + lane / kLanes;
+        const int row = __shfl_sync(0xFFFFFFFFu, live ? q_row : -1, from);
+        const int head = __shfl_sync(0xFFFFFFFFu, q_hd, from);
+        const uint32_t sr = static_cast<uint32_t>((warp & 3) * 32 + from);
+        const uint4 y = *reinterpret_cast<const uint4*>(
+            gbase + (q_smem - base) + (piece >> 3) * (kTile * 128) + sr * 128 +
+            (((piece & 7) ^ (sr & 7)) << 4));
+        if (row >= 0 && piece * 8 < D)
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row * a.out_token +
+                                    head * a.out_head + piece * 8) = y;
+      }
+      __syncwarp();
     }
   } else if (warp < kMmaWarp) {
     // --------------------------------------------------------- conversion --
@@ -625,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (uint32_t k = 0; ok; ++k) {
       Unit u;
       if (!take_unit(k, u) || u.n[0] < 0) break;
-      const int n = max(u.n[0], u.n[1]);
+      const int n = u.tiles;
       if (n == 0) continue;
       int next = pages_of(u, 0);
       load_k(u, 0, next);
@@ -640,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (w == 0 && lane < 8)
           factors[(it % kFactorSlots) * 8 + lane] =
-              Factor{f_k, __log2f(f_v), f_v > 0.0f ? __fdividef(1.0f, f_v) : 0.0f, 0.0f};
+              Factor{a.scale_log2 * f_k, __log2f(f_v), f_v > 0.0f ? __fdividef(1.0f, f_v) : 0.0f, 0.0f};
         const uint32_t ks = base + L::kK + stage * L::kKBytes;
 #pragma unroll
         for (int o = 0; o < 4; ++o) {
@@ -650,7 +697,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t* c = reinterpret_cast<const uint32_t*>(&kx[o * (HSP / 64) + h]);
             uint32_t y[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) codes4_to_half2x2<kFormat>(c[i], y[2 * i], y[2 * i + 1]);
+            for (int i = 0; i < 4; ++i) {
+              if constexpr (kBf16) codes4_to_bf162x2<kFormat>(c[i], y[2 * i], y[2 * i + 1]);
+              else codes4_to_half2x2<kFormat>(c[i], y[2 * i], y[2 * i + 1]);
+            }
             const uint32_t at = ks + h * (kTile * 128) + row * 128;
             const uint32_t unit = 2 * (lane >> 3);
             st_shared16(at + ((unit ^ (row & 7)) << 4), y);
@@ -727,76 +777,95 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else {
-    // --------------------------------------------------------- MMA issuer --
-    {
-      constexpr uint32_t kIdescS = idesc_f16_f32(kTile, kTile), kIdescO = idesc_f16_f32(kTile, HSP);
-      uint32_t it = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
-      bool ok = true;
-      for (uint32_t k = 0; ok; ++k) {
-        Unit u;
-        if (!take_unit(k, u) || u.n[0] < 0) break;
-        const int n = max(u.n[0], u.n[1]);
-        if (n == 0) continue;
-        if (lane == 0) for (int j = 0; ok && j <= n; ++j) {
-          const uint32_t stage = (it + j) % kStages, phase = ((it + j) / kStages) & 1u;
-          const uint32_t prev = (it + j - 1) % kStages, prev_phase = ((it + j - 1) / kStages) & 1u;
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            if (!ok) break;
-            const uint32_t s_tmem = tmem + g * kTile, o_tmem = tmem + 2 * kTile + g * HSP;
-            if (j >= 1 && j <= u.n[g]) {
-              if (!mbar_wait(v_full(prev), prev_phase, wd, kSiteMmaFull) ||
-                  !mbar_wait(p_ready(g), p_phase[g], wd, kSiteMmaTmemEmpty)) {
-                ok = false;
-                break;
-              }
-              p_phase[g] ^= 1u;
-              tc_fence_after_sync();
-              const uint32_t vs = base + L::kV + prev * L::kVBytes;
-#pragma unroll
-              for (int s = 0; s < kTile / 16; ++s)
-                umma_f16_ts(o_tmem, s_tmem + 8 * s,
-                            umma_desc_k_sw128(vs + (s >> 2) * (HSP * 128) + (s & 3) * 32), kIdescO,
-                            j > 1 || s > 0);
-              if (j == u.n[g]) umma_commit(o_full(g));
-            }
-            if (j < u.n[g]) {
-              if (j == 0) {
-                if (!mbar_wait(q_ready(g), q_phase[g], wd, kSiteMmaFull)) {
-                  ok = false;
-                  break;
-                }
-                q_phase[g] ^= 1u;
-              }
-              if (!mbar_wait(k_full(stage), phase, wd, kSiteMmaFull)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after_sync();
-              const uint32_t qs = base + L::kQ + g * L::kQBytes;
-              const uint32_t ks = base + L::kK + stage * L::kKBytes;
-#pragma unroll
-              for (int s = 0; s < HSP / 16; ++s)
-                umma_bf16(s_tmem,
-                          umma_desc_k_sw128(qs + (s >> 2) * (kTile * 128) + (s & 3) * 32),
-                          umma_desc_k_sw128(ks + (s >> 2) * (kTile * 128) + (s & 3) * 32), kIdescS,
-                          s > 0);
-              umma_commit(s_full(g));
-            }
+    // -------------------------------------------------------- MMA issuers --
+    const uint32_t g = warp - kMmaWarp;
+    constexpr uint32_t kIdescS = kBf16 ? idesc_bf16_f32(kTile, kHalf) : idesc_f16_f32(kTile, kHalf);
+    constexpr uint32_t kIdescO = idesc_f16_f32(kTile, HSP);
+    // Descriptors' low words (the start address in units of 16 bytes); moving along a
+    // tile adds to them.
+    const uint64_t desc = umma_desc_k_sw128(base);
+    const uint32_t desc_hi = static_cast<uint32_t>(desc >> 32), lo = static_cast<uint32_t>(desc);
+    const uint32_t s_tmem = tmem + g * kTile, o_tmem = tmem + 2 * kTile + g * HSP;
+    const uint32_t qd = lo + ((L::kQ + g * L::kQBytes) >> 4);
+    uint32_t tiles = 0, products = 0, q_phase = 0;
+    bool ok = true;
+    for (uint32_t k = 0; ok; ++k) {
+      Unit u;
+      if (!take_unit(k, u) || u.n[0] < 0) break;
+      // (shuffled so that the compiler knows them to be the warp's: what is computed
+      // from them then stays in uniform registers, which the MMAs' operands are)
+      const int n = __shfl_sync(0xFFFFFFFFu, g == 0 ? u.n[0] : u.n[1], 0);
+      const int n_tiles = __shfl_sync(0xFFFFFFFFu, u.tiles, 0);
+      // step -1 starts the first scores; tiles past this group's own are only given back
+      for (int step = -1; ok && step < 2 * n_tiles; ++step) {
+        const int ahead = step + 1;
+        if (ahead < n) {
+          const uint32_t t = tiles + (ahead >> 1), stage = t % kStages;
+          if (ahead == 0) {
+            ok = mbar_wait_warp_inline(q_ready(g), q_phase, wd, kSiteMmaFull);
+            q_phase ^= 1u;
           }
+          if ((ahead & 1) == 0)
+            ok = ok && mbar_wait_warp_inline(k_full(stage), (t / kStages) & 1u, wd, kSiteMmaFull);
           if (!ok) break;
-          if (j < n) umma_commit(k_empty(stage));
-          if (j >= 1) umma_commit(v_empty(prev));
+          tc_fence_after_sync();
+          const uint32_t buffer = (products + ahead) & 1u;
+          const uint32_t kd =
+              lo + ((L::kK + stage * L::kKBytes + (ahead & 1) * (kHalf * 128)) >> 4);
+          if (elect_one()) {
+#pragma unroll
+            for (int s = 0; s < HSP / 16; ++s) {
+              const uint32_t at = ((s >> 2) * (kTile * 128) + (s & 3) * 32) >> 4;
+              umma_f16_ss(s_tmem + buffer * kHalf, qd + at, kd + at, desc_hi, kIdescS, s > 0);
+            }
+            umma_commit(s_full(g, buffer));
+          }
+          __syncwarp();
         }
-        it += n;
-        ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;  // lane 0's: the warp leaves together
+        if ((ahead & 1) == 1 && ahead < 2 * n_tiles) {
+          const uint32_t t = tiles + (ahead >> 1);
+          // (a stage is filled before it is given back, by either group)
+          ok = mbar_wait_warp_inline(k_full(t % kStages), (t / kStages) & 1u, wd, kSiteMmaFull);
+          if (!ok) break;
+          if (elect_one()) umma_commit(k_empty(t % kStages));
+          __syncwarp();
+        }
+        if (step < 0) continue;
+        const uint32_t t = tiles + (step >> 1), stage = t % kStages;
+        if ((step & 1) == 0 &&
+            !mbar_wait_warp_inline(v_full(stage), (t / kStages) & 1u, wd, kSiteMmaFull)) {
+          ok = false;
+          break;
+        }
+        if (step < n) {
+          const uint32_t p = products + step;
+          const uint32_t vd =
+              lo + ((L::kV + stage * L::kVBytes + (step & 1) * (HSP * 128)) >> 4);
+          ok = mbar_wait_warp_inline(p_ready(g, p & 1u), (p >> 1) & 1u, wd, kSiteMmaTmemEmpty);
+          if (!ok) break;
+          tc_fence_after_sync();
+          if (elect_one()) {
+#pragma unroll
+            for (int s = 0; s < kHalf / 16; ++s)
+              umma_f16_ts(o_tmem, s_tmem + (p & 1u) * kHalf + 8 * s, vd + 2 * s, desc_hi, kIdescO,
+                          step > 0 || s > 0);
+            umma_commit(pv_done(g, p & 1u));
+          }
+          __syncwarp();
+        }
+        if ((step & 1) == 1) {
+          if (elect_one()) umma_commit(v_empty(stage));
+          __syncwarp();
+        }
       }
-      // Every MMA must be complete before TMEM and shared memory go away.
-      if (lane == 0) {
-        umma_commit(drain);
-        const uint64_t t0 = globaltimer_ns();
-        while (!mbar_test(drain, 0) && globaltimer_ns() - t0 < a.wait_limit_ns) {
-        }
+      tiles += n_tiles;
+      products += n;
+    }
+    // Every MMA must be complete before TMEM and shared memory go away.
+    if (elect_one()) {
+      umma_commit(drain);
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_test(drain, 0) && globaltimer_ns() - t0 < a.wait_limit_ns) {
       }
     }
     __syncwarp();
@@ -807,14 +876,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
-template <int HSP, int kFormat>
+template <int HSP, int kFormat, bool kBf16>
 cudaError_t launch_prompt(const PromptArgs& a, const DeviceInfo& dev, cudaStream_t stream, int& rc,
                           std::string& err) {
-  const auto kernel = attend_prompt_sm103a_kernel<HSP, kFormat>;
+  const auto kernel = attend_prompt_sm103a_kernel<HSP, kFormat, kBf16>;
   const int smem = Layout<HSP>::kTotal + 1024;
   rc = set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), smem, dev.device, err);
   if (rc != CSA_OK) return cudaSuccess;
   return launch_programmatic(kernel, static_cast<unsigned>(dev.sm_count), kThreads, smem, stream, a);
+}
+
+template <int HSP>
+cudaError_t launch_prompt(const PromptArgs& a, int format, const DeviceInfo& dev,
+                          cudaStream_t stream, int& rc, std::string& err) {
+  if (format == CSA_KV_INT8)
+    return a.half ? launch_prompt<HSP, CSA_KV_INT8, false>(a, dev, stream, rc, err)
+                  : launch_prompt<HSP, CSA_KV_INT8, true>(a, dev, stream, rc, err);
+  return a.half ? launch_prompt<HSP, CSA_KV_E4M3, false>(a, dev, stream, rc, err)
+                : launch_prompt<HSP, CSA_KV_E4M3, true>(a, dev, stream, rc, err);
 }
 
 }  // namespace
@@ -835,20 +914,15 @@ int cache_prompt_launch(const csa_kv_cache& cache, const csa_kv_batch& batch,
   a.window = call.window;
   a.sinks = call.window > 0 ? call.sinks : 0;
   a.row_limit = row_limit;
-  a.scale_log2 = static_cast<float>(std::fabs(static_cast<double>(call.scale)) * 1.4426950408889634);
-  a.q_flip = call.scale < 0 ? 0x80008000u : 0u;
+  a.scale_log2 = static_cast<float>(static_cast<double>(call.scale) * 1.4426950408889634);
   a.status = dev.status_word;
   a.wait_limit_ns = wait_limit_ns();
   a.inject = take_inject() ? 1 : 0;
   a.counter = counter;
   int rc = CSA_OK;
   cudaError_t e;
-  if (cache.head_size <= 64)
-    e = cache.format == CSA_KV_INT8 ? launch_prompt<64, CSA_KV_INT8>(a, dev, stream, rc, err)
-                                    : launch_prompt<64, CSA_KV_E4M3>(a, dev, stream, rc, err);
-  else
-    e = cache.format == CSA_KV_INT8 ? launch_prompt<128, CSA_KV_INT8>(a, dev, stream, rc, err)
-                                    : launch_prompt<128, CSA_KV_E4M3>(a, dev, stream, rc, err);
+  e = cache.head_size <= 64 ? launch_prompt<64>(a, cache.format, dev, stream, rc, err)
+                            : launch_prompt<128>(a, cache.format, dev, stream, rc, err);
   if (rc != CSA_OK) return rc;
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) {

@@ -126,6 +126,31 @@ __device__ __forceinline__ void codes4_to_half2x2(uint32_t w, uint32_t& p01, uin
   }
 }
 
+// Four codes of one word as two bf16 pairs, exactly. int8: 0x43xx with the code's
+// byte as xx is, without bit 7, 128 + (its low 7 bits), and with bit 7 alone, which
+// is the exponent's last, 128 or 256: their difference is the code.
+__device__ __forceinline__ uint32_t bf162_sub(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <int kFormat>
+__device__ __forceinline__ void codes4_to_bf162x2(uint32_t w, uint32_t& p01, uint32_t& p23) {
+  if (kFormat == CSA_KV_INT8) {
+    const uint32_t t = byte_perm(w, 0x43434343u, 0x4140), u = byte_perm(w, 0x43434343u, 0x4342);
+    p01 = bf162_sub(t & 0xFF7FFF7Fu, t & 0xFF80FF80u);
+    p23 = bf162_sub(u & 0xFF7FFF7Fu, u & 0xFF80FF80u);
+  } else {
+    uint32_t h[2] = {e4m3x2_to_half2(w & 0xFFFFu), e4m3x2_to_half2(w >> 16)};
+    uint32_t* to[2] = {&p01, &p23};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<__half2*>(&h[i]));
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(*to[i]) : "f"(f.y), "f"(f.x));
+    }
+  }
+}
+
 // The same four codes as fp32 values.
 template <int kFormat>
 __device__ __forceinline__ void codes4_to_float(uint32_t w, float (&f)[4]) {
