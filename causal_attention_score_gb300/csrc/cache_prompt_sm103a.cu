@@ -22,8 +22,9 @@
 //    last. A thread's MMAs run in issue order, so S may overwrite the weights that
 //    the product issued before it reads. (With both groups on one warp the issue
 //    itself, some 90 cycles an MMA, was the longest path.)
-//  - warp 14: takes units from the counter (workspace, cleared by the rows kernel
-//    ahead in the stream) and passes them on a unit ahead.
+//  - warp 14: takes a unit from the counter (workspace, cleared by the rows kernel
+//    ahead in the stream) when the conversion, which is two tiles ahead, asks for it:
+//    a CTA holds no unit that another could have begun.
 //
 // Scales (see cache_attention_sm103a.cu): with c ks and log2(vs) per 16 tokens in
 // shared memory, x = s (c ks) + log2(vs) and the weight has V's scale in it; the
@@ -287,6 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto u_full = [&](uint32_t s) { return bars + 8u * (20 + s); };
   auto u_empty = [&](uint32_t s) { return bars + 8u * (22 + s); };
   const uint32_t drain = bars + 8u * 24;
+  const uint32_t u_want = bars + 8u * 29;
   const uint32_t tmem_slot = base + L::kMisc;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::kMisc + 4);
   Factor* factors = reinterpret_cast<Factor*>(gbase + L::kFactors);
@@ -309,6 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     mbar_init(drain, 2);
+    mbar_init(u_want, kConvertWarps);
     for (int s = 0; s < kUnitSlots; ++s) {
       mbar_init(u_full(s), 1);
       mbar_init(u_empty(s), kListWarp);  // every warp but the list's
@@ -671,6 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     for (uint32_t k = 0; ok; ++k) {
       Unit u;
+      if (lane == 0) mbar_arrive(u_want);
       if (!take_unit(k, u) || u.n[0] < 0) break;
       const int n = u.tiles;
       if (n == 0) continue;
@@ -765,6 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       for (uint32_t k = 0;; ++k) {
         const uint32_t slot = k % kUnitSlots;
+        if (!mbar_wait(u_want, k & 1u, wd, kSiteSched)) break;
         const long long at = atomicAdd(a.counter, 1u);
         Unit u;
         if (at < total) u = decode_unit(a, s_prefix, per, at);
