@@ -40,7 +40,6 @@
 #include <cmath>
 #include <cstdint>
 #include <string>
-#include <type_traits>
 
 #include "csa_internal.h"
 #include "kv_cache.cuh"
@@ -429,109 +428,104 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int last = pos - tb;
         const int first_window = a.window ? last - a.window + 1 : -kHalf;
         const int sink_cols = a.window ? a.sinks - tb : 0;
-        auto softmax = [&](auto edge_tile) {
-          constexpr bool kEdge = decltype(edge_tile)::value;
-          // x = score * c.k + c.log2v - less of 32 keys, masked: -inf; returns the maximum
-          auto scores = [&](int h, uint32_t (&x)[32], float less) {
-            float top = -INFINITY;
+        // Weights of keys 32 h .. from their scores in x, to P. `coming`: registers that a
+        // TMEM load may still be writing.
+        auto quarter = [&](int h, uint32_t (&x)[32], uint32_t (&coming)[32]) {
+          const bool fresh = m == kNothing;  // nothing seen yet: the first value sets m
+          const float less = fresh ? 0.0f : m;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const Factor c = fac[2 * h + i];
-              const float add = c.log2v - less;
-              const uint64_t fk2 = pack_f32x2(c.k, c.k), add2 = pack_f32x2(add, add);
+          for (int i = 0; i < 2; ++i) {
+            const Factor c = fac[2 * h + i];
+            const float add = c.log2v - less;
+            const uint64_t fk2 = pack_f32x2(c.k, c.k), add2 = pack_f32x2(add, add);
 #pragma unroll
-              for (int e = 0; e < 16; e += 2) {
-                const int at = 16 * i + e;
-                float y0, y1;
-                fma_f32x2(y0, y1, __uint_as_float(x[at]), __uint_as_float(x[at + 1]), fk2, add2);
-                if (kEdge) {
-                  const int c0 = 32 * h + at;
-                  if (c0 > last || (c0 < first_window && c0 >= sink_cols)) y0 = -INFINITY;
-                  if (c0 + 1 > last || (c0 + 1 < first_window && c0 + 1 >= sink_cols))
-                    y1 = -INFINITY;
-                }
-                x[at] = __float_as_uint(y0);
-                x[at + 1] = __float_as_uint(y1);
-                top = fmaxf(top, fmaxf(y0, y1));
+            for (int e = 0; e < 16; e += 2) {
+              float y0, y1;
+              fma_f32x2(y0, y1, __uint_as_float(x[16 * i + e]), __uint_as_float(x[16 * i + e + 1]),
+                        fk2, add2);
+              x[16 * i + e] = __float_as_uint(y0);
+              x[16 * i + e + 1] = __float_as_uint(y1);
+            }
+          }
+          if (edge) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int c = 32 * h + i;
+              if (c > last || (c < first_window && c >= sink_cols))
+                x[i] = __float_as_uint(-INFINITY);
+            }
+          }
+          float top = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 32; i += 2)
+            top = fmaxf(top, fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])));
+          if (__any_sync(0xFFFFFFFFu, top > (fresh ? -INFINITY : kRaise))) {
+            // (rare) a new maximum: what was computed with the old one is rescaled, which
+            // is O, l and this half's weights so far
+            tmem_wait_ld_32(coming);
+            const float up = fresh ? fmaxf(top, kNothing) : fmaxf(top, 0.0f);
+            const float corr = fresh ? 1.0f : ex2_approx(-up);
+            m = less + up;
+            l *= corr;
+            const float off = fresh && top == -INFINITY ? 0.0f : up;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) - off);
+            uint32_t y[16];
+            if (step > 0) {
+              // O is the product issued last's until that is complete (the one before it
+              // is: this half tile's scores were issued later)
+              const uint32_t before = products + step - 1;
+              if (!mbar_wait_warp_inline(pv_done(g, before & 1u), (before >> 1) & 1u, wd,
+                                         kSiteEpilogueFull))
+                ok = false;
+              tc_fence_after_sync();
+#pragma unroll 1
+              for (int c = 0; c < HSP; c += 16) {
+                tmem_ld_16cols(o_tmem + c, y);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  y[i] = __float_as_uint(__uint_as_float(y[i]) * corr);
+                tmem_st_16cols(o_tmem + c, y);
               }
             }
-            return top;
-          };
-          // Weights of keys 32 h .. from their scores in x, to P. `coming`: registers
-          // that a TMEM load may still be writing.
-          auto quarter = [&](int h, uint32_t (&x)[32], uint32_t (&coming)[32]) {
-            const float top = scores(h, x, m);
-            if (__any_sync(0xFFFFFFFFu, top > kRaise)) {
-              // (rare) the true values from S again, the new maximum, and what was
-              // computed with the old one: O, l, this half's weights so far
-              tmem_wait_ld_32(coming);
-              tmem_ld_32cols(s_tmem + 32 * h, x);
-              const float to = fmaxf(m, scores(h, x, 0.0f));
-              const float corr = ex2_approx(m - to);
-              m = to;
-              l *= corr;
-#pragma unroll
-              for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) - m);
-              uint32_t y[16];
-              if (step > 0) {
-                // O is the product issued last's until that is complete (the one before
-                // it is: this half tile's scores were issued later)
-                const uint32_t before = products + step - 1;
-                if (!mbar_wait_warp_inline(pv_done(g, before & 1u), (before >> 1) & 1u, wd,
-                                           kSiteEpilogueFull))
-                  ok = false;
-                tc_fence_after_sync();
-#pragma unroll 1
-                for (int c = 0; c < HSP; c += 16) {
-                  tmem_ld_16cols(o_tmem + c, y);
-#pragma unroll
-                  for (int i = 0; i < 16; ++i)
-                    y[i] = __float_as_uint(__uint_as_float(y[i]) * corr);
-                  tmem_st_16cols(o_tmem + c, y);
-                }
-              }
+            if (h > 0) {
               tmem_wait_st();
-#pragma unroll 1
-              for (int c = 0; c < 16 * h; c += 16) {
-                tmem_ld_16cols(s_tmem + c, y);
+              tmem_ld_16cols(s_tmem, y);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  const float2 w = __half22float2(*reinterpret_cast<__half2*>(&y[i]));
-                  y[i] = half2_of(w.x * corr, w.y * corr);
-                }
-                tmem_st_16cols(s_tmem + c, y);
+              for (int i = 0; i < 16; ++i) {
+                const float2 w = __half22float2(*reinterpret_cast<__half2*>(&y[i]));
+                y[i] = half2_of(w.x * corr, w.y * corr);
               }
+              tmem_st_16cols(s_tmem, y);
             }
-            uint32_t p[16];
+          }
+          uint32_t p[16];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              uint64_t sum = 0;
+          for (int i = 0; i < 2; ++i) {
+            uint64_t sum = 0;
 #pragma unroll
-              for (int e = 0; e < 16; e += 2) {
-                const int at = 16 * i + e;
-                const float y0 = ex2_approx(__uint_as_float(x[at]));
-                const float y1 = ex2_approx(__uint_as_float(x[at + 1]));
-                sum = add_f32x2(sum, pack_f32x2(y0, y1));
-                p[at / 2] = half2_of(y0, y1);
-              }
-              float s0, s1;
-              unpack_f32x2(sum, s0, s1);
-              l = fmaf(s0 + s1, fac[2 * h + i].inv, l);
+            for (int e = 0; e < 16; e += 2) {
+              const int at = 16 * i + e;
+              const float y0 = ex2_approx(__uint_as_float(x[at]));
+              const float y1 = ex2_approx(__uint_as_float(x[at + 1]));
+              sum = add_f32x2(sum, pack_f32x2(y0, y1));
+              p[at / 2] = half2_of(y0, y1);
             }
-            // P over S: columns 16 h .., whose scores have been read
-            tmem_st_16cols(s_tmem + 16 * h, p);
-          };
-          // The second quarter's scores are on their way while the first is worked on.
-          uint32_t xa[32], xb[32];
-          tmem_ld_32cols_async(s_tmem, xa);
-          tmem_wait_ld_32(xa);
-          tmem_ld_32cols_async(s_tmem + 32, xb);
-          quarter(0, xa, xb);
-          tmem_wait_ld_32(xb);
-          quarter(1, xb, xa);
+            float s0, s1;
+            unpack_f32x2(sum, s0, s1);
+            l = fmaf(s0 + s1, fac[2 * h + i].inv, l);
+          }
+          // P over S: columns 16 h .., whose scores have been read
+          tmem_st_16cols(s_tmem + 16 * h, p);
         };
-        if (edge) softmax(std::true_type{});
-        else softmax(std::false_type{});
+        // The second quarter's scores are on their way while the first is worked on.
+        uint32_t xa[32], xb[32];
+        tmem_ld_32cols_async(s_tmem, xa);
+        tmem_wait_ld_32(xa);
+        tmem_ld_32cols_async(s_tmem + 32, xb);
+        quarter(0, xa, xb);
+        tmem_wait_ld_32(xb);
+        quarter(1, xb, xa);
         tmem_wait_st();
         tc_fence_before_sync();
         __syncwarp();
