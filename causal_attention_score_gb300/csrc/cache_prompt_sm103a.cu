@@ -4,34 +4,38 @@
 //
 // A unit of work is 256 rows (tokens x query heads of one kv head) of a
 // sequence: two groups A and B of 128, each a TMEM accumulator's lanes, which
-// share every tile of 128 keys. One CTA per SM takes units from a counter
+// share every tile of 64 keys. One CTA per SM takes units from a counter
 // (longest first within a sequence), with 15 warps:
-//  - warps 0..7: softmax, warps 0..3 group A, 4..7 group B, a thread a row. Per
-//    half tile of 64 keys: scores from TMEM, x - m, their maximum, and the
-//    weights exp2(x - m) as fp16 over S (P, the second product's A operand in
+//  - warps 0..7: softmax, warps 0..3 group A, 4..7 group B, a thread a row. Per 32
+//    keys: scores from TMEM (the next 32 on their way), x - m, their maximum, and
+//    the weights exp2(x - m) as fp16 over S (P, the second product's A operand in
 //    TMEM). m is raised only when a value passes m + 8; then the thread's O row,
-//    its l and the half tile's weights so far are rescaled. Before a unit they
-//    copy Q's rows to shared memory; after it they write O / l.
+//    its l and the tile's weights so far are rescaled. The loop is not unrolled:
+//    with separate code for each part of a tile and for edges a quarter of the
+//    cycles went to waiting for instructions. Before a unit they copy Q's rows to
+//    shared memory; after it they write O / l.
 //  - warps 8..11: conversion. Codes come from HBM into registers a tile ahead
 //    (their page numbers two) and go to shared memory in the 128-byte-swizzle
 //    K-major layout, K as [token][element] in Q's type, V transposed in registers
-//    to [element][token] in fp16 (both exact). Two stages each.
-//  - warps 12 and 13: one thread each issues a group's products: per half tile
-//    S = Q K^T of the next one, then O += P V of this one. S has two buffers of 64
+//    to [element][token] in fp16 (both exact). A slot of the ring of four holds V
+//    of tile j and K of tile j + 1, what one step of the products reads.
+//  - warps 12 and 13: one thread each issues a group's products, per step
+//    S = Q K^T of tile j + 1, then O += P V of tile j. S has two buffers of 64
 //    columns, so the softmax finds the next scores ready when it is done with the
 //    last. A thread's MMAs run in issue order, so S may overwrite the weights that
 //    the product issued before it reads. (With both groups on one warp the issue
 //    itself, some 90 cycles an MMA, was the longest path.)
 //  - warp 14: takes a unit from the counter (workspace, cleared by the rows kernel
-//    ahead in the stream) when the conversion, which is two tiles ahead, asks for it:
-//    a CTA holds no unit that another could have begun.
+//    ahead in the stream) when the conversion asks for it, some tiles before it is
+//    through with the last one: early enough to hide the way to the first scores, late
+//    enough that a CTA holds no unit that another could have begun.
 //
 // Scales (see cache_attention_sm103a.cu): with c ks and log2(vs) per 16 tokens in
 // shared memory, x = s (c ks) + log2(vs) and the weight has V's scale in it; the
 // denominator sums w / vs.
 //
-// Bound: 4 HSP flops and one exp2 per row and key; per 256 x 128 tile 2048 cycles
-// of MMA at the dense rate and 2048 cycles of the 16-a-cycle exponential unit.
+// Bound: 4 HSP flops and one exp2 per row and key; per 256 rows x 64 keys 1024 cycles
+// of MMA at the dense rate (HSP = 128).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -53,12 +57,13 @@ constexpr int kConvertWarps = 4;
 constexpr int kMmaWarp = kSoftmaxWarps + kConvertWarps;
 constexpr int kListWarp = kMmaWarp + 2;
 constexpr int kThreads = 32 * (kListWarp + 1);
-constexpr int kTile = 128;          // keys per tile, rows per group
-constexpr int kUnitRows = 2 * kTile;
-constexpr int kStages = 2;
-constexpr int kFactorSlots = 4;
+constexpr int kRows = 128;          // per group
+constexpr int kUnitRows = 2 * kRows;
+constexpr int kTile = 64;           // keys per step
+constexpr int kSlots = 4;           // of the ring of converted keys and values
+constexpr int kFactorSlots = 8;     // tiles whose factors are kept
 constexpr int kUnitSlots = 2;
-constexpr int kHalf = 64;           // keys per step of the products and the softmax
+constexpr int kAskAhead = 12;       // tiles before a unit's end when the next is asked for
 constexpr int kTmemCols = 512;      // S_A (two buffers), S_B, O_A, O_B
 constexpr float kRaise = 8.0f;
 constexpr float kNothing = -1e30f;  // the running maximum of a row that has seen nothing
@@ -89,18 +94,17 @@ struct Unit {
   KvSequence q;
   int s, head, row0, rows;  // rows [row0, row0 + rows) of the sequence
   int sink_tiles, window_tile;
-  int tiles;                // of 128 keys
-  int n[2];                 // half tiles of each group; n[0] < 0: the list has ended
+  int n[2];                 // tiles of each group; n[0] < 0: the list has ended
 };
 
 template <int HSP>
 struct Layout {
-  static constexpr int kQBytes = kTile * HSP * 2;  // per group: [HSP / 64][128 rows][128 B]
-  static constexpr int kKBytes = kTile * HSP * 2;  // per stage: the same
-  static constexpr int kVBytes = HSP * kTile * 2;  // per stage: [2][HSP rows][128 B]
-  static constexpr int kQ = 0, kK = 2 * kQBytes, kV = kK + kStages * kKBytes,
-                       kFactors = kV + kStages * kVBytes,
-                       kBars = kFactors + kFactorSlots * 8 * static_cast<int>(sizeof(Factor)),
+  static constexpr int kQBytes = kRows * HSP * 2;  // per group: [HSP / 64][128 rows][128 B]
+  static constexpr int kKBytes = kTile * HSP * 2;  // per slot: [HSP / 64][64 rows][128 B]
+  static constexpr int kVBytes = HSP * kTile * 2;  // per slot: [HSP rows][128 B]
+  static constexpr int kQ = 0, kK = 2 * kQBytes, kV = kK + kSlots * kKBytes,
+                       kFactors = kV + kSlots * kVBytes,
+                       kBars = kFactors + kFactorSlots * 4 * static_cast<int>(sizeof(Factor)),
                        kMisc = kBars + 8 * 30, kUnits = kMisc + 16,
                        kTotal = kUnits + kUnitSlots * static_cast<int>(sizeof(Unit));
 };
@@ -144,14 +148,12 @@ __device__ Unit decode_unit(const PromptArgs& a, const long long* prefix, int pe
   }
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
-    const int rows = min(r.rows - g * kTile, kTile);
+    const int rows = min(r.rows - g * kRows, kRows);
     r.n[g] = 0;
     if (rows <= 0) continue;
-    const int last = r.q.first + (r.row0 + g * kTile + rows - 1) / a.group;  // position
-    if (last >= 0)
-      r.n[g] = 2 * r.sink_tiles + max(last / kHalf + 1 - 2 * r.window_tile, 0);
+    const int last = r.q.first + (r.row0 + g * kRows + rows - 1) / a.group;  // position
+    if (last >= 0) r.n[g] = r.sink_tiles + max(last / kTile + 1 - r.window_tile, 0);
   }
-  r.tiles = (max(r.n[0], r.n[1]) + 1) / 2;
   return r;
 }
 
@@ -203,7 +205,24 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       : "memory");
 }
 
-// 32 lanes x 16 consecutive 32-bit columns from 16 registers, without the wait.
+// 32 lanes x consecutive 32-bit columns and a thread's registers: stores without
+// their wait, loads with and (async) without; an async load's registers are valid
+// after tmem_wait_ld_32 on the same array.
+__device__ __forceinline__ void tmem_st_8cols(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_8cols(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st_16cols(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -213,18 +232,6 @@ __device__ __forceinline__ void tmem_st_16cols(uint32_t taddr, const uint32_t (&
       "r"(r[15])
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld_16cols(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-}
-// 32 columns without the wait: valid after tmem_wait_ld_32 on the same array.
 __device__ __forceinline__ void tmem_ld_32cols_async(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
@@ -253,6 +260,35 @@ __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// Read-only loads of 16, 8 or 4 bytes where `in`, else zeros: predicated, as a branch
+// around each load costs more than the load.
+__device__ __forceinline__ uint4 load16_if(const uint8_t* from, bool in) {
+  uint4 x;
+  asm("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+      "@p ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(x.x), "=&r"(x.y), "=&r"(x.z), "=&r"(x.w)
+      : "l"(from), "r"(in ? 1 : 0));
+  return x;
+}
+__device__ __forceinline__ uint2 load8_if(const uint8_t* from, bool in) {
+  uint2 x;
+  asm("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
+      "@p ld.global.nc.v2.b32 {%0, %1}, [%2];\n\t}"
+      : "=&r"(x.x), "=&r"(x.y)
+      : "l"(from), "r"(in ? 1 : 0));
+  return x;
+}
+__device__ __forceinline__ uint32_t load4_if(const void* from, bool in, uint32_t other) {
+  uint32_t x;
+  asm("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b32 %0, %3;\n\t"
+      "@p ld.global.nc.b32 %0, [%1];\n\t}"
+      : "=&r"(x)
+      : "l"(from), "r"(in ? 1 : 0), "r"(other));
+  return x;
+}
+
 // 16-byte global -> shared copy past L1; zeros where bytes is 0.
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
@@ -274,20 +310,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - raw);
   const uint32_t bars = base + L::kBars;
-  auto k_full = [&](uint32_t s) { return bars + 8u * s; };
-  auto k_empty = [&](uint32_t s) { return bars + 8u * (2 + s); };
-  auto v_full = [&](uint32_t s) { return bars + 8u * (4 + s); };
-  auto v_empty = [&](uint32_t s) { return bars + 8u * (6 + s); };
+  auto full = [&](uint32_t s) { return bars + 8u * s; };
+  auto empty = [&](uint32_t s) { return bars + 8u * (4 + s); };
   auto q_ready = [&](uint32_t g) { return bars + 8u * (8 + g); };
+  auto s_full = [&](uint32_t g, uint32_t b) { return bars + 8u * (10 + 2 * g + b); };
+  auto p_ready = [&](uint32_t g, uint32_t b) { return bars + 8u * (14 + 2 * g + b); };
   // (of a group's even and odd products: a parity tells only neighbouring phases apart,
   // and a waiter may be up to two products behind)
-  auto pv_done = [&](uint32_t g, uint32_t b) { return bars + 8u * (25 + 2 * g + b); };
-  auto s_full = [&](uint32_t g, uint32_t b) { return bars + 8u * (12 + 2 * g + b); };
-  auto p_ready = [&](uint32_t g, uint32_t b) { return bars + 8u * (16 + 2 * g + b); };
-  auto u_full = [&](uint32_t s) { return bars + 8u * (20 + s); };
-  auto u_empty = [&](uint32_t s) { return bars + 8u * (22 + s); };
-  const uint32_t drain = bars + 8u * 24;
-  const uint32_t u_want = bars + 8u * 29;
+  auto pv_done = [&](uint32_t g, uint32_t b) { return bars + 8u * (18 + 2 * g + b); };
+  auto u_full = [&](uint32_t s) { return bars + 8u * (22 + s); };
+  auto u_empty = [&](uint32_t s) { return bars + 8u * (24 + s); };
+  const uint32_t u_want = bars + 8u * 26;
+  const uint32_t drain = bars + 8u * 27;
   const uint32_t tmem_slot = base + L::kMisc;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::kMisc + 4);
   Factor* factors = reinterpret_cast<Factor*>(gbase + L::kFactors);
@@ -295,11 +329,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(k_full(s), kConvertWarps);
-      mbar_init(v_full(s), kConvertWarps);
-      mbar_init(k_empty(s), 2);  // one commit of each group's issuer
-      mbar_init(v_empty(s), 2);
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(full(s), kConvertWarps);
+      mbar_init(empty(s), 2);  // one commit of each group's issuer
     }
     for (int g = 0; g < 2; ++g) {
       mbar_init(q_ready(g), 4);
@@ -366,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t g = warp >> 2;
     const int r = threadIdx.x & 127;                       // row of the group
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // TMEM lane field
-    const uint32_t o_tmem = tmem + lanes + 2 * kTile + g * HSP;
+    const uint32_t o_tmem = tmem + lanes + 2 * kRows + g * HSP;
     const uint32_t q_smem = base + L::kQ + g * L::kQBytes;
     // Rows go between HBM and shared memory a warp's 32 at a time: kLanes lanes of 16
     // bytes to a row.
@@ -379,10 +411,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       Unit u;
       if (!take_unit(k, u) || u.n[0] < 0) break;
       const int n = g == 0 ? u.n[0] : u.n[1];
-      const int rr = u.row0 + static_cast<int>(g) * kTile + r;
+      const int rr = u.row0 + static_cast<int>(g) * kRows + r;
       const int j_tok = rr / a.group;
       const int q_row = u.q.row0 + j_tok, q_hd = u.head * a.group + (rr - j_tok * a.group);
-      const bool live = static_cast<int>(g) * kTile + r < u.rows;
+      const bool live = static_cast<int>(g) * kRows + r < u.rows;
       const int pos = live ? u.q.first + j_tok : -1;
       float l = 0.0f, m = kNothing;
       if (n > 0) {
@@ -395,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int head = __shfl_sync(0xFFFFFFFFu, q_hd, from);
           const bool in = row >= 0 && piece * 8 < D;
           const uint32_t sr = static_cast<uint32_t>((warp & 3) * 32 + from);
-          cp_async_16(q_smem + (piece >> 3) * (kTile * 128) + sr * 128 +
+          cp_async_16(q_smem + (piece >> 3) * (kRows * 128) + sr * 128 +
                           (((piece & 7) ^ (sr & 7)) << 4),
                       static_cast<const uint16_t*>(a.q) +
                           (in ? row * a.q_token + head * a.q_head + piece * 8 : 0),
@@ -410,27 +442,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int pos_low = __reduce_min_sync(0xFFFFFFFFu, live ? pos : 0x7FFFFFFF);
       const int pos_high = __reduce_max_sync(0xFFFFFFFFu, pos);
       for (int step = 0; ok && step < n; ++step) {
-        const uint32_t buffer = (products + step) & 1u;
-        const uint32_t s_tmem = tmem + lanes + g * kTile + buffer * kHalf;
-        const int tb = tile_token(u, step >> 1) + (step & 1) * kHalf;
-        if (!mbar_wait_warp_inline(s_full(g, buffer), ((products + step) >> 1) & 1u, wd,
+        const uint32_t product = products + step, buffer = product & 1u;
+        const uint32_t s_tmem = tmem + lanes + g * kRows + buffer * kTile;
+        const int tb = tile_token(u, step);
+        if (!mbar_wait_warp_inline(s_full(g, buffer), (product >> 1) & 1u, wd,
                                    kSiteEpilogueFull)) {
           ok = false;
           break;
         }
         tc_fence_after_sync();
-        const Factor* fac =
-            factors + ((tiles + (step >> 1)) % kFactorSlots) * 8 + (step & 1) * 4;
-        const bool edge = !(tb + kHalf - 1 <= pos_low &&
-                            (a.window == 0 || pos_high - tb < a.window || tb + kHalf - 1 < a.sinks));
+        const Factor* fac = factors + ((tiles + step) % kFactorSlots) * 4;
+        const bool edge = !(tb + kTile - 1 <= pos_low &&
+                            (a.window == 0 || pos_high - tb < a.window || tb + kTile - 1 < a.sinks));
         // columns 0 .. last are at or before this row; from first_window on, or below
         // sink_cols, they are in its window or sinks
         const int last = pos - tb;
-        const int first_window = a.window ? last - a.window + 1 : -kHalf;
+        const int first_window = a.window ? last - a.window + 1 : -kTile;
         const int sink_cols = a.window ? a.sinks - tb : 0;
-        // Weights of keys 32 h .. from their scores in x, to P. `coming`: registers that a
-        // TMEM load may still be writing.
-        auto quarter = [&](int h, uint32_t (&x)[32], uint32_t (&coming)[32]) {
+        uint32_t x[32], next[32];
+        tmem_ld_32cols_async(s_tmem, next);
+#pragma unroll 1
+        for (int h = 0; h < kTile / 32; ++h) {
+          tmem_wait_ld_32(next);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = next[i];
+          if (h + 1 < kTile / 32) tmem_ld_32cols_async(s_tmem + 32 * (h + 1), next);
           const bool fresh = m == kNothing;  // nothing seen yet: the first value sets m
           const float less = fresh ? 0.0f : m;
 #pragma unroll
@@ -439,19 +475,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float add = c.log2v - less;
             const uint64_t fk2 = pack_f32x2(c.k, c.k), add2 = pack_f32x2(add, add);
 #pragma unroll
-            for (int e = 0; e < 16; e += 2) {
+            for (int e = 16 * i; e < 16 * i + 16; e += 2) {
               float y0, y1;
-              fma_f32x2(y0, y1, __uint_as_float(x[16 * i + e]), __uint_as_float(x[16 * i + e + 1]),
-                        fk2, add2);
-              x[16 * i + e] = __float_as_uint(y0);
-              x[16 * i + e + 1] = __float_as_uint(y1);
+              fma_f32x2(y0, y1, __uint_as_float(x[e]), __uint_as_float(x[e + 1]), fk2, add2);
+              x[e] = __float_as_uint(y0);
+              x[e + 1] = __float_as_uint(y1);
             }
           }
           if (edge) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-              const int c = 32 * h + i;
-              if (c > last || (c < first_window && c >= sink_cols))
+              const int col = 32 * h + i;
+              if (col > last || (col < first_window && col >= sink_cols))
                 x[i] = __float_as_uint(-INFINITY);
             }
           }
@@ -461,8 +496,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             top = fmaxf(top, fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])));
           if (__any_sync(0xFFFFFFFFu, top > (fresh ? -INFINITY : kRaise))) {
             // (rare) a new maximum: what was computed with the old one is rescaled, which
-            // is O, l and this half's weights so far
-            tmem_wait_ld_32(coming);
+            // is O, l and this tile's weights so far
+            tmem_wait_ld_32(next);
             const float up = fresh ? fmaxf(top, kNothing) : fmaxf(top, 0.0f);
             const float corr = fresh ? 1.0f : ex2_approx(-up);
             m = less + up;
@@ -470,33 +505,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float off = fresh && top == -INFINITY ? 0.0f : up;
 #pragma unroll
             for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) - off);
-            uint32_t y[16];
+            uint32_t y[8];
             if (step > 0) {
               // O is the product issued last's until that is complete (the one before it
-              // is: this half tile's scores were issued later)
-              const uint32_t before = products + step - 1;
+              // is: this tile's scores were issued later)
+              const uint32_t before = product - 1;
               if (!mbar_wait_warp_inline(pv_done(g, before & 1u), (before >> 1) & 1u, wd,
                                          kSiteEpilogueFull))
                 ok = false;
               tc_fence_after_sync();
 #pragma unroll 1
-              for (int c = 0; c < HSP; c += 16) {
-                tmem_ld_16cols(o_tmem + c, y);
+              for (int d = 0; d < HSP; d += 8) {
+                tmem_ld_8cols(o_tmem + d, y);
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                  y[i] = __float_as_uint(__uint_as_float(y[i]) * corr);
-                tmem_st_16cols(o_tmem + c, y);
+                for (int i = 0; i < 8; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * corr);
+                tmem_st_8cols(o_tmem + d, y);
               }
             }
-            if (h > 0) {
-              tmem_wait_st();
-              tmem_ld_16cols(s_tmem, y);
+            tmem_wait_st();
+#pragma unroll 1
+            for (int d = 0; d < 16 * h; d += 8) {
+              tmem_ld_8cols(s_tmem + d, y);
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
+              for (int i = 0; i < 8; ++i) {
                 const float2 w = __half22float2(*reinterpret_cast<__half2*>(&y[i]));
                 y[i] = half2_of(w.x * corr, w.y * corr);
               }
-              tmem_st_16cols(s_tmem, y);
+              tmem_st_8cols(s_tmem + d, y);
             }
           }
           uint32_t p[16];
@@ -504,12 +539,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 2; ++i) {
             uint64_t sum = 0;
 #pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-              const int at = 16 * i + e;
-              const float y0 = ex2_approx(__uint_as_float(x[at]));
-              const float y1 = ex2_approx(__uint_as_float(x[at + 1]));
+            for (int e = 16 * i; e < 16 * i + 16; e += 2) {
+              const float y0 = ex2_approx(__uint_as_float(x[e]));
+              const float y1 = ex2_approx(__uint_as_float(x[e + 1]));
               sum = add_f32x2(sum, pack_f32x2(y0, y1));
-              p[at / 2] = half2_of(y0, y1);
+              p[e / 2] = half2_of(y0, y1);
             }
             float s0, s1;
             unpack_f32x2(sum, s0, s1);
@@ -517,15 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           // P over S: columns 16 h .., whose scores have been read
           tmem_st_16cols(s_tmem + 16 * h, p);
-        };
-        // The second quarter's scores are on their way while the first is worked on.
-        uint32_t xa[32], xb[32];
-        tmem_ld_32cols_async(s_tmem, xa);
-        tmem_wait_ld_32(xa);
-        tmem_ld_32cols_async(s_tmem + 32, xb);
-        quarter(0, xa, xb);
-        tmem_wait_ld_32(xb);
-        quarter(1, xb, xa);
+        }
         tmem_wait_st();
         tc_fence_before_sync();
         __syncwarp();
@@ -533,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       products += n;
-      tiles += u.tiles;
+      tiles += max(u.n[0], u.n[1]);
       if (n > 0) {
         const uint32_t final = products - 1;
         if (!mbar_wait_warp_inline(pv_done(g, final & 1u), (final >> 1) & 1u, wd,
@@ -568,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           const int unit = 4 * h + i;
-          st_shared16(q_smem + (unit >> 3) * (kTile * 128) + r * 128 +
+          st_shared16(q_smem + (unit >> 3) * (kRows * 128) + r * 128 +
                           (((unit & 7) ^ (r & 7)) << 4),
                       y);
         }
@@ -582,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int head = __shfl_sync(0xFFFFFFFFu, q_hd, from);
         const uint32_t sr = static_cast<uint32_t>((warp & 3) * 32 + from);
         const uint4 y = *reinterpret_cast<const uint4*>(
-            gbase + (q_smem - base) + (piece >> 3) * (kTile * 128) + sr * 128 +
+            gbase + (q_smem - base) + (piece >> 3) * (kRows * 128) + sr * 128 +
             (((piece & 7) ^ (sr & 7)) << 4));
         if (row >= 0 && piece * 8 < D)
           *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row * a.out_token +
@@ -593,41 +619,53 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp < kMmaWarp) {
     // --------------------------------------------------------- conversion --
     const int w = warp - kSoftmaxWarps;
-    constexpr int kLaneVBytes = HSP / 8;  // V elements a lane transposes, for 8 tokens
-    constexpr int kKLoads = 4 * (HSP / 64);
-    // K: tokens 32 w + 8 o + lane % 8, elements 64 h + 16 (lane / 8) ..
-    // V: tokens 64 (w & 1) + 8 (lane % 8) .., elements (w >> 1) HSP / 2 + (lane / 8) kLaneVBytes ..
-    const int vt = 64 * (w & 1) + 8 * (lane & 7);
-    const int vd = (w >> 1) * (HSP / 2) + (lane >> 3) * kLaneVBytes;
-    uint32_t it = 0;
+    constexpr int kLaneVBytes = HSP / 16;  // V elements a lane transposes, for 8 tokens
+    constexpr int kKLoads = HSP / 32;
+    // K: tokens 16 w + 8 o + lane % 8, elements 64 h + 16 (lane / 8) ..
+    // V: tokens 8 (lane % 8) .., elements w HSP / 4 + (lane / 8) kLaneVBytes ..
+    const int vt = 8 * (lane & 7);
+    const int vd = w * (HSP / 4) + (lane >> 3) * kLaneVBytes;
+    uint32_t it = 0;     // slots filled
+    uint32_t tiles = 0;  // before this unit (the factors' slots)
     uint4 kx[kKLoads];
     uint32_t vx[8][kLaneVBytes / 4];
+    float f_k = 1.0f, f_v = 0.0f;  // scales on their way
     bool ok = true, injected = false;
-
-    // The pages of a tile's eight groups of 16 tokens, in lanes 0..7 (-1: none there).
-    auto pages_of = [&](const Unit& u, int j) {
-      const int tok = tile_token(u, j) + 16 * lane;
-      return lane < 8 && tok < u.q.length ? kv_page(a.v, u.s, tok >> a.v.page_shift) : -1;
-    };
-    const long long page_bytes = static_cast<long long>(a.v.page_tokens) * D;
     const int page_mask = a.v.page_tokens - 1;
+    const long long page_bytes = static_cast<long long>(a.v.page_tokens) * D;
+
+    // The table's entries for a tile's four groups of 16 tokens, in lanes 0..3; read a
+    // step before they are checked, so that nothing waits for them.
+    auto entries_of = [&](const Unit& u, int j) {
+      const int tok = tile_token(u, j) + 16 * lane;
+      return static_cast<int>(load4_if(a.v.table + (static_cast<long long>(u.s) * a.v.table_width +
+                                                    (tok >> a.v.page_shift)),
+                                       lane < 4 && tok < u.q.length, 0xFFFFFFFFu));
+    };
+    auto pages_of = [&](const Unit& u, int j, int entry) {  // -1: none there
+      if (lane < 4 && tile_token(u, j) + 16 * lane < u.q.length &&
+          (entry < 0 || entry >= a.v.pages)) {
+        report_index(a.v.status, kIndexPage);
+        return -1;
+      }
+      return entry;
+    };
     auto load_k = [&](const Unit& u, int j, int pages) {
-      const int tb = tile_token(u, j);
+      const int page = __shfl_sync(0xFFFFFFFFu, pages, w);
+      const int tok = tile_token(u, j) + 16 * w + (lane & 7);
+      const uint8_t* from =
+          a.v.codes[0] + (static_cast<long long>(page) * a.v.heads + u.head) * page_bytes +
+          ((tok & page_mask) * D + 16 * (lane >> 3));
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {  // 16 tokens each
-        const int page = __shfl_sync(0xFFFFFFFFu, pages, 2 * w + half);
-        const int tok = tb + 32 * w + 16 * half + (lane & 7);
-        const uint8_t* from =
-            a.v.codes[0] + (static_cast<long long>(page) * a.v.heads + u.head) * page_bytes +
-            ((tok & page_mask) * D + 16 * (lane >> 3));
+      for (int o = 0; o < 2; ++o)
 #pragma unroll
-        for (int o = 0; o < 2; ++o)
-#pragma unroll
-          for (int h = 0; h < HSP / 64; ++h)
-            kx[(2 * half + o) * (HSP / 64) + h] =
-                page >= 0 && 64 * h + 16 * (lane >> 3) < D
-                    ? __ldg(reinterpret_cast<const uint4*>(from + 8 * o * D + 64 * h))
-                    : make_uint4(0, 0, 0, 0);
+        for (int h = 0; h < HSP / 64; ++h)
+          kx[o * (HSP / 64) + h] =
+              load16_if(from + 8 * o * D + 64 * h, page >= 0 && 64 * h + 16 * (lane >> 3) < D);
+      if (w == 0) {  // the factors: lanes 0..3, a group of 16 tokens each
+        const long long unit = static_cast<long long>(pages) * a.v.heads + u.head;
+        f_k = __uint_as_float(load4_if(a.v.scale[0] + unit, pages >= 0, 0x3F800000u));
+        f_v = __uint_as_float(load4_if(a.v.scale[1] + unit, pages >= 0, 0u));  // 0 masks the 16
       }
     };
     auto load_v = [&](const Unit& u, int j, int pages) {
@@ -639,124 +677,111 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const bool in = page >= 0 && tok + i < u.q.length && vd < D;
-        if constexpr (kLaneVBytes == 16) {
-          const uint4 x = in ? __ldg(reinterpret_cast<const uint4*>(from + i * D))
-                             : make_uint4(0, 0, 0, 0);
+        if constexpr (kLaneVBytes == 8) {
+          const uint2 x = load8_if(from + i * D, in);
           vx[i][0] = x.x;
           vx[i][1] = x.y;
-          vx[i][2] = x.z;
-          vx[i][3] = x.w;
         } else {
-          const uint2 x = in ? __ldg(reinterpret_cast<const uint2*>(from + i * D)) : make_uint2(0, 0);
-          vx[i][0] = x.x;
-          vx[i][1] = x.y;
+          vx[i][0] = load4_if(from + i * D, in, 0u);
         }
-      }
-    };
-    float f_k = 1.0f, f_v = 0.0f;  // scales on their way
-    auto load_scales = [&](const Unit& u, int pages) {
-      if (w != 0) return;
-      if (pages >= 0) {
-        const long long unit = static_cast<long long>(pages) * a.v.heads + u.head;
-        f_k = __ldg(a.v.scale[0] + unit);
-        f_v = __ldg(a.v.scale[1] + unit);
-      } else {
-        f_k = 1.0f;
-        f_v = 0.0f;  // log2: -inf, which masks the 16 tokens
       }
     };
 
     for (uint32_t k = 0; ok; ++k) {
       Unit u;
-      if (lane == 0) mbar_arrive(u_want);
+      if (k == 0 && lane == 0) mbar_arrive(u_want);
       if (!take_unit(k, u) || u.n[0] < 0) break;
-      const int n = u.tiles;
-      if (n == 0) continue;
-      int next = pages_of(u, 0);
-      load_k(u, 0, next);
-      load_v(u, 0, next);
-      load_scales(u, next);
-      if (n > 1) next = pages_of(u, 1);
-      for (int j = 0; j < n; ++j, ++it) {
-        const uint32_t stage = it % kStages, phase = (it / kStages) & 1u;
-        if (!mbar_wait_warp_inline(k_empty(stage), phase ^ 1u, wd, kSiteLoaderEmpty)) {
+      const int n = max(u.n[0], u.n[1]);
+      const int ask = max(n - kAskAhead, -1);
+      if (n == 0) {
+        if (lane == 0) mbar_arrive(u_want);
+        continue;
+      }
+      int pages = pages_of(u, 0, entries_of(u, 0));
+      int entry = n > 1 ? entries_of(u, 1) : -1;
+      load_k(u, 0, pages);
+      // slot j: K of tile j + 1, V of tile j
+      for (int j = -1; j < n; ++j, ++it) {
+        const uint32_t slot = it % kSlots;
+        if (j == ask && lane == 0) mbar_arrive(u_want);
+        if (!mbar_wait_warp_inline(empty(slot), ((it / kSlots) & 1u) ^ 1u, wd, kSiteLoaderEmpty)) {
           ok = false;
           break;
         }
-        if (w == 0 && lane < 8)
-          factors[(it % kFactorSlots) * 8 + lane] =
-              Factor{a.scale_log2 * f_k, __log2f(f_v), f_v > 0.0f ? __fdividef(1.0f, f_v) : 0.0f, 0.0f};
-        const uint32_t ks = base + L::kK + stage * L::kKBytes;
+        if (j + 1 < n) {
+          if (w == 0 && lane < 4)
+            factors[((tiles + j + 1) % kFactorSlots) * 4 + lane] =
+                Factor{a.scale_log2 * f_k, __log2f(f_v),
+                       f_v > 0.0f ? __fdividef(1.0f, f_v) : 0.0f, 0.0f};
+          const uint32_t ks = base + L::kK + slot * L::kKBytes;
 #pragma unroll
-        for (int o = 0; o < 4; ++o) {
-          const uint32_t row = 32 * w + 8 * o + (lane & 7);
+          for (int o = 0; o < 2; ++o) {
+            const uint32_t row = 16 * w + 8 * o + (lane & 7);
 #pragma unroll
-          for (int h = 0; h < HSP / 64; ++h) {
-            const uint32_t* c = reinterpret_cast<const uint32_t*>(&kx[o * (HSP / 64) + h]);
-            uint32_t y[8];
+            for (int h = 0; h < HSP / 64; ++h) {
+              const uint32_t* c = reinterpret_cast<const uint32_t*>(&kx[o * (HSP / 64) + h]);
+              uint32_t y[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if constexpr (kBf16) codes4_to_bf162x2<kFormat>(c[i], y[2 * i], y[2 * i + 1]);
-              else codes4_to_half2x2<kFormat>(c[i], y[2 * i], y[2 * i + 1]);
+              for (int i = 0; i < 4; ++i) {
+                if constexpr (kBf16) codes4_to_bf162x2<kFormat>(c[i], y[2 * i], y[2 * i + 1]);
+                else codes4_to_half2x2<kFormat>(c[i], y[2 * i], y[2 * i + 1]);
+              }
+              const uint32_t at = ks + h * (kTile * 128) + row * 128;
+              const uint32_t unit = 2 * (lane >> 3);
+              st_shared16(at + ((unit ^ (row & 7)) << 4), y);
+              st_shared16(at + (((unit + 1) ^ (row & 7)) << 4), y + 4);
             }
-            const uint32_t at = ks + h * (kTile * 128) + row * 128;
-            const uint32_t unit = 2 * (lane >> 3);
-            st_shared16(at + ((unit ^ (row & 7)) << 4), y);
-            st_shared16(at + (((unit + 1) ^ (row & 7)) << 4), y + 4);
+          }
+        }
+        if (j >= 0) {
+          const uint32_t vs = base + L::kV + slot * L::kVBytes;
+#pragma unroll
+          for (int c = 0; c < kLaneVBytes / 4; ++c) {
+            // eight tokens of four elements: pairs of tokens, then rows of V^T
+            uint32_t y[4][4];
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+              uint32_t x0 = vx[2 * p][c], x1 = vx[2 * p + 1][c];
+              if (kFormat == CSA_KV_INT8) {
+                x0 ^= 0x80808080u;
+                x1 ^= 0x80808080u;
+              }
+              const uint32_t lo = byte_perm(x0, x1, 0x5140), hi = byte_perm(x0, x1, 0x7362);
+              if (kFormat == CSA_KV_INT8) {
+                y[0][p] = flipped_pair_to_half2<0x4140>(lo);
+                y[1][p] = flipped_pair_to_half2<0x4342>(lo);
+                y[2][p] = flipped_pair_to_half2<0x4140>(hi);
+                y[3][p] = flipped_pair_to_half2<0x4342>(hi);
+              } else {
+                y[0][p] = e4m3x2_to_half2(lo & 0xFFFFu);
+                y[1][p] = e4m3x2_to_half2(lo >> 16);
+                y[2][p] = e4m3x2_to_half2(hi & 0xFFFFu);
+                y[3][p] = e4m3x2_to_half2(hi >> 16);
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t row = vd + 4 * c + e;
+              st_shared16(vs + row * 128 + (((lane & 7) ^ (row & 7)) << 4), y[e]);
+            }
           }
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (a.inject && !injected) {
-          injected = true;  // withhold the CTA's first K tile: the MMA warp's wait runs out
+          injected = true;  // withhold the CTA's first K tile: the issuers' wait runs out
         } else if (lane == 0) {
-          mbar_arrive(k_full(stage));
+          mbar_arrive(full(slot));
         }
-        if (j + 1 < n) {
-          load_k(u, j + 1, next);
-          load_scales(u, next);
+        // the next slot's codes: V of tile j + 1, K of tile j + 2
+        if (j + 1 < n) load_v(u, j + 1, pages);
+        if (j + 2 < n) {
+          pages = pages_of(u, j + 2, entry);
+          load_k(u, j + 2, pages);
+          if (j + 3 < n) entry = entries_of(u, j + 3);
         }
-        if (!mbar_wait_warp_inline(v_empty(stage), phase ^ 1u, wd, kSiteLoaderEmpty)) {
-          ok = false;
-          break;
-        }
-        const uint32_t vs = base + L::kV + stage * L::kVBytes + (w & 1) * (HSP * 128);
-#pragma unroll
-        for (int c = 0; c < kLaneVBytes / 4; ++c) {
-          // eight tokens of four elements: pairs of tokens, then rows of V^T
-          uint32_t y[4][4];
-#pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            uint32_t x0 = vx[2 * p][c], x1 = vx[2 * p + 1][c];
-            if (kFormat == CSA_KV_INT8) {
-              x0 ^= 0x80808080u;
-              x1 ^= 0x80808080u;
-            }
-            const uint32_t lo = byte_perm(x0, x1, 0x5140), hi = byte_perm(x0, x1, 0x7362);
-            if (kFormat == CSA_KV_INT8) {
-              y[0][p] = flipped_pair_to_half2<0x4140>(lo);
-              y[1][p] = flipped_pair_to_half2<0x4342>(lo);
-              y[2][p] = flipped_pair_to_half2<0x4140>(hi);
-              y[3][p] = flipped_pair_to_half2<0x4342>(hi);
-            } else {
-              y[0][p] = e4m3x2_to_half2(lo & 0xFFFFu);
-              y[1][p] = e4m3x2_to_half2(lo >> 16);
-              y[2][p] = e4m3x2_to_half2(hi & 0xFFFFu);
-              y[3][p] = e4m3x2_to_half2(hi >> 16);
-            }
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t row = vd + 4 * c + e;
-            st_shared16(vs + row * 128 + (((lane & 7) ^ (row & 7)) << 4), y[e]);
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(v_full(stage));
-        if (j + 1 < n) load_v(u, j + 1, next);
-        if (j + 2 < n) next = pages_of(u, j + 2);
       }
+      tiles += n;
     }
   } else if (warp == kListWarp) {
     // --------------------------------------------------------------- list --
@@ -778,15 +803,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // -------------------------------------------------------- MMA issuers --
     const uint32_t g = warp - kMmaWarp;
-    constexpr uint32_t kIdescS = kBf16 ? idesc_bf16_f32(kTile, kHalf) : idesc_f16_f32(kTile, kHalf);
-    constexpr uint32_t kIdescO = idesc_f16_f32(kTile, HSP);
+    constexpr uint32_t kIdescS = kBf16 ? idesc_bf16_f32(kRows, kTile) : idesc_f16_f32(kRows, kTile);
+    constexpr uint32_t kIdescO = idesc_f16_f32(kRows, HSP);
     // Descriptors' low words (the start address in units of 16 bytes); moving along a
     // tile adds to them.
     const uint64_t desc = umma_desc_k_sw128(base);
     const uint32_t desc_hi = static_cast<uint32_t>(desc >> 32), lo = static_cast<uint32_t>(desc);
-    const uint32_t s_tmem = tmem + g * kTile, o_tmem = tmem + 2 * kTile + g * HSP;
+    const uint32_t s_tmem = tmem + g * kRows, o_tmem = tmem + 2 * kRows + g * HSP;
     const uint32_t qd = lo + ((L::kQ + g * L::kQBytes) >> 4);
-    uint32_t tiles = 0, products = 0, q_phase = 0;
+    uint32_t it = 0, products = 0, q_phase = 0;
     bool ok = true;
     for (uint32_t k = 0; ok; ++k) {
       Unit u;
@@ -794,70 +819,54 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (shuffled so that the compiler knows them to be the warp's: what is computed
       // from them then stays in uniform registers, which the MMAs' operands are)
       const int n = __shfl_sync(0xFFFFFFFFu, g == 0 ? u.n[0] : u.n[1], 0);
-      const int n_tiles = __shfl_sync(0xFFFFFFFFu, u.tiles, 0);
-      // step -1 starts the first scores; tiles past this group's own are only given back
-      for (int step = -1; ok && step < 2 * n_tiles; ++step) {
-        const int ahead = step + 1;
-        if (ahead < n) {
-          const uint32_t t = tiles + (ahead >> 1), stage = t % kStages;
-          if (ahead == 0) {
-            ok = mbar_wait_warp_inline(q_ready(g), q_phase, wd, kSiteMmaFull);
-            q_phase ^= 1u;
-          }
-          if ((ahead & 1) == 0)
-            ok = ok && mbar_wait_warp_inline(k_full(stage), (t / kStages) & 1u, wd, kSiteMmaFull);
-          if (!ok) break;
+      const int n_all = __shfl_sync(0xFFFFFFFFu, max(u.n[0], u.n[1]), 0);
+      if (n_all == 0) continue;
+      if (n > 0) {
+        if (!mbar_wait_warp_inline(q_ready(g), q_phase, wd, kSiteMmaFull)) break;
+        q_phase ^= 1u;
+      }
+      // slots of tiles past this group's own are only given back
+      for (int j = -1; j < n_all; ++j, ++it) {
+        const uint32_t slot = it % kSlots;
+        if (!mbar_wait_warp_inline(full(slot), (it / kSlots) & 1u, wd, kSiteMmaFull)) {
+          ok = false;
+          break;
+        }
+        if (j + 1 < n) {
           tc_fence_after_sync();
-          const uint32_t buffer = (products + ahead) & 1u;
-          const uint32_t kd =
-              lo + ((L::kK + stage * L::kKBytes + (ahead & 1) * (kHalf * 128)) >> 4);
+          const uint32_t buffer = (products + j + 1) & 1u;
+          const uint32_t kd = lo + ((L::kK + slot * L::kKBytes) >> 4);
           if (elect_one()) {
 #pragma unroll
-            for (int s = 0; s < HSP / 16; ++s) {
-              const uint32_t at = ((s >> 2) * (kTile * 128) + (s & 3) * 32) >> 4;
-              umma_f16_ss(s_tmem + buffer * kHalf, qd + at, kd + at, desc_hi, kIdescS, s > 0);
-            }
+            for (int s = 0; s < HSP / 16; ++s)
+              umma_f16_ss(s_tmem + buffer * kTile,
+                          qd + (((s >> 2) * (kRows * 128) + (s & 3) * 32) >> 4),
+                          kd + (((s >> 2) * (kTile * 128) + (s & 3) * 32) >> 4), desc_hi, kIdescS,
+                          s > 0);
             umma_commit(s_full(g, buffer));
           }
           __syncwarp();
         }
-        if ((ahead & 1) == 1 && ahead < 2 * n_tiles) {
-          const uint32_t t = tiles + (ahead >> 1);
-          // (a stage is filled before it is given back, by either group)
-          ok = mbar_wait_warp_inline(k_full(t % kStages), (t / kStages) & 1u, wd, kSiteMmaFull);
-          if (!ok) break;
-          if (elect_one()) umma_commit(k_empty(t % kStages));
-          __syncwarp();
-        }
-        if (step < 0) continue;
-        const uint32_t t = tiles + (step >> 1), stage = t % kStages;
-        if ((step & 1) == 0 &&
-            !mbar_wait_warp_inline(v_full(stage), (t / kStages) & 1u, wd, kSiteMmaFull)) {
-          ok = false;
-          break;
-        }
-        if (step < n) {
-          const uint32_t p = products + step;
-          const uint32_t vd =
-              lo + ((L::kV + stage * L::kVBytes + (step & 1) * (HSP * 128)) >> 4);
-          ok = mbar_wait_warp_inline(p_ready(g, p & 1u), (p >> 1) & 1u, wd, kSiteMmaTmemEmpty);
-          if (!ok) break;
+        if (j >= 0 && j < n) {
+          const uint32_t p = products + j;
+          const uint32_t vd = lo + ((L::kV + slot * L::kVBytes) >> 4);
+          if (!mbar_wait_warp_inline(p_ready(g, p & 1u), (p >> 1) & 1u, wd, kSiteMmaTmemEmpty)) {
+            ok = false;
+            break;
+          }
           tc_fence_after_sync();
           if (elect_one()) {
 #pragma unroll
-            for (int s = 0; s < kHalf / 16; ++s)
-              umma_f16_ts(o_tmem, s_tmem + (p & 1u) * kHalf + 8 * s, vd + 2 * s, desc_hi, kIdescO,
-                          step > 0 || s > 0);
+            for (int s = 0; s < kTile / 16; ++s)
+              umma_f16_ts(o_tmem, s_tmem + (p & 1u) * kTile + 8 * s, vd + 2 * s, desc_hi, kIdescO,
+                          j > 0 || s > 0);
             umma_commit(pv_done(g, p & 1u));
           }
           __syncwarp();
         }
-        if ((step & 1) == 1) {
-          if (elect_one()) umma_commit(v_empty(stage));
-          __syncwarp();
-        }
+        if (elect_one()) umma_commit(empty(slot));
+        __syncwarp();
       }
-      tiles += n_tiles;
       products += n;
     }
     // Every MMA must be complete before TMEM and shared memory go away.
