@@ -5,7 +5,7 @@
 // A unit of work is 256 rows (tokens x query heads of one kv head) of a
 // sequence: two groups A and B of 128, each a TMEM accumulator's lanes, which
 // share every tile of 64 keys. One CTA per SM takes units from a counter
-// (longest first within a sequence), with 15 warps:
+// (longest first within a sequence), with 16 warps:
 //  - warps 0..7: softmax, warps 0..3 group A, 4..7 group B, a thread a row. Per 32
 //    keys: scores from TMEM (the next 32 on their way), x - m, their maximum, and
 //    the weights exp2(x - m) as fp16 over S (P, the second product's A operand in
@@ -14,11 +14,11 @@
 //    with separate code for each part of a tile and for edges a quarter of the
 //    cycles went to waiting for instructions. Before a unit they copy Q's rows to
 //    shared memory; after it they write O / l.
-//  - warps 8..11: conversion. Codes come from HBM into registers a tile ahead
-//    (their page numbers two) and go to shared memory in the 128-byte-swizzle
-//    K-major layout, K as [token][element] in Q's type, V transposed in registers
-//    to [element][token] in fp16 (both exact). A slot of the ring of four holds V
-//    of tile j and K of tile j + 1, what one step of the products reads.
+//  - warps 8..11: conversion, from raw codes in shared memory to the
+//    128-byte-swizzle K-major layout, K as [token][element] in Q's type, V
+//    transposed in registers to [element][token] in fp16 (both exact). A slot of
+//    the ring holds V of tile j and K of tile j + 1, what one step of the products
+//    reads.
 //  - warps 12 and 13: one thread each issues a group's products, per step
 //    S = Q K^T of tile j + 1, then O += P V of tile j. S has two buffers of 64
 //    columns, so the softmax finds the next scores ready when it is done with the
@@ -26,9 +26,15 @@
 //    the product issued before it reads. (With both groups on one warp the issue
 //    itself, some 90 cycles an MMA, was the longest path.)
 //  - warp 14: takes a unit from the counter (workspace, cleared by the rows kernel
-//    ahead in the stream) when the conversion asks for it, some tiles before it is
+//    ahead in the stream) when the copies ask for it, some tiles before they are
 //    through with the last one: early enough to hide the way to the first scores, late
 //    enough that a CTA holds no unit that another could have begun.
+//  - warp 15: copies. A page's part of a tile is contiguous, so one thread moves it
+//    with bulk copies (two slots ahead of the conversion); the warp also turns the
+//    scales into the softmax's factors.
+// Every role's loop is kept short: with the codes fetched to registers by the
+// conversion warps themselves, straight-line code that one warp in four executes once
+// per tile missed the instruction cache and the conversion was the longest path.
 //
 // Scales (see cache_attention_sm103a.cu): with c ks and log2(vs) per 16 tokens in
 // shared memory, x = s (c ks) + log2(vs) and the weight has V's scale in it; the
@@ -56,11 +62,13 @@ constexpr int kSoftmaxWarps = 8;
 constexpr int kConvertWarps = 4;
 constexpr int kMmaWarp = kSoftmaxWarps + kConvertWarps;
 constexpr int kListWarp = kMmaWarp + 2;
-constexpr int kThreads = 32 * (kListWarp + 1);
+constexpr int kCopyWarp = kListWarp + 1;
+constexpr int kThreads = 32 * (kCopyWarp + 1);
 constexpr int kRows = 128;          // per group
 constexpr int kUnitRows = 2 * kRows;
 constexpr int kTile = 64;           // keys per step
-constexpr int kSlots = 4;           // of the ring of converted keys and values
+constexpr int kSlots = 3;           // of the ring of converted keys and values
+constexpr int kRawSlots = 2;        // of the ring of codes
 constexpr int kFactorSlots = 8;     // tiles whose factors are kept
 constexpr int kUnitSlots = 2;
 constexpr int kAskAhead = 12;       // tiles before a unit's end when the next is asked for
@@ -102,10 +110,12 @@ struct Layout {
   static constexpr int kQBytes = kRows * HSP * 2;  // per group: [HSP / 64][128 rows][128 B]
   static constexpr int kKBytes = kTile * HSP * 2;  // per slot: [HSP / 64][64 rows][128 B]
   static constexpr int kVBytes = HSP * kTile * 2;  // per slot: [HSP rows][128 B]
+  static constexpr int kRawBytes = kTile * HSP;    // K's or V's codes: [64 tokens][head_size]
   static constexpr int kQ = 0, kK = 2 * kQBytes, kV = kK + kSlots * kKBytes,
-                       kFactors = kV + kSlots * kVBytes,
+                       kRaw = kV + kSlots * kVBytes,
+                       kFactors = kRaw + kRawSlots * 2 * kRawBytes,
                        kBars = kFactors + kFactorSlots * 4 * static_cast<int>(sizeof(Factor)),
-                       kMisc = kBars + 8 * 30, kUnits = kMisc + 16,
+                       kMisc = kBars + 8 * 32, kUnits = kMisc + 16,
                        kTotal = kUnits + kUnitSlots * static_cast<int>(sizeof(Unit));
 };
 
@@ -260,33 +270,14 @@ __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// Read-only loads of 16, 8 or 4 bytes where `in`, else zeros: predicated, as a branch
-// around each load costs more than the load.
-__device__ __forceinline__ uint4 load16_if(const uint8_t* from, bool in) {
-  uint4 x;
-  asm("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t"
-      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
-      "@p ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
-      : "=&r"(x.x), "=&r"(x.y), "=&r"(x.z), "=&r"(x.w)
-      : "l"(from), "r"(in ? 1 : 0));
-  return x;
-}
-__device__ __forceinline__ uint2 load8_if(const uint8_t* from, bool in) {
-  uint2 x;
-  asm("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\t"
-      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
-      "@p ld.global.nc.v2.b32 {%0, %1}, [%2];\n\t}"
-      : "=&r"(x.x), "=&r"(x.y)
-      : "l"(from), "r"(in ? 1 : 0));
-  return x;
-}
-__device__ __forceinline__ uint32_t load4_if(const void* from, bool in, uint32_t other) {
-  uint32_t x;
-  asm("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b32 %0, %3;\n\t"
-      "@p ld.global.nc.b32 %0, [%1];\n\t}"
-      : "=&r"(x)
-      : "l"(from), "r"(in ? 1 : 0), "r"(other));
-  return x;
+// Bulk copy global -> shared (16-byte multiples), completing on an mbarrier.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
 }
 
 // 16-byte global -> shared copy past L1; zeros where bytes is 0.
@@ -312,6 +303,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t bars = base + L::kBars;
   auto full = [&](uint32_t s) { return bars + 8u * s; };
   auto empty = [&](uint32_t s) { return bars + 8u * (4 + s); };
+  auto raw_full = [&](uint32_t s) { return bars + 8u * (28 + s); };
+  auto raw_empty = [&](uint32_t s) { return bars + 8u * (30 + s); };
   auto q_ready = [&](uint32_t g) { return bars + 8u * (8 + g); };
   auto s_full = [&](uint32_t g, uint32_t b) { return bars + 8u * (10 + 2 * g + b); };
   auto p_ready = [&](uint32_t g, uint32_t b) { return bars + 8u * (14 + 2 * g + b); };
@@ -325,6 +318,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem_slot = base + L::kMisc;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::kMisc + 4);
   Factor* factors = reinterpret_cast<Factor*>(gbase + L::kFactors);
+  // Bit i: the 16 tokens i of a raw slot's K (bits 4..7: V) have a page.
+  volatile uint32_t* raw_pages = reinterpret_cast<volatile uint32_t*>(gbase + L::kMisc + 8);
   const Watchdog wd{a.wait_limit_ns, a.status, abort_flag};
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
@@ -332,6 +327,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(full(s), kConvertWarps);
       mbar_init(empty(s), 2);  // one commit of each group's issuer
+    }
+    for (int s = 0; s < kRawSlots; ++s) {
+      mbar_init(raw_full(s), 1);
+      mbar_init(raw_empty(s), kConvertWarps);
     }
     for (int g = 0; g < 2; ++g) {
       mbar_init(q_ready(g), 4);
@@ -342,10 +341,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     mbar_init(drain, 2);
-    mbar_init(u_want, kConvertWarps);
+    mbar_init(u_want, 1);
     for (int s = 0; s < kUnitSlots; ++s) {
       mbar_init(u_full(s), 1);
-      mbar_init(u_empty(s), kListWarp);  // every warp but the list's
+      mbar_init(u_empty(s), kThreads / 32 - 1);  // every warp but the list's
     }
     *abort_flag = 0;
     fence_barrier_init();
@@ -620,27 +619,132 @@ __global__ void __launch_bounds__(kThreads, 1)
     // --------------------------------------------------------- conversion --
     const int w = warp - kSoftmaxWarps;
     constexpr int kLaneVBytes = HSP / 16;  // V elements a lane transposes, for 8 tokens
-    constexpr int kKLoads = HSP / 32;
-    // K: tokens 16 w + 8 o + lane % 8, elements 64 h + 16 (lane / 8) ..
-    // V: tokens 8 (lane % 8) .., elements w HSP / 4 + (lane / 8) kLaneVBytes ..
-    const int vt = 8 * (lane & 7);
-    const int vd = w * (HSP / 4) + (lane >> 3) * kLaneVBytes;
-    uint32_t it = 0;     // slots filled
-    uint32_t tiles = 0;  // before this unit (the factors' slots)
-    uint4 kx[kKLoads];
-    uint32_t vx[8][kLaneVBytes / 4];
-    float f_k = 1.0f, f_v = 0.0f;  // scales on their way
+    constexpr int kChunks = HSP / 16, kKRows = 32 / kChunks;  // 16-byte chunks of a row
+    // K: a warp's 16 tokens, kKRows rows at once. V: tokens 8 oct .., elements vd ..;
+    // four octets and eight runs of elements a warp, so that neither the loads' nor the
+    // stores' bank conflicts are more than four- and twofold.
+    const int chunk = lane % kChunks, k_row = 16 * w + lane / kChunks;
+    const int oct = 4 * (w & 1) + (lane & 3), vt = 8 * oct;
+    const int vd = (w >> 1) * (HSP / 2) + (lane >> 2) * kLaneVBytes;
+    uint32_t it = 0;  // slots filled
+    bool ok = true;
+    for (uint32_t k = 0; ok; ++k) {
+      Unit u;
+      if (!take_unit(k, u) || u.n[0] < 0) break;
+      const int n = max(u.n[0], u.n[1]);
+      // slot j: K of tile j + 1, V of tile j
+      if (n > 0)
+        for (int j = -1; j < n; ++j, ++it) {
+          const uint32_t slot = it % kSlots, rs = it % kRawSlots;
+          if (!mbar_wait_warp_inline(raw_full(rs), (it / kRawSlots) & 1u, wd, kSiteLoaderEmpty) ||
+              !mbar_wait_warp_inline(empty(slot), ((it / kSlots) & 1u) ^ 1u, wd,
+                                     kSiteLoaderEmpty)) {
+            ok = false;
+            break;
+          }
+          const uint8_t* codes = gbase + L::kRaw + rs * 2 * L::kRawBytes;
+          const uint32_t here = raw_pages[rs];
+          if (j + 1 < n) {
+            const uint32_t ks = base + L::kK + slot * L::kKBytes;
+            const bool in = (here >> w & 1u) != 0 && chunk * 16 < D;
+#pragma unroll 2
+            for (int i = 0; i < 16; i += kKRows) {
+              const uint32_t row = k_row + i;
+              uint4 x = make_uint4(0, 0, 0, 0);
+              if (in) x = *reinterpret_cast<const uint4*>(codes + row * D + chunk * 16);
+              const uint32_t c[4] = {x.x, x.y, x.z, x.w};
+              uint32_t y[8];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if constexpr (kBf16) codes4_to_bf162x2<kFormat>(c[e], y[2 * e], y[2 * e + 1]);
+                else codes4_to_half2x2<kFormat>(c[e], y[2 * e], y[2 * e + 1]);
+              }
+              const uint32_t at = ks + (chunk >> 2) * (kTile * 128) + row * 128;
+              const uint32_t unit = 2 * (chunk & 3);
+              st_shared16(at + ((unit ^ (row & 7)) << 4), y);
+              st_shared16(at + (((unit + 1) ^ (row & 7)) << 4), y + 4);
+            }
+          }
+          if (j >= 0) {
+            codes += L::kRawBytes;
+            uint32_t vx[8][kLaneVBytes / 4];
+            // (what is loaded past the sequence's end, or past head_size, is whatever the
+            // slot held, and zeroed)
+            const int have = (here >> (4 + (oct >> 1)) & 1u) != 0 && vd < D
+                                 ? u.q.length - tile_token(u, j) - vt  // tokens of the octet
+                                 : 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint8_t* from = codes + (vt + i) * D + vd;
+              if constexpr (kLaneVBytes == 8) {
+                const uint2 x = *reinterpret_cast<const uint2*>(from);
+                vx[i][0] = x.x;
+                vx[i][1] = x.y;
+              } else {
+                vx[i][0] = *reinterpret_cast<const uint32_t*>(from);
+              }
+            }
+            if (have < 8) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int c = 0; c < kLaneVBytes / 4; ++c)
+                  if (i >= have) vx[i][c] = 0;
+            }
+            const uint32_t vs = base + L::kV + slot * L::kVBytes;
+#pragma unroll
+            for (int c = 0; c < kLaneVBytes / 4; ++c) {
+              // eight tokens of four elements: pairs of tokens, then rows of V^T
+              uint32_t y[4][4];
+#pragma unroll
+              for (int p = 0; p < 4; ++p) {
+                uint32_t x0 = vx[2 * p][c], x1 = vx[2 * p + 1][c];
+                if (kFormat == CSA_KV_INT8) {
+                  x0 ^= 0x80808080u;
+                  x1 ^= 0x80808080u;
+                }
+                const uint32_t lo = byte_perm(x0, x1, 0x5140), hi = byte_perm(x0, x1, 0x7362);
+                if (kFormat == CSA_KV_INT8) {
+                  y[0][p] = flipped_pair_to_half2<0x4140>(lo);
+                  y[1][p] = flipped_pair_to_half2<0x4342>(lo);
+                  y[2][p] = flipped_pair_to_half2<0x4140>(hi);
+                  y[3][p] = flipped_pair_to_half2<0x4342>(hi);
+                } else {
+                  y[0][p] = e4m3x2_to_half2(lo & 0xFFFFu);
+                  y[1][p] = e4m3x2_to_half2(lo >> 16);
+                  y[2][p] = e4m3x2_to_half2(hi & 0xFFFFu);
+                  y[3][p] = e4m3x2_to_half2(hi >> 16);
+                }
+              }
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t row = vd + 4 * c + e;
+                st_shared16(vs + row * 128 + ((oct ^ (row & 7)) << 4), y[e]);
+              }
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(full(slot));
+            mbar_arrive(raw_empty(rs));
+          }
+        }
+    }
+  } else if (warp == kCopyWarp) {
+    // ------------------------------------------------------------- copies --
+    uint32_t it = 0, tiles = 0;
     bool ok = true, injected = false;
-    const int page_mask = a.v.page_tokens - 1;
-    const long long page_bytes = static_cast<long long>(a.v.page_tokens) * D;
-
+    const int P = a.v.page_tokens, page_mask = P - 1;
+    const long long page_bytes = static_cast<long long>(P) * D;
     // The table's entries for a tile's four groups of 16 tokens, in lanes 0..3; read a
     // step before they are checked, so that nothing waits for them.
     auto entries_of = [&](const Unit& u, int j) {
       const int tok = tile_token(u, j) + 16 * lane;
-      return static_cast<int>(load4_if(a.v.table + (static_cast<long long>(u.s) * a.v.table_width +
-                                                    (tok >> a.v.page_shift)),
-                                       lane < 4 && tok < u.q.length, 0xFFFFFFFFu));
+      return lane < 4 && tok < u.q.length
+                 ? __ldg(a.v.table + (static_cast<long long>(u.s) * a.v.table_width +
+                                      (tok >> a.v.page_shift)))
+                 : -1;
     };
     auto pages_of = [&](const Unit& u, int j, int entry) {  // -1: none there
       if (lane < 4 && tile_token(u, j) + 16 * lane < u.q.length &&
@@ -650,43 +754,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return entry;
     };
-    auto load_k = [&](const Unit& u, int j, int pages) {
-      const int page = __shfl_sync(0xFFFFFFFFu, pages, w);
-      const int tok = tile_token(u, j) + 16 * w + (lane & 7);
-      const uint8_t* from =
-          a.v.codes[0] + (static_cast<long long>(page) * a.v.heads + u.head) * page_bytes +
-          ((tok & page_mask) * D + 16 * (lane >> 3));
-#pragma unroll
-      for (int o = 0; o < 2; ++o)
-#pragma unroll
-        for (int h = 0; h < HSP / 64; ++h)
-          kx[o * (HSP / 64) + h] =
-              load16_if(from + 8 * o * D + 64 * h, page >= 0 && 64 * h + 16 * (lane >> 3) < D);
-      if (w == 0) {  // the factors: lanes 0..3, a group of 16 tokens each
-        const long long unit = static_cast<long long>(pages) * a.v.heads + u.head;
-        f_k = __uint_as_float(load4_if(a.v.scale[0] + unit, pages >= 0, 0x3F800000u));
-        f_v = __uint_as_float(load4_if(a.v.scale[1] + unit, pages >= 0, 0u));  // 0 masks the 16
-      }
+    // Lanes that copy: the first of each page's groups in the tile.
+    const int groups = min(P, kTile) / 16;  // of a page in a tile
+    const bool copies = lane < 4 && lane % groups == 0;
+    const uint32_t copy_bytes = static_cast<uint32_t>(groups) * 16u * D;
+    auto copy = [&](const Unit& u, int j, int page, int which, uint32_t to, uint32_t bar) {
+      const int tok = tile_token(u, j) + 16 * lane;
+      const uint8_t* from = a.v.codes[which] +
+                            (static_cast<long long>(page) * a.v.heads + u.head) * page_bytes +
+                            (tok & page_mask) * D;
+      bulk_load(to + 16 * lane * D, from, copy_bytes, bar);
     };
-    auto load_v = [&](const Unit& u, int j, int pages) {
-      const int tok = tile_token(u, j) + vt;
-      const int page = __shfl_sync(0xFFFFFFFFu, pages, vt >> 4);
-      const uint8_t* from =
-          a.v.codes[1] + (static_cast<long long>(page) * a.v.heads + u.head) * page_bytes +
-          ((tok & page_mask) * D + vd);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const bool in = page >= 0 && tok + i < u.q.length && vd < D;
-        if constexpr (kLaneVBytes == 8) {
-          const uint2 x = load8_if(from + i * D, in);
-          vx[i][0] = x.x;
-          vx[i][1] = x.y;
-        } else {
-          vx[i][0] = load4_if(from + i * D, in, 0u);
-        }
-      }
-    };
-
     for (uint32_t k = 0; ok; ++k) {
       Unit u;
       if (k == 0 && lane == 0) mbar_arrive(u_want);
@@ -697,92 +775,66 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(u_want);
         continue;
       }
-      int pages = pages_of(u, 0, entries_of(u, 0));
-      int entry = n > 1 ? entries_of(u, 1) : -1;
-      load_k(u, 0, pages);
-      // slot j: K of tile j + 1, V of tile j
+      int page_v = -1;                                 // of tile j
+      int page = pages_of(u, 0, entries_of(u, 0));     // of tile j + 1
+      int entry = n > 1 ? entries_of(u, 1) : -1;       // of tile j + 2
+      float f_k = 1.0f, f_v = 0.0f;                    // scales of tile j + 1
+      auto load_scales = [&]() {
+        f_k = 1.0f;
+        f_v = 0.0f;  // log2: -inf, which masks the 16 tokens
+        if (page >= 0) {
+          const long long unit = static_cast<long long>(page) * a.v.heads + u.head;
+          f_k = __ldg(a.v.scale[0] + unit);
+          f_v = __ldg(a.v.scale[1] + unit);
+        }
+      };
+      load_scales();
       for (int j = -1; j < n; ++j, ++it) {
-        const uint32_t slot = it % kSlots;
+        const uint32_t rs = it % kRawSlots;
         if (j == ask && lane == 0) mbar_arrive(u_want);
-        if (!mbar_wait_warp_inline(empty(slot), ((it / kSlots) & 1u) ^ 1u, wd, kSiteLoaderEmpty)) {
+        if (!mbar_wait_warp_inline(raw_empty(rs), ((it / kRawSlots) & 1u) ^ 1u, wd,
+                                   kSiteProducerEmpty)) {
           ok = false;
           break;
         }
-        if (j + 1 < n) {
-          if (w == 0 && lane < 4)
-            factors[((tiles + j + 1) % kFactorSlots) * 4 + lane] =
-                Factor{a.scale_log2 * f_k, __log2f(f_v),
-                       f_v > 0.0f ? __fdividef(1.0f, f_v) : 0.0f, 0.0f};
-          const uint32_t ks = base + L::kK + slot * L::kKBytes;
-#pragma unroll
-          for (int o = 0; o < 2; ++o) {
-            const uint32_t row = 16 * w + 8 * o + (lane & 7);
-#pragma unroll
-            for (int h = 0; h < HSP / 64; ++h) {
-              const uint32_t* c = reinterpret_cast<const uint32_t*>(&kx[o * (HSP / 64) + h]);
-              uint32_t y[8];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                if constexpr (kBf16) codes4_to_bf162x2<kFormat>(c[i], y[2 * i], y[2 * i + 1]);
-                else codes4_to_half2x2<kFormat>(c[i], y[2 * i], y[2 * i + 1]);
-              }
-              const uint32_t at = ks + h * (kTile * 128) + row * 128;
-              const uint32_t unit = 2 * (lane >> 3);
-              st_shared16(at + ((unit ^ (row & 7)) << 4), y);
-              st_shared16(at + (((unit + 1) ^ (row & 7)) << 4), y + 4);
-            }
-          }
-        }
-        if (j >= 0) {
-          const uint32_t vs = base + L::kV + slot * L::kVBytes;
-#pragma unroll
-          for (int c = 0; c < kLaneVBytes / 4; ++c) {
-            // eight tokens of four elements: pairs of tokens, then rows of V^T
-            uint32_t y[4][4];
-#pragma unroll
-            for (int p = 0; p < 4; ++p) {
-              uint32_t x0 = vx[2 * p][c], x1 = vx[2 * p + 1][c];
-              if (kFormat == CSA_KV_INT8) {
-                x0 ^= 0x80808080u;
-                x1 ^= 0x80808080u;
-              }
-              const uint32_t lo = byte_perm(x0, x1, 0x5140), hi = byte_perm(x0, x1, 0x7362);
-              if (kFormat == CSA_KV_INT8) {
-                y[0][p] = flipped_pair_to_half2<0x4140>(lo);
-                y[1][p] = flipped_pair_to_half2<0x4342>(lo);
-                y[2][p] = flipped_pair_to_half2<0x4140>(hi);
-                y[3][p] = flipped_pair_to_half2<0x4342>(hi);
-              } else {
-                y[0][p] = e4m3x2_to_half2(lo & 0xFFFFu);
-                y[1][p] = e4m3x2_to_half2(lo >> 16);
-                y[2][p] = e4m3x2_to_half2(hi & 0xFFFFu);
-                y[3][p] = e4m3x2_to_half2(hi >> 16);
-              }
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t row = vd + 4 * c + e;
-              st_shared16(vs + row * 128 + (((lane & 7) ^ (row & 7)) << 4), y[e]);
-            }
-          }
-        }
-        fence_proxy_async_smem();
+        const bool k_here = j + 1 < n && page >= 0, v_here = page_v >= 0;
+        const uint32_t k_mask = __ballot_sync(0xFFFFFFFFu, k_here && lane < 4);
+        const uint32_t v_mask = __ballot_sync(0xFFFFFFFFu, v_here && lane < 4);
+        const uint32_t n_copies = __popc(__ballot_sync(0xFFFFFFFFu, k_here && copies)) +
+                                  __popc(__ballot_sync(0xFFFFFFFFu, v_here && copies));
+        if (j + 1 < n && lane < 4)
+          factors[((tiles + j + 1) % kFactorSlots) * 4 + lane] =
+              Factor{a.scale_log2 * f_k, __log2f(f_v), f_v > 0.0f ? __fdividef(1.0f, f_v) : 0.0f,
+                     0.0f};
+        if (lane == 0) raw_pages[rs] = k_mask | v_mask << 4;
         __syncwarp();
         if (a.inject && !injected) {
-          injected = true;  // withhold the CTA's first K tile: the issuers' wait runs out
-        } else if (lane == 0) {
-          mbar_arrive(full(slot));
+          injected = true;  // withhold the CTA's first slot: the conversion's wait runs out
+        } else {
+          if (lane == 0) mbar_arrive_expect_tx(raw_full(rs), n_copies * copy_bytes);
+          __syncwarp();
+          const uint32_t to = base + L::kRaw + rs * 2 * L::kRawBytes;
+          if (k_here && copies) copy(u, j + 1, page, 0, to, raw_full(rs));
+          if (v_here && copies) copy(u, j, page_v, 1, to + L::kRawBytes, raw_full(rs));
         }
-        // the next slot's codes: V of tile j + 1, K of tile j + 2
-        if (j + 1 < n) load_v(u, j + 1, pages);
-        if (j + 2 < n) {
-          pages = pages_of(u, j + 2, entry);
-          load_k(u, j + 2, pages);
-          if (j + 3 < n) entry = entries_of(u, j + 3);
-        }
+        page_v = j + 1 < n ? page : -1;
+        page = j + 2 < n ? pages_of(u, j + 2, entry) : -1;
+        entry = j + 3 < n ? entries_of(u, j + 3) : -1;
+        load_scales();
       }
       tiles += n;
     }
+    // Copies in flight (after a wait that ran out: otherwise the conversion has seen
+    // them all) land before shared memory goes away.
+    if (lane == 0 && *abort_flag) {
+      for (uint32_t i = it > kRawSlots ? it - kRawSlots : (injected ? 1u : 0u); i < it; ++i) {
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_test(raw_full(i % kRawSlots), (i / kRawSlots) & 1u) &&
+               globaltimer_ns() - t0 < a.wait_limit_ns) {
+        }
+      }
+    }
+    __syncwarp();
   } else if (warp == kListWarp) {
     // --------------------------------------------------------------- list --
     if (lane == 0) {
