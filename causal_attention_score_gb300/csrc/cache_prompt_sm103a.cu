@@ -6,13 +6,11 @@
 // sequence: two groups A and B of 128, each a TMEM accumulator's lanes, which
 // share every tile of 64 keys. One CTA per SM takes units from a counter
 // (longest first within a sequence), with 16 warps:
-//  - warps 0..7: softmax, warps 0..3 group A, 4..7 group B, a thread a row. Per 32
-//    keys: scores from TMEM (the next 32 on their way), x - m, their maximum, and
-//    the weights exp2(x - m) as fp16 over S (P, the second product's A operand in
-//    TMEM). m is raised only when a value passes m + 8; then the thread's O row,
-//    its l and the tile's weights so far are rescaled. The loop is not unrolled:
-//    with separate code for each part of a tile and for edges a quarter of the
-//    cycles went to waiting for instructions. Before a unit they copy Q's rows to
+//  - warps 0..7: softmax, warps 0..3 group A, 4..7 group B, a thread a row. Per
+//    tile: scores from TMEM, x - m, their maximum, and the weights exp2(x - m) as
+//    fp16 over S (P, the second product's A operand in TMEM), all 64 of a row in
+//    registers at once. m is raised only when a value passes m + 8; then the
+//    thread's O row and its l are rescaled. Before a unit they copy Q's rows to
 //    shared memory; after it they write O / l.
 //  - warps 8..11: conversion, from raw codes in shared memory to the
 //    128-byte-swizzle K-major layout, K as [token][element] in Q's type, V
@@ -68,7 +66,6 @@ constexpr int kRows = 128;          // per group
 constexpr int kUnitRows = 2 * kRows;
 constexpr int kTile = 64;           // keys per step
 constexpr int kSlots = 3;           // of the ring of converted keys and values
-constexpr int kRawSlots = 2;        // of the ring of codes
 constexpr int kFactorSlots = 8;     // tiles whose factors are kept
 constexpr int kUnitSlots = 2;
 constexpr int kAskAhead = 12;       // tiles before a unit's end when the next is asked for
@@ -111,11 +108,12 @@ struct Layout {
   static constexpr int kKBytes = kTile * HSP * 2;  // per slot: [HSP / 64][64 rows][128 B]
   static constexpr int kVBytes = HSP * kTile * 2;  // per slot: [HSP rows][128 B]
   static constexpr int kRawBytes = kTile * HSP;    // K's or V's codes: [64 tokens][head_size]
+  static constexpr int kRawSlots = HSP == 64 ? 4 : 2;  // of the ring of codes: what fits
   static constexpr int kQ = 0, kK = 2 * kQBytes, kV = kK + kSlots * kKBytes,
                        kRaw = kV + kSlots * kVBytes,
                        kFactors = kRaw + kRawSlots * 2 * kRawBytes,
                        kBars = kFactors + kFactorSlots * 4 * static_cast<int>(sizeof(Factor)),
-                       kMisc = kBars + 8 * 32, kUnits = kMisc + 16,
+                       kMisc = kBars + 8 * 36, kUnits = kMisc + 32,
                        kTotal = kUnits + kUnitSlots * static_cast<int>(sizeof(Unit));
 };
 
@@ -215,12 +213,11 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       : "memory");
 }
 
-// 32 lanes x consecutive 32-bit columns and a thread's registers: stores without
-// their wait, loads with and (async) without; an async load's registers are valid
-// after tmem_wait_ld_32 on the same array.
+// 32 lanes x 8 consecutive 32-bit columns and a thread's registers, with their waits.
 __device__ __forceinline__ void tmem_st_8cols(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n\t"
+      "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
       : "memory");
 }
@@ -233,43 +230,6 @@ __device__ __forceinline__ void tmem_ld_8cols(uint32_t taddr, uint32_t (&r)[8]) 
       : "r"(taddr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_st_16cols(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_ld_32cols_async(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, "
-      "%20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_wait_ld_32(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
-                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
-                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
-                 "+r"(r[30]), "+r"(r[31])
-               :
-               : "memory");
-}
-__device__ __forceinline__ void tmem_wait_st() {
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
 // Bulk copy global -> shared (16-byte multiples), completing on an mbarrier.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
                                           uint32_t bar) {
@@ -303,8 +263,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t bars = base + L::kBars;
   auto full = [&](uint32_t s) { return bars + 8u * s; };
   auto empty = [&](uint32_t s) { return bars + 8u * (4 + s); };
+  constexpr int kRawSlots = L::kRawSlots;
   auto raw_full = [&](uint32_t s) { return bars + 8u * (28 + s); };
-  auto raw_empty = [&](uint32_t s) { return bars + 8u * (30 + s); };
+  auto raw_empty = [&](uint32_t s) { return bars + 8u * (32 + s); };
   auto q_ready = [&](uint32_t g) { return bars + 8u * (8 + g); };
   auto s_full = [&](uint32_t g, uint32_t b) { return bars + 8u * (10 + 2 * g + b); };
   auto p_ready = [&](uint32_t g, uint32_t b) { return bars + 8u * (14 + 2 * g + b); };
@@ -319,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::kMisc + 4);
   Factor* factors = reinterpret_cast<Factor*>(gbase + L::kFactors);
   // Bit i: the 16 tokens i of a raw slot's K (bits 4..7: V) have a page.
-  volatile uint32_t* raw_pages = reinterpret_cast<volatile uint32_t*>(gbase + L::kMisc + 8);
+  volatile uint32_t* raw_pages = reinterpret_cast<volatile uint32_t*>(gbase + L::kMisc + 16);
   const Watchdog wd{a.wait_limit_ns, a.status, abort_flag};
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
@@ -458,100 +419,84 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int last = pos - tb;
         const int first_window = a.window ? last - a.window + 1 : -kTile;
         const int sink_cols = a.window ? a.sinks - tb : 0;
-        uint32_t x[32], next[32];
-        tmem_ld_32cols_async(s_tmem, next);
-#pragma unroll 1
-        for (int h = 0; h < kTile / 32; ++h) {
-          tmem_wait_ld_32(next);
+        const bool fresh = m == kNothing;  // nothing seen yet: the first value sets m
+        const float less = fresh ? 0.0f : m;
+        uint32_t x[kTile];
+        tmem_ld_64cols(s_tmem, x);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = next[i];
-          if (h + 1 < kTile / 32) tmem_ld_32cols_async(s_tmem + 32 * (h + 1), next);
-          const bool fresh = m == kNothing;  // nothing seen yet: the first value sets m
-          const float less = fresh ? 0.0f : m;
+        for (int i = 0; i < kTile / 16; ++i) {
+          const Factor c = fac[i];
+          const float add = c.log2v - less;
+          const uint64_t fk2 = pack_f32x2(c.k, c.k), add2 = pack_f32x2(add, add);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const Factor c = fac[2 * h + i];
-            const float add = c.log2v - less;
-            const uint64_t fk2 = pack_f32x2(c.k, c.k), add2 = pack_f32x2(add, add);
-#pragma unroll
-            for (int e = 16 * i; e < 16 * i + 16; e += 2) {
-              float y0, y1;
-              fma_f32x2(y0, y1, __uint_as_float(x[e]), __uint_as_float(x[e + 1]), fk2, add2);
-              x[e] = __float_as_uint(y0);
-              x[e + 1] = __float_as_uint(y1);
-            }
+          for (int e = 16 * i; e < 16 * i + 16; e += 2) {
+            float y0, y1;
+            fma_f32x2(y0, y1, __uint_as_float(x[e]), __uint_as_float(x[e + 1]), fk2, add2);
+            x[e] = __float_as_uint(y0);
+            x[e + 1] = __float_as_uint(y1);
           }
-          if (edge) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int col = 32 * h + i;
-              if (col > last || (col < first_window && col >= sink_cols))
-                x[i] = __float_as_uint(-INFINITY);
-            }
-          }
-          float top = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < 32; i += 2)
-            top = fmaxf(top, fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])));
-          if (__any_sync(0xFFFFFFFFu, top > (fresh ? -INFINITY : kRaise))) {
-            // (rare) a new maximum: what was computed with the old one is rescaled, which
-            // is O, l and this tile's weights so far
-            tmem_wait_ld_32(next);
-            const float up = fresh ? fmaxf(top, kNothing) : fmaxf(top, 0.0f);
-            const float corr = fresh ? 1.0f : ex2_approx(-up);
-            m = less + up;
-            l *= corr;
-            const float off = fresh && top == -INFINITY ? 0.0f : up;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) - off);
-            uint32_t y[8];
-            if (step > 0) {
-              // O is the product issued last's until that is complete (the one before it
-              // is: this tile's scores were issued later)
-              const uint32_t before = product - 1;
-              if (!mbar_wait_warp_inline(pv_done(g, before & 1u), (before >> 1) & 1u, wd,
-                                         kSiteEpilogueFull))
-                ok = false;
-              tc_fence_after_sync();
-#pragma unroll 1
-              for (int d = 0; d < HSP; d += 8) {
-                tmem_ld_8cols(o_tmem + d, y);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * corr);
-                tmem_st_8cols(o_tmem + d, y);
-              }
-            }
-            tmem_wait_st();
-#pragma unroll 1
-            for (int d = 0; d < 16 * h; d += 8) {
-              tmem_ld_8cols(s_tmem + d, y);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float2 w = __half22float2(*reinterpret_cast<__half2*>(&y[i]));
-                y[i] = half2_of(w.x * corr, w.y * corr);
-              }
-              tmem_st_8cols(s_tmem + d, y);
-            }
-          }
-          uint32_t p[16];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            uint64_t sum = 0;
-#pragma unroll
-            for (int e = 16 * i; e < 16 * i + 16; e += 2) {
-              const float y0 = ex2_approx(__uint_as_float(x[e]));
-              const float y1 = ex2_approx(__uint_as_float(x[e + 1]));
-              sum = add_f32x2(sum, pack_f32x2(y0, y1));
-              p[e / 2] = half2_of(y0, y1);
-            }
-            float s0, s1;
-            unpack_f32x2(sum, s0, s1);
-            l = fmaf(s0 + s1, fac[2 * h + i].inv, l);
-          }
-          // P over S: columns 16 h .., whose scores have been read
-          tmem_st_16cols(s_tmem + 16 * h, p);
         }
-        tmem_wait_st();
+        if (__builtin_expect(edge, 0)) {
+#pragma unroll
+          for (int i = 0; i < kTile; ++i)
+            if (i > last || (i < first_window && i >= sink_cols))
+              x[i] = __float_as_uint(-INFINITY);
+        }
+        float tops[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tops[i] = fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 4]));
+#pragma unroll
+        for (int i = 8; i < kTile; i += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            tops[e] = fmaxf(fmaxf(tops[e], __uint_as_float(x[i + e])), __uint_as_float(x[i + 4 + e]));
+        const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+        if (__builtin_expect(__any_sync(0xFFFFFFFFu, top > (fresh ? -INFINITY : kRaise)), 0)) {
+          // (rare) a new maximum: what was computed with the old one, O and l, is rescaled
+          const float up = fresh ? fmaxf(top, kNothing) : fmaxf(top, 0.0f);
+          const float corr = fresh ? 1.0f : ex2_approx(-up);
+          m = less + up;
+          l *= corr;
+          const float off = fresh && top == -INFINITY ? 0.0f : up;
+#pragma unroll
+          for (int i = 0; i < kTile; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) - off);
+          if (step > 0) {
+            // O is the product issued last's until that is complete (the one before it
+            // is: this tile's scores were issued later)
+            const uint32_t before = product - 1;
+            if (!mbar_wait_warp_inline(pv_done(g, before & 1u), (before >> 1) & 1u, wd,
+                                       kSiteEpilogueFull))
+              ok = false;
+            tc_fence_after_sync();
+#pragma unroll 1
+            for (int d = 0; d < HSP; d += 8) {
+              uint32_t y[8];
+              tmem_ld_8cols(o_tmem + d, y);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * corr);
+              tmem_st_8cols(o_tmem + d, y);
+            }
+          }
+        }
+        // Weights, as fp16 over S (whose scores have all been read)
+#pragma unroll
+        for (int i = 0; i < kTile / 16; ++i) {
+          uint64_t sum = 0;
+#pragma unroll
+          for (int e = 16 * i; e < 16 * i + 16; e += 2) {
+            const float y0 = ex2_approx(__uint_as_float(x[e]));
+            const float y1 = ex2_approx(__uint_as_float(x[e + 1]));
+            sum = add_f32x2(sum, pack_f32x2(y0, y1));
+            x[e / 2] = half2_of(y0, y1);
+          }
+          float s0, s1;
+          unpack_f32x2(sum, s0, s1);
+          l = fmaf(s0 + s1, fac[i].inv, l);
+        }
+        uint32_t p[kTile / 2];
+#pragma unroll
+        for (int i = 0; i < kTile / 2; ++i) p[i] = x[i];
+        tmem_st_32cols(s_tmem, p);
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(p_ready(g, buffer));
@@ -684,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 vx[i][0] = *reinterpret_cast<const uint32_t*>(from);
               }
             }
-            if (have < 8) {
+            if (__builtin_expect(have < 8, 0)) {
 #pragma unroll
               for (int i = 0; i < 8; ++i)
 #pragma unroll
@@ -775,20 +720,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(u_want);
         continue;
       }
-      int page_v = -1;                                 // of tile j
-      int page = pages_of(u, 0, entries_of(u, 0));     // of tile j + 1
-      int entry = n > 1 ? entries_of(u, 1) : -1;       // of tile j + 2
-      float f_k = 1.0f, f_v = 0.0f;                    // scales of tile j + 1
-      auto load_scales = [&]() {
-        f_k = 1.0f;
-        f_v = 0.0f;  // log2: -inf, which masks the 16 tokens
-        if (page >= 0) {
-          const long long unit = static_cast<long long>(page) * a.v.heads + u.head;
-          f_k = __ldg(a.v.scale[0] + unit);
-          f_v = __ldg(a.v.scale[1] + unit);
-        }
+      // A pipeline over the tiles, as each stage waits for the one before: the table's
+      // entry (read), the page (checked), its scales (read), the copy.
+      int page_v = -1;                              // of tile j
+      int page = pages_of(u, 0, entries_of(u, 0));  // of tile j + 1
+      int page2 = n > 1 ? pages_of(u, 1, entries_of(u, 1)) : -1;
+      int entry = n > 2 ? entries_of(u, 2) : -1;    // of tile j + 3
+      struct Scales {
+        float k, v;
       };
-      load_scales();
+      auto scales_of = [&](int pg) {
+        Scales f{1.0f, 0.0f};  // log2 of 0: -inf, which masks the 16 tokens
+        if (pg >= 0) {
+          const long long unit = static_cast<long long>(pg) * a.v.heads + u.head;
+          f.k = __ldg(a.v.scale[0] + unit);
+          f.v = __ldg(a.v.scale[1] + unit);
+        }
+        return f;
+      };
+      Scales f = scales_of(page), f2 = scales_of(page2);
       for (int j = -1; j < n; ++j, ++it) {
         const uint32_t rs = it % kRawSlots;
         if (j == ask && lane == 0) mbar_arrive(u_want);
@@ -804,7 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                   __popc(__ballot_sync(0xFFFFFFFFu, v_here && copies));
         if (j + 1 < n && lane < 4)
           factors[((tiles + j + 1) % kFactorSlots) * 4 + lane] =
-              Factor{a.scale_log2 * f_k, __log2f(f_v), f_v > 0.0f ? __fdividef(1.0f, f_v) : 0.0f,
+              Factor{a.scale_log2 * f.k, __log2f(f.v), f.v > 0.0f ? __fdividef(1.0f, f.v) : 0.0f,
                      0.0f};
         if (lane == 0) raw_pages[rs] = k_mask | v_mask << 4;
         __syncwarp();
@@ -818,9 +768,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (v_here && copies) copy(u, j, page_v, 1, to + L::kRawBytes, raw_full(rs));
         }
         page_v = j + 1 < n ? page : -1;
-        page = j + 2 < n ? pages_of(u, j + 2, entry) : -1;
-        entry = j + 3 < n ? entries_of(u, j + 3) : -1;
-        load_scales();
+        page = page2;
+        f = f2;
+        page2 = j + 3 < n ? pages_of(u, j + 3, entry) : -1;
+        f2 = scales_of(page2);
+        entry = j + 4 < n ? entries_of(u, j + 4) : -1;
       }
       tiles += n;
     }
