@@ -66,7 +66,7 @@ constexpr int kRows = 128;          // per group
 constexpr int kUnitRows = 2 * kRows;
 constexpr int kTile = 64;           // keys per step
 constexpr int kSlots = 3;           // of the ring of converted keys and values
-constexpr int kFactorSlots = 8;     // tiles whose factors are kept
+constexpr int kFactorSlots = 16;    // tiles whose factors are kept (more than are in the rings)
 constexpr int kUnitSlots = 2;
 constexpr int kAskAhead = 12;       // tiles before a unit's end when the next is asked for
 constexpr int kTmemCols = 512;      // S_A (two buffers), S_B, O_A, O_B
@@ -108,7 +108,7 @@ struct Layout {
   static constexpr int kKBytes = kTile * HSP * 2;  // per slot: [HSP / 64][64 rows][128 B]
   static constexpr int kVBytes = HSP * kTile * 2;  // per slot: [HSP rows][128 B]
   static constexpr int kRawBytes = kTile * HSP;    // K's or V's codes: [64 tokens][head_size]
-  static constexpr int kRawSlots = HSP == 64 ? 4 : 2;  // of the ring of codes: what fits
+  static constexpr int kRawSlots = HSP == 64 ? 4 : 3;  // of the ring of codes: what fits
   static constexpr int kQ = 0, kK = 2 * kQBytes, kV = kK + kSlots * kKBytes,
                        kRaw = kV + kSlots * kVBytes,
                        kFactors = kRaw + kRawSlots * 2 * kRawBytes,
@@ -702,13 +702,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Lanes that copy: the first of each page's groups in the tile.
     const int groups = min(P, kTile) / 16;  // of a page in a tile
     const bool copies = lane < 4 && lane % groups == 0;
+    const uint32_t copy_mask = __ballot_sync(0xFFFFFFFFu, copies);
     const uint32_t copy_bytes = static_cast<uint32_t>(groups) * 16u * D;
-    auto copy = [&](const Unit& u, int j, int page, int which, uint32_t to, uint32_t bar) {
-      const int tok = tile_token(u, j) + 16 * lane;
-      const uint8_t* from = a.v.codes[which] +
-                            (static_cast<long long>(page) * a.v.heads + u.head) * page_bytes +
-                            (tok & page_mask) * D;
-      bulk_load(to + 16 * lane * D, from, copy_bytes, bar);
+    auto part_of = [&](const Unit& u, int j, int page, int which) {  // of a page: this lane's
+      return a.v.codes[which] + (static_cast<long long>(page) * a.v.heads + u.head) * page_bytes +
+             ((tile_token(u, j) + 16 * lane) & page_mask) * D;
     };
     for (uint32_t k = 0; ok; ++k) {
       Unit u;
@@ -741,31 +739,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       Scales f = scales_of(page), f2 = scales_of(page2);
       for (int j = -1; j < n; ++j, ++it) {
         const uint32_t rs = it % kRawSlots;
+        // Everything is worked out before the slot is free.
+        const bool k_here = j + 1 < n && page >= 0, v_here = page_v >= 0;
+        const uint32_t here = __ballot_sync(0xFFFFFFFFu, k_here && lane < 4) |
+                              __ballot_sync(0xFFFFFFFFu, v_here && lane < 4) << 4;
+        const uint32_t bytes = copy_bytes * (__popc(here & copy_mask) + __popc(here >> 4 & copy_mask));
+        const uint8_t* k_from = part_of(u, j + 1, page, 0);
+        const uint8_t* v_from = part_of(u, j, page_v, 1);
+        const uint32_t to = base + L::kRaw + rs * 2 * L::kRawBytes + 16 * lane * D;
+        if (j + 1 < n && lane < 4)
+          factors[((tiles + j + 1) % kFactorSlots) * 4 + lane] =
+              Factor{a.scale_log2 * f.k, __log2f(f.v), f.v > 0.0f ? __fdividef(1.0f, f.v) : 0.0f,
+                     0.0f};
         if (j == ask && lane == 0) mbar_arrive(u_want);
         if (!mbar_wait_warp_inline(raw_empty(rs), ((it / kRawSlots) & 1u) ^ 1u, wd,
                                    kSiteProducerEmpty)) {
           ok = false;
           break;
         }
-        const bool k_here = j + 1 < n && page >= 0, v_here = page_v >= 0;
-        const uint32_t k_mask = __ballot_sync(0xFFFFFFFFu, k_here && lane < 4);
-        const uint32_t v_mask = __ballot_sync(0xFFFFFFFFu, v_here && lane < 4);
-        const uint32_t n_copies = __popc(__ballot_sync(0xFFFFFFFFu, k_here && copies)) +
-                                  __popc(__ballot_sync(0xFFFFFFFFu, v_here && copies));
-        if (j + 1 < n && lane < 4)
-          factors[((tiles + j + 1) % kFactorSlots) * 4 + lane] =
-              Factor{a.scale_log2 * f.k, __log2f(f.v), f.v > 0.0f ? __fdividef(1.0f, f.v) : 0.0f,
-                     0.0f};
-        if (lane == 0) raw_pages[rs] = k_mask | v_mask << 4;
-        __syncwarp();
         if (a.inject && !injected) {
           injected = true;  // withhold the CTA's first slot: the conversion's wait runs out
         } else {
-          if (lane == 0) mbar_arrive_expect_tx(raw_full(rs), n_copies * copy_bytes);
+          if (lane == 0) {
+            raw_pages[rs] = here;
+            mbar_arrive_expect_tx(raw_full(rs), bytes);
+          }
           __syncwarp();
-          const uint32_t to = base + L::kRaw + rs * 2 * L::kRawBytes;
-          if (k_here && copies) copy(u, j + 1, page, 0, to, raw_full(rs));
-          if (v_here && copies) copy(u, j, page_v, 1, to + L::kRawBytes, raw_full(rs));
+          if (k_here && copies) bulk_load(to, k_from, copy_bytes, raw_full(rs));
+          if (v_here && copies) bulk_load(to + L::kRawBytes, v_from, copy_bytes, raw_full(rs));
         }
         page_v = j + 1 < n ? page : -1;
         page = page2;
