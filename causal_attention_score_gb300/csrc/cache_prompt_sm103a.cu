@@ -10,8 +10,8 @@
 //    tile: scores from TMEM, x - m, their maximum, and the weights exp2(x - m) as
 //    fp16 over S (P, the second product's A operand in TMEM), all 64 of a row in
 //    registers at once. m is raised only when a value passes m + 8; then the
-//    thread's O row and its l are rescaled. Before a unit they copy Q's rows to
-//    shared memory; after it they write O / l.
+//    thread's O row and its l are rescaled. They copy a unit's Q
+//    to shared memory before they write the last one's O / l.
 //  - warps 8..11: conversion, from raw codes in shared memory to the
 //    128-byte-swizzle K-major layout, K as [token][element] in Q's type, V
 //    transposed in registers to [element][token] in fp16 (both exact). A slot of
@@ -117,14 +117,16 @@ struct Layout {
                        kTotal = kUnits + kUnitSlots * static_cast<int>(sizeof(Unit));
 };
 
-// The list's u-th unit: sequences in order, the last (longest) rows first.
+// The list's u-th unit: sequences by their longest unit, the longest first (up to
+// kThreads of them; more keep their order), within a sequence the last rows, which see
+// the most keys, first.
 __device__ __forceinline__ long long units_of(const PromptArgs& a, const KvSequence& q) {
   const long long rows = static_cast<long long>(q.n) * a.group;
   return rows <= a.row_limit ? 0 : (rows + kUnitRows - 1) / kUnitRows * a.v.heads;
 }
 
-__device__ Unit decode_unit(const PromptArgs& a, const long long* prefix, int per,
-                                            long long u) {
+__device__ Unit decode_unit(const PromptArgs& a, const long long* prefix, const int* order,
+                            int per, long long u) {
   int lo = 0, hi = kThreads;
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
@@ -133,13 +135,11 @@ __device__ Unit decode_unit(const PromptArgs& a, const long long* prefix, int pe
   }
   Unit r;
   long long base = prefix[lo];
-  r.s = lo * per;
-  for (;;) {
+  for (r.s = per == 1 ? order[lo] : lo * per;; ++r.s) {
     r.q = kv_sequence(a.v, r.s);
     const long long n = units_of(a, r.q);
-    if (u < base + n) break;
+    if (per == 1 || u < base + n) break;
     base += n;
-    ++r.s;
   }
   const int all_rows = static_cast<int>(static_cast<long long>(r.q.n) * a.group);
   const int blocks = (all_rows + kUnitRows - 1) / kUnitRows;
@@ -213,12 +213,23 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       : "memory");
 }
 
-// 32 lanes x 8 consecutive 32-bit columns and a thread's registers, with their waits.
+// 32 lanes x 8 or 16 consecutive 32-bit columns and a thread's registers, with their waits.
 __device__ __forceinline__ void tmem_st_8cols(uint32_t taddr, const uint32_t (&r)[8]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n\t"
       "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_16cols(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
       : "memory");
 }
 __device__ __forceinline__ void tmem_ld_8cols(uint32_t taddr, uint32_t (&r)[8]) {
@@ -257,6 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ long long s_prefix[kThreads + 1];
   __shared__ long long s_warp[kThreads / 32];
+  __shared__ int s_order[kThreads], s_keys[kThreads];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - raw);
@@ -322,9 +334,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int per = (S + kThreads - 1) / kThreads;
   {
     long long mine = 0;
-    const long long from = static_cast<long long>(threadIdx.x) * per;
-    for (long long s = from; s < min(static_cast<long long>(S), from + per); ++s)
-      mine += units_of(a, kv_sequence(a.v, static_cast<int>(s)));
+    if (per == 1) {
+      const int i = threadIdx.x;
+      int key = -1;
+      if (i < S) {
+        const KvSequence q = kv_sequence(a.v, i);
+        if (units_of(a, q) > 0)
+          key = a.window > 0 && a.window < q.length - q.n ? a.window + q.n : q.length;
+      }
+      s_keys[i] = key;
+      __syncthreads();
+      if (i < S) {
+        int rank = 0;
+        for (int o = 0; o < S; ++o) rank += s_keys[o] > key || (s_keys[o] == key && o < i);
+        s_order[rank] = i;
+      }
+      __syncthreads();
+      if (i < S) mine = units_of(a, kv_sequence(a.v, s_order[i]));
+    } else {
+      const long long from = static_cast<long long>(threadIdx.x) * per;
+      for (long long s = from; s < min(static_cast<long long>(S), from + per); ++s)
+        mine += units_of(a, kv_sequence(a.v, static_cast<int>(s)));
+    }
     long long sum = mine;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
@@ -367,30 +398,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t products = 0;            // of the group, before this unit
     uint32_t tiles = 0;               // of the CTA, before this unit (the factors' slots)
     bool ok = true;
-    for (uint32_t k = 0; ok; ++k) {
-      Unit u;
-      if (!take_unit(k, u) || u.n[0] < 0) break;
-      const int n = g == 0 ? u.n[0] : u.n[1];
+    // A unit as this thread's row sees it.
+    struct Row {
+      int token, head, pos;  // row of q and out, head; -1: no such row
+      bool live;
+    };
+    Unit u;
+    Row row;
+    // Takes the k-th unit and copies its Q to shared memory; false: no more units.
+    auto next_unit = [&](uint32_t k) {
+      if (!take_unit(k, u) || u.n[0] < 0) return false;
       const int rr = u.row0 + static_cast<int>(g) * kRows + r;
       const int j_tok = rr / a.group;
-      const int q_row = u.q.row0 + j_tok, q_hd = u.head * a.group + (rr - j_tok * a.group);
-      const bool live = static_cast<int>(g) * kRows + r < u.rows;
-      const int pos = live ? u.q.first + j_tok : -1;
-      float l = 0.0f, m = kNothing;
-      if (n > 0) {
-        // Q's rows to shared memory (the group's last S product is complete: this thread
-        // has seen the end of the product after it)
+      row.live = static_cast<int>(g) * kRows + r < u.rows;
+      row.token = u.q.row0 + j_tok;
+      row.head = u.head * a.group + (rr - j_tok * a.group);
+      row.pos = row.live ? u.q.first + j_tok : -1;
+      if ((g == 0 ? u.n[0] : u.n[1]) > 0) {
 #pragma unroll 4
         for (int i = 0; i < kLanes; ++i) {
           const int from = i * kRowsAtOnce + lane / kLanes;  // row of the warp
-          const int row = __shfl_sync(0xFFFFFFFFu, live ? q_row : -1, from);
-          const int head = __shfl_sync(0xFFFFFFFFu, q_hd, from);
-          const bool in = row >= 0 && piece * 8 < D;
+          const int token = __shfl_sync(0xFFFFFFFFu, row.live ? row.token : -1, from);
+          const int head = __shfl_sync(0xFFFFFFFFu, row.head, from);
+          const bool in = token >= 0 && piece * 8 < D;
           const uint32_t sr = static_cast<uint32_t>((warp & 3) * 32 + from);
           cp_async_16(q_smem + (piece >> 3) * (kRows * 128) + sr * 128 +
                           (((piece & 7) ^ (sr & 7)) << 4),
                       static_cast<const uint16_t*>(a.q) +
-                          (in ? row * a.q_token + head * a.q_head + piece * 8 : 0),
+                          (in ? token * a.q_token + head * a.q_head + piece * 8 : 0),
                       in ? 16u : 0u);
         }
         cp_async_commit();
@@ -399,6 +434,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(q_ready(g));
       }
+      return true;
+    };
+    bool more = next_unit(0);
+    for (uint32_t k = 1; more; ++k) {
+      const int n = g == 0 ? u.n[0] : u.n[1];
+      const bool live = row.live;
+      const int pos = row.pos;
+      float l = 0.0f, m = kNothing;
       const int pos_low = __reduce_min_sync(0xFFFFFFFFu, live ? pos : 0x7FFFFFFF);
       const int pos_high = __reduce_max_sync(0xFFFFFFFFu, pos);
       for (int step = 0; ok && step < n; ++step) {
@@ -504,6 +547,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       products += n;
       tiles += max(u.n[0], u.n[1]);
+      // The next unit's Q takes the place of this one's, whose last scores have been
+      // seen, so that its first scores are computed while O is written.
+      uint16_t* to = static_cast<uint16_t*>(a.out) +
+                     (live ? row.token * a.out_token + row.head * a.out_head : 0);
+      more = next_unit(k);
       if (n > 0) {
         const uint32_t final = products - 1;
         if (!mbar_wait_warp_inline(pv_done(g, final & 1u), (final >> 1) & 1u, wd,
@@ -511,54 +559,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         tc_fence_after_sync();
       }
-      // O / l, through Q's place in shared memory (no product reads that any more)
       const float inv_l = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll 1
-      for (int h = 0; h < HSP / 32; ++h) {
-        uint32_t x[32];
+      for (int d = 0; d < D; d += 16) {
+        uint32_t x[16];
         if (n > 0) {
-          tmem_ld_32cols(o_tmem + 32 * h, x);
+          tmem_ld_16cols(o_tmem + d, x);
         } else {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = 0u;
+          for (int i = 0; i < 16; ++i) x[i] = 0u;
         }
+        uint32_t y[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t y[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float v0 = __uint_as_float(x[8 * i + 2 * e]) * inv_l;
-            float v1 = __uint_as_float(x[8 * i + 2 * e + 1]) * inv_l;
-            if (l == 0.0f) v0 = v1 = 0.0f;
-            if (a.half) {
-              y[e] = half2_of(v0, v1);
-            } else {
-              const __nv_bfloat162 b = __floats2bfloat162_rn(v0, v1);
-              y[e] = *reinterpret_cast<const uint32_t*>(&b);
-            }
+        for (int i = 0; i < 8; ++i) {
+          float v0 = __uint_as_float(x[2 * i]) * inv_l, v1 = __uint_as_float(x[2 * i + 1]) * inv_l;
+          if (l == 0.0f) v0 = v1 = 0.0f;
+          if (kBf16) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(v0, v1);
+            y[i] = *reinterpret_cast<const uint32_t*>(&b);
+          } else {
+            y[i] = half2_of(v0, v1);
           }
-          const int unit = 4 * h + i;
-          st_shared16(q_smem + (unit >> 3) * (kRows * 128) + r * 128 +
-                          (((unit & 7) ^ (r & 7)) << 4),
-                      y);
+        }
+        if (live) {
+          reinterpret_cast<uint4*>(to + d)[0] = make_uint4(y[0], y[1], y[2], y[3]);
+          reinterpret_cast<uint4*>(to + d)[1] = make_uint4(y[4], y[5], y[6], y[7]);
         }
       }
       tc_fence_before_sync();  // O may be overwritten after the next unit's p_ready
-      __syncwarp();
-#pragma unroll 4
-      for (int i = 0; i < kLanes; ++i) {
-        const int from = i * kRowsAtOnce + lane / kLanes;
-        const int row = __shfl_sync(0xFFFFFFFFu, live ? q_row : -1, from);
-        const int head = __shfl_sync(0xFFFFFFFFu, q_hd, from);
-        const uint32_t sr = static_cast<uint32_t>((warp & 3) * 32 + from);
-        const uint4 y = *reinterpret_cast<const uint4*>(
-            gbase + (q_smem - base) + (piece >> 3) * (kRows * 128) + sr * 128 +
-            (((piece & 7) ^ (sr & 7)) << 4));
-        if (row >= 0 && piece * 8 < D)
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + row * a.out_token +
-                                    head * a.out_head + piece * 8) = y;
-      }
-      __syncwarp();
     }
   } else if (warp < kMmaWarp) {
     // --------------------------------------------------------- conversion --
@@ -796,7 +824,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!mbar_wait(u_want, k & 1u, wd, kSiteSched)) break;
         const long long at = atomicAdd(a.counter, 1u);
         Unit u;
-        if (at < total) u = decode_unit(a, s_prefix, per, at);
+        if (at < total) u = decode_unit(a, s_prefix, s_order, per, at);
         else u.n[0] = -1;
         if (!mbar_wait(u_empty(slot), ((k / kUnitSlots) & 1u) ^ 1u, wd, kSiteSched)) break;
         reinterpret_cast<Unit*>(gbase + L::kUnits)[slot] = u;
