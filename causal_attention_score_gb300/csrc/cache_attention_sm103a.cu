@@ -48,6 +48,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <limits>
 #include <string>
 
 #include "csa_internal.h"
@@ -68,8 +69,15 @@ constexpr int kTileTokens = 64 * kSub;
 constexpr int kMaxSms = 152;
 constexpr int kMaxWorkers = kMaxSms * 3;
 constexpr int kMaxRows = 16;
-// Sequences of more rows than this go to the prompt kernel.
-constexpr int kRowLimit = 64;
+// Which kernel a sequence's rows go to. Here each block of 16 rows reads the keys again;
+// the prompt kernel reads them once for 256 rows, but nothing splits its units along the
+// keys. With 8K keys a block of 16 rows of one kv head takes 0.41 us of the whole
+// GPU, 48 rows as much as a unit there (1.18 us) where units fill it; where they do
+// not, its 180 us for the first unit buy this kernel 3 blocks an SM: 1 sequence of 64
+// new tokens (8 rows each, 8 heads) takes 113 us here and 180 us there (64K keys: 808
+// and 1255 us; none: 15 and 23 us), one of 128 tokens 210 and 182 us.
+constexpr int kRowLimit = 48;
+constexpr int kBlocksPerSm = 3;
 constexpr float kRaise = 8.0f;              // the running maximum is raised past this
 // The running maximum of a row that has seen nothing: finite, so that
 // differences of two of them are 0.
@@ -85,6 +93,7 @@ struct AttendArgs {
   int window, sinks;
   float scale_log2;
   int workers;
+  int most_rows;   // of a block
   int row_limit;   // sequences of more rows (tokens x group) are left to another kernel
   int* headers;    // [workers][8]
   unsigned int* counter;  // the prompt kernel's, cleared here
@@ -683,59 +692,55 @@ __global__ void __launch_bounds__(128 * kGroups<NB>, 1)
   if (!left_open && gtid == 0) header[kHeadPieces] = 0;
 }
 
-// Joins the pieces of each unit that was split: the CTA of the worker whose
-// last piece begins the unit. Piece 0 is that worker's second slot, piece i the
-// first slot of worker + i. Warp w takes pieces w, w + 4, ...; the four sums
-// are added in order.
+// Joins the pieces of each unit that was split: row blockIdx.y of the unit that the
+// last piece of worker blockIdx.x begins. Piece 0 is that worker's second slot, piece
+// i the first slot of worker + i. Warp w takes pieces w, w + 4, ...; the four sums are
+// added in order.
 template <int HSP>
 __global__ void __launch_bounds__(128) attend_join_sm103a_kernel(const AttendArgs a) {
   __shared__ float s_o[4][HSP];
   __shared__ float s_l[4], s_m[4];
   grid_dependency_wait();
-  const int worker = blockIdx.x;
+  const int worker = blockIdx.x, r = blockIdx.y;
   const int* header = a.headers + worker * 8;
   const int pieces = header[kHeadPieces];
-  if (pieces == 0) return;
-  const int row0 = header[kHeadRow0], first = header[kHeadFirst], head = header[kHeadHead];
-  const int rows = header[kHeadRows];
+  if (pieces == 0 || r >= header[kHeadRows]) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int E = HSP / 32;
   auto part_of = [&](int i) {
     const int slot = i == 0 ? 2 * worker + 1 : 2 * (worker + i);
     return a.parts + static_cast<long long>(slot) * a.part_floats;
   };
-  for (int r = 0; r < rows; ++r) {
-    float m = kNothing;
-    for (int i = threadIdx.x; i < pieces; i += 128) m = fmaxf(m, part_of(i)[r]);
+  float m = kNothing;
+  for (int i = threadIdx.x; i < pieces; i += 128) m = fmaxf(m, part_of(i)[r]);
 #pragma unroll
-    for (int d = 1; d < 32; d *= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-    if (lane == 0) s_m[warp] = m;
-    __syncthreads();
-    m = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-    float acc[E] = {}, l = 0.0f;
+  for (int d = 1; d < 32; d *= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+  if (lane == 0) s_m[warp] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+  float acc[E] = {}, l = 0.0f;
 #pragma unroll 4
-    for (int i = warp; i < pieces; i += 4) {
-      const float* p = part_of(i);
-      const float c = ex2_approx(p[r] - m);
-      l = fmaf(p[kMaxRows + r], c, l);
+  for (int i = warp; i < pieces; i += 4) {
+    const float* p = part_of(i);
+    const float c = ex2_approx(p[r] - m);
+    l = fmaf(p[kMaxRows + r], c, l);
 #pragma unroll
-      for (int k = 0; k < E; ++k)
-        acc[k] = fmaf(p[2 * kMaxRows + r * HSP + lane * E + k], c, acc[k]);
-    }
-#pragma unroll
-    for (int k = 0; k < E; ++k) s_o[warp][lane * E + k] = acc[k];
-    if (lane == 0) s_l[warp] = l;
-    __syncthreads();
-    const float lt = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
-    const int rr = first + r;
-    const int j = rr / a.group;
-    const int d = threadIdx.x;
-    if (d < a.v.head_size)
-      store_out(a, (row0 + j) * a.out_token + (head * a.group + (rr - j * a.group)) * a.out_head + d,
-                lt == 0.0f ? 0.0f
-                           : ((s_o[0][d] + s_o[1][d]) + (s_o[2][d] + s_o[3][d])) / lt);
-    __syncthreads();
+    for (int k = 0; k < E; ++k)
+      acc[k] = fmaf(p[2 * kMaxRows + r * HSP + lane * E + k], c, acc[k]);
   }
+#pragma unroll
+  for (int k = 0; k < E; ++k) s_o[warp][lane * E + k] = acc[k];
+  if (lane == 0) s_l[warp] = l;
+  __syncthreads();
+  const float lt = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
+  const int rr = header[kHeadFirst] + r;
+  const int j = rr / a.group;
+  const int d = threadIdx.x;
+  if (d < a.v.head_size)
+    store_out(a,
+              (header[kHeadRow0] + j) * a.out_token +
+                  (header[kHeadHead] * a.group + (rr - j * a.group)) * a.out_head + d,
+              lt == 0.0f ? 0.0f : ((s_o[0][d] + s_o[1][d]) + (s_o[2][d] + s_o[3][d])) / lt);
 }
 
 template <int HSP, int NB, int kSub, int kFormat, bool kFull>
@@ -749,8 +754,10 @@ cudaError_t launch_rows(AttendArgs a, int sms, const DeviceInfo& dev, cudaStream
   cudaError_t e = launch_programmatic(kernel, static_cast<unsigned>(sms), 128 * kGroups<NB>, smem,
                                       stream, a);
   if (e != cudaSuccess) return e;
-  return launch_programmatic(attend_join_sm103a_kernel<HSP>, static_cast<unsigned>(a.workers), 128,
-                             0, stream, a);
+  return launch_programmatic(attend_join_sm103a_kernel<HSP>,
+                             dim3(static_cast<unsigned>(a.workers),
+                                  static_cast<unsigned>(std::min(a.most_rows, 8 * NB))),
+                             128, 0, stream, a);
 }
 
 template <int HSP, int NB, int kSub>
@@ -800,14 +807,24 @@ int cache_attention_launch(const csa_kv_cache& cache, const csa_kv_batch& batch,
   a.scale_log2 = static_cast<float>(static_cast<double>(call.scale) * 1.4426950408889634);
   const int sms = std::min(dev.sm_count, kMaxSms);
   a.workers = 0;
-  a.row_limit = kRowLimit;
+  const long long most_rows = static_cast<long long>(batch.max_new) * a.group;
+  const long long batch_rows = static_cast<long long>(batch.rows) * a.group;
+  const bool prompts = most_rows > kRowLimit &&
+                       (batch_rows / 16 + batch.sequences) * cache.heads > kBlocksPerSm * sms;
+  a.row_limit = prompts ? kRowLimit : std::numeric_limits<int>::max();
   const int hsp = padded_head(cache.head_size);
   a.headers = static_cast<int*>(call.workspace);
   a.counter = reinterpret_cast<unsigned int*>(a.headers + kMaxWorkers * 8);
   a.parts = reinterpret_cast<float*>(a.headers + (kMaxWorkers + 1) * 8);
   a.part_floats = 2 * kMaxRows + kMaxRows * hsp;
-  const long long most_rows = static_cast<long long>(batch.max_new) * a.group;
-  const bool one = most_rows <= 8;
+  a.most_rows = static_cast<int>(std::min<long long>(most_rows, kMaxRows));
+  // Rows a block. 16 read the codes of 9 to 16 rows once instead of twice, but cost 8 and
+  // fewer a second product for nothing and a third group of warps: 64 sequences of 16 rows
+  // over 4K tokens take 93 us with 16, 109 us with 8; a batch of 4, 8 and 12 rows takes
+  // 102 us with 16, 81 us with 8. So: 16 where a token alone has more than 8, or where
+  // the batch's average does (prompts, which are another kernel's, left out of it).
+  const bool one = most_rows <= 8 ||
+                   (a.group <= 8 && (prompts || batch_rows <= 8LL * batch.sequences));
   int rc = CSA_OK;
   cudaError_t e;
   if (hsp == 64)
@@ -825,7 +842,7 @@ int cache_attention_launch(const csa_kv_cache& cache, const csa_kv_batch& batch,
     err = std::string("cache_attention_forward: launch: ") + cudaGetErrorString(e);
     return CSA_ERR_LAUNCH;
   }
-  if (most_rows > kRowLimit) {
+  if (prompts) {
     rc = cache_prompt_launch(cache, batch, call, kRowLimit, a.counter, stream, dev, err);
     if (rc != CSA_OK) {
       err = "cache_attention_forward: " + err;

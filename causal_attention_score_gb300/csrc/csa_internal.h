@@ -37,10 +37,10 @@ int set_max_dynamic_smem(const void* kernel, int bytes, int device, std::string&
 // the previous kernel in the stream finishes, and waits for it (griddepcontrol)
 // before it touches global memory.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_programmatic(void (*kernel)(KArgs...), unsigned grid, unsigned block,
-                                size_t smem, cudaStream_t stream, Args&&... args) {
+cudaError_t launch_programmatic(void (*kernel)(KArgs...), dim3 grid, unsigned block, size_t smem,
+                                cudaStream_t stream, Args&&... args) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;

@@ -9,6 +9,18 @@ import serving_ref as ref
 pytestmark = pytest.mark.gpu
 
 
+@pytest.fixture(autouse=True, params=[0, 2], ids=["all_sms", "2_sms"])
+def sms(request):
+    """Every test on the whole GPU, where a short batch has a kernel for few rows, and held
+    to two SMs, where sequences of many rows take the kernel for prompts and every worker
+    has many units."""
+    stream = torch.cuda.current_stream()
+    csa.set_stream_sm_limit(stream, request.param)
+    yield request.param
+    torch.cuda.synchronize()
+    csa.set_stream_sm_limit(stream, 0)
+
+
 def run(b: ref.Batch, Hq, dtype, window=0, sinks=0, scale=None, q=None, q_scale=1.0):
     q = b.rows_of(Hq, dtype, q_scale, seed=11) if q is None else q
     cache, batch = b.device(csa)
@@ -164,7 +176,7 @@ def test_page_order_and_shared_pages():
 
 
 @pytest.mark.parametrize("new,old", [([1, 2], [900, 100]), ([200, 1], [100, 500])])
-def test_repeatable_limited_and_captured(new, old):
+def test_repeatable_limited_and_captured(new, old, sms):
     """Same bits call after call; an SM limit changes no more than the sums' order; a
     captured call follows its inputs and lengths."""
     b = ref.Batch(new, old, 2, 128, 64, "int8", seed=10)
@@ -187,8 +199,12 @@ def test_repeatable_limited_and_captured(new, old):
     ws = torch.empty(csa.cache_attention_workspace_size(cache, batch, 4), dtype=torch.uint8, device="cuda")
     ws.fill_(255)
     graph = torch.cuda.CUDAGraph()
-    with torch.cuda.graph(graph):
-        csa.cache_attention_forward(out, qd, cache, batch, workspace=ws)
+    csa.set_stream_sm_limit(st, sms)
+    try:
+        with torch.cuda.graph(graph, stream=st):
+            csa.cache_attention_forward(out, qd, cache, batch, workspace=ws)
+    finally:
+        csa.set_stream_sm_limit(st, 0)
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, first)

@@ -32,8 +32,18 @@ def reference(qkv, pos, f, mem):
     return ref.attention(rot[:, :Hq], *mem["k"], *mem["v"], [0, n], [L], [list(range(WIDTH))])
 
 
+@pytest.fixture(params=[0, 2], ids=["all_sms", "2_sms"])
+def sms(request):
+    """The whole GPU (few rows for it: one kernel) or two SMs (prompts take the other)."""
+    stream = torch.cuda.current_stream()
+    csa.set_stream_sm_limit(stream, request.param)
+    yield request.param
+    torch.cuda.synchronize()
+    csa.set_stream_sm_limit(stream, 0)
+
+
 @pytest.mark.parametrize("fmt", ["int8", "e4m3"])
-def test_prompt_chunks_then_tokens(fmt):
+def test_prompt_chunks_then_tokens(fmt, sms):
     """Bits of K that round the other way on the GPU move a code by one step at most, so the
     room is that of the derived bound, the output's half step, and of one code in 128 keys;
     the two paths' outputs over the whole run differ by 2^-6 of the values' size at most."""
