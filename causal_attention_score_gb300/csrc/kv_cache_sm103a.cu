@@ -17,11 +17,15 @@
 // 8 bits cost at most 2^-7 of the step. A power of two does the same for e4m3
 // for free, where the step is relative to begin with.
 //
-// Bound: HBM. A write reads the new rows once (two passes over registers: the
-// magnitude, then the codes) and writes one byte an element; older codes of a
-// block are read and written only when its scale grew. A unit of work is one
-// (sequence, page, K or V, head); units of one page's heads are neighbours, so
-// that CTAs running side by side read neighbouring memory of a row.
+// Bound: HBM, with the issue slots close behind (a bf16 element is 3 bytes moved: at
+// the copy rate an SM has 16 instructions' worth of lanes for it), so quotients are
+// computed two at a time (packed fp32) and positions with a multiplication. A write
+// reads the new rows once (two passes over registers: the magnitude, then the codes)
+// and writes one byte an element; older codes of a block are read and written only when
+// its scale grew. A unit of work is one (sequence, page, K or V, head); units of one
+// page's heads are neighbours, so that CTAs running side by side read neighbouring
+// memory of a row. A unit's place (sequence, page) is looked up while the rows of the one
+// before are on their way.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -29,6 +33,7 @@
 #include <algorithm>
 #include <cstdint>
 #include <string>
+#include <type_traits>
 
 #include "csa_internal.h"
 #include "kv_cache.cuh"
@@ -38,11 +43,14 @@ namespace csa {
 namespace {
 
 constexpr int kBlockThreads = 256;
-constexpr int kBlockVecs = 8;  // 8-element vectors a thread holds: 128 tokens x 128 / 256 / 8
-// Sequences of at most this many new tokens take a warp per unit (and up to 4
-// vectors a lane); longer ones a CTA of 256 threads.
+// A unit that is written has one worker, which holds its new rows in registers: a warp
+// (4 vectors of 8 elements a lane) where no sequence has more than 8 new tokens, else as
+// many warps as hold a whole block in 8 vectors a lane, one (16 x 128) to eight
+// (128 x 128). (With 256 threads for every block the lanes without elements took
+// the issue slots: 96 us instead of 57 for 28K tokens of 16 heads of 128.)
 constexpr int kStepTokens = 8;
 constexpr int kStepVecs = 4;
+constexpr int kBlockVecs = 8;
 constexpr float kScaleFloor = 7.888609052210118e-31f;  // 2^-100
 
 struct CacheArgs {
@@ -50,23 +58,38 @@ struct CacheArgs {
   void* x[2];                           // rows of K, V
   long long token[2], head_stride[2];   // their strides in elements
   int touched;                          // most pages a sequence's new tokens lie in
-  long long units;
+  unsigned by_chunks;                   // 2^31 / (8-element chunks of a row), rounded up
+  unsigned step_s;                      // gridDim.x * workers of a CTA, in units:
+  int step_j, step_which, step_h;       //   sequences, pages, K or V, heads
 };
+
+// e / chunks: exact while e * chunks < 2^31 (both stay below 2^13).
+__device__ __forceinline__ int row_of(const CacheArgs& a, int e) {
+  return static_cast<int>(__umulhi(2u * static_cast<unsigned>(e), a.by_chunks));
+}
 
 struct Unit {
-  int s, j, which, h;
+  unsigned s;
+  int j, which, h;
 };
 
-__device__ __forceinline__ Unit decode_unit(const CacheArgs& a, long long u) {
+__device__ __forceinline__ Unit first_unit(const CacheArgs& a, unsigned u) {
   Unit r;
-  const int H = a.v.heads;
-  const long long q = u / H;
-  r.h = static_cast<int>(u - q * H);
+  const unsigned q = u / a.v.heads;
+  r.h = static_cast<int>(u - q * a.v.heads);
   r.which = static_cast<int>(q & 1);
-  const long long p = q >> 1;
-  r.s = static_cast<int>(p / a.touched);
-  r.j = static_cast<int>(p - static_cast<long long>(r.s) * a.touched);
+  r.s = (q >> 1) / a.touched;
+  r.j = static_cast<int>((q >> 1) - r.s * a.touched);
   return r;
+}
+__device__ __forceinline__ void next_unit(const CacheArgs& a, Unit& u) {
+  u.h += a.step_h;
+  u.which += a.step_which;
+  u.j += a.step_j;
+  u.s += a.step_s;
+  if (u.h >= a.v.heads) u.h -= a.v.heads, ++u.which;
+  if (u.which >= 2) u.which -= 2, ++u.j;
+  if (u.j >= a.touched) u.j -= a.touched, ++u.s;
 }
 
 // The part of a sequence's rows that lies in its j-th page from the first that
@@ -96,6 +119,20 @@ template <>
 __device__ __forceinline__ float to_float<__half>(uint32_t b) {
   return __half2float(__ushort_as_half(static_cast<unsigned short>(b)));
 }
+// Both values of a word.
+template <typename T>
+__device__ __forceinline__ void to_float2(uint32_t w, float& lo, float& hi);
+template <>
+__device__ __forceinline__ void to_float2<__nv_bfloat16>(uint32_t w, float& lo, float& hi) {
+  lo = __uint_as_float(w << 16);
+  hi = __uint_as_float(w & 0xFFFF0000u);
+}
+template <>
+__device__ __forceinline__ void to_float2<__half>(uint32_t w, float& lo, float& hi) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  lo = f.x;
+  hi = f.y;
+}
 template <typename T>
 constexpr uint32_t kInfBits = 0x7F80u;
 template <>
@@ -114,21 +151,26 @@ __device__ __forceinline__ float scale_of(float m) {
   return e < -100 ? kScaleFloor : __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-// x / s correctly rounded: r is 1 / s to nearest, and one Newton correction of
-// the quotient x * r gives the rounded quotient (Markstein, 1990).
-__device__ __forceinline__ float quotient(float x, float s, float r) {
-  const float y = x * r;
-  return fmaf(fmaf(-y, s, x), r, y);
-}
-
+// x / s correctly rounded, two at a time: r is 1 / s to nearest, and one Newton
+// correction of the quotient x * r gives the rounded quotient (Markstein, 1990).
 // Four values (finite, within 127 s or 448 s) as codes.
 template <int kFormat>
 __device__ __forceinline__ uint32_t codes4(const float (&x)[4], float s, float r) {
   if (kFormat == CSA_KV_INT8) {
+    const uint64_t r2 = pack_f32x2(r, r), s2 = pack_f32x2(-s, -s);
+    // 1.5 * 2^23 + code: the code is the low byte
+    const uint64_t magic = pack_f32x2(12582912.0f, 12582912.0f);
     uint32_t b[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)  // 1.5 * 2^23 + code: the code is the low byte
-      b[i] = __float_as_uint(quotient(x[i], s, r) + 12582912.0f);
+    for (int i = 0; i < 4; i += 2) {
+      const uint64_t v = pack_f32x2(x[i], x[i + 1]);
+      const uint64_t y = mul_f32x2(v, r2);
+      const uint64_t q = fma_f32x2(fma_f32x2(y, s2, v), r2, y);
+      float lo, hi;
+      unpack_f32x2(add_f32x2(q, magic), lo, hi);
+      b[i] = __float_as_uint(lo);
+      b[i + 1] = __float_as_uint(hi);
+    }
     return byte_perm(byte_perm(b[0], b[1], 0x0040), byte_perm(b[2], b[3], 0x0040), 0x5410);
   }
   return e4m3x2_from_float2(x[0] * r, x[1] * r) | (e4m3x2_from_float2(x[2] * r, x[3] * r) << 16);
@@ -149,42 +191,65 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// kThreads = 32: a warp is the worker (kStepVecs vectors a lane); else the CTA.
-template <typename T, int kFormat, int kThreads>
+// Where a unit's rows and codes are; page < 0: it has nothing to do.
+struct Place {
+  Part p;
+  int page;
+};
+__device__ __forceinline__ Place place_of(const CacheArgs& a, const Unit& u) {
+  Place r;
+  r.page = -1;
+  if (u.s >= static_cast<unsigned>(a.v.sequences)) return r;
+  const KvSequence q = kv_sequence(a.v, u.s);
+  if (part_of(a.v, q, u.j, r.p)) r.page = kv_page(a.v, u.s, r.p.block);
+  return r;
+}
+
+template <int kThreads>
+__device__ __forceinline__ void worker_sync(int worker) {
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + worker), "n"(kThreads) : "memory");
+}
+
+// kThreads are a worker, NV the vectors that each holds.
+template <typename T, int kFormat, int kThreads, int NV>
 __global__ void __launch_bounds__(kBlockThreads) cache_write_sm103a_kernel(const CacheArgs a) {
   grid_dependency_wait();
-  constexpr int NV = kThreads == 32 ? kStepVecs : kBlockVecs;
+  constexpr int kWorkers = kBlockThreads / kThreads;
   __shared__ uint32_t s_max[kBlockThreads / 32];
   const int tid = threadIdx.x % kThreads;
   const int worker = threadIdx.x / kThreads;
-  constexpr int kWorkers = kBlockThreads / kThreads;
   const int D8 = a.v.head_size / 8;
-  for (long long u = static_cast<long long>(blockIdx.x) * kWorkers + worker; u < a.units;
-       u += static_cast<long long>(gridDim.x) * kWorkers) {
-    const Unit w = decode_unit(a, u);
-    const KvSequence q = kv_sequence(a.v, w.s);
-    Part p;
-    if (!part_of(a.v, q, w.j, p)) continue;
-    const int page = kv_page(a.v, w.s, p.block);
-    if (page < 0) continue;
-    const T* x = static_cast<const T*>(a.x[w.which]) +
-                 static_cast<long long>(p.row) * a.token[w.which] + w.h * a.head_stride[w.which];
-    uint8_t* codes = a.v.codes[w.which] + kv_page_offset(a.v, page, w.h);
-    float* scale = a.v.scale[w.which] + static_cast<long long>(page) * a.v.heads + w.h;
+  Unit u = first_unit(a, blockIdx.x * kWorkers + worker);
+  Place next = place_of(a, u);
+  while (u.s < static_cast<unsigned>(a.v.sequences)) {
+    const Place at = next;
+    const Unit w = u;
+    next_unit(a, u);
+    if (at.page < 0) {
+      next = place_of(a, u);
+      continue;
+    }
+    const Part& p = at.p;
+    const long long token = a.token[w.which];
+    const T* x = static_cast<const T*>(a.x[w.which]) + static_cast<long long>(p.row) * token +
+                 w.h * a.head_stride[w.which];
+    uint8_t* codes = a.v.codes[w.which] + kv_page_offset(a.v, at.page, w.h);
+    float* scale = a.v.scale[w.which] + static_cast<long long>(at.page) * a.v.heads + w.h;
     const float s_old = p.t0 > 0 ? *scale : 0.0f;
 
     const int nvec = (p.t1 - p.t0) * D8;
     uint4 in[NV];
-    uint32_t all = 0, finite = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int e = tid + i * kThreads;
       in[i] = make_uint4(0, 0, 0, 0);
       if (e < nvec) {
-        const int t = e / D8;
-        in[i] = *reinterpret_cast<const uint4*>(x + t * a.token[w.which] + (e - t * D8) * 8);
+        const int t = row_of(a, e);
+        in[i] = __ldg(reinterpret_cast<const uint4*>(x + t * token + (e - t * D8) * 8));
       }
     }
+    next = place_of(a, u);
+    uint32_t all = 0, finite = 0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const uint32_t m = max_u16x2(
@@ -196,12 +261,12 @@ __global__ void __launch_bounds__(kBlockThreads) cache_write_sm103a_kernel(const
     // Largest magnitude over the worker, as the type's bits (ordered like the values).
     auto reduce = [&](uint32_t m) {
       m = __reduce_max_sync(0xFFFFFFFFu, m);
-      if (kThreads > 32) {
-        __syncthreads();
+      if constexpr (kThreads > 32) {
+        worker_sync<kThreads>(worker);
         if ((threadIdx.x & 31) == 0) s_max[threadIdx.x / 32] = m;
-        __syncthreads();
+        worker_sync<kThreads>(worker);
 #pragma unroll
-        for (int i = 0; i < kBlockThreads / 32; ++i) m = max(m, s_max[i]);
+        for (int i = 0; i < kThreads / 32; ++i) m = max(m, s_max[worker * (kThreads / 32) + i]);
       }
       return m;
     };
@@ -229,8 +294,8 @@ __global__ void __launch_bounds__(kBlockThreads) cache_write_sm103a_kernel(const
       // older codes of the block, to the new scale
       const int n8 = p.t0 * D8;
       for (int e = tid; e < n8; e += kThreads) {
-        uint2* at = reinterpret_cast<uint2*>(codes) + e;
-        uint2 c = *at;
+        uint2* to = reinterpret_cast<uint2*>(codes) + e;
+        uint2 c = *to;
         uint32_t* half = reinterpret_cast<uint32_t*>(&c);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -240,24 +305,30 @@ __global__ void __launch_bounds__(kBlockThreads) cache_write_sm103a_kernel(const
           for (int i = 0; i < 4; ++i) f[i] *= s_old;
           half[k] = codes4_any<kFormat>(f, s, r);
         }
-        *at = c;
+        *to = c;
       }
     }
     uint2* to = reinterpret_cast<uint2*>(codes) + p.t0 * D8;
+    auto put = [&](auto any) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = tid + i * kThreads;
-      if (e >= nvec) break;
-      const uint32_t part[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
-      uint32_t c[2];
+      for (int i = 0; i < NV; ++i) {
+        const int e = tid + i * kThreads;
+        if (e >= nvec) break;
+        const uint32_t part[4] = {in[i].x, in[i].y, in[i].z, in[i].w};
+        uint32_t c[2];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float f[4] = {to_float<T>(part[2 * k] & 0xFFFFu), to_float<T>(part[2 * k] >> 16),
-                      to_float<T>(part[2 * k + 1] & 0xFFFFu), to_float<T>(part[2 * k + 1] >> 16)};
-        c[k] = odd ? codes4_any<kFormat>(f, s, r) : codes4<kFormat>(f, s, r);
+        for (int k = 0; k < 2; ++k) {
+          float f[4];
+          to_float2<T>(part[2 * k], f[0], f[1]);
+          to_float2<T>(part[2 * k + 1], f[2], f[3]);
+          if constexpr (decltype(any)::value) c[k] = codes4_any<kFormat>(f, s, r);
+          else c[k] = codes4<kFormat>(f, s, r);
+        }
+        to[e] = make_uint2(c[0], c[1]);
       }
-      to[e] = make_uint2(c[0], c[1]);
-    }
+    };
+    if (odd) put(std::true_type{});
+    else put(std::false_type{});
     if (tid == 0) *scale = s;
   }
 }
@@ -293,60 +364,102 @@ __device__ __forceinline__ void store8<__half>(__half* to, const float (&f)[8]) 
 }
 
 // code * s in fp32 is exact for int8 (7 and 8 bits) and e4m3 (a power of two)
-// where this library wrote it; it is rounded once, to T.
-template <typename T, int kFormat, int kThreads>
+// where this library wrote it; it is rounded once, to T. A warp a unit, a lane 8 codes a
+// load and kReadVecs loads in flight; a warp's store of 16-bit values is one run of
+// memory. (A CTA a unit with one load in flight: 86 us instead of 53; 16 codes a load,
+// whose values leave gaps between a store's lanes: 66 us.)
+constexpr int kReadVecs = 8;
+template <typename T, int kFormat>
 __global__ void __launch_bounds__(kBlockThreads) cache_read_sm103a_kernel(const CacheArgs a) {
   grid_dependency_wait();
-  const int tid = threadIdx.x % kThreads;
-  const int worker = threadIdx.x / kThreads;
-  constexpr int kWorkers = kBlockThreads / kThreads;
+  constexpr int kWorkers = kBlockThreads / 32;
+  const int lane = threadIdx.x % 32;
   const int D8 = a.v.head_size / 8;
-  for (long long u = static_cast<long long>(blockIdx.x) * kWorkers + worker; u < a.units;
-       u += static_cast<long long>(gridDim.x) * kWorkers) {
-    const Unit w = decode_unit(a, u);
-    const KvSequence q = kv_sequence(a.v, w.s);
-    Part p;
-    if (!part_of(a.v, q, w.j, p)) continue;
-    const int page = kv_page(a.v, w.s, p.block);
-    if (page < 0) continue;
-    T* y = static_cast<T*>(a.x[w.which]) + static_cast<long long>(p.row) * a.token[w.which] +
+  Unit u = first_unit(a, blockIdx.x * kWorkers + threadIdx.x / 32);
+  Place next = place_of(a, u);
+  while (u.s < static_cast<unsigned>(a.v.sequences)) {
+    const Place at = next;
+    const Unit w = u;
+    next_unit(a, u);
+    if (at.page < 0) {
+      next = place_of(a, u);
+      continue;
+    }
+    const Part& p = at.p;
+    const long long token = a.token[w.which];
+    T* y = static_cast<T*>(a.x[w.which]) + static_cast<long long>(p.row) * token +
            w.h * a.head_stride[w.which];
     const uint2* codes = reinterpret_cast<const uint2*>(a.v.codes[w.which] +
-                                                        kv_page_offset(a.v, page, w.h)) +
+                                                        kv_page_offset(a.v, at.page, w.h)) +
                          p.t0 * D8;
-    const float s = a.v.scale[w.which][static_cast<long long>(page) * a.v.heads + w.h];
+    const float s = a.v.scale[w.which][static_cast<long long>(at.page) * a.v.heads + w.h];
     const int nvec = (p.t1 - p.t0) * D8;
-#pragma unroll 4
-    for (int e = tid; e < nvec; e += kThreads) {
-      const int t = e / D8;
-      const uint2 c = codes[e];
-      float f[4], g[4];
-      codes4_to_float<kFormat>(c.x, f);
-      codes4_to_float<kFormat>(c.y, g);
-      const float o[8] = {f[0] * s, f[1] * s, f[2] * s, f[3] * s,
-                          g[0] * s, g[1] * s, g[2] * s, g[3] * s};
-      store8<T>(y + t * a.token[w.which] + (e - t * D8) * 8, o);
+    for (int e0 = 0; e0 < nvec; e0 += 32 * kReadVecs) {
+      uint2 c[kReadVecs];
+#pragma unroll
+      for (int i = 0; i < kReadVecs; ++i) {
+        const int e = e0 + lane + 32 * i;
+        c[i] = make_uint2(0, 0);
+        if (e < nvec) c[i] = codes[e];
+      }
+      if (e0 == 0) next = place_of(a, u);
+#pragma unroll
+      for (int i = 0; i < kReadVecs; ++i) {
+        const int e = e0 + lane + 32 * i;
+        if (e >= nvec) break;
+        const int t = row_of(a, e);
+        float f[4], g[4];
+        codes4_to_float<kFormat>(c[i].x, f);
+        codes4_to_float<kFormat>(c[i].y, g);
+        const float o[8] = {f[0] * s, f[1] * s, f[2] * s, f[3] * s,
+                            g[0] * s, g[1] * s, g[2] * s, g[3] * s};
+        store8<T>(y + t * token + (e - t * D8) * 8, o);
+      }
     }
   }
 }
 
-template <typename T, int kFormat, bool kWrite>
-cudaError_t launch_cache(CacheArgs a, int sms, cudaStream_t stream) {
-  const bool step = a.v.max_new <= kStepTokens;
-  const int workers = step ? kBlockThreads / 32 : 1;
-  const long long blocks = (a.units + workers - 1) / workers;
+template <typename Kernel>
+cudaError_t launch_workers(Kernel kernel, int workers, CacheArgs a, int sms,
+                           cudaStream_t stream) {
+  const long long units =
+      static_cast<long long>(a.v.sequences) * a.touched * 2 * a.v.heads;
   const unsigned grid = static_cast<unsigned>(
-      std::min<long long>(blocks, static_cast<long long>(sms) * (2048 / kBlockThreads)));
-  if constexpr (kWrite)
-    return step ? launch_programmatic(cache_write_sm103a_kernel<T, kFormat, 32>, grid,
-                                      kBlockThreads, 0, stream, a)
-                : launch_programmatic(cache_write_sm103a_kernel<T, kFormat, kBlockThreads>, grid,
-                                      kBlockThreads, 0, stream, a);
-  else
-    return step ? launch_programmatic(cache_read_sm103a_kernel<T, kFormat, 32>, grid,
-                                      kBlockThreads, 0, stream, a)
-                : launch_programmatic(cache_read_sm103a_kernel<T, kFormat, kBlockThreads>, grid,
-                                      kBlockThreads, 0, stream, a);
+      std::min<long long>((units + workers - 1) / workers,
+                          static_cast<long long>(sms) * (2048 / kBlockThreads)));
+  unsigned step = grid * workers;
+  a.step_h = static_cast<int>(step % a.v.heads);
+  step /= a.v.heads;
+  a.step_which = static_cast<int>(step % 2);
+  step /= 2;
+  a.step_j = static_cast<int>(step % a.touched);
+  a.step_s = step / a.touched;
+  const unsigned chunks = a.v.head_size / 8;
+  a.by_chunks = ((1u << 31) + chunks - 1) / chunks;
+  return launch_programmatic(kernel, grid, kBlockThreads, 0, stream, a);
+}
+
+template <typename T, int kFormat, bool kWrite>
+cudaError_t launch_cache(const CacheArgs& a, int sms, cudaStream_t stream) {
+  if constexpr (kWrite) {
+    const int vectors = a.v.page_tokens * a.v.head_size / 8;
+    if (a.v.max_new <= kStepTokens)
+      return launch_workers(cache_write_sm103a_kernel<T, kFormat, 32, kStepVecs>, 8, a, sms,
+                            stream);
+    if (vectors <= 32 * kBlockVecs)
+      return launch_workers(cache_write_sm103a_kernel<T, kFormat, 32, kBlockVecs>, 8, a, sms,
+                            stream);
+    if (vectors <= 64 * kBlockVecs)
+      return launch_workers(cache_write_sm103a_kernel<T, kFormat, 64, kBlockVecs>, 4, a, sms,
+                            stream);
+    if (vectors <= 128 * kBlockVecs)
+      return launch_workers(cache_write_sm103a_kernel<T, kFormat, 128, kBlockVecs>, 2, a, sms,
+                            stream);
+    return launch_workers(cache_write_sm103a_kernel<T, kFormat, 256, kBlockVecs>, 1, a, sms,
+                          stream);
+  } else {
+    return launch_workers(cache_read_sm103a_kernel<T, kFormat>, 8, a, sms, stream);
+  }
 }
 
 template <typename T, bool kWrite>
@@ -393,7 +506,6 @@ int kv_cache_launch(const csa_kv_cache& cache, const csa_kv_batch& batch, const 
   a.touched = static_cast<int>(std::min<long long>(
       (static_cast<long long>(batch.max_new) + cache.page_tokens - 2) / cache.page_tokens + 1,
       batch.table_width));
-  a.units = static_cast<long long>(batch.sequences) * a.touched * 2 * cache.heads;
   cudaError_t e;
   if (write)
     e = rows.dtype == CSA_F16
