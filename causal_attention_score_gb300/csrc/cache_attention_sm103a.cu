@@ -66,6 +66,13 @@ constexpr int kGroups = NB == 1 ? 3 : 2;
 // tokens or more. A tile is what a group's four warps take.
 template <int kSub>
 constexpr int kTileTokens = 64 * kSub;
+// A unit counts in the division of work as kUnitTiles tiles more than it has: about what
+// finishing a unit and starting the next takes a group. Without it the groups that short
+// sequences fall to come last: 64 sequences of 300 to 8191 tokens take 171 us instead
+// of 139, 32 of 60 to 2000 tokens 44 instead of 29, 16-row units of 4K tokens 90 instead of 69.
+// (One tile: 153, 32, 80; four: 141, 31, 67.)
+template <int NB, int kSub>
+constexpr int kUnitTiles = (NB == 1 ? 2 : 3) * (2 / kSub);
 constexpr int kMaxSms = 152;
 constexpr int kMaxWorkers = kMaxSms * 3;
 constexpr int kMaxRows = 16;
@@ -169,36 +176,53 @@ __device__ __forceinline__ SeqWork seq_work(const AttendArgs& a, int s) {
   return w;
 }
 
+// What a unit of a sequence counts.
+template <int NB, int kSub>
+__device__ __forceinline__ long long unit_weight(const SeqWork& w) {
+  return w.tiles + kUnitTiles<NB, kSub>;
+}
+
 // A group's place in the work list and the piece of a unit that it is at. Kept
 // in shared memory: the main loop needs the registers.
 struct Piece {
-  long long at, end;  // the group's run of tiles still to do
+  long long at, end;  // the group's run still to do
   long long base;     // where sequence s begins in the list
   SeqWork w;
   int s;
   int head, row_first, rows;  // the unit
   int tile0, count;           // its tiles [tile0, tile0 + count); count 0: no more pieces
+  long long after;            // what the unit counts past this piece
 };
 
 template <int NB, int kSub>
 __device__ __forceinline__ void next_piece(const AttendArgs& a, Piece& p) {
+  constexpr int E = kUnitTiles<NB, kSub>;
   p.count = 0;
-  if (p.at >= p.end) return;
-  long long units;
-  for (;;) {
-    units = static_cast<long long>(p.w.blocks) * a.v.heads;
-    if (p.at < p.base + units * p.w.tiles) break;
-    p.base += units * p.w.tiles;
-    p.w = seq_work<NB, kSub>(a, ++p.s);
+  while (p.at < p.end) {
+    long long weight;
+    for (;;) {
+      weight = unit_weight<NB, kSub>(p.w);
+      const long long all = static_cast<long long>(p.w.blocks) * a.v.heads * weight;
+      if (p.at < p.base + all) break;
+      p.base += all;
+      p.w = seq_work<NB, kSub>(a, ++p.s);
+    }
+    const long long off = p.at - p.base;
+    const int unit = static_cast<int>(
+        (off >> 32) == 0 ? static_cast<unsigned>(off) / static_cast<unsigned>(weight)
+                         : off / weight);
+    const int from = static_cast<int>(off - static_cast<long long>(unit) * weight);
+    const int to = static_cast<int>(min(weight, static_cast<long long>(from) + (p.end - p.at)));
+    p.at += to - from;
+    if (to <= E) continue;  // the run ends before the unit's first tile
+    p.tile0 = max(from - E, 0);
+    p.count = to - E - p.tile0;
+    p.after = weight - to;
+    p.head = unit / p.w.blocks;
+    p.row_first = (unit - p.head * p.w.blocks) * (8 * NB);
+    p.rows = min(p.w.rows - p.row_first, 8 * NB);
+    return;
   }
-  const long long off = p.at - p.base;
-  const int unit = static_cast<int>(off / p.w.tiles);
-  p.tile0 = static_cast<int>(off - static_cast<long long>(unit) * p.w.tiles);
-  p.head = unit / p.w.blocks;
-  p.row_first = (unit - p.head * p.w.blocks) * (8 * NB);
-  p.rows = min(p.w.rows - p.row_first, 8 * NB);
-  p.count = static_cast<int>(min(static_cast<long long>(p.w.tiles - p.tile0), p.end - p.at));
-  p.at += p.count;
 }
 
 template <int HSP, int NB>
@@ -212,7 +236,7 @@ struct GroupSmem {
   float o[4][8 * NB][kRowStride];
   uint4 q[kSharedQ ? NB * HSP / 32 : 1][32];
   float m[4][8 * NB], l[4][8 * NB];
-  Piece piece;
+  Piece piece[2];  // the one at hand and the next
 };
 
 // HSP: head size padded to 64 or 128; kFull: head_size == HSP (no bounds on the
@@ -245,7 +269,7 @@ __global__ void __launch_bounds__(128 * kGroups<NB>, 1)
     const long long from = static_cast<long long>(threadIdx.x) * c;
     for (long long s = from; s < min(static_cast<long long>(S), from + c); ++s) {
       const SeqWork w = seq_work<NB, kSub>(a, static_cast<int>(s));
-      mine += static_cast<long long>(w.blocks) * w.tiles * a.v.heads;
+      mine += static_cast<long long>(w.blocks) * a.v.heads * unit_weight<NB, kSub>(w);
     }
     long long sum = mine;
 #pragma unroll
@@ -274,7 +298,7 @@ __global__ void __launch_bounds__(128 * kGroups<NB>, 1)
   bool left_open = false;
 
   if (gtid == 0) {
-    Piece& p = sm.piece;
+    Piece& p = sm.piece[0];
     p.at = min(share * worker, total);
     p.end = min(p.at + share, total);
     if (p.at < p.end) {
@@ -288,40 +312,50 @@ __global__ void __launch_bounds__(128 * kGroups<NB>, 1)
       p.base = s_prefix[lo];
       p.w = seq_work<NB, kSub>(a, p.s);
     }
+    next_piece<NB, kSub>(a, p);
   }
-  for (;;) {
-    if (gtid == 0) next_piece<NB, kSub>(a, sm.piece);
-    group_sync(gi);
-    const volatile Piece& piece = sm.piece;
+  group_sync(gi);
+
+  // K's chunks and V's of a step's blocks as they come from HBM, their page's scales.
+  uint4 kr[kSub][2][kChunks];
+  uint32_t vr[kSub][4][kVWords];
+  float ks = 1.0f, vs = 1.0f;
+  // Where this warp's tokens of the step at hand and of the next are: page * heads + head
+  // (below 2^31 for any cache that fits in memory), -1 where there is nothing to read; the
+  // first of the tokens.
+  int unit = -1, unit_next = -1, tb = 0, tb_next = 0;
+  bool begin = true;
+  for (int cur = 0;; cur ^= 1) {
+    const volatile Piece& piece = sm.piece[cur];
     const int count = piece.count;
     if (count == 0) break;
-    const int s = piece.s, head = piece.head, tile0 = piece.tile0;
+    const int head = piece.head;
     const int length = piece.w.q.length;
 
-    // K's chunks and V's of the step's blocks as they come from HBM, their page's scales.
-    uint4 kr[kSub][2][kChunks];
-    uint32_t vr[kSub][4][kVWords];
-    float ks = 1.0f, vs = 1.0f;
-    const int sink_tiles = piece.w.sink_tiles, window_skip = piece.w.window_tile - sink_tiles;
-    // First token of this warp's in step i, and its page (-1: nothing there).
-    auto token_of = [&](int i) {
-      const int tile = tile0 + i;
-      return (tile < sink_tiles ? tile : tile + window_skip) * kTileTokens<kSub> +
-             warp * (16 * kSub);
-    };
-    auto page_of = [&](int i) {
-      if (i >= count) return -1;
-      const int tb = token_of(i);
-      return tb < length ? kv_page(a.v, s, tb >> a.v.page_shift) : -1;
+    // The same of step i; past the piece's end, of the next piece's.
+    auto look = [&](int i, int& first) {
+      const bool past = i >= count;
+      const volatile Piece& p = sm.piece[past ? cur ^ 1 : cur];
+      if (past) {
+        i -= count;
+        if (i >= p.count) return -1;
+      }
+      const int tile = p.tile0 + i;
+      first = (tile < p.w.sink_tiles ? tile : tile + p.w.window_tile - p.w.sink_tiles) *
+                  kTileTokens<kSub> +
+              warp * (16 * kSub);
+      if (first >= p.w.q.length) return -1;
+      const int page = kv_page(a.v, p.s, first >> a.v.page_shift);
+      return page < 0 ? -1 : page * a.v.heads + p.head;
     };
     // Lane (g, t): tokens g and g + 8, chunks t and t + 4 of their K rows; tokens
     // 2t, 2t + 1, 2t + 8, 2t + 9, chunk g of their V rows.
     const uint8_t* k_lane = a.v.codes[0] + (g * D + t * 16);
     const uint8_t* v_lane = a.v.codes[1] + (2 * t * D + g * kVBytes);
     const int page_bytes = a.v.page_tokens * D;
-    auto load_k = [&](int tb, int page) {
-      const long long unit = static_cast<long long>(page) * a.v.heads + head;
-      const uint8_t* from = k_lane + (unit * page_bytes + (tb & (a.v.page_tokens - 1)) * D);
+    auto load_k = [&](int first, int u0) {
+      const uint8_t* from = k_lane + (static_cast<long long>(u0) * page_bytes +
+                                      (first & (a.v.page_tokens - 1)) * D);
 #pragma unroll
       for (int u = 0; u < kSub; ++u)
 #pragma unroll
@@ -332,11 +366,11 @@ __global__ void __launch_bounds__(128 * kGroups<NB>, 1)
                               ? __ldg(reinterpret_cast<const uint4*>(from + (16 * u + 8 * n) * D +
                                                                      64 * h))
                               : make_uint4(0, 0, 0, 0);
-      ks = __ldg(a.v.scale[0] + unit);
+      ks = __ldg(a.v.scale[0] + u0);
     };
-    auto load_v = [&](int tb, int page) {
-      const long long unit = static_cast<long long>(page) * a.v.heads + head;
-      const uint8_t* from = v_lane + (unit * page_bytes + (tb & (a.v.page_tokens - 1)) * D);
+    auto load_v = [&](int first, int u0) {
+      const uint8_t* from = v_lane + (static_cast<long long>(u0) * page_bytes +
+                                      (first & (a.v.page_tokens - 1)) * D);
       const bool in = kFull || g * kVBytes < D;
 #pragma unroll
       for (int u = 0; u < kSub; ++u)
@@ -355,12 +389,23 @@ __global__ void __launch_bounds__(128 * kGroups<NB>, 1)
             vr[u][i][1] = x.y;
           }
         }
-      vs = __ldg(a.v.scale[1] + unit);
+      vs = __ldg(a.v.scale[1] + u0);
     };
-    int page = page_of(0), page_next = page_of(1);
-    if (page >= 0) {
-      load_k(token_of(0), page);
-      load_v(token_of(0), page);
+    // Asks for a step's codes in L2 (they are one run of memory in K and in V).
+    auto prefetch = [&](int first, int u0) {
+      if (lane < 2)
+        bulk_prefetch_l2(a.v.codes[lane] + static_cast<long long>(u0) * page_bytes +
+                             (first & (a.v.page_tokens - 1)) * D,
+                         16 * kSub * D);
+    };
+    if (begin) {
+      begin = false;
+      unit = look(0, tb);
+      if (count > 1) unit_next = look(1, tb_next);
+      if (unit >= 0) {
+        load_k(tb, unit);
+        load_v(tb, unit);
+      }
     }
 
     // ------------------------------------------------------ Q's fragments --
@@ -431,7 +476,15 @@ __global__ void __launch_bounds__(128 * kGroups<NB>, 1)
       pos_low = first + row_first / a.group;
       pos_high = first + (row_first + rows - 1) / a.group;
     }
-    if constexpr (Smem::kSharedQ) group_sync(gi);
+    // The next piece, so that its first steps' codes are asked for before this one ends.
+    if (gtid == 0) {
+      Piece& next = sm.piece[cur ^ 1];
+      next = sm.piece[cur];
+      next_piece<NB, kSub>(a, next);
+    }
+    group_sync(gi);
+    if (count == 1) unit_next = look(1, tb_next);
+    if (unit_next >= 0) prefetch(tb_next, unit_next);
 
     float o[NB][kTilesM][4];
 #pragma unroll
@@ -446,9 +499,9 @@ __global__ void __launch_bounds__(128 * kGroups<NB>, 1)
     }
 
     for (int i = 0; i < count; ++i) {
-      const int tb = token_of(i);
-      const int page_after = page_of(i + 2);
-      if (page >= 0) {
+      int tb_after = 0;
+      const int unit_after = look(i + 2, tb_after);
+      if (unit >= 0) {
         float sc[kSub][NB][4];
 #pragma unroll
         for (int u = 0; u < kSub; ++u)
@@ -493,7 +546,7 @@ __global__ void __launch_bounds__(128 * kGroups<NB>, 1)
           fk[b][0] = fr[b][0] * ks;
           fk[b][1] = fr[b][1] * ks;
         }
-        if (page_next >= 0) load_k(token_of(i + 1), page_next);
+        if (unit_next >= 0) load_k(tb_next, unit_next);
         // sc element e: token g + 8 (e / 2), row 2t + e % 2. A masked score is -inf, and
         // stays so whatever the scales.
         const int last = tb + 16 * kSub - 1;
@@ -607,12 +660,15 @@ __global__ void __launch_bounds__(128 * kGroups<NB>, 1)
                       pb[u][b][1]);
             }
           }
-      } else if (page_next >= 0) {
-        load_k(token_of(i + 1), page_next);
+      } else if (unit_next >= 0) {
+        load_k(tb_next, unit_next);
       }
-      if (page_next >= 0) load_v(token_of(i + 1), page_next);
-      page = page_next;
-      page_next = page_after;
+      if (unit_next >= 0) load_v(tb_next, unit_next);
+      if (unit_after >= 0) prefetch(tb_after, unit_after);
+      unit = unit_next;
+      tb = tb_next;
+      unit_next = unit_after;
+      tb_next = tb_after;
     }
 
     // ------------------------------------------- the four warps' results --
@@ -679,8 +735,7 @@ __global__ void __launch_bounds__(128 * kGroups<NB>, 1)
     if (!whole && begins) {
       left_open = true;
       if (gtid == 0) {
-        header[kHeadPieces] =
-            1 + static_cast<int>((piece.w.tiles - piece.count + share - 1) / share);
+        header[kHeadPieces] = 1 + static_cast<int>((piece.after + share - 1) / share);
         header[kHeadRow0] = row0;
         header[kHeadFirst] = row_first;
         header[kHeadHead] = piece.head;

@@ -172,6 +172,14 @@ __device__ __forceinline__ bool mbar_wait_warp_inline(uint32_t bar, uint32_t par
   return ok != 0;
 }
 
+// Asks for `bytes` (a multiple of 16, at a 16-byte boundary) in L2.
+__device__ __forceinline__ void bulk_prefetch_l2(const void* from, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                   reinterpret_cast<uint64_t>(from)),
+               "r"(bytes)
+               : "memory");
+}
+
 // -------------------------------------------------------------------- TMA --
 
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* m) {
