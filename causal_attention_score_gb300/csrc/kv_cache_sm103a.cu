@@ -47,10 +47,12 @@ constexpr int kBlockThreads = 256;
 // (4 vectors of 8 elements a lane) where no sequence has more than 8 new tokens, else as
 // many warps as hold a whole block in 8 vectors a lane, one (16 x 128) to eight
 // (128 x 128). (With 256 threads for every block the lanes without elements took
-// the issue slots: 96 us instead of 57 for 28K tokens of 16 heads of 128.)
+// the issue slots: 96 us instead of 53 for 28K tokens of 16 heads of 128.)
 constexpr int kStepTokens = 8;
 constexpr int kStepVecs = 4;
 constexpr int kBlockVecs = 8;
+constexpr int kWritePerSm = 4;  // CTAs by registers; the grid has kWriteGrid an SM
+constexpr int kWriteGrid = 8;
 constexpr float kScaleFloor = 7.888609052210118e-31f;  // 2^-100
 
 struct CacheArgs {
@@ -212,7 +214,8 @@ __device__ __forceinline__ void worker_sync(int worker) {
 
 // kThreads are a worker, NV the vectors that each holds.
 template <typename T, int kFormat, int kThreads, int NV>
-__global__ void __launch_bounds__(kBlockThreads) cache_write_sm103a_kernel(const CacheArgs a) {
+__global__ void __launch_bounds__(kBlockThreads, kWritePerSm)
+    cache_write_sm103a_kernel(const CacheArgs a) {
   grid_dependency_wait();
   constexpr int kWorkers = kBlockThreads / kThreads;
   __shared__ uint32_t s_max[kBlockThreads / 32];
@@ -366,11 +369,14 @@ __device__ __forceinline__ void store8<__half>(__half* to, const float (&f)[8]) 
 // code * s in fp32 is exact for int8 (7 and 8 bits) and e4m3 (a power of two)
 // where this library wrote it; it is rounded once, to T. A warp a unit, a lane 8 codes a
 // load and kReadVecs loads in flight; a warp's store of 16-bit values is one run of
-// memory. (A CTA a unit with one load in flight: 86 us instead of 53; 16 codes a load,
+// memory. (A CTA a unit with one load in flight: 86 us instead of 49; 16 codes a load,
 // whose values leave gaps between a store's lanes: 66 us.)
 constexpr int kReadVecs = 8;
+constexpr int kReadPerSm = 3;  // CTAs by registers; 32 an SM in the grid: 49 us, 3: 57
+constexpr int kReadGrid = 32;
 template <typename T, int kFormat>
-__global__ void __launch_bounds__(kBlockThreads) cache_read_sm103a_kernel(const CacheArgs a) {
+__global__ void __launch_bounds__(kBlockThreads, kReadPerSm)
+    cache_read_sm103a_kernel(const CacheArgs a) {
   grid_dependency_wait();
   constexpr int kWorkers = kBlockThreads / 32;
   const int lane = threadIdx.x % 32;
@@ -420,13 +426,13 @@ __global__ void __launch_bounds__(kBlockThreads) cache_read_sm103a_kernel(const 
 }
 
 template <typename Kernel>
-cudaError_t launch_workers(Kernel kernel, int workers, CacheArgs a, int sms,
+cudaError_t launch_workers(Kernel kernel, int workers, int per_sm, CacheArgs a, int sms,
                            cudaStream_t stream) {
   const long long units =
       static_cast<long long>(a.v.sequences) * a.touched * 2 * a.v.heads;
   const unsigned grid = static_cast<unsigned>(
       std::min<long long>((units + workers - 1) / workers,
-                          static_cast<long long>(sms) * (2048 / kBlockThreads)));
+                          static_cast<long long>(sms) * per_sm));
   unsigned step = grid * workers;
   a.step_h = static_cast<int>(step % a.v.heads);
   step /= a.v.heads;
@@ -444,21 +450,21 @@ cudaError_t launch_cache(const CacheArgs& a, int sms, cudaStream_t stream) {
   if constexpr (kWrite) {
     const int vectors = a.v.page_tokens * a.v.head_size / 8;
     if (a.v.max_new <= kStepTokens)
-      return launch_workers(cache_write_sm103a_kernel<T, kFormat, 32, kStepVecs>, 8, a, sms,
+      return launch_workers(cache_write_sm103a_kernel<T, kFormat, 32, kStepVecs>, 8, kWriteGrid, a, sms,
                             stream);
     if (vectors <= 32 * kBlockVecs)
-      return launch_workers(cache_write_sm103a_kernel<T, kFormat, 32, kBlockVecs>, 8, a, sms,
+      return launch_workers(cache_write_sm103a_kernel<T, kFormat, 32, kBlockVecs>, 8, kWriteGrid, a, sms,
                             stream);
     if (vectors <= 64 * kBlockVecs)
-      return launch_workers(cache_write_sm103a_kernel<T, kFormat, 64, kBlockVecs>, 4, a, sms,
+      return launch_workers(cache_write_sm103a_kernel<T, kFormat, 64, kBlockVecs>, 4, kWriteGrid, a, sms,
                             stream);
     if (vectors <= 128 * kBlockVecs)
-      return launch_workers(cache_write_sm103a_kernel<T, kFormat, 128, kBlockVecs>, 2, a, sms,
+      return launch_workers(cache_write_sm103a_kernel<T, kFormat, 128, kBlockVecs>, 2, kWriteGrid, a, sms,
                             stream);
-    return launch_workers(cache_write_sm103a_kernel<T, kFormat, 256, kBlockVecs>, 1, a, sms,
+    return launch_workers(cache_write_sm103a_kernel<T, kFormat, 256, kBlockVecs>, 1, kWriteGrid, a, sms,
                           stream);
   } else {
-    return launch_workers(cache_read_sm103a_kernel<T, kFormat>, 8, a, sms, stream);
+    return launch_workers(cache_read_sm103a_kernel<T, kFormat>, 8, kReadGrid, a, sms, stream);
   }
 }
 
