@@ -22,27 +22,45 @@ _FORMAT = {torch.int8: CSA_KV_INT8, torch.float8_e4m3fn: CSA_KV_E4M3}
 _SCALING = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
 
 
-def _on_device(t: torch.Tensor, name: str) -> None:
+_ANY = tuple(_DTYPE)
+_get_device, _get_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
+def _elsewhere(device, name: str) -> ValueError:
     """Every call works on the current device: its tensors must be there."""
-    if t.get_device() != torch._C._cuda_getDevice():
-        raise ValueError(f"{name} is on {t.device}, but calls work on the current device "
-                         f"cuda:{torch.cuda.current_device()}")
+    return ValueError(f"{name} is on {device}, but calls work on the current device "
+                      f"cuda:{torch.cuda.current_device()}")
 
 
-def _stream_ptr(stream) -> int:
-    """The raw handle of ``stream``, by default of the current device's current stream
+def _device_of(t: torch.Tensor, name: str) -> int:
+    """The current device, where ``t`` must be."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dev != _get_device():
+        raise _elsewhere(t.device, name)
+    return dev
+
+
+def _stream_ptr(stream, dev: int) -> int:
+    """The raw handle of ``stream``, by default of device ``dev``'s current stream
     (asked for directly: building a torch.cuda.Stream takes as long as a launch)."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return _get_stream(dev)
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _rows(t: torch.Tensor, name: str, shape, dtypes) -> tuple[int, int]:
-    """(token stride, head stride) of a [tokens, heads, size] tensor of the given shape."""
+def _rows(t: torch.Tensor, name: str, shape, dtypes, dev: int) -> tuple[int, int]:
+    """(token stride, head stride) of a [tokens, heads, size] tensor of the given shape on
+    device ``dev``."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != dev:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        raise _elsewhere(t.device, name)
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be one of {dtypes}, got {t.dtype}")
     if t.shape != shape:
@@ -50,18 +68,9 @@ def _rows(t: torch.Tensor, name: str, shape, dtypes) -> tuple[int, int]:
     token, head, one = t.stride()
     if one != 1:
         raise ValueError(f"{name}: the elements of a head must be contiguous")
-    _on_device(t, name)
     # the stride of a dimension of one entry means nothing
     n, heads, size = shape
-    head = head if heads > 1 else size
-    return (token if n > 1 else heads * size), head
-
-
-def _same_storage(tensors, ptrs, what: str) -> None:
-    for t, p in zip(tensors, ptrs):
-        if t.data_ptr() != p:
-            raise ValueError(f"a tensor of this {what} no longer has the storage it was made "
-                             f"with; make a new {what}")
+    return (token if n > 1 else heads * size), (head if heads > 1 else size)
 
 
 class RotaryTable:
@@ -98,20 +107,27 @@ def _rotary(which: str, out, x, table, positions, start, period, interleaved, st
         out = out.as_strided(x.shape, out.stride()[1:])
     if x.dim() != 3:
         raise ValueError("x must be [tokens, heads, size] or [B, T, heads, size]")
-    xt, xh = _rows(x, "x", x.shape, tuple(_DTYPE))
-    ot, oh = _rows(out, "out", x.shape, (x.dtype,))
-    n, heads, size = x.shape
+    dev = _device_of(x, "x")
+    shape, dtype = x.shape, x.dtype
+    xt, xh = _rows(x, "x", shape, _ANY, dev)
+    ot, oh = _rows(out, "out", shape, (dtype,), dev)
+    n, heads, size = shape
     pos = None
     if positions is not None:
         _need(positions, "positions", torch.int32, n)
-        _on_device(positions, "positions")
+        if positions.get_device() != dev:
+            raise _elsewhere(positions.device, "positions")
         pos = positions.data_ptr()
-    _on_device(table.turns, "the rotary table")
-    lib = _lib.load()
+    turns = table.turns
+    if turns.get_device() != dev:
+        raise _elsewhere(turns.device, "the rotary table")
+    lib = _lib._lib or _lib.load()
     fn = lib.rotary_backward if which == "rotary_backward" else lib.rotary_forward
-    _lib.check(fn(out.data_ptr(), x.data_ptr(), _DTYPE[x.dtype], n, heads, size, table.rot_dim,
-                  ot, oh, xt, xh, table.turns.data_ptr(), table.amplitude, pos, start, period,
-                  1 if interleaved else 0, _stream_ptr(stream)), which)
+    rc = fn(out.data_ptr(), x.data_ptr(), _DTYPE[dtype], n, heads, size, table.rot_dim, ot, oh,
+            xt, xh, turns.data_ptr(), table.amplitude, pos, start, period,
+            1 if interleaved else 0, _stream_ptr(stream, dev))
+    if rc:
+        _lib.check(rc, which)
 
 
 def rotary_forward(out: torch.Tensor, x: torch.Tensor, table: RotaryTable, positions=None,
@@ -158,7 +174,20 @@ class _KvBatchStruct(ctypes.Structure):
                 ("table_width", ctypes.c_int), ("rows", ctypes.c_int), ("max_new", ctypes.c_int)]
 
 
-class KvCache:
+class _Marshalled:
+    """Tensors (``_tensors``) whose addresses were written into a struct once."""
+
+    def _pointer(self, dev: int) -> int:
+        """Address of the struct, for a call on device ``dev``."""
+        if [t.data_ptr() for t in self._tensors] != self._ptrs:
+            raise ValueError(f"a tensor of this {type(self).__name__} no longer has the storage it "
+                             f"was made with; make a new {type(self).__name__}")
+        if self._device != dev:
+            raise _elsewhere(self._tensors[0].device, f"the {type(self).__name__}")
+        return self._ref
+
+
+class KvCache(_Marshalled):
     """A paged cache of keys and values in 8 bits (csa_kv_cache in include/csa.h): codes
     ``k`` and ``v`` [pages, heads, page_tokens, head_size], torch.int8 or
     torch.float8_e4m3fn, and fp32 scales ``k_scale`` and ``v_scale`` [pages, heads]."""
@@ -183,6 +212,7 @@ class KvCache:
         self.pages, self.heads, self.page_tokens, self.head_size = pages, heads, page_tokens, head_size
         self._tensors = (k, v, k_scale, v_scale)
         self._ptrs = [t.data_ptr() for t in self._tensors]
+        self._device = k.get_device()
         self._struct = _KvCacheStruct(*self._ptrs, pages, heads, page_tokens, head_size,
                                       _FORMAT[k.dtype])
         self._ref = ctypes.addressof(self._struct)
@@ -200,13 +230,8 @@ class KvCache:
         scales = [torch.empty(shape[:2], dtype=torch.float32, device=device) for _ in range(2)]
         return cls(*codes, *scales)
 
-    def _pointer(self) -> int:
-        _same_storage(self._tensors, self._ptrs, "KvCache")
-        _on_device(self.k, "the cache")
-        return self._ref
 
-
-class KvBatch:
+class KvBatch(_Marshalled):
     """Which rows of a call are which tokens (csa_kv_batch in include/csa.h): int32 tensors
     ``offsets`` [S + 1], ``lengths`` [S] (including the rows) and ``table`` [S, width], which
     may change between calls in place. ``rows`` is the number of rows the calls' tensors
@@ -226,43 +251,45 @@ class KvBatch:
         self.rows, self.max_new = int(rows), int(rows if max_new is None else max_new)
         self._tensors = (offsets, lengths, table)
         self._ptrs = [t.data_ptr() for t in self._tensors]
+        self._device = offsets.get_device()
         self._struct = _KvBatchStruct(*self._ptrs, S, width, self.rows, self.max_new)
         self._ref = ctypes.addressof(self._struct)
-
-    def _pointer(self) -> int:
-        _same_storage(self._tensors, self._ptrs, "KvBatch")
-        _on_device(self.offsets, "the batch")
-        return self._ref
 
 
 def kv_cache_write(cache: KvCache, batch: KvBatch, k: torch.Tensor, v: torch.Tensor,
                    stream=None) -> None:
     """Quantises rows ``k`` and ``v`` [rows, heads, head_size] (bf16 or fp16) into the cache,
     as the last tokens of the batch's sequences; see kv_cache_write in include/csa.h."""
+    dev, dtype = _device_of(k, "k"), k.dtype
     shape = (batch.rows, cache.heads, cache.head_size)
-    kt, kh = _rows(k, "k", shape, _HALF)
-    vt, vh = _rows(v, "v", shape, (k.dtype,))
-    _lib.check(_lib.load().kv_cache_write(cache._pointer(), batch._pointer(), k.data_ptr(),
-                                          v.data_ptr(), _DTYPE[k.dtype], kt, kh, vt, vh,
-                                          _stream_ptr(stream)), "kv_cache_write")
+    kt, kh = _rows(k, "k", shape, _HALF, dev)
+    vt, vh = _rows(v, "v", shape, (dtype,), dev)
+    rc = (_lib._lib or _lib.load()).kv_cache_write(
+        cache._pointer(dev), batch._pointer(dev), k.data_ptr(), v.data_ptr(), _DTYPE[dtype], kt, kh,
+        vt, vh, _stream_ptr(stream, dev))
+    if rc:
+        _lib.check(rc, "kv_cache_write")
 
 
 def kv_cache_read(k: torch.Tensor, v: torch.Tensor, cache: KvCache, batch: KvBatch,
                   stream=None) -> None:
     """The values of the batch's rows (the last tokens of its sequences) into ``k`` and ``v``
     [rows, heads, head_size], bf16, fp16 or fp32; see kv_cache_read in include/csa.h."""
+    dev, dtype = _device_of(k, "k"), k.dtype
     shape = (batch.rows, cache.heads, cache.head_size)
-    kt, kh = _rows(k, "k", shape, tuple(_DTYPE))
-    vt, vh = _rows(v, "v", shape, (k.dtype,))
-    _lib.check(_lib.load().kv_cache_read(k.data_ptr(), v.data_ptr(), _DTYPE[k.dtype], kt, kh, vt,
-                                         vh, cache._pointer(), batch._pointer(),
-                                         _stream_ptr(stream)), "kv_cache_read")
+    kt, kh = _rows(k, "k", shape, _ANY, dev)
+    vt, vh = _rows(v, "v", shape, (dtype,), dev)
+    rc = (_lib._lib or _lib.load()).kv_cache_read(
+        k.data_ptr(), v.data_ptr(), _DTYPE[dtype], kt, kh, vt, vh, cache._pointer(dev),
+        batch._pointer(dev), _stream_ptr(stream, dev))
+    if rc:
+        _lib.check(rc, "kv_cache_read")
 
 
 def cache_attention_workspace_size(cache: KvCache, batch: KvBatch, q_heads: int) -> int:
     """Bytes of workspace ``cache_attention_forward`` needs (the same for any batch)."""
     n = ctypes.c_size_t(0)
-    _lib.check(_lib.load().cache_attention_workspace_size(cache._pointer(), q_heads,
+    _lib.check(_lib.load().cache_attention_workspace_size(cache._ref, q_heads,
                                                           ctypes.byref(n)),
                "cache_attention_workspace_size")
     return int(n.value)
@@ -278,30 +305,32 @@ def cache_attention_forward(out: torch.Tensor, q: torch.Tensor, cache: KvCache, 
     call's stream. See cache_attention_forward in include/csa.h."""
     if q.dim() != 3:
         raise ValueError("q must be [rows, q_heads, head_size]")
-    shape = (batch.rows, q.shape[1], cache.head_size)
-    qt, qh = _rows(q, "q", shape, _HALF)
-    ot, oh = _rows(out, "out", shape, (q.dtype,))
-    ref = cache._pointer()
+    dev, dtype, q_heads = _device_of(q, "q"), q.dtype, q.shape[1]
+    shape = (batch.rows, q_heads, cache.head_size)
+    qt, qh = _rows(q, "q", shape, _HALF, dev)
+    ot, oh = _rows(out, "out", shape, (dtype,), dev)
+    ref = cache._pointer(dev)
     if workspace is None:
+        size = cache_attention_workspace_size(cache, batch, q_heads)
         if stream is None:
-            st = torch.cuda.current_stream(q.device)
-        elif isinstance(stream, torch.cuda.Stream):
-            st = stream
+            workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
         else:
-            st = torch.cuda.ExternalStream(int(stream), device=q.device)
-        with torch.cuda.stream(st):
-            workspace = torch.empty(cache_attention_workspace_size(cache, batch, q.shape[1]),
-                                    dtype=torch.uint8, device=q.device)
-        stream = st
-    elif not workspace.is_cuda or not workspace.is_contiguous():
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream), device=q.device)
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != dev:
+        if not workspace.is_cuda:
+            raise ValueError("workspace must be a contiguous CUDA tensor")
+        raise _elsewhere(workspace.device, "workspace")
+    elif not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
-    else:
-        _on_device(workspace, "workspace")
-    _lib.check(_lib.load().cache_attention_forward(
-        out.data_ptr(), q.data_ptr(), _DTYPE[q.dtype], q.shape[1], ot, oh, qt, qh, ref,
-        batch._pointer(), 1.0 / math.sqrt(cache.head_size) if scale is None else scale, window,
-        sinks, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-        _stream_ptr(stream)), "cache_attention_forward")
+    rc = (_lib._lib or _lib.load()).cache_attention_forward(
+        out.data_ptr(), q.data_ptr(), _DTYPE[dtype], q_heads, ot, oh, qt, qh, ref,
+        batch._pointer(dev), 1.0 / math.sqrt(cache.head_size) if scale is None else scale, window,
+        sinks, workspace.data_ptr(), workspace.nbytes, _stream_ptr(stream, dev))
+    if rc:
+        _lib.check(rc, "cache_attention_forward")
 
 
 def cache_attention(q: torch.Tensor, cache: KvCache, batch: KvBatch, scale: float | None = None,
