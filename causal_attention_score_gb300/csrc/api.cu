@@ -833,6 +833,27 @@ bool rows_apart(long long tokens, int heads, int size, long long token, long lon
          static_cast<__int128>(head) >= static_cast<__int128>(tokens - 1) * token + size;
 }
 
+// The first and last byte + 1 of [tokens][heads][size] rows whose span was checked.
+struct Range {
+  uintptr_t from, to;
+};
+Range range_of(const void* p, int esize, long long span) {
+  const uintptr_t from = reinterpret_cast<uintptr_t>(p);
+  return {from, from + static_cast<uintptr_t>(span) * esize};
+}
+bool ranges_meet(const Range& a, const Range& b) { return a.from < b.to && b.from < a.to; }
+
+// An entry point's body: what it throws (no memory on the host) becomes a status.
+template <typename Body>
+csa_status no_throw(Body body) noexcept {
+  try {
+    return body();
+  } catch (...) {
+    t_last_error.clear();
+    return CSA_ERR_LAUNCH;
+  }
+}
+
 int rotary(const char* who, const RotaryCall& c, void* stream) {
   t_last_error.clear();
   const std::string w(who);
@@ -864,8 +885,7 @@ int rotary(const char* who, const RotaryCall& c, void* stream) {
     if ((c.tokens > 1 && c.x_token != c.out_token) || (c.heads > 1 && c.x_head != c.out_head))
       return set_error(CSA_ERR_UNSUPPORTED, w + ": in place needs equal strides");
   } else {
-    const uintptr_t x0 = reinterpret_cast<uintptr_t>(c.x), o0 = reinterpret_cast<uintptr_t>(c.out);
-    if (x0 < o0 + static_cast<uintptr_t>(no) * esize && o0 < x0 + static_cast<uintptr_t>(nx) * esize)
+    if (ranges_meet(range_of(c.x, esize, nx), range_of(c.out, esize, no)))
       return set_error(CSA_ERR_UNSUPPORTED, w + ": input and output overlap in part");
   }
   DeviceInfo dev;
@@ -963,11 +983,13 @@ csa_status rotary_forward(void* out, const void* x, int dtype, int64_t tokens, i
                           int64_t out_head_stride, int64_t x_token_stride, int64_t x_head_stride,
                           const uint64_t* turns, float amplitude, const int32_t* positions,
                           int start, int period, int interleaved, void* stream) {
-  return rotary("rotary_forward",
-                {x, out, dtype, tokens, heads, head_size, rot_dim, x_token_stride, x_head_stride,
-                 out_token_stride, out_head_stride, turns, positions, start, period, amplitude,
-                 interleaved != 0, 0},
-                stream);
+  return no_throw([&] {
+    return rotary("rotary_forward",
+                  {x, out, dtype, tokens, heads, head_size, rot_dim, x_token_stride, x_head_stride,
+                   out_token_stride, out_head_stride, turns, positions, start, period, amplitude,
+                   interleaved != 0, 0},
+                  stream);
+  });
 }
 
 csa_status rotary_backward(void* dx, const void* dy, int dtype, int64_t tokens, int heads,
@@ -976,71 +998,84 @@ csa_status rotary_backward(void* dx, const void* dy, int dtype, int64_t tokens, 
                            int64_t dy_head_stride, const uint64_t* turns, float amplitude,
                            const int32_t* positions, int start, int period, int interleaved,
                            void* stream) {
-  return rotary("rotary_backward",
-                {dy, dx, dtype, tokens, heads, head_size, rot_dim, dy_token_stride, dy_head_stride,
-                 dx_token_stride, dx_head_stride, turns, positions, start, period, amplitude,
-                 interleaved != 0, 1},
-                stream);
+  return no_throw([&] {
+    return rotary("rotary_backward",
+                  {dy, dx, dtype, tokens, heads, head_size, rot_dim, dy_token_stride,
+                   dy_head_stride, dx_token_stride, dx_head_stride, turns, positions, start, period,
+                   amplitude, interleaved != 0, 1},
+                  stream);
+  });
 }
 
 csa_status csa_rotary_turns(uint64_t* turns, int rot_dim, double base, int scaling, double factor,
                             double original_length, double slow, double fast) {
-  t_last_error.clear();
-  if (!turns) return set_error(CSA_ERR_NULL, "csa_rotary_turns: null pointer");
-  if (scaling < CSA_ROTARY_NONE || scaling > CSA_ROTARY_BY_PARTS)
-    return set_error(CSA_ERR_UNSUPPORTED, "csa_rotary_turns: unknown scaling");
-  if (rot_dim < 2 || rot_dim % 2 != 0 || !(base > 1.0) || !std::isfinite(base))
-    return set_error(CSA_ERR_SHAPE, "csa_rotary_turns: rot_dim must be even and >= 2, base > 1");
-  if (scaling != CSA_ROTARY_NONE && !(factor >= 1.0 && std::isfinite(factor)))
-    return set_error(CSA_ERR_SHAPE, "csa_rotary_turns: factor must be >= 1");
-  if (scaling == CSA_ROTARY_BY_PARTS &&
-      !(original_length > 0.0 && std::isfinite(original_length) && fast > slow &&
-        std::isfinite(fast) && std::isfinite(slow)))
-    return set_error(CSA_ERR_SHAPE,
-                     "csa_rotary_turns: original_length must be > 0, fast > slow");
-  const double two_pi = 6.283185307179586476925286766559;
-  if (scaling == CSA_ROTARY_NTK && rot_dim > 2)
-    base *= std::pow(factor, static_cast<double>(rot_dim) / (rot_dim - 2));
-  for (int i = 0; i < rot_dim / 2; ++i) {
-    double f = std::pow(base, -2.0 * i / rot_dim);
-    if (scaling == CSA_ROTARY_LINEAR) f /= factor;
-    if (scaling == CSA_ROTARY_BY_PARTS) {
-      const double g =
-          std::min(1.0, std::max(0.0, (original_length * f / two_pi - slow) / (fast - slow)));
-      f *= g + (1.0 - g) / factor;
+  return no_throw([&] {
+    t_last_error.clear();
+    if (!turns) return set_error(CSA_ERR_NULL, "csa_rotary_turns: null pointer");
+    if (scaling < CSA_ROTARY_NONE || scaling > CSA_ROTARY_BY_PARTS)
+      return set_error(CSA_ERR_UNSUPPORTED, "csa_rotary_turns: unknown scaling");
+    if (rot_dim < 2 || rot_dim % 2 != 0 || !(base > 1.0) || !std::isfinite(base))
+      return set_error(CSA_ERR_SHAPE, "csa_rotary_turns: rot_dim must be even and >= 2, base > 1");
+    if (scaling != CSA_ROTARY_NONE && !(factor >= 1.0 && std::isfinite(factor)))
+      return set_error(CSA_ERR_SHAPE, "csa_rotary_turns: factor must be >= 1");
+    if (scaling == CSA_ROTARY_BY_PARTS &&
+        !(original_length > 0.0 && std::isfinite(original_length) && fast > slow &&
+          std::isfinite(fast) && std::isfinite(slow)))
+      return set_error(CSA_ERR_SHAPE,
+                       "csa_rotary_turns: original_length must be > 0, fast > slow");
+    const double two_pi = 6.283185307179586476925286766559;
+    if (scaling == CSA_ROTARY_NTK && rot_dim > 2)
+      base *= std::pow(factor, static_cast<double>(rot_dim) / (rot_dim - 2));
+    for (int i = 0; i < rot_dim / 2; ++i) {
+      double f = std::pow(base, -2.0 * i / rot_dim);
+      if (scaling == CSA_ROTARY_LINEAR) f /= factor;
+      if (scaling == CSA_ROTARY_BY_PARTS) {
+        const double g =
+            std::min(1.0, std::max(0.0, (original_length * f / two_pi - slow) / (fast - slow)));
+        f *= g + (1.0 - g) / factor;
+      }
+      turns[i] = static_cast<uint64_t>(std::nearbyint(std::ldexp(f / two_pi, 64)));
     }
-    turns[i] = static_cast<uint64_t>(std::nearbyint(std::ldexp(f / two_pi, 64)));
-  }
-  return CSA_OK;
+    return static_cast<int>(CSA_OK);
+  });
 }
 
 csa_status kv_cache_write(const csa_kv_cache* cache, const csa_kv_batch* batch, const void* k,
                           const void* v, int dtype, int64_t k_token_stride, int64_t k_head_stride,
                           int64_t v_token_stride, int64_t v_head_stride, void* stream) {
-  return kv_rows("kv_cache_write", cache, batch,
-                 {{const_cast<void*>(k), const_cast<void*>(v)},
-                  dtype,
-                  {k_token_stride, v_token_stride},
-                  {k_head_stride, v_head_stride}},
-                 true, stream);
+  return no_throw([&] {
+    return kv_rows("kv_cache_write", cache, batch,
+                   {{const_cast<void*>(k), const_cast<void*>(v)},
+                    dtype,
+                    {k_token_stride, v_token_stride},
+                    {k_head_stride, v_head_stride}},
+                   true, stream);
+  });
 }
 
 csa_status kv_cache_read(void* k, void* v, int dtype, int64_t k_token_stride,
                          int64_t k_head_stride, int64_t v_token_stride, int64_t v_head_stride,
                          const csa_kv_cache* cache, const csa_kv_batch* batch, void* stream) {
-  return kv_rows("kv_cache_read", cache, batch,
-                 {{k, v}, dtype, {k_token_stride, v_token_stride}, {k_head_stride, v_head_stride}},
-                 false, stream);
+  return no_throw([&] {
+    return kv_rows(
+        "kv_cache_read", cache, batch,
+        {{k, v}, dtype, {k_token_stride, v_token_stride}, {k_head_stride, v_head_stride}}, false,
+        stream);
+  });
 }
 
 csa_status cache_attention_workspace_size(const csa_kv_cache* cache, int q_heads, size_t* bytes) {
   t_last_error.clear();
-  if (!bytes) return set_error(CSA_ERR_NULL, "cache_attention_workspace_size: null pointer");
+  if (!bytes)
+    return no_throw([] {
+      return set_error(CSA_ERR_NULL, "cache_attention_workspace_size: null pointer");
+    });
   *bytes = 0;
-  const int rc = attention_heads_ok("cache_attention_workspace_size", cache, q_heads);
-  if (rc != CSA_OK) return rc;
-  *bytes = cache_attention_workspace_bytes(cache->head_size);
-  return CSA_OK;
+  return no_throw([&] {
+    const int rc = attention_heads_ok("cache_attention_workspace_size", cache, q_heads);
+    if (rc == CSA_OK) *bytes = cache_attention_workspace_bytes(cache->head_size);
+    return rc;
+  });
 }
 
 csa_status cache_attention_forward(void* out, const void* q, int dtype, int q_heads,
@@ -1049,41 +1084,52 @@ csa_status cache_attention_forward(void* out, const void* q, int dtype, int q_he
                                    const csa_kv_cache* cache, const csa_kv_batch* batch,
                                    float scale, int window, int sinks, void* workspace,
                                    size_t workspace_bytes, void* stream) {
-  t_last_error.clear();
-  const std::string w("cache_attention_forward");
-  int rc = attention_heads_ok(w, cache, q_heads);
-  if (rc == CSA_OK) rc = batch_args_ok(w, batch);
-  if (rc != CSA_OK) return rc;
-  if (!out || !q) return set_error(CSA_ERR_NULL, w + ": null pointer");
-  if (dtype != CSA_BF16 && dtype != CSA_F16)
-    return set_error(CSA_ERR_UNSUPPORTED, w + ": unknown dtype");
-  if (!std::isfinite(scale)) return set_error(CSA_ERR_SHAPE, w + ": scale not finite");
-  if (window < 0 || sinks < 0)
-    return set_error(CSA_ERR_SHAPE, w + ": window and sinks must be >= 0");
-  rc = rows_ok(w, q, dtype, batch->rows, q_heads, cache->head_size, q_token_stride, q_head_stride,
-               false);
-  if (rc == CSA_OK)
-    rc = rows_ok(w, out, dtype, batch->rows, q_heads, cache->head_size, out_token_stride,
-                 out_head_stride, true);
-  if (rc != CSA_OK) return rc;
-  const size_t need = cache_attention_workspace_bytes(cache->head_size);
-  if (!workspace || workspace_bytes < need)
-    return set_error(CSA_ERR_WORKSPACE, w + ": " + std::to_string(need) +
-                                            " bytes of workspace needed, " +
-                                            std::to_string(workspace ? workspace_bytes : 0) +
-                                            " given");
-  if (!aligned(workspace, 16))
-    return set_error(CSA_ERR_ALIGN, w + ": workspace must be 16-byte aligned");
-  DeviceInfo dev;
-  std::string err;
-  rc = current_device(dev, err);
-  if (rc != CSA_OK) return set_error(rc, err);
-  apply_stream_sm_limit(dev, static_cast<cudaStream_t>(stream));
-  rc = cache_attention_launch(*cache, *batch,
-                              {q, out, dtype, q_heads, q_token_stride, q_head_stride,
-                               out_token_stride, out_head_stride, scale, window, sinks, workspace},
-                              static_cast<cudaStream_t>(stream), dev, err);
-  return rc == CSA_OK ? CSA_OK : set_error(rc, err);
+  return no_throw([&] {
+    t_last_error.clear();
+    const std::string w("cache_attention_forward");
+    int rc = attention_heads_ok(w, cache, q_heads);
+    if (rc == CSA_OK) rc = batch_args_ok(w, batch);
+    if (rc != CSA_OK) return rc;
+    if (!out || !q) return set_error(CSA_ERR_NULL, w + ": null pointer");
+    if (dtype != CSA_BF16 && dtype != CSA_F16)
+      return set_error(CSA_ERR_UNSUPPORTED, w + ": unknown dtype");
+    if (!std::isfinite(scale)) return set_error(CSA_ERR_SHAPE, w + ": scale not finite");
+    if (window < 0 || sinks < 0)
+      return set_error(CSA_ERR_SHAPE, w + ": window and sinks must be >= 0");
+    rc = rows_ok(w, q, dtype, batch->rows, q_heads, cache->head_size, q_token_stride, q_head_stride,
+                 false);
+    if (rc == CSA_OK)
+      rc = rows_ok(w, out, dtype, batch->rows, q_heads, cache->head_size, out_token_stride,
+                   out_head_stride, true);
+    if (rc != CSA_OK) return rc;
+    // A unit reads its own rows of q before it writes them, so in place is fine.
+    const bool in_place = out == q && (batch->rows == 1 || q_token_stride == out_token_stride) &&
+                          (q_heads == 1 || q_head_stride == out_head_stride);
+    const int D = cache->head_size;
+    if (!in_place &&
+        ranges_meet(range_of(q, 2, span_of(batch->rows, q_heads, D, q_token_stride, q_head_stride)),
+                    range_of(out, 2,
+                             span_of(batch->rows, q_heads, D, out_token_stride, out_head_stride))))
+      return set_error(CSA_ERR_UNSUPPORTED, w + ": q and out overlap in part");
+    const size_t need = cache_attention_workspace_bytes(cache->head_size);
+    if (!workspace || workspace_bytes < need)
+      return set_error(CSA_ERR_WORKSPACE, w + ": " + std::to_string(need) +
+                                              " bytes of workspace needed, " +
+                                              std::to_string(workspace ? workspace_bytes : 0) +
+                                              " given");
+    if (!aligned(workspace, 16))
+      return set_error(CSA_ERR_ALIGN, w + ": workspace must be 16-byte aligned");
+    DeviceInfo dev;
+    std::string err;
+    rc = current_device(dev, err);
+    if (rc != CSA_OK) return set_error(rc, err);
+    apply_stream_sm_limit(dev, static_cast<cudaStream_t>(stream));
+    rc = cache_attention_launch(*cache, *batch,
+                                {q, out, dtype, q_heads, q_token_stride, q_head_stride,
+                                 out_token_stride, out_head_stride, scale, window, sinks, workspace},
+                                static_cast<cudaStream_t>(stream), dev, err);
+    return rc == CSA_OK ? CSA_OK : set_error(rc, err);
+  });
 }
 
 }  // extern "C"

@@ -205,7 +205,11 @@ __device__ __forceinline__ void next_piece(const AttendArgs& a, Piece& p) {
       const long long all = static_cast<long long>(p.w.blocks) * a.v.heads * weight;
       if (p.at < p.base + all) break;
       p.base += all;
-      p.w = seq_work<NB, kSub>(a, ++p.s);
+      if (++p.s >= a.v.sequences) {  // lengths changed under the call: nothing more
+        p.at = p.end;
+        return;
+      }
+      p.w = seq_work<NB, kSub>(a, p.s);
     }
     const long long off = p.at - p.base;
     const int unit = static_cast<int>(

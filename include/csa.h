@@ -9,7 +9,11 @@
  * causal softmax of the scores (causal_softmax_forward), the score product
  * over fp32 inputs (trimul_forward_f32), many dense layers sharing W in one
  * launch (dense_xwt_grouped), and an allocation-free score entry point
- * (trimul_forward_noalloc). Each is documented at its declaration below.
+ * (trimul_forward_noalloc). For training on and answering with such layers: rotary
+ * positions and their gradient (rotary_forward, rotary_backward), a paged 8-bit cache of
+ * keys and values (kv_cache_write, kv_cache_read), and attention over that cache for single
+ * tokens and whole prompts (cache_attention_forward). Each is documented at its
+ * declaration below.
  *
  *  trimul_forward  the causal triangular score product of
  *                  "llm.c dev/cuda/trimat_forward.cu" (the CPU referee
@@ -315,12 +319,16 @@ csa_status csa_dense_tiling(int M, int H, int sms, int* bn, int* pairs);
  * csa_set_stream_sm_limit -- later calls of this library on `stream` (a
  * cudaStream_t; NULL is the legacy default stream) size their grids and tilings for
  * at most `max_sms` SMs: persistent kernels launch at most that many CTAs (CTA
- * pairs: max_sms / 2 clusters). Every kernel of this library holds a whole SM per
+ * pairs: max_sms / 2 clusters). Each of these kernels holds a whole SM per
  * CTA (its shared memory), so a call limited to S SMs on one stream and a call
  * limited to the device's SM count minus S on another can run side by side on
  * disjoint SMs, as long as the first is launched first (clusters need whole pairs
  * of SMs). max_sms = 0 removes the limit; a limit above the device's SM count has
- * no effect. Results are the same bits under any limit. Limits are keyed by the
+ * no effect. Results are the same bits under any limit, but for cache_attention_forward,
+ * whose sums are split by it. The rotary and cache calls and the second, short kernel of
+ * cache_attention_forward have small CTAs, of which a limit allows in proportion (8 to 32
+ * for each of max_sms): it bounds their share of the memory system, not the SMs they are
+ * on. Limits are keyed by the
  * stream's handle value, process-wide, for at most 64 streams at once (then
  * CSA_ERR_BUSY); a stream destroyed with a limit set should have it removed
  * first, since a new stream may reuse the handle. Returns CSA_OK, CSA_ERR_SHAPE
@@ -463,8 +471,9 @@ typedef struct csa_kv_cache {
  * (more rows than its length) are neither written nor read; attention gives zeros there.
  * These arrays are read on the device: a sequence whose entries break the rules is skipped,
  * as is a block whose page number is outside [0, pages), and csa_get_status reports
- * CSA_ERR_INDEX. Pages that a call writes belong to one sequence each (prefix pages that
- * several sequences share are full, and only read).
+ * CSA_ERR_INDEX. Pages that a call writes belong to one sequence each and are in its
+ * table once (prefix pages that several sequences share are full, and only read). The
+ * arrays must not change while a call is under way.
  */
 typedef struct csa_kv_batch {
   const int32_t* offsets;
@@ -486,7 +495,8 @@ typedef struct csa_kv_batch {
  *
  * kv_cache_read -- the values code * scale of the batch's rows, rounded once to `dtype`
  * (CSA_BF16, CSA_F16 or CSA_F32), into k and v. The batch may name other rows than those of
- * a write: any sequence's last offsets[s + 1] - offsets[s] tokens.
+ * a write: any sequence's last offsets[s + 1] - offsets[s] tokens. k and v must not share
+ * elements.
  */
 csa_status kv_cache_write(const csa_kv_cache* cache, const csa_kv_batch* batch, const void* k,
                           const void* v, int dtype, int64_t k_token_stride, int64_t k_head_stride,
@@ -502,17 +512,19 @@ csa_status kv_cache_read(void* k, void* v, int dtype, int64_t k_token_stride,
  * over the visible t: t <= p, and with window > 0 also p - t < window or t < sinks. Query
  * heads h share kv head h / (q_heads / heads). A row that sees nothing gives zeros.
  *   out, q     device, [rows][q_heads][head_size] of CSA_BF16 or CSA_F16, strides as above;
+ *              out == q with equal strides is fine, ranges that overlap otherwise are
+ *              refused (CSA_ERR_UNSUPPORTED);
  *   q_heads    a multiple of cache->heads;
  *   scale      finite (the framework's score uses 1/sqrt(head_size));
  *   window     0: none; sinks >= 0 (used with a window);
  *   workspace  device, 16-byte aligned, cache_attention_workspace_size bytes; needs no
  *              clearing, in use until the call's kernels complete: calls that may overlap on
  *              the GPU, replays of captured ones too, need separate workspaces.
- * Codes enter the tensor cores as exact fp16 values; scores, the running maximum, sums and
+ * Codes enter the tensor cores as exact 16-bit values; scores, the running maximum, sums and
  * the output accumulate in fp32; weights are rounded to fp16 (11 bits) for the product with
  * V; the result is rounded once. Visible codes must not be NaN (kv_cache_write stores none).
- * The order of every sum is fixed: same inputs and SM limit, same bits. Asynchronous on
- * `stream`; nothing is allocated.
+ * A query with an infinity or a NaN spoils its own rows only. The order of every sum is
+ * fixed: same inputs and SM limit, same bits. Asynchronous on `stream`; nothing is allocated.
  */
 csa_status cache_attention_forward(void* out, const void* q, int dtype, int q_heads,
                                    int64_t out_token_stride, int64_t out_head_stride,
@@ -528,7 +540,8 @@ csa_status cache_attention_workspace_size(const csa_kv_cache* cache, int q_heads
 /*
  * csa_get_status -- synchronises `stream`, then returns and clears the current
  * device's status word: CSA_OK, or CSA_ERR_TIMEOUT if a kernel's bounded wait
- * ran out since the last call, or CSA_ERR_INDEX (see csa_kv_batch). Returns CSA_ERR_CUDA if synchronisation fails.
+ * ran out since the last call, or CSA_ERR_INDEX if a kernel met an index out of range
+ * (see csa_kv_batch). Returns CSA_ERR_CUDA if synchronisation fails.
  */
 csa_status csa_get_status(void* stream);
 
@@ -551,10 +564,12 @@ const char* csa_version(void);
  * csa_get_wait_limit_ns -- the bound the next launch will use.
  * csa_debug_inject -- when nonzero, the next kernel launch (any entry point)
  *   withholds one hand-off in every CTA: the first operand load (score
- *   products, the softmax's first Q tile, the dense layer's TMA form) or the
- *   first stage arrival (the dense layer's loader-warp forms), so a bounded wait
+ *   products, the softmax's first Q tile, the dense layer's TMA form, the first codes of
+ *   attention over prompts) or the first stage arrival (the dense layer's loader-warp
+ *   forms), so a bounded wait
  *   downstream runs out; the kernel records CSA_ERR_TIMEOUT and returns with its
- *   output incomplete. Consumed by that launch.
+ *   output incomplete. Consumed by that launch (kernels without such waits, those of
+ *   the rotary and cache calls and of attention for few rows, leave it set).
  */
 void csa_set_wait_limit_ns(uint64_t ns);
 uint64_t csa_get_wait_limit_ns(void);

@@ -215,6 +215,58 @@ def test_repeatable_limited_and_captured(new, old, sms):
     check(b, q, out, torch.bfloat16, what="shorter")
 
 
+@pytest.mark.parametrize("new,old", [([1, 4, 2], [300, 50, 0]), ([150, 30], [70, 200])])
+def test_in_place(new, old):
+    """The output over Q itself, inside a packed row: the same bits, its neighbours untouched."""
+    b = ref.Batch(new, old, 2, 64, 32, "e4m3", seed=15, extra_rows=1)
+    q, want = run(b, 4, torch.float16)
+    cache, batch = b.device(csa)
+    packed = torch.full((b.rows, 8, 64), 7.0, dtype=torch.float16, device="cuda")
+    packed[:, 2:6] = q.cuda()
+    n = b.offsets[-1]
+    csa.cache_attention_forward(packed[:, 2:6], packed[:, 2:6], cache, batch)
+    assert csa.get_status() == 0
+    assert torch.equal(packed[:n, 2:6], want[:n])
+    assert torch.equal(packed[n:, 2:6].cpu(), q[n:])
+    assert bool((packed[:, :2] == 7.0).all()) and bool((packed[:, 6:] == 7.0).all())
+
+
+@pytest.mark.parametrize("new,old,window", [([1] * 70, [1] * 69 + [2000], 0), ([1] * 9, [128 * i for i in range(9)], 0),
+                                            ([1, 1, 2], [5000, 3, 40], 200), ([1], [20000], 0)])
+def test_units_shared_by_many_groups(new, old, window):
+    """Runs that end at a unit's first tile, inside it and after it; one-tile units in a row."""
+    b = ref.Batch(new, old, 3, 64, 64, "int8", seed=16)
+    q, out = run(b, 3, torch.bfloat16, window, 4)
+    check(b, q, out, torch.bfloat16, window, 4)
+
+
+def test_withheld_codes_time_out_and_recover():
+    """The prompt kernel's bounded waits: codes that never arrive end in a status."""
+    b = ref.Batch([300, 260], [40, 500], 2, 64, 32, "int8", seed=17)
+    q = b.rows_of(8, torch.bfloat16).cuda()
+    cache, batch = b.device(csa)
+    out = torch.empty_like(q)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    csa.set_stream_sm_limit(st, 2)
+    assert csa.get_status() == 0
+    csa.set_wait_limit_ns(20_000_000)  # 20 ms
+    try:
+        with torch.cuda.stream(st):
+            csa.debug_inject(True)
+            csa.cache_attention_forward(out, q, cache, batch)
+            assert csa.get_status(st) == csa.CSA_ERR_TIMEOUT
+            assert csa.get_status(st) == 0
+            csa.set_wait_limit_ns(0)
+            csa.cache_attention_forward(out, q, cache, batch)
+            assert csa.get_status(st) == 0
+    finally:
+        csa.set_wait_limit_ns(0)
+        csa.debug_inject(False)
+        csa.set_stream_sm_limit(st, 0)
+    check(b, q.cpu(), out, torch.bfloat16, what="after the timeout")
+
+
 def test_workspace_that_is_too_small_or_absent():
     b = ref.Batch([1], [5], 1, 64, 16, "int8")
     cache, batch = b.device(csa)

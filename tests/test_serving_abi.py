@@ -141,6 +141,8 @@ def test_batch_refusals(lib, change, code):
     (dict(t0=132), AL, None), (dict(h1=68), AL, None), (dict(t1=-128), SH, None),
     (dict(t0=64), SH, ("read", "attend")), (dict(h0=32), SH, ("read", "attend")),
     (dict(t1=64), SH, ("read",)),
+    # q over out in part: one element further, or in place with other strides
+    (dict(y=(1 << 20) + 16), UN, ("attend",)), (dict(y=1 << 20, t1=136), UN, ("attend",)),
 ])
 def test_row_refusals(lib, change, code, only):
     c, b = _refs()
