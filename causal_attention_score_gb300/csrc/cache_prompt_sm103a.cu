@@ -113,7 +113,7 @@ struct Layout {
                        kRaw = kV + kSlots * kVBytes,
                        kFactors = kRaw + kRawSlots * 2 * kRawBytes,
                        kBars = kFactors + kFactorSlots * 4 * static_cast<int>(sizeof(Factor)),
-                       kMisc = kBars + 8 * 36, kUnits = kMisc + 32,
+                       kMisc = kBars + 8 * 40, kUnits = kMisc + 32,
                        kTotal = kUnits + kUnitSlots * static_cast<int>(sizeof(Unit));
 };
 
@@ -273,7 +273,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - raw);
   const uint32_t bars = base + L::kBars;
-  auto full = [&](uint32_t s) { return bars + 8u * s; };
+  auto k_full = [&](uint32_t s) { return bars + 8u * s; };
+  auto v_full = [&](uint32_t s) { return bars + 8u * (36 + s); };
   auto empty = [&](uint32_t s) { return bars + 8u * (4 + s); };
   constexpr int kRawSlots = L::kRawSlots;
   auto raw_full = [&](uint32_t s) { return bars + 8u * (28 + s); };
@@ -298,7 +299,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kSlots; ++s) {
-      mbar_init(full(s), kConvertWarps);
+      mbar_init(k_full(s), kConvertWarps);
+      mbar_init(v_full(s), kConvertWarps);
       mbar_init(empty(s), 2);  // one commit of each group's issuer
     }
     for (int s = 0; s < kRawSlots; ++s) {
@@ -638,6 +640,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               st_shared16(at + (((unit + 1) ^ (row & 7)) << 4), y + 4);
             }
           }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(k_full(slot));
           if (j >= 0) {
             codes += L::kRawBytes;
             uint32_t vx[8][kLaneVBytes / 4];
@@ -699,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(full(slot));
+            mbar_arrive(v_full(slot));
             mbar_arrive(raw_empty(rs));
           }
         }
@@ -861,7 +866,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // slots of tiles past this group's own are only given back
       for (int j = -1; j < n_all; ++j, ++it) {
         const uint32_t slot = it % kSlots;
-        if (!mbar_wait_warp_inline(full(slot), (it / kSlots) & 1u, wd, kSiteMmaFull)) {
+        if (!mbar_wait_warp_inline(k_full(slot), (it / kSlots) & 1u, wd, kSiteMmaFull)) {
           ok = false;
           break;
         }
@@ -879,6 +884,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             umma_commit(s_full(g, buffer));
           }
           __syncwarp();
+        }
+        if (!mbar_wait_warp_inline(v_full(slot), (it / kSlots) & 1u, wd, kSiteMmaFull)) {
+          ok = false;
+          break;
         }
         if (j >= 0 && j < n) {
           const uint32_t p = products + j;
