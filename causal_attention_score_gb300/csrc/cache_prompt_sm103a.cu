@@ -251,6 +251,35 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
+// Whether a phase has completed, for a whole warp, without waiting.
+__device__ __forceinline__ bool mbar_poll_warp(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return __shfl_sync(0xFFFFFFFFu, done, 0) != 0;
+}
+
+// For a warp that polls: whether it may go on, `since` being when it began. False (recorded)
+// when the CTA has given up or the time has run out.
+__device__ __forceinline__ bool mbar_time_left(uint64_t since, const Watchdog& wd, int site) {
+  int ok = 1;
+  if (lane_id() == 0) {
+    if (*wd.abort_flag) {
+      ok = 0;
+    } else if (globaltimer_ns() - since > wd.limit_ns) {
+      *wd.abort_flag = 1;
+      if (atomicCAS(wd.status, 0, CSA_ERR_TIMEOUT) == 0) atomicExch(wd.status + 1, site);
+      ok = 0;
+    }
+  }
+  return __shfl_sync(0xFFFFFFFFu, ok, 0) != 0;
+}
+
 // 16-byte global -> shared copy past L1; zeros where bytes is 0.
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint32_t bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
@@ -863,52 +892,77 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!mbar_wait_warp_inline(q_ready(g), q_phase, wd, kSiteMmaFull)) break;
         q_phase ^= 1u;
       }
-      // slots of tiles past this group's own are only given back
-      for (int j = -1; j < n_all; ++j, ++it) {
-        const uint32_t slot = it % kSlots;
-        if (!mbar_wait_warp_inline(k_full(slot), (it / kSlots) & 1u, wd, kSiteMmaFull)) {
-          ok = false;
-          break;
-        }
-        if (j + 1 < n) {
-          tc_fence_after_sync();
-          const uint32_t buffer = (products + j + 1) & 1u;
-          const uint32_t kd = lo + ((L::kK + slot * L::kKBytes) >> 4);
-          if (elect_one()) {
+      // Scores of tile `next_s` and output of tile `next_o`, whichever has its operands
+      // first; S(i) takes the buffer that O(i - 2) has read. Slot e of the unit (K of tile e,
+      // V of tile e - 1) goes back when both are issued.
+      int next_s = 0, next_o = 0, given = 0;
+      uint64_t since = 0;
+      uint32_t spins = 0;
+      while (next_o < n) {
+        bool did = false;
+        if (next_s < n && next_s <= next_o + 1) {
+          const uint32_t at = it + next_s, slot = at % kSlots;
+          if (mbar_poll_warp(k_full(slot), (at / kSlots) & 1u)) {
+            tc_fence_after_sync();
+            const uint32_t buffer = (products + next_s) & 1u;
+            const uint32_t kd = lo + ((L::kK + slot * L::kKBytes) >> 4);
+            if (elect_one()) {
 #pragma unroll
-            for (int s = 0; s < HSP / 16; ++s)
-              umma_f16_ss(s_tmem + buffer * kTile,
-                          qd + (((s >> 2) * (kRows * 128) + (s & 3) * 32) >> 4),
-                          kd + (((s >> 2) * (kTile * 128) + (s & 3) * 32) >> 4), desc_hi, kIdescS,
-                          s > 0);
-            umma_commit(s_full(g, buffer));
+              for (int s = 0; s < HSP / 16; ++s)
+                umma_f16_ss(s_tmem + buffer * kTile,
+                            qd + (((s >> 2) * (kRows * 128) + (s & 3) * 32) >> 4),
+                            kd + (((s >> 2) * (kTile * 128) + (s & 3) * 32) >> 4), desc_hi,
+                            kIdescS, s > 0);
+              umma_commit(s_full(g, buffer));
+            }
+            __syncwarp();
+            ++next_s;
+            did = true;
           }
-          __syncwarp();
         }
-        if (!mbar_wait_warp_inline(v_full(slot), (it / kSlots) & 1u, wd, kSiteMmaFull)) {
-          ok = false;
-          break;
+        if (next_o < next_s) {
+          const uint32_t p = products + next_o, at = it + next_o + 1, slot = at % kSlots;
+          if (mbar_poll_warp(p_ready(g, p & 1u), (p >> 1) & 1u) &&
+              mbar_poll_warp(v_full(slot), (at / kSlots) & 1u)) {
+            tc_fence_after_sync();
+            const uint32_t vd = lo + ((L::kV + slot * L::kVBytes) >> 4);
+            if (elect_one()) {
+#pragma unroll
+              for (int s = 0; s < kTile / 16; ++s)
+                umma_f16_ts(o_tmem, s_tmem + (p & 1u) * kTile + 8 * s, vd + 2 * s, desc_hi, kIdescO,
+                            next_o > 0 || s > 0);
+              umma_commit(pv_done(g, p & 1u));
+            }
+            __syncwarp();
+            ++next_o;
+            did = true;
+          }
         }
-        if (j >= 0 && j < n) {
-          const uint32_t p = products + j;
-          const uint32_t vd = lo + ((L::kV + slot * L::kVBytes) >> 4);
-          if (!mbar_wait_warp_inline(p_ready(g, p & 1u), (p >> 1) & 1u, wd, kSiteMmaTmemEmpty)) {
+        if (did) {
+          while (given <= next_o && next_s >= min(given + 1, n)) {
+            if (elect_one()) umma_commit(empty((it + given) % kSlots));
+            __syncwarp();
+            ++given;
+          }
+          spins = 0;
+        } else if ((++spins & 127u) == 0) {
+          if (spins == 128) since = globaltimer_ns();
+          if (!mbar_time_left(since, wd, kSiteMmaFull)) {
             ok = false;
             break;
           }
-          tc_fence_after_sync();
-          if (elect_one()) {
-#pragma unroll
-            for (int s = 0; s < kTile / 16; ++s)
-              umma_f16_ts(o_tmem, s_tmem + (p & 1u) * kTile + 8 * s, vd + 2 * s, desc_hi, kIdescO,
-                          j > 0 || s > 0);
-            umma_commit(pv_done(g, p & 1u));
-          }
-          __syncwarp();
         }
+      }
+      // slots of tiles past this group's own are only given back
+      for (; ok && given <= n_all; ++given) {
+        const uint32_t at = it + given, slot = at % kSlots;
+        ok = mbar_wait_warp_inline(k_full(slot), (at / kSlots) & 1u, wd, kSiteMmaFull) &&
+             mbar_wait_warp_inline(v_full(slot), (at / kSlots) & 1u, wd, kSiteMmaFull);
+        if (!ok) break;
         if (elect_one()) umma_commit(empty(slot));
         __syncwarp();
       }
+      it += n_all + 1;
       products += n;
     }
     // Every MMA must be complete before TMEM and shared memory go away.
