@@ -11,6 +11,12 @@
 // registers, is the right instruction here: codes go from HBM to registers to
 // the tensor core with no trip through shared memory.
 //
+// Measured: 64 sequences of 300 to 8191 tokens, 16 heads of 128: 138 us, 6.5 TB/s of
+// codes (0.95 of the copy rate); 48 of 100 to 15000 with a window of 4096, 8 kv heads:
+// 62 us (0.72). One sequence of 777 tokens, 12 heads of 64: 8.9 us, all latency (the work
+// list 1.3 us, the way to the first codes 2.5 us, the join 3 us). With 16 rows a block
+// the instructions of a step bound it (4 TB/s at 64 x 4K tokens), not HBM.
+//
 // Roles: mma.m16n8k16 with the cache as its A operand: scores are S^T = K Q^T
 // (16 tokens x 8 rows) and the output O^T = V^T P^T (16 elements x 8 rows), so
 // that 8 rows fill the instruction (with Q as A, 16 would be needed) and the
@@ -36,11 +42,16 @@
 // contiguous bytes of a V row that a lane loads are 16 rows of V^T.
 //
 // Work split: all (sequence, head, row block) units in a row, each of as many
-// tiles of tokens as its rows see; every group of four warps takes an equal run
-// of tiles, wherever it begins and ends, so ragged batches and few sequences
-// alike use every SM. A group that covers a unit writes its rows; the others
-// leave (m, l, O) in the workspace, and a second kernel joins them in a fixed
+// tiles of tokens as its rows see and some for its start (kUnitTiles); every group of
+// four warps takes an equal run of that, wherever it begins and ends, so ragged batches
+// and few sequences alike use every SM. A group that covers a unit writes its rows; the
+// others leave (m, l, O) in the workspace, and a second kernel joins them in a fixed
 // order. The work list is computed on the device from the lengths.
+//
+// Loads: a step's codes are asked for in registers while the step before is computed,
+// and in L2 a step before that; across units too (the next piece of the run is worked
+// out while the one at hand begins). Without the L2 requests the first case takes 2 % more,
+// without those across units another 4 %.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
