@@ -11,6 +11,26 @@
 
 namespace csa {
 
+// Asks for `bytes` (a multiple of 16, at a 16-byte boundary) in L2.
+__device__ __forceinline__ void bulk_prefetch_l2(const void* from, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                   reinterpret_cast<uint64_t>(from)),
+               "r"(bytes)
+               : "memory");
+}
+
+// Two fp32 products and multiply-adds at once, each rounded to nearest.
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
 // Device view of csa_kv_cache + csa_kv_batch.
 struct KvView {
   uint8_t* codes[2];  // K, V: [pages][heads][page_tokens][head_size]

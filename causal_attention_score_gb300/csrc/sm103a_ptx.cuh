@@ -172,14 +172,6 @@ __device__ __forceinline__ bool mbar_wait_warp_inline(uint32_t bar, uint32_t par
   return ok != 0;
 }
 
-// Asks for `bytes` (a multiple of 16, at a 16-byte boundary) in L2.
-__device__ __forceinline__ void bulk_prefetch_l2(const void* from, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
-                   reinterpret_cast<uint64_t>(from)),
-               "r"(bytes)
-               : "memory");
-}
-
 // -------------------------------------------------------------------- TMA --
 
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* m) {
@@ -590,18 +582,6 @@ __device__ __forceinline__ void fma_f32x2(float& y0, float& y1, float x0, float 
       "mov.b64 {%0, %1}, d;\n\t}"
       : "=f"(y0), "=f"(y1)
       : "f"(x0), "f"(x1), "l"(b), "l"(c));
-}
-
-__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
-__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
 }
 
 __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
