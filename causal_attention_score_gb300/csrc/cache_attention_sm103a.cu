@@ -69,10 +69,12 @@
 namespace csa {
 namespace {
 
-// Groups of four warps per CTA (one CTA per SM): 384 threads of 168 registers
-// with one 8-row block, 256 of up to 255 with two.
-template <int NB>
-constexpr int kGroups = NB == 1 ? 3 : 2;
+// Groups of four warps per CTA (one CTA per SM), as many as registers allow: heads of up
+// to 128 elements need 168 a thread with one 8-row block, 255 with two; of up to 64, 128
+// and 168 (64 sequences of 4K tokens, 16 kv heads of 64: 78 us with four groups, 87 with
+// three; 4 kv heads with 16 rows each: 41 with three, 50 with two).
+template <int HSP, int NB>
+constexpr int kGroups = (HSP == 64 ? 4 : 3) - (NB - 1);
 // A warp takes kSub blocks of 16 tokens per step, all in one page: two where pages hold 32
 // tokens or more. A tile is what a group's four warps take.
 template <int kSub>
@@ -85,7 +87,7 @@ constexpr int kTileTokens = 64 * kSub;
 template <int NB, int kSub>
 constexpr int kUnitTiles = (NB == 1 ? 2 : 3) * (2 / kSub);
 constexpr int kMaxSms = 152;
-constexpr int kMaxWorkers = kMaxSms * 3;
+constexpr int kMaxWorkers = kMaxSms * 4;
 constexpr int kMaxRows = 16;
 // Which kernel a sequence's rows go to. Here each block of 16 rows reads the keys again;
 // the prompt kernel reads them once for 256 rows, but nothing splits its units along the
@@ -257,9 +259,9 @@ struct GroupSmem {
 // HSP: head size padded to 64 or 128; kFull: head_size == HSP (no bounds on the
 // element loads).
 template <int HSP, int NB, int kSub, int kFormat, bool kFull>
-__global__ void __launch_bounds__(128 * kGroups<NB>, 1)
+__global__ void __launch_bounds__(128 * kGroups<HSP, NB>, 1)
     attend_rows_sm103a_kernel(const AttendArgs a) {
-  constexpr int kThreads = 128 * kGroups<NB>;
+  constexpr int kThreads = 128 * kGroups<HSP, NB>;
   extern __shared__ __align__(16) uint8_t smem_raw[];
   __shared__ long long s_prefix[kThreads + 1];
   __shared__ long long s_warp[kThreads / 32];
@@ -304,7 +306,7 @@ __global__ void __launch_bounds__(128 * kGroups<NB>, 1)
   const int gi = warp_id >> 2;       // group in the CTA
   const int warp = warp_id & 3;      // warp in the group
   const int gtid = threadIdx.x & 127;
-  const int worker = blockIdx.x * kGroups<NB> + gi;
+  const int worker = blockIdx.x * kGroups<HSP, NB> + gi;
   const long long share = (total + a.workers - 1) / a.workers;
   Smem& sm = groups[gi];
   const int g = lane >> 2, t = lane & 3;
@@ -817,11 +819,11 @@ template <int HSP, int NB, int kSub, int kFormat, bool kFull>
 cudaError_t launch_rows(AttendArgs a, int sms, const DeviceInfo& dev, cudaStream_t stream, int& rc,
                         std::string& err) {
   const auto kernel = attend_rows_sm103a_kernel<HSP, NB, kSub, kFormat, kFull>;
-  const int smem = static_cast<int>(sizeof(GroupSmem<HSP, NB>)) * kGroups<NB>;
-  a.workers = sms * kGroups<NB>;
+  const int smem = static_cast<int>(sizeof(GroupSmem<HSP, NB>)) * kGroups<HSP, NB>;
+  a.workers = sms * kGroups<HSP, NB>;
   rc = set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), smem, dev.device, err);
   if (rc != CSA_OK) return cudaSuccess;
-  cudaError_t e = launch_programmatic(kernel, static_cast<unsigned>(sms), 128 * kGroups<NB>, smem,
+  cudaError_t e = launch_programmatic(kernel, static_cast<unsigned>(sms), 128 * kGroups<HSP, NB>, smem,
                                       stream, a);
   if (e != cudaSuccess) return e;
   return launch_programmatic(attend_join_sm103a_kernel<HSP>,
