@@ -657,15 +657,35 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const uint8_t* codes = gbase + L::kRaw + rs * 2 * L::kRawBytes;
           const uint32_t here = raw_pages[rs];
+          uint32_t vx[8][kLaneVBytes / 4];
+          if (j >= 0) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint8_t* from = codes + L::kRawBytes + (vt + i) * D + vd;
+              if constexpr (kLaneVBytes == 8) {
+                const uint2 x = *reinterpret_cast<const uint2*>(from);
+                vx[i][0] = x.x;
+                vx[i][1] = x.y;
+              } else {
+                vx[i][0] = *reinterpret_cast<const uint32_t*>(from);
+              }
+            }
+          }
           if (j + 1 < n) {
             const uint32_t ks = base + L::kK + slot * L::kKBytes;
             const bool in = (here >> w & 1u) != 0 && chunk * 16 < D;
-#pragma unroll 2
-            for (int i = 0; i < 16; i += kKRows) {
-              const uint32_t row = k_row + i;
-              uint4 x = make_uint4(0, 0, 0, 0);
-              if (in) x = *reinterpret_cast<const uint4*>(codes + row * D + chunk * 16);
-              const uint32_t c[4] = {x.x, x.y, x.z, x.w};
+            uint4 xs[16 / kKRows];  // all of a lane's loads before the first store
+#pragma unroll
+            for (int i = 0; i < 16 / kKRows; ++i) {
+              xs[i] = make_uint4(0, 0, 0, 0);
+              if (in)
+                xs[i] = *reinterpret_cast<const uint4*>(codes + (k_row + i * kKRows) * D +
+                                                        chunk * 16);
+            }
+#pragma unroll
+            for (int i = 0; i < 16 / kKRows; ++i) {
+              const uint32_t row = k_row + i * kKRows;
+              const uint32_t c[4] = {xs[i].x, xs[i].y, xs[i].z, xs[i].w};
               uint32_t y[8];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
@@ -682,24 +702,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(k_full(slot));
           if (j >= 0) {
-            codes += L::kRawBytes;
-            uint32_t vx[8][kLaneVBytes / 4];
             // (what is loaded past the sequence's end, or past head_size, is whatever the
             // slot held, and zeroed)
             const int have = (here >> (4 + (oct >> 1)) & 1u) != 0 && vd < D
                                  ? u.q.length - tile_token(u, j) - vt  // tokens of the octet
                                  : 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint8_t* from = codes + (vt + i) * D + vd;
-              if constexpr (kLaneVBytes == 8) {
-                const uint2 x = *reinterpret_cast<const uint2*>(from);
-                vx[i][0] = x.x;
-                vx[i][1] = x.y;
-              } else {
-                vx[i][0] = *reinterpret_cast<const uint32_t*>(from);
-              }
-            }
             if (__builtin_expect(have < 8, 0)) {
 #pragma unroll
               for (int i = 0; i < 8; ++i)
