@@ -260,6 +260,32 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
+// mbar_wait_warp_inline with every lane looking for itself: nothing to hand round when the
+// phase is complete.
+__device__ __forceinline__ bool mbar_wait_lanes(uint32_t bar, uint32_t parity, const Watchdog& wd,
+                                                int site) {
+  bool ok = true;
+  if (!mbar_test(bar, parity)) {
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t it = 1;; ++it) {
+      if (mbar_test(bar, parity)) break;
+      if ((it & 127u) == 0u) {
+        if (*wd.abort_flag) {
+          ok = false;
+          break;
+        }
+        if (globaltimer_ns() - t0 > wd.limit_ns) {
+          *wd.abort_flag = 1;
+          if (atomicCAS(wd.status, 0, CSA_ERR_TIMEOUT) == 0) atomicExch(wd.status + 1, site);
+          ok = false;
+          break;
+        }
+      }
+    }
+  }
+  return __all_sync(0xFFFFFFFFu, ok);
+}
+
 // Whether a phase has completed, for a whole warp, without waiting.
 __device__ __forceinline__ bool mbar_poll_warp(uint32_t bar, uint32_t parity) {
   uint32_t done;
@@ -488,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t product = products + step, buffer = product & 1u;
         const uint32_t s_tmem = tmem + lanes + g * kRows + buffer * kTile;
         const int tb = tile_token(u, step);
-        if (!mbar_wait_warp_inline(s_full(g, buffer), (product >> 1) & 1u, wd,
+        if (!mbar_wait_lanes(s_full(g, buffer), (product >> 1) & 1u, wd,
                                    kSiteEpilogueFull)) {
           ok = false;
           break;
@@ -649,8 +675,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (n > 0)
         for (int j = -1; j < n; ++j, ++it) {
           const uint32_t slot = it % kSlots, rs = it % kRawSlots;
-          if (!mbar_wait_warp_inline(raw_full(rs), (it / kRawSlots) & 1u, wd, kSiteLoaderEmpty) ||
-              !mbar_wait_warp_inline(empty(slot), ((it / kSlots) & 1u) ^ 1u, wd,
+          if (!mbar_wait_lanes(raw_full(rs), (it / kRawSlots) & 1u, wd, kSiteLoaderEmpty) ||
+              !mbar_wait_lanes(empty(slot), ((it / kSlots) & 1u) ^ 1u, wd,
                                      kSiteLoaderEmpty)) {
             ok = false;
             break;
