@@ -296,7 +296,7 @@ __device__ __forceinline__ bool mbar_poll_warp(uint32_t bar, uint32_t parity) {
       : "=r"(done)
       : "r"(bar), "r"(parity)
       : "memory");
-  return __shfl_sync(0xFFFFFFFFu, done, 0) != 0;
+  return __all_sync(0xFFFFFFFFu, done != 0);
 }
 
 // For a warp that polls: whether it may go on, `since` being when it began. False (recorded)
@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The k-th unit that this CTA works on, for a whole warp; false: a wait ran out.
   auto take_unit = [&](uint32_t k, Unit& u) {
     const uint32_t slot = k % kUnitSlots;
-    if (!mbar_wait_warp_inline(u_full(slot), (k / kUnitSlots) & 1u, wd, kSiteSched)) return false;
+    if (!mbar_wait_lanes(u_full(slot), (k / kUnitSlots) & 1u, wd, kSiteSched)) return false;
     u = reinterpret_cast<const Unit*>(gbase + L::kUnits)[slot];
     __syncwarp();
     if (lane == 0) mbar_arrive(u_empty(slot));
@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // O is the product issued last's until that is complete (the one before it
             // is: this tile's scores were issued later)
             const uint32_t before = product - 1;
-            if (!mbar_wait_warp_inline(pv_done(g, before & 1u), (before >> 1) & 1u, wd,
+            if (!mbar_wait_lanes(pv_done(g, before & 1u), (before >> 1) & 1u, wd,
                                        kSiteEpilogueFull))
               ok = false;
             tc_fence_after_sync();
@@ -620,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       more = next_unit(k);
       if (n > 0) {
         const uint32_t final = products - 1;
-        if (!mbar_wait_warp_inline(pv_done(g, final & 1u), (final >> 1) & 1u, wd,
+        if (!mbar_wait_lanes(pv_done(g, final & 1u), (final >> 1) & 1u, wd,
                                    kSiteEpilogueFull))
           break;
         tc_fence_after_sync();
@@ -856,7 +856,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               Factor{a.scale_log2 * f.k, __log2f(f.v), f.v > 0.0f ? __fdividef(1.0f, f.v) : 0.0f,
                      0.0f};
         if (j == ask && lane == 0) mbar_arrive(u_want);
-        if (!mbar_wait_warp_inline(raw_empty(rs), ((it / kRawSlots) & 1u) ^ 1u, wd,
+        if (!mbar_wait_lanes(raw_empty(rs), ((it / kRawSlots) & 1u) ^ 1u, wd,
                                    kSiteProducerEmpty)) {
           ok = false;
           break;
@@ -931,7 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n_all = __shfl_sync(0xFFFFFFFFu, max(u.n[0], u.n[1]), 0);
       if (n_all == 0) continue;
       if (n > 0) {
-        if (!mbar_wait_warp_inline(q_ready(g), q_phase, wd, kSiteMmaFull)) break;
+        if (!mbar_wait_lanes(q_ready(g), q_phase, wd, kSiteMmaFull)) break;
         q_phase ^= 1u;
       }
       // Scores of tile `next_s` and output of tile `next_o`, whichever has its operands
@@ -942,6 +942,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t spins = 0;
       while (next_o < n) {
         bool did = false;
+        if (next_o < next_s) {
+          const uint32_t p = products + next_o, at = it + next_o + 1, slot = at % kSlots;
+          if (mbar_poll_warp(p_ready(g, p & 1u), (p >> 1) & 1u) &&
+              mbar_poll_warp(v_full(slot), (at / kSlots) & 1u)) {
+            tc_fence_after_sync();
+            const uint32_t vd = lo + ((L::kV + slot * L::kVBytes) >> 4);
+            if (elect_one()) {
+#pragma unroll
+              for (int s = 0; s < kTile / 16; ++s)
+                umma_f16_ts(o_tmem, s_tmem + (p & 1u) * kTile + 8 * s, vd + 2 * s, desc_hi, kIdescO,
+                            next_o > 0 || s > 0);
+              umma_commit(pv_done(g, p & 1u));
+            }
+            __syncwarp();
+            ++next_o;
+            did = true;
+          }
+        }
         if (next_s < n && next_s <= next_o + 1) {
           const uint32_t at = it + next_s, slot = at % kSlots;
           if (mbar_poll_warp(k_full(slot), (at / kSlots) & 1u)) {
@@ -959,24 +977,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             ++next_s;
-            did = true;
-          }
-        }
-        if (next_o < next_s) {
-          const uint32_t p = products + next_o, at = it + next_o + 1, slot = at % kSlots;
-          if (mbar_poll_warp(p_ready(g, p & 1u), (p >> 1) & 1u) &&
-              mbar_poll_warp(v_full(slot), (at / kSlots) & 1u)) {
-            tc_fence_after_sync();
-            const uint32_t vd = lo + ((L::kV + slot * L::kVBytes) >> 4);
-            if (elect_one()) {
-#pragma unroll
-              for (int s = 0; s < kTile / 16; ++s)
-                umma_f16_ts(o_tmem, s_tmem + (p & 1u) * kTile + 8 * s, vd + 2 * s, desc_hi, kIdescO,
-                            next_o > 0 || s > 0);
-              umma_commit(pv_done(g, p & 1u));
-            }
-            __syncwarp();
-            ++next_o;
             did = true;
           }
         }
@@ -998,8 +998,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // slots of tiles past this group's own are only given back
       for (; ok && given <= n_all; ++given) {
         const uint32_t at = it + given, slot = at % kSlots;
-        ok = mbar_wait_warp_inline(k_full(slot), (at / kSlots) & 1u, wd, kSiteMmaFull) &&
-             mbar_wait_warp_inline(v_full(slot), (at / kSlots) & 1u, wd, kSiteMmaFull);
+        ok = mbar_wait_lanes(k_full(slot), (at / kSlots) & 1u, wd, kSiteMmaFull) &&
+             mbar_wait_lanes(v_full(slot), (at / kSlots) & 1u, wd, kSiteMmaFull);
         if (!ok) break;
         if (elect_one()) umma_commit(empty(slot));
         __syncwarp();
