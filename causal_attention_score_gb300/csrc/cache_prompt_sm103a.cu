@@ -184,6 +184,20 @@ __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
   return r;
 }
 
+// A place in a ring of kSize barriers and the parity of its phase.
+template <uint32_t kSize>
+struct Ring {
+  uint32_t slot = 0, phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == kSize) slot = 0, phase ^= 1u;
+  }
+  __device__ __forceinline__ void skip(uint32_t n) {
+    const uint32_t at = slot + n;
+    slot = at % kSize;
+    phase ^= at / kSize & 1u;
+  }
+};
+
 // One lane of a converged warp: its MMAs' operands may stay in uniform registers.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
@@ -665,7 +679,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int chunk = lane % kChunks, k_row = 16 * w + lane / kChunks;
     const int oct = 4 * (w & 1) + (lane & 3), vt = 8 * oct;
     const int vd = (w >> 1) * (HSP / 2) + (lane >> 2) * kLaneVBytes;
-    uint32_t it = 0;  // slots filled
+    Ring<kSlots> to_slot;
+    Ring<kRawSlots> from_slot;
     bool ok = true;
     for (uint32_t k = 0; ok; ++k) {
       Unit u;
@@ -673,11 +688,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = max(u.n[0], u.n[1]);
       // slot j: K of tile j + 1, V of tile j
       if (n > 0)
-        for (int j = -1; j < n; ++j, ++it) {
-          const uint32_t slot = it % kSlots, rs = it % kRawSlots;
-          if (!mbar_wait_lanes(raw_full(rs), (it / kRawSlots) & 1u, wd, kSiteLoaderEmpty) ||
-              !mbar_wait_lanes(empty(slot), ((it / kSlots) & 1u) ^ 1u, wd,
-                                     kSiteLoaderEmpty)) {
+        for (int j = -1; j < n; ++j, to_slot.next(), from_slot.next()) {
+          const uint32_t slot = to_slot.slot, rs = from_slot.slot;
+          if (!mbar_wait_lanes(raw_full(rs), from_slot.phase, wd, kSiteLoaderEmpty) ||
+              !mbar_wait_lanes(empty(slot), to_slot.phase ^ 1u, wd, kSiteLoaderEmpty)) {
             ok = false;
             break;
           }
@@ -920,7 +934,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t desc_hi = static_cast<uint32_t>(desc >> 32), lo = static_cast<uint32_t>(desc);
     const uint32_t s_tmem = tmem + g * kRows, o_tmem = tmem + 2 * kRows + g * HSP;
     const uint32_t qd = lo + ((L::kQ + g * L::kQBytes) >> 4);
-    uint32_t it = 0, products = 0, q_phase = 0;
+    uint32_t products = 0, q_phase = 0;
+    Ring<kSlots> unit_slot;
     bool ok = true;
     for (uint32_t k = 0; ok; ++k) {
       Unit u;
@@ -938,14 +953,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       // first; S(i) takes the buffer that O(i - 2) has read. Slot e of the unit (K of tile e,
       // V of tile e - 1) goes back when both are issued.
       int next_s = 0, next_o = 0, given = 0;
+      Ring<kSlots> at_s = unit_slot, at_o = unit_slot, at_given = unit_slot;
+      at_o.next();
       uint64_t since = 0;
       uint32_t spins = 0;
       while (next_o < n) {
         bool did = false;
         if (next_o < next_s) {
-          const uint32_t p = products + next_o, at = it + next_o + 1, slot = at % kSlots;
+          const uint32_t p = products + next_o, slot = at_o.slot;
           if (mbar_poll_warp(p_ready(g, p & 1u), (p >> 1) & 1u) &&
-              mbar_poll_warp(v_full(slot), (at / kSlots) & 1u)) {
+              mbar_poll_warp(v_full(slot), at_o.phase)) {
             tc_fence_after_sync();
             const uint32_t vd = lo + ((L::kV + slot * L::kVBytes) >> 4);
             if (elect_one()) {
@@ -957,12 +974,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             ++next_o;
+            at_o.next();
             did = true;
           }
         }
         if (next_s < n && next_s <= next_o + 1) {
-          const uint32_t at = it + next_s, slot = at % kSlots;
-          if (mbar_poll_warp(k_full(slot), (at / kSlots) & 1u)) {
+          const uint32_t slot = at_s.slot;
+          if (mbar_poll_warp(k_full(slot), at_s.phase)) {
             tc_fence_after_sync();
             const uint32_t buffer = (products + next_s) & 1u;
             const uint32_t kd = lo + ((L::kK + slot * L::kKBytes) >> 4);
@@ -977,14 +995,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             ++next_s;
+            at_s.next();
             did = true;
           }
         }
         if (did) {
           while (given <= next_o && next_s >= min(given + 1, n)) {
-            if (elect_one()) umma_commit(empty((it + given) % kSlots));
+            if (elect_one()) umma_commit(empty(at_given.slot));
             __syncwarp();
             ++given;
+            at_given.next();
           }
           spins = 0;
         } else if ((++spins & 127u) == 0) {
@@ -996,15 +1016,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       // slots of tiles past this group's own are only given back
-      for (; ok && given <= n_all; ++given) {
-        const uint32_t at = it + given, slot = at % kSlots;
-        ok = mbar_wait_lanes(k_full(slot), (at / kSlots) & 1u, wd, kSiteMmaFull) &&
-             mbar_wait_lanes(v_full(slot), (at / kSlots) & 1u, wd, kSiteMmaFull);
+      for (; ok && given <= n_all; ++given, at_given.next()) {
+        ok = mbar_wait_lanes(k_full(at_given.slot), at_given.phase, wd, kSiteMmaFull) &&
+             mbar_wait_lanes(v_full(at_given.slot), at_given.phase, wd, kSiteMmaFull);
         if (!ok) break;
-        if (elect_one()) umma_commit(empty(slot));
+        if (elect_one()) umma_commit(empty(at_given.slot));
         __syncwarp();
       }
-      it += n_all + 1;
+      unit_slot.skip(static_cast<uint32_t>(n_all) + 1u);
       products += n;
     }
     // Every MMA must be complete before TMEM and shared memory go away.
