@@ -92,12 +92,12 @@ constexpr int kMaxRows = 16;
 // Which kernel a sequence's rows go to. Here each block of 16 rows reads the keys again;
 // the prompt kernel reads them once for 256 rows, but nothing splits its units along the
 // keys. With 8K keys a block of 16 rows of one kv head takes 0.41 us of the whole
-// GPU, 48 rows as much as a unit there (1.18 us) where units fill it; where they do
-// not, its 180 us for the first unit buy this kernel 3 blocks an SM: 1 sequence of 64
-// new tokens (8 rows each, 8 heads) takes 113 us here and 180 us there (64K keys: 808
-// and 1255 us; none: 15 and 23 us), one of 128 tokens 210 and 182 us.
-constexpr int kRowLimit = 48;
-constexpr int kBlocksPerSm = 3;
+// GPU, 32 rows as much as a unit there (0.82 us) where units fill it; where they do
+// not, its 120 us for the first unit buy this kernel 2 blocks an SM: 1 sequence of 64
+// new tokens (8 rows each, 8 heads) takes 113 us here and 130 us there (64K keys: 790
+// and 960 us; none: 15 and 16 us), one of 96 tokens 164 and 131 us.
+constexpr int kRowLimit = 32;
+constexpr int kBlocksPerSm = 2;
 constexpr float kRaise = 8.0f;              // the running maximum is raised past this
 // The running maximum of a row that has seen nothing: finite, so that
 // differences of two of them are 0.
