@@ -43,12 +43,17 @@
 // of MMA at the dense rate (HSP = 128), 1280 at the rates that these shapes run at alone
 // (48 cycles for 128 x 64 x 16 with both operands in shared memory, whose reads bound it;
 // 64 for 128 x 128 x 16 with A in TMEM). Measured: 2 prompts of 4096 tokens, 16 heads of
-// 128: 192 us (716 TFLOP/s); 5 chunks of 200 to 777 tokens after up to 9000, 32 query and
-// 4 kv heads of 64: 197 us. A step takes 2600 cycles: a softmax warp 1600 and 900 of
-// waiting, a conversion warp 2050. No unit is saturated (issue slots 47 %, MUFU 16 %); the
-// warps run straight-line code whose instructions come from beyond the first-level
-// instruction cache, two or three cycles each. Tried without gain: one pass over the
-// scores with the maximum checked afterwards (196 us), four ring slots instead of three (192).
+// 128: 144 us (955 TFLOP/s); 5 chunks of 200 to 777 tokens after up to 9000, 32 query and
+// 4 kv heads of 64: 170 us. A step takes 1900 cycles (1650 with heads of 64): a softmax
+// warp 1450 (1230) and the rest of waiting, a conversion warp 1700 (1160); a unit's end
+// and the next one's first scores 9000. No unit is saturated (tensor pipe 44 %, issue
+// slots 53 %, MUFU 22 %): what counts is the latency of each role's chain. What moved it:
+// waits in which every lane looks at the barrier (one lane looking for its warp: 176 us
+// instead of 147), all of the conversion's loads ahead of its stores (192 / 176), ring
+// places counted instead of divided (147 / 144). Without gain: one pass over the scores
+// with the maximum checked afterwards (155), a fourth ring slot (147), Q as fp16 for
+// bf16 rows, which shortens K's conversion (154), the next unit's Q asked for under the last
+// tile (146).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -641,29 +646,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const float inv_l = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll 1
-      for (int d = 0; d < D; d += 16) {
-        uint32_t x[16];
+      for (int d0 = 0; d0 < D; d0 += 64) {
+        uint32_t x[64];
         if (n > 0) {
-          tmem_ld_16cols(o_tmem + d, x);
+          tmem_ld_64cols(o_tmem + d0, x);
         } else {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = 0u;
+          for (int i = 0; i < 64; ++i) x[i] = 0u;
         }
-        uint32_t y[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float v0 = __uint_as_float(x[2 * i]) * inv_l, v1 = __uint_as_float(x[2 * i + 1]) * inv_l;
-          if (l == 0.0f) v0 = v1 = 0.0f;
-          if (kBf16) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(v0, v1);
-            y[i] = *reinterpret_cast<const uint32_t*>(&b);
-          } else {
-            y[i] = half2_of(v0, v1);
+        for (int d = 0; d < 64; d += 8) {
+          uint32_t y[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float v0 = __uint_as_float(x[d + 2 * i]) * inv_l;
+            float v1 = __uint_as_float(x[d + 2 * i + 1]) * inv_l;
+            if (l == 0.0f) v0 = v1 = 0.0f;
+            if (kBf16) {
+              const __nv_bfloat162 b = __floats2bfloat162_rn(v0, v1);
+              y[i] = *reinterpret_cast<const uint32_t*>(&b);
+            } else {
+              y[i] = half2_of(v0, v1);
+            }
           }
-        }
-        if (live) {
-          reinterpret_cast<uint4*>(to + d)[0] = make_uint4(y[0], y[1], y[2], y[3]);
-          reinterpret_cast<uint4*>(to + d)[1] = make_uint4(y[4], y[5], y[6], y[7]);
+          if (live && d0 + d < D)
+            *reinterpret_cast<uint4*>(to + d0 + d) = make_uint4(y[0], y[1], y[2], y[3]);
         }
       }
       tc_fence_before_sync();  // O may be overwritten after the next unit's p_ready
