@@ -892,8 +892,8 @@ int cache_attention_launch(const csa_kv_cache& cache, const csa_kv_batch& batch,
   a.most_rows = static_cast<int>(std::min<long long>(most_rows, kMaxRows));
   // Rows a block. 16 read the codes of 9 to 16 rows once instead of twice, but cost 8 and
   // fewer a second product for nothing and a third group of warps: 64 sequences of 16 rows
-  // over 4K tokens take 93 us with 16, 109 us with 8; a batch of 4, 8 and 12 rows takes
-  // 102 us with 16, 81 us with 8. So: 16 where a token alone has more than 8, or where
+  // over 4K tokens take 69 us with 16, 81 us with 8; a batch of 4, 8 and 12 rows takes
+  // 81 us with 16, 62 us with 8. So: 16 where a token alone has more than 8, or where
   // the batch's average does (prompts, which are another kernel's, left out of it).
   const bool one = most_rows <= 8 ||
                    (a.group <= 8 && (prompts || batch_rows <= 8LL * batch.sequences));

@@ -326,7 +326,7 @@ csa_status csa_dense_tiling(int M, int H, int sms, int* bn, int* pairs);
  * of SMs). max_sms = 0 removes the limit; a limit above the device's SM count has
  * no effect. Results are the same bits under any limit, but for cache_attention_forward,
  * whose sums are split by it. The rotary and cache calls and the second, short kernel of
- * cache_attention_forward have small CTAs, of which a limit allows in proportion (8 to 32
+ * cache_attention_forward have small CTAs, of which a limit allows in proportion (8 to 48
  * for each of max_sms): it bounds their share of the memory system, not the SMs they are
  * on. Limits are keyed by the
  * stream's handle value, process-wide, for at most 64 streams at once (then
