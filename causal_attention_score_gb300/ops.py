@@ -18,6 +18,18 @@ def _stream_ptr(stream) -> int:
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _torch_stream(stream, device) -> torch.cuda.Stream:
+    """``stream`` (None, a torch stream or a raw handle) as a torch stream of ``device``."""
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    handle = _stream_ptr(stream)
+    # (ExternalStream takes the handle 0, the legacy default stream's, for a new stream)
+    return (torch.cuda.ExternalStream(handle, device=device) if handle
+            else torch.cuda.default_stream(device))
+
+
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, numel: int) -> None:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -95,12 +107,7 @@ def dense_xwt(Y: torch.Tensor, X: torch.Tensor, W: torch.Tensor, M: int, I: int,
         return
     # The workspace is in use until the kernel completes on `stream`: allocated with
     # that stream current, so the caching allocator reuses it only in stream order.
-    if stream is None:
-        st = torch.cuda.current_stream(X.device)
-    elif isinstance(stream, torch.cuda.Stream):
-        st = stream
-    else:
-        st = torch.cuda.ExternalStream(int(stream), device=X.device)
+    st = _torch_stream(stream, X.device)
     with torch.cuda.stream(st):
         ws = torch.empty(nbytes, dtype=torch.uint8, device=X.device)
     rc = lib.dense_xwt_ws(Y.data_ptr(), X.data_ptr(), W.data_ptr(), M, I, H, ws.data_ptr(),

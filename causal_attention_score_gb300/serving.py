@@ -12,7 +12,7 @@ import math
 import torch
 
 from . import _lib
-from .ops import _need
+from .ops import _need, _torch_stream
 
 CSA_BF16, CSA_F16, CSA_F32 = 0, 1, 2
 CSA_KV_INT8, CSA_KV_E4M3 = 0, 1
@@ -315,8 +315,7 @@ def cache_attention_forward(out: torch.Tensor, q: torch.Tensor, cache: KvCache, 
         if stream is None:
             workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
         else:
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(stream), device=q.device)
+            stream = _torch_stream(stream, q.device)
             with torch.cuda.stream(stream):
                 workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
     elif workspace.get_device() != dev:

@@ -1,0 +1,72 @@
+"""Calls on a stream that is not the current one: what the binding allocates and fills for
+them is in that stream's order (GPU). Streams are held by a host function
+(csa_debug_hold_stream), so nothing waits on the GPU."""
+import contextlib
+import time
+
+import pytest
+import torch
+
+import causal_attention_score_gb300 as csa
+import serving_ref as ref
+from causal_attention_score_gb300 import _lib
+
+pytestmark = pytest.mark.gpu
+
+
+@contextlib.contextmanager
+def held(handle: int):
+    """The stream of this handle stands still inside (10 s at most)."""
+    lib = _lib.load()
+    assert lib.csa_debug_hold_stream(handle) == 0
+    try:
+        yield
+    finally:
+        lib.csa_debug_release_streams()
+
+
+def attention_case(seed=3):
+    """A small call: (q, cache, batch), and its result."""
+    b = ref.Batch([2, 1], [90, 40], 2, 64, 32, "int8", seed=seed)
+    cache, batch = b.device(csa)
+    q = b.rows_of(4, torch.bfloat16).cuda()
+    want = csa.cache_attention(q, cache, batch)
+    torch.cuda.synchronize()
+    return q, cache, batch, want
+
+
+class Aside:
+    """Looks at tensors from a stream of its own, whatever the others still have to do."""
+
+    def __init__(self, *tensors):
+        self.stream = torch.cuda.Stream()
+        self.host = [torch.empty(t.shape, dtype=t.dtype, pin_memory=True) for t in tensors]
+
+    def look(self, *tensors):
+        with torch.cuda.stream(self.stream):
+            for h, t in zip(self.host, tensors):
+                h.copy_(t, non_blocking=True)
+        self.stream.synchronize()
+        return self.host
+
+
+def test_raw_handle_of_the_default_stream():
+    """stream=0 is the legacy default stream, also where the binding allocates a workspace."""
+    q, cache, batch, want = attention_case()
+    X, W = (torch.randn((n, 770), device="cuda").to(torch.bfloat16) for n in (96, 64))
+    y = csa.dense(X, W)
+    assert csa.dense_workspace_size(X, W, 96, 770, 64) > 0
+    out, y2 = torch.full_like(want, 7.0), torch.full_like(y, 7.0)
+    csa.cache_attention_forward(torch.empty_like(want), q, cache, batch, stream=0)
+    csa.dense_xwt(torch.empty_like(y), X, W, 96, 770, 64, stream=0)
+    aside = Aside(out, y2)
+    aside.look(out, y2)
+    torch.cuda.synchronize()
+    with held(0):
+        csa.cache_attention_forward(out, q, cache, batch, stream=0)
+        csa.dense_xwt(y2, X, W, 96, 770, 64, stream=0)
+        time.sleep(0.1)
+        early = aside.look(out, y2)
+    torch.cuda.synchronize()
+    assert all(bool((t == 7.0).all()) for t in early), "ran past the held stream"
+    assert torch.equal(out, want) and torch.equal(y2, y)
