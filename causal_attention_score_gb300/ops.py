@@ -30,6 +30,19 @@ def _torch_stream(stream, device) -> torch.cuda.Stream:
             else torch.cuda.default_stream(device))
 
 
+def _allocate(make, shape, dtype, device, stream) -> torch.Tensor:
+    """``make(shape)`` (torch.empty, torch.zeros) for a call on ``stream``: its memory and what
+    fills it are in that stream's order."""
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    current, stream = torch.cuda.current_stream(device), _torch_stream(stream, device)
+    with torch.cuda.stream(stream):
+        t = make(shape, dtype=dtype, device=device)
+    if stream != current:
+        t.record_stream(current)  # the caller may read it there, and let go of it at any time
+    return t
+
+
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, numel: int) -> None:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")

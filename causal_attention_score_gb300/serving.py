@@ -12,7 +12,7 @@ import math
 import torch
 
 from . import _lib
-from .ops import _need, _torch_stream
+from .ops import _allocate, _need, _torch_stream
 
 CSA_BF16, CSA_F16, CSA_F32 = 0, 1, 2
 CSA_KV_INT8, CSA_KV_E4M3 = 0, 1
@@ -334,7 +334,8 @@ def cache_attention_forward(out: torch.Tensor, q: torch.Tensor, cache: KvCache, 
 
 def cache_attention(q: torch.Tensor, cache: KvCache, batch: KvBatch, scale: float | None = None,
                     window: int = 0, sinks: int = 0, stream=None) -> torch.Tensor:
-    """Allocating form of cache_attention_forward; rows of no sequence are zero."""
-    out = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+    """Allocating form of cache_attention_forward; rows of no sequence are zero. The output is
+    allocated and cleared on the call's stream."""
+    out = _allocate(torch.zeros, q.shape, q.dtype, q.device, stream)
     cache_attention_forward(out, q, cache, batch, scale, window, sinks, None, stream)
     return out

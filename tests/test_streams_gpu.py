@@ -70,3 +70,26 @@ def test_raw_handle_of_the_default_stream():
     torch.cuda.synchronize()
     assert all(bool((t == 7.0).all()) for t in early), "ran past the held stream"
     assert torch.equal(out, want) and torch.equal(y2, y)
+
+
+def test_allocating_attention_while_the_current_stream_is_busy():
+    """cache_attention(stream=B) with the current stream held: its zeros and its rows are in
+    B's order, so the result is there when B is done and stays."""
+    q, cache, batch, want = attention_case()
+    host_want = want.cpu()
+    A, B = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(2):  # (once for the allocator's blocks and the modules)
+        with torch.cuda.stream(B):
+            csa.cache_attention(q, cache, batch)
+    aside = Aside(want)
+    aside.look(want)
+    torch.cuda.synchronize()
+    for stream in (B, B.cuda_stream):
+        with torch.cuda.stream(A), held(A.cuda_stream):
+            out = csa.cache_attention(q, cache, batch, stream=stream)
+            B.synchronize()
+            early, = aside.look(out)
+            assert torch.equal(early, host_want)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    assert csa.get_status() == 0
