@@ -232,7 +232,7 @@ def causal_softmax(qkv: torch.Tensor, stream=None) -> torch.Tensor:
     B, T, three, NH, HS = qkv.shape
     if three != 3:
         raise ValueError("qkv must have shape (B, T, 3, NH, HS)")
-    att = torch.empty((B, NH, T, T), dtype=torch.float32, device=qkv.device)
+    att = _allocate(torch.empty, (B, NH, T, T), torch.float32, qkv.device, stream)
     causal_softmax_forward(att, qkv, B, T, NH * HS, NH, stream=stream)
     return att
 
@@ -242,7 +242,7 @@ def trimul(qkv: torch.Tensor, mask="nan", lower_only: bool = False, stream=None)
     B, T, three, NH, HS = qkv.shape
     if three != 3:
         raise ValueError("qkv must have shape (B, T, 3, NH, HS)")
-    out = torch.empty((B, NH, T, T), dtype=torch.float32, device=qkv.device)
+    out = _allocate(torch.empty, (B, NH, T, T), torch.float32, qkv.device, stream)
     trimul_forward(out, qkv, B, T, NH * HS, NH, mask=mask, lower_only=lower_only, stream=stream)
     return out
 
@@ -253,7 +253,7 @@ def dense(X: torch.Tensor, W: torch.Tensor, stream=None) -> torch.Tensor:
     H, I2 = W.shape
     if I2 != I:
         raise ValueError("X and W disagree on I")
-    Y = torch.empty((M, H), dtype=torch.float32, device=X.device)
+    Y = _allocate(torch.empty, (M, H), torch.float32, X.device, stream)
     dense_xwt(Y, X, W, M, I, H, stream=stream)
     return Y
 

@@ -93,3 +93,34 @@ def test_allocating_attention_while_the_current_stream_is_busy():
         torch.cuda.synchronize()
         assert torch.equal(out, want)
     assert csa.get_status() == 0
+
+
+@pytest.mark.parametrize("which", ["trimul", "causal_softmax", "dense", "cache_attention"])
+def test_allocating_forms_leave_the_current_stream_its_memory(which):
+    """What the current stream has freed but still has to read is not what a call on another
+    stream gets for its output."""
+    g = torch.Generator().manual_seed(2)
+    qkv = torch.randn((1, 200, 3, 2, 64), generator=g).to(torch.bfloat16).cuda()
+    X, W = (torch.randn((n, 768), generator=g).to(torch.bfloat16).cuda() for n in (300, 256))
+    if which == "cache_attention":
+        q, cache, batch, _ = attention_case()
+    call = {"trimul": lambda st: csa.trimul(qkv, mask="-inf", stream=st),
+            "causal_softmax": lambda st: csa.causal_softmax(qkv, stream=st),
+            "dense": lambda st: csa.dense(X, W, stream=st),
+            "cache_attention": lambda st: csa.cache_attention(q, cache, batch, stream=st)}[which]
+    want = call(None)
+    A, B = torch.cuda.Stream(), torch.cuda.Stream()
+    call(B)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(A):
+        t, keep = torch.full_like(want, 5.0), torch.empty_like(want)
+        A.synchronize()
+        with held(A.cuda_stream):
+            keep.copy_(t)
+            del t
+            out = call(B)
+            B.synchronize()
+    torch.cuda.synchronize()
+    assert bool((keep == 5.0).all()), "the output took memory that the current stream still read"
+    assert torch.equal(out, want)
+    assert csa.get_status() == 0
