@@ -155,8 +155,9 @@ class DenseGroupedPlan:
 
     When no tensor map can describe the rows (I * 2 not a multiple of 16, or a
     misaligned view), the plan also holds the workspace dense_xwt_grouped_ws copies
-    them into (torch memory, allocated once with the plan), so the batch still runs as
-    one grouped launch; calls of one plan must then not overlap on the GPU.
+    them into (torch memory, allocated once with the plan on the current stream: calls on
+    another one have to come after that stream's work until then), so the batch still runs
+    as one grouped launch; calls of one plan must then not overlap on the GPU.
     """
 
     def __init__(self, Ys, Xs, W: torch.Tensor, I: int, H: int):
@@ -193,6 +194,9 @@ class DenseGroupedPlan:
         if [t.data_ptr() for t in self._tensors] != self._ptrs:
             raise ValueError("a tensor of this DenseGroupedPlan no longer has the storage it "
                              "was planned with; make a new plan")
+        if self._ws is not None:  # kept until the call is done, whoever lets go of the plan
+            stream = _torch_stream(stream, self._ws.device)
+            self._ws.record_stream(stream)
         rc = _lib.load().dense_xwt_grouped_ws(*self._args, *self._ws_args, _stream_ptr(stream))
         _lib.check(rc, "dense_xwt_grouped")
 
@@ -201,7 +205,11 @@ def dense_xwt_grouped(Ys, Xs, W: torch.Tensor, I: int, H: int, stream=None) -> N
     """Y[g] = X[g] W^T for every g, one launch per 48 problems: fp32 Y[g] [M_g, H] from
     bf16 X[g] [M_g, I] and the shared W [H, I]; see dense_xwt_grouped in include/csa.h.
     For repeated calls on the same tensors, DenseGroupedPlan checks them once."""
-    DenseGroupedPlan(Ys, Xs, W, I, H)(stream)
+    if stream is None:
+        DenseGroupedPlan(Ys, Xs, W, I, H)()
+        return
+    with torch.cuda.stream(_torch_stream(stream, W.device)):  # whose workspace is in its order
+        DenseGroupedPlan(Ys, Xs, W, I, H)(stream)
 
 
 def batch_matmul_nt(Y: torch.Tensor, X: torch.Tensor, W: torch.Tensor, batch: int, T1: int,

@@ -124,3 +124,61 @@ def test_allocating_forms_leave_the_current_stream_its_memory(which):
     assert bool((keep == 5.0).all()), "the output took memory that the current stream still read"
     assert torch.equal(out, want)
     assert csa.get_status() == 0
+
+
+def grouped_case():
+    """A batch whose rows no tensor map can describe: (Ys, Xs, W, its workspace's bytes)."""
+    g = torch.Generator().manual_seed(3)
+    Xs = [torch.randn((m, 770), generator=g).to(torch.bfloat16).cuda() for m in (500, 301)]
+    W = torch.randn((256, 770), generator=g).to(torch.bfloat16).cuda()
+    Ys = [torch.zeros((len(X), 256), device="cuda") for X in Xs]
+    return Ys, Xs, W, csa.DenseGroupedPlan(Ys, Xs, W, 770, 256)._ws.numel()
+
+
+def test_grouped_workspace_is_in_the_calls_order():
+    """dense_xwt_grouped(stream=B): its workspace is not memory that the current stream still
+    reads, nor does that stream get it while the call is under way."""
+    Ys, Xs, W, nbytes = grouped_case()
+    csa.dense_xwt_grouped(Ys, Xs, W, 770, 256)
+    want = [Y.clone() for Y in Ys]
+    A, B = torch.cuda.Stream(), torch.cuda.Stream()
+    csa.dense_xwt_grouped(Ys, Xs, W, 770, 256, stream=B)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(A):
+        t = torch.full((nbytes,), 5, dtype=torch.uint8, device="cuda")
+        keep = torch.empty_like(t)
+        A.synchronize()
+        with held(A.cuda_stream):
+            keep.copy_(t)
+            del t
+            csa.dense_xwt_grouped(Ys, Xs, W, 770, 256, stream=B)
+            B.synchronize()
+        torch.cuda.synchronize()
+        assert bool((keep == 5).all()), "took memory that the current stream still read"
+        with held(B.cuda_stream):
+            csa.dense_xwt_grouped(Ys, Xs, W, 770, 256, stream=B)
+            t = torch.full((nbytes,), 7, dtype=torch.uint8, device="cuda")
+            A.synchronize()
+        torch.cuda.synchronize()
+        assert bool((t == 7).all()), "gave memory back before the call was done with it"
+    assert all(torch.equal(Y, w) for Y, w in zip(Ys, want))
+
+
+def test_plan_let_go_while_its_call_is_under_way():
+    """A plan made on one stream, called on another and let go of: its workspace stays the call's."""
+    Ys, Xs, W, nbytes = grouped_case()
+    csa.dense_xwt_grouped(Ys, Xs, W, 770, 256)
+    want = [Y.clone() for Y in Ys]
+    A, B = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(A):
+        plan = csa.DenseGroupedPlan(Ys, Xs, W, 770, 256)
+        A.synchronize()
+        with held(B.cuda_stream):
+            plan(B)
+            del plan
+            t = torch.full((nbytes,), 7, dtype=torch.uint8, device="cuda")
+            A.synchronize()
+        torch.cuda.synchronize()
+        assert bool((t == 7).all())
+    assert all(torch.equal(Y, w) for Y, w in zip(Ys, want))
