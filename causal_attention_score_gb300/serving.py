@@ -94,17 +94,23 @@ class RotaryTable:
         self.turns = torch.tensor(signed, dtype=torch.int64).to(device)
 
 
+def _flat(t: torch.Tensor, name: str) -> torch.Tensor:
+    """(B, T, heads, size) whose tokens are one stride apart, through all batches, as
+    [B * T, heads, size]; with one token a batch that is the batches' stride."""
+    B, T, heads, size = t.shape
+    batch, token, head, one = t.stride()
+    if T == 1:
+        token = batch
+    elif B > 1 and batch != T * token:
+        raise ValueError(f"{name}: a 4-D tensor's batches must follow one another")
+    return t.as_strided((B * T, heads, size), (token, head, one))
+
+
 def _rotary(which: str, out, x, table, positions, start, period, interleaved, stream) -> None:
-    if x.dim() == 4:  # (B, T, heads, size) whose batches follow one another
-        if x.shape[0] > 1 and x.stride(0) != x.shape[1] * x.stride(1):
-            raise ValueError("x: a 4-D tensor's batches must follow one another")
-        if out.shape[0] > 1 and out.stride(0) != out.shape[1] * out.stride(1):
-            raise ValueError("out: a 4-D tensor's batches must follow one another")
+    if x.dim() == 4:
         if out.shape != x.shape:
             raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(x.shape)}")
-        B, T = x.shape[0], x.shape[1]
-        x = x.as_strided((B * T, x.shape[2], x.shape[3]), x.stride()[1:])
-        out = out.as_strided(x.shape, out.stride()[1:])
+        x, out = _flat(x, "x"), _flat(out, "out")
     if x.dim() != 3:
         raise ValueError("x must be [tokens, heads, size] or [B, T, heads, size]")
     dev = _device_of(x, "x")
@@ -136,8 +142,9 @@ def rotary_forward(out: torch.Tensor, x: torch.Tensor, table: RotaryTable, posit
     """Turns every head's first ``table.rot_dim`` elements by its token's position into
     ``out`` (``x`` itself, or a tensor apart from it): [tokens, heads, size] or
     [B, T, heads, size], bf16, fp16 or fp32. ``positions`` int32, one per token (negative:
-    padding, left as it is), or None for ``start + (t % period if period else t)``; see
-    rotary_forward in include/csa.h."""
+    padding, left as it is), or None for ``start + (t % period if period else t)``, t counting
+    the tokens through all batches (``period=T`` starts each batch anew); see rotary_forward
+    in include/csa.h."""
     _rotary("rotary_forward", out, x, table, positions, start, period, interleaved, stream)
 
 
