@@ -556,6 +556,9 @@ __global__ void __launch_bounds__(128 * kGroups<HSP, NB>, 1)
                   mma_f16(sc[u][b], a0, a1, a2, a3, q4[b][2 * k], q4[b][2 * k + 1]);
               }
           }
+        // A block of scale 0 holds zeros, at any scale.
+        const bool zeros = vs == 0.0f;
+        vs = fmaxf(vs, kScaleFloor);
         const float lv = __log2f(vs), inv = __fdividef(1.0f, vs);
         float fk[NB][2];
 #pragma unroll
@@ -632,13 +635,14 @@ __global__ void __launch_bounds__(128 * kGroups<HSP, NB>, 1)
             pb[u][b][0] = transpose_8x8(half2_of(x[u][b][0], x[u][b][1]));
             pb[u][b][1] = transpose_8x8(half2_of(x[u][b][2], x[u][b][3]));
           }
-        if (last >= length) {
+        if (last >= length || zeros) {
           // slots past the sequence's end may hold the codes of no number
+          const int end = zeros ? 0 : length;
 #pragma unroll
           for (int u = 0; u < kSub; ++u)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              if (tb + 16 * u + 2 * t + (k & 1) + 8 * (k >> 1) >= length) {
+              if (tb + 16 * u + 2 * t + (k & 1) + 8 * (k >> 1) >= end) {
 #pragma unroll
                 for (int j = 0; j < kVWords; ++j) vr[u][k][j] = 0;
               }

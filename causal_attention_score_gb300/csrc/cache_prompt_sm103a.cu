@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem_slot = base + L::kMisc;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + L::kMisc + 4);
   Factor* factors = reinterpret_cast<Factor*>(gbase + L::kFactors);
-  // Bit i: the 16 tokens i of a raw slot's K (bits 4..7: V) have a page.
+  // Bit i: the 16 tokens i of a raw slot's K (bits 4..7: V) have codes there.
   volatile uint32_t* raw_pages = reinterpret_cast<volatile uint32_t*>(gbase + L::kMisc + 16);
   const Watchdog wd{a.wait_limit_ns, a.status, abort_flag};
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -853,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float k, v;
       };
       auto scales_of = [&](int pg) {
-        Scales f{1.0f, 0.0f};  // log2 of 0: -inf, which masks the 16 tokens
+        Scales f{1.0f, 1.0f};
         if (pg >= 0) {
           const long long unit = static_cast<long long>(pg) * a.v.heads + u.head;
           f.k = __ldg(a.v.scale[0] + unit);
@@ -872,10 +872,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint8_t* k_from = part_of(u, j + 1, page, 0);
         const uint8_t* v_from = part_of(u, j, page_v, 1);
         const uint32_t to = base + L::kRaw + rs * 2 * L::kRawBytes + 16 * lane * D;
+        // -inf masks 16 tokens of no page. A block of scale 0 holds zeros, at any scale (and
+        // its V is not copied).
+        const float scale_v = fmaxf(f.v, kScaleFloor);
         if (j + 1 < n && lane < 4)
           factors[((tiles + j + 1) % kFactorSlots) * 4 + lane] =
-              Factor{a.scale_log2 * f.k, __log2f(f.v), f.v > 0.0f ? __fdividef(1.0f, f.v) : 0.0f,
-                     0.0f};
+              Factor{a.scale_log2 * f.k, page >= 0 ? __log2f(scale_v) : -INFINITY,
+                     __fdividef(1.0f, scale_v), 0.0f};
         if (j == ask && lane == 0) mbar_arrive(u_want);
         if (!mbar_wait_lanes(raw_empty(rs), ((it / kRawSlots) & 1u) ^ 1u, wd,
                                    kSiteProducerEmpty)) {
@@ -893,7 +896,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (k_here && copies) bulk_load(to, k_from, copy_bytes, raw_full(rs));
           if (v_here && copies) bulk_load(to + L::kRawBytes, v_from, copy_bytes, raw_full(rs));
         }
-        page_v = j + 1 < n ? page : -1;
+        page_v = j + 1 < n && f.v != 0.0f ? page : -1;
         page = page2;
         f = f2;
         page2 = j + 3 < n ? pages_of(u, j + 3, entry) : -1;

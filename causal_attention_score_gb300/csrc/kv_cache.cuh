@@ -31,6 +31,8 @@ __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c
   return d;
 }
 
+constexpr float kScaleFloor = 7.888609052210118e-31f;  // 2^-100, the smallest scale written
+
 // Device view of csa_kv_cache + csa_kv_batch.
 struct KvView {
   uint8_t* codes[2];  // K, V: [pages][heads][page_tokens][head_size]

@@ -53,7 +53,6 @@ constexpr int kStepVecs = 4;
 constexpr int kBlockVecs = 8;
 constexpr int kWritePerSm = 4;  // CTAs by registers; the grid has kWriteGrid an SM
 constexpr int kWriteGrid = 8;
-constexpr float kScaleFloor = 7.888609052210118e-31f;  // 2^-100
 
 struct CacheArgs {
   KvView v;

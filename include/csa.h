@@ -440,7 +440,8 @@ csa_status csa_rotary_turns(uint64_t* turns, int rot_dim, double base, int scali
  * tokens of one sequence; each (page, head) is a block with one fp32 scale for K and one
  * for V, and its values are code * scale.
  *   k, v              device, 8-bit codes [pages][heads][page_tokens][head_size], 16-byte aligned;
- *   k_scale, v_scale  device, fp32 [pages][heads];
+ *   k_scale, v_scale  device, fp32 [pages][heads]: 0 (a block of zeros), or from 2^-100 up,
+ *                     finite;
  *   page_tokens       16, 32, 64 or 128;
  *   head_size         a multiple of 16, at most 128;
  *   format            CSA_KV_INT8 (codes -127 .. 127) or CSA_KV_E4M3 (the 8-bit float of 4
