@@ -203,6 +203,7 @@ struct Piece {
   SeqWork w;
   int s;
   int head, row_first, rows;  // the unit
+  int hidden_to;              // keys below this, from a.sinks on, are no row's to see
   int tile0, count;           // its tiles [tile0, tile0 + count); count 0: no more pieces
   long long after;            // what the unit counts past this piece
 };
@@ -238,6 +239,7 @@ __device__ __forceinline__ void next_piece(const AttendArgs& a, Piece& p) {
     p.head = unit / p.w.blocks;
     p.row_first = (unit - p.head * p.w.blocks) * (8 * NB);
     p.rows = min(p.w.rows - p.row_first, 8 * NB);
+    p.hidden_to = a.window > 0 ? p.w.q.first + p.row_first / a.group - a.window + 1 : 0;
     return;
   }
 }
@@ -362,6 +364,7 @@ __global__ void __launch_bounds__(128 * kGroups<HSP, NB>, 1)
                   kTileTokens<kSub> +
               warp * (16 * kSub);
       if (first >= p.w.q.length) return -1;
+      if (a.window != 0 && first >= a.sinks && first + 16 * kSub <= p.hidden_to) return -1;
       const int page = kv_page(a.v, p.s, first >> a.v.page_shift);
       return page < 0 ? -1 : page * a.v.heads + p.head;
     };
@@ -635,17 +638,23 @@ __global__ void __launch_bounds__(128 * kGroups<HSP, NB>, 1)
             pb[u][b][0] = transpose_8x8(half2_of(x[u][b][0], x[u][b][1]));
             pb[u][b][1] = transpose_8x8(half2_of(x[u][b][2], x[u][b][3]));
           }
-        if (last >= length || zeros) {
-          // slots past the sequence's end may hold the codes of no number
+        // Slots past the sequence's end, and those that no row's window reaches, may hold the
+        // codes of no number (int8 has none: there a weight of 0 is enough).
+        if (last >= length || zeros ||
+            (kFormat == CSA_KV_E4M3 && a.window != 0 && pos_low - tb >= a.window)) {
+          const int hidden_to = a.window != 0 ? pos_low - a.window + 1 : 0;
           const int end = zeros ? 0 : length;
 #pragma unroll
           for (int u = 0; u < kSub; ++u)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (tb + 16 * u + 2 * t + (k & 1) + 8 * (k >> 1) >= end) {
+            for (int k = 0; k < 4; ++k) {
+              const int tok = tb + 16 * u + 2 * t + (k & 1) + 8 * (k >> 1);
+              if (tok >= end ||
+                  (kFormat == CSA_KV_E4M3 && tok < hidden_to && tok >= a.sinks)) {
 #pragma unroll
                 for (int j = 0; j < kVWords; ++j) vr[u][k][j] = 0;
               }
+            }
         }
 #pragma unroll
         for (int u = 0; u < kSub; ++u)

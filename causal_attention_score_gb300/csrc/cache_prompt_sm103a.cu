@@ -113,6 +113,7 @@ struct Unit {
   KvSequence q;
   int s, head, row0, rows;  // rows [row0, row0 + rows) of the sequence
   int sink_tiles, window_tile;
+  int hidden_to;            // keys below this, from a.sinks on, are no row's to see
   int n[2];                 // tiles of each group; n[0] < 0: the list has ended
 };
 
@@ -162,9 +163,10 @@ __device__ Unit decode_unit(const PromptArgs& a, const long long* prefix, const 
   r.head = i - back * a.v.heads;
   r.row0 = (blocks - 1 - back) * kUnitRows;
   r.rows = min(all_rows - r.row0, kUnitRows);
-  r.sink_tiles = r.window_tile = 0;
+  r.sink_tiles = r.window_tile = r.hidden_to = 0;
   if (a.window > 0) {
     const int from = max(max(r.q.first + r.row0 / a.group, 0) - a.window + 1, 0);
+    r.hidden_to = from;
     r.window_tile = from / kTile;
     r.sink_tiles = min((min(a.sinks, from) + kTile - 1) / kTile, r.window_tile);
   }
@@ -749,17 +751,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(k_full(slot));
           if (j >= 0) {
-            // (what is loaded past the sequence's end, or past head_size, is whatever the
-            // slot held, and zeroed)
-            const int have = (here >> (4 + (oct >> 1)) & 1u) != 0 && vd < D
-                                 ? u.q.length - tile_token(u, j) - vt  // tokens of the octet
-                                 : 0;
-            if (__builtin_expect(have < 8, 0)) {
+            // (what is loaded past the sequence's end, where no row's window reaches, or past
+            // head_size, is whatever the slot held, and zeroed)
+            const int from = tile_token(u, j) + vt;  // the octet's first token
+            const int have =
+                (here >> (4 + (oct >> 1)) & 1u) != 0 && vd < D ? u.q.length - from : 0;
+            if (__builtin_expect(have < 8 || from < u.hidden_to, 0)) {
 #pragma unroll
               for (int i = 0; i < 8; ++i)
 #pragma unroll
                 for (int c = 0; c < kLaneVBytes / 4; ++c)
-                  if (i >= have) vx[i][c] = 0;
+                  if (i >= have || (from + i < u.hidden_to && from + i >= a.sinks)) vx[i][c] = 0;
             }
             const uint32_t vs = base + L::kV + slot * L::kVBytes;
 #pragma unroll
@@ -807,28 +809,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true, injected = false;
     const int P = a.v.page_tokens, page_mask = P - 1;
     const long long page_bytes = static_cast<long long>(P) * D;
-    // The table's entries for a tile's four groups of 16 tokens, in lanes 0..3; read a
-    // step before they are checked, so that nothing waits for them.
-    auto entries_of = [&](const Unit& u, int j) {
-      const int tok = tile_token(u, j) + 16 * lane;
-      return lane < 4 && tok < u.q.length
-                 ? __ldg(a.v.table + (static_cast<long long>(u.s) * a.v.table_width +
-                                      (tok >> a.v.page_shift)))
-                 : -1;
-    };
-    auto pages_of = [&](const Unit& u, int j, int entry) {  // -1: none there
-      if (lane < 4 && tile_token(u, j) + 16 * lane < u.q.length &&
-          (entry < 0 || entry >= a.v.pages)) {
-        report_index(a.v.status, kIndexPage);
-        return -1;
-      }
-      return entry;
-    };
     // Lanes that copy: the first of each page's groups in the tile.
     const int groups = min(P, kTile) / 16;  // of a page in a tile
     const bool copies = lane < 4 && lane % groups == 0;
     const uint32_t copy_mask = __ballot_sync(0xFFFFFFFFu, copies);
     const uint32_t copy_bytes = static_cast<uint32_t>(groups) * 16u * D;
+    // The table's entries for a tile's four groups of 16 tokens, in lanes 0..3; read a
+    // step before they are checked, so that nothing waits for them. (None past the length,
+    // nor where no row sees any of a page's tokens in the tile.)
+    struct Entry {
+      int page;
+      bool there;
+    };
+    const int before = lane % groups * 16, after = groups * 16 - before;
+    auto entries_of = [&](const Unit& u, int j) {
+      const int tok = tile_token(u, j) + 16 * lane;
+      Entry e{-1, lane < 4 && tok < u.q.length &&
+                      (tok + after > u.hidden_to || tok - before < a.sinks)};
+      if (e.there)
+        e.page = __ldg(a.v.table + (static_cast<long long>(u.s) * a.v.table_width +
+                                    (tok >> a.v.page_shift)));
+      return e;
+    };
+    auto pages_of = [&](const Entry& e) {  // -1: none there
+      if (e.there && (e.page < 0 || e.page >= a.v.pages)) {
+        report_index(a.v.status, kIndexPage);
+        return -1;
+      }
+      return e.page;
+    };
     auto part_of = [&](const Unit& u, int j, int page, int which) {  // of a page: this lane's
       return a.v.codes[which] + (static_cast<long long>(page) * a.v.heads + u.head) * page_bytes +
              ((tile_token(u, j) + 16 * lane) & page_mask) * D;
@@ -846,9 +855,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // A pipeline over the tiles, as each stage waits for the one before: the table's
       // entry (read), the page (checked), its scales (read), the copy.
       int page_v = -1;                              // of tile j
-      int page = pages_of(u, 0, entries_of(u, 0));  // of tile j + 1
-      int page2 = n > 1 ? pages_of(u, 1, entries_of(u, 1)) : -1;
-      int entry = n > 2 ? entries_of(u, 2) : -1;    // of tile j + 3
+      const Entry none{-1, false};
+      int page = pages_of(entries_of(u, 0));        // of tile j + 1
+      int page2 = n > 1 ? pages_of(entries_of(u, 1)) : -1;
+      Entry entry = n > 2 ? entries_of(u, 2) : none;  // of tile j + 3
       struct Scales {
         float k, v;
       };
@@ -899,9 +909,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         page_v = j + 1 < n && f.v != 0.0f ? page : -1;
         page = page2;
         f = f2;
-        page2 = j + 3 < n ? pages_of(u, j + 3, entry) : -1;
+        page2 = j + 3 < n ? pages_of(entry) : -1;
         f2 = scales_of(page2);
-        entry = j + 4 < n ? entries_of(u, j + 4) : -1;
+        entry = j + 4 < n ? entries_of(u, j + 4) : none;
       }
       tiles += n;
     }

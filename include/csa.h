@@ -524,8 +524,10 @@ csa_status kv_cache_read(void* k, void* v, int dtype, int64_t k_token_stride,
  * Codes enter the tensor cores as exact 16-bit values; scores, the running maximum, sums and
  * the output accumulate in fp32; weights are rounded to fp16 (11 bits) for the product with
  * V; the result is rounded once. Visible codes must not be NaN (kv_cache_write stores none).
- * A query with an infinity or a NaN spoils its own rows only. The order of every sum is
- * fixed: same inputs and SM limit, same bits. Asynchronous on `stream`; nothing is allocated.
+ * What no row of a sequence sees (behind every window, past the sinks) does not matter: codes,
+ * and for pages of nothing else their scales and table entries, which are not read. A query
+ * with an infinity or a NaN spoils its own rows only. The order of every sum is fixed: same
+ * inputs and SM limit, same bits. Asynchronous on `stream`; nothing is allocated.
  */
 csa_status cache_attention_forward(void* out, const void* q, int dtype, int q_heads,
                                    int64_t out_token_stride, int64_t out_head_stride,

@@ -1,5 +1,7 @@
-"""cache_attention_forward on unusual scales of blocks: both kernels, against the definition
-in 64 bits (GPU)."""
+"""cache_attention_forward where codes, scales and pages hold what no row sees, and on unusual
+scales of blocks: both kernels, against the definition in 64 bits (GPU)."""
+import math
+
 import pytest
 import torch
 
@@ -38,6 +40,44 @@ def check(b, q, got, dtype, window=0, sinks=0, scale=None, what=""):
     bad = ~((got - want).abs() <= room)
     assert not bad.any(), (what, int(bad.sum()), bad.nonzero()[:3].tolist(),
                            got[bad][:3].tolist(), want[bad][:3].tolist())
+
+
+HIDDEN = [
+    # new, old, Hq, Hkv, D, P, window, sinks
+    ([1, 2], [700, 300], 4, 2, 64, 16, 40, 0),
+    ([1, 1, 3], [1000, 129, 515], 4, 2, 128, 64, 100, 4),
+    ([1, 2], [777, 200], 2, 1, 48, 32, 33, 70),
+    ([1], [500], 8, 1, 80, 128, 1, 17),
+    ([150, 40], [600, 300], 4, 2, 64, 16, 50, 3),
+    ([200, 90], [500, 77], 2, 2, 128, 64, 65, 0),
+    ([130], [900], 4, 1, 112, 128, 100, 130),
+]
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("new,old,Hq,Hkv,D,P,window,sinks", HIDDEN)
+def test_what_no_row_sees_does_not_matter(new, old, Hq, Hkv, D, P, window, sinks, fmt):
+    """Keys left of every row's window and past the sinks: their codes are NaN, the scales of
+    pages that hold nothing else NaN, infinite, negative or zero, those pages' entries no page."""
+    dtype = torch.bfloat16
+    b = ref.Batch(new, old, Hkv, D, P, fmt, seed=D + P)
+    table = [list(row) for row in b.table]
+    gone = 0
+    for s, (n, L) in enumerate(zip(b.new, b.lengths)):
+        to = L - n - window + 1  # the first row's window begins here
+        for t in range(sinks, to):
+            for name in ("k", "v"):
+                b.codes[name].view(torch.uint8)[b.table[s][t // P], :, t % P] = 0x7F
+        for i in range(-(-sinks // P), max(to, 0) // P):
+            for name, bad in (("k", (math.nan, math.inf, -1.0)), ("v", (math.nan, math.inf, -1.0, 0.0))):
+                b.scale[name][b.table[s][i]] = bad[i % len(bad)]
+            table[s][i] = (-7, b.pages, 2 ** 31 - 1)[i % 3]
+            gone += 1
+    assert gone > 0
+    q = b.rows_of(Hq, dtype, seed=11)
+    for t in (None, table):
+        got = attend(b, q, dtype, window, sinks, table=t)
+        check(b, q, got, dtype, window, sinks, what="entries" if t else "codes and scales")
 
 
 @pytest.mark.parametrize("fmt", ["int8", "e4m3"])
