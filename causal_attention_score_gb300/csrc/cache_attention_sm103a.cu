@@ -31,7 +31,10 @@
 // 1/sqrt and log2(e) multiply the score. V's scale s goes into the exponent:
 // with x = c q.k log2(e) + log2(s) the weight w = exp2(x - m) has V's scale in
 // it, so one accumulator in units of codes serves blocks of different scales,
-// and the denominator sums w / s. m is within 8 of the running maximum of x
+// and the denominator sums w / s. Beside a block whose scale is more than 2^60 times its own a
+// block's weights may come out as 0 (below 2^-126) although their keys count: those are
+// added to the denominator as exp2(c q.k log2(e) - m), and the denominator is rescaled
+// in two factors, neither of which comes out as 0. m is within 8 of the running maximum of x
 // (it is raised when a value passes m + 8, so that most blocks rescale
 // nothing): w <= 256, and w is rounded to fp16 (11 bits) for the tensor core;
 // sums stay in fp32.
@@ -99,6 +102,7 @@ constexpr int kMaxRows = 16;
 constexpr int kRowLimit = 32;
 constexpr int kBlocksPerSm = 2;
 constexpr float kRaise = 8.0f;              // the running maximum is raised past this
+constexpr float kFar = 8.673617379884035e-19f;  // 2^-60: scales of V this far apart
 // The running maximum of a row that has seen nothing: finite, so that
 // differences of two of them are 0.
 constexpr float kNothing = -1e30f;
@@ -512,6 +516,7 @@ __global__ void __launch_bounds__(128 * kGroups<HSP, NB>, 1)
 #pragma unroll
       for (int i = 0; i < kTilesM; ++i) o[b][i][0] = o[b][i][1] = o[b][i][2] = o[b][i][3] = 0.0f;
     float m[NB][2], l[NB][2];
+    float far = 0.0f;  // 2^-60 of the largest scale of V so far
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       m[b][0] = m[b][1] = kNothing;
@@ -593,6 +598,8 @@ __global__ void __launch_bounds__(128 * kGroups<HSP, NB>, 1)
               }
               raise |= x[u][b][e] > kRaise;
             }
+        raise |= vs < far;  // (rare, and the warp's)
+        far = fmaxf(far, vs * kFar);
         if (__any_sync(0xFFFFFFFFu, raise)) {
 #pragma unroll
           for (int b = 0; b < NB; ++b)
@@ -612,9 +619,9 @@ __global__ void __launch_bounds__(128 * kGroups<HSP, NB>, 1)
               most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 8));
               most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 16));
               const float top = fmaxf(m[b][r], most);
-              const float corr = ex2_approx(m[b][r] - top);
+              const float half = ex2_approx(0.5f * (m[b][r] - top)), corr = half * half;
               m[b][r] = top;
-              l[b][r] *= corr;
+              l[b][r] = l[b][r] * half * half;
 #pragma unroll
               for (int j = 0; j < kTilesM; ++j) {
                 o[b][j][r] *= corr;
@@ -623,7 +630,11 @@ __global__ void __launch_bounds__(128 * kGroups<HSP, NB>, 1)
 #pragma unroll
               for (int u = 0; u < kSub; ++u)
 #pragma unroll
-                for (int n = 0; n < 2; ++n) x[u][b][2 * n + r] = y[u][n] - top;
+                for (int n = 0; n < 2; ++n) {
+                  x[u][b][2 * n + r] = y[u][n] - top;
+                  // (V far below that of others: what comes out as 0 is added without its scale)
+                  if (x[u][b][2 * n + r] < -126.0f) l[b][r] += ex2_approx(x[u][b][2 * n + r] - lv);
+                }
             }
         }
         uint32_t pb[kSub][NB][2];
@@ -746,7 +757,10 @@ __global__ void __launch_bounds__(128 * kGroups<HSP, NB>, 1)
       const float acc = (sm.o[0][r][idx] + sm.o[1][r][idx]) + (sm.o[2][r][idx] + sm.o[3][r][idx]);
       float lt = 0.0f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) lt += sm.l[k][r] * ex2_approx(sm.m[k][r] - mm);
+      for (int k = 0; k < 4; ++k) {
+        const float half = ex2_approx(0.5f * (sm.m[k][r] - mm));
+        lt += sm.l[k][r] * half * half;
+      }
       if (whole) {
         const int rr = row_first + r;
         const int j = rr / a.group;
@@ -807,8 +821,8 @@ __global__ void __launch_bounds__(128) attend_join_sm103a_kernel(const AttendArg
 #pragma unroll 4
   for (int i = warp; i < pieces; i += 4) {
     const float* p = part_of(i);
-    const float c = ex2_approx(p[r] - m);
-    l = fmaf(p[kMaxRows + r], c, l);
+    const float half = ex2_approx(0.5f * (p[r] - m)), c = half * half;
+    l = fmaf(p[kMaxRows + r] * half, half, l);
 #pragma unroll
     for (int k = 0; k < E; ++k)
       acc[k] = fmaf(p[2 * kMaxRows + r * HSP + lane * E + k], c, acc[k]);

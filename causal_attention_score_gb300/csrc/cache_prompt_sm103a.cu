@@ -37,7 +37,7 @@
 //
 // Scales (see cache_attention_sm103a.cu): with c ks and log2(vs) per 16 tokens in
 // shared memory, x = s (c ks) + log2(vs) and the weight has V's scale in it; the
-// denominator sums w / vs.
+// denominator sums w / vs, and what that loses beside far larger scales apart.
 //
 // Bound: 4 HSP flops and one exp2 per row and key; per 256 rows x 64 keys 1024 cycles
 // of MMA at the dense rate (HSP = 128), 1280 at the rates that these shapes run at alone
@@ -85,6 +85,7 @@ constexpr int kUnitSlots = 2;
 constexpr int kAskAhead = 12;       // tiles before a unit's end when the next is asked for
 constexpr int kTmemCols = 512;      // S_A (two buffers), S_B, O_A, O_B
 constexpr float kRaise = 8.0f;
+constexpr float kFar = 8.673617379884035e-19f;  // 2^-60: scales of V this far apart
 constexpr float kNothing = -1e30f;  // the running maximum of a row that has seen nothing
 
 struct PromptArgs {
@@ -106,7 +107,8 @@ struct PromptArgs {
 // What 16 keys' scores are multiplied with (to the base-2 exponent), log2 of their V's
 // scale, its inverse.
 struct Factor {
-  float k, log2v, inv, pad;
+  float k, log2v, inv;
+  uint32_t far;  // of a tile's first: not 0 where V of 16 of its keys lies far below others'
 };
 
 struct Unit {
@@ -581,30 +583,53 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 4; ++e)
             tops[e] = fmaxf(fmaxf(tops[e], __uint_as_float(x[i + e])), __uint_as_float(x[i + 4 + e]));
         const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-        if (__builtin_expect(__any_sync(0xFFFFFFFFu, top > (fresh ? -INFINITY : kRaise)), 0)) {
-          // (rare) a new maximum: what was computed with the old one, O and l, is rescaled
-          const float up = fresh ? fmaxf(top, kNothing) : fmaxf(top, 0.0f);
-          const float corr = fresh ? 1.0f : ex2_approx(-up);
-          m = less + up;
-          l *= corr;
-          const float off = fresh && top == -INFINITY ? 0.0f : up;
+        const bool far = fac[0].far != 0;  // (the CTA's)
+        const bool raise = top > (fresh ? -INFINITY : kRaise);
+        if (__builtin_expect(__any_sync(0xFFFFFFFFu, raise || far), 0)) {
+          if (__any_sync(0xFFFFFFFFu, raise)) {
+            // (rare) a new maximum: what was computed with the old one, O and l, is rescaled
+            const float up = fresh ? fmaxf(top, kNothing) : fmaxf(top, 0.0f);
+            const float half = fresh ? 1.0f : ex2_approx(-0.5f * up), corr = half * half;
+            m = less + up;
+            l = l * half * half;
+            const float off = fresh && top == -INFINITY ? 0.0f : up;
 #pragma unroll
-          for (int i = 0; i < kTile; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) - off);
-          if (step > 0) {
-            // O is the product issued last's until that is complete (the one before it
-            // is: this tile's scores were issued later)
-            const uint32_t before = product - 1;
-            if (!mbar_wait_lanes(pv_done(g, before & 1u), (before >> 1) & 1u, wd,
-                                       kSiteEpilogueFull))
-              ok = false;
-            tc_fence_after_sync();
+            for (int i = 0; i < kTile; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) - off);
+            if (step > 0) {
+              // O is the product issued last's until that is complete (the one before it
+              // is: this tile's scores were issued later)
+              const uint32_t before = product - 1;
+              if (!mbar_wait_lanes(pv_done(g, before & 1u), (before >> 1) & 1u, wd,
+                                   kSiteEpilogueFull))
+                ok = false;
+              tc_fence_after_sync();
 #pragma unroll 1
-            for (int d = 0; d < HSP; d += 8) {
-              uint32_t y[8];
-              tmem_ld_8cols(o_tmem + d, y);
+              for (int d = 0; d < HSP; d += 8) {
+                uint32_t y[8];
+                tmem_ld_8cols(o_tmem + d, y);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * corr);
-              tmem_st_8cols(o_tmem + d, y);
+                for (int i = 0; i < 8; ++i)
+                  y[i] = __float_as_uint(__uint_as_float(y[i]) * corr);
+                tmem_st_8cols(o_tmem + d, y);
+              }
+            }
+          }
+          if (far) {
+            // V far below that of others: weights that come out as 0 are added to the sum
+            // without V's scale, from the scores again
+#pragma unroll 1
+            for (int e = 0; e < kTile; e += 8) {
+              uint32_t y[8];
+              tmem_ld_8cols(s_tmem + e, y);
+              const Factor c = fac[e / 16];
+              const float add = c.log2v - m;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float z = fmaf(__uint_as_float(y[i]), c.k, add);
+                if (z < -126.0f && z != -INFINITY && e + i <= last &&
+                    (e + i >= first_window || e + i < sink_cols))
+                  l += ex2_approx(z - c.log2v);
+              }
             }
           }
         }
@@ -872,6 +897,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return f;
       };
       Scales f = scales_of(page), f2 = scales_of(page2);
+      float vmost = 0.0f;  // the largest scale of V so far
       for (int j = -1; j < n; ++j, ++it) {
         const uint32_t rs = it % kRawSlots;
         // Everything is worked out before the slot is free.
@@ -885,10 +911,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // -inf masks 16 tokens of no page. A block of scale 0 holds zeros, at any scale (and
         // its V is not copied).
         const float scale_v = fmaxf(f.v, kScaleFloor);
+        vmost = fmaxf(vmost, __uint_as_float(__reduce_max_sync(
+                                 0xFFFFFFFFu, page >= 0 ? __float_as_uint(scale_v) : 0u)));
+        const uint32_t fars = __ballot_sync(0xFFFFFFFFu, page >= 0 && scale_v < vmost * kFar);
         if (j + 1 < n && lane < 4)
           factors[((tiles + j + 1) % kFactorSlots) * 4 + lane] =
               Factor{a.scale_log2 * f.k, page >= 0 ? __log2f(scale_v) : -INFINITY,
-                     __fdividef(1.0f, scale_v), 0.0f};
+                     __fdividef(1.0f, scale_v), fars};
         if (j == ask && lane == 0) mbar_arrive(u_want);
         if (!mbar_wait_lanes(raw_empty(rs), ((it / kRawSlots) & 1u) ^ 1u, wd,
                                    kSiteProducerEmpty)) {

@@ -1,5 +1,5 @@
-"""cache_attention_forward where codes, scales and pages hold what no row sees, and on unusual
-scales of blocks: both kernels, against the definition in 64 bits (GPU)."""
+"""cache_attention_forward where codes, scales and pages hold what no row sees, and where V's
+scales are zero or far apart: both kernels, against the definition in 64 bits (GPU)."""
 import math
 
 import pytest
@@ -98,3 +98,26 @@ def test_blocks_of_scale_zero(new, old, window, fmt):
     for name in ("v",):
         b.scale[name][:] = 0.0
     assert bool((attend(b, q, dtype, window, 5) == 0).all())
+
+
+@pytest.mark.parametrize("big", [2.0 ** 27, 2.0 ** 53, 2.0 ** 93])
+@pytest.mark.parametrize("small", ["zeros", 2.0 ** -60, 2.0 ** -95])
+@pytest.mark.parametrize("new,old,window", [([1], [900], 0), ([1, 2], [15000, 70], 0), ([140], [500], 0),
+                                            ([3, 140], [300, 500], 200)])
+def test_every_key_counts_in_the_denominator(new, old, window, small, big):
+    """Blocks of V far smaller than others (a written block of zeros has scale 2^-100), with
+    scores as large: what they weigh does not depend on V."""
+    dtype = torch.bfloat16
+    for first in range(3):
+        b = ref.Batch(new, old, 1, 64, 32, "int8", seed=7 + first)
+        for s, L in enumerate(b.lengths):
+            blocks = -(-L // 32)
+            for i in range(blocks):
+                p = b.table[s][i]
+                tiny = (i < blocks // 2, i >= blocks // 2, i % 3 == 0)[first]
+                b.scale["v"][p, 0] = (2.0 ** -100 if small == "zeros" else small) if tiny else big
+                if tiny and small == "zeros":
+                    b.codes["v"][p] = torch.where(b.live[p][None, :, None], 0, b.codes["v"][p])
+        for q_scale in (0.0, 1.0):
+            q = b.rows_of(2, dtype, q_scale, seed=11)
+            check(b, q, attend(b, q, dtype, window, 3), dtype, window, 3, what=(first, q_scale))
