@@ -31,13 +31,14 @@
 // 1/sqrt and log2(e) multiply the score. V's scale s goes into the exponent:
 // with x = c q.k log2(e) + log2(s) the weight w = exp2(x - m) has V's scale in
 // it, so one accumulator in units of codes serves blocks of different scales,
-// and the denominator sums w / s. Beside a block whose scale is more than 2^60 times its own a
-// block's weights may come out as 0 (below 2^-126) although their keys count: those are
-// added to the denominator as exp2(c q.k log2(e) - m), and the denominator is rescaled
-// in two factors, neither of which comes out as 0. m is within 8 of the running maximum of x
-// (it is raised when a value passes m + 8, so that most blocks rescale
-// nothing): w <= 256, and w is rounded to fp16 (11 bits) for the tensor core;
-// sums stay in fp32.
+// and the denominator sums w / s. Beside a block whose scale is more than 2^60
+// times its own a block's weights may come out as 0 (below 2^-126) although their
+// keys count: those are added to the denominator as exp2(c q.k log2(e) - m), and
+// the denominator is rescaled in two factors, neither of which comes out as 0.
+// m is set to 7 below the running maximum of x and raised when a value passes
+// m + 15, so that most blocks rescale nothing: the largest w is from 2^7 to 2^15,
+// at the upper end of fp16, to which w is rounded for the tensor core (to 11 bits,
+// and to 2^-32 of the largest where fp16 is subnormal); sums stay in fp32.
 //
 // Layout trick: a dot product may run over the elements in any order, so lane
 // (g, t) of a warp loads 16 contiguous bytes of token g's K row and uses its
@@ -101,7 +102,8 @@ constexpr int kMaxRows = 16;
 // and 960 us; none: 15 and 16 us), one of 96 tokens 164 and 131 us.
 constexpr int kRowLimit = 32;
 constexpr int kBlocksPerSm = 2;
-constexpr float kRaise = 8.0f;              // the running maximum is raised past this
+constexpr float kRaise = 15.0f;             // an exponent past this raises m,
+constexpr float kHeadroom = 7.0f;           // to this far below it
 constexpr float kFar = 8.673617379884035e-19f;  // 2^-60: scales of V this far apart
 // The running maximum of a row that has seen nothing: finite, so that
 // differences of two of them are 0.
@@ -618,7 +620,7 @@ __global__ void __launch_bounds__(128 * kGroups<HSP, NB>, 1)
               most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 4));
               most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 8));
               most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 16));
-              const float top = fmaxf(m[b][r], most);
+              const float top = fmaxf(m[b][r], most - kHeadroom);
               const float half = ex2_approx(0.5f * (m[b][r] - top)), corr = half * half;
               m[b][r] = top;
               l[b][r] = l[b][r] * half * half;

@@ -9,8 +9,8 @@
 //  - warps 0..7: softmax, warps 0..3 group A, 4..7 group B, a thread a row. Per
 //    tile: scores from TMEM, x - m, their maximum, and the weights exp2(x - m) as
 //    fp16 over S (P, the second product's A operand in TMEM), all 64 of a row in
-//    registers at once. m is raised only when a value passes m + 8; then the
-//    thread's O row and its l are rescaled. They copy a unit's Q
+//    registers at once. m is raised, to 7 below the maximum, only when a value passes
+//    m + 15; then the thread's O row and its l are rescaled. They copy a unit's Q
 //    to shared memory before they write the last one's O / l.
 //  - warps 8..11: conversion, from raw codes in shared memory to the
 //    128-byte-swizzle K-major layout, K as [token][element] in Q's type, V
@@ -84,7 +84,8 @@ constexpr int kFactorSlots = 16;    // tiles whose factors are kept (more than a
 constexpr int kUnitSlots = 2;
 constexpr int kAskAhead = 12;       // tiles before a unit's end when the next is asked for
 constexpr int kTmemCols = 512;      // S_A (two buffers), S_B, O_A, O_B
-constexpr float kRaise = 8.0f;
+constexpr float kRaise = 15.0f;     // an exponent past this raises m,
+constexpr float kHeadroom = 7.0f;   // to this far below it
 constexpr float kFar = 8.673617379884035e-19f;  // 2^-60: scales of V this far apart
 constexpr float kNothing = -1e30f;  // the running maximum of a row that has seen nothing
 
@@ -588,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (__builtin_expect(__any_sync(0xFFFFFFFFu, raise || far), 0)) {
           if (__any_sync(0xFFFFFFFFu, raise)) {
             // (rare) a new maximum: what was computed with the old one, O and l, is rescaled
-            const float up = fresh ? fmaxf(top, kNothing) : fmaxf(top, 0.0f);
+            const float up = fmaxf(top - kHeadroom, fresh ? kNothing : 0.0f);
             const float half = fresh ? 1.0f : ex2_approx(-0.5f * up), corr = half * half;
             m = less + up;
             l = l * half * half;

@@ -522,14 +522,14 @@ csa_status kv_cache_read(void* k, void* v, int dtype, int64_t k_token_stride,
  *              clearing, in use until the call's kernels complete: calls that may overlap on
  *              the GPU, replays of captured ones too, need separate workspaces.
  * Codes enter the tensor cores as exact 16-bit values; scores, the running maximum, sums and
- * the output accumulate in fp32; weights are rounded to fp16 (11 bits) for the product with
- * V; the result is rounded once. Every visible key counts in the denominator, however far
- * apart V's scales are (for V of up to 2^100). Visible codes must not be NaN (kv_cache_write
- * stores none).
- * What no row of a sequence sees (behind every window, past the sinks) does not matter: codes,
- * and for pages of nothing else their scales and table entries, which are not read. A query
- * with an infinity or a NaN spoils its own rows only. The order of every sum is fixed: same
- * inputs and SM limit, same bits. Asynchronous on `stream`; nothing is allocated.
+ * the output accumulate in fp32; weights, with V's scale, are rounded to fp16 for the product
+ * with V (to 11 bits, and to 2^-32 of a row's largest); the result is rounded once. Every
+ * visible key counts in the denominator, however far apart V's scales are (for V of up to
+ * 2^100). Visible codes must not be NaN (kv_cache_write stores none). What no row of a
+ * sequence sees (behind every window, past the sinks) does not matter: codes, and for pages of
+ * nothing else their scales and table entries, which are not read. A query with an infinity or
+ * a NaN spoils its own rows only. The order of every sum is fixed: same inputs and SM limit,
+ * same bits. Asynchronous on `stream`; nothing is allocated.
  */
 csa_status cache_attention_forward(void* out, const void* q, int dtype, int q_heads,
                                    int64_t out_token_stride, int64_t out_head_stride,

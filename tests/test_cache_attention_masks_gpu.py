@@ -1,5 +1,6 @@
-"""cache_attention_forward where codes, scales and pages hold what no row sees, and where V's
-scales are zero or far apart: both kernels, against the definition in 64 bits (GPU)."""
+"""cache_attention_forward where codes, scales and pages hold what no row sees, where V's
+scales are zero or far apart, and where many small weights add up: both kernels, against the
+definition in 64 bits (GPU)."""
 import math
 
 import pytest
@@ -121,3 +122,39 @@ def test_every_key_counts_in_the_denominator(new, old, window, small, big):
         for q_scale in (0.0, 1.0):
             q = b.rows_of(2, dtype, q_scale, seed=11)
             check(b, q, attend(b, q, dtype, window, 3), dtype, window, 3, what=(first, q_scale))
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("new", [1, 70])
+def test_many_small_weights_add_up(new, fmt):
+    """One key of weight 1 whose V is 0, before N = 2^15 keys of weight 2^-27: the output is
+    theirs, N 2^-27 v.
+
+    A weight is rounded to fp16: 2^-11 relatively, and 2^-25 absolutely where subnormal, where
+    the largest of its row is at least 2^7: 2^-32 of that for each key. The weights' own
+    errors are those of ref.attention (scores here are exact: one product of a key)."""
+    dtype, D, P = torch.bfloat16, 64, 128
+    N = 2 ** 15
+    b = ref.Batch([new], [N - new], 1, D, P, fmt, seed=2)
+    top = 127 if fmt == "int8" else 448
+    pages = b.table[0][: N // P]
+    for name in ("k", "v"):
+        b.codes[name][:] = torch.zeros_like(b.codes[name].float()).to(b.codes[name].dtype)
+        b.scale[name][:] = 2.0 ** -6
+    b.codes["k"][pages[0], 0, 0, 0] = top
+    b.codes["v"][pages] = (torch.randn((len(pages), 1, P, D), generator=b.g).abs() * 30 + 1).clamp(max=120).round().to(
+        b.codes["v"].dtype)
+    b.codes["v"][pages[0], 0, 0] = torch.zeros(D).to(b.codes["v"].dtype)
+    q = torch.zeros((new, 1, D), dtype=dtype)
+    q[:, 0, 0] = 1.0
+    scale = 27 * math.log(2) / (top * 2.0 ** -6)
+    got = attend(b, q, dtype, scale=scale)
+    want, _ = ref.attention(q, *b.values("k"), *b.values("v"), b.offsets, b.lengths, b.table, scale=scale)
+    v = b.values("v")
+    vmax = float((v[0] * v[1][..., None, None]).max())
+    # exponents up to 32 in size: their roundings are worth 2^-18; sums of N terms
+    d = 2.0 ** -16 + 2.0 ** -18 + N * 2.0 ** -24
+    room = want * (2 * d + 2.0 ** -11 + ref.half_step(dtype)) * 1.01 + N * 2.0 ** -32 * vmax
+    assert bool((want > 4 * N * 2.0 ** -32 * vmax).all())
+    bad = ~((got - want).abs() <= room)
+    assert not bad.any(), (int(bad.sum()), got[bad][:3].tolist(), want[bad][:3].tolist())
