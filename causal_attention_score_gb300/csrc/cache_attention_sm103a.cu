@@ -93,15 +93,20 @@ constexpr int kUnitTiles = (NB == 1 ? 2 : 3) * (2 / kSub);
 constexpr int kMaxSms = 152;
 constexpr int kMaxWorkers = kMaxSms * 4;
 constexpr int kMaxRows = 16;
-// Which kernel a sequence's rows go to. Here each block of 16 rows reads the keys again;
-// the prompt kernel reads them once for 256 rows, but nothing splits its units along the
-// keys. With 8K keys a block of 16 rows of one kv head takes 0.41 us of the whole
-// GPU, 32 rows as much as a unit there (0.82 us) where units fill it; where they do
-// not, its 120 us for the first unit buy this kernel 2 blocks an SM: 1 sequence of 64
-// new tokens (8 rows each, 8 heads) takes 113 us here and 130 us there (64K keys: 790
-// and 960 us; none: 15 and 16 us), one of 96 tokens 164 and 131 us.
+// Which kernel a sequence's rows go to: those of more than kRowLimit to the one for prompts
+// where the batch holds more than kBlocksPerSm blocks of 16 of them for each SM. These are
+// counted on the device: single tokens beside a short prompt must not make it one of a
+// batch of prompts (63 of 300 to 7300 tokens and one of 40 new over 64K, 8 heads: 176 us, and
+// 1022 us with that one in the prompt kernel; the count takes the others' calls 1 us).
+// Here each block of 16 rows reads the keys again; the prompt kernel reads them once for 256
+// rows, but nothing splits its units along the keys. With 8K keys a block of 16 rows of one
+// kv head takes 0.41 us of the whole GPU, 32 rows as much as a unit there (0.82 us) where
+// units fill it; where they do not, its 120 us for the first unit buy this kernel 2 blocks an
+// SM: 1 sequence of 64 new tokens (8 rows each, 8 heads) takes 113 us here and 130 us there
+// (64K keys: 790 and 960 us; none: 15 and 16 us), one of 96 tokens 164 and 131 us.
 constexpr int kRowLimit = 32;
 constexpr int kBlocksPerSm = 2;
+constexpr int kNoRowLimit = std::numeric_limits<int>::max();
 constexpr float kRaise = 15.0f;             // an exponent past this raises m,
 constexpr float kHeadroom = 7.0f;           // to this far below it
 constexpr float kFar = 8.673617379884035e-19f;  // 2^-60: scales of V this far apart
@@ -120,9 +125,11 @@ struct AttendArgs {
   float scale_log2;
   int workers;
   int most_rows;   // of a block
-  int row_limit;   // sequences of more rows (tokens x group) are left to another kernel
-  int* headers;    // [workers][8]
-  unsigned int* counter;  // the prompt kernel's, cleared here
+  // Sequences of more than kRowLimit rows (tokens x group) are left to the prompt kernel
+  // where their blocks of 16 rows, times heads, are more than this.
+  long long prompt_blocks;
+  int* headers;  // [workers][8]
+  PromptList* list;  // the prompt kernel's, written here
   float* parts;    // [2 * workers][part_floats]
   int part_floats;
 };
@@ -172,11 +179,11 @@ struct SeqWork {
 };
 
 template <int NB, int kSub>
-__device__ __forceinline__ SeqWork seq_work(const AttendArgs& a, int s) {
+__device__ __forceinline__ SeqWork seq_work(const AttendArgs& a, int row_limit, int s) {
   SeqWork w;
   w.q = kv_sequence(a.v, s);
   const long long rows = static_cast<long long>(w.q.n) * a.group;
-  if (rows == 0 || rows > a.row_limit) {
+  if (rows == 0 || rows > row_limit) {
     w.rows = w.blocks = w.tiles = w.sink_tiles = w.window_tile = 0;
     return w;
   }
@@ -215,7 +222,7 @@ struct Piece {
 };
 
 template <int NB, int kSub>
-__device__ __forceinline__ void next_piece(const AttendArgs& a, Piece& p) {
+__device__ __forceinline__ void next_piece(const AttendArgs& a, int row_limit, Piece& p) {
   constexpr int E = kUnitTiles<NB, kSub>;
   p.count = 0;
   while (p.at < p.end) {
@@ -229,7 +236,7 @@ __device__ __forceinline__ void next_piece(const AttendArgs& a, Piece& p) {
         p.at = p.end;
         return;
       }
-      p.w = seq_work<NB, kSub>(a, p.s);
+      p.w = seq_work<NB, kSub>(a, row_limit, p.s);
     }
     const long long off = p.at - p.base;
     const int unit = static_cast<int>(
@@ -273,6 +280,7 @@ __global__ void __launch_bounds__(128 * kGroups<HSP, NB>, 1)
   extern __shared__ __align__(16) uint8_t smem_raw[];
   __shared__ long long s_prefix[kThreads + 1];
   __shared__ long long s_warp[kThreads / 32];
+  __shared__ unsigned long long s_blocks;
   using Smem = GroupSmem<HSP, NB>;
   Smem* groups = reinterpret_cast<Smem*>(smem_raw);
   constexpr int kChunks = HSP / 64;       // 16-byte chunks of a K row per lane
@@ -281,7 +289,6 @@ __global__ void __launch_bounds__(128 * kGroups<HSP, NB>, 1)
   constexpr int kTilesM = HSP / 16;       // m-tiles of the output
 
   grid_dependency_wait();
-  if (blockIdx.x == 0 && threadIdx.x == 0) *a.counter = 0;
 
   // -------------------------------------------------------- the work list --
   // Thread i sums the work of sequences [i c, (i + 1) c); a scan over the CTA
@@ -289,11 +296,29 @@ __global__ void __launch_bounds__(128 * kGroups<HSP, NB>, 1)
   const int S = a.v.sequences;
   const int c = (S + kThreads - 1) / kThreads;
   const int lane = threadIdx.x & 31, warp_id = threadIdx.x >> 5;
+  const long long from = static_cast<long long>(threadIdx.x) * c;
+  const long long until = min(static_cast<long long>(S), from + c);
+  if (threadIdx.x == 0) s_blocks = 0;
+  __syncthreads();
+  if (a.prompt_blocks > 0) {
+    unsigned long long mine = 0;
+    for (long long s = from; s < until; ++s) {
+      const long long rows =
+          static_cast<long long>(kv_sequence(a.v, static_cast<int>(s)).n) * a.group;
+      if (rows > kRowLimit) mine += (rows + 15) / 16 * a.v.heads;
+    }
+    if (mine > 0) atomicAdd(&s_blocks, mine);
+    __syncthreads();
+  }
+  // (read again wherever it is needed: the main loop needs the registers)
+  auto row_limit = [&] {
+    return static_cast<long long>(s_blocks) > a.prompt_blocks ? kRowLimit : kNoRowLimit;
+  };
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.list = PromptList{0u, row_limit()};
   {
     long long mine = 0;
-    const long long from = static_cast<long long>(threadIdx.x) * c;
-    for (long long s = from; s < min(static_cast<long long>(S), from + c); ++s) {
-      const SeqWork w = seq_work<NB, kSub>(a, static_cast<int>(s));
+    for (long long s = from; s < until; ++s) {
+      const SeqWork w = seq_work<NB, kSub>(a, row_limit(), static_cast<int>(s));
       mine += static_cast<long long>(w.blocks) * a.v.heads * unit_weight<NB, kSub>(w);
     }
     long long sum = mine;
@@ -335,9 +360,9 @@ __global__ void __launch_bounds__(128 * kGroups<HSP, NB>, 1)
       }
       p.s = lo * c;
       p.base = s_prefix[lo];
-      p.w = seq_work<NB, kSub>(a, p.s);
+      p.w = seq_work<NB, kSub>(a, row_limit(), p.s);
     }
-    next_piece<NB, kSub>(a, p);
+    next_piece<NB, kSub>(a, row_limit(), p);
   }
   group_sync(gi);
 
@@ -506,7 +531,7 @@ __global__ void __launch_bounds__(128 * kGroups<HSP, NB>, 1)
     if (gtid == 0) {
       Piece& next = sm.piece[cur ^ 1];
       next = sm.piece[cur];
-      next_piece<NB, kSub>(a, next);
+      next_piece<NB, kSub>(a, row_limit(), next);
     }
     group_sync(gi);
     if (count == 1) unit_next = look(1, tb_next);
@@ -910,12 +935,15 @@ int cache_attention_launch(const csa_kv_cache& cache, const csa_kv_batch& batch,
   a.workers = 0;
   const long long most_rows = static_cast<long long>(batch.max_new) * a.group;
   const long long batch_rows = static_cast<long long>(batch.rows) * a.group;
+  // Whether the batch's rows could be prompts enough, however they are shared out.
+  a.prompt_blocks = static_cast<long long>(kBlocksPerSm) * sms;
+  const long long sequences = std::min<long long>(batch.sequences, batch_rows / (kRowLimit + 1));
   const bool prompts = most_rows > kRowLimit &&
-                       (batch_rows / 16 + batch.sequences) * cache.heads > kBlocksPerSm * sms;
-  a.row_limit = prompts ? kRowLimit : std::numeric_limits<int>::max();
+                       (batch_rows / 16 + sequences) * cache.heads > a.prompt_blocks;
+  if (!prompts) a.prompt_blocks = 0;
   const int hsp = padded_head(cache.head_size);
   a.headers = static_cast<int*>(call.workspace);
-  a.counter = reinterpret_cast<unsigned int*>(a.headers + kMaxWorkers * 8);
+  a.list = reinterpret_cast<PromptList*>(a.headers + kMaxWorkers * 8);
   a.parts = reinterpret_cast<float*>(a.headers + (kMaxWorkers + 1) * 8);
   a.part_floats = 2 * kMaxRows + kMaxRows * hsp;
   a.most_rows = static_cast<int>(std::min<long long>(most_rows, kMaxRows));
@@ -944,7 +972,7 @@ int cache_attention_launch(const csa_kv_cache& cache, const csa_kv_batch& batch,
     return CSA_ERR_LAUNCH;
   }
   if (prompts) {
-    rc = cache_prompt_launch(cache, batch, call, kRowLimit, a.counter, stream, dev, err);
+    rc = cache_prompt_launch(cache, batch, call, a.list, stream, dev, err);
     if (rc != CSA_OK) {
       err = "cache_attention_forward: " + err;
       return rc;

@@ -24,8 +24,8 @@
 //    last. A thread's MMAs run in issue order, so S may overwrite the weights that
 //    the product issued before it reads. (With both groups on one warp the issue
 //    itself, 48 to 96 cycles an MMA, was the longest path.)
-//  - warp 14: takes a unit from the counter (workspace, cleared by the rows kernel
-//    ahead in the stream) when the copies ask for it, some tiles before they are
+//  - warp 14: takes a unit from the list's counter (workspace, cleared by the rows
+//    kernel ahead in the stream) when the copies ask for it, some tiles before they are
 //    through with the last one: early enough to hide the way to the first scores, late
 //    enough that a CTA holds no unit that another could have begun.
 //  - warp 15: copies. A page's part of a tile is contiguous, so one thread moves it
@@ -97,9 +97,8 @@ struct PromptArgs {
   int half;
   int group;
   int window, sinks;
-  int row_limit;        // sequences of at most this many rows are the rows kernel's
   float scale_log2;
-  unsigned int* counter;  // units taken, zero at launch
+  PromptList* list;
   int* status;
   unsigned long long wait_limit_ns;
   int inject;
@@ -138,13 +137,14 @@ struct Layout {
 // The list's u-th unit: sequences by their longest unit, the longest first (up to
 // kThreads of them; more keep their order), within a sequence the last rows, which see
 // the most keys, first.
-__device__ __forceinline__ long long units_of(const PromptArgs& a, const KvSequence& q) {
+__device__ __forceinline__ long long units_of(const PromptArgs& a, int row_limit,
+                                              const KvSequence& q) {
   const long long rows = static_cast<long long>(q.n) * a.group;
-  return rows <= a.row_limit ? 0 : (rows + kUnitRows - 1) / kUnitRows * a.v.heads;
+  return rows <= row_limit ? 0 : (rows + kUnitRows - 1) / kUnitRows * a.v.heads;
 }
 
-__device__ Unit decode_unit(const PromptArgs& a, const long long* prefix, const int* order,
-                            int per, long long u) {
+__device__ Unit decode_unit(const PromptArgs& a, int row_limit, const long long* prefix,
+                            const int* order, int per, long long u) {
   int lo = 0, hi = kThreads;
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
@@ -155,7 +155,7 @@ __device__ Unit decode_unit(const PromptArgs& a, const long long* prefix, const 
   long long base = prefix[lo];
   for (r.s = per == 1 ? order[lo] : lo * per;; ++r.s) {
     r.q = kv_sequence(a.v, r.s);
-    const long long n = units_of(a, r.q);
+    const long long n = units_of(a, row_limit, r.q);
     if (per == 1 || u < base + n) break;
     base += n;
   }
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dependency_wait();
 
   // The work list: thread i counts the units of sequences [i per, (i + 1) per).
-  const int S = a.v.sequences;
+  const int S = a.v.sequences, row_limit = a.list->row_limit;
   const int per = (S + kThreads - 1) / kThreads;
   {
     long long mine = 0;
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int key = -1;
       if (i < S) {
         const KvSequence q = kv_sequence(a.v, i);
-        if (units_of(a, q) > 0)
+        if (units_of(a, row_limit, q) > 0)
           key = a.window > 0 && a.window < q.length - q.n ? a.window + q.n : q.length;
       }
       s_keys[i] = key;
@@ -440,11 +440,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         s_order[rank] = i;
       }
       __syncthreads();
-      if (i < S) mine = units_of(a, kv_sequence(a.v, s_order[i]));
+      if (i < S) mine = units_of(a, row_limit, kv_sequence(a.v, s_order[i]));
     } else {
       const long long from = static_cast<long long>(threadIdx.x) * per;
       for (long long s = from; s < min(static_cast<long long>(S), from + per); ++s)
-        mine += units_of(a, kv_sequence(a.v, static_cast<int>(s)));
+        mine += units_of(a, row_limit, kv_sequence(a.v, static_cast<int>(s)));
     }
     long long sum = mine;
 #pragma unroll
@@ -962,9 +962,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint32_t k = 0;; ++k) {
         const uint32_t slot = k % kUnitSlots;
         if (!mbar_wait(u_want, k & 1u, wd, kSiteSched)) break;
-        const long long at = atomicAdd(a.counter, 1u);
+        const long long at = atomicAdd(&a.list->taken, 1u);
         Unit u;
-        if (at < total) u = decode_unit(a, s_prefix, s_order, per, at);
+        if (at < total) u = decode_unit(a, row_limit, s_prefix, s_order, per, at);
         else u.n[0] = -1;
         if (!mbar_wait(u_empty(slot), ((k / kUnitSlots) & 1u) ^ 1u, wd, kSiteSched)) break;
         reinterpret_cast<Unit*>(gbase + L::kUnits)[slot] = u;
@@ -1114,8 +1114,8 @@ cudaError_t launch_prompt(const PromptArgs& a, int format, const DeviceInfo& dev
 }  // namespace
 
 int cache_prompt_launch(const csa_kv_cache& cache, const csa_kv_batch& batch,
-                        const AttendCall& call, int row_limit, unsigned int* counter,
-                        cudaStream_t stream, const DeviceInfo& dev, std::string& err) {
+                        const AttendCall& call, PromptList* list, cudaStream_t stream,
+                        const DeviceInfo& dev, std::string& err) {
   PromptArgs a;
   a.v = kv_view(cache, batch, dev);
   a.q = call.q;
@@ -1128,12 +1128,11 @@ int cache_prompt_launch(const csa_kv_cache& cache, const csa_kv_batch& batch,
   a.group = call.q_heads / cache.heads;
   a.window = call.window;
   a.sinks = call.window > 0 ? call.sinks : 0;
-  a.row_limit = row_limit;
   a.scale_log2 = static_cast<float>(static_cast<double>(call.scale) * 1.4426950408889634);
   a.status = dev.status_word;
   a.wait_limit_ns = wait_limit_ns();
   a.inject = take_inject() ? 1 : 0;
-  a.counter = counter;
+  a.list = list;
   int rc = CSA_OK;
   cudaError_t e;
   e = cache.head_size <= 64 ? launch_prompt<64>(a, cache.format, dev, stream, rc, err)

@@ -199,11 +199,15 @@ int cache_attention_launch(const csa_kv_cache& cache, const csa_kv_batch& batch,
                            const AttendCall& call, cudaStream_t stream, const DeviceInfo& dev,
                            std::string& err);
 
-// The tcgen05 form, for the sequences of more than row_limit rows (tokens x query
-// heads of a kv head). `counter` (device) must be zero when the kernel starts.
+// What the kernel for few rows leaves the one for prompts in the workspace.
+struct PromptList {
+  unsigned int taken;  // units taken: 0
+  int row_limit;       // sequences of more rows (tokens x query heads of a kv head) are its
+};
+// The tcgen05 form, behind the kernel for few rows in the stream. `list` is on the device.
 int cache_prompt_launch(const csa_kv_cache& cache, const csa_kv_batch& batch,
-                        const AttendCall& call, int row_limit, unsigned int* counter,
-                        cudaStream_t stream, const DeviceInfo& dev, std::string& err);
+                        const AttendCall& call, PromptList* list, cudaStream_t stream,
+                        const DeviceInfo& dev, std::string& err);
 
 // The device's view of a cache and a batch (kv_cache.cuh).
 struct KvView;
