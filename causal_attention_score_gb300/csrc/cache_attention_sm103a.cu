@@ -257,6 +257,16 @@ __device__ __forceinline__ void next_piece(const AttendArgs& a, int row_limit, P
   }
 }
 
+// (checking build) whether a piece's rows and tiles are its sequence's.
+[[maybe_unused]] __device__ __forceinline__ bool piece_ok(const AttendArgs& a,
+                                                          const volatile Piece& p) {
+  return p.s >= 0 && p.s < a.v.sequences && p.head >= 0 && p.head < a.v.heads &&
+         p.row_first >= 0 && p.rows > 0 && p.rows <= kMaxRows &&
+         p.row_first + p.rows <= p.w.rows && p.w.q.row0 >= 0 &&
+         p.w.q.row0 + p.w.q.n <= a.v.rows && p.tile0 >= 0 && p.count > 0 &&
+         p.tile0 + p.count <= p.w.tiles;
+}
+
 template <int HSP, int NB>
 struct GroupSmem {
   // Floats per lane column and row, padded so that the float4 accesses of eight
@@ -281,6 +291,8 @@ __global__ void __launch_bounds__(128 * kGroups<HSP, NB>, 1)
   __shared__ long long s_prefix[kThreads + 1];
   __shared__ long long s_warp[kThreads / 32];
   __shared__ unsigned long long s_blocks;
+  [[maybe_unused]] __shared__ int s_abort;
+  [[maybe_unused]] const Watchdog wd{0, a.v.status, &s_abort};
   using Smem = GroupSmem<HSP, NB>;
   Smem* groups = reinterpret_cast<Smem*>(smem_raw);
   constexpr int kChunks = HSP / 64;       // 16-byte chunks of a K row per lane
@@ -379,6 +391,7 @@ __global__ void __launch_bounds__(128 * kGroups<HSP, NB>, 1)
     const volatile Piece& piece = sm.piece[cur];
     const int count = piece.count;
     if (count == 0) break;
+    if (!CSA_CHECK(piece_ok(a, piece), wd, kCheckTile)) break;
     const int head = piece.head;
     const int length = piece.w.q.length;
 
@@ -396,6 +409,9 @@ __global__ void __launch_bounds__(128 * kGroups<HSP, NB>, 1)
               warp * (16 * kSub);
       if (first >= p.w.q.length) return -1;
       if (a.window != 0 && first >= a.sinks && first + 16 * kSub <= p.hidden_to) return -1;
+      if (!CSA_CHECK(first >= 0 && (first & (a.v.page_tokens - 1)) + 16 * kSub <= a.v.page_tokens,
+                     wd, kCheckTile))
+        return -1;
       const int page = kv_page(a.v, p.s, first >> a.v.page_shift);
       return page < 0 ? -1 : page * a.v.heads + p.head;
     };
@@ -776,6 +792,7 @@ __global__ void __launch_bounds__(128 * kGroups<HSP, NB>, 1)
     const bool begins = piece.tile0 == 0, whole = begins && piece.count == piece.w.tiles;
     const int row_first = piece.row_first, row0 = piece.w.q.row0, out_head = piece.head * a.group;
     const int slot = 2 * worker + (begins ? 1 : 0);
+    if (!CSA_CHECK(slot < 2 * kMaxWorkers, wd, kCheckRing)) break;
     float* part = a.parts + static_cast<long long>(slot) * a.part_floats;
     for (int e = gtid; e < rows * HSP; e += 128) {
       const int r = e / HSP, d = e % HSP;
@@ -831,6 +848,12 @@ __global__ void __launch_bounds__(128) attend_join_sm103a_kernel(const AttendArg
   const int* header = a.headers + worker * 8;
   const int pieces = header[kHeadPieces];
   if (pieces == 0 || r >= header[kHeadRows]) return;
+  [[maybe_unused]] __shared__ int s_abort;
+  [[maybe_unused]] const Watchdog wd{0, a.v.status, &s_abort};
+  if (!CSA_CHECK(pieces > 0 && worker + pieces <= static_cast<int>(gridDim.x) &&
+                     2 * (worker + pieces) <= 2 * kMaxWorkers,
+                 wd, kCheckRing))
+    return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int E = HSP / 32;
   auto part_of = [&](int i) {

@@ -184,6 +184,15 @@ __device__ Unit decode_unit(const PromptArgs& a, int row_limit, const long long*
   return r;
 }
 
+// (checking build) whether a unit's rows and tiles are its sequence's.
+[[maybe_unused]] __device__ __forceinline__ bool unit_ok(const PromptArgs& a, const Unit& u) {
+  const int tiles = (u.q.length + kTile - 1) / kTile;
+  return u.s >= 0 && u.s < a.v.sequences && u.head >= 0 && u.head < a.v.heads && u.row0 >= 0 &&
+         u.rows > 0 && u.rows <= kUnitRows &&
+         u.row0 + u.rows <= static_cast<long long>(u.q.n) * a.group && u.q.row0 >= 0 &&
+         u.q.row0 + u.q.n <= a.v.rows && u.n[0] <= tiles && u.n[1] >= 0 && u.n[1] <= tiles;
+}
+
 __device__ __forceinline__ int tile_token(const Unit& u, int j) {
   return (j < u.sink_tiles ? j : j - u.sink_tiles + u.window_tile) * kTile;
 }
@@ -470,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     u = reinterpret_cast<const Unit*>(gbase + L::kUnits)[slot];
     __syncwarp();
     if (lane == 0) mbar_arrive(u_empty(slot));
-    return true;
+    return CSA_CHECK(u.n[0] < 0 || unit_ok(a, u), wd, kCheckTile);
   };
   const int D = a.v.head_size;
 
@@ -725,6 +734,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (n > 0)
         for (int j = -1; j < n; ++j, to_slot.next(), from_slot.next()) {
           const uint32_t slot = to_slot.slot, rs = from_slot.slot;
+          if (!CSA_CHECK(slot < kSlots && rs < kRawSlots, wd, kCheckRing)) {
+            ok = false;
+            break;
+          }
           if (!mbar_wait_lanes(raw_full(rs), from_slot.phase, wd, kSiteLoaderEmpty) ||
               !mbar_wait_lanes(empty(slot), to_slot.phase ^ 1u, wd, kSiteLoaderEmpty)) {
             ok = false;
@@ -903,6 +916,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t rs = it % kRawSlots;
         // Everything is worked out before the slot is free.
         const bool k_here = j + 1 < n && page >= 0, v_here = page_v >= 0;
+        if (!__all_sync(0xFFFFFFFFu,
+                        CSA_CHECK(rs < kRawSlots && page < a.v.pages && page_v < a.v.pages &&
+                                      (!copies || (tile_token(u, j + 1) + 16 * lane) % P +
+                                                          16 * groups <= P),
+                                  wd, kCheckRing))) {
+          ok = false;
+          break;
+        }
         const uint32_t here = __ballot_sync(0xFFFFFFFFu, k_here && lane < 4) |
                               __ballot_sync(0xFFFFFFFFu, v_here && lane < 4) << 4;
         const uint32_t bytes = copy_bytes * (__popc(here & copy_mask) + __popc(here >> 4 & copy_mask));
@@ -1011,6 +1032,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool did = false;
         if (next_o < next_s) {
           const uint32_t p = products + next_o, slot = at_o.slot;
+          if (!CSA_CHECK(slot < kSlots && o_tmem - tmem + HSP <= kTmemCols, wd, kCheckTmem)) {
+            ok = false;
+            break;
+          }
           if (mbar_poll_warp(p_ready(g, p & 1u), (p >> 1) & 1u) &&
               mbar_poll_warp(v_full(slot), at_o.phase)) {
             tc_fence_after_sync();
@@ -1030,6 +1055,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (next_s < n && next_s <= next_o + 1) {
           const uint32_t slot = at_s.slot;
+          if (!CSA_CHECK(slot < kSlots && s_tmem - tmem + 2 * kTile <= kTmemCols, wd,
+                         kCheckTmem)) {
+            ok = false;
+            break;
+          }
           if (mbar_poll_warp(k_full(slot), at_s.phase)) {
             tc_fence_after_sync();
             const uint32_t buffer = (products + next_s) & 1u;

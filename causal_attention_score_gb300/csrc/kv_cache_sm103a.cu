@@ -206,6 +206,15 @@ __device__ __forceinline__ Place place_of(const CacheArgs& a, const Unit& u) {
   return r;
 }
 
+// (checking build) whether a place is inside the cache and the rows.
+[[maybe_unused]] __device__ __forceinline__ bool place_ok(const CacheArgs& a, const Unit& u,
+                                                          const Place& at) {
+  const Part& p = at.p;
+  return u.h >= 0 && u.h < a.v.heads && (u.which == 0 || u.which == 1) && at.page < a.v.pages &&
+         p.t0 >= 0 && p.t0 < p.t1 && p.t1 <= a.v.page_tokens && p.row >= 0 &&
+         p.row + p.t1 - p.t0 <= a.v.rows;
+}
+
 template <int kThreads>
 __device__ __forceinline__ void worker_sync(int worker) {
   asm volatile("bar.sync %0, %1;" ::"r"(1 + worker), "n"(kThreads) : "memory");
@@ -218,6 +227,8 @@ __global__ void __launch_bounds__(kBlockThreads, kWritePerSm)
   grid_dependency_wait();
   constexpr int kWorkers = kBlockThreads / kThreads;
   __shared__ uint32_t s_max[kBlockThreads / 32];
+  [[maybe_unused]] __shared__ int s_abort;
+  [[maybe_unused]] const Watchdog wd{0, a.v.status, &s_abort};
   const int tid = threadIdx.x % kThreads;
   const int worker = threadIdx.x / kThreads;
   const int D8 = a.v.head_size / 8;
@@ -232,6 +243,10 @@ __global__ void __launch_bounds__(kBlockThreads, kWritePerSm)
       continue;
     }
     const Part& p = at.p;
+    if (!CSA_CHECK(place_ok(a, w, at) && (p.t1 - p.t0) * D8 <= kThreads * NV, wd, kCheckTile)) {
+      next = place_of(a, u);
+      continue;
+    }
     const long long token = a.token[w.which];
     const T* x = static_cast<const T*>(a.x[w.which]) + static_cast<long long>(p.row) * token +
                  w.h * a.head_stride[w.which];
@@ -378,6 +393,8 @@ __global__ void __launch_bounds__(kBlockThreads, kReadPerSm)
     cache_read_sm103a_kernel(const CacheArgs a) {
   grid_dependency_wait();
   constexpr int kWorkers = kBlockThreads / 32;
+  [[maybe_unused]] __shared__ int s_abort;
+  [[maybe_unused]] const Watchdog wd{0, a.v.status, &s_abort};
   const int lane = threadIdx.x % 32;
   const int D8 = a.v.head_size / 8;
   Unit u = first_unit(a, blockIdx.x * kWorkers + threadIdx.x / 32);
@@ -391,6 +408,10 @@ __global__ void __launch_bounds__(kBlockThreads, kReadPerSm)
       continue;
     }
     const Part& p = at.p;
+    if (!CSA_CHECK(place_ok(a, w, at), wd, kCheckTile)) {
+      next = place_of(a, u);
+      continue;
+    }
     const long long token = a.token[w.which];
     T* y = static_cast<T*>(a.x[w.which]) + static_cast<long long>(p.row) * token +
            w.h * a.head_stride[w.which];

@@ -56,6 +56,7 @@ struct RotaryArgs {
   int start, period;
   float amplitude;
   int backward;
+  int* status;
 };
 
 // Elements of type T in 32-bit words: one (fp32) or two.
@@ -164,6 +165,8 @@ __global__ void __launch_bounds__(kRotThreads, 8) rotary_sm103a_kernel(const Rot
   const T* x = static_cast<const T*>(a.x);  // may be out itself
   T* out = static_cast<T*>(a.out);
   constexpr int kMost = kHeads<V, kInterleaved>;
+  [[maybe_unused]] __shared__ int s_abort;
+  [[maybe_unused]] const Watchdog wd{0, a.status, &s_abort};
   const unsigned first = blockIdx.x * kRotThreads + threadIdx.x;
   const unsigned rest = first / a.slots;
   int slot = static_cast<int>(first - rest * a.slots);
@@ -177,6 +180,13 @@ __global__ void __launch_bounds__(kRotThreads, 8) rotary_sm103a_kernel(const Rot
     if (h0 >= a.groups) h0 -= a.groups, ++t;
   };
   for (; t < a.tokens; advance()) {
+    if (!CSA_CHECK(t >= 0 && slot >= 0 && slot < a.slots && h0 >= 0 && h0 < a.groups &&
+                       h0 < a.heads &&
+                       (slot < a.rot_slots
+                            ? (slot + 1) * kRun * kRuns <= a.rot_dim
+                            : a.rot_dim + (slot - a.rot_slots + 1) * V <= a.head_size),
+                   wd, kCheckTile))
+      break;
     int pos;
     if (a.positions)
       pos = a.positions[t];
@@ -306,6 +316,7 @@ int rotary_launch(const RotaryCall& call, cudaStream_t stream, const DeviceInfo&
   a.period = call.period;
   a.amplitude = call.amplitude;
   a.backward = call.backward;
+  a.status = dev.status_word;
   const int esize = call.dtype == CSA_F32 ? 4 : 2;
   const int V = 16 / esize;
   auto rows16 = [&](const void* p, long long token, long long head) {
