@@ -843,6 +843,34 @@ Range range_of(const void* p, int esize, long long span) {
 }
 bool ranges_meet(const Range& a, const Range& b) { return a.from < b.to && b.from < a.to; }
 
+// One of two tensors of [tokens][heads][size] rows.
+struct Rows {
+  const void* p;
+  long long token, head;
+};
+// Whether two such tensors may share elements: their ranges meet, and they do not lie side by
+// side in a larger tensor, where the elements of one, counted modulo a stride that both have,
+// come before the other's, as slices of a packed tensor do. Spans and alignment were checked.
+bool rows_meet(const Rows& a, const Rows& b, long long tokens, int heads, int size, int esize) {
+  if (!ranges_meet(range_of(a.p, esize, span_of(tokens, heads, size, a.token, a.head)),
+                   range_of(b.p, esize, span_of(tokens, heads, size, b.token, b.head))))
+    return false;
+  const long long apart = (static_cast<const char*>(b.p) - static_cast<const char*>(a.p)) / esize;
+  // What `count` runs of `size`, `step` apart, take of a stride.
+  auto taken = [&](long long stride, long long step, long long count) {
+    return step % stride == 0 ? size : (count - 1) * step + size;
+  };
+  auto beside = [&](long long stride, long long step_a, long long step_b, long long count) {
+    const long long d = (apart % stride + stride) % stride;
+    return d >= taken(stride, step_a, count) && d + taken(stride, step_b, count) <= stride;
+  };
+  if (a.token == b.token && a.token > 0 && tokens > 1 &&
+      beside(a.token, a.head, b.head, heads))
+    return false;
+  return !(a.head == b.head && a.head > 0 && heads > 1 &&
+           beside(a.head, a.token, b.token, tokens));
+}
+
 // An entry point's body: what it throws (no memory on the host) becomes a status.
 template <typename Body>
 csa_status no_throw(Body body) noexcept {
@@ -885,7 +913,8 @@ int rotary(const char* who, const RotaryCall& c, void* stream) {
     if ((c.tokens > 1 && c.x_token != c.out_token) || (c.heads > 1 && c.x_head != c.out_head))
       return set_error(CSA_ERR_UNSUPPORTED, w + ": in place needs equal strides");
   } else {
-    if (ranges_meet(range_of(c.x, esize, nx), range_of(c.out, esize, no)))
+    if (rows_meet({c.x, c.x_token, c.x_head}, {c.out, c.out_token, c.out_head}, c.tokens, c.heads,
+                  c.head_size, esize))
       return set_error(CSA_ERR_UNSUPPORTED, w + ": input and output overlap in part");
   }
   DeviceInfo dev;
@@ -1105,11 +1134,9 @@ csa_status cache_attention_forward(void* out, const void* q, int dtype, int q_he
     // A unit reads its own rows of q before it writes them, so in place is fine.
     const bool in_place = out == q && (batch->rows == 1 || q_token_stride == out_token_stride) &&
                           (q_heads == 1 || q_head_stride == out_head_stride);
-    const int D = cache->head_size;
     if (!in_place &&
-        ranges_meet(range_of(q, 2, span_of(batch->rows, q_heads, D, q_token_stride, q_head_stride)),
-                    range_of(out, 2,
-                             span_of(batch->rows, q_heads, D, out_token_stride, out_head_stride))))
+        rows_meet({q, q_token_stride, q_head_stride}, {out, out_token_stride, out_head_stride},
+                  batch->rows, q_heads, cache->head_size, 2))
       return set_error(CSA_ERR_UNSUPPORTED, w + ": q and out overlap in part");
     const size_t need = cache_attention_workspace_bytes(cache->head_size);
     if (!workspace || workspace_bytes < need)

@@ -387,9 +387,11 @@ csa_status batch_matmul_nt(float* Y, const void* X, const void* W, int batch, in
  *                tokens and heads *_token_stride and *_head_stride elements apart (so the
  *                Q and K parts of a packed (B,T,3,NH,HS) tensor are rotated in one call
  *                with heads = 2 NH and token stride 3C). out == x with equal strides
- *                rotates in place (elements from rot_dim on are then not touched); memory
- *                ranges that overlap otherwise are refused (CSA_ERR_UNSUPPORTED), as are
- *                strides with which rows of `out` would overlap (CSA_ERR_SHAPE).
+ *                rotates in place (elements from rot_dim on are then not touched). Memory
+ *                ranges that overlap otherwise are refused (CSA_ERR_UNSUPPORTED), but for
+ *                slices side by side in one tensor (with one stride between tokens, or
+ *                between heads), and so are strides with which rows of `out` would overlap
+ *                (CSA_ERR_SHAPE).
  *   turns        device, rot_dim/2 values of csa_rotary_turns.
  *   amplitude    a, finite.
  *   positions    device, int32 [tokens]; a negative one marks padding, whose rows of out
@@ -513,8 +515,8 @@ csa_status kv_cache_read(void* k, void* v, int dtype, int64_t k_token_stride,
  * over the visible t: t <= p, and with window > 0 also p - t < window or t < sinks. Query
  * heads h share kv head h / (q_heads / heads). A row that sees nothing gives zeros.
  *   out, q     device, [rows][q_heads][head_size] of CSA_BF16 or CSA_F16, strides as above;
- *              out == q with equal strides is fine, ranges that overlap otherwise are
- *              refused (CSA_ERR_UNSUPPORTED);
+ *              out == q with equal strides is fine, and so are slices side by side in one
+ *              tensor; ranges that overlap otherwise are refused (CSA_ERR_UNSUPPORTED);
  *   q_heads    a multiple of cache->heads;
  *   scale      finite (the framework's score uses 1/sqrt(head_size));
  *   window     0: none; sinks >= 0 (used with a window);
