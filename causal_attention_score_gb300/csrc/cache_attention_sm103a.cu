@@ -11,9 +11,9 @@
 // registers, is the right instruction here: codes go from HBM to registers to
 // the tensor core with no trip through shared memory.
 //
-// Measured: 64 sequences of 300 to 8191 tokens, 16 heads of 128: 138 us, 6.5 TB/s of
-// codes (0.95 of the copy rate); 48 of 100 to 15000 with a window of 4096, 8 kv heads:
-// 62 us (0.72). One sequence of 777 tokens, 12 heads of 64: 8.9 us, all latency (the work
+// Measured: 64 sequences of 300 to 8191 tokens, 16 heads of 128: 139 us, 6.4 TB/s of
+// codes (0.94 of the copy rate); 48 of 100 to 15000 with a window of 4096, 8 kv heads:
+// 62 us (0.71). One sequence of 777 tokens, 12 heads of 64: 10 us, all latency (the work
 // list 1.3 us, the way to the first codes 2.5 us, the join 3 us). With 16 rows a block
 // the instructions of a step bound it (4 TB/s at 64 x 4K tokens), not HBM.
 //

@@ -44,7 +44,7 @@
 // (48 cycles for 128 x 64 x 16 with both operands in shared memory, whose reads bound it;
 // 64 for 128 x 128 x 16 with A in TMEM). Measured: 2 prompts of 4096 tokens, 16 heads of
 // 128: 144 us (955 TFLOP/s); 5 chunks of 200 to 777 tokens after up to 9000, 32 query and
-// 4 kv heads of 64: 170 us. A step takes 1900 cycles (1650 with heads of 64): a softmax
+// 4 kv heads of 64: 174 us. A step takes 1900 cycles (1650 with heads of 64): a softmax
 // warp 1450 (1230) and the rest of waiting, a conversion warp 1700 (1160); a unit's end
 // and the next one's first scores 9000. No unit is saturated (tensor pipe 44 %, issue
 // slots 53 %, MUFU 22 %): what counts is the latency of each role's chain. What moved it:

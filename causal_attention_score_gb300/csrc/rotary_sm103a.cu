@@ -11,14 +11,16 @@
 // fp64 arithmetic is slow on this GPU. The frequencies come as turns per
 // position in 64-bit fixed point, F = round(f / 2pi * 2^64): the product p * F
 // modulo 2^64, one integer multiplication, is the fraction of a turn itself,
-// reduced exactly, off by at most |p| * 2^-65 turns. Its upper 32 bits become
-// an angle in half turns for sincospif.
+// reduced exactly. It is off by |p| times what F is: 2^-65 turns by its own
+// rounding, f 2^-51 / 2pi by f's, which is a double after a few operations (p f 2^-51
+// radians: 2^-20 at f = 1 and p = 2^31, below the rounding to fp32 up to p f = 2^27).
+// Its upper 32 bits become an angle in half turns for sincospif.
 //
 // Bound: HBM (one read and one write of x). A thread takes one slot (16 bytes of
 // each half of the rotated part, or 16 bytes of interleaved pairs) of one token in
 // several heads, 64 bytes that it asks for at once, and computes the sines of that slot
 // once for all of them. Where that leaves SMs without work, a thread takes one head.
-// 8192 x 24 heads of 64 in bf16: 10.2 us (4.9 TB/s); 8192 x 32 of 128 in fp32: 46 us
+// 8192 x 24 heads of 64 in bf16: 10.3 us (4.9 TB/s); 8192 x 32 of 128 in fp32: 46 us
 // (5.8 TB/s). With 128 bytes a thread and 80 registers: 11.5 and 51 us; with the sines
 // before the loads and divisions for every item: 14.2 and 59 us.
 #include <cuda_bf16.h>

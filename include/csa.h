@@ -399,7 +399,9 @@ csa_status batch_matmul_nt(float* Y, const void* X, const void* W, int batch, in
  *                start + (period > 0 ? t % period : t), start >= 0.
  * Any head_size >= 2, rot_dim even, 2 <= rot_dim <= head_size. Pointers and strides need
  * only the type's alignment; rows of 16-byte multiples take 16-byte loads. Angles come
- * from 64-bit fixed-point turns: no precision is lost at any 32-bit position.
+ * from 64-bit fixed-point turns, whose product with the position is exact: what they are off
+ * by is the frequency's rounding in double precision, p f 2^-51 radians at position p (below
+ * the rounding to fp32 up to p f = 2^27, 2^-20 near 2^31).
  * Asynchronous on `stream`.
  *
  * rotary_backward -- the gradient: dx = a R(-p f) dy, same arguments (dx for out, dy for x).
@@ -472,6 +474,7 @@ typedef struct csa_kv_cache {
  *   max_new      at least every offsets[s + 1] - offsets[s] (it sizes the launch).
  * Rows past offsets[sequences] are left as they were. Rows before a sequence's beginning
  * (more rows than its length) are neither written nor read; attention gives zeros there.
+ * sequences, table_width, rows and max_new are at least 1 (an empty batch is no call).
  * These arrays are read on the device: a sequence whose entries break the rules is skipped,
  * as is a block whose page number is outside [0, pages), and csa_get_status reports
  * CSA_ERR_INDEX. Pages that a call writes belong to one sequence each and are in its
