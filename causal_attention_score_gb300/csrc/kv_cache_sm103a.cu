@@ -22,11 +22,11 @@
 // computed two at a time (packed fp32) and positions with a multiplication. A write
 // reads the new rows once (two passes over registers: the magnitude, then the codes)
 // and writes one byte an element; older codes of a block are read and written only when
-// its scale grew (a token of 256 sequences, 8 heads of 128: 5.5 us, and 16 us where every
-// block of up to 32 tokens grows, 48 us with 128: one warp a block). A unit of work is one (sequence, page, K or V, head); units of one
-// page's heads are neighbours, so that CTAs running side by side read neighbouring
-// memory of a row. A unit's place (sequence, page) is looked up while the rows of the one
-// before are on their way.
+// its scale grew (a token of 256 sequences, 8 heads of 128: 5.5 us, and 16 us where
+// every block of up to 32 tokens grows, 48 us with 128: one warp a block). A unit of
+// work is one (sequence, page, K or V, head); units of one page's heads are neighbours,
+// so that CTAs running side by side read neighbouring memory of a row. A unit's place
+// (sequence, page) is looked up while the rows of the one before are on their way.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
