@@ -497,7 +497,9 @@ typedef struct csa_kv_batch {
  * e4m3 the smallest power of two with 448 s >= m, and at least 2^-100. Codes are x / s
  * rounded to nearest even (NaN: 0; infinities: the largest code); when a block's scale
  * grows, its older codes become code * s_old / s, rounded again. The codes are those of
- * this definition in real numbers (no fp32 rounding shows). Asynchronous on `stream`.
+ * this definition in real numbers (no fp32 rounding shows). A call whose rows begin inside a
+ * block takes the slots before them as written, with the scale that is there. Asynchronous on
+ * `stream`.
  *
  * kv_cache_read -- the values code * scale of the batch's rows, rounded once to `dtype`
  * (CSA_BF16, CSA_F16 or CSA_F32), into k and v. The batch may name other rows than those of
