@@ -823,7 +823,9 @@ __global__ void __launch_bounds__(128 * kGroups<HSP, NB>, 1)
     if (!whole && begins) {
       left_open = true;
       if (gtid == 0) {
-        header[kHeadPieces] = 1 + static_cast<int>((piece.after + share - 1) / share);
+        // (at most those there are: lengths may have changed under the call)
+        header[kHeadPieces] = static_cast<int>(
+            min(1 + (piece.after + share - 1) / share, static_cast<long long>(a.workers - worker)));
         header[kHeadRow0] = row0;
         header[kHeadFirst] = row_first;
         header[kHeadHead] = piece.head;

@@ -151,13 +151,14 @@ __device__ Unit decode_unit(const PromptArgs& a, int row_limit, const long long*
     if (prefix[mid] <= u) lo = mid;
     else hi = mid;
   }
-  Unit r;
+  Unit r{};
   long long base = prefix[lo];
   for (r.s = per == 1 ? order[lo] : lo * per;; ++r.s) {
     r.q = kv_sequence(a.v, r.s);
     const long long n = units_of(a, row_limit, r.q);
-    if (per == 1 || u < base + n) break;
+    if (u < base + n) break;
     base += n;
+    if (per == 1 || r.s + 1 >= a.v.sequences) return r;  // lengths changed under the call: no rows
   }
   const int all_rows = static_cast<int>(static_cast<long long>(r.q.n) * a.group);
   const int blocks = (all_rows + kUnitRows - 1) / kUnitRows;

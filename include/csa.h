@@ -479,7 +479,8 @@ typedef struct csa_kv_cache {
  * as is a block whose page number is outside [0, pages), and csa_get_status reports
  * CSA_ERR_INDEX. Pages that a call writes belong to one sequence each and are in its
  * table once (prefix pages that several sequences share are full, and only read). The
- * arrays must not change while a call is under way.
+ * arrays must not change while a call is under way: what it computes is then undefined,
+ * though it stays within the rows, the pages and the workspace.
  */
 typedef struct csa_kv_batch {
   const int32_t* offsets;
