@@ -15,6 +15,8 @@ Public API (all compute runs in libcsa_gb300.so; see include/csa.h):
 * ``kv_cache_write`` / ``kv_cache_read`` on a ``KvCache`` (paged keys and values in 8 bits)
   for the rows a ``KvBatch`` names, and ``cache_attention_forward`` over it
   (``cache_attention`` allocates; ``cache_attention_workspace_size`` for its scratch)
+* ``token_logprobs_forward`` / ``token_logprobs_backward`` (``token_logprobs`` allocates): log
+  probabilities of given tokens from rows of logits, entropy, top alternatives, the gradient
 * allocating helpers ``trimul(qkv)``, ``causal_softmax(qkv)`` and ``dense(X, W)``
 * ``get_status()`` for the device watchdog word, ``set_wait_limit_ns`` /
   ``get_wait_limit_ns`` for its bound (default 2 s, or ``CSA_WAIT_LIMIT_NS``),
@@ -32,6 +34,7 @@ from .ops import (DENSE_FETCH_AUTO, DENSE_FETCH_LOADERS, DenseGroupedPlan, batch
                   dense_xwt_grouped, get_status, get_stream_sm_limit, get_wait_limit_ns,
                   set_dense_fetch, set_stream_sm_limit, set_wait_limit_ns, trimul, trimul_forward,
                   trimul_forward_f32, version)
+from .logprobs import token_logprobs, token_logprobs_backward, token_logprobs_forward
 from .serving import (KvBatch, KvCache, RotaryTable, cache_attention, cache_attention_forward,
                       cache_attention_workspace_size, kv_cache_read, kv_cache_write,
                       rotary_backward, rotary_forward, rotary_qkv)
@@ -45,6 +48,7 @@ __all__ = [
     "RotaryTable", "rotary_forward", "rotary_backward", "rotary_qkv",
     "KvCache", "KvBatch", "kv_cache_write", "kv_cache_read",
     "cache_attention_forward", "cache_attention", "cache_attention_workspace_size",
+    "token_logprobs_forward", "token_logprobs_backward", "token_logprobs",
     "CSA_ERR_INDEX",
     "DENSE_FETCH_AUTO", "DENSE_FETCH_LOADERS", "version", "CsaError", "CSA_OK", "CSA_ERR_NULL",
     "CSA_ERR_SHAPE",

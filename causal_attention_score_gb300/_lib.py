@@ -61,6 +61,10 @@ SIGNATURES = {
     "cache_attention_forward": (_i, [_vp, _vp, _i, _i, _i64, _i64, _i64, _i64, _vp, _vp, _f, _i,
                                      _i, _vp, ctypes.c_size_t, _vp]),
     "cache_attention_workspace_size": (_i, [_vp, _i, ctypes.POINTER(ctypes.c_size_t)]),
+    "token_logprobs_forward": (_i, [_vp, _vp, _vp, _vp, _i, _i64, _i, _i64, _vp, _f, _i, _vp, _vp,
+                                    _vp]),
+    "token_logprobs_backward": (_i, [_vp, _vp, _i, _i64, _i, _i64, _i64, _vp, _f, _vp, _vp, _vp,
+                                     _vp, _i, _vp, _vp, _vp]),
     "csa_get_status": (_i, [_vp]),
     "csa_status_string": (ctypes.c_char_p, [_i]),
     "csa_last_error": (ctypes.c_char_p, []),

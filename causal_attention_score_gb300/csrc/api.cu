@@ -995,6 +995,25 @@ int kv_rows(const char* who, const csa_kv_cache* cache, const csa_kv_batch* batc
   return rc == CSA_OK ? CSA_OK : set_error(rc, err);
 }
 
+// Checks shared by the two calls on logits.
+int logits_ok(const std::string& w, const void* logits, int dtype, long long rows, int vocab,
+              long long stride, const int32_t* tokens, float scale, int top) {
+  if (!logits || !tokens) return set_error(CSA_ERR_NULL, w + ": null pointer");
+  if (dtype != CSA_BF16 && dtype != CSA_F16 && dtype != CSA_F32)
+    return set_error(CSA_ERR_UNSUPPORTED, w + ": unknown dtype");
+  if (rows <= 0 || vocab <= 0) return set_error(CSA_ERR_SHAPE, w + ": rows, vocab must be >= 1");
+  if (vocab > 1 << 30) return set_error(CSA_ERR_UNSUPPORTED, w + ": vocab > 2^30");
+  if (top < 0 || top > 32 || top > vocab)
+    return set_error(CSA_ERR_SHAPE, w + ": top must be within [0, min(32, vocab)]");
+  if (!(scale > 0.0f && scale <= 18446744073709551616.0f))
+    return set_error(CSA_ERR_SHAPE, w + ": scale must be > 0, at most 2^64");
+  if ((rows > 1 && stride < vocab) || span_of(rows, 1, vocab, rows > 1 ? stride : vocab, 0) < 0)
+    return set_error(CSA_ERR_SHAPE, w + ": bad stride");
+  if (!aligned(logits, dtype == CSA_F32 ? 4 : 2) || !aligned(tokens, 4))
+    return set_error(CSA_ERR_ALIGN, w + ": a pointer breaks its type's alignment");
+  return CSA_OK;
+}
+
 int attention_heads_ok(const std::string& w, const csa_kv_cache* cache, int q_heads) {
   const int rc = cache_args_ok(w, cache);
   if (rc != CSA_OK) return rc;
@@ -1155,6 +1174,73 @@ csa_status cache_attention_forward(void* out, const void* q, int dtype, int q_he
                                 {q, out, dtype, q_heads, q_token_stride, q_head_stride,
                                  out_token_stride, out_head_stride, scale, window, sinks, workspace},
                                 static_cast<cudaStream_t>(stream), dev, err);
+    return rc == CSA_OK ? CSA_OK : set_error(rc, err);
+  });
+}
+
+csa_status token_logprobs_forward(float* logprob, float* entropy, float* stats, const void* logits,
+                                  int dtype, int64_t rows, int vocab, int64_t stride,
+                                  const int32_t* tokens, float scale, int top, float* top_logprob,
+                                  int32_t* top_token, void* stream) {
+  return no_throw([&] {
+    t_last_error.clear();
+    const std::string w("token_logprobs_forward");
+    int rc = logits_ok(w, logits, dtype, rows, vocab, stride, tokens, scale, top);
+    if (rc != CSA_OK) return rc;
+    if (!logprob || !entropy || !stats || (top > 0 && (!top_logprob || !top_token)))
+      return set_error(CSA_ERR_NULL, w + ": null pointer");
+    if (!aligned(logprob, 4) || !aligned(entropy, 4) || !aligned(stats, 8) ||
+        (top > 0 && (!aligned(top_logprob, 4) || !aligned(top_token, 4))))
+      return set_error(CSA_ERR_ALIGN, w + ": a pointer breaks its type's alignment");
+    DeviceInfo dev;
+    std::string err;
+    rc = current_device(dev, err);
+    if (rc != CSA_OK) return set_error(rc, err);
+    apply_stream_sm_limit(dev, static_cast<cudaStream_t>(stream));
+    rc = logprobs_forward_launch({logits, dtype, stride, rows, vocab, top, tokens, scale, logprob,
+                                  entropy, stats, top_logprob, top_token},
+                                 static_cast<cudaStream_t>(stream), dev, err);
+    return rc == CSA_OK ? CSA_OK : set_error(rc, err);
+  });
+}
+
+csa_status token_logprobs_backward(void* dlogits, const void* logits, int dtype, int64_t rows,
+                                   int vocab, int64_t d_stride, int64_t stride,
+                                   const int32_t* tokens, float scale, const float* stats,
+                                   const float* entropy, const float* d_logprob,
+                                   const float* d_entropy, int top, const float* d_top,
+                                   const int32_t* top_token, void* stream) {
+  return no_throw([&] {
+    t_last_error.clear();
+    const std::string w("token_logprobs_backward");
+    int rc = logits_ok(w, logits, dtype, rows, vocab, stride, tokens, scale, top);
+    if (rc != CSA_OK) return rc;
+    const bool with_top = top > 0 && d_top;
+    if (!dlogits || !stats || !entropy || (with_top && !top_token))
+      return set_error(CSA_ERR_NULL, w + ": null pointer");
+    const int esize = dtype == CSA_F32 ? 4 : 2;
+    if (!aligned(dlogits, esize) || !aligned(stats, 8) || !aligned(entropy, 4) ||
+        !aligned(d_logprob, 4) || !aligned(d_entropy, 4) ||
+        (with_top && (!aligned(d_top, 4) || !aligned(top_token, 4))))
+      return set_error(CSA_ERR_ALIGN, w + ": a pointer breaks its type's alignment");
+    if (rows == 1) stride = d_stride = vocab;
+    if (d_stride < vocab || span_of(rows, 1, vocab, d_stride, 0) < 0)
+      return set_error(CSA_ERR_SHAPE, w + ": bad stride");
+    if (dlogits == logits) {
+      if (stride != d_stride)
+        return set_error(CSA_ERR_UNSUPPORTED, w + ": in place needs equal strides");
+    } else if (rows_meet({logits, stride, 0}, {dlogits, d_stride, 0}, rows, 1, vocab, esize)) {
+      return set_error(CSA_ERR_UNSUPPORTED, w + ": logits and gradient overlap in part");
+    }
+    DeviceInfo dev;
+    std::string err;
+    rc = current_device(dev, err);
+    if (rc != CSA_OK) return set_error(rc, err);
+    apply_stream_sm_limit(dev, static_cast<cudaStream_t>(stream));
+    rc = logprobs_backward_launch(
+        {logits, dlogits, dtype, stride, d_stride, rows, vocab, with_top ? top : 0, tokens, scale,
+         stats, entropy, d_logprob, d_entropy, with_top ? d_top : nullptr, top_token},
+        static_cast<cudaStream_t>(stream), dev, err);
     return rc == CSA_OK ? CSA_OK : set_error(rc, err);
   });
 }

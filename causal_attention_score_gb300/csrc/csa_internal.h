@@ -209,6 +209,34 @@ int cache_prompt_launch(const csa_kv_cache& cache, const csa_kv_batch& batch,
                         const AttendCall& call, PromptList* list, cudaStream_t stream,
                         const DeviceInfo& dev, std::string& err);
 
+// Log probabilities of tokens: logits [rows][vocab], strides in elements.
+struct LogprobsCall {
+  const void* logits;
+  int dtype;
+  long long stride, rows;
+  int vocab, top;
+  const int* tokens;
+  float scale;
+  float *logprob, *entropy, *stats, *top_logprob;
+  int* top_token;
+};
+struct LogprobsGrad {
+  const void* logits;
+  void* dlogits;
+  int dtype;
+  long long stride, d_stride, rows;
+  int vocab, top;
+  const int* tokens;
+  float scale;
+  const float *stats, *entropy;
+  const float *d_logprob, *d_entropy, *d_top;  // any may be nullptr
+  const int* top_token;
+};
+int logprobs_forward_launch(const LogprobsCall& call, cudaStream_t stream, const DeviceInfo& dev,
+                            std::string& err);
+int logprobs_backward_launch(const LogprobsGrad& call, cudaStream_t stream, const DeviceInfo& dev,
+                             std::string& err);
+
 // The device's view of a cache and a batch (kv_cache.cuh).
 struct KvView;
 KvView kv_view(const csa_kv_cache& cache, const csa_kv_batch& batch, const DeviceInfo& dev);

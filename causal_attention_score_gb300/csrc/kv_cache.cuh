@@ -50,6 +50,7 @@ enum IndexSite : int {
   kIndexPage = 201,     // a table entry outside [0, pages)
   kIndexRows = 202,     // offsets outside [0, rows], decreasing, or more than max_new apart
   kIndexLength = 203,   // a length outside [0, table_width * page_tokens]
+  kIndexToken = 204,    // a token outside the vocabulary
 };
 
 __device__ __forceinline__ void report_index(int* status, int site) {

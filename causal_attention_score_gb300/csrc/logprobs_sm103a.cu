@@ -1,0 +1,769 @@
+// Log probabilities of given tokens, with entropy and the top alternatives, from rows of
+// logits x [rows][vocab], and the gradient of what is made of them. With p = softmax(s x):
+//
+//   logprob = s x[tok] - lse,   lse = s m + log S,   m = max x,  S = sum exp(s (x - m))
+//   entropy = -sum p log p = log S - T / S,          T = sum exp(d) d,  d = s (x - m)
+//   top: the k largest logits (of equal ones the lowest index), and their log probabilities
+//   dx_j = s [ g (1{j = tok} - p_j) - h p_j (log p_j + H) + sum_i g_i (1{j = top_i} - p_j) ]
+//
+// One pass over the logits: a thread keeps the maximum of what it has seen and S and T
+// relative to it, rescaled when the maximum grows (T' = r (T - D S), S' = r S, r = exp(-D)).
+// Exponents are worked out as (x - m) c with c = s log2(e), the difference first, which is
+// exact near the maximum. All sums are fp32 over at most a few hundred terms a thread, then a
+// tree. A forbidden word's -inf has weight 0 and adds 0 to T (its d is clamped for the
+// product); a NaN or +inf makes its row's results NaN.
+//
+// Top alternatives without a second pass: the k-th largest of the threads' maxima, found by
+// a search over the bits of the order-preserving integer of a float, is a lower bound of the
+// k-th largest logit, and only the k threads whose maximum reaches it hold larger ones. Their
+// elements alone (k / 512 of the row) are read again, what reaches the bound is ranked by
+// counting. Threads whose maxima tie at the bound are told apart by the index of their first
+// such element.
+//
+// Bound: HBM, one read of the logits (and one write of the gradient). A CTA of 256 threads takes
+// a row and four 16-byte loads a thread at once; six such CTAs an SM, so that some load while
+// others rank. 8192 x 50257 in fp32 with two alternatives: 255 us (6.5 TB/s, 0.96 of the copy
+// rate; five CTAs 261, four 283, two of 512 threads 323). Few rows are split over a cluster of up
+// to eight CTAs, whose results meet in the first one's shared memory.
+// The searches take four bits a round (a round is a barrier; bit by bit one row of 50257 with 20
+// alternatives took 15.6 us instead of 12.3).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cfloat>
+#include <cmath>
+#include <cstdint>
+#include <string>
+
+#include "csa_internal.h"
+#include "kv_cache.cuh"
+#include "sm103a_ptx.cuh"
+
+namespace csa {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kForwardPerSm = 6, kBackwardPerSm = 5;  // CTAs an SM
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxTop = 32;
+constexpr int kMaxCluster = 8;
+static_assert(kWarps >= kMaxCluster, "a warp for each CTA's list");
+constexpr int kLoads = 4;         // 16-byte loads that a thread has in flight
+constexpr int kCandidates = 1024; // elements that reach the bound
+constexpr int kColumns = 64;      // threads whose elements are looked at again (at least kMaxTop)
+constexpr int kRounds = 8;        // of a search, four bits each
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLeast = -1000.0f;  // exponents below have weight 0; finite, for products with it
+
+template <typename T>
+struct Logit;
+template <>
+struct Logit<float> {
+  static constexpr int kVec = 4;
+  static __device__ __forceinline__ float get(float v) { return v; }
+  static __device__ __forceinline__ float put(float v) { return v; }
+  static __device__ __forceinline__ void unpack(const uint4& w, float (&x)[4]) {
+    x[0] = __uint_as_float(w.x);
+    x[1] = __uint_as_float(w.y);
+    x[2] = __uint_as_float(w.z);
+    x[3] = __uint_as_float(w.w);
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&x)[4]) {
+    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                      __float_as_uint(x[3]));
+  }
+};
+template <>
+struct Logit<__nv_bfloat16> {
+  static constexpr int kVec = 8;
+  static __device__ __forceinline__ float get(__nv_bfloat16 v) { return __bfloat162float(v); }
+  static __device__ __forceinline__ __nv_bfloat16 put(float v) { return __float2bfloat16_rn(v); }
+  static __device__ __forceinline__ void unpack(const uint4& q, float (&x)[8]) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&x)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+template <>
+struct Logit<__half> {
+  static constexpr int kVec = 8;
+  static __device__ __forceinline__ float get(__half v) { return __half2float(v); }
+  static __device__ __forceinline__ __half put(float v) { return __float2half_rn(v); }
+  static __device__ __forceinline__ void unpack(const uint4& q, float (&x)[8]) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      x[2 * i] = f.x;
+      x[2 * i + 1] = f.y;
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const float (&x)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+struct ForwardArgs {
+  const void* logits;
+  long long stride;
+  long long rows;
+  int vocab, top;
+  const int* tokens;
+  float scale;
+  float* logprob;
+  float* entropy;
+  float2* stats;
+  float* top_logprob;
+  int* top_token;
+  int* status;
+  int cluster;  // CTAs of a row
+};
+
+// A float as an integer of the same order, zeros alike; NaN counts as -inf. Above 0.
+__device__ __forceinline__ uint32_t order_key(float x) {
+  if (x != x) x = -INFINITY;
+  const uint32_t b = __float_as_uint(x + 0.0f);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
+}
+
+// What a thread has seen: S and T relative to m, in units of log2.
+struct Partial {
+  float top = -INFINITY;  // the largest; m = max(top, -FLT_MAX), so that differences from it are numbers
+  float m = -FLT_MAX, s = 0.0f, t = 0.0f;
+
+  // S and T relative to a larger maximum.
+  __device__ __forceinline__ void raise(float to, float c) {
+    const float d = fminf((to - m) * c, 1e30f);  // (finite, so that it times 0 is 0)
+    const float r = ex2_approx(-d);
+    t = r * fmaf(-d, s, t);
+    s *= r;
+    m = to;
+  }
+  template <int N>
+  __device__ __forceinline__ void add(const float (&x)[N], float c) {
+    float most = x[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) most = fmaxf(most, x[i]);
+    if (most > m) raise(most, c);
+    top = fmaxf(top, most);
+    const uint64_t less = pack_f32x2(-m, -m), c2 = pack_f32x2(c, c);
+    uint64_t s2 = 0, t2 = 0;
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const uint64_t y = mul_f32x2(add_f32x2(pack_f32x2(x[i], x[i + 1]), less), c2);
+      float y0, y1;
+      unpack_f32x2(y, y0, y1);
+      const uint64_t e = pack_f32x2(ex2_approx(y0), ex2_approx(y1));
+      s2 = add_f32x2(s2, e);
+      t2 = fma_f32x2(e, pack_f32x2(fmaxf(y0, kLeast), fmaxf(y1, kLeast)), t2);
+    }
+    float a, b;
+    unpack_f32x2(s2, a, b);
+    s += a + b;
+    unpack_f32x2(t2, a, b);
+    t += a + b;
+  }
+  __device__ __forceinline__ void add_one(float x, float c) {
+    if (x > m) raise(x, c);
+    top = fmaxf(top, x);
+    const float y = (x - m) * c, e = ex2_approx(y);
+    s += e;
+    t = fmaf(e, fmaxf(y, kLeast), t);
+  }
+};
+
+// A run [begin, end) of a row's elements as 16-byte chunks with the elements before the first
+// and behind the last.
+template <typename T>
+struct Run {
+  const T* row;
+  int begin, end;
+  int head, tail;  // elements at begin, and at the end, that belong to no chunk
+  int chunks;
+  const uint4* body;
+  __device__ Run(const T* r, int from, int to) : row(r), begin(from), end(to) {
+    constexpr int V = Logit<T>::kVec;
+    const int n = to - from;
+    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(r + from) % 16) / static_cast<int>(sizeof(T));
+    head = min(n, off == 0 ? 0 : V - off);
+    chunks = (n - head) / V;
+    tail = n - head - chunks * V;
+    body = reinterpret_cast<const uint4*>(r + from + head);
+  }
+  // Element index of the i-th that belongs to no chunk.
+  __device__ __forceinline__ int loose(int i) const {
+    return i < head ? begin + i : begin + head + chunks * Logit<T>::kVec + (i - head);
+  }
+};
+
+struct alignas(16) Shared {
+  float m[kWarps], s[kWarps], t[kWarps];
+  float row_m, row_s, row_t;   // of this CTA's part of the row
+  uint32_t key[kMaxTop];       // its top alternatives, in order
+  int index[kMaxTop];
+  int columns[kColumns];       // threads that may hold them
+  int count, found;
+  int counts[2 * kRounds][16];
+  float3 all[kMaxCluster];     // of every CTA of the row, at its first one
+  uint32_t all_key[kMaxCluster][kMaxTop];
+  int all_index[kMaxCluster][kMaxTop];
+  uint32_t best_key[kWarps];
+  int best_index[kWarps];
+  uint32_t cand_key[kCandidates];
+  int cand_index[kCandidates];
+};
+
+// Whether (key, index) comes before (k2, i2).
+__device__ __forceinline__ bool before(uint32_t key, int index, uint32_t k2, int i2) {
+  return key > k2 || (key == k2 && index < i2);
+}
+
+// The largest v below 2^bits with at least k threads' `mine` >= v (0 if there is none above),
+// or one that exactly k reach; `count` is how many do. Four bits a round: the threads that reach
+// each of 15 steps are counted by ballots and added up in a row of `counts` of the round's own
+// (cleared before), so that a round takes one barrier.
+__device__ __forceinline__ uint32_t kth_largest(uint32_t mine, int bits, int k, int (*counts)[16],
+                                                int& count) {
+  const int lane = static_cast<int>(lane_id());
+  uint32_t v = 0;
+  count = kThreads;
+#pragma unroll 1
+  for (int shift = (bits - 1) / 4 * 4; shift >= 0; shift -= 4, ++counts) {
+    int reach = 0;
+#pragma unroll
+    for (uint32_t i = 1; i < 16; ++i) {
+      const int n = __popc(__ballot_sync(0xFFFFFFFFu, mine >= (v | i << shift)));
+      if (lane == static_cast<int>(i)) reach = n;
+    }
+    if (reach > 0) atomicAdd(&(*counts)[lane & 15], reach);
+    __syncwarp();
+    __syncthreads();
+    const int n = *const_cast<volatile int*>(&(*counts)[lane & 15]);  // (of step 0: none)
+    const uint32_t enough = __ballot_sync(0xFFFFFFFFu, n >= k && lane < 16);
+    if (enough != 0) {
+      const int step = 31 - __clz(enough);
+      v |= static_cast<uint32_t>(step) << shift;
+      count = __shfl_sync(0xFFFFFFFFu, n, step);
+    }
+    if (count == k) break;
+  }
+  return v;
+}
+
+// The k first elements of the CTA's run into sh.key / sh.index (fewer where the run is
+// shorter: key 0). `top` is the thread's largest; all threads take part.
+template <typename T>
+__device__ void select_top(const Run<T>& run, float top, int k, Shared& sh) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int V = Logit<T>::kVec;
+  const bool any = tid < run.chunks || tid < run.head + run.tail;
+  const uint32_t mine = any ? order_key(top) : 0u;
+  if (tid < k) sh.key[tid] = 0, sh.index[tid] = -1;
+  for (int i = tid; i < 2 * kRounds * 16; i += kThreads) sh.counts[i / 16][i % 16] = 0;
+  if (tid == 0) sh.count = sh.found = 0;
+  __syncwarp();
+  __syncthreads();
+  int reach;
+  uint32_t bound = kth_largest(mine, 32, k, sh.counts, reach);
+  if (bound == 0) bound = 1, reach = 0;  // fewer than k threads hold elements: all of theirs
+  bool holds = mine >= bound;
+  // Where too many threads tie at the bound: those whose first such element comes first.
+  int last = 0x7FFFFFFF;
+  if (reach > kColumns) {
+    int first = run.end;
+    if (mine == bound) {
+      if (tid < run.head + run.tail) {
+        const int i = run.loose(tid);
+        if (order_key(Logit<T>::get(run.row[i])) == bound) first = i;
+      }
+      for (int c = tid, at = run.begin + run.head + tid * V; c < run.chunks && at < first;
+           c += kThreads, at += kThreads * V) {
+        float x[V];
+        Logit<T>::unpack(__ldg(run.body + c), x);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (order_key(x[i]) == bound) first = min(first, at + i);
+      }
+    }
+    __syncwarp();
+    // (threads above the bound, fewer than k, count as if theirs were before all)
+    const uint32_t left = mine > bound ? run.end - run.begin + 1 : mine == bound ? run.end - first : 0;
+    const uint32_t least = max(
+        kth_largest(left, 32 - __clz(run.end - run.begin + 1), k, sh.counts + kRounds, reach), 1u);
+    holds = left >= least;
+    last = run.end - static_cast<int>(least);
+  }
+  if (holds) {
+    const int at = atomicAdd(&sh.count, 1);
+    if (at < kColumns) sh.columns[at] = tid;
+  }
+  __syncwarp();
+  __syncthreads();
+  // Their elements: an item is a 16-byte chunk of one, or its loose element.
+  const int columns = min(sh.count, kColumns);
+  const int per = (run.chunks + kThreads - 1) / kThreads + 1, items = columns * per;
+  auto for_items = [&](auto f) {
+#pragma unroll 2
+    for (int i = tid; i < items; i += kThreads) {
+      const int column = sh.columns[i / per], n = i % per - 1;
+      if (n < 0) {
+        if (column < run.head + run.tail) {
+          const int e = run.loose(column);
+          f(Logit<T>::get(run.row[e]), e);
+        }
+      } else if (column + n * kThreads < run.chunks) {
+        float x[V];
+        Logit<T>::unpack(__ldg(run.body + column + n * kThreads), x);
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          f(x[e], run.begin + run.head + (column + n * kThreads) * V + e);
+      }
+    }
+    __syncwarp();
+  };
+  for_items([&](float x, int index) {
+    const uint32_t key = order_key(x);
+    if (key > bound || (key == bound && index <= last)) {
+      const int at = atomicAdd(&sh.found, 1);
+      if (at < kCandidates) {
+        sh.cand_key[at] = key;
+        sh.cand_index[at] = index;
+      }
+    }
+  });
+  __syncthreads();
+  const int found = sh.found;
+  if (found <= kCandidates) {
+    for (int i = tid; i < found; i += kThreads) {
+      const uint32_t key = sh.cand_key[i];
+      const int index = sh.cand_index[i];
+      int rank = 0;
+      for (int j = 0; j < found; ++j) rank += before(sh.cand_key[j], sh.cand_index[j], key, index);
+      if (rank < k) {
+        sh.key[rank] = key;
+        sh.index[rank] = index;
+      }
+    }
+    __syncwarp();
+    __syncthreads();
+    return;
+  }
+  // (rare: a few threads hold very many of the largest) one after another
+  uint32_t last_key = 0xFFFFFFFFu;
+  int last_index = -1;
+  for (int n = 0; n < k; ++n) {
+    uint32_t key = 0;
+    int index = 0x7FFFFFFF;
+    for_items([&](float x, int at) {
+      const uint32_t q = order_key(x);
+      if (before(last_key, last_index, q, at) && before(q, at, key, index)) key = q, index = at;
+    });
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) {
+      const uint32_t q = __shfl_xor_sync(0xFFFFFFFFu, key, d);
+      const int at = __shfl_xor_sync(0xFFFFFFFFu, index, d);
+      if (before(q, at, key, index)) key = q, index = at;
+    }
+    if (lane == 0) sh.best_key[warp] = key, sh.best_index[warp] = index;
+    __syncthreads();
+    key = 0, index = 0x7FFFFFFF;
+    for (int w = 0; w < kWarps; ++w)
+      if (before(sh.best_key[w], sh.best_index[w], key, index))
+        key = sh.best_key[w], index = sh.best_index[w];
+    if (tid == 0) sh.key[n] = key, sh.index[n] = key == 0 ? -1 : index;
+    last_key = key;
+    last_index = index;
+    __syncthreads();
+  }
+}
+
+// kCluster: a row's CTAs are a cluster of a.cluster (else 1).
+template <typename T, bool kTop, bool kCluster>
+__global__ void __launch_bounds__(kThreads, kForwardPerSm)
+    logprobs_forward_sm103a_kernel(const ForwardArgs a) {
+  __shared__ Shared sh;
+  constexpr int V = Logit<T>::kVec;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cluster = kCluster ? a.cluster : 1;
+  const int rank = static_cast<int>(blockIdx.x) % cluster;
+  const float c = a.scale * kLog2e;
+  // This CTA's part of every row: 16-byte multiples but for the last one's end.
+  const int each = ((a.vocab + cluster - 1) / cluster + 15) / 16 * 16;
+  const int from = min(rank * each, a.vocab), to = min(from + each, a.vocab);
+  grid_dependency_wait();
+  if constexpr (kCluster) cluster_sync();  // (all have begun before one writes to another)
+  for (long long r = blockIdx.x / cluster; r < a.rows; r += gridDim.x / cluster) {
+    const int token = a.tokens[r];
+    if (token < 0 || token >= a.vocab) {  // left out
+      if (rank == 0) {
+        if (tid == 0) {
+          if (token >= 0) report_index(a.status, kIndexToken);
+          a.logprob[r] = 0.0f;
+          a.entropy[r] = 0.0f;
+          a.stats[r] = make_float2(0.0f, 0.0f);
+        }
+        if (kTop && tid < a.top) {
+          a.top_logprob[r * a.top + tid] = 0.0f;
+          a.top_token[r * a.top + tid] = -1;
+        }
+      }
+      __syncwarp();
+      continue;
+    }
+    const T* row = static_cast<const T*>(a.logits) + r * a.stride;
+    const Run<T> run(row, from, to);
+    const float given = Logit<T>::get(row[token]);  // (asked for before it is needed)
+    Partial p;
+    for (int i = tid; i < run.chunks; i += kLoads * kThreads) {
+      uint4 w[kLoads];
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k)
+        if (k == 0 || i + k * kThreads < run.chunks) w[k] = __ldg(run.body + i + k * kThreads);
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k) {
+        if (k > 0 && i + k * kThreads >= run.chunks) break;
+        float x[V];
+        Logit<T>::unpack(w[k], x);
+        p.add(x, c);
+      }
+    }
+    if (tid < run.head + run.tail) p.add_one(Logit<T>::get(row[run.loose(tid)]), c);
+    __syncwarp();
+
+    // The CTA's maximum, then S and T relative to it.
+    float m = p.m;
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+    if (lane == 0) sh.m[warp] = m;
+    __syncthreads();
+    m = sh.m[lane % kWarps];
+#pragma unroll
+    for (int d = kWarps / 2; d > 0; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+    if (m > p.m) p.raise(m, c);
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) {
+      p.s += __shfl_xor_sync(0xFFFFFFFFu, p.s, d);
+      p.t += __shfl_xor_sync(0xFFFFFFFFu, p.t, d);
+    }
+    if (lane == 0) sh.s[warp] = p.s, sh.t[warp] = p.t;
+    __syncthreads();
+    if (warp == 0) {
+      float s = sh.s[lane % kWarps], t = sh.t[lane % kWarps];
+#pragma unroll
+      for (int d = kWarps / 2; d > 0; d /= 2) {
+        s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+        t += __shfl_xor_sync(0xFFFFFFFFu, t, d);
+      }
+      if (lane == 0) sh.row_m = m, sh.row_s = s, sh.row_t = t;
+    }
+    __syncwarp();
+    if constexpr (kTop) select_top(run, p.top, a.top, sh);
+    else __syncthreads();
+    if constexpr (kCluster) {  // to the first CTA of the row
+      Shared* first = reinterpret_cast<Shared*>(__cluster_map_shared_rank(&sh, 0));
+      if (tid == 0) first->all[rank] = {sh.row_m, sh.row_s, sh.row_t};
+      if (kTop && tid < a.top) {
+        first->all_key[rank][tid] = sh.key[tid];
+        first->all_index[rank][tid] = sh.index[tid];
+      }
+      __syncwarp();
+      cluster_sync();
+    }
+    if (rank == 0 && warp < (kTop ? cluster : 1)) {
+      // The row's S and T, from its CTAs' (each of these warps for itself).
+      Partial all;
+      if (lane < cluster) {
+        const float3 part = kCluster ? sh.all[lane] : make_float3(sh.row_m, sh.row_s, sh.row_t);
+        all.m = part.x, all.s = part.y, all.t = part.z;
+      }
+      __syncwarp();
+      float most = all.m;
+#pragma unroll
+      for (int d = kMaxCluster / 2; d > 0; d /= 2) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
+      if (most > all.m) all.raise(most, c);
+#pragma unroll
+      for (int d = kMaxCluster / 2; d > 0; d /= 2) {
+        all.s += __shfl_xor_sync(0xFFFFFFFFu, all.s, d);
+        all.t += __shfl_xor_sync(0xFFFFFFFFu, all.t, d);
+      }
+      const float s = __shfl_sync(0xFFFFFFFFu, all.s, 0), t = __shfl_sync(0xFFFFFFFFu, all.t, 0);
+      most = __shfl_sync(0xFFFFFFFFu, most, 0);
+      const bool none = s == 0.0f;  // every logit is -inf
+      const float log_s = none ? 0.0f : logf(s);
+      if (warp == 0 && lane == 0) {
+        a.stats[r] = make_float2(none ? -INFINITY : most, log_s);
+        a.logprob[r] = none ? -INFINITY : fmaf(given - most, a.scale, -log_s);
+        a.entropy[r] = none ? 0.0f : log_s - kLn2 * (t / s);
+      }
+      if constexpr (kTop) {
+        // Warp o places list o's elements among all of them: as far behind the first as there
+        // are elements before it.
+        const int k = a.top, my = min(lane, k - 1);
+        const uint32_t key = kCluster ? sh.all_key[warp][my] : sh.key[my];
+        const int index = kCluster ? sh.all_index[warp][my] : sh.index[my];
+        int place = my;
+        if constexpr (kCluster) {
+          for (int q = 0; q < cluster; ++q) {
+            int n = 0;
+#pragma unroll 8
+            for (int i = 0; i < k; ++i)
+              n += before(sh.all_key[q][i], sh.all_index[q][i], key, index);
+            if (q != warp) place += n;
+          }
+        }
+        if (lane < k && key != 0 && place < k) {
+          const float x = key_value(key);
+          a.top_logprob[r * k + place] = none ? -INFINITY : fmaf(x - most, a.scale, -log_s);
+          a.top_token[r * k + place] = index;
+        }
+      }
+    }
+    __syncwarp();
+    if constexpr (kCluster) cluster_sync();  // the next row's part overwrites what was read
+    else __syncthreads();
+  }
+}
+
+struct BackwardArgs {
+  const void* logits;
+  void* dlogits;
+  long long stride, d_stride;
+  long long rows;
+  int vocab, top;
+  const int* tokens;
+  float scale;
+  const float2* stats;
+  const float* entropy;
+  const float* d_logprob;  // or nullptr, as the next two
+  const float* d_entropy;
+  const float* d_top;
+  const int* top_token;
+  int* status;
+  int parts;  // CTAs of a row
+};
+
+// -s p (g + h (log p + H)) of a logit, with z = log2 p: p (A + B z).
+struct Slope {
+  float m, c, log2_s, A, B;
+  __device__ __forceinline__ float operator()(float x) const {
+    const float z = (x - m) * c - log2_s;
+    return ex2_approx(z) * fmaf(B, fmaxf(z, kLeast), A);
+  }
+};
+
+// kVector: rows of logits and gradient begin at the same place of a 16-byte chunk.
+template <typename T, bool kVector>
+__global__ void __launch_bounds__(kThreads, kBackwardPerSm)
+    logprobs_backward_sm103a_kernel(const BackwardArgs a) {
+  __shared__ int s_at[kMaxTop + 1];    // the token and the alternatives
+  __shared__ float s_g[kMaxTop + 1];
+  constexpr int V = Logit<T>::kVec;
+  const int tid = threadIdx.x;
+  const int each = ((a.vocab + a.parts - 1) / a.parts + 15) / 16 * 16;
+  grid_dependency_wait();
+  for (long long job = blockIdx.x; job < a.rows * a.parts; job += gridDim.x) {
+    const long long r = job / a.parts;
+    const int from = min(static_cast<int>(job - r * a.parts) * each, a.vocab);
+    const int to = min(from + each, a.vocab);
+    const T* row = static_cast<const T*>(a.logits) + r * a.stride;
+    T* drow = static_cast<T*>(a.dlogits) + r * a.d_stride;
+    const Run<T> run(row, from, to);
+    const int token = a.tokens[r];
+    const float2 st = a.stats[r];
+    const int k = a.d_top ? a.top : 0;
+    const bool out = token < 0 || token >= a.vocab;
+    if (out && token >= 0 && tid == 0 && from == 0) report_index(a.status, kIndexToken);
+    const bool zero = out || st.x == -INFINITY;  // left out, or no logit above -inf
+    __syncwarp();
+    if (tid == 0) {
+      s_at[0] = token;
+      s_g[0] = a.d_logprob ? a.d_logprob[r] : 0.0f;
+    } else if (tid <= k) {
+      const int t = a.top_token[r * a.top + tid - 1];
+      s_at[tid] = t;
+      s_g[tid] = a.d_top[r * a.top + tid - 1];
+      if (!out && (t < 0 || t >= a.vocab)) {
+        report_index(a.status, kIndexToken);
+        s_g[tid] = 0.0f;
+      }
+    }
+    __syncwarp();
+    __syncthreads();
+    float g = 0.0f;
+    for (int i = 0; i <= k; ++i) g += s_g[i];
+    const float h = a.d_entropy ? a.d_entropy[r] : 0.0f;
+    Slope f;
+    f.m = st.x;
+    f.c = a.scale * kLog2e;
+    f.log2_s = st.y * kLog2e;
+    f.A = -a.scale * fmaf(h, h != 0.0f ? a.entropy[r] : 0.0f, g);
+    f.B = -a.scale * h * kLn2;
+    // The elements with a weight of their own: thread i the i-th, unless an earlier one is the same.
+    bool special = false;
+    float d_special = 0.0f;
+    int at = -1;
+    if (tid <= k && !zero) {
+      at = s_at[tid];
+      special = at >= from && at < to;
+      float own = 0.0f;
+      for (int i = 0; i <= k; ++i)
+        if (s_at[i] == at) {
+          if (i < tid) special = false;
+          own += s_g[i];
+        }
+      if (special) d_special = fmaf(a.scale, own, f(Logit<T>::get(row[at])));
+    }
+    __syncwarp();
+    __syncthreads();  // (before the gradient takes the logits' place)
+    if constexpr (kVector) {
+      uint4* to_body = reinterpret_cast<uint4*>(drow + (reinterpret_cast<const T*>(run.body) - row));
+      int i = tid;
+      for (; i < run.chunks; i += kLoads * kThreads) {
+        uint4 w[kLoads];
+#pragma unroll
+        for (int n = 0; n < kLoads; ++n)
+          if (!zero && i + n * kThreads < run.chunks) w[n] = run.body[i + n * kThreads];
+#pragma unroll
+        for (int n = 0; n < kLoads; ++n) {
+          if (i + n * kThreads >= run.chunks) break;
+          float x[V];
+          if (zero) {
+            to_body[i + n * kThreads] = make_uint4(0, 0, 0, 0);
+          } else {
+            Logit<T>::unpack(w[n], x);
+#pragma unroll
+            for (int e = 0; e < V; ++e) x[e] = f(x[e]);
+            to_body[i + n * kThreads] = Logit<T>::pack(x);
+          }
+        }
+      }
+      if (tid < run.head + run.tail) {
+        const int e = run.loose(tid);
+        drow[e] = Logit<T>::put(zero ? 0.0f : f(Logit<T>::get(row[e])));
+      }
+    } else {
+      for (int e = from + tid; e < to; e += kThreads)
+        drow[e] = Logit<T>::put(zero ? 0.0f : f(Logit<T>::get(row[e])));
+    }
+    __syncwarp();
+    __syncthreads();
+    if (special) drow[at] = Logit<T>::put(d_special);
+  }
+}
+
+template <typename T>
+cudaError_t launch_forward(ForwardArgs a, const DeviceInfo& dev, cudaStream_t stream) {
+  // CTAs of a row: as many as leave each 16 KB of it, while there are SMs without work.
+  const long long bytes = static_cast<long long>(a.vocab) * static_cast<long long>(sizeof(T));
+  a.cluster = 1;
+  while (a.cluster < kMaxCluster && a.rows * a.cluster < dev.sm_count &&
+         bytes / (2 * a.cluster) >= 8192)
+    a.cluster *= 2;
+  const long long most = std::max(kForwardPerSm * dev.sm_count / a.cluster, 1);
+  const unsigned grid = static_cast<unsigned>(std::min(a.rows, most) * a.cluster);
+  if (a.cluster > 1)
+    return launch_programmatic_cluster(a.top > 0 ? logprobs_forward_sm103a_kernel<T, true, true>
+                                                 : logprobs_forward_sm103a_kernel<T, false, true>,
+                                       grid, kThreads, 0, stream,
+                                       static_cast<unsigned>(a.cluster), a);
+  return launch_programmatic(a.top > 0 ? logprobs_forward_sm103a_kernel<T, true, false>
+                                       : logprobs_forward_sm103a_kernel<T, false, false>,
+                             dim3(grid), kThreads, 0, stream, a);
+}
+
+template <typename T>
+cudaError_t launch_backward(BackwardArgs a, const DeviceInfo& dev, cudaStream_t stream) {
+  const long long bytes = static_cast<long long>(a.vocab) * static_cast<long long>(sizeof(T));
+  a.parts = 1;
+  const long long most = static_cast<long long>(kBackwardPerSm) * dev.sm_count;
+  while (a.rows * a.parts < most && bytes / (2 * a.parts) >= 8192) a.parts *= 2;
+  const unsigned grid = static_cast<unsigned>(std::min(a.rows * a.parts, most));
+  const bool vector =
+      reinterpret_cast<uintptr_t>(a.logits) % 16 == reinterpret_cast<uintptr_t>(a.dlogits) % 16 &&
+      (a.rows == 1 || (a.stride - a.d_stride) * static_cast<long long>(sizeof(T)) % 16 == 0);
+  const auto kernel = vector ? logprobs_backward_sm103a_kernel<T, true>
+                             : logprobs_backward_sm103a_kernel<T, false>;
+  return launch_programmatic(kernel, dim3(grid), kThreads, 0, stream, a);
+}
+
+int launched(const char* who, cudaError_t e, std::string& err) {
+  if (e == cudaSuccess) e = cudaGetLastError();
+  if (e == cudaSuccess) return CSA_OK;
+  err = std::string(who) + ": launch: " + cudaGetErrorString(e);
+  return CSA_ERR_LAUNCH;
+}
+
+}  // namespace
+
+int logprobs_forward_launch(const LogprobsCall& c, cudaStream_t stream, const DeviceInfo& dev,
+                            std::string& err) {
+  ForwardArgs a;
+  a.logits = c.logits;
+  a.stride = c.stride;
+  a.rows = c.rows;
+  a.vocab = c.vocab;
+  a.top = c.top;
+  a.tokens = c.tokens;
+  a.scale = c.scale;
+  a.logprob = c.logprob;
+  a.entropy = c.entropy;
+  a.stats = reinterpret_cast<float2*>(c.stats);
+  a.top_logprob = c.top_logprob;
+  a.top_token = c.top_token;
+  a.status = dev.status_word;
+  const cudaError_t e = c.dtype == CSA_F32   ? launch_forward<float>(a, dev, stream)
+                        : c.dtype == CSA_F16 ? launch_forward<__half>(a, dev, stream)
+                                             : launch_forward<__nv_bfloat16>(a, dev, stream);
+  return launched("token_logprobs_forward", e, err);
+}
+
+int logprobs_backward_launch(const LogprobsGrad& c, cudaStream_t stream, const DeviceInfo& dev,
+                             std::string& err) {
+  BackwardArgs a;
+  a.logits = c.logits;
+  a.dlogits = c.dlogits;
+  a.stride = c.stride;
+  a.d_stride = c.d_stride;
+  a.rows = c.rows;
+  a.vocab = c.vocab;
+  a.top = c.top;
+  a.tokens = c.tokens;
+  a.scale = c.scale;
+  a.stats = reinterpret_cast<const float2*>(c.stats);
+  a.entropy = c.entropy;
+  a.d_logprob = c.d_logprob;
+  a.d_entropy = c.d_entropy;
+  a.d_top = c.d_top;
+  a.top_token = c.top_token;
+  a.status = dev.status_word;
+  const cudaError_t e = c.dtype == CSA_F32   ? launch_backward<float>(a, dev, stream)
+                        : c.dtype == CSA_F16 ? launch_backward<__half>(a, dev, stream)
+                                             : launch_backward<__nv_bfloat16>(a, dev, stream);
+  return launched("token_logprobs_backward", e, err);
+}
+
+}  // namespace csa

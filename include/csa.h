@@ -551,6 +551,54 @@ csa_status cache_attention_forward(void* out, const void* q, int dtype, int q_he
 csa_status cache_attention_workspace_size(const csa_kv_cache* cache, int q_heads, size_t* bytes);
 
 /*
+ * token_logprobs_forward -- for each row x of logits (a dense layer's outputs) and its token,
+ * with p = softmax(scale x):
+ *   logprob[r]    log p[tokens[r]];
+ *   entropy[r]    -sum_j p_j log p_j;
+ *   stats[r]      (m, log sum_j exp(scale (x_j - m))), m the largest x: what the backward call
+ *                 needs; their log-sum-exp is scale m + stats[r][1];
+ *   top_token[r][0 .. top - 1], top_logprob[r][...]   the tokens of the largest x in falling
+ *                 order, of equal ones the lowest number first (-0 equals 0), and their log p.
+ *   logits       device, CSA_BF16, CSA_F16 or CSA_F32, [rows][vocab], rows `stride` elements
+ *                apart (>= vocab; any alignment of the type);
+ *   tokens       device, int32 [rows]; a negative one leaves its row out: its logits are not
+ *                read, its results are 0 and its top tokens -1. So does one from vocab on, which
+ *                csa_get_status reports as CSA_ERR_INDEX;
+ *   scale        1 / temperature: > 0, at most 2^64;
+ *   logprob, entropy   device, fp32 [rows]; stats device, fp32 [rows][2], 8-byte aligned;
+ *   top          0 .. min(32, vocab); top_logprob fp32 and top_token int32, [rows][top] (unused
+ *                and may be NULL with top = 0).
+ * Computed in fp32 (the difference to m first, so that log p near 0 is exact to fp32's
+ * 2^-24 of the sum, not of m). A logit of -inf is a forbidden token: p = 0, nothing added to the
+ * entropy. Where every logit of a row is -inf, log p is -inf, the entropy 0 and stats (-inf, 0).
+ * A NaN or +inf makes its row's logprob, entropy and top_logprob NaN; among the top tokens a NaN
+ * counts as -inf. Outputs must not overlap the inputs or each other. Asynchronous on `stream`;
+ * results do not depend on an SM limit beyond the order in which fp32 sums are taken.
+ *
+ * token_logprobs_backward -- the gradient of sum_r d_logprob[r] logprob[r] + d_entropy[r]
+ * entropy[r] + sum_i d_top[r][i] top_logprob[r][i] by the logits, rounded once to their type:
+ *   dlogits[r][j] = scale (g 1{j = token} - d_entropy p_j (log p_j + entropy)
+ *                          + sum_i d_top[i] 1{j = top_token[i]} - (d_logprob + sum_i d_top[i]) p_j).
+ *   stats, entropy     as the forward call left them (same logits, tokens and scale);
+ *   d_logprob, d_entropy [rows], d_top [rows][top]   device, fp32; any may be NULL (no such
+ *                term; top_token is read with d_top only);
+ *   dlogits      device, of the logits' type, rows d_stride apart; the logits themselves with
+ *                equal strides (in place), or apart from them (CSA_ERR_UNSUPPORTED otherwise).
+ * Every element of dlogits is written: 0 in rows left out and in rows with every logit -inf.
+ * The choice of the alternatives has no gradient. Asynchronous on `stream`.
+ */
+csa_status token_logprobs_forward(float* logprob, float* entropy, float* stats, const void* logits,
+                                  int dtype, int64_t rows, int vocab, int64_t stride,
+                                  const int32_t* tokens, float scale, int top, float* top_logprob,
+                                  int32_t* top_token, void* stream);
+csa_status token_logprobs_backward(void* dlogits, const void* logits, int dtype, int64_t rows,
+                                   int vocab, int64_t d_stride, int64_t stride,
+                                   const int32_t* tokens, float scale, const float* stats,
+                                   const float* entropy, const float* d_logprob,
+                                   const float* d_entropy, int top, const float* d_top,
+                                   const int32_t* top_token, void* stream);
+
+/*
  * csa_get_status -- synchronises `stream`, then returns and clears the current
  * device's status word: CSA_OK, or CSA_ERR_TIMEOUT if a kernel's bounded wait
  * ran out since the last call, or CSA_ERR_INDEX if a kernel met an index out of range
