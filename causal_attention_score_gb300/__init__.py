@@ -15,6 +15,10 @@ Public API (all compute runs in libcsa_gb300.so; see include/csa.h):
 * ``kv_cache_write`` / ``kv_cache_read`` on a ``KvCache`` (paged keys and values in 8 bits)
   for the rows a ``KvBatch`` names, and ``cache_attention_forward`` over it
   (``cache_attention`` allocates; ``cache_attention_workspace_size`` for its scratch)
+* ``KvPages``, the books of a cache: ``kv_pages_extend`` (room for more tokens),
+  ``kv_cache_fork`` (a sequence that shares another's tokens), ``kv_pages_free``,
+  ``kv_cache_copy`` (pages of one cache into another), ``kv_cache_compact``;
+  ``kv_pages_workspace_size`` for their scratch
 * ``token_logprobs_forward`` / ``token_logprobs_backward`` (``token_logprobs`` allocates): log
   probabilities of given tokens from rows of logits, entropy, top alternatives, the gradient
 * allocating helpers ``trimul(qkv)``, ``causal_softmax(qkv)`` and ``dense(X, W)``
@@ -25,7 +29,8 @@ Public API (all compute runs in libcsa_gb300.so; see include/csa.h):
 The library is loaded on first use; importing this package needs no GPU.
 """
 from ._lib import (CSA_ERR_ALIGN, CSA_ERR_ARCH, CSA_ERR_CHECK, CSA_ERR_CUDA, CSA_ERR_LAUNCH,
-                   CSA_ERR_INDEX, CSA_ERR_NULL, CSA_ERR_SHAPE, CSA_ERR_TIMEOUT, CSA_ERR_UNSUPPORTED,
+                   CSA_ERR_INDEX, CSA_ERR_NULL, CSA_ERR_PAGES, CSA_ERR_SHAPE, CSA_ERR_TIMEOUT,
+                   CSA_ERR_UNSUPPORTED,
                    CSA_ERR_WORKSPACE,
                    CSA_MASK_NAN, CSA_MASK_NEG_INF, CSA_OK, CsaError)
 from .ops import (DENSE_FETCH_AUTO, DENSE_FETCH_LOADERS, DenseGroupedPlan, batch_matmul_nt,
@@ -35,6 +40,8 @@ from .ops import (DENSE_FETCH_AUTO, DENSE_FETCH_LOADERS, DenseGroupedPlan, batch
                   set_dense_fetch, set_stream_sm_limit, set_wait_limit_ns, trimul, trimul_forward,
                   trimul_forward_f32, version)
 from .logprobs import token_logprobs, token_logprobs_backward, token_logprobs_forward
+from .pages import (KvPages, kv_cache_compact, kv_cache_copy, kv_cache_fork, kv_pages_extend,
+                    kv_pages_free, kv_pages_workspace_size)
 from .serving import (KvBatch, KvCache, RotaryTable, cache_attention, cache_attention_forward,
                       cache_attention_workspace_size, kv_cache_read, kv_cache_write,
                       rotary_backward, rotary_forward, rotary_qkv)
@@ -48,6 +55,8 @@ __all__ = [
     "RotaryTable", "rotary_forward", "rotary_backward", "rotary_qkv",
     "KvCache", "KvBatch", "kv_cache_write", "kv_cache_read",
     "cache_attention_forward", "cache_attention", "cache_attention_workspace_size",
+    "KvPages", "kv_pages_extend", "kv_cache_fork", "kv_pages_free", "kv_cache_copy",
+    "kv_cache_compact", "kv_pages_workspace_size", "CSA_ERR_PAGES",
     "token_logprobs_forward", "token_logprobs_backward", "token_logprobs",
     "CSA_ERR_INDEX",
     "DENSE_FETCH_AUTO", "DENSE_FETCH_LOADERS", "version", "CsaError", "CSA_OK", "CSA_ERR_NULL",

@@ -24,6 +24,7 @@ CSA_ERR_CHECK = -9
 CSA_ERR_WORKSPACE = -10
 CSA_ERR_BUSY = -11
 CSA_ERR_INDEX = -12
+CSA_ERR_PAGES = -13
 
 CSA_MASK_NAN = 0x7FC00000
 CSA_MASK_NEG_INF = 0xFF800000
@@ -61,6 +62,12 @@ SIGNATURES = {
     "cache_attention_forward": (_i, [_vp, _vp, _i, _i, _i64, _i64, _i64, _i64, _vp, _vp, _f, _i,
                                      _i, _vp, ctypes.c_size_t, _vp]),
     "cache_attention_workspace_size": (_i, [_vp, _i, ctypes.POINTER(ctypes.c_size_t)]),
+    "kv_pages_workspace_size": (_i, [_vp, _i, ctypes.POINTER(ctypes.c_size_t)]),
+    "kv_pages_extend": (_i, [_vp, _vp, _vp, _i, _vp, ctypes.c_size_t, _vp]),
+    "kv_cache_fork": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _vp, ctypes.c_size_t, _vp]),
+    "kv_pages_free": (_i, [_vp, _vp, _i, _vp]),
+    "kv_cache_copy": (_i, [_vp, _vp, _vp, _vp, _i, _vp]),
+    "kv_cache_compact": (_i, [_vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
     "token_logprobs_forward": (_i, [_vp, _vp, _vp, _vp, _i, _i64, _i, _i64, _vp, _f, _i, _vp, _vp,
                                     _vp]),
     "token_logprobs_backward": (_i, [_vp, _vp, _i, _i64, _i, _i64, _i64, _vp, _f, _vp, _vp, _vp,

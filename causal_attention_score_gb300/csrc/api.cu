@@ -675,8 +675,9 @@ csa_status csa_get_status(void* stream) {
     const int zero[2] = {0, 0};
     e = cudaMemcpy(dev.status_word, zero, sizeof zero, cudaMemcpyHostToDevice);
     if (e != cudaSuccess) return cuda_error("csa_get_status: clear status", e);
-    t_last_error = (host[0] == CSA_ERR_INDEX ? "index out of range on the device, site "
-                                             : "device wait ran out at site ") +
+    t_last_error = (host[0] == CSA_ERR_INDEX   ? "index out of range on the device, site "
+                    : host[0] == CSA_ERR_PAGES ? "too few free pages, site "
+                                               : "device wait ran out at site ") +
                    std::to_string(host[1]);
     return host[0];
   }
@@ -698,6 +699,7 @@ const char* csa_status_string(csa_status s) {
     case CSA_ERR_WORKSPACE: return "workspace missing or too small";
     case CSA_ERR_BUSY: return "work-list counter sets exhausted";
     case CSA_ERR_INDEX: return "index in device memory out of range";
+    case CSA_ERR_PAGES: return "too few free pages in a cache";
     default: return "unknown status";
   }
 }
@@ -995,6 +997,67 @@ int kv_rows(const char* who, const csa_kv_cache* cache, const csa_kv_batch* batc
   return rc == CSA_OK ? CSA_OK : set_error(rc, err);
 }
 
+// Checks shared by the calls on a cache's books.
+int pages_args_ok(const std::string& w, const csa_kv_pages* p) {
+  if (!p) return set_error(CSA_ERR_NULL, w + ": null pages");
+  if (!p->refs || !p->lengths || !p->table)
+    return set_error(CSA_ERR_NULL, w + ": null pointer in the pages");
+  if (p->pages <= 0 || p->sequences <= 0 || p->table_width <= 0)
+    return set_error(CSA_ERR_SHAPE, w + ": pages, sequences, table_width must be >= 1");
+  if (p->pages > 1 << 30) return set_error(CSA_ERR_UNSUPPORTED, w + ": more than 2^30 pages");
+  if (p->page_tokens != 16 && p->page_tokens != 32 && p->page_tokens != 64 &&
+      p->page_tokens != 128)
+    return set_error(CSA_ERR_UNSUPPORTED, w + ": page_tokens must be 16, 32, 64 or 128");
+  if (!aligned(p->refs, 4) || !aligned(p->lengths, 4) || !aligned(p->table, 4))
+    return set_error(CSA_ERR_ALIGN, w + ": the pages' arrays must be 4-byte aligned");
+  return CSA_OK;
+}
+
+int pages_of_cache_ok(const std::string& w, const csa_kv_cache* c, const csa_kv_pages* p) {
+  int rc = cache_args_ok(w, c);
+  if (rc == CSA_OK) rc = pages_args_ok(w, p);
+  if (rc != CSA_OK) return rc;
+  if (c->pages != p->pages || c->page_tokens != p->page_tokens)
+    return set_error(CSA_ERR_SHAPE, w + ": the pages are not those of this cache");
+  return CSA_OK;
+}
+
+// Bytes of a page's K, as the copies count them.
+int page_bytes_ok(const std::string& w, const csa_kv_cache* c) {
+  return static_cast<long long>(c->heads) * c->page_tokens * c->head_size > 1 << 30
+             ? set_error(CSA_ERR_UNSUPPORTED, w + ": a page of more than 2^30 bytes")
+             : CSA_OK;
+}
+
+int list_ok(const std::string& w, const void* list, int n) {
+  if (!list) return set_error(CSA_ERR_NULL, w + ": null pointer");
+  if (n <= 0) return set_error(CSA_ERR_SHAPE, w + ": n must be >= 1");
+  if (!aligned(list, 4)) return set_error(CSA_ERR_ALIGN, w + ": a list must be 4-byte aligned");
+  return CSA_OK;
+}
+
+int workspace_ok(const std::string& w, const void* workspace, size_t have, size_t need) {
+  if (!workspace || have < need)
+    return set_error(CSA_ERR_WORKSPACE, w + ": " + std::to_string(need) +
+                                            " bytes of workspace needed, " +
+                                            std::to_string(workspace ? have : 0) + " given");
+  if (!aligned(workspace, 16))
+    return set_error(CSA_ERR_ALIGN, w + ": workspace must be 16-byte aligned");
+  return CSA_OK;
+}
+
+// The device, and what the launch returns.
+template <typename Launch>
+int on_device(void* stream, Launch launch) {
+  DeviceInfo dev;
+  std::string err;
+  int rc = current_device(dev, err);
+  if (rc != CSA_OK) return set_error(rc, err);
+  apply_stream_sm_limit(dev, static_cast<cudaStream_t>(stream));
+  rc = launch(dev, static_cast<cudaStream_t>(stream), err);
+  return rc == CSA_OK ? CSA_OK : set_error(rc, err);
+}
+
 // Checks shared by the two calls on logits.
 int logits_ok(const std::string& w, const void* logits, int dtype, long long rows, int vocab,
               long long stride, const int32_t* tokens, float scale, int top) {
@@ -1192,15 +1255,11 @@ csa_status token_logprobs_forward(float* logprob, float* entropy, float* stats, 
     if (!aligned(logprob, 4) || !aligned(entropy, 4) || !aligned(stats, 8) ||
         (top > 0 && (!aligned(top_logprob, 4) || !aligned(top_token, 4))))
       return set_error(CSA_ERR_ALIGN, w + ": a pointer breaks its type's alignment");
-    DeviceInfo dev;
-    std::string err;
-    rc = current_device(dev, err);
-    if (rc != CSA_OK) return set_error(rc, err);
-    apply_stream_sm_limit(dev, static_cast<cudaStream_t>(stream));
-    rc = logprobs_forward_launch({logits, dtype, stride, rows, vocab, top, tokens, scale, logprob,
-                                  entropy, stats, top_logprob, top_token},
-                                 static_cast<cudaStream_t>(stream), dev, err);
-    return rc == CSA_OK ? CSA_OK : set_error(rc, err);
+    return on_device(stream, [&](const DeviceInfo& dev, cudaStream_t st, std::string& err) {
+      return logprobs_forward_launch({logits, dtype, stride, rows, vocab, top, tokens, scale,
+                                      logprob, entropy, stats, top_logprob, top_token},
+                                     st, dev, err);
+    });
   });
 }
 
@@ -1232,16 +1291,117 @@ csa_status token_logprobs_backward(void* dlogits, const void* logits, int dtype,
     } else if (rows_meet({logits, stride, 0}, {dlogits, d_stride, 0}, rows, 1, vocab, esize)) {
       return set_error(CSA_ERR_UNSUPPORTED, w + ": logits and gradient overlap in part");
     }
-    DeviceInfo dev;
-    std::string err;
-    rc = current_device(dev, err);
-    if (rc != CSA_OK) return set_error(rc, err);
-    apply_stream_sm_limit(dev, static_cast<cudaStream_t>(stream));
-    rc = logprobs_backward_launch(
-        {logits, dlogits, dtype, stride, d_stride, rows, vocab, with_top ? top : 0, tokens, scale,
-         stats, entropy, d_logprob, d_entropy, with_top ? d_top : nullptr, top_token},
-        static_cast<cudaStream_t>(stream), dev, err);
-    return rc == CSA_OK ? CSA_OK : set_error(rc, err);
+    return on_device(stream, [&](const DeviceInfo& dev, cudaStream_t st, std::string& err) {
+      return logprobs_backward_launch(
+          {logits, dlogits, dtype, stride, d_stride, rows, vocab, with_top ? top : 0, tokens, scale,
+           stats, entropy, d_logprob, d_entropy, with_top ? d_top : nullptr, top_token},
+          st, dev, err);
+    });
+  });
+}
+
+csa_status kv_pages_workspace_size(const csa_kv_pages* pages, int n, size_t* bytes) {
+  return no_throw([&] {
+    t_last_error.clear();
+    const std::string w("kv_pages_workspace_size");
+    if (!bytes) return set_error(CSA_ERR_NULL, w + ": null pointer");
+    *bytes = 0;
+    const int rc = pages_args_ok(w, pages);
+    if (rc != CSA_OK) return rc;
+    if (n < 0) return set_error(CSA_ERR_SHAPE, w + ": n must be >= 0");
+    *bytes = kv_pages_workspace_bytes(*pages, n);
+    return static_cast<int>(CSA_OK);
+  });
+}
+
+csa_status kv_pages_extend(const csa_kv_pages* pages, const int32_t* sequences,
+                           const int32_t* more, int n, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  return no_throw([&] {
+    t_last_error.clear();
+    const std::string w("kv_pages_extend");
+    int rc = pages_args_ok(w, pages);
+    if (rc == CSA_OK) rc = list_ok(w, sequences, n);
+    if (rc == CSA_OK) rc = list_ok(w, more, n);
+    if (rc == CSA_OK)
+      rc = workspace_ok(w, workspace, workspace_bytes, kv_pages_workspace_bytes(*pages, n));
+    if (rc != CSA_OK) return rc;
+    return on_device(stream, [&](const DeviceInfo& dev, cudaStream_t st, std::string& err) {
+      return kv_pages_extend_launch(*pages, sequences, more, n, workspace, st, dev, err);
+    });
+  });
+}
+
+csa_status kv_cache_fork(const csa_kv_cache* cache, const csa_kv_pages* pages,
+                         const int32_t* parents, const int32_t* children, const int32_t* tokens,
+                         int n, void* workspace, size_t workspace_bytes, void* stream) {
+  return no_throw([&] {
+    t_last_error.clear();
+    const std::string w("kv_cache_fork");
+    int rc = pages_of_cache_ok(w, cache, pages);
+    if (rc == CSA_OK) rc = page_bytes_ok(w, cache);
+    if (rc == CSA_OK) rc = list_ok(w, parents, n);
+    if (rc == CSA_OK) rc = list_ok(w, children, n);
+    if (rc == CSA_OK && tokens) rc = list_ok(w, tokens, n);
+    if (rc == CSA_OK)
+      rc = workspace_ok(w, workspace, workspace_bytes, kv_pages_workspace_bytes(*pages, n));
+    if (rc != CSA_OK) return rc;
+    return on_device(stream, [&](const DeviceInfo& dev, cudaStream_t st, std::string& err) {
+      return kv_cache_fork_launch(*cache, *pages, parents, children, tokens, n, workspace, st, dev,
+                                  err);
+    });
+  });
+}
+
+csa_status kv_pages_free(const csa_kv_pages* pages, const int32_t* sequences, int n, void* stream) {
+  return no_throw([&] {
+    t_last_error.clear();
+    const std::string w("kv_pages_free");
+    int rc = pages_args_ok(w, pages);
+    if (rc == CSA_OK) rc = list_ok(w, sequences, n);
+    if (rc != CSA_OK) return rc;
+    return on_device(stream, [&](const DeviceInfo& dev, cudaStream_t st, std::string& err) {
+      return kv_pages_free_launch(*pages, sequences, n, st, dev, err);
+    });
+  });
+}
+
+csa_status kv_cache_copy(const csa_kv_cache* to, const csa_kv_cache* from,
+                         const int32_t* to_pages, const int32_t* from_pages, int n, void* stream) {
+  return no_throw([&] {
+    t_last_error.clear();
+    const std::string w("kv_cache_copy");
+    int rc = cache_args_ok(w, to);
+    if (rc == CSA_OK) rc = cache_args_ok(w, from);
+    if (rc == CSA_OK) rc = page_bytes_ok(w, from);
+    if (rc == CSA_OK) rc = list_ok(w, to_pages, n);
+    if (rc == CSA_OK) rc = list_ok(w, from_pages, n);
+    if (rc != CSA_OK) return rc;
+    if (to->heads != from->heads || to->page_tokens != from->page_tokens ||
+        to->head_size != from->head_size || to->format != from->format)
+      return set_error(CSA_ERR_SHAPE, w + ": the caches' pages differ");
+    return on_device(stream, [&](const DeviceInfo& dev, cudaStream_t st, std::string& err) {
+      return kv_cache_copy_launch(*to, *from, to_pages, from_pages, n, st, dev, err);
+    });
+  });
+}
+
+csa_status kv_cache_compact(const csa_kv_cache* cache, const csa_kv_pages* pages, int32_t* moves,
+                            int32_t* in_use, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+  return no_throw([&] {
+    t_last_error.clear();
+    const std::string w("kv_cache_compact");
+    int rc = pages_of_cache_ok(w, cache, pages);
+    if (rc == CSA_OK) rc = page_bytes_ok(w, cache);
+    if (rc == CSA_OK) rc = list_ok(w, moves, 1);
+    if (rc == CSA_OK) rc = list_ok(w, in_use, 1);
+    if (rc == CSA_OK)
+      rc = workspace_ok(w, workspace, workspace_bytes, kv_pages_workspace_bytes(*pages, 0));
+    if (rc != CSA_OK) return rc;
+    return on_device(stream, [&](const DeviceInfo& dev, cudaStream_t st, std::string& err) {
+      return kv_cache_compact_launch(*cache, *pages, moves, in_use, workspace, st, dev, err);
+    });
   });
 }
 

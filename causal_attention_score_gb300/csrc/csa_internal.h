@@ -209,6 +209,23 @@ int cache_prompt_launch(const csa_kv_cache& cache, const csa_kv_batch& batch,
                         const AttendCall& call, PromptList* list, cudaStream_t stream,
                         const DeviceInfo& dev, std::string& err);
 
+// The books of a paged cache (pages_sm103a.cu).
+size_t kv_pages_workspace_bytes(const csa_kv_pages& pages, int entries);
+int kv_pages_extend_launch(const csa_kv_pages& pages, const int* sequences, const int* tokens,
+                           int n, void* workspace, cudaStream_t stream, const DeviceInfo& dev,
+                           std::string& err);
+int kv_cache_fork_launch(const csa_kv_cache& cache, const csa_kv_pages& pages, const int* parents,
+                         const int* children, const int* tokens, int n, void* workspace,
+                         cudaStream_t stream, const DeviceInfo& dev, std::string& err);
+int kv_pages_free_launch(const csa_kv_pages& pages, const int* sequences, int n,
+                         cudaStream_t stream, const DeviceInfo& dev, std::string& err);
+int kv_cache_copy_launch(const csa_kv_cache& to, const csa_kv_cache& from, const int* to_pages,
+                         const int* from_pages, int n, cudaStream_t stream, const DeviceInfo& dev,
+                         std::string& err);
+int kv_cache_compact_launch(const csa_kv_cache& cache, const csa_kv_pages& pages, int* moves,
+                            int* in_use, void* workspace, cudaStream_t stream,
+                            const DeviceInfo& dev, std::string& err);
+
 // Log probabilities of tokens: logits [rows][vocab], strides in elements.
 struct LogprobsCall {
   const void* logits;

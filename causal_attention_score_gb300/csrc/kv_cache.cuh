@@ -51,10 +51,16 @@ enum IndexSite : int {
   kIndexRows = 202,     // offsets outside [0, rows], decreasing, or more than max_new apart
   kIndexLength = 203,   // a length outside [0, table_width * page_tokens]
   kIndexToken = 204,    // a token outside the vocabulary
+  kIndexSequence = 205,  // a sequence that is none, or named twice
+  kIndexNoPage = 206,    // (with CSA_ERR_PAGES) no page free
 };
 
 __device__ __forceinline__ void report_index(int* status, int site) {
   if (atomicCAS(status, 0, CSA_ERR_INDEX) == 0) atomicExch(status + 1, site);
+}
+
+__device__ __forceinline__ void report_pages(int* status) {
+  if (atomicCAS(status, 0, CSA_ERR_PAGES) == 0) atomicExch(status + 1, kIndexNoPage);
 }
 
 // One sequence of a batch: its rows [row0, row0 + n) are its last n tokens, at

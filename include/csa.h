@@ -98,6 +98,10 @@ typedef int csa_status;
                                      out of range; what it named was skipped (reported by
                                      csa_get_status) */
 
+#define CSA_ERR_PAGES        -13  /* kv_pages_extend or kv_cache_fork found too few free pages;
+                                     entries they were not enough for were left as they were
+                                     (reported by csa_get_status) */
+
 /* Causal mask bit patterns for the upper triangle (t2 > t). The page writes
  * NAN (the float quiet NaN, 0x7FC00000) and notes -inf would also do. */
 #define CSA_MASK_NAN          0x7FC00000u
@@ -551,6 +555,74 @@ csa_status cache_attention_forward(void* out, const void* q, int dtype, int q_he
 csa_status cache_attention_workspace_size(const csa_kv_cache* cache, int q_heads, size_t* bytes);
 
 /*
+ * csa_kv_pages -- the books of a cache: which pages each of `sequences` places has.
+ *   refs         device, int32 [pages]: how many table entries name each page, 0: free;
+ *   lengths      device, int32 [sequences]: tokens of each place's sequence, 0: none there;
+ *   table        device, int32 [sequences][table_width]: block b of a sequence (tokens
+ *                b * page_tokens on) is page table[s][b]; entries past a length mean nothing.
+ * New books are zeros in refs and lengths; the calls below keep them in step. A csa_kv_batch over
+ * all places uses the same lengths and table (places without rows in a call have equal offsets).
+ * Whole pages may be shared, a page that is written to never is. Who names pages beside the
+ * tables (a store of prompts) adds to their refs. refs, lengths and table do not overlap.
+ *
+ * All of these run on the device, asynchronous on `stream`, and may be captured; none allocates.
+ * Lists of entries are device int32 arrays of n >= 1. An entry that breaks a rule is left out and
+ * csa_get_status reports CSA_ERR_INDEX: a place outside [0, sequences), a length outside
+ * [0, table_width * page_tokens] before or after, a page outside [0, pages) (skipped), a place
+ * that an earlier entry of the call extends or forks into. Free pages are given out lowest number
+ * first, in the order of the entries; an entry whose pages are no longer there, all entries before
+ * it served, is left as it was, reported as CSA_ERR_PAGES.
+ *
+ * kv_pages_extend -- room for more[i] >= 0 more tokens of sequences[i]: its length grows by them
+ * and pages are given to the blocks that it had none for (a place of length 0 begins a sequence).
+ * What the pages hold is for kv_cache_write to write.
+ *
+ * kv_cache_fork -- children[i], a place of length 0, becomes a sequence of the first tokens[i]
+ * tokens of parents[i] (tokens NULL: of all of them). Whole pages are shared, their refs grow; where
+ * the last one is whole only in part, its written slots and its scales are copied to a page of the
+ * child's own. A parent may have any number of children; a place is not both in one call.
+ *
+ * kv_pages_free -- sequences[i] ends: its length becomes 0 and the refs of its pages go down by
+ * one each; those that reach 0 are free. A place named twice, or of length 0, has nothing to end.
+ *
+ * kv_cache_copy -- page to_pages[i] of `to` becomes a copy of page from_pages[i] of `from` (codes
+ * of all slots, scales). Caches of the same heads, page_tokens, head_size and format, or one
+ * cache; no page may be named twice in to_pages, nor in both lists of one cache (which of the
+ * contents it has then is not said).
+ *
+ * kv_cache_compact -- with n pages in use (refs above 0), those from n on move to the free ones
+ * below n, both in ascending order: codes, scales and refs, and every sequence's table entries.
+ * Afterwards pages 0 .. n - 1 are in use and the rest free.
+ *   moves    device, int32 [pages]: each page's new number, -1 for those that were free;
+ *   in_use   device, int32 [1]: n.
+ *
+ * kv_pages_workspace_size -- bytes of workspace that kv_pages_extend and kv_cache_fork with up to
+ * n entries and kv_cache_compact need, into *bytes (host only; n >= 0). The workspace: device,
+ * 16-byte aligned, needs no clearing, in use until the call's kernels complete: calls that may
+ * overlap on the GPU, replays of captured ones too, need separate ones.
+ */
+typedef struct csa_kv_pages {
+  int32_t* refs;
+  int32_t* lengths;
+  int32_t* table;
+  int pages, sequences, table_width, page_tokens;
+} csa_kv_pages;
+
+csa_status kv_pages_workspace_size(const csa_kv_pages* pages, int n, size_t* bytes);
+csa_status kv_pages_extend(const csa_kv_pages* pages, const int32_t* sequences,
+                           const int32_t* more, int n, void* workspace, size_t workspace_bytes,
+                           void* stream);
+csa_status kv_cache_fork(const csa_kv_cache* cache, const csa_kv_pages* pages,
+                         const int32_t* parents, const int32_t* children, const int32_t* tokens,
+                         int n, void* workspace, size_t workspace_bytes, void* stream);
+csa_status kv_pages_free(const csa_kv_pages* pages, const int32_t* sequences, int n, void* stream);
+csa_status kv_cache_copy(const csa_kv_cache* to, const csa_kv_cache* from,
+                         const int32_t* to_pages, const int32_t* from_pages, int n, void* stream);
+csa_status kv_cache_compact(const csa_kv_cache* cache, const csa_kv_pages* pages, int32_t* moves,
+                            int32_t* in_use, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
+/*
  * token_logprobs_forward -- for each row x of logits (a dense layer's outputs) and its token,
  * with p = softmax(scale x):
  *   logprob[r]    log p[tokens[r]];
@@ -602,7 +674,8 @@ csa_status token_logprobs_backward(void* dlogits, const void* logits, int dtype,
  * csa_get_status -- synchronises `stream`, then returns and clears the current
  * device's status word: CSA_OK, or CSA_ERR_TIMEOUT if a kernel's bounded wait
  * ran out since the last call, or CSA_ERR_INDEX if a kernel met an index out of range
- * (see csa_kv_batch). Returns CSA_ERR_CUDA if synchronisation fails.
+ * (see csa_kv_batch, csa_kv_pages), or CSA_ERR_PAGES if one found too few free pages: the first
+ * of them since. Returns CSA_ERR_CUDA if synchronisation fails.
  */
 csa_status csa_get_status(void* stream);
 
