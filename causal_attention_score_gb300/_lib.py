@@ -62,6 +62,10 @@ SIGNATURES = {
     "cache_attention_forward": (_i, [_vp, _vp, _i, _i, _i64, _i64, _i64, _i64, _vp, _vp, _f, _i,
                                      _i, _vp, ctypes.c_size_t, _vp]),
     "cache_attention_workspace_size": (_i, [_vp, _i, ctypes.POINTER(ctypes.c_size_t)]),
+    "cache_attention_shared_forward": (_i, [_vp, _vp, _i, _i, _i64, _i64, _i64, _i64, _vp, _vp, _vp,
+                                            _vp, _i, _f, _vp, ctypes.c_size_t, _vp]),
+    "cache_attention_shared_workspace_size": (_i, [_vp, _i, _i, _i, _i,
+                                                   ctypes.POINTER(ctypes.c_size_t)]),
     "kv_pages_workspace_size": (_i, [_vp, _i, ctypes.POINTER(ctypes.c_size_t)]),
     "kv_pages_extend": (_i, [_vp, _vp, _vp, _i, _vp, ctypes.c_size_t, _vp]),
     "kv_cache_fork": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _vp, ctypes.c_size_t, _vp]),

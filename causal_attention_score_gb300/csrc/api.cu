@@ -1085,6 +1085,42 @@ int attention_heads_ok(const std::string& w, const csa_kv_cache* cache, int q_he
   return CSA_OK;
 }
 
+int attention_args_ok(const std::string& w, const void* out, const void* q, int dtype, int q_heads,
+                      long long out_token, long long out_head, long long q_token, long long q_head,
+                      const csa_kv_cache* cache, const csa_kv_batch* batch, float scale, int window,
+                      int sinks) {
+  int rc = attention_heads_ok(w, cache, q_heads);
+  if (rc == CSA_OK) rc = batch_args_ok(w, batch);
+  if (rc != CSA_OK) return rc;
+  if (!out || !q) return set_error(CSA_ERR_NULL, w + ": null pointer");
+  if (dtype != CSA_BF16 && dtype != CSA_F16)
+    return set_error(CSA_ERR_UNSUPPORTED, w + ": unknown dtype");
+  if (!std::isfinite(scale)) return set_error(CSA_ERR_SHAPE, w + ": scale not finite");
+  if (window < 0 || sinks < 0)
+    return set_error(CSA_ERR_SHAPE, w + ": window and sinks must be >= 0");
+  rc = rows_ok(w, q, dtype, batch->rows, q_heads, cache->head_size, q_token, q_head, false);
+  if (rc == CSA_OK)
+    rc = rows_ok(w, out, dtype, batch->rows, q_heads, cache->head_size, out_token, out_head, true);
+  if (rc != CSA_OK) return rc;
+  // A unit reads its own rows of q before it writes them, so in place is fine.
+  const bool in_place = out == q && (batch->rows == 1 || q_token == out_token) &&
+                        (q_heads == 1 || q_head == out_head);
+  if (!in_place && rows_meet({q, q_token, q_head}, {out, out_token, out_head}, batch->rows, q_heads,
+                             cache->head_size, 2))
+    return set_error(CSA_ERR_UNSUPPORTED, w + ": q and out overlap in part");
+  return CSA_OK;
+}
+
+int shared_sizes_ok(const std::string& w, int q_heads, int rows, int sequences, int groups) {
+  if (rows <= 0 || sequences <= 0 || groups <= 0)
+    return set_error(CSA_ERR_SHAPE, w + ": rows, sequences, group_count must be >= 1");
+  if (groups == INT32_MAX)
+    return set_error(CSA_ERR_UNSUPPORTED, w + ": too many groups");
+  if (static_cast<long long>(rows) * q_heads > 1 << 30)
+    return set_error(CSA_ERR_UNSUPPORTED, w + ": rows * q_heads > 2^30");
+  return CSA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1198,46 +1234,66 @@ csa_status cache_attention_forward(void* out, const void* q, int dtype, int q_he
   return no_throw([&] {
     t_last_error.clear();
     const std::string w("cache_attention_forward");
+    int rc = attention_args_ok(w, out, q, dtype, q_heads, out_token_stride, out_head_stride,
+                               q_token_stride, q_head_stride, cache, batch, scale, window, sinks);
+    if (rc != CSA_OK) return rc;
+    rc = workspace_ok(w, workspace, workspace_bytes,
+                      cache_attention_workspace_bytes(cache->head_size));
+    if (rc != CSA_OK) return rc;
+    return on_device(stream, [&](const DeviceInfo& dev, cudaStream_t st, std::string& err) {
+      return cache_attention_launch(
+          *cache, *batch,
+          {q, out, dtype, q_heads, q_token_stride, q_head_stride, out_token_stride,
+           out_head_stride, scale, window, sinks, workspace},
+          st, dev, err);
+    });
+  });
+}
+
+csa_status cache_attention_shared_workspace_size(const csa_kv_cache* cache, int q_heads, int rows,
+                                                 int sequences, int group_count, size_t* bytes) {
+  return no_throw([&] {
+    t_last_error.clear();
+    const std::string w("cache_attention_shared_workspace_size");
+    if (!bytes) return set_error(CSA_ERR_NULL, w + ": null pointer");
+    *bytes = 0;
     int rc = attention_heads_ok(w, cache, q_heads);
-    if (rc == CSA_OK) rc = batch_args_ok(w, batch);
-    if (rc != CSA_OK) return rc;
-    if (!out || !q) return set_error(CSA_ERR_NULL, w + ": null pointer");
-    if (dtype != CSA_BF16 && dtype != CSA_F16)
-      return set_error(CSA_ERR_UNSUPPORTED, w + ": unknown dtype");
-    if (!std::isfinite(scale)) return set_error(CSA_ERR_SHAPE, w + ": scale not finite");
-    if (window < 0 || sinks < 0)
-      return set_error(CSA_ERR_SHAPE, w + ": window and sinks must be >= 0");
-    rc = rows_ok(w, q, dtype, batch->rows, q_heads, cache->head_size, q_token_stride, q_head_stride,
-                 false);
+    if (rc == CSA_OK) rc = shared_sizes_ok(w, q_heads, rows, sequences, group_count);
     if (rc == CSA_OK)
-      rc = rows_ok(w, out, dtype, batch->rows, q_heads, cache->head_size, out_token_stride,
-                   out_head_stride, true);
+      *bytes = cache_attention_shared_workspace_bytes(
+          cache->head_size, static_cast<long long>(rows) * q_heads, sequences, group_count);
+    return rc;
+  });
+}
+
+csa_status cache_attention_shared_forward(void* out, const void* q, int dtype, int q_heads,
+                                          int64_t out_token_stride, int64_t out_head_stride,
+                                          int64_t q_token_stride, int64_t q_head_stride,
+                                          const csa_kv_cache* cache, const csa_kv_batch* batch,
+                                          const int32_t* groups, const int32_t* shared,
+                                          int group_count, float scale, void* workspace,
+                                          size_t workspace_bytes, void* stream) {
+  return no_throw([&] {
+    t_last_error.clear();
+    const std::string w("cache_attention_shared_forward");
+    int rc = attention_args_ok(w, out, q, dtype, q_heads, out_token_stride, out_head_stride,
+                               q_token_stride, q_head_stride, cache, batch, scale, 0, 0);
+    if (rc == CSA_OK) rc = shared_sizes_ok(w, q_heads, batch->rows, batch->sequences, group_count);
+    if (rc == CSA_OK) rc = list_ok(w, groups, group_count);
+    if (rc == CSA_OK) rc = list_ok(w, shared, group_count);
+    if (rc == CSA_OK)
+      rc = workspace_ok(w, workspace, workspace_bytes,
+                        cache_attention_shared_workspace_bytes(
+                            cache->head_size, static_cast<long long>(batch->rows) * q_heads,
+                            batch->sequences, group_count));
     if (rc != CSA_OK) return rc;
-    // A unit reads its own rows of q before it writes them, so in place is fine.
-    const bool in_place = out == q && (batch->rows == 1 || q_token_stride == out_token_stride) &&
-                          (q_heads == 1 || q_head_stride == out_head_stride);
-    if (!in_place &&
-        rows_meet({q, q_token_stride, q_head_stride}, {out, out_token_stride, out_head_stride},
-                  batch->rows, q_heads, cache->head_size, 2))
-      return set_error(CSA_ERR_UNSUPPORTED, w + ": q and out overlap in part");
-    const size_t need = cache_attention_workspace_bytes(cache->head_size);
-    if (!workspace || workspace_bytes < need)
-      return set_error(CSA_ERR_WORKSPACE, w + ": " + std::to_string(need) +
-                                              " bytes of workspace needed, " +
-                                              std::to_string(workspace ? workspace_bytes : 0) +
-                                              " given");
-    if (!aligned(workspace, 16))
-      return set_error(CSA_ERR_ALIGN, w + ": workspace must be 16-byte aligned");
-    DeviceInfo dev;
-    std::string err;
-    rc = current_device(dev, err);
-    if (rc != CSA_OK) return set_error(rc, err);
-    apply_stream_sm_limit(dev, static_cast<cudaStream_t>(stream));
-    rc = cache_attention_launch(*cache, *batch,
-                                {q, out, dtype, q_heads, q_token_stride, q_head_stride,
-                                 out_token_stride, out_head_stride, scale, window, sinks, workspace},
-                                static_cast<cudaStream_t>(stream), dev, err);
-    return rc == CSA_OK ? CSA_OK : set_error(rc, err);
+    return on_device(stream, [&](const DeviceInfo& dev, cudaStream_t st, std::string& err) {
+      return cache_attention_shared_launch(
+          *cache, *batch,
+          {q, out, dtype, q_heads, q_token_stride, q_head_stride, out_token_stride,
+           out_head_stride, scale, 0, 0, workspace},
+          groups, shared, group_count, st, dev, err);
+    });
   });
 }
 

@@ -199,6 +199,14 @@ int cache_attention_launch(const csa_kv_cache& cache, const csa_kv_batch& batch,
                            const AttendCall& call, cudaStream_t stream, const DeviceInfo& dev,
                            std::string& err);
 
+// Attention whose sequences share long beginnings; call.workspace of the bytes below.
+size_t cache_attention_shared_workspace_bytes(int head_size, long long rows_heads, int sequences,
+                                              int groups);
+int cache_attention_shared_launch(const csa_kv_cache& cache, const csa_kv_batch& batch,
+                                  const AttendCall& call, const int* groups, const int* shared,
+                                  int group_count, cudaStream_t stream, const DeviceInfo& dev,
+                                  std::string& err);
+
 // What the kernel for few rows leaves the one for prompts in the workspace.
 struct PromptList {
   unsigned int taken;  // units taken: 0

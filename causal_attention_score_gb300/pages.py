@@ -7,8 +7,9 @@ import ctypes
 import torch
 
 from . import _lib
-from .ops import _need, _torch_stream
-from .serving import KvCache, _elsewhere, _get_device, _Marshalled, _stream_ptr
+from .ops import _need
+from .serving import (KvCache, _elsewhere, _get_device, _given, _Marshalled, _stream_ptr,
+                      _workspace)
 
 
 class _KvPagesStruct(ctypes.Structure):
@@ -78,21 +79,10 @@ def _list(t: torch.Tensor, name: str, n: int, dev: int) -> int:
 
 
 def _scratch(workspace, pages: KvPages, n: int, stream, dev: int):
-    """(workspace, stream): without a workspace one from torch's caching allocator, in the
-    call's stream's order."""
+    """(workspace, stream): the caller's workspace checked, or one of our own."""
     if workspace is None:
-        size, device = kv_pages_workspace_size(pages, n), pages.refs.device
-        if stream is None:
-            return torch.empty(size, dtype=torch.uint8, device=device), None
-        stream = _torch_stream(stream, device)
-        with torch.cuda.stream(stream):
-            return torch.empty(size, dtype=torch.uint8, device=device), stream
-    if workspace.get_device() != dev:
-        if not workspace.is_cuda:
-            raise ValueError("workspace must be a contiguous CUDA tensor")
-        raise _elsewhere(workspace.device, "workspace")
-    if not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor")
+        return _workspace(kv_pages_workspace_size(pages, n), pages.refs.device, stream)
+    _given(workspace, dev)
     return workspace, stream
 
 

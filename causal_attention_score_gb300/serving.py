@@ -293,6 +293,25 @@ def kv_cache_read(k: torch.Tensor, v: torch.Tensor, cache: KvCache, batch: KvBat
         _lib.check(rc, "kv_cache_read")
 
 
+def _workspace(size: int, device, stream):
+    """(workspace, stream): scratch from torch's caching allocator, in the call's stream's order."""
+    if stream is None:
+        return torch.empty(size, dtype=torch.uint8, device=device), None
+    stream = _torch_stream(stream, device)
+    with torch.cuda.stream(stream):
+        return torch.empty(size, dtype=torch.uint8, device=device), stream
+
+
+def _given(workspace: torch.Tensor, dev: int) -> None:
+    """Checks the caller's workspace."""
+    if workspace.get_device() != dev:
+        if not workspace.is_cuda:
+            raise ValueError("workspace must be a contiguous CUDA tensor")
+        raise _elsewhere(workspace.device, "workspace")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+
+
 def cache_attention_workspace_size(cache: KvCache, batch: KvBatch, q_heads: int) -> int:
     """Bytes of workspace ``cache_attention_forward`` needs (the same for any batch)."""
     n = ctypes.c_size_t(0)
@@ -319,24 +338,73 @@ def cache_attention_forward(out: torch.Tensor, q: torch.Tensor, cache: KvCache, 
     ref = cache._pointer(dev)
     if workspace is None:
         size = cache_attention_workspace_size(cache, batch, q_heads)
-        if stream is None:
-            workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
-        else:
-            stream = _torch_stream(stream, q.device)
-            with torch.cuda.stream(stream):
-                workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
-    elif workspace.get_device() != dev:
-        if not workspace.is_cuda:
-            raise ValueError("workspace must be a contiguous CUDA tensor")
-        raise _elsewhere(workspace.device, "workspace")
-    elif not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor")
+        workspace, stream = _workspace(size, q.device, stream)
+    else:
+        _given(workspace, dev)
     rc = (_lib._lib or _lib.load()).cache_attention_forward(
         out.data_ptr(), q.data_ptr(), _DTYPE[dtype], q_heads, ot, oh, qt, qh, ref,
         batch._pointer(dev), 1.0 / math.sqrt(cache.head_size) if scale is None else scale, window,
         sinks, workspace.data_ptr(), workspace.nbytes, _stream_ptr(stream, dev))
     if rc:
         _lib.check(rc, "cache_attention_forward")
+
+
+def cache_attention_shared_workspace_size(cache: KvCache, batch: KvBatch, q_heads: int,
+                                          groups: int) -> int:
+    """Bytes of workspace ``cache_attention_shared_forward`` needs for batches of up to this one's
+    rows and sequences and ``groups`` groups."""
+    n = ctypes.c_size_t(0)
+    _lib.check(_lib.load().cache_attention_shared_workspace_size(
+        cache._ref, q_heads, batch.rows, batch.lengths.numel(), groups, ctypes.byref(n)),
+        "cache_attention_shared_workspace_size")
+    return int(n.value)
+
+
+def cache_attention_shared_forward(out: torch.Tensor, q: torch.Tensor, cache: KvCache,
+                                   batch: KvBatch, groups: torch.Tensor, shared: torch.Tensor,
+                                   scale: float | None = None,
+                                   workspace: torch.Tensor | None = None, stream=None) -> None:
+    """cache_attention_forward (without a window) for sequences that share long beginnings: those
+    from ``groups[g]`` to ``groups[g + 1] - 1`` (int32 [G + 1]) share their first ``shared[g]``
+    tokens (int32 [G], whole pages), which are looked up in the first one's table row and read
+    once; rows lie behind them. Without a ``workspace`` (at least
+    cache_attention_shared_workspace_size bytes) one is taken from torch's caching allocator on the
+    call's stream. See cache_attention_shared_forward in include/csa.h."""
+    if q.dim() != 3:
+        raise ValueError("q must be [rows, q_heads, head_size]")
+    dev, dtype, q_heads = _device_of(q, "q"), q.dtype, q.shape[1]
+    shape = (batch.rows, q_heads, cache.head_size)
+    qt, qh = _rows(q, "q", shape, _HALF, dev)
+    ot, oh = _rows(out, "out", shape, (dtype,), dev)
+    _need(shared, "shared", torch.int32, shared.numel())
+    G = shared.numel()
+    _need(groups, "groups", torch.int32, G + 1)
+    for name, t in (("groups", groups), ("shared", shared)):
+        if t.get_device() != dev:
+            raise _elsewhere(t.device, name)
+    ref, rows = cache._pointer(dev), batch._pointer(dev)
+    if workspace is None:
+        size = cache_attention_shared_workspace_size(cache, batch, q_heads, G)
+        workspace, stream = _workspace(size, q.device, stream)
+    else:
+        _given(workspace, dev)
+    rc = (_lib._lib or _lib.load()).cache_attention_shared_forward(
+        out.data_ptr(), q.data_ptr(), _DTYPE[dtype], q_heads, ot, oh, qt, qh, ref, rows,
+        groups.data_ptr(), shared.data_ptr(), G,
+        1.0 / math.sqrt(cache.head_size) if scale is None else scale, workspace.data_ptr(),
+        workspace.nbytes, _stream_ptr(stream, dev))
+    if rc:
+        _lib.check(rc, "cache_attention_shared_forward")
+
+
+def cache_attention_shared(q: torch.Tensor, cache: KvCache, batch: KvBatch, groups: torch.Tensor,
+                           shared: torch.Tensor, scale: float | None = None,
+                           stream=None) -> torch.Tensor:
+    """Allocating form of cache_attention_shared_forward; rows of no sequence are zero. The output
+    is allocated and cleared on the call's stream."""
+    out = _allocate(torch.zeros, q.shape, q.dtype, q.device, stream)
+    cache_attention_shared_forward(out, q, cache, batch, groups, shared, scale, None, stream)
+    return out
 
 
 def cache_attention(q: torch.Tensor, cache: KvCache, batch: KvBatch, scale: float | None = None,

@@ -555,6 +555,40 @@ csa_status cache_attention_forward(void* out, const void* q, int dtype, int q_he
 csa_status cache_attention_workspace_size(const csa_kv_cache* cache, int q_heads, size_t* bytes);
 
 /*
+ * cache_attention_shared_forward -- cache_attention_forward (without a window) for a batch whose
+ * sequences share long beginnings, such as answers sampled from one prompt or requests behind one
+ * set of instructions: the keys of what a group of sequences shares are read, and multiplied with
+ * the rows of all of them, once.
+ *   groups     device, int32 [group_count + 1], not decreasing, within [0, sequences]: group g is
+ *              sequences groups[g] .. groups[g + 1] - 1 of the batch, next to each other;
+ *              sequences of no group share nothing;
+ *   shared     device, int32 [group_count]: the tokens that the group's sequences share, whole
+ *              pages (a multiple of page_tokens, at most table_width * page_tokens). They are
+ *              looked up in the table's row of the group's FIRST sequence (which need not have
+ *              rows); the others' entries for them are not read. 0: nothing is shared.
+ *   workspace  cache_attention_shared_workspace_size bytes, otherwise as there.
+ * Row j of sequence s, at position p = lengths[s] - n + j, sees the shared[g] tokens and its
+ * sequence's own from there to p: with table rows that begin alike the result is
+ * cache_attention_forward's, up to the order of sums. Rows lie behind what their sequence shares
+ * (lengths[s] - n >= shared[g]); a sequence with rows that do not is left out and
+ * csa_get_status reports CSA_ERR_INDEX, as is a group whose shared[g] breaks the rules; where the
+ * bounds in `groups` do, nothing is computed. Numerics, outputs, in-place use, rows past the last
+ * sequence's and the fixed order of sums as cache_attention_forward. rows * q_heads up to 2^30.
+ *
+ * cache_attention_shared_workspace_size -- bytes of workspace it needs for batches of up to this
+ * many rows, sequences and groups, into *bytes. Host only.
+ */
+csa_status cache_attention_shared_workspace_size(const csa_kv_cache* cache, int q_heads, int rows,
+                                                 int sequences, int group_count, size_t* bytes);
+csa_status cache_attention_shared_forward(void* out, const void* q, int dtype, int q_heads,
+                                          int64_t out_token_stride, int64_t out_head_stride,
+                                          int64_t q_token_stride, int64_t q_head_stride,
+                                          const csa_kv_cache* cache, const csa_kv_batch* batch,
+                                          const int32_t* groups, const int32_t* shared,
+                                          int group_count, float scale, void* workspace,
+                                          size_t workspace_bytes, void* stream);
+
+/*
  * csa_kv_pages -- the books of a cache: which pages each of `sequences` places has.
  *   refs         device, int32 [pages]: how many table entries name each page, 0: free;
  *   lengths      device, int32 [sequences]: tokens of each place's sequence, 0: none there;
