@@ -16,7 +16,8 @@ Public API (all compute runs in libcsa_gb300.so; see include/csa.h):
   for the rows a ``KvBatch`` names, and ``cache_attention_forward`` over it
   (``cache_attention`` allocates; ``cache_attention_workspace_size`` for its scratch)
 * ``cache_attention_shared_forward`` for a batch whose sequences share long beginnings
-  (``cache_attention_shared`` allocates; ``cache_attention_shared_workspace_size``)
+  (``cache_attention_shared`` allocates; ``cache_attention_shared_workspace_size``;
+  ``set_shared_part`` to have the shared part always worked out apart)
 * ``KvPages``, the books of a cache: ``kv_pages_extend`` (room for more tokens),
   ``kv_cache_fork`` (a sequence that shares another's tokens), ``kv_pages_free``,
   ``kv_cache_copy`` (pages of one cache into another), ``kv_cache_compact``;
@@ -44,10 +45,10 @@ from .ops import (DENSE_FETCH_AUTO, DENSE_FETCH_LOADERS, DenseGroupedPlan, batch
 from .logprobs import token_logprobs, token_logprobs_backward, token_logprobs_forward
 from .pages import (KvPages, kv_cache_compact, kv_cache_copy, kv_cache_fork, kv_pages_extend,
                     kv_pages_free, kv_pages_workspace_size)
-from .serving import (KvBatch, KvCache, RotaryTable, cache_attention, cache_attention_forward,
+from .serving import (SHARED_ALWAYS, SHARED_AUTO, KvBatch, KvCache, RotaryTable, cache_attention, cache_attention_forward,
                       cache_attention_shared, cache_attention_shared_forward,
                       cache_attention_shared_workspace_size, cache_attention_workspace_size, kv_cache_read, kv_cache_write,
-                      rotary_backward, rotary_forward, rotary_qkv)
+                      rotary_backward, rotary_forward, rotary_qkv, set_shared_part)
 
 __all__ = [
     "trimul_forward", "trimul_forward_f32", "dense_xwt", "dense_xwt_ws", "dense_workspace_size",
@@ -59,7 +60,7 @@ __all__ = [
     "KvCache", "KvBatch", "kv_cache_write", "kv_cache_read",
     "cache_attention_forward", "cache_attention", "cache_attention_workspace_size",
     "cache_attention_shared_forward", "cache_attention_shared",
-    "cache_attention_shared_workspace_size",
+    "cache_attention_shared_workspace_size", "set_shared_part", "SHARED_AUTO", "SHARED_ALWAYS",
     "KvPages", "kv_pages_extend", "kv_cache_fork", "kv_pages_free", "kv_cache_copy",
     "kv_cache_compact", "kv_pages_workspace_size", "CSA_ERR_PAGES",
     "token_logprobs_forward", "token_logprobs_backward", "token_logprobs",

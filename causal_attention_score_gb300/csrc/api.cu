@@ -36,6 +36,7 @@ PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::atomic<uint64_t> g_wait_limit_ns{0};
 std::atomic<int> g_inject{0};
 std::atomic<int> g_dense_fetch{CSA_DENSE_FETCH_AUTO};
+std::atomic<int> g_shared_part{CSA_SHARED_AUTO};
 constexpr uint64_t kDefaultWaitLimitNs = 2000000000ull;  // 2 s
 
 int set_error(int code, const std::string& msg) {
@@ -387,6 +388,7 @@ void abandon_counter_slot(int family, const DeviceInfo& dev, const CounterSlot& 
 
 bool take_inject() { return g_inject.exchange(0) != 0; }
 int dense_fetch_mode() { return g_dense_fetch.load(); }
+int shared_part_mode() { return g_shared_part.load(); }
 
 }  // namespace csa
 
@@ -1247,6 +1249,16 @@ csa_status cache_attention_forward(void* out, const void* q, int dtype, int q_he
            out_head_stride, scale, window, sinks, workspace},
           st, dev, err);
     });
+  });
+}
+
+csa_status csa_set_shared_part(int mode) {
+  return no_throw([&] {
+    t_last_error.clear();
+    if (mode != CSA_SHARED_AUTO && mode != CSA_SHARED_ALWAYS)
+      return set_error(CSA_ERR_SHAPE, "csa_set_shared_part: unknown mode " + std::to_string(mode));
+    g_shared_part.store(mode);
+    return static_cast<int>(CSA_OK);
   });
 }
 

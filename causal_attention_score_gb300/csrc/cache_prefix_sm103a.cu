@@ -1,6 +1,6 @@
-// The shared part of attention for a batch whose sequences share long beginnings, on tcgen05
-// (cache_prompt.cuh): the plan's units, 256 rows of all the group's sequences over a run of its
-// tokens, whose results the kernel of the sequences' own parts joins.
+// Attention for a batch whose sequences share long beginnings, on tcgen05 (cache_prompt.cuh): the
+// shared part, the plan's units of 256 rows of all the group's sequences over a run of its tokens;
+// and the own parts of sequences with many rows, behind the kernel of few rows.
 #include <string>
 
 #include "cache_prompt.cuh"
@@ -10,11 +10,13 @@
 namespace csa {
 
 int cache_prefix_launch(const csa_kv_cache& cache, const csa_kv_batch& batch,
-                        const AttendCall& call, const SharedPlan& plan, cudaStream_t stream,
-                        const DeviceInfo& dev, std::string& err) {
-  PromptArgs a = prompt_args(cache, batch, call, &plan.head->list, dev);
+                        const AttendCall& call, const SharedPlan& plan, bool own,
+                        cudaStream_t stream, const DeviceInfo& dev, std::string& err) {
+  PromptArgs a =
+      prompt_args(cache, batch, call, own ? &plan.head->own : &plan.head->shared, dev);
   a.plan = plan;
-  return launch_prompt<true>(a, cache, stream, dev, err);
+  return own ? launch_prompt<kOwnPart>(a, cache, stream, dev, err)
+             : launch_prompt<kSharedPart>(a, cache, stream, dev, err);
 }
 
 }  // namespace csa

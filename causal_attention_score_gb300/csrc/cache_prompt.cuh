@@ -1,4 +1,4 @@
-// The kernel of cache_prompt_sm103a.cu and, with kShared, of cache_prefix_sm103a.cu.
+// The kernel of cache_prompt_sm103a.cu and, with another kMode, of cache_prefix_sm103a.cu.
 //
 // Attention of many new tokens per sequence (prompts and their chunks) over the
 // paged 8-bit cache: the same function as the rows kernel of
@@ -109,7 +109,7 @@ struct PromptArgs {
   int* status;
   unsigned long long wait_limit_ns;
   int inject;
-  SharedPlan plan;  // kShared: the units are the plan's, what they leave goes to its parts
+  SharedPlan plan;  // kSharedPart, kOwnPart
 };
 
 // What 16 keys' scores are multiplied with (to the base-2 exponent), log2 of their V's
@@ -119,17 +119,28 @@ struct Factor {
   uint32_t far;  // of a tile's first: not 0 where V of 16 of its keys lies far below others'
 };
 
-// kShared: where the unit's rows' parts are.
-template <bool kShared>
+// kSharedPart: the units are the plan's, 256 rows of a group over a run of its tokens; kOwnPart:
+// as in kWhole those of sequences, but from their first own token on. What they leave is joined
+// later.
+enum Mode { kWhole, kSharedPart, kOwnPart };
+
+// Where the unit's rows' parts are (kOwnPart: what the joining needs to find the shared ones); its
+// first token; whose table row names which tokens.
+template <int kMode>
 struct UnitParts {};
 template <>
-struct UnitParts<true> {
+struct UnitParts<kSharedPart> {
   long long first;
-  int pieces;
+  int pieces, base;
+};
+template <>
+struct UnitParts<kOwnPart> {
+  long long first;
+  int pieces, base, lead, leader;
 };
 
-template <bool kShared>
-struct Unit : UnitParts<kShared> {
+template <int kMode>
+struct Unit : UnitParts<kMode> {
   KvSequence q;
   int s, head, row0, rows;  // rows [row0, row0 + rows) of the sequence
   int sink_tiles, window_tile;
@@ -137,7 +148,7 @@ struct Unit : UnitParts<kShared> {
   int n[2];                 // tiles of each group; n[0] < 0: the list has ended
 };
 
-template <int HSP, bool kShared>
+template <int HSP, int kMode>
 struct Layout {
   static constexpr int kQBytes = kRows * HSP * 2;  // per group: [HSP / 64][128 rows][128 B]
   static constexpr int kKBytes = kTile * HSP * 2;  // per slot: [HSP / 64][64 rows][128 B]
@@ -149,7 +160,7 @@ struct Layout {
                        kFactors = kRaw + kRawSlots * 2 * kRawBytes,
                        kBars = kFactors + kFactorSlots * 4 * static_cast<int>(sizeof(Factor)),
                        kMisc = kBars + 8 * 40, kUnits = kMisc + 32,
-                       kTotal = kUnits + kUnitSlots * static_cast<int>(sizeof(Unit<kShared>));
+                       kTotal = kUnits + kUnitSlots * static_cast<int>(sizeof(Unit<kMode>));
 };
 
 // The list's u-th unit: sequences by their longest unit, the longest first (up to
@@ -161,7 +172,14 @@ __device__ __forceinline__ long long units_of(const PromptArgs& a, int row_limit
   return rows <= row_limit ? 0 : (rows + kUnitRows - 1) / kUnitRows * a.v.heads;
 }
 
-__device__ inline Unit<false> decode_unit(const PromptArgs& a, int row_limit, const long long* prefix,
+template <int kMode>
+__device__ KvSequence sequence_of(const PromptArgs& a, int s) {
+  if constexpr (kMode == kOwnPart) return a.plan.sequences[s].q;
+  return kv_sequence(a.v, s);
+}
+
+template <int kMode>
+__device__ Unit<kMode> decode_unit(const PromptArgs& a, int row_limit, const long long* prefix,
                             const int* order, int per, long long u) {
   int lo = 0, hi = kThreads;
   while (hi - lo > 1) {
@@ -169,10 +187,10 @@ __device__ inline Unit<false> decode_unit(const PromptArgs& a, int row_limit, co
     if (prefix[mid] <= u) lo = mid;
     else hi = mid;
   }
-  Unit<false> r{};
+  Unit<kMode> r{};
   long long base = prefix[lo];
   for (r.s = per == 1 ? order[lo] : lo * per;; ++r.s) {
-    r.q = kv_sequence(a.v, r.s);
+    r.q = sequence_of<kMode>(a, r.s);
     const long long n = units_of(a, row_limit, r.q);
     if (u < base + n) break;
     base += n;
@@ -198,23 +216,37 @@ __device__ inline Unit<false> decode_unit(const PromptArgs& a, int row_limit, co
     r.n[g] = 0;
     if (rows <= 0) continue;
     const int last = r.q.first + (r.row0 + g * kRows + rows - 1) / a.group;  // position
+    if constexpr (kMode == kOwnPart) {
+      const SharedSequence p = a.plan.sequences[r.s];
+      r.base = p.start;
+      r.lead = p.lead;
+      r.leader = p.leader;
+      r.first = r.pieces = 0;
+      if (p.group >= 0) {
+        const SharedGroup g0 = a.plan.groups[p.group];
+        r.first = shared_part(g0, a.group, r.head, (r.q.row0 - g0.row0) * a.group + r.row0);
+        r.pieces = g0.pieces;
+      }
+      if (last >= p.start) r.n[g] = (last - p.start) / kTile + 1;
+      continue;
+    }
     if (last >= 0) r.n[g] = r.sink_tiles + max(last / kTile + 1 - r.window_tile, 0);
   }
   return r;
 }
 
 // Unit u of the plan: 256 rows of a group over a run of its tokens, all of which they see.
-__device__ inline Unit<true> decode_shared(const PromptArgs& a, int u) {
+__device__ inline Unit<kSharedPart> decode_shared(const PromptArgs& a, int u) {
   const SharedGroup g = a.plan.groups[shared_group_of(a.plan, u)];
   const SharedUnit unit = shared_unit(g, a.v.heads, u);
-  Unit<true> r{};
+  Unit<kSharedPart> r{};
   r.q = {g.row0, g.rows, g.tokens, 1 << 30};  // (behind every key)
   r.s = g.sequence;
   r.head = unit.head;
   r.row0 = unit.block * kUnitRows;
   r.rows = min(g.rows * a.group - r.row0, kUnitRows);
-  r.sink_tiles = r.hidden_to = 0;
-  r.window_tile = unit.tile0;
+  r.sink_tiles = r.window_tile = r.hidden_to = 0;
+  r.base = unit.tile0 * kTile;
   r.n[0] = unit.tiles;
   r.n[1] = r.rows > kRows ? unit.tiles : 0;
   r.first = shared_part(g, a.group, r.head, r.row0) + unit.piece;
@@ -223,9 +255,9 @@ __device__ inline Unit<true> decode_shared(const PromptArgs& a, int u) {
 }
 
 // (checking build) whether a unit's rows and tiles are its sequence's.
-template <bool kShared>
-__device__ __forceinline__ bool unit_ok(const PromptArgs& a, const Unit<kShared>& u) {
-  if constexpr (kShared) {
+template <int kMode>
+__device__ __forceinline__ bool unit_ok(const PromptArgs& a, const Unit<kMode>& u) {
+  if constexpr (kMode != kWhole) {
     if (u.first < 0 || u.first + static_cast<long long>(u.rows - 1) * u.pieces >= a.plan.parts)
       return false;
   }
@@ -236,8 +268,9 @@ __device__ __forceinline__ bool unit_ok(const PromptArgs& a, const Unit<kShared>
          u.q.row0 + u.q.n <= a.v.rows && u.n[0] <= tiles && u.n[1] >= 0 && u.n[1] <= tiles;
 }
 
-template <bool kShared>
-__device__ __forceinline__ int tile_token(const Unit<kShared>& u, int j) {
+template <int kMode>
+__device__ __forceinline__ int tile_token(const Unit<kMode>& u, int j) {
+  if constexpr (kMode != kWhole) return u.base + j * kTile;
   return (j < u.sink_tiles ? j : j - u.sink_tiles + u.window_tile) * kTile;
 }
 
@@ -402,11 +435,11 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, const uint32_t* w) {
   st_shared_v4(addr, w[0], w[1], w[2], w[3]);
 }
 
-template <int HSP, int kFormat, bool kBf16, bool kShared>
+template <int HSP, int kFormat, bool kBf16, int kMode>
 __global__ void __launch_bounds__(kThreads, 1)
     attend_prompt_sm103a_kernel(const PromptArgs a) {
-  using L = Layout<HSP, kShared>;
-  using Unit = Unit<kShared>;
+  using L = Layout<HSP, kMode>;
+  using Unit = Unit<kMode>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ long long s_prefix[kThreads + 1];
   __shared__ long long s_warp[kThreads / 32];
@@ -474,15 +507,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dependency_wait();
 
   // The work list: thread i counts the units of sequences [i per, (i + 1) per).
-  const int S = a.v.sequences, row_limit = kShared ? 0 : a.list->row_limit;
+  const int S = a.v.sequences, row_limit = kMode == kSharedPart ? 0 : a.list->row_limit;
   const int per = (S + kThreads - 1) / kThreads;
-  if constexpr (!kShared) {
+  if constexpr (kMode != kSharedPart) {
     long long mine = 0;
     if (per == 1) {
       const int i = threadIdx.x;
       int key = -1;
       if (i < S) {
-        const KvSequence q = kv_sequence(a.v, i);
+        const KvSequence q = sequence_of<kMode>(a, i);
         if (units_of(a, row_limit, q) > 0)
           key = a.window > 0 && a.window < q.length - q.n ? a.window + q.n : q.length;
       }
@@ -494,11 +527,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         s_order[rank] = i;
       }
       __syncthreads();
-      if (i < S) mine = units_of(a, row_limit, kv_sequence(a.v, s_order[i]));
+      if (i < S) mine = units_of(a, row_limit, sequence_of<kMode>(a, s_order[i]));
     } else {
       const long long from = static_cast<long long>(threadIdx.x) * per;
       for (long long s = from; s < min(static_cast<long long>(S), from + per); ++s)
-        mine += units_of(a, row_limit, kv_sequence(a.v, static_cast<int>(s)));
+        mine += units_of(a, row_limit, sequence_of<kMode>(a, static_cast<int>(s)));
     }
     long long sum = mine;
 #pragma unroll
@@ -516,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, ld_shared_b32(tmem_slot), 0);
-  const long long total = kShared ? a.plan.head->units : s_prefix[kThreads];
+  const long long total = kMode == kSharedPart ? a.plan.head->units : s_prefix[kThreads];
   // The k-th unit that this CTA works on, for a whole warp; false: a wait ran out.
   auto take_unit = [&](uint32_t k, Unit& u) {
     const uint32_t slot = k % kUnitSlots;
@@ -599,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after_sync();
         const Factor* fac = factors + ((tiles + step) % kFactorSlots) * 4;
-        const bool edge = !kShared &&
+        const bool edge = kMode != kSharedPart &&
                           !(tb + kTile - 1 <= pos_low &&
                             (a.window == 0 || pos_high - tb < a.window || tb + kTile - 1 < a.sinks));
         // columns 0 .. last are at or before this row; from first_window on, or below
@@ -719,9 +752,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // seen, so that its first scores are computed while O is written.
       uint16_t* to = static_cast<uint16_t*>(a.out) +
                      (live ? row.token * a.out_token + row.head * a.out_head : 0);
-      [[maybe_unused]] long long part = 0;
-      if constexpr (kShared)
+      [[maybe_unused]] long long part = 0, own = 0;
+      [[maybe_unused]] int shared = 0;
+      if constexpr (kMode != kWhole) {
         part = u.first + (static_cast<long long>(g) * kRows + r) * u.pieces;
+        own = static_cast<long long>(row.token) * (a.v.heads * a.group) + row.head;
+        shared = u.pieces;
+      }
       more = next_unit(k);
       if (n > 0) {
         const uint32_t final = products - 1;
@@ -730,16 +767,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         tc_fence_after_sync();
       }
-      if constexpr (kShared) {
-        if (n > 0 && live) a.plan.ml[part] = make_float2(m, l);
+      if constexpr (kMode != kWhole) {
+        constexpr bool kOwn = kMode == kOwnPart;
+        if (live && (kOwn || n > 0)) {
+          if (kOwn) {
+            a.plan.own_ml[own] = make_float2(m, l);
+            a.plan.own[own] = OwnRow{part, shared, 0, 0, 0};
+            a.plan.own_there[own] = 1;
+          } else {
+            a.plan.ml[part] = make_float2(m, l);
+          }
+        }
+        __syncwarp();
+        float* to_o = kOwn ? a.plan.own_o + own * HSP : a.plan.o + part * HSP;
 #pragma unroll 1
-        for (int d0 = 0; n > 0 && d0 < HSP; d0 += 64) {
+        for (int d0 = 0; (kOwn || n > 0) && d0 < HSP; d0 += 64) {
           uint32_t x[64];
-          tmem_ld_64cols(o_tmem + d0, x);
+          if (n > 0) {
+            tmem_ld_64cols(o_tmem + d0, x);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) x[i] = 0u;
+          }
           if (live) {
 #pragma unroll
             for (int d = 0; d < 64; d += 4)
-              *reinterpret_cast<uint4*>(a.plan.o + part * HSP + d0 + d) =
+              *reinterpret_cast<uint4*>(to_o + d0 + d) =
                   make_uint4(x[d], x[d + 1], x[d + 2], x[d + 3]);
           }
           __syncwarp();
@@ -927,12 +980,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool there;
     };
     const int before = lane % groups * 16, after = groups * 16 - before;
+    auto row_of = [&](const Unit& u, int tok) {
+      if constexpr (kMode == kOwnPart) return tok < u.lead ? u.leader : u.s;
+      return u.s;
+    };
     auto entries_of = [&](const Unit& u, int j) {
       const int tok = tile_token(u, j) + 16 * lane;
       Entry e{-1, lane < 4 && tok < u.q.length &&
                       (tok + after > u.hidden_to || tok - before < a.sinks)};
       if (e.there)
-        e.page = __ldg(a.v.table + (static_cast<long long>(u.s) * a.v.table_width +
+        e.page = __ldg(a.v.table + (static_cast<long long>(row_of(u, tok)) * a.v.table_width +
                                     (tok >> a.v.page_shift)));
       return e;
     };
@@ -1052,8 +1109,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long long at = atomicAdd(&a.list->taken, 1u);
         Unit u;
         if (at >= total) u.n[0] = -1;
-        else if constexpr (kShared) u = decode_shared(a, static_cast<int>(at));
-        else u = decode_unit(a, row_limit, s_prefix, s_order, per, at);
+        else if constexpr (kMode == kSharedPart) u = decode_shared(a, static_cast<int>(at));
+        else u = decode_unit<kMode>(a, row_limit, s_prefix, s_order, per, at);
         if (!mbar_wait(u_empty(slot), ((k / kUnitSlots) & 1u) ^ 1u, wd, kSiteSched)) break;
         reinterpret_cast<Unit*>(gbase + L::kUnits)[slot] = u;
         mbar_arrive(u_full(slot));
@@ -1188,24 +1245,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
-template <int HSP, int kFormat, bool kBf16, bool kShared>
+template <int HSP, int kFormat, bool kBf16, int kMode>
 cudaError_t launch_prompt(const PromptArgs& a, const DeviceInfo& dev, cudaStream_t stream, int& rc,
                           std::string& err) {
-  const auto kernel = attend_prompt_sm103a_kernel<HSP, kFormat, kBf16, kShared>;
-  const int smem = Layout<HSP, kShared>::kTotal + 1024;
+  const auto kernel = attend_prompt_sm103a_kernel<HSP, kFormat, kBf16, kMode>;
+  const int smem = Layout<HSP, kMode>::kTotal + 1024;
   rc = set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), smem, dev.device, err);
   if (rc != CSA_OK) return cudaSuccess;
   return launch_programmatic(kernel, static_cast<unsigned>(dev.sm_count), kThreads, smem, stream, a);
 }
 
-template <int HSP, bool kShared>
+template <int HSP, int kMode>
 cudaError_t launch_prompt(const PromptArgs& a, int format, const DeviceInfo& dev,
                           cudaStream_t stream, int& rc, std::string& err) {
   if (format == CSA_KV_INT8)
-    return a.half ? launch_prompt<HSP, CSA_KV_INT8, false, kShared>(a, dev, stream, rc, err)
-                  : launch_prompt<HSP, CSA_KV_INT8, true, kShared>(a, dev, stream, rc, err);
-  return a.half ? launch_prompt<HSP, CSA_KV_E4M3, false, kShared>(a, dev, stream, rc, err)
-                : launch_prompt<HSP, CSA_KV_E4M3, true, kShared>(a, dev, stream, rc, err);
+    return a.half ? launch_prompt<HSP, CSA_KV_INT8, false, kMode>(a, dev, stream, rc, err)
+                  : launch_prompt<HSP, CSA_KV_INT8, true, kMode>(a, dev, stream, rc, err);
+  return a.half ? launch_prompt<HSP, CSA_KV_E4M3, false, kMode>(a, dev, stream, rc, err)
+                : launch_prompt<HSP, CSA_KV_E4M3, true, kMode>(a, dev, stream, rc, err);
 }
 
 // What both callers' arguments have in common, and the launch.
@@ -1231,13 +1288,13 @@ PromptArgs prompt_args(const csa_kv_cache& cache, const csa_kv_batch& batch,
   return a;
 }
 
-template <bool kShared>
+template <int kMode>
 int launch_prompt(const PromptArgs& a, const csa_kv_cache& cache, cudaStream_t stream,
                   const DeviceInfo& dev, std::string& err) {
   int rc = CSA_OK;
   cudaError_t e;
-  e = cache.head_size <= 64 ? launch_prompt<64, kShared>(a, cache.format, dev, stream, rc, err)
-                            : launch_prompt<128, kShared>(a, cache.format, dev, stream, rc, err);
+  e = cache.head_size <= 64 ? launch_prompt<64, kMode>(a, cache.format, dev, stream, rc, err)
+                            : launch_prompt<128, kMode>(a, cache.format, dev, stream, rc, err);
   if (rc != CSA_OK) return rc;
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) {

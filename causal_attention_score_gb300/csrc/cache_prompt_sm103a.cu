@@ -10,7 +10,7 @@ namespace csa {
 int cache_prompt_launch(const csa_kv_cache& cache, const csa_kv_batch& batch,
                         const AttendCall& call, PromptList* list, cudaStream_t stream,
                         const DeviceInfo& dev, std::string& err) {
-  return launch_prompt<false>(prompt_args(cache, batch, call, list, dev), cache, stream, dev, err);
+  return launch_prompt<kWhole>(prompt_args(cache, batch, call, list, dev), cache, stream, dev, err);
 }
 
 }  // namespace csa

@@ -137,14 +137,14 @@ struct AttendArgs {
   PromptList* list;  // the prompt kernel's, written here
   float* parts;    // [2 * workers][part_floats]
   int part_floats;
-  // kShared: sequences from their first own token on, joined with the shared part; or, with
-  // `prefix`, the shared part itself, the plan's units dealt to the workers in turn.
+  // kShared: sequences from their first own token on, left for the joining; or, with `prefix`,
+  // the shared part, the plan's units dealt to the workers in turn.
   SharedPlan plan;
   int prefix;
 };
 
 // A piece that begins a unit but does not end it: what the join needs.
-enum HeaderWord { kHeadPieces = 0, kHeadRow0, kHeadFirst, kHeadHead, kHeadRows, kHeadSequence };
+enum HeaderWord { kHeadPieces = 0, kHeadRow0, kHeadFirst, kHeadHead, kHeadRows };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -180,31 +180,15 @@ __device__ __forceinline__ void store_out(const AttendArgs& a, long long at, flo
     static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
 }
 
-// Four elements of acc / l (0 where nothing was seen), at a multiple of four.
-__device__ __forceinline__ void store_out4(const AttendArgs& a, long long at, const float4& acc,
-                                           float l) {
-  float v[4] = {acc.x, acc.y, acc.z, acc.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = l == 0.0f ? 0.0f : v[i] / l;
-  uint2 w;
-  if (a.half) {
-    w = make_uint2(half2_of(v[0], v[1]), half2_of(v[2], v[3]));
-  } else {
-    const __nv_bfloat162 x = __floats2bfloat162_rn(v[0], v[1]), y = __floats2bfloat162_rn(v[2], v[3]);
-    w = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
-  }
-  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) = w;
-}
-
 // What a sequence asks for: rows (tokens x group), their tiles of tokens (the
 // first `sink_tiles`, then those from `window_tile` on).
-// kShared: its first token (the first tile begins there), its group, its first row in that; which
-// of the group's pieces a unit of the shared part is.
+// kShared: its first token (the first tile begins there), whose table row names which tokens, its
+// group, its first row in that; which of the group's pieces a unit of the shared part is.
 template <bool kShared>
 struct Shift {};
 template <>
 struct Shift<true> {
-  int start, group, row, part;
+  int start, lead, leader, group, row, part;
 };
 template <bool kShared>
 struct SeqWork : Shift<kShared> {
@@ -219,10 +203,13 @@ __device__ __forceinline__ SeqWork<kShared> seq_work(const AttendArgs& a, int ro
     const SharedSequence p = a.plan.sequences[s];
     w.q = p.q;
     w.start = p.start;
+    w.lead = p.lead;
+    w.leader = p.leader;
     w.group = p.group;
     w.row = p.group < 0 ? 0 : (p.q.row0 - a.plan.groups[p.group].row0) * a.group;
     w.part = 0;
     w.rows = p.q.n * a.group;
+    if (w.rows > row_limit) w.rows = 0;
     w.blocks = (w.rows + 8 * NB - 1) / (8 * NB);
     w.sink_tiles = w.window_tile = 0;
     constexpr int kTokens = kTileTokens<kSub>;
@@ -282,7 +269,7 @@ __device__ __forceinline__ void next_shared_unit(const AttendArgs& a, Piece<true
   const SharedGroup g = a.plan.groups[at];
   const SharedUnit unit = shared_unit(g, a.v.heads, u);
   p.w.q = {g.row0, g.rows, g.tokens, 1 << 30};  // (behind every key)
-  p.w.start = 0;
+  p.w.start = p.w.lead = 0;
   p.w.group = at;
   p.w.row = 0;
   p.w.part = unit.piece;
@@ -409,7 +396,8 @@ __global__ void __launch_bounds__(128 * kGroups<HSP, NB>, 1)
   }
   // (read again wherever it is needed: the main loop needs the registers)
   auto row_limit = [&] {
-    return !kShared && static_cast<long long>(s_blocks) > a.prompt_blocks ? kRowLimit : kNoRowLimit;
+    if constexpr (kShared) return a.plan.head->own.row_limit;
+    return static_cast<long long>(s_blocks) > a.prompt_blocks ? kRowLimit : kNoRowLimit;
   };
   if (!kShared && blockIdx.x == 0 && threadIdx.x == 0) *a.list = PromptList{0u, row_limit()};
   const bool prefix = kShared && a.prefix;
@@ -499,7 +487,9 @@ __global__ void __launch_bounds__(128 * kGroups<HSP, NB>, 1)
       if (!CSA_CHECK(first >= 0 && (first & (a.v.page_tokens - 1)) + 16 * kSub <= a.v.page_tokens,
                      wd, kCheckTile))
         return -1;
-      const int page = kv_page(a.v, p.s, first >> a.v.page_shift);
+      int of = p.s;
+      if constexpr (kShared) of = first < p.w.lead ? p.w.leader : of;
+      const int page = kv_page(a.v, of, first >> a.v.page_shift);
       return page < 0 ? -1 : page * a.v.heads + p.head;
     };
     // Lane (g, t): tokens g and g + 8, chunks t and t + 4 of their K rows; tokens
@@ -882,7 +872,7 @@ __global__ void __launch_bounds__(128 * kGroups<HSP, NB>, 1)
     if (!CSA_CHECK(slot < 2 * kMaxWorkers, wd, kCheckRing)) break;
     float* part = a.parts + static_cast<long long>(slot) * a.part_floats;
     if constexpr (kShared) {
-      // The same by four elements, for what the shared part adds to each.
+      // Left for the joining, four elements at a time.
       const int group = piece.w.group;
       const SharedGroup gr = group < 0 ? SharedGroup{} : a.plan.groups[group];
       for (int e = gtid; e < rows * (HSP / 4); e += 128) {
@@ -903,23 +893,30 @@ __global__ void __launch_bounds__(128 * kGroups<HSP, NB>, 1)
             group < 0 ? 0 : shared_part(gr, a.group, piece.head, piece.w.row + row_first + r);
         if (!CSA_CHECK(at >= 0 && (group < 0 || at + gr.pieces <= a.plan.parts), wd, kCheckTile))
           continue;
+        const int rr = row_first + r, j = rr / a.group;
+        const long long own = static_cast<long long>(row0 + j) * (a.v.heads * a.group) + out_head +
+                              (rr - j * a.group);
         if (prefix) {
           *reinterpret_cast<float4*>(a.plan.o + (at + piece.w.part) * HSP + d) = acc;
           if (d == 0) a.plan.ml[at + piece.w.part] = make_float2(mm, lt);
         } else if (whole) {
-          join_parts<HSP>(a.plan, at, gr.pieces, d, mm, lt, acc);
-          const int rr = row_first + r;
-          const int j = rr / a.group;
-          if (kFull || d < D)
-            store_out4(a,
-                       (row0 + j) * a.out_token + (out_head + (rr - j * a.group)) * a.out_head + d,
-                       acc, lt);
+          *reinterpret_cast<float4*>(a.plan.own_o + own * HSP + d) = acc;
+          if (d == 0) a.plan.own_ml[own] = make_float2(mm, lt);
         } else {
           *reinterpret_cast<float4*>(part + 2 * kMaxRows + r * HSP + d) = acc;
           if (d == 0) {
             part[r] = mm;
             part[kMaxRows + r] = lt;
           }
+        }
+        if (!prefix && begins && d == 0) {
+          // (at most the pieces that there are workers for)
+          const int pieces =
+              whole ? 0
+                    : static_cast<int>(min(1 + (piece.after + share - 1) / share,
+                                           static_cast<long long>(a.workers - worker)));
+          a.plan.own[own] = OwnRow{at, gr.pieces, pieces, worker, r};
+          a.plan.own_there[own] = 1;
         }
       }
     } else {
@@ -950,7 +947,7 @@ __global__ void __launch_bounds__(128 * kGroups<HSP, NB>, 1)
         }
       }
     }
-    if (!prefix && !whole && begins) {
+    if (!kShared && !whole && begins) {
       left_open = true;
       if (gtid == 0) {
         // (at most those there are: lengths may have changed under the call)
@@ -960,19 +957,18 @@ __global__ void __launch_bounds__(128 * kGroups<HSP, NB>, 1)
         header[kHeadFirst] = row_first;
         header[kHeadHead] = piece.head;
         header[kHeadRows] = rows;
-        if constexpr (kShared) header[kHeadSequence] = piece.s;
       }
     }
     group_sync(gi);  // sm is reused
   }
-  if (!prefix && !left_open && gtid == 0) header[kHeadPieces] = 0;
+  if (!kShared && !left_open && gtid == 0) header[kHeadPieces] = 0;
 }
 
 // Joins the pieces of each unit that was split: row blockIdx.y of the unit that the
 // last piece of worker blockIdx.x begins. Piece 0 is that worker's second slot, piece
 // i the first slot of worker + i. Warp w takes pieces w, w + 4, ...; the four sums are
 // added in order.
-template <int HSP, bool kShared>
+template <int HSP>
 __global__ void __launch_bounds__(128) attend_join_sm103a_kernel(const AttendArgs a) {
   __shared__ float s_o[4][HSP];
   __shared__ float s_l[4], s_m[4];
@@ -993,31 +989,8 @@ __global__ void __launch_bounds__(128) attend_join_sm103a_kernel(const AttendArg
     const int slot = i == 0 ? 2 * worker + 1 : 2 * (worker + i);
     return a.parts + static_cast<long long>(slot) * a.part_floats;
   };
-  // (kShared: then the shared part's, in their order)
-  int all = pieces;
-  long long at = 0;
-  if constexpr (kShared) {
-    const SharedSequence q = a.plan.sequences[header[kHeadSequence]];
-    if (q.group >= 0) {
-      const SharedGroup gr = a.plan.groups[q.group];
-      at = shared_part(gr, a.group, header[kHeadHead],
-                       (q.q.row0 - gr.row0) * a.group + header[kHeadFirst] + r);
-      if (!CSA_CHECK(at >= 0 && at + gr.pieces <= a.plan.parts, wd, kCheckTile)) return;
-      all += gr.pieces;
-    }
-  }
-  auto m_of = [&](int i) {
-    return !kShared || i < pieces ? part_of(i)[r] : a.plan.ml[at + i - pieces].x;
-  };
-  auto l_of = [&](int i) {
-    return !kShared || i < pieces ? part_of(i)[kMaxRows + r] : a.plan.ml[at + i - pieces].y;
-  };
-  auto o_of = [&](int i) {
-    return !kShared || i < pieces ? part_of(i) + (2 * kMaxRows + r * HSP)
-                                  : a.plan.o + (at + i - pieces) * HSP;
-  };
   float m = kNothing;
-  for (int i = threadIdx.x; i < all; i += 128) m = fmaxf(m, m_of(i));
+  for (int i = threadIdx.x; i < pieces; i += 128) m = fmaxf(m, part_of(i)[r]);
 #pragma unroll
   for (int d = 1; d < 32; d *= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
   if (lane == 0) s_m[warp] = m;
@@ -1025,12 +998,13 @@ __global__ void __launch_bounds__(128) attend_join_sm103a_kernel(const AttendArg
   m = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
   float acc[E] = {}, l = 0.0f;
 #pragma unroll 4
-  for (int i = warp; i < all; i += 4) {
-    const float* p = o_of(i);
-    const float half = ex2_approx(0.5f * (m_of(i) - m)), c = half * half;
-    l = fmaf(l_of(i) * half, half, l);
+  for (int i = warp; i < pieces; i += 4) {
+    const float* p = part_of(i);
+    const float half = ex2_approx(0.5f * (p[r] - m)), c = half * half;
+    l = fmaf(p[kMaxRows + r] * half, half, l);
 #pragma unroll
-    for (int k = 0; k < E; ++k) acc[k] = fmaf(p[lane * E + k], c, acc[k]);
+    for (int k = 0; k < E; ++k)
+      acc[k] = fmaf(p[2 * kMaxRows + r * HSP + lane * E + k], c, acc[k]);
   }
 #pragma unroll
   for (int k = 0; k < E; ++k) s_o[warp][lane * E + k] = acc[k];
@@ -1057,8 +1031,8 @@ cudaError_t launch_rows(AttendArgs a, int sms, const DeviceInfo& dev, cudaStream
   if (rc != CSA_OK) return cudaSuccess;
   cudaError_t e = launch_programmatic(kernel, static_cast<unsigned>(sms), 128 * kGroups<HSP, NB>, smem,
                                       stream, a);
-  if (e != cudaSuccess || a.prefix) return e;
-  return launch_programmatic(attend_join_sm103a_kernel<HSP, kShared>,
+  if (e != cudaSuccess || kShared) return e;
+  return launch_programmatic(attend_join_sm103a_kernel<HSP>,
                              dim3(static_cast<unsigned>(a.workers),
                                   static_cast<unsigned>(std::min(a.most_rows, 8 * NB))),
                              128, 0, stream, a);

@@ -24,16 +24,27 @@ struct SharedGroup {
   long long part0;    // parts of the groups before
 };
 
-// A sequence as the plan read and checked it.
+// A sequence as the plan read and checked it. Its tokens below `lead` are looked up in sequence
+// `leader`'s table row; those below `start` are the shared part's (start is 0 or lead).
 struct SharedSequence {
   KvSequence q;
-  int start;  // its first token that is not shared
-  int group;  // -1: none, or none with shared tokens
+  int start, lead, leader;
+  int group;  // -1: none, or one whose shared part is not worth a unit of its own
+};
+
+// What the kernels of the own parts leave for one row and head, beside its maximum, sum and output:
+// where the rest of it is.
+struct OwnRow {
+  long long at;        // of its shared parts, the first
+  int shared;          // how many
+  int pieces, worker;  // an own part in pieces, the first by this worker (0: whole, below)
+  int row;             // of that piece's rows
 };
 
 struct SharedHead {
-  int units;
-  PromptList list;  // of the tcgen05 form
+  int units;          // of the shared part
+  PromptList shared;  // those taken
+  PromptList own;     // of the own parts: sequences of more than row_limit rows are its kernel's
 };
 
 // What a unit leaves for each of its rows: the running maximum, the sum and the output. Row rr
@@ -46,6 +57,11 @@ struct SharedPlan {
   float* o;     // [parts][padded head size]
   int group_count;
   long long parts;  // that there is room for
+  // by row and query head:
+  int* own_there;   // 0: no row of a sequence
+  OwnRow* own;
+  float2* own_ml;
+  float* own_o;     // [..][padded head size]
 };
 
 __device__ __forceinline__ long long shared_part(const SharedGroup& g, int group_heads, int head,
@@ -82,37 +98,10 @@ __device__ __forceinline__ SharedUnit shared_unit(const SharedGroup& g, int head
   return r;
 }
 
-// Joins the n parts from `at` on to (m, l, acc), four elements from d on of a row.
-template <int HSP>
-__device__ __forceinline__ void join_parts(const SharedPlan& plan, long long at, int n, int d,
-                                           float m, float& l, float4& acc) {
-  float top = m;
-#pragma unroll 8
-  for (int i = 0; i < n; ++i) top = fmaxf(top, plan.ml[at + i].x);
-  // (in two factors, neither of which comes out as 0, for the sum)
-  float half = ex2_approx(0.5f * (m - top)), c = half * half;
-  l = l * half * half;
-  acc.x *= c;
-  acc.y *= c;
-  acc.z *= c;
-  acc.w *= c;
-#pragma unroll 8
-  for (int i = 0; i < n; ++i) {
-    const float2 x = plan.ml[at + i];
-    const float4 o = *reinterpret_cast<const float4*>(plan.o + (at + i) * HSP + d);
-    half = ex2_approx(0.5f * (x.x - top));
-    c = half * half;
-    l = fmaf(x.y * half, half, l);
-    acc.x = fmaf(o.x, c, acc.x);
-    acc.y = fmaf(o.y, c, acc.y);
-    acc.z = fmaf(o.z, c, acc.z);
-    acc.w = fmaf(o.w, c, acc.w);
-  }
-}
-
-// The tcgen05 kernel over the shared tokens (cache_prefix_sm103a.cu).
+// The tcgen05 kernel over the shared tokens, and over the own parts of sequences with many rows
+// (cache_prefix_sm103a.cu).
 int cache_prefix_launch(const csa_kv_cache& cache, const csa_kv_batch& batch,
-                        const AttendCall& call, const SharedPlan& plan, cudaStream_t stream,
-                        const DeviceInfo& dev, std::string& err);
+                        const AttendCall& call, const SharedPlan& plan, bool own,
+                        cudaStream_t stream, const DeviceInfo& dev, std::string& err);
 
 }  // namespace csa

@@ -9,10 +9,10 @@
 // a running maximum m, l = sum exp(x - m) and O = sum exp(x - m) v in fp32, joined by
 // O exp(m - M), l exp(m - M).
 //
-// Four launches: a plan (one CTA: the batch's entries read and checked once, units of the shared
-// part and where their results go), the shared part, the own parts, and the joining of own parts
-// that were split. The shared part is cut along its tokens too, as far as SMs are left without
-// work; a row of an own part that no split touches takes its shared parts in as it is finished.
+// Launches: a plan (the batch's entries read and checked once, units of the shared part and where
+// their results go), the shared part, the own parts (and those of sequences with many rows, where
+// there may be any, on tcgen05), and the joining, a warp for each row and head. The shared part is
+// cut along its tokens too, as far as SMs are left without work.
 //
 // The shared part goes to the tcgen05 kernel (256 rows x 64 keys a step; its units here have no
 // masks) where the groups have rows enough, to the kernel of few rows otherwise.
@@ -22,6 +22,7 @@
 #include <climits>
 #include <cstdint>
 #include <string>
+#include <type_traits>
 
 #include "cache_rows.cuh"
 #include "cache_shared.cuh"
@@ -34,6 +35,9 @@ constexpr int kPlanThreads = 1024;
 // From this many rows a group on average (tokens x query heads of a kv head) the shared part is
 // the tcgen05 kernel's.
 constexpr int kPrefixFrom = 33;
+// Below so many bytes of codes that it would keep from being read again (by all SMs), the shared
+// part is not worth its launches: sequences read it for themselves.
+constexpr long long kWorthBytes = 32LL << 20;
 // Room for parts beyond one for each row and head: what cutting along the tokens may take.
 constexpr long long kSpareParts = 2LL * kMaxSms * kPrefixRows;
 
@@ -42,53 +46,39 @@ struct PlanArgs {
   const int* groups;  // [group_count + 1]
   const int* shared;  // [group_count]
   SharedPlan plan;
+  long long rows_heads;  // rows of own_there
   int group_heads;
   int unit_rows, tile;  // of the shared part's kernel
   int workers;          // what works on a unit at a time
   int start;            // what a unit costs beyond its tiles, in tiles
+  long long worth;      // keys, over all kv heads, whose reading the shared part has to save
+  long long prompt_blocks;  // as in AttendArgs
 };
 
-// Sum over the CTA and each thread's share of it before it, for a run of values a thread each.
-struct Sums {
-  long long warp[kPlanThreads / 32];
-  __device__ long long before(long long mine, long long& total) {
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    long long up = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d *= 2) {
-      const long long x = __shfl_up_sync(0xFFFFFFFFu, up, d);
-      if (lane >= d) up += x;
-    }
-    __syncthreads();
-    if (lane == 31) warp[w] = up;
-    __syncthreads();
-    long long at = up - mine;
-    total = 0;
-    for (int i = 0; i < kPlanThreads / 32; ++i) {
-      if (i < w) at += warp[i];
-      total += warp[i];
-    }
-    return at;
-  }
-};
-
+// CTA 0 plans, the others clear the marks of the rows.
 __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_sm103a_kernel(const PlanArgs a) {
-  __shared__ Sums sums;
-  __shared__ int s_bad, s_most;
-  __shared__ unsigned long long s_best;
-  __shared__ int s_chunk;
+  __shared__ int s_bad, s_most, s_chunk;
+  __shared__ unsigned long long s_saved, s_blocks, s_key[kPlanThreads / 32];
   const KvView& v = a.v;
   const SharedPlan& plan = a.plan;
-  const int tid = threadIdx.x, G = plan.group_count, S = v.sequences;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = plan.group_count,
+            S = v.sequences;
   grid_dependency_wait();
-  if (tid == 0) s_bad = s_most = 0, s_best = ~0ull;
+  if (blockIdx.x > 0) {
+    const long long n = (a.rows_heads + 3) / 4;
+    for (long long i = (blockIdx.x - 1) * static_cast<long long>(kPlanThreads) + tid; i < n;
+         i += static_cast<long long>(gridDim.x - 1) * kPlanThreads)
+      reinterpret_cast<int4*>(plan.own_there)[i] = make_int4(0, 0, 0, 0);
+    return;
+  }
+  if (tid == 0) s_bad = s_most = 0, s_saved = s_blocks = 0;
   __syncthreads();
 
   // The groups: bounds in order, whole pages.
   for (int g = tid; g < G; g += kPlanThreads) {
     const int from = a.groups[g], to = a.groups[g + 1], tokens = a.shared[g];
     if (from < 0 || to < from || to > S) s_bad = 1;
-    const bool ok = tokens >= 0 && tokens % v.page_tokens == 0 &&
+    const bool ok = tokens >= 0 && (tokens & (v.page_tokens - 1)) == 0 &&
                     tokens <= static_cast<long long>(v.table_width) * v.page_tokens;
     SharedGroup p{};
     p.sequence = from;
@@ -112,98 +102,218 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_sm103a_kernel(con
       if (plan.groups[mid].sequence <= s) lo = mid;
       else hi = mid;
     }
-    if (lo >= 0 && s < plan.groups[lo].rows && r.q.n > 0) {
-      const int tokens = plan.groups[lo].tokens;
-      if (tokens < 0 || (tokens > 0 && r.q.first < tokens)) {
-        report_index(v.status, tokens < 0 ? kIndexLength : kIndexRows);
-        r.q.n = 0;
-      } else if (tokens > 0) {
-        r.group = lo;
-        r.start = tokens;
+    if (lo >= 0 && r.q.n > 0) {
+      const SharedGroup p = plan.groups[lo];
+      if (s < p.rows) {
+        if (p.tokens < 0 || (p.tokens > 0 && r.q.first < p.tokens)) {
+          report_index(v.status, p.tokens < 0 ? kIndexLength : kIndexRows);
+          r.q.n = 0;
+        } else if (p.tokens > 0) {
+          r.group = lo;
+          r.lead = p.tokens;
+          r.leader = p.sequence;
+        }
       }
     }
+    const long long rows = static_cast<long long>(r.q.n) * a.group_heads;
+    if (a.prompt_blocks > 0 && rows > kRowLimit)
+      atomicAdd(&s_blocks, static_cast<unsigned long long>((rows + 15) / 16 * v.heads));
     plan.sequences[s] = r;
   }
   __syncthreads();
 
-  // The groups' rows: from the first to the last of their sequences that have any.
-  for (int g = tid >> 5; g < G; g += kPlanThreads / 32) {
+  // The groups' rows: from the first to the last of their sequences that have any; and what a
+  // shared part saves: all of their sequences but one would read its tokens again.
+  for (int g = warp; g < G; g += kPlanThreads / 32) {
     SharedGroup p = plan.groups[g];
     // (bounds out of order may be any numbers)
     const int from = bad ? 0 : p.sequence, to = bad ? 0 : p.rows;
-    int row0 = INT_MAX, end = 0;
-    for (int s = from + (tid & 31); s < to; s += 32) {
+    int row0 = INT_MAX, end = 0, members = 0;
+    for (int s = from + lane; s < to; s += 32) {
       const SharedSequence q = plan.sequences[s];
       if (q.group == g) {
         row0 = min(row0, q.q.row0);
         end = max(end, q.q.row0 + q.q.n);
+        ++members;
       }
     }
     __syncwarp();
     row0 = __reduce_min_sync(0xFFFFFFFFu, row0);
     end = __reduce_max_sync(0xFFFFFFFFu, end);
+    members = __reduce_add_sync(0xFFFFFFFFu, members);
     p.row0 = p.rows = p.tiles = p.blocks = p.pieces = 0;
     if (row0 < end) {
       p.row0 = row0;
       p.rows = end - row0;
       p.tiles = (p.tokens + a.tile - 1) / a.tile;
       p.blocks = (p.rows * a.group_heads + a.unit_rows - 1) / a.unit_rows;
-      if ((tid & 31) == 0) atomicMax(&s_most, p.tiles);
+      if (lane == 0) {
+        atomicMax(&s_most, p.tiles);
+        atomicAdd(&s_saved, static_cast<unsigned long long>(members - 1) * p.tokens);
+      }
     }
-    if ((tid & 31) == 0) plan.groups[g] = p;
+    if (lane == 0) plan.groups[g] = p;
     __syncwarp();
   }
   __syncthreads();
+  const bool worth = static_cast<long long>(s_saved) * v.heads >= a.worth;
 
   // The longest run of tiles of a unit: the longest group's cut into 1, 2, ... 1024 pieces, that
   // which takes the least time as rounds of equal units, and room.
+  const int mine = max((s_most + tid) / (tid + 1), 1);
   {
-    const int chunk = max((s_most + tid) / (tid + 1), 1);
     long long units = 0, parts = 0;
-    for (int g = 0; g < G; ++g) {
+    for (int g = 0; g < G && worth; ++g) {
       const SharedGroup p = plan.groups[g];
-      const long long pieces = (p.tiles + chunk - 1) / chunk;
+      const long long pieces = (p.tiles + mine - 1) / mine;
       units += pieces * p.blocks * v.heads;
       parts += pieces * p.rows * a.group_heads * v.heads;
     }
-    const unsigned long long rounds = (units + a.workers - 1) / a.workers;
-    const unsigned long long cost =
-        parts <= plan.parts ? min(rounds * (chunk + a.start), 1ull << 50) : 1ull << 51;
+    const float rounds = ceilf(static_cast<float>(units) / static_cast<float>(a.workers));
+    const float cost = parts <= plan.parts ? rounds * static_cast<float>(mine + a.start) : INFINITY;
     // (of equal ones the fewest pieces)
-    atomicMin(&s_best, cost << 11 | static_cast<unsigned long long>(tid));
+    unsigned long long key =
+        static_cast<unsigned long long>(__float_as_uint(cost)) << 32 | static_cast<unsigned>(tid);
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) key = min(key, __shfl_xor_sync(0xFFFFFFFFu, key, d));
+    if (lane == 0) s_key[warp] = key;
     __syncthreads();
-    if (tid == static_cast<int>(s_best & 2047)) s_chunk = chunk;
+    key = s_key[lane];
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) key = min(key, __shfl_xor_sync(0xFFFFFFFFu, key, d));
+    if (tid == static_cast<int>(key & 0xFFFFFFFFu)) s_chunk = mine;
     __syncthreads();
   }
-  const int chunk = s_chunk;
-  long long units_before = 0, parts_before = 0;
-  for (int g0 = 0; g0 < G; g0 += kPlanThreads) {
-    const int g = g0 + tid;
-    SharedGroup p{};
-    if (g < G) {
-      p = plan.groups[g];
-      p.pieces = (p.tiles + chunk - 1) / chunk;
+  if (warp == 0) {
+    const int chunk = s_chunk;
+    long long units_before = 0, parts_before = 0;
+    for (int g0 = 0; g0 < G; g0 += 32) {
+      const int g = g0 + lane;
+      SharedGroup p{};
+      if (g < G) p = plan.groups[g];
+      p.pieces = worth ? (p.tiles + chunk - 1) / chunk : 0;
+      long long units = static_cast<long long>(p.pieces) * p.blocks * v.heads;
+      long long parts = static_cast<long long>(p.pieces) * p.rows * a.group_heads * v.heads;
+      const long long my_units = units, my_parts = parts;
+#pragma unroll
+      for (int d = 1; d < 32; d *= 2) {
+        const long long u = __shfl_up_sync(0xFFFFFFFFu, units, d);
+        const long long q = __shfl_up_sync(0xFFFFFFFFu, parts, d);
+        if (lane >= d) units += u, parts += q;
+      }
+      p.unit0 = static_cast<int>(min(units_before + units - my_units, 0x7FFFFFFFll));
+      p.part0 = parts_before + parts - my_parts;
+      if (g < G) plan.groups[g] = p;
+      units_before += __shfl_sync(0xFFFFFFFFu, units, 31);
+      parts_before += __shfl_sync(0xFFFFFFFFu, parts, 31);
     }
-    long long units = 0, parts = 0;
-    const long long mine = static_cast<long long>(p.pieces) * p.blocks * v.heads;
-    const long long room = static_cast<long long>(p.pieces) * p.rows * a.group_heads * v.heads;
-    p.unit0 = static_cast<int>(units_before + sums.before(mine, units));
-    p.part0 = parts_before + sums.before(room, parts);
-    units_before += units;
-    parts_before += parts;
-    if (g < G) plan.groups[g] = p;
-  }
-  if (tid == 0) {
-    // (more than there is room for only where rows are in several sequences: nothing is computed)
-    const bool room = parts_before <= plan.parts && units_before <= INT_MAX;
-    plan.head->units = room ? static_cast<int>(units_before) : 0;
-    plan.head->list = PromptList{0u, 0};
-    if (!room) report_index(v.status, kIndexRows);
-    s_bad = room ? 0 : 1;
+    if (lane == 0) {
+      // (more than there is room for only where rows are in several sequences: nothing is computed)
+      const bool room = parts_before <= plan.parts && units_before <= INT_MAX;
+      plan.head->units = room ? static_cast<int>(units_before) : 0;
+      plan.head->shared = PromptList{0u, 0};
+      plan.head->own = PromptList{
+          0u, static_cast<long long>(s_blocks) > a.prompt_blocks ? kRowLimit : kNoRowLimit};
+      if (!room) report_index(v.status, kIndexRows);
+      s_bad = room ? 0 : 1;
+    }
+    __syncwarp();
   }
   __syncthreads();
-  if (s_bad)
-    for (int s = tid; s < S; s += kPlanThreads) plan.sequences[s].q.n = 0;
+  for (int s = tid; s < S; s += kPlanThreads) {
+    SharedSequence& r = plan.sequences[s];
+    if (r.group >= 0) {
+      if (worth) r.start = r.lead;
+      else r.group = -1;
+    }
+    if (s_bad) r.q.n = 0;
+  }
+}
+
+// A warp a row and head: its own part, whole or in pieces, and its shared ones, in a fixed order.
+template <int HSP>
+__global__ void __launch_bounds__(128) shared_join_sm103a_kernel(const AttendArgs a, int q_heads) {
+  grid_dependency_wait();
+  constexpr int V = HSP / 32;
+  using Vec = typename std::conditional<V == 4, float4, float2>::type;
+  const int lane = threadIdx.x & 31;
+  const long long all = static_cast<long long>(a.v.rows) * q_heads;
+  [[maybe_unused]] __shared__ int s_abort;
+  [[maybe_unused]] const Watchdog wd{0, a.v.status, &s_abort};
+  for (long long i = blockIdx.x * 4ll + (threadIdx.x >> 5); i < all; i += gridDim.x * 4ll) {
+    if (a.plan.own_there[i] == 0) continue;
+    const OwnRow w = a.plan.own[i];
+    const int first = max(w.pieces, 1), n = first + w.shared;
+    if (!CSA_CHECK(w.pieces >= 0 && w.shared >= 0 && w.at >= 0 &&
+                       w.at + w.shared <= a.plan.parts && w.row >= 0 && w.row < kMaxRows &&
+                       w.worker >= 0 && w.worker + w.pieces <= kMaxWorkers,
+                   wd, kCheckRing))
+      continue;
+    // Piece p's maximum, sum and output.
+    auto piece = [&](int p, float& m, float& l) -> const float* {
+      if (p < first && w.pieces > 0) {
+        const int slot = p == 0 ? 2 * w.worker + 1 : 2 * (w.worker + p);
+        const float* part = a.parts + static_cast<long long>(slot) * a.part_floats;
+        m = part[w.row];
+        l = part[kMaxRows + w.row];
+        return part + 2 * kMaxRows + w.row * HSP;
+      }
+      const long long at = p < first ? i : w.at + p - first;
+      const float2 x = p < first ? a.plan.own_ml[at] : a.plan.ml[at];
+      m = x.x;
+      l = x.y;
+      return (p < first ? a.plan.own_o : a.plan.o) + at * HSP;
+    };
+    float top = kNothing;
+    for (int p0 = 0; p0 < n; p0 += 32) {
+      float m = kNothing, l;
+      if (p0 + lane < n) piece(p0 + lane, m, l);
+      top = fmaxf(top, m);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+    float acc[V] = {}, sum = 0.0f;
+    for (int p0 = 0; p0 < n; p0 += 32) {
+      float m = kNothing, l = 0.0f;
+      const float* o = nullptr;
+      if (p0 + lane < n) o = piece(p0 + lane, m, l);
+      __syncwarp();
+      // (in two factors, neither of which comes out as 0, for the sum)
+      const float half = ex2_approx(0.5f * (m - top)), c = half * half;
+      sum = fmaf(l * half, half, sum);
+      const int here = min(n - p0, 32);
+#pragma unroll 8
+      for (int p = 0; p < here; ++p) {
+        const float cp = __shfl_sync(0xFFFFFFFFu, c, p);
+        const float* from = reinterpret_cast<const float*>(
+            __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(o), p));
+        const Vec x = reinterpret_cast<const Vec*>(from)[lane];
+        const float* v = reinterpret_cast<const float*>(&x);
+#pragma unroll
+        for (int k = 0; k < V; ++k) acc[k] = fmaf(v[k], cp, acc[k]);
+      }
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+    const int row = static_cast<int>(i / q_heads), head = static_cast<int>(i - static_cast<long long>(row) * q_heads);
+    uint32_t y[V / 2];
+#pragma unroll
+    for (int k = 0; k < V; k += 2) {
+      const float v0 = sum == 0.0f ? 0.0f : acc[k] / sum, v1 = sum == 0.0f ? 0.0f : acc[k + 1] / sum;
+      if (a.half) {
+        y[k / 2] = half2_of(v0, v1);
+      } else {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v0, v1);
+        y[k / 2] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+    }
+    if (lane * V < a.v.head_size) {
+      uint16_t* to = static_cast<uint16_t*>(a.out) + row * a.out_token + head * a.out_head + lane * V;
+      if constexpr (V == 4) *reinterpret_cast<uint2*>(to) = make_uint2(y[0], y[1]);
+      else *reinterpret_cast<uint32_t*>(to) = y[0];
+    }
+  }
 }
 
 size_t up16(size_t n) { return (n + 15) / 16 * 16; }
@@ -224,8 +334,12 @@ size_t lay_out(int head_size, long long rows_heads, int sequences, int groups, c
   plan.sequences =
       reinterpret_cast<SharedSequence*>(take(static_cast<size_t>(sequences) * sizeof(SharedSequence)));
   plan.ml = reinterpret_cast<float2*>(take(static_cast<size_t>(plan.parts) * sizeof(float2)));
-  plan.o = reinterpret_cast<float*>(
-      take(static_cast<size_t>(plan.parts) * padded_head(head_size) * sizeof(float)));
+  const size_t row = static_cast<size_t>(padded_head(head_size)) * sizeof(float);
+  plan.o = reinterpret_cast<float*>(take(static_cast<size_t>(plan.parts) * row));
+  plan.own_there = reinterpret_cast<int*>(take(static_cast<size_t>(rows_heads) * sizeof(int)));
+  plan.own = reinterpret_cast<OwnRow*>(take(static_cast<size_t>(rows_heads) * sizeof(OwnRow)));
+  plan.own_ml = reinterpret_cast<float2*>(take(static_cast<size_t>(rows_heads) * sizeof(float2)));
+  plan.own_o = reinterpret_cast<float*>(take(static_cast<size_t>(rows_heads) * row));
   return at;
 }
 
@@ -242,20 +356,35 @@ int cache_attention_shared_launch(const csa_kv_cache& cache, const csa_kv_batch&
                                   int group_count, cudaStream_t stream, const DeviceInfo& dev,
                                   std::string& err) {
   AttendArgs a = rows_args(cache, batch, call, call.workspace, dev);
-  lay_out(cache.head_size, static_cast<long long>(batch.rows) * call.q_heads, batch.sequences,
-          group_count, static_cast<char*>(call.workspace), a.plan);
+  const long long rows_heads = static_cast<long long>(batch.rows) * call.q_heads;
+  lay_out(cache.head_size, rows_heads, batch.sequences, group_count,
+          static_cast<char*>(call.workspace), a.plan);
   const int sms = std::min(dev.sm_count, kMaxSms);
   const long long batch_rows = static_cast<long long>(batch.rows) * a.group;
   const bool prefix_tc = batch_rows >= static_cast<long long>(kPrefixFrom) * group_count;
   const bool prefix_eight = batch_rows <= 8LL * group_count;
   const int hsp = padded_head(cache.head_size), sub = cache.page_tokens < 32 ? 1 : 2;
+  // (rows a block of the own parts, and whether some may be prompts': see cache_attention_launch)
+  const long long most_rows = static_cast<long long>(batch.max_new) * a.group;
+  a.prompt_blocks = static_cast<long long>(kBlocksPerSm) * sms;
+  const long long sequences = std::min<long long>(batch.sequences, batch_rows / (kRowLimit + 1));
+  const bool prompts = most_rows > kRowLimit &&
+                       (batch_rows / 16 + sequences) * cache.heads > a.prompt_blocks;
+  if (!prompts) a.prompt_blocks = 0;
+  const bool eight =
+      most_rows <= 8 || (a.group <= 8 && (prompts || batch_rows <= 8LL * batch.sequences));
 
   PlanArgs p;
   p.v = a.v;
   p.groups = groups;
   p.shared = shared;
   p.plan = a.plan;
+  p.rows_heads = rows_heads;
   p.group_heads = a.group;
+  p.worth = shared_part_mode() == CSA_SHARED_ALWAYS
+                ? 0
+                : kWorthBytes * sms / kMaxSms / (2 * cache.head_size);
+  p.prompt_blocks = a.prompt_blocks;
   if (prefix_tc) {
     p.unit_rows = kPrefixRows;
     p.tile = kPrefixTile;
@@ -268,22 +397,31 @@ int cache_attention_shared_launch(const csa_kv_cache& cache, const csa_kv_batch&
                                  : (prefix_eight ? kGroups<128, 1> : kGroups<128, 2>));
     p.start = (prefix_eight ? 2 : 3) * (2 / sub);
   }
-  cudaError_t e = launch_programmatic(shared_plan_sm103a_kernel, dim3(1), kPlanThreads, 0, stream, p);
+  const unsigned clear =
+      static_cast<unsigned>(std::min<long long>((rows_heads / 4 + kPlanThreads) / kPlanThreads, sms));
+  cudaError_t e = launch_programmatic(shared_plan_sm103a_kernel, dim3(1 + clear), kPlanThreads, 0,
+                                      stream, p);
   int rc = CSA_OK;
   if (e == cudaSuccess) {
     if (prefix_tc) {
-      rc = cache_prefix_launch(cache, batch, call, a.plan, stream, dev, err);
+      rc = cache_prefix_launch(cache, batch, call, a.plan, false, stream, dev, err);
     } else {
       a.prefix = 1;
       e = launch_rows<true>(a, prefix_eight, cache.format, sms, dev, stream, rc, err);
       a.prefix = 0;
     }
   }
-  // (rows a block: see cache_attention_launch)
-  const long long most_rows = static_cast<long long>(batch.max_new) * a.group;
-  const bool eight = most_rows <= 8 || (a.group <= 8 && batch_rows <= 8LL * batch.sequences);
   if (e == cudaSuccess && rc == CSA_OK)
     e = launch_rows<true>(a, eight, cache.format, sms, dev, stream, rc, err);
+  if (e == cudaSuccess && rc == CSA_OK && prompts)
+    rc = cache_prefix_launch(cache, batch, call, a.plan, true, stream, dev, err);
+  if (e == cudaSuccess && rc == CSA_OK) {
+    const unsigned grid = static_cast<unsigned>(std::min<long long>((rows_heads + 3) / 4, 16LL * sms));
+    e = hsp == 64 ? launch_programmatic(shared_join_sm103a_kernel<64>, dim3(grid), 128, 0, stream, a,
+                                        call.q_heads)
+                  : launch_programmatic(shared_join_sm103a_kernel<128>, dim3(grid), 128, 0, stream, a,
+                                        call.q_heads);
+  }
   if (rc != CSA_OK) {
     err = "cache_attention_shared_forward: " + err;
     return rc;

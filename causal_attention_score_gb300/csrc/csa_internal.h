@@ -114,6 +114,8 @@ uint64_t wait_limit_ns();
 bool take_inject();
 // The dense layer's fetch mode set by csa_set_dense_fetch (CSA_DENSE_FETCH_*).
 int dense_fetch_mode();
+// When attention works its shared part out apart, as csa_set_shared_part says (CSA_SHARED_*).
+int shared_part_mode();
 
 // Kernel launchers; each validates what is specific to its kernel.
 // `counters`: work-list counter pair to use instead of the library's per-launch

@@ -349,6 +349,16 @@ def cache_attention_forward(out: torch.Tensor, q: torch.Tensor, cache: KvCache, 
         _lib.check(rc, "cache_attention_forward")
 
 
+SHARED_AUTO, SHARED_ALWAYS = 0, 1
+
+
+def set_shared_part(mode: int) -> None:
+    """Whether later calls of cache_attention_shared_forward work out what sequences share apart
+    where that saves time (SHARED_AUTO) or always (SHARED_ALWAYS); see csa_set_shared_part in
+    include/csa.h."""
+    _lib.check(_lib.load().csa_set_shared_part(mode), "csa_set_shared_part")
+
+
 def cache_attention_shared_workspace_size(cache: KvCache, batch: KvBatch, q_heads: int,
                                           groups: int) -> int:
     """Bytes of workspace ``cache_attention_shared_forward`` needs for batches of up to this one's

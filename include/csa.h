@@ -577,7 +577,15 @@ csa_status cache_attention_workspace_size(const csa_kv_cache* cache, int q_heads
  *
  * cache_attention_shared_workspace_size -- bytes of workspace it needs for batches of up to this
  * many rows, sequences and groups, into *bytes. Host only.
+ *
+ * csa_set_shared_part -- process-wide, for later calls: whether what sequences share is worked out
+ * apart where that saves time (CSA_SHARED_AUTO: decided on the device, from the lengths; elsewhere
+ * each sequence reads it for itself) or always (CSA_SHARED_ALWAYS). The function is the same, sums
+ * are taken in another order. CSA_ERR_SHAPE for an unknown mode (the mode is unchanged).
  */
+#define CSA_SHARED_AUTO   0
+#define CSA_SHARED_ALWAYS 1
+csa_status csa_set_shared_part(int mode);
 csa_status cache_attention_shared_workspace_size(const csa_kv_cache* cache, int q_heads, int rows,
                                                  int sequences, int group_count, size_t* bytes);
 csa_status cache_attention_shared_forward(void* out, const void* q, int dtype, int q_heads,

@@ -71,3 +71,9 @@ def test_workspace_size(lib):
     assert size(4, 1 << 29, 1, 1) == (UN, 0)
     small = size(4, 1, 1, 1)[1]
     assert 0 < small < size(4, 1000, 1, 1)[1] and small < size(4, 1, 1000, 1)[1] and small < size(4, 1, 1, 1000)[1]
+
+
+def test_modes_of_the_shared_part(lib):
+    for mode in (-1, 2):
+        assert lib.csa_set_shared_part(mode) == SH
+    assert lib.csa_set_shared_part(1) == 0 and lib.csa_set_shared_part(0) == 0

@@ -9,14 +9,17 @@ import shared_ref as ref
 pytestmark = pytest.mark.gpu
 
 
-@pytest.fixture(autouse=True, params=[0, 2], ids=["all_sms", "2_sms"])
+@pytest.fixture(autouse=True, params=[(0, csa.SHARED_ALWAYS), (2, csa.SHARED_ALWAYS), (0, csa.SHARED_AUTO)],
+                ids=["all_sms", "2_sms", "where_it_pays"])
 def sms(request):
     """On the whole GPU, where the shared part is cut into many pieces, and held to two SMs, where
-    every worker has many units."""
+    every worker has many units; and as short a shared part as here is left to the sequences."""
     stream = torch.cuda.current_stream()
-    csa.set_stream_sm_limit(stream, request.param)
+    csa.set_stream_sm_limit(stream, request.param[0])
+    csa.set_shared_part(request.param[1])
     yield request.param
     torch.cuda.synchronize()
+    csa.set_shared_part(csa.SHARED_AUTO)
     csa.set_stream_sm_limit(stream, 0)
 
 
@@ -263,7 +266,8 @@ def test_a_wait_that_runs_out_is_reported(sms):
         csa.set_wait_limit_ns(3_000_000)
         csa.debug_inject(True)
         csa.cache_attention_shared_forward(out, q.cuda(), cache, batch, *b.lists())
-        assert csa.get_status() == csa.CSA_ERR_TIMEOUT
+        # (a shared part left to the sequences has no such wait)
+        assert csa.get_status() == (csa.CSA_ERR_TIMEOUT if sms[1] == csa.SHARED_ALWAYS else 0)
     finally:
         csa.set_wait_limit_ns(0)
         csa.debug_inject(False)
@@ -277,6 +281,44 @@ def test_same_bits_every_time():
     for _ in range(5):
         _, got = run(b, 8, torch.bfloat16)
         assert torch.equal(got, want)
+
+
+def test_many_sequences_and_groups_share_where_it_pays(sms):
+    """As many as the plan's threads take in several rounds; one long shared part among short ones."""
+    S, G = 1300, 60
+    bounds = [S * g // G for g in range(G + 1)]
+    groups = [(bounds[g], bounds[g + 1], 16 * (g % 4)) for g in range(G)]
+    b = ref.SharedBatch([1] * S, [i % 3 for i in range(S)], groups, 1, 16, 16, "int8", seed=14)
+    q, out = run(b, 2, torch.bfloat16)
+    check(b, q, out)
+
+
+@pytest.mark.parametrize("many", [False, True])
+def test_long_shared_parts(many, sms):
+    """Long enough to be worked out apart of itself, against cache_attention_forward's result. Each of
+    the two is off by serving_ref.attention's bound, (2 d + 2^-11) sum p|v| + N 2^-25 max|v| with
+    d = (D + 8) 2^-24 max sum |q||k| scale + 2^-16 + N 2^-24, and a rounding to bf16; sum p|v| is the
+    latter call's over |v|, which is off by its own rounding and bound (less than a tenth)."""
+    n, heads = (40, 4) if many else (4, 2)
+    b = ref.SharedBatch([1] * n, [(i * 11) % 70 for i in range(n)], [(0, n, 20000 // 64 * 64)], 4, 64, 64, "int8", seed=15)
+    q, out = run(b, 4 * heads, torch.bfloat16)
+    cache, batch = b.device_whole(csa)
+    whole, spread = torch.full_like(out, 7.0), torch.full_like(out, 7.0)
+    csa.cache_attention_forward(whole, q.cuda(), cache, batch)
+    positive = csa.KvCache(cache.k, cache.v.clamp(min=-127).abs(), cache.k_scale, cache.v_scale)
+    csa.cache_attention_forward(spread, q.cuda(), positive, batch)
+    assert csa.get_status() == 0
+    N = max(b.lengths)
+    (kc, ks), (vc, vs) = b.values("k"), b.values("v")
+    live = b.live.any(1)
+    k = (kc.abs() * ks[..., None, None])[live].cuda()       # [pages, Hkv, P, D]
+    x = q.double().abs().cuda().view(n, 4, heads, 64)
+    A = max(float(torch.einsum("nhgd,hpd->nhgp", x, k[i].double()).max()) for i in range(len(k))) / 8
+    d = 72 * 2.0 ** -24 * A + 2.0 ** -16 + N * 2.0 ** -24
+    most = float((vc.abs() * vs[..., None, None])[live].max())
+    one = (2 * d + 2.0 ** -11) * 1.1 * spread.double() + N * 2.0 ** -25 * most
+    room = 2 * one * (1 + 2.0 ** -8) + 2.0 ** -8 * (out.double().abs() + whole.double().abs())
+    assert bool(((out.double() - whole.double()).abs() <= room).all())
 
 
 def test_workspace_that_is_too_small_or_misplaced():
