@@ -505,6 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before_sync();
   }
   grid_dependency_wait();
+  if constexpr (kMode == kSharedPart) grid_dependents_launch();  // (the own parts, beside this)
 
   // The work list: thread i counts the units of sequences [i per, (i + 1) per).
   const int S = a.v.sequences, row_limit = kMode == kSharedPart ? 0 : a.list->row_limit;
@@ -549,7 +550,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, ld_shared_b32(tmem_slot), 0);
-  const long long total = kMode == kSharedPart ? a.plan.head->units : s_prefix[kThreads];
+  const long long total =
+      kMode != kSharedPart ? s_prefix[kThreads]
+      : static_cast<int>(blockIdx.x) < a.plan.head->shared_sms ? a.plan.head->units : 0;
   // The k-th unit that this CTA works on, for a whole warp; false: a wait ran out.
   auto take_unit = [&](uint32_t k, Unit& u) {
     const uint32_t slot = k % kUnitSlots;
@@ -1106,7 +1109,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint32_t k = 0;; ++k) {
         const uint32_t slot = k % kUnitSlots;
         if (!mbar_wait(u_want, k & 1u, wd, kSiteSched)) break;
-        const long long at = atomicAdd(&a.list->taken, 1u);
+        const long long at =
+            kMode == kSharedPart && total == 0 ? 0 : atomicAdd(&a.list->taken, 1u);
         Unit u;
         if (at >= total) u.n[0] = -1;
         else if constexpr (kMode == kSharedPart) u = decode_shared(a, static_cast<int>(at));

@@ -141,6 +141,7 @@ struct AttendArgs {
   // the shared part, the plan's units dealt to the workers in turn.
   SharedPlan plan;
   int prefix;
+  int beside;  // (own parts) the shared part runs at the same time: its end is waited for last
 };
 
 // A piece that begins a unit but does not end it: what the join needs.
@@ -264,7 +265,7 @@ __device__ __forceinline__ void next_shared_unit(const AttendArgs& a, Piece<true
   p.count = 0;
   if (p.at >= p.end) return;
   const int u = static_cast<int>(p.at);
-  p.at += a.workers;
+  p.at += p.after;  // (the workers' number)
   const int at = shared_group_of(a.plan, u);
   const SharedGroup g = a.plan.groups[at];
   const SharedUnit unit = shared_unit(g, a.v.heads, u);
@@ -284,7 +285,6 @@ __device__ __forceinline__ void next_shared_unit(const AttendArgs& a, Piece<true
   p.hidden_to = 0;
   p.tile0 = unit.tile0;
   p.count = unit.tiles;
-  p.after = 0;
 }
 
 template <int NB, int kSub, bool kShared>
@@ -372,7 +372,12 @@ __global__ void __launch_bounds__(128 * kGroups<HSP, NB>, 1)
   constexpr int kVWords = kVBytes / 4;
   constexpr int kTilesM = HSP / 16;       // m-tiles of the output
 
-  grid_dependency_wait();
+  // (beside the shared part: that kernel let this one start when the plan was complete)
+  if (!kShared || !a.beside) grid_dependency_wait();
+  if (kShared && a.prefix) grid_dependents_launch();
+  int workers = a.workers;
+  if constexpr (kShared)
+    workers = (a.prefix ? a.plan.head->shared_sms : a.plan.head->own_sms) * kGroups<HSP, NB>;
 
   // -------------------------------------------------------- the work list --
   // Thread i sums the work of sequences [i c, (i + 1) c); a scan over the CTA
@@ -426,7 +431,7 @@ __global__ void __launch_bounds__(128 * kGroups<HSP, NB>, 1)
   const int warp = warp_id & 3;      // warp in the group
   const int gtid = threadIdx.x & 127;
   const int worker = blockIdx.x * kGroups<HSP, NB> + gi;
-  const long long share = (total + a.workers - 1) / a.workers;
+  const long long share = (total + workers - 1) / max(workers, 1);
   Smem& sm = groups[gi];
   const int g = lane >> 2, t = lane & 3;
   const int D = kFull ? HSP : a.v.head_size;
@@ -435,7 +440,8 @@ __global__ void __launch_bounds__(128 * kGroups<HSP, NB>, 1)
 
   if (gtid == 0) {
     Piece<kShared>& p = sm.piece[0];
-    p.at = prefix ? worker : min(share * worker, total);
+    p.at = prefix ? (worker < workers ? worker : total) : min(share * worker, total);
+    if (prefix) p.after = workers;
     p.end = prefix ? total : min(p.at + share, total);
     if (!prefix && p.at < p.end) {
       int lo = 0, hi = kThreads;  // s_prefix[lo] <= at < s_prefix[hi]
@@ -914,7 +920,7 @@ __global__ void __launch_bounds__(128 * kGroups<HSP, NB>, 1)
           const int pieces =
               whole ? 0
                     : static_cast<int>(min(1 + (piece.after + share - 1) / share,
-                                           static_cast<long long>(a.workers - worker)));
+                                           static_cast<long long>(workers - worker)));
           a.plan.own[own] = OwnRow{at, gr.pieces, pieces, worker, r};
           a.plan.own_there[own] = 1;
         }
@@ -962,6 +968,7 @@ __global__ void __launch_bounds__(128 * kGroups<HSP, NB>, 1)
     group_sync(gi);  // sm is reused
   }
   if (!kShared && !left_open && gtid == 0) header[kHeadPieces] = 0;
+  if (kShared && a.beside) grid_dependency_wait();
 }
 
 // Joins the pieces of each unit that was split: row blockIdx.y of the unit that the

@@ -9,6 +9,11 @@
 
 namespace csa {
 
+// Lets the kernel behind this one in the stream start; it waits for this one's end itself.
+__device__ __forceinline__ void grid_dependents_launch() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // A unit of the tcgen05 form: rows and tokens of a tile.
 constexpr int kPrefixRows = 256, kPrefixTile = 64;
 
@@ -43,6 +48,8 @@ struct OwnRow {
 
 struct SharedHead {
   int units;          // of the shared part
+  int shared_sms;     // that work on it, while
+  int own_sms;        // these work on the own parts
   PromptList shared;  // those taken
   PromptList own;     // of the own parts: sequences of more than row_limit rows are its kernel's
 };

@@ -32,12 +32,13 @@ namespace csa {
 namespace {
 
 constexpr int kPlanThreads = 1024;
+
 // From this many rows a group on average (tokens x query heads of a kv head) the shared part is
 // the tcgen05 kernel's.
 constexpr int kPrefixFrom = 33;
 // Below so many bytes of codes that it would keep from being read again (by all SMs), the shared
 // part is not worth its launches: sequences read it for themselves.
-constexpr long long kWorthBytes = 32LL << 20;
+constexpr long long kWorthBytes = 96LL << 20;
 // Room for parts beyond one for each row and head: what cutting along the tokens may take.
 constexpr long long kSpareParts = 2LL * kMaxSms * kPrefixRows;
 
@@ -49,8 +50,14 @@ struct PlanArgs {
   long long rows_heads;  // rows of own_there
   int group_heads;
   int unit_rows, tile;  // of the shared part's kernel
-  int workers;          // what works on a unit at a time
-  int start;            // what a unit costs beyond its tiles, in tiles
+  int sms, per_sm;      // and what works on a unit at a time, of an SM
+  float tile_us;        // a tile's time there
+  float start;          // what a unit costs beyond its tiles, in tiles
+  float part;           // what one part costs, written and read again, in tiles
+  int own_rows, own_tile;  // of the own parts' kernel, the same
+  int own_start;
+  float own_us;
+  bool drop;            // whether a sequence or two may be left out of a group
   long long worth;      // keys, over all kv heads, whose reading the shared part has to save
   long long prompt_blocks;  // as in AttendArgs
 };
@@ -58,11 +65,12 @@ struct PlanArgs {
 // CTA 0 plans, the others clear the marks of the rows.
 __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_sm103a_kernel(const PlanArgs a) {
   __shared__ int s_bad, s_most, s_chunk;
-  __shared__ unsigned long long s_saved, s_blocks, s_key[kPlanThreads / 32];
+  __shared__ unsigned long long s_saved, s_blocks, s_tiles, s_own, s_key[kPlanThreads / 32];
   const KvView& v = a.v;
   const SharedPlan& plan = a.plan;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = plan.group_count,
             S = v.sequences;
+  grid_dependents_launch();  // (which wait for this grid's end themselves)
   grid_dependency_wait();
   if (blockIdx.x > 0) {
     const long long n = (a.rows_heads + 3) / 4;
@@ -71,7 +79,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_sm103a_kernel(con
       reinterpret_cast<int4*>(plan.own_there)[i] = make_int4(0, 0, 0, 0);
     return;
   }
-  if (tid == 0) s_bad = s_most = 0, s_saved = s_blocks = 0;
+  if (tid == 0) s_bad = s_most = 0, s_saved = s_blocks = s_tiles = s_own = 0;
   __syncthreads();
 
   // The groups: bounds in order, whole pages.
@@ -90,7 +98,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_sm103a_kernel(con
   const bool bad = s_bad != 0;  // then nothing is computed
   if (bad && tid == 0) report_index(v.status, kIndexSequence);
 
-  // The sequences, each with its group (found by its bounds).
+  // The sequences, each with its group (found by its bounds); and what their own parts take.
+  long long own = 0;
   for (int s = tid; s < S; s += kPlanThreads) {
     SharedSequence r{};
     r.q = kv_sequence(v, s);
@@ -118,8 +127,14 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_sm103a_kernel(con
     const long long rows = static_cast<long long>(r.q.n) * a.group_heads;
     if (a.prompt_blocks > 0 && rows > kRowLimit)
       atomicAdd(&s_blocks, static_cast<unsigned long long>((rows + 15) / 16 * v.heads));
+    else if (rows > 0)
+      own += (rows + a.own_rows - 1) / a.own_rows *
+             (max((r.q.length - r.lead + a.own_tile - 1) / a.own_tile, 1) + a.own_start);
     plan.sequences[s] = r;
   }
+#pragma unroll
+  for (int d = 16; d > 0; d /= 2) own += __shfl_xor_sync(0xFFFFFFFFu, own, d);
+  if (lane == 0 && own > 0) atomicAdd(&s_own, static_cast<unsigned long long>(own));
   __syncthreads();
 
   // The groups' rows: from the first to the last of their sequences that have any; and what a
@@ -141,6 +156,32 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_sm103a_kernel(con
     row0 = __reduce_min_sync(0xFFFFFFFFu, row0);
     end = __reduce_max_sync(0xFFFFFFFFu, end);
     members = __reduce_add_sync(0xFFFFFFFFu, members);
+    // A last block of few rows costs as much as a whole one: where one or two sequences are all of
+    // it, they read the shared tokens for themselves.
+    const int rest = row0 < end ? (end - row0) * a.group_heads % a.unit_rows : 0;
+    if (a.drop && rest > 0 && rest <= kRowLimit && (end - row0) * a.group_heads > a.unit_rows) {
+      const int s = to - 1 - lane;
+      const SharedSequence q = plan.sequences[max(s, 0)];
+      const bool in = s >= from && q.group == g;
+      const int first = in ? q.q.row0 : INT_MAX;
+      const uint32_t there = __ballot_sync(0xFFFFFFFFu, in);
+      int cut = end, dropped = 0;
+      for (uint32_t left = there; left != 0 && dropped < 2 && (end - cut) * a.group_heads < rest;
+           left &= left - 1, ++dropped)
+        cut = min(cut, __shfl_sync(0xFFFFFFFFu, first, __ffs(left) - 1));
+      if ((end - cut) * a.group_heads >= rest && (end - cut) * a.group_heads <= kRowLimit &&
+          cut > row0) {
+        if (in && first >= cut) {
+          plan.sequences[s].group = -1;
+          const long long rows = static_cast<long long>(q.q.n) * a.group_heads;
+          atomicAdd(&s_own, static_cast<unsigned long long>((rows + a.own_rows - 1) / a.own_rows *
+                                                            (q.lead / a.own_tile)));
+        }
+        end = cut;
+        members -= dropped;
+      }
+    }
+    __syncwarp();
     p.row0 = p.rows = p.tiles = p.blocks = p.pieces = 0;
     if (row0 < end) {
       p.row0 = row0;
@@ -149,6 +190,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_sm103a_kernel(con
       p.blocks = (p.rows * a.group_heads + a.unit_rows - 1) / a.unit_rows;
       if (lane == 0) {
         atomicMax(&s_most, p.tiles);
+        atomicAdd(&s_tiles, static_cast<unsigned long long>(p.tiles) * p.blocks * v.heads);
         atomicAdd(&s_saved, static_cast<unsigned long long>(members - 1) * p.tokens);
       }
     }
@@ -157,9 +199,19 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_sm103a_kernel(con
   }
   __syncthreads();
   const bool worth = static_cast<long long>(s_saved) * v.heads >= a.worth;
+  // SMs are shared out by the time that the two parts take.
+  const float shared_us = worth ? static_cast<float>(s_tiles) * a.tile_us / a.per_sm : 0.0f;
+  const float own_us = static_cast<float>(s_own) * a.own_us;
+  int shared_sms = 0;
+  if (shared_us > 0.0f) {
+    shared_sms = a.sms == 1 ? 1
+                            : min(max(static_cast<int>(a.sms * (shared_us / (shared_us + own_us)) + 0.5f), 1),
+                                  a.sms - 1);
+  }
+  const float workers = static_cast<float>(max(shared_sms, 1) * a.per_sm);
 
   // The longest run of tiles of a unit: the longest group's cut into 1, 2, ... 1024 pieces, that
-  // which takes the least time as rounds of equal units, and room.
+  // which takes the least time as rounds of equal units and in parts, and room.
   const int mine = max((s_most + tid) / (tid + 1), 1);
   {
     long long units = 0, parts = 0;
@@ -169,8 +221,10 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_sm103a_kernel(con
       units += pieces * p.blocks * v.heads;
       parts += pieces * p.rows * a.group_heads * v.heads;
     }
-    const float rounds = ceilf(static_cast<float>(units) / static_cast<float>(a.workers));
-    const float cost = parts <= plan.parts ? rounds * static_cast<float>(mine + a.start) : INFINITY;
+    const float rounds = ceilf(static_cast<float>(units) / workers);
+    const float cost = parts <= plan.parts ? rounds * (static_cast<float>(mine) + a.start) +
+                                                 static_cast<float>(parts) * a.part
+                                           : INFINITY;
     // (of equal ones the fewest pieces)
     unsigned long long key =
         static_cast<unsigned long long>(__float_as_uint(cost)) << 32 | static_cast<unsigned>(tid);
@@ -211,6 +265,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_sm103a_kernel(con
       // (more than there is room for only where rows are in several sequences: nothing is computed)
       const bool room = parts_before <= plan.parts && units_before <= INT_MAX;
       plan.head->units = room ? static_cast<int>(units_before) : 0;
+      plan.head->shared_sms = shared_sms;
+      plan.head->own_sms = a.sms == 1 ? 1 : a.sms - shared_sms;
       plan.head->shared = PromptList{0u, 0};
       plan.head->own = PromptList{
           0u, static_cast<long long>(s_blocks) > a.prompt_blocks ? kRowLimit : kNoRowLimit};
@@ -223,84 +279,123 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_sm103a_kernel(con
   for (int s = tid; s < S; s += kPlanThreads) {
     SharedSequence& r = plan.sequences[s];
     if (r.group >= 0) {
-      if (worth) r.start = r.lead;
-      else r.group = -1;
+      // (its rows are the group's, whatever the offsets are)
+      const SharedGroup p = plan.groups[r.group];
+      if (p.pieces > 0 && r.q.row0 >= p.row0 && r.q.row0 + r.q.n <= p.row0 + p.rows)
+        r.start = r.lead;
+      else
+        r.group = -1;
     }
     if (s_bad) r.q.n = 0;
   }
 }
 
-// A warp a row and head: its own part, whole or in pieces, and its shared ones, in a fixed order.
-template <int HSP>
+// kWarps warps a row and head: its own part, whole or in pieces, and its shared ones, in a fixed
+// order.
+template <int HSP, int kWarps>
 __global__ void __launch_bounds__(128) shared_join_sm103a_kernel(const AttendArgs a, int q_heads) {
   grid_dependency_wait();
-  constexpr int V = HSP / 32;
+  constexpr int V = HSP / 32, kRowsAtOnce = 4 / kWarps;
   using Vec = typename std::conditional<V == 4, float4, float2>::type;
-  const int lane = threadIdx.x & 31;
-  const long long all = static_cast<long long>(a.v.rows) * q_heads;
+  __shared__ Vec s_acc[4][32];
+  __shared__ float s_sum[4], s_top[4];
   [[maybe_unused]] __shared__ int s_abort;
   [[maybe_unused]] const Watchdog wd{0, a.v.status, &s_abort};
-  for (long long i = blockIdx.x * 4ll + (threadIdx.x >> 5); i < all; i += gridDim.x * 4ll) {
-    if (a.plan.own_there[i] == 0) continue;
-    const OwnRow w = a.plan.own[i];
-    const int first = max(w.pieces, 1), n = first + w.shared;
-    if (!CSA_CHECK(w.pieces >= 0 && w.shared >= 0 && w.at >= 0 &&
-                       w.at + w.shared <= a.plan.parts && w.row >= 0 && w.row < kMaxRows &&
-                       w.worker >= 0 && w.worker + w.pieces <= kMaxWorkers,
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w0 = warp % kWarps;
+  const unsigned all = static_cast<unsigned>(a.v.rows) * static_cast<unsigned>(q_heads);
+  const unsigned step = gridDim.x * kRowsAtOnce;
+  unsigned i = blockIdx.x * kRowsAtOnce + warp / kWarps;
+  int there = i < all ? a.plan.own_there[i] : 0;
+  OwnRow w = i < all ? a.plan.own[i] : OwnRow{};
+  for (; i < all; i += step) {
+    const int this_there = there;
+    const OwnRow r = w;
+    if (i + step < all) {  // (asked for before this row is done)
+      there = a.plan.own_there[i + step];
+      w = a.plan.own[i + step];
+    }
+    if (this_there == 0) continue;  // (the warps of a row alike)
+    const int first = max(r.pieces, 1), n = first + r.shared;
+    if (!CSA_CHECK(r.pieces >= 0 && r.shared >= 0 && r.at >= 0 &&
+                       r.at + r.shared <= a.plan.parts && r.row >= 0 && r.row < kMaxRows &&
+                       r.worker >= 0 && r.worker + r.pieces <= kMaxWorkers,
                    wd, kCheckRing))
       continue;
     // Piece p's maximum, sum and output.
     auto piece = [&](int p, float& m, float& l) -> const float* {
-      if (p < first && w.pieces > 0) {
-        const int slot = p == 0 ? 2 * w.worker + 1 : 2 * (w.worker + p);
+      if (p < first && r.pieces > 0) {
+        const int slot = p == 0 ? 2 * r.worker + 1 : 2 * (r.worker + p);
         const float* part = a.parts + static_cast<long long>(slot) * a.part_floats;
-        m = part[w.row];
-        l = part[kMaxRows + w.row];
-        return part + 2 * kMaxRows + w.row * HSP;
+        m = part[r.row];
+        l = part[kMaxRows + r.row];
+        return part + 2 * kMaxRows + r.row * HSP;
       }
-      const long long at = p < first ? i : w.at + p - first;
+      const long long at = p < first ? static_cast<long long>(i) : r.at + p - first;
       const float2 x = p < first ? a.plan.own_ml[at] : a.plan.ml[at];
       m = x.x;
       l = x.y;
       return (p < first ? a.plan.own_o : a.plan.o) + at * HSP;
     };
-    float top = kNothing;
-    for (int p0 = 0; p0 < n; p0 += 32) {
-      float m = kNothing, l;
-      if (p0 + lane < n) piece(p0 + lane, m, l);
-      top = fmaxf(top, m);
-    }
-    __syncwarp();
-#pragma unroll
-    for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-    float acc[V] = {}, sum = 0.0f;
-    for (int p0 = 0; p0 < n; p0 += 32) {
+    // Warp w0 takes pieces w0, w0 + kWarps, ..., relative to the largest maximum among its own.
+    float top = kNothing, sum = 0.0f, acc[V] = {};
+    for (int p0 = w0; p0 < n; p0 += 32 * kWarps) {
+      const int p = p0 + lane * kWarps;
       float m = kNothing, l = 0.0f;
       const float* o = nullptr;
-      if (p0 + lane < n) o = piece(p0 + lane, m, l);
+      if (p < n) o = piece(p, m, l);
       __syncwarp();
-      // (in two factors, neither of which comes out as 0, for the sum)
+      float most = fmaxf(top, m);
+#pragma unroll
+      for (int d = 16; d > 0; d /= 2) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
+      // (in two factors, neither of which comes out as 0, for the sums)
+      const float back = ex2_approx(0.5f * (top - most));
+      sum = sum * back * back;
+#pragma unroll
+      for (int k = 0; k < V; ++k) acc[k] *= back * back;
+      top = most;
       const float half = ex2_approx(0.5f * (m - top)), c = half * half;
       sum = fmaf(l * half, half, sum);
-      const int here = min(n - p0, 32);
+      const int here = min((n - p0 + kWarps - 1) / kWarps, 32);
 #pragma unroll 8
-      for (int p = 0; p < here; ++p) {
-        const float cp = __shfl_sync(0xFFFFFFFFu, c, p);
+      for (int q = 0; q < here; ++q) {
+        const float cq = __shfl_sync(0xFFFFFFFFu, c, q);
         const float* from = reinterpret_cast<const float*>(
-            __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(o), p));
+            __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(o), q));
         const Vec x = reinterpret_cast<const Vec*>(from)[lane];
         const float* v = reinterpret_cast<const float*>(&x);
 #pragma unroll
-        for (int k = 0; k < V; ++k) acc[k] = fmaf(v[k], cp, acc[k]);
+        for (int k = 0; k < V; ++k) acc[k] = fmaf(v[k], cq, acc[k]);
       }
     }
 #pragma unroll
     for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-    const int row = static_cast<int>(i / q_heads), head = static_cast<int>(i - static_cast<long long>(row) * q_heads);
+    if constexpr (kWarps > 1) {
+      s_acc[warp][lane] = *reinterpret_cast<const Vec*>(acc);
+      if (lane == 0) s_sum[warp] = sum, s_top[warp] = top;
+      __syncthreads();
+      top = fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]));
+      sum = 0.0f;
+#pragma unroll
+      for (int k = 0; k < V; ++k) acc[k] = 0.0f;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float half = ex2_approx(0.5f * (s_top[q] - top)), c = half * half;
+        sum = fmaf(s_sum[q] * half, half, sum);
+        const Vec x = s_acc[q][lane];
+        const float* v = reinterpret_cast<const float*>(&x);
+#pragma unroll
+        for (int k = 0; k < V; ++k) acc[k] = fmaf(v[k], c, acc[k]);
+      }
+      __syncthreads();
+      if (warp > 0) continue;
+    }
+    const int row = static_cast<int>(i / static_cast<unsigned>(q_heads));
+    const int head = static_cast<int>(i - static_cast<unsigned>(row) * static_cast<unsigned>(q_heads));
     uint32_t y[V / 2];
 #pragma unroll
     for (int k = 0; k < V; k += 2) {
-      const float v0 = sum == 0.0f ? 0.0f : acc[k] / sum, v1 = sum == 0.0f ? 0.0f : acc[k + 1] / sum;
+      const float v0 = sum == 0.0f ? 0.0f : acc[k] / sum;
+      const float v1 = sum == 0.0f ? 0.0f : acc[k + 1] / sum;
       if (a.half) {
         y[k / 2] = half2_of(v0, v1);
       } else {
@@ -314,6 +409,19 @@ __global__ void __launch_bounds__(128) shared_join_sm103a_kernel(const AttendArg
       else *reinterpret_cast<uint32_t*>(to) = y[0];
     }
   }
+}
+
+template <int HSP>
+cudaError_t launch_join(const AttendArgs& a, int q_heads, long long rows_heads, int sms,
+                        cudaStream_t stream) {
+  // Four warps a row while there are places for all of them at once.
+  const long long most = 16LL * sms;
+  return rows_heads <= most
+             ? launch_programmatic(shared_join_sm103a_kernel<HSP, 4>,
+                                   dim3(static_cast<unsigned>(rows_heads)), 128, 0, stream, a, q_heads)
+             : launch_programmatic(shared_join_sm103a_kernel<HSP, 1>,
+                                   dim3(static_cast<unsigned>(std::min((rows_heads + 3) / 4, most))),
+                                   128, 0, stream, a, q_heads);
 }
 
 size_t up16(size_t n) { return (n + 15) / 16 * 16; }
@@ -374,8 +482,24 @@ int cache_attention_shared_launch(const csa_kv_cache& cache, const csa_kv_batch&
   const bool eight =
       most_rows <= 8 || (a.group <= 8 && (prompts || batch_rows <= 8LL * batch.sequences));
 
+  // What the kernel of few rows needs for a tile: an SM's groups take its codes at 42 GB/s between
+  // them (6.4 TB/s over all), or twice as long with 16 rows.
+  auto groups_of = [&](bool of_eight) {
+    return hsp == 64 ? (of_eight ? kGroups<64, 1> : kGroups<64, 2>)
+                     : (of_eight ? kGroups<128, 1> : kGroups<128, 2>);
+  };
+  auto rows_tile_us = [&](bool of_eight) {
+    return (of_eight ? 1.0f : 2.0f) * 64.0f * sub * 2.0f * cache.head_size / 42e3f *
+           groups_of(of_eight);
+  };
+
   PlanArgs p;
   p.v = a.v;
+  p.sms = sms;
+  p.own_rows = eight ? 8 : 16;
+  p.own_tile = 64 * sub;
+  p.own_start = (eight ? 2 : 3) * (2 / sub);
+  p.own_us = cache.heads * rows_tile_us(eight) / groups_of(eight);
   p.groups = groups;
   p.shared = shared;
   p.plan = a.plan;
@@ -385,24 +509,33 @@ int cache_attention_shared_launch(const csa_kv_cache& cache, const csa_kv_batch&
                 ? 0
                 : kWorthBytes * sms / kMaxSms / (2 * cache.head_size);
   p.prompt_blocks = a.prompt_blocks;
+  // (8 HSP bytes at 5 TB/s, in tiles of 1.2 us)
+  p.part = 8.0f * static_cast<float>(hsp) / 5e6f / 1.2f;
   if (prefix_tc) {
     p.unit_rows = kPrefixRows;
     p.tile = kPrefixTile;
-    p.workers = dev.sm_count;
-    p.start = 5;  // (9000 cycles from a unit's end to the next one's first scores, 1900 a tile)
+    p.per_sm = 1;
+    p.tile_us = hsp == 64 ? 1.0f : 1.2f;
+    p.start = 5.0f;  // (9000 cycles from a unit's end to the next one's first scores, 1900 a tile)
+    p.drop = true;
   } else {
     p.unit_rows = prefix_eight ? 8 : 16;
     p.tile = 64 * sub;
-    p.workers = sms * (hsp == 64 ? (prefix_eight ? kGroups<64, 1> : kGroups<64, 2>)
-                                 : (prefix_eight ? kGroups<128, 1> : kGroups<128, 2>));
-    p.start = (prefix_eight ? 2 : 3) * (2 / sub);
+    p.per_sm = groups_of(prefix_eight);
+    p.tile_us = rows_tile_us(prefix_eight);
+    p.start = static_cast<float>((prefix_eight ? 2 : 3) * (2 / sub));
+    p.drop = false;
   }
   const unsigned clear =
       static_cast<unsigned>(std::min<long long>((rows_heads / 4 + kPlanThreads) / kPlanThreads, sms));
   cudaError_t e = launch_programmatic(shared_plan_sm103a_kernel, dim3(1 + clear), kPlanThreads, 0,
                                       stream, p);
   int rc = CSA_OK;
-  if (e == cudaSuccess) {
+  // (not even were all tables full and shared)
+  const bool never = static_cast<double>(batch.sequences - 1) * batch.table_width *
+                         cache.page_tokens * cache.heads <
+                     static_cast<double>(p.worth);
+  if (e == cudaSuccess && !never) {
     if (prefix_tc) {
       rc = cache_prefix_launch(cache, batch, call, a.plan, false, stream, dev, err);
     } else {
@@ -410,17 +543,15 @@ int cache_attention_shared_launch(const csa_kv_cache& cache, const csa_kv_batch&
       e = launch_rows<true>(a, prefix_eight, cache.format, sms, dev, stream, rc, err);
       a.prefix = 0;
     }
+    a.beside = sms > 1 ? 1 : 0;
   }
   if (e == cudaSuccess && rc == CSA_OK)
     e = launch_rows<true>(a, eight, cache.format, sms, dev, stream, rc, err);
   if (e == cudaSuccess && rc == CSA_OK && prompts)
     rc = cache_prefix_launch(cache, batch, call, a.plan, true, stream, dev, err);
   if (e == cudaSuccess && rc == CSA_OK) {
-    const unsigned grid = static_cast<unsigned>(std::min<long long>((rows_heads + 3) / 4, 16LL * sms));
-    e = hsp == 64 ? launch_programmatic(shared_join_sm103a_kernel<64>, dim3(grid), 128, 0, stream, a,
-                                        call.q_heads)
-                  : launch_programmatic(shared_join_sm103a_kernel<128>, dim3(grid), 128, 0, stream, a,
-                                        call.q_heads);
+    e = hsp == 64 ? launch_join<64>(a, call.q_heads, rows_heads, sms, stream)
+                  : launch_join<128>(a, call.q_heads, rows_heads, sms, stream);
   }
   if (rc != CSA_OK) {
     err = "cache_attention_shared_forward: " + err;

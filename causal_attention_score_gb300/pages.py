@@ -68,6 +68,9 @@ def kv_pages_workspace_size(pages: KvPages, n: int) -> int:
 
 def _list(t: torch.Tensor, name: str, n: int, dev: int) -> int:
     """Address of an int32 list of n entries on device ``dev``."""
+    if (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.get_device() == dev
+            and t.numel() == n and t.is_contiguous()):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.get_device() != dev:
