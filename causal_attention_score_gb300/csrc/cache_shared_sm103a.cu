@@ -51,12 +51,11 @@ struct PlanArgs {
   int group_heads;
   int unit_rows, tile;  // of the shared part's kernel
   int sms, per_sm;      // and what works on a unit at a time, of an SM
-  float tile_us;        // a tile's time there
-  float start;          // what a unit costs beyond its tiles, in tiles
-  float part;           // what one part costs, written and read again, in tiles
-  int own_rows, own_tile;  // of the own parts' kernel, the same
-  int own_start;
-  float own_us;
+  float tile_us, start, first;  // a tile's time there, what a unit takes beyond its tiles (in
+                                // tiles), the kernel beyond its units
+  float part_us;        // what one part takes, written and read again
+  int own_rows, own_tile, own_start;  // of the own parts' kernel, the same
+  float own_us, own_first;            // (own_us: a tile of all kv heads on one SM)
   bool drop;            // whether a sequence or two may be left out of a group
   long long worth;      // keys, over all kv heads, whose reading the shared part has to save
   long long prompt_blocks;  // as in AttendArgs
@@ -64,7 +63,7 @@ struct PlanArgs {
 
 // CTA 0 plans, the others clear the marks of the rows.
 __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_sm103a_kernel(const PlanArgs a) {
-  __shared__ int s_bad, s_most, s_chunk;
+  __shared__ int s_bad, s_most, s_chunk, s_sms;
   __shared__ unsigned long long s_saved, s_blocks, s_tiles, s_own, s_key[kPlanThreads / 32];
   const KvView& v = a.v;
   const SharedPlan& plan = a.plan;
@@ -199,35 +198,45 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_sm103a_kernel(con
   }
   __syncthreads();
   const bool worth = static_cast<long long>(s_saved) * v.heads >= a.worth;
-  // SMs are shared out by the time that the two parts take.
-  const float shared_us = worth ? static_cast<float>(s_tiles) * a.tile_us / a.per_sm : 0.0f;
-  const float own_us = static_cast<float>(s_own) * a.own_us;
-  int shared_sms = 0;
-  if (shared_us > 0.0f) {
-    shared_sms = a.sms == 1 ? 1
-                            : min(max(static_cast<int>(a.sms * (shared_us / (shared_us + own_us)) + 0.5f), 1),
-                                  a.sms - 1);
-  }
-  const float workers = static_cast<float>(max(shared_sms, 1) * a.per_sm);
-
-  // The longest run of tiles of a unit: the longest group's cut into 1, 2, ... 1024 pieces, that
-  // which takes the least time as rounds of equal units and in parts, and room.
-  const int mine = max((s_most + tid) / (tid + 1), 1);
+  // How many SMs take the shared part, and the longest run of tiles of a unit there (the longest
+  // group's cut into 1, 2, ... pieces): what takes the least time, the shared part as rounds of
+  // equal units and in parts, the own ones beside it, and has room. Numbers of SMs around those
+  // that the two parts' work is in proportion to.
   {
-    long long units = 0, parts = 0;
-    for (int g = 0; g < G && worth; ++g) {
-      const SharedGroup p = plan.groups[g];
-      const long long pieces = (p.tiles + mine - 1) / mine;
-      units += pieces * p.blocks * v.heads;
-      parts += pieces * p.rows * a.group_heads * v.heads;
+    const float own_us = static_cast<float>(s_own) * a.own_us;
+    const float shared_us = static_cast<float>(s_tiles) * a.tile_us / static_cast<float>(a.per_sm);
+    const float middle = static_cast<float>(a.sms) * (shared_us / (shared_us + own_us + 1e-6f));
+    const int sms = min(max(static_cast<int>(middle + static_cast<float>(a.sms * ((tid & 15) - 7)) / 32.0f + 0.5f), 1),
+                        max(a.sms - 1, 1));
+    float best = INFINITY;
+    int best_chunk = 1;
+    const int most_pieces = min(s_most, G <= 16 ? 512 : 64);
+    for (int cut = (tid >> 4) + 1; cut <= most_pieces && worth; cut += kPlanThreads / 16) {
+      const int chunk = (s_most + cut - 1) / cut;
+      long long units = 0, parts = 0, tiles = 0;
+      for (int g = 0; g < G; ++g) {
+        const SharedGroup p = plan.groups[g];
+        const long long pieces = (p.tiles + chunk - 1) / chunk;
+        units += pieces * p.blocks * v.heads;
+        tiles += static_cast<long long>(p.tiles) * p.blocks * v.heads;
+        parts += pieces * p.rows * a.group_heads * v.heads;
+      }
+      // (half as rounds of units of the longest run, half as if work could be dealt out evenly)
+      const float takers = static_cast<float>(sms * a.per_sm);
+      const float rounds = ceilf(static_cast<float>(units) / takers);
+      float us = 0.5f * a.tile_us *
+                 (rounds * (static_cast<float>(chunk) + a.start) +
+                  fmaxf((static_cast<float>(tiles) + a.start * static_cast<float>(units)) / takers,
+                        static_cast<float>(chunk) + a.start));
+      const float other = own_us / static_cast<float>(max(a.sms - sms, 1)) + a.own_first;
+      us = a.sms == 1 ? us + other : fmaxf(us + a.first, other);
+      us += static_cast<float>(parts) * a.part_us;
+      if (parts <= plan.parts && us < best) best = us, best_chunk = chunk;
     }
-    const float rounds = ceilf(static_cast<float>(units) / workers);
-    const float cost = parts <= plan.parts ? rounds * (static_cast<float>(mine) + a.start) +
-                                                 static_cast<float>(parts) * a.part
-                                           : INFINITY;
-    // (of equal ones the fewest pieces)
+    __syncwarp();
+    // (of equal ones the lowest thread's)
     unsigned long long key =
-        static_cast<unsigned long long>(__float_as_uint(cost)) << 32 | static_cast<unsigned>(tid);
+        static_cast<unsigned long long>(__float_as_uint(best)) << 32 | static_cast<unsigned>(tid);
 #pragma unroll
     for (int d = 16; d > 0; d /= 2) key = min(key, __shfl_xor_sync(0xFFFFFFFFu, key, d));
     if (lane == 0) s_key[warp] = key;
@@ -235,7 +244,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_sm103a_kernel(con
     key = s_key[lane];
 #pragma unroll
     for (int d = 16; d > 0; d /= 2) key = min(key, __shfl_xor_sync(0xFFFFFFFFu, key, d));
-    if (tid == static_cast<int>(key & 0xFFFFFFFFu)) s_chunk = mine;
+    if (tid == static_cast<int>(key & 0xFFFFFFFFu)) s_chunk = best_chunk, s_sms = worth ? sms : 0;
     __syncthreads();
   }
   if (warp == 0) {
@@ -265,8 +274,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_sm103a_kernel(con
       // (more than there is room for only where rows are in several sequences: nothing is computed)
       const bool room = parts_before <= plan.parts && units_before <= INT_MAX;
       plan.head->units = room ? static_cast<int>(units_before) : 0;
-      plan.head->shared_sms = shared_sms;
-      plan.head->own_sms = a.sms == 1 ? 1 : a.sms - shared_sms;
+      plan.head->shared_sms = s_sms;
+      plan.head->own_sms = max(a.sms - s_sms, 1);
       plan.head->shared = PromptList{0u, 0};
       plan.head->own = PromptList{
           0u, static_cast<long long>(s_blocks) > a.prompt_blocks ? kRowLimit : kNoRowLimit};
@@ -482,14 +491,14 @@ int cache_attention_shared_launch(const csa_kv_cache& cache, const csa_kv_batch&
   const bool eight =
       most_rows <= 8 || (a.group <= 8 && (prompts || batch_rows <= 8LL * batch.sequences));
 
-  // What the kernel of few rows needs for a tile: an SM's groups take its codes at 42 GB/s between
-  // them (6.4 TB/s over all), or twice as long with 16 rows.
+  // What the kernel of few rows needs for a tile: an SM's groups take its codes at 38 GB/s between
+  // them (5.8 TB/s over all), or twice as long with 16 rows.
   auto groups_of = [&](bool of_eight) {
     return hsp == 64 ? (of_eight ? kGroups<64, 1> : kGroups<64, 2>)
                      : (of_eight ? kGroups<128, 1> : kGroups<128, 2>);
   };
   auto rows_tile_us = [&](bool of_eight) {
-    return (of_eight ? 1.0f : 2.0f) * 64.0f * sub * 2.0f * cache.head_size / 42e3f *
+    return (of_eight ? 1.0f : 2.0f) * 64.0f * sub * 2.0f * cache.head_size / 38e3f *
            groups_of(of_eight);
   };
 
@@ -509,13 +518,14 @@ int cache_attention_shared_launch(const csa_kv_cache& cache, const csa_kv_batch&
                 ? 0
                 : kWorthBytes * sms / kMaxSms / (2 * cache.head_size);
   p.prompt_blocks = a.prompt_blocks;
-  // (8 HSP bytes at 5 TB/s, in tiles of 1.2 us)
-  p.part = 8.0f * static_cast<float>(hsp) / 5e6f / 1.2f;
+  p.part_us = 8.0f * static_cast<float>(hsp) / 5e6f;  // (8 HSP bytes at 5 TB/s)
+  p.own_first = 8.0f;
   if (prefix_tc) {
     p.unit_rows = kPrefixRows;
     p.tile = kPrefixTile;
     p.per_sm = 1;
     p.tile_us = hsp == 64 ? 1.0f : 1.2f;
+    p.first = 8.0f;
     p.start = 5.0f;  // (9000 cycles from a unit's end to the next one's first scores, 1900 a tile)
     p.drop = true;
   } else {
@@ -524,6 +534,7 @@ int cache_attention_shared_launch(const csa_kv_cache& cache, const csa_kv_batch&
     p.per_sm = groups_of(prefix_eight);
     p.tile_us = rows_tile_us(prefix_eight);
     p.start = static_cast<float>((prefix_eight ? 2 : 3) * (2 / sub));
+    p.first = 4.0f;
     p.drop = false;
   }
   const unsigned clear =
