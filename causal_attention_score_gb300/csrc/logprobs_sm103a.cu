@@ -417,26 +417,12 @@ __global__ void __launch_bounds__(kThreads, kForwardPerSm)
   grid_dependency_wait();
   if constexpr (kCluster) cluster_sync();  // (all have begun before one writes to another)
   for (long long r = blockIdx.x / cluster; r < a.rows; r += gridDim.x / cluster) {
+    // A row left out takes part as one of no elements: no barrier depends on what is read.
     const int token = a.tokens[r];
-    if (token < 0 || token >= a.vocab) {  // left out
-      if (rank == 0) {
-        if (tid == 0) {
-          if (token >= 0) report_index(a.status, kIndexToken);
-          a.logprob[r] = 0.0f;
-          a.entropy[r] = 0.0f;
-          a.stats[r] = make_float2(0.0f, 0.0f);
-        }
-        if (kTop && tid < a.top) {
-          a.top_logprob[r * a.top + tid] = 0.0f;
-          a.top_token[r * a.top + tid] = -1;
-        }
-      }
-      __syncwarp();
-      continue;
-    }
+    const bool out = token < 0 || token >= a.vocab;
     const T* row = static_cast<const T*>(a.logits) + r * a.stride;
-    const Run<T> run(row, from, to);
-    const float given = Logit<T>::get(row[token]);  // (asked for before it is needed)
+    const Run<T> run(row, from, out ? from : to);
+    const float given = out ? 0.0f : Logit<T>::get(row[token]);  // (before it is needed)
     Partial p;
     for (int i = tid; i < run.chunks; i += kLoads * kThreads) {
       uint4 w[kLoads];
@@ -515,10 +501,12 @@ __global__ void __launch_bounds__(kThreads, kForwardPerSm)
       const bool none = s == 0.0f;  // every logit is -inf
       const float log_s = none ? 0.0f : logf(s);
       if (warp == 0 && lane == 0) {
-        a.stats[r] = make_float2(none ? -INFINITY : most, log_s);
-        a.logprob[r] = none ? -INFINITY : fmaf(given - most, a.scale, -log_s);
+        if (token >= a.vocab) report_index(a.status, kIndexToken);
+        a.stats[r] = out ? make_float2(0.0f, 0.0f) : make_float2(none ? -INFINITY : most, log_s);
+        a.logprob[r] = out ? 0.0f : none ? -INFINITY : fmaf(given - most, a.scale, -log_s);
         a.entropy[r] = none ? 0.0f : log_s - kLn2 * (t / s);
       }
+      __syncwarp();
       if constexpr (kTop) {
         // Warp o places list o's elements among all of them: as far behind the first as there
         // are elements before it.
@@ -535,7 +523,12 @@ __global__ void __launch_bounds__(kThreads, kForwardPerSm)
             if (q != warp) place += n;
           }
         }
-        if (lane < k && key != 0 && place < k) {
+        if (out) {
+          if (warp == 0 && lane < k) {
+            a.top_logprob[r * k + lane] = 0.0f;
+            a.top_token[r * k + lane] = -1;
+          }
+        } else if (lane < k && key != 0 && place < k) {
           const float x = key_value(key);
           a.top_logprob[r * k + place] = none ? -INFINITY : fmaf(x - most, a.scale, -log_s);
           a.top_token[r * k + place] = index;

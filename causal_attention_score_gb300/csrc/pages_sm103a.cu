@@ -376,23 +376,23 @@ __global__ void __launch_bounds__(kThreads) cache_fork_sm103a_kernel(const ForkA
 
 // A CTA an entry: its pages' counts go down.
 __global__ void __launch_bounds__(128) pages_free_sm103a_kernel(const Books b, const int* which) {
-  __shared__ int s_tokens;
+  __shared__ int s_sequence, s_tokens;
   grid_dependency_wait();
-  const int s = which[blockIdx.x];
-  if (s < 0 || s >= b.sequences) {
-    if (threadIdx.x == 0) report_index(b.status, kIndexSequence);
-    return;
-  }
   if (threadIdx.x == 0) {
+    const int at = which[blockIdx.x];
+    s_sequence = at;
     s_tokens = 0;
-    if (length_ok(b, b.lengths[s])) {
-      const int tokens = atomicExch(b.lengths + s, 0);  // (named twice, the second finds nothing)
-      if (length_ok(b, tokens)) s_tokens = tokens;
-    } else {
+    if (at < 0 || at >= b.sequences) {
+      report_index(b.status, kIndexSequence);
+    } else if (!length_ok(b, b.lengths[at])) {
       report_index(b.status, kIndexLength);
+    } else {
+      const int tokens = atomicExch(b.lengths + at, 0);  // (named twice, the second finds nothing)
+      if (length_ok(b, tokens)) s_tokens = tokens;
     }
   }
   __syncthreads();
+  const int s = s_sequence;
   const int blocks = blocks_of(b, s_tokens);
   for (int i = threadIdx.x; i < blocks; i += 128) {
     const int p = b.table[static_cast<long long>(s) * b.width + i];
