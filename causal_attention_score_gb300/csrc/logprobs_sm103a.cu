@@ -403,7 +403,7 @@ __device__ void select_top(const Run<T>& run, float top, int k, Shared& sh) {
 
 // kCluster: a row's CTAs are a cluster of a.cluster (else 1).
 template <typename T, bool kTop, bool kCluster>
-__global__ void __launch_bounds__(kThreads, kForwardPerSm)
+__global__ void __launch_bounds__(kThreads, kCluster ? 2 : kForwardPerSm)
     logprobs_forward_sm103a_kernel(const ForwardArgs a) {
   __shared__ Shared sh;
   constexpr int V = Logit<T>::kVec;
@@ -417,18 +417,29 @@ __global__ void __launch_bounds__(kThreads, kForwardPerSm)
   grid_dependency_wait();
   if constexpr (kCluster) cluster_sync();  // (all have begun before one writes to another)
   for (long long r = blockIdx.x / cluster; r < a.rows; r += gridDim.x / cluster) {
-    // A row left out takes part as one of no elements: no barrier depends on what is read.
     const int token = a.tokens[r];
-    const bool out = token < 0 || token >= a.vocab;
     const T* row = static_cast<const T*>(a.logits) + r * a.stride;
-    const Run<T> run(row, from, out ? from : to);
-    const float given = out ? 0.0f : Logit<T>::get(row[token]);  // (before it is needed)
+    // A row left out takes part as one of no elements: no barrier depends on what is read.
+    const bool out = token < 0 || token >= a.vocab;
+    // (few rows: the first loads are asked for before the token is there)
+    Run<T> run(row, from, !kCluster && out ? from : to);
+    uint4 early[kCluster ? kLoads : 1];
+    if constexpr (kCluster) {
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k)
+        if (tid + k * kThreads < run.chunks) early[k] = __ldg(run.body + tid + k * kThreads);
+      if (out) run.chunks = run.head = run.tail = 0;
+    }
+    const float given = out ? 0.0f : Logit<T>::get(row[token]);
     Partial p;
     for (int i = tid; i < run.chunks; i += kLoads * kThreads) {
       uint4 w[kLoads];
 #pragma unroll
-      for (int k = 0; k < kLoads; ++k)
-        if (k == 0 || i + k * kThreads < run.chunks) w[k] = __ldg(run.body + i + k * kThreads);
+      for (int k = 0; k < kLoads; ++k) {
+        if (k > 0 && i + k * kThreads >= run.chunks) continue;
+        if (kCluster && i == tid) w[k] = early[kCluster ? k : 0];
+        else w[k] = __ldg(run.body + i + k * kThreads);
+      }
 #pragma unroll
       for (int k = 0; k < kLoads; ++k) {
         if (k > 0 && i + k * kThreads >= run.chunks) break;
@@ -676,7 +687,8 @@ cudaError_t launch_forward(ForwardArgs a, const DeviceInfo& dev, cudaStream_t st
   while (a.cluster < kMaxCluster && a.rows * a.cluster < dev.sm_count &&
          bytes / (2 * a.cluster) >= 8192)
     a.cluster *= 2;
-  const long long most = std::max(kForwardPerSm * dev.sm_count / a.cluster, 1);
+  const int per_sm = a.cluster > 1 ? 2 : kForwardPerSm;
+  const long long most = std::max(per_sm * dev.sm_count / a.cluster, 1);
   const unsigned grid = static_cast<unsigned>(std::min(a.rows, most) * a.cluster);
   if (a.cluster > 1)
     return launch_programmatic_cluster(a.top > 0 ? logprobs_forward_sm103a_kernel<T, true, true>

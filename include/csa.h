@@ -675,8 +675,8 @@ csa_status kv_cache_compact(const csa_kv_cache* cache, const csa_kv_pages* pages
  *                 order, of equal ones the lowest number first (-0 equals 0), and their log p.
  *   logits       device, CSA_BF16, CSA_F16 or CSA_F32, [rows][vocab], rows `stride` elements
  *                apart (>= vocab; any alignment of the type);
- *   tokens       device, int32 [rows]; a negative one leaves its row out: its logits are not
- *                read, its results are 0 and its top tokens -1. So does one from vocab on, which
+ *   tokens       device, int32 [rows]; a negative one leaves its row out: its logits do not
+ *                matter, its results are 0 and its top tokens -1. So does one from vocab on, which
  *                csa_get_status reports as CSA_ERR_INDEX;
  *   scale        1 / temperature: > 0, at most 2^64;
  *   logprob, entropy   device, fp32 [rows]; stats device, fp32 [rows][2], 8-byte aligned;
