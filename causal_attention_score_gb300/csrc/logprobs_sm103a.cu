@@ -13,20 +13,17 @@
 // tree. A forbidden word's -inf has weight 0 and adds 0 to T (its d is clamped for the
 // product); a NaN or +inf makes its row's results NaN.
 //
-// Top alternatives without a second pass: the k-th largest of the threads' maxima, found by
-// a search over the bits of the order-preserving integer of a float, is a lower bound of the
-// k-th largest logit, and only the k threads whose maximum reaches it hold larger ones. Their
-// elements alone (k / 512 of the row) are read again, what reaches the bound is ranked by
-// counting. Threads whose maxima tie at the bound are told apart by the index of their first
-// such element.
+// Top alternatives without a second pass: the k-th largest of the maxima that four threads have
+// between them is a lower bound of the k-th largest logit, and only threads whose own maximum
+// reaches it (about k of 256) hold larger ones. Their elements alone are read again, what
+// reaches the bound is ranked by counting. Where many threads' maxima tie at the bound, the
+// index of their first such element tells them apart.
 //
 // Bound: HBM, one read of the logits (and one write of the gradient). A CTA of 256 threads takes
 // a row and four 16-byte loads a thread at once; six such CTAs an SM, so that some load while
 // others rank. 8192 x 50257 in fp32 with two alternatives: 255 us (6.5 TB/s, 0.96 of the copy
 // rate; five CTAs 261, four 283, two of 512 threads 323). Few rows are split over a cluster of up
 // to eight CTAs, whose results meet in the first one's shared memory.
-// The searches take four bits a round (a round is a barrier; bit by bit one row of 50257 with 20
-// alternatives took 15.6 us instead of 12.3).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -52,8 +49,7 @@ constexpr int kMaxCluster = 8;
 static_assert(kWarps >= kMaxCluster, "a warp for each CTA's list");
 constexpr int kLoads = 4;         // 16-byte loads that a thread has in flight
 constexpr int kCandidates = 1024; // elements that reach the bound
-constexpr int kColumns = 64;      // threads whose elements are looked at again (at least kMaxTop)
-constexpr int kRounds = 8;        // of a search, four bits each
+constexpr int kColumns = 4 * kMaxTop;  // threads whose elements are looked at again
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLeast = -1000.0f;  // exponents below have weight 0; finite, for products with it
 
@@ -227,7 +223,8 @@ struct alignas(16) Shared {
   int index[kMaxTop];
   int columns[kColumns];       // threads that may hold them
   int count, found;
-  int counts[2 * kRounds][16];
+  uint32_t quads[64];          // the largest of four threads each
+  uint32_t bound;
   float3 all[kMaxCluster];     // of every CTA of the row, at its first one
   uint32_t all_key[kMaxCluster][kMaxTop];
   int all_index[kMaxCluster][kMaxTop];
@@ -242,36 +239,34 @@ __device__ __forceinline__ bool before(uint32_t key, int index, uint32_t k2, int
   return key > k2 || (key == k2 && index < i2);
 }
 
-// The largest v below 2^bits with at least k threads' `mine` >= v (0 if there is none above),
-// or one that exactly k reach; `count` is how many do. Four bits a round: the threads that reach
-// each of 15 steps are counted by ballots and added up in a row of `counts` of the round's own
-// (cleared before), so that a round takes one barrier.
-__device__ __forceinline__ uint32_t kth_largest(uint32_t mine, int bits, int k, int (*counts)[16],
-                                                int& count) {
-  const int lane = static_cast<int>(lane_id());
-  uint32_t v = 0;
-  count = kThreads;
-#pragma unroll 1
-  for (int shift = (bits - 1) / 4 * 4; shift >= 0; shift -= 4, ++counts) {
-    int reach = 0;
-#pragma unroll
-    for (uint32_t i = 1; i < 16; ++i) {
-      const int n = __popc(__ballot_sync(0xFFFFFFFFu, mine >= (v | i << shift)));
-      if (lane == static_cast<int>(i)) reach = n;
+// The k-th largest (or, found sooner, a number that exactly k reach) of the 64 largest `mine` of
+// four threads next to each other, by one warp. Between two barriers.
+__device__ __forceinline__ uint32_t kth_largest(uint32_t mine, int k, Shared& sh) {
+  static_assert(kThreads == 256 && kMaxTop <= 32, "two of them a lane");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t quad = max(mine, __shfl_xor_sync(0xFFFFFFFFu, mine, 1));
+  quad = max(quad, __shfl_xor_sync(0xFFFFFFFFu, quad, 2));
+  if (lane % 4 == 0) sh.quads[warp * 8 + lane / 4] = quad;
+  __syncwarp();
+  __syncthreads();
+  if (warp == 0) {
+    const uint32_t x = sh.quads[lane], y = sh.quads[lane + 32];
+    // 32 of them reach the least of the lanes' larger ones
+    uint32_t v = __reduce_min_sync(0xFFFFFFFFu, max(x, y));
+    uint32_t top = __reduce_max_sync(0xFFFFFFFFu, max(x, y));
+    while (v < top) {
+      const uint32_t mid = top - (top - v) / 2;
+      const int n = __popc(__ballot_sync(0xFFFFFFFFu, x >= mid)) +
+                    __popc(__ballot_sync(0xFFFFFFFFu, y >= mid));
+      if (n >= k) v = mid;
+      else top = mid - 1;
+      if (n == k) break;
     }
-    if (reach > 0) atomicAdd(&(*counts)[lane & 15], reach);
+    if (lane == 0) sh.bound = v;
     __syncwarp();
-    __syncthreads();
-    const int n = *const_cast<volatile int*>(&(*counts)[lane & 15]);  // (of step 0: none)
-    const uint32_t enough = __ballot_sync(0xFFFFFFFFu, n >= k && lane < 16);
-    if (enough != 0) {
-      const int step = 31 - __clz(enough);
-      v |= static_cast<uint32_t>(step) << shift;
-      count = __shfl_sync(0xFFFFFFFFu, n, step);
-    }
-    if (count == k) break;
   }
-  return v;
+  __syncthreads();
+  return sh.bound;
 }
 
 // The k first elements of the CTA's run into sh.key / sh.index (fewer where the run is
@@ -283,17 +278,21 @@ __device__ void select_top(const Run<T>& run, float top, int k, Shared& sh) {
   const bool any = tid < run.chunks || tid < run.head + run.tail;
   const uint32_t mine = any ? order_key(top) : 0u;
   if (tid < k) sh.key[tid] = 0, sh.index[tid] = -1;
-  for (int i = tid; i < 2 * kRounds * 16; i += kThreads) sh.counts[i / 16][i % 16] = 0;
   if (tid == 0) sh.count = sh.found = 0;
-  __syncwarp();
-  __syncthreads();
-  int reach;
-  uint32_t bound = kth_largest(mine, 32, k, sh.counts, reach);
-  if (bound == 0) bound = 1, reach = 0;  // fewer than k threads hold elements: all of theirs
-  bool holds = mine >= bound;
-  // Where too many threads tie at the bound: those whose first such element comes first.
+  // (0: fewer than k of them hold elements; then all there are)
+  const uint32_t bound = max(kth_largest(mine, k, sh), 1u);
+  auto take = [&](bool holds) {
+    if (holds) {
+      const int at = atomicAdd(&sh.count, 1);
+      if (at < kColumns) sh.columns[at] = tid;
+    }
+    __syncwarp();
+    __syncthreads();
+  };
+  take(mine >= bound);
+  // Where many threads tie at the bound: those whose first such element comes first.
   int last = 0x7FFFFFFF;
-  if (reach > kColumns) {
+  if (sh.count > kColumns) {
     int first = run.end;
     if (mine == bound) {
       if (tid < run.head + run.tail) {
@@ -310,19 +309,15 @@ __device__ void select_top(const Run<T>& run, float top, int k, Shared& sh) {
       }
     }
     __syncwarp();
-    // (threads above the bound, fewer than k, count as if theirs were before all)
+    // (threads above the bound count as if theirs were before all)
     const uint32_t left = mine > bound ? run.end - run.begin + 1 : mine == bound ? run.end - first : 0;
-    const uint32_t least = max(
-        kth_largest(left, 32 - __clz(run.end - run.begin + 1), k, sh.counts + kRounds, reach), 1u);
-    holds = left >= least;
+    const uint32_t least = max(kth_largest(left, k, sh), 1u);
     last = run.end - static_cast<int>(least);
+    if (tid == 0) sh.count = 0;
+    __syncwarp();
+    __syncthreads();
+    take(left >= least);
   }
-  if (holds) {
-    const int at = atomicAdd(&sh.count, 1);
-    if (at < kColumns) sh.columns[at] = tid;
-  }
-  __syncwarp();
-  __syncthreads();
   // Their elements: an item is a 16-byte chunk of one, or its loose element.
   const int columns = min(sh.count, kColumns);
   const int per = (run.chunks + kThreads - 1) / kThreads + 1, items = columns * per;
@@ -526,13 +521,19 @@ __global__ void __launch_bounds__(kThreads, kCluster ? 2 : kForwardPerSm)
         const int index = kCluster ? sh.all_index[warp][my] : sh.index[my];
         int place = my;
         if constexpr (kCluster) {
-          for (int q = 0; q < cluster; ++q) {
-            int n = 0;
-#pragma unroll 8
-            for (int i = 0; i < k; ++i)
-              n += before(sh.all_key[q][i], sh.all_index[q][i], key, index);
-            if (q != warp) place += n;
-          }
+          int n[kMaxCluster] = {};
+#pragma unroll
+          for (int step = kMaxTop; step > 0; step /= 2)
+#pragma unroll
+            for (int q = 0; q < kMaxCluster; ++q) {
+              const int to = min(n[q] + step, k);
+              if (q < cluster && n[q] + step <= k &&
+                  before(sh.all_key[q][to - 1], sh.all_index[q][to - 1], key, index))
+                n[q] = to;
+            }
+#pragma unroll
+          for (int q = 0; q < kMaxCluster; ++q)
+            if (q != warp) place += n[q];
         }
         if (out) {
           if (warp == 0 && lane < k) {
