@@ -269,6 +269,25 @@ __device__ __forceinline__ uint32_t kth_largest(uint32_t mine, int k, Shared& sh
   return sh.bound;
 }
 
+// The k first of the candidates, of which those from `bound` on matter, into sh.key / sh.index.
+// Ends in a barrier.
+__device__ __forceinline__ void rank_candidates(int k, uint32_t bound, Shared& sh) {
+  const int found = sh.found;
+  for (int i = threadIdx.x; i < found; i += kThreads) {
+    const uint32_t key = sh.cand_key[i];
+    const int index = sh.cand_index[i];
+    if (key < bound) continue;
+    int rank = 0;
+    for (int j = 0; j < found; ++j) rank += before(sh.cand_key[j], sh.cand_index[j], key, index);
+    if (rank < k) {
+      sh.key[rank] = key;
+      sh.index[rank] = index;
+    }
+  }
+  __syncwarp();
+  __syncthreads();
+}
+
 // The k first elements of the CTA's run into sh.key / sh.index (fewer where the run is
 // shorter: key 0). `top` is the thread's largest; all threads take part.
 template <typename T>
@@ -353,18 +372,13 @@ __device__ void select_top(const Run<T>& run, float top, int k, Shared& sh) {
   __syncthreads();
   const int found = sh.found;
   if (found <= kCandidates) {
-    for (int i = tid; i < found; i += kThreads) {
-      const uint32_t key = sh.cand_key[i];
-      const int index = sh.cand_index[i];
-      int rank = 0;
-      for (int j = 0; j < found; ++j) rank += before(sh.cand_key[j], sh.cand_index[j], key, index);
-      if (rank < k) {
-        sh.key[rank] = key;
-        sh.index[rank] = index;
-      }
+    uint32_t least = 0;
+    if (found > 2 * kColumns) {  // (short rows: a bound from all of them is closer)
+      uint32_t most = 0;
+      for (int i = tid; i < found; i += kThreads) most = max(most, sh.cand_key[i]);
+      least = kth_largest(most, k, sh);
     }
-    __syncwarp();
-    __syncthreads();
+    rank_candidates(k, least, sh);
     return;
   }
   // (rare: a few threads hold very many of the largest) one after another
@@ -485,8 +499,8 @@ __global__ void __launch_bounds__(kThreads, kCluster ? 2 : kForwardPerSm)
       __syncwarp();
       cluster_sync();
     }
-    if (rank == 0 && warp < (kTop ? cluster : 1)) {
-      // The row's S and T, from its CTAs' (each of these warps for itself).
+    if (rank == 0 && ((kCluster && kTop) || warp == 0)) {
+      // The row's S and T, from its CTAs' (each warp for itself).
       Partial all;
       if (lane < cluster) {
         const float3 part = kCluster ? sh.all[lane] : make_float3(sh.row_m, sh.row_s, sh.row_t);
@@ -495,7 +509,8 @@ __global__ void __launch_bounds__(kThreads, kCluster ? 2 : kForwardPerSm)
       __syncwarp();
       float most = all.m;
 #pragma unroll
-      for (int d = kMaxCluster / 2; d > 0; d /= 2) most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
+      for (int d = kMaxCluster / 2; d > 0; d /= 2)
+        most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, d));
       if (most > all.m) all.raise(most, c);
 #pragma unroll
       for (int d = kMaxCluster / 2; d > 0; d /= 2) {
@@ -506,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? 2 : kForwardPerSm)
       most = __shfl_sync(0xFFFFFFFFu, most, 0);
       const bool none = s == 0.0f;  // every logit is -inf
       const float log_s = none ? 0.0f : logf(s);
-      if (warp == 0 && lane == 0) {
+      if (tid == 0) {
         if (token >= a.vocab) report_index(a.status, kIndexToken);
         a.stats[r] = out ? make_float2(0.0f, 0.0f) : make_float2(none ? -INFINITY : most, log_s);
         a.logprob[r] = out ? 0.0f : none ? -INFINITY : fmaf(given - most, a.scale, -log_s);
@@ -514,36 +529,29 @@ __global__ void __launch_bounds__(kThreads, kCluster ? 2 : kForwardPerSm)
       }
       __syncwarp();
       if constexpr (kTop) {
-        // Warp o places list o's elements among all of them: as far behind the first as there
-        // are elements before it.
-        const int k = a.top, my = min(lane, k - 1);
-        const uint32_t key = kCluster ? sh.all_key[warp][my] : sh.key[my];
-        const int index = kCluster ? sh.all_index[warp][my] : sh.index[my];
-        int place = my;
-        if constexpr (kCluster) {
-          int n[kMaxCluster] = {};
-#pragma unroll
-          for (int step = kMaxTop; step > 0; step /= 2)
-#pragma unroll
-            for (int q = 0; q < kMaxCluster; ++q) {
-              const int to = min(n[q] + step, k);
-              if (q < cluster && n[q] + step <= k &&
-                  before(sh.all_key[q][to - 1], sh.all_index[q][to - 1], key, index))
-                n[q] = to;
-            }
-#pragma unroll
-          for (int q = 0; q < kMaxCluster; ++q)
-            if (q != warp) place += n[q];
-        }
-        if (out) {
-          if (warp == 0 && lane < k) {
-            a.top_logprob[r * k + lane] = 0.0f;
-            a.top_token[r * k + lane] = -1;
+        const int k = a.top;
+        if constexpr (kCluster) {  // the first of the CTAs' alternatives, one a thread
+          const bool in = warp < cluster && lane < k;
+          const uint32_t key = in ? sh.all_key[warp][lane] : 0u;
+          if (tid == 0) sh.found = 0;
+          const uint32_t bound = max(kth_largest(key, k, sh), 1u);
+          if (key >= bound) {
+            const int at = atomicAdd(&sh.found, 1);
+            sh.cand_key[at] = key;
+            sh.cand_index[at] = sh.all_index[warp][lane];
           }
-        } else if (lane < k && key != 0 && place < k) {
-          const float x = key_value(key);
-          a.top_logprob[r * k + place] = none ? -INFINITY : fmaf(x - most, a.scale, -log_s);
-          a.top_token[r * k + place] = index;
+          __syncwarp();
+          __syncthreads();
+          rank_candidates(k, 0, sh);
+        }
+        if (tid < k) {
+          const uint32_t key = sh.key[tid];
+          if (out || key != 0) {
+            a.top_logprob[r * k + tid] = out    ? 0.0f
+                                         : none ? -INFINITY
+                                                : fmaf(key_value(key) - most, a.scale, -log_s);
+            a.top_token[r * k + tid] = out ? -1 : sh.index[tid];
+          }
         }
       }
     }
