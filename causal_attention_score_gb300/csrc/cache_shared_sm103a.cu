@@ -69,7 +69,6 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_sm103a_kernel(con
   const SharedPlan& plan = a.plan;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = plan.group_count,
             S = v.sequences;
-  grid_dependents_launch();  // (which wait for this grid's end themselves)
   grid_dependency_wait();
   if (blockIdx.x > 0) {
     const long long n = (a.rows_heads + 3) / 4;
