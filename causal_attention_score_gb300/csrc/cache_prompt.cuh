@@ -221,12 +221,8 @@ __device__ Unit<kMode> decode_unit(const PromptArgs& a, int row_limit, const lon
       r.base = p.start;
       r.lead = p.lead;
       r.leader = p.leader;
-      r.first = r.pieces = 0;
-      if (p.group >= 0) {
-        const SharedGroup g0 = a.plan.groups[p.group];
-        r.first = shared_part(g0, a.group, r.head, (r.q.row0 - g0.row0) * a.group + r.row0);
-        r.pieces = g0.pieces;
-      }
+      r.first = shared_part(p.part0, p.group_rows, p.pieces, r.head, p.row + r.row0);
+      r.pieces = p.pieces;
       if (last >= p.start) r.n[g] = (last - p.start) / kTile + 1;
       continue;
     }
@@ -249,7 +245,7 @@ __device__ inline Unit<kSharedPart> decode_shared(const PromptArgs& a, int u) {
   r.base = unit.tile0 * kTile;
   r.n[0] = unit.tiles;
   r.n[1] = r.rows > kRows ? unit.tiles : 0;
-  r.first = shared_part(g, a.group, r.head, r.row0) + unit.piece;
+  r.first = shared_part(g.part0, g.rows * a.group, g.pieces, r.head, r.row0) + unit.piece;
   r.pieces = g.pieces;
   return r;
 }

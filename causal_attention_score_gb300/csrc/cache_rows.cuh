@@ -183,13 +183,15 @@ __device__ __forceinline__ void store_out(const AttendArgs& a, long long at, flo
 
 // What a sequence asks for: rows (tokens x group), their tiles of tokens (the
 // first `sink_tiles`, then those from `window_tile` on).
-// kShared: its first token (the first tile begins there), whose table row names which tokens, its
-// group, its first row in that; which of the group's pieces a unit of the shared part is.
+// kShared: its first token (the first tile begins there), whose table row names which tokens, where
+// its shared parts are (as in SharedSequence); which of the group's pieces a unit of the shared
+// part is.
 template <bool kShared>
 struct Shift {};
 template <>
 struct Shift<true> {
-  int start, lead, leader, group, row, part;
+  int start, lead, leader, group_rows, pieces, row, part;
+  long long part0;
 };
 template <bool kShared>
 struct SeqWork : Shift<kShared> {
@@ -206,8 +208,10 @@ __device__ __forceinline__ SeqWork<kShared> seq_work(const AttendArgs& a, int ro
     w.start = p.start;
     w.lead = p.lead;
     w.leader = p.leader;
-    w.group = p.group;
-    w.row = p.group < 0 ? 0 : (p.q.row0 - a.plan.groups[p.group].row0) * a.group;
+    w.part0 = p.part0;
+    w.group_rows = p.group_rows;
+    w.pieces = p.pieces;
+    w.row = p.row;
     w.part = 0;
     w.rows = p.q.n * a.group;
     if (w.rows > row_limit) w.rows = 0;
@@ -266,12 +270,13 @@ __device__ __forceinline__ void next_shared_unit(const AttendArgs& a, Piece<true
   if (p.at >= p.end) return;
   const int u = static_cast<int>(p.at);
   p.at += p.after;  // (the workers' number)
-  const int at = shared_group_of(a.plan, u);
-  const SharedGroup g = a.plan.groups[at];
+  const SharedGroup g = a.plan.groups[shared_group_of(a.plan, u)];
   const SharedUnit unit = shared_unit(g, a.v.heads, u);
   p.w.q = {g.row0, g.rows, g.tokens, 1 << 30};  // (behind every key)
   p.w.start = p.w.lead = 0;
-  p.w.group = at;
+  p.w.part0 = g.part0;
+  p.w.group_rows = g.rows * a.group;
+  p.w.pieces = g.pieces;
   p.w.row = 0;
   p.w.part = unit.piece;
   p.w.rows = g.rows * a.group;
@@ -879,8 +884,9 @@ __global__ void __launch_bounds__(128 * kGroups<HSP, NB>, 1)
     float* part = a.parts + static_cast<long long>(slot) * a.part_floats;
     if constexpr (kShared) {
       // Left for the joining, four elements at a time.
-      const int group = piece.w.group;
-      const SharedGroup gr = group < 0 ? SharedGroup{} : a.plan.groups[group];
+      const long long part0 = piece.w.part0;
+      const int group_rows = piece.w.group_rows, shared_pieces = piece.w.pieces;
+      const int rr0 = piece.w.row + row_first;
       for (int e = gtid; e < rows * (HSP / 4); e += 128) {
         const int r = e / (HSP / 4), d = e % (HSP / 4) * 4;
         const int idx = (d / kVBytes) * Smem::kColStride + d % kVBytes;
@@ -895,10 +901,8 @@ __global__ void __launch_bounds__(128 * kGroups<HSP, NB>, 1)
           const float half = ex2_approx(0.5f * (sm.m[k][r] - mm));
           lt += sm.l[k][r] * half * half;
         }
-        const long long at =
-            group < 0 ? 0 : shared_part(gr, a.group, piece.head, piece.w.row + row_first + r);
-        if (!CSA_CHECK(at >= 0 && (group < 0 || at + gr.pieces <= a.plan.parts), wd, kCheckTile))
-          continue;
+        const long long at = shared_part(part0, group_rows, shared_pieces, piece.head, rr0 + r);
+        if (!CSA_CHECK(at >= 0 && at + shared_pieces <= a.plan.parts, wd, kCheckTile)) continue;
         const int rr = row_first + r, j = rr / a.group;
         const long long own = static_cast<long long>(row0 + j) * (a.v.heads * a.group) + out_head +
                               (rr - j * a.group);
@@ -921,7 +925,7 @@ __global__ void __launch_bounds__(128 * kGroups<HSP, NB>, 1)
               whole ? 0
                     : static_cast<int>(min(1 + (piece.after + share - 1) / share,
                                            static_cast<long long>(workers - worker)));
-          a.plan.own[own] = OwnRow{at, gr.pieces, pieces, worker, r};
+          a.plan.own[own] = OwnRow{at, shared_pieces, pieces, worker, r};
           a.plan.own_there[own] = 1;
         }
       }

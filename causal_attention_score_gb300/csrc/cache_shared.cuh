@@ -31,10 +31,14 @@ struct SharedGroup {
 
 // A sequence as the plan read and checked it. Its tokens below `lead` are looked up in sequence
 // `leader`'s table row; those below `start` are the shared part's (start is 0 or lead).
-struct SharedSequence {
+struct alignas(16) SharedSequence {
   KvSequence q;
   int start, lead, leader;
   int group;  // -1: none, or one whose shared part is not worth a unit of its own
+  // Where its shared parts are (see shared_part): the group's first one, its query rows of a kv
+  // head and pieces, and this sequence's first query row there.
+  long long part0;
+  int group_rows, pieces, row;
 };
 
 // What the kernels of the own parts leave for one row and head, beside its maximum, sum and output:
@@ -71,10 +75,9 @@ struct SharedPlan {
   float* own_o;     // [..][padded head size]
 };
 
-__device__ __forceinline__ long long shared_part(const SharedGroup& g, int group_heads, int head,
-                                                 int rr) {
-  return g.part0 +
-         (static_cast<long long>(head) * g.rows * group_heads + rr) * g.pieces;
+__device__ __forceinline__ long long shared_part(long long part0, int group_rows, int pieces,
+                                                 int head, int rr) {
+  return part0 + (static_cast<long long>(head) * group_rows + rr) * pieces;
 }
 
 // The group of unit u.

@@ -32,6 +32,7 @@ namespace csa {
 namespace {
 
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanGroups = 64, kPlanSequences = 256;
 
 // From this many rows a group on average (tokens x query heads of a kv head) the shared part is
 // the tcgen05 kernel's.
@@ -65,10 +66,15 @@ struct PlanArgs {
 __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_sm103a_kernel(const PlanArgs a) {
   __shared__ int s_bad, s_most, s_chunk, s_sms;
   __shared__ unsigned long long s_saved, s_blocks, s_tiles, s_own, s_key[kPlanThreads / 32];
+  // (what fits is kept here until the end)
+  __shared__ SharedGroup s_groups[kPlanGroups];
+  __shared__ SharedSequence s_sequences[kPlanSequences];
   const KvView& v = a.v;
   const SharedPlan& plan = a.plan;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = plan.group_count,
             S = v.sequences;
+  SharedGroup* const groups = G <= kPlanGroups ? s_groups : plan.groups;
+  SharedSequence* const sequences = S <= kPlanSequences ? s_sequences : plan.sequences;
   grid_dependency_wait();
   if (blockIdx.x > 0) {
     const long long n = (a.rows_heads + 3) / 4;
@@ -90,7 +96,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_sm103a_kernel(con
     p.sequence = from;
     p.rows = to;  // (for now: where the group ends)
     p.tokens = ok ? tokens : -1;
-    plan.groups[g] = p;
+    groups[g] = p;
   }
   __syncthreads();
   const bool bad = s_bad != 0;  // then nothing is computed
@@ -106,11 +112,11 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_sm103a_kernel(con
     int lo = -1, hi = G;  // the last group that begins at s or before
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
-      if (plan.groups[mid].sequence <= s) lo = mid;
+      if (groups[mid].sequence <= s) lo = mid;
       else hi = mid;
     }
     if (lo >= 0 && r.q.n > 0) {
-      const SharedGroup p = plan.groups[lo];
+      const SharedGroup p = groups[lo];
       if (s < p.rows) {
         if (p.tokens < 0 || (p.tokens > 0 && r.q.first < p.tokens)) {
           report_index(v.status, p.tokens < 0 ? kIndexLength : kIndexRows);
@@ -128,7 +134,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_sm103a_kernel(con
     else if (rows > 0)
       own += (rows + a.own_rows - 1) / a.own_rows *
              (max((r.q.length - r.lead + a.own_tile - 1) / a.own_tile, 1) + a.own_start);
-    plan.sequences[s] = r;
+    sequences[s] = r;
   }
 #pragma unroll
   for (int d = 16; d > 0; d /= 2) own += __shfl_xor_sync(0xFFFFFFFFu, own, d);
@@ -138,12 +144,12 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_sm103a_kernel(con
   // The groups' rows: from the first to the last of their sequences that have any; and what a
   // shared part saves: all of their sequences but one would read its tokens again.
   for (int g = warp; g < G; g += kPlanThreads / 32) {
-    SharedGroup p = plan.groups[g];
+    SharedGroup p = groups[g];
     // (bounds out of order may be any numbers)
     const int from = bad ? 0 : p.sequence, to = bad ? 0 : p.rows;
     int row0 = INT_MAX, end = 0, members = 0;
     for (int s = from + lane; s < to; s += 32) {
-      const SharedSequence q = plan.sequences[s];
+      const SharedSequence q = sequences[s];
       if (q.group == g) {
         row0 = min(row0, q.q.row0);
         end = max(end, q.q.row0 + q.q.n);
@@ -159,7 +165,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_sm103a_kernel(con
     const int rest = row0 < end ? (end - row0) * a.group_heads % a.unit_rows : 0;
     if (a.drop && rest > 0 && rest <= kRowLimit && (end - row0) * a.group_heads > a.unit_rows) {
       const int s = to - 1 - lane;
-      const SharedSequence q = plan.sequences[max(s, 0)];
+      const SharedSequence q = sequences[max(s, 0)];
       const bool in = s >= from && q.group == g;
       const int first = in ? q.q.row0 : INT_MAX;
       const uint32_t there = __ballot_sync(0xFFFFFFFFu, in);
@@ -170,7 +176,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_sm103a_kernel(con
       if ((end - cut) * a.group_heads >= rest && (end - cut) * a.group_heads <= kRowLimit &&
           cut > row0) {
         if (in && first >= cut) {
-          plan.sequences[s].group = -1;
+          sequences[s].group = -1;
           const long long rows = static_cast<long long>(q.q.n) * a.group_heads;
           atomicAdd(&s_own, static_cast<unsigned long long>((rows + a.own_rows - 1) / a.own_rows *
                                                             (q.lead / a.own_tile)));
@@ -192,7 +198,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_sm103a_kernel(con
         atomicAdd(&s_saved, static_cast<unsigned long long>(members - 1) * p.tokens);
       }
     }
-    if (lane == 0) plan.groups[g] = p;
+    if (lane == 0) groups[g] = p;
     __syncwarp();
   }
   __syncthreads();
@@ -214,7 +220,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_sm103a_kernel(con
       const int chunk = (s_most + cut - 1) / cut;
       long long units = 0, parts = 0, tiles = 0;
       for (int g = 0; g < G; ++g) {
-        const SharedGroup p = plan.groups[g];
+        const SharedGroup p = groups[g];
         const long long pieces = (p.tiles + chunk - 1) / chunk;
         units += pieces * p.blocks * v.heads;
         tiles += static_cast<long long>(p.tiles) * p.blocks * v.heads;
@@ -252,7 +258,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_sm103a_kernel(con
     for (int g0 = 0; g0 < G; g0 += 32) {
       const int g = g0 + lane;
       SharedGroup p{};
-      if (g < G) p = plan.groups[g];
+      if (g < G) p = groups[g];
       p.pieces = worth ? (p.tiles + chunk - 1) / chunk : 0;
       long long units = static_cast<long long>(p.pieces) * p.blocks * v.heads;
       long long parts = static_cast<long long>(p.pieces) * p.rows * a.group_heads * v.heads;
@@ -265,7 +271,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_sm103a_kernel(con
       }
       p.unit0 = static_cast<int>(min(units_before + units - my_units, 0x7FFFFFFFll));
       p.part0 = parts_before + parts - my_parts;
-      if (g < G) plan.groups[g] = p;
+      if (g < G) groups[g] = p;
       units_before += __shfl_sync(0xFFFFFFFFu, units, 31);
       parts_before += __shfl_sync(0xFFFFFFFFu, parts, 31);
     }
@@ -285,17 +291,25 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_sm103a_kernel(con
   }
   __syncthreads();
   for (int s = tid; s < S; s += kPlanThreads) {
-    SharedSequence& r = plan.sequences[s];
+    SharedSequence r = sequences[s];
     if (r.group >= 0) {
       // (its rows are the group's, whatever the offsets are)
-      const SharedGroup p = plan.groups[r.group];
-      if (p.pieces > 0 && r.q.row0 >= p.row0 && r.q.row0 + r.q.n <= p.row0 + p.rows)
+      const SharedGroup p = groups[r.group];
+      if (p.pieces > 0 && r.q.row0 >= p.row0 && r.q.row0 + r.q.n <= p.row0 + p.rows) {
         r.start = r.lead;
-      else
+        r.part0 = p.part0;
+        r.group_rows = p.rows * a.group_heads;
+        r.pieces = p.pieces;
+        r.row = (r.q.row0 - p.row0) * a.group_heads;
+      } else {
         r.group = -1;
+      }
     }
     if (s_bad) r.q.n = 0;
+    plan.sequences[s] = r;
   }
+  if (G <= kPlanGroups)
+    for (int g = tid; g < G; g += kPlanThreads) plan.groups[g] = groups[g];
 }
 
 // kWarps warps a row and head: its own part, whole or in pieces, and its shared ones, in a fixed
