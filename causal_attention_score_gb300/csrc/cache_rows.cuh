@@ -1,4 +1,6 @@
-// The kernels of cache_attention_sm103a.cu and, with kShared, of cache_shared_sm103a.cu.
+// The kernels of cache_attention_sm103a.cu and, with kShared, of cache_shared_sm103a.cu: there a
+// sequence begins at its first own token (or, for the shared part, a unit is rows of many
+// sequences), and what a unit leaves is joined later.
 //
 // Attention of new tokens over the paged 8-bit cache, for few rows per
 // sequence and kv head (decoding): row r of a sequence sits at position p and
@@ -378,7 +380,8 @@ __global__ void __launch_bounds__(128 * kGroups<HSP, NB>, 1)
   constexpr int kTilesM = HSP / 16;       // m-tiles of the output
 
   // (beside the shared part: that kernel let this one start when the plan was complete)
-  if (!kShared || !a.beside) grid_dependency_wait();
+  if (kShared && a.beside) __threadfence();
+  else grid_dependency_wait();
   if (kShared && a.prefix) grid_dependents_launch();
   int workers = a.workers;
   if constexpr (kShared)

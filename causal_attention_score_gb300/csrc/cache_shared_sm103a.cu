@@ -11,11 +11,20 @@
 //
 // Launches: a plan (the batch's entries read and checked once, units of the shared part and where
 // their results go), the shared part, the own parts (and those of sequences with many rows, where
-// there may be any, on tcgen05), and the joining, a warp for each row and head. The shared part is
-// cut along its tokens too, as far as SMs are left without work.
+// there may be any, on tcgen05), and the joining. The shared part is cut along its tokens too, as
+// far as SMs are left without work. The own parts do not wait for it: the shared part's kernel
+// takes as many SMs as the plan gives it and lets the other start on the rest (64 answers to a
+// prompt of 8192 tokens, 32 query and 8 kv heads of 128: 49 us, and 58 one after the other). The
+// joining is a kernel of its own: taking the shared parts in at the end of every own unit cost
+// that kernel 9 of 34 us there and 40 of 100 with 200 sequences.
 //
 // The shared part goes to the tcgen05 kernel (256 rows x 64 keys a step; its units here have no
 // masks) where the groups have rows enough, to the kernel of few rows otherwise.
+//
+// Bound: for long shared parts the tcgen05 kernel's step (1.3 us for 256 rows x 64 keys of 128
+// elements, 6.5 of 12.4 TFLOP/s an SM; 64 x 1 token over 65536 shared: 102 us, 1050 with every
+// sequence reading them), for short ones the launches (17 us for 2 sequences over 1024 tokens) and
+// the own units' beginnings and ends.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -35,11 +44,14 @@ constexpr int kPlanThreads = 1024;
 constexpr int kPlanGroups = 64, kPlanSequences = 256;
 
 // From this many rows a group on average (tokens x query heads of a kv head) the shared part is
-// the tcgen05 kernel's.
+// the tcgen05 kernel's: over 65536 tokens (8 kv heads) 16 and 32 rows take 65 and 89 us there and
+// 65 and 87 here, 64 rows 89 there and 150 here; over 4 groups of 8192 32 rows take 66 there, 60 here.
 constexpr int kPrefixFrom = 33;
 // Below so many bytes of codes that it would keep from being read again (by all SMs), the shared
-// part is not worth its launches: sequences read it for themselves.
-constexpr long long kWorthBytes = 96LL << 20;
+// part is not worth its launches and sequences read it for themselves: with 66 MB (64 x 1 token
+// over 512) it takes 28 us with a shared part and 32 without, with 33 MB (over 256) 27 and 28, with
+// 30 MB (20 over 5008, 2 heads of 80) 28 and 25, with 16 MB (64 over 128) 27 and 25.
+constexpr long long kWorthBytes = 32LL << 20;
 // Room for parts beyond one for each row and head: what cutting along the tokens may take.
 constexpr long long kSpareParts = 2LL * kMaxSms * kPrefixRows;
 
@@ -435,7 +447,8 @@ __global__ void __launch_bounds__(128) shared_join_sm103a_kernel(const AttendArg
 template <int HSP>
 cudaError_t launch_join(const AttendArgs& a, int q_heads, long long rows_heads, int sms,
                         cudaStream_t stream) {
-  // Four warps a row while there are places for all of them at once.
+  // Four warps a row while there are places for all of them at once (64 rows of 57 pieces take 8 us
+  // with four warps each, 21 with one).
   const long long most = 16LL * sms;
   return rows_heads <= most
              ? launch_programmatic(shared_join_sm103a_kernel<HSP, 4>,
@@ -503,6 +516,8 @@ int cache_attention_shared_launch(const csa_kv_cache& cache, const csa_kv_batch&
   const bool eight =
       most_rows <= 8 || (a.group <= 8 && (prompts || batch_rows <= 8LL * batch.sequences));
 
+  // The times that the plan weighs the two parts by (measured as the best of 9 divisions of the SMs
+  // for 12 batches; what it chooses is within 5 % of those).
   // What the kernel of few rows needs for a tile: an SM's groups take its codes at 38 GB/s between
   // them (5.8 TB/s over all), or twice as long with 16 rows.
   auto groups_of = [&](bool of_eight) {
