@@ -215,6 +215,30 @@ def test_number_of_pages(pages):
     assert books.table[2, :first].tolist() == expect[free[:first]].tolist()
 
 
+@pytest.mark.parametrize("pages,n", [(3000, 513), (40000, 700), (40000, 3), (33000, 1500)])
+def test_many_entries(pages, n):
+    """Entries in several rounds of the planning CTA, pages in many chunks."""
+    cache = csa.KvCache.empty(pages, 1, 16, 16)
+    books = csa.KvPages.empty(cache, n + 5, 8)
+    want = Books(books.refs, books.lengths, books.table, 16)
+    rng = random.Random(n)
+    for _ in range(3):
+        at = rng.sample(range(n + 5), n)
+        more = [rng.choice((0, 1, 16, 30)) for _ in at]
+        status = want.extend(at, more)
+        csa.kv_pages_extend(books, ints(at), ints(more))
+        assert csa.get_status() in (status or {0})
+        want.check(books)
+        gone = rng.sample(range(n + 5), n // 3)
+        csa.kv_pages_free(books, ints(gone))
+        want.free(gone)
+    moves, used = ints([0] * pages), ints([0])
+    csa.kv_cache_compact(cache, books, moves, used)
+    m, u = want.compact()
+    assert csa.get_status() == 0 and moves.tolist() == m and used.item() == u
+    want.check(books)
+
+
 def test_captured_and_on_other_streams():
     """A turn (end, fork, extend, compact) captured once and replayed from other books; two caches on
     two streams with workspaces of their own."""
