@@ -179,7 +179,8 @@ struct SmemSetting {
   int device;
   int bytes;
 };
-SmemSetting g_smem_set[64];
+constexpr int kMaxSmemSettings = 256;  // kernels with dynamic shared memory, and devices
+SmemSetting g_smem_set[kMaxSmemSettings];
 int g_smem_count = 0;
 
 }  // namespace
@@ -204,7 +205,7 @@ int set_max_dynamic_smem(const void* kernel, int bytes, int device, std::string&
     err = std::string("cudaFuncSetAttribute: ") + cudaGetErrorString(r);
     return CSA_ERR_LAUNCH;
   }
-  if (g_smem_count < 64) g_smem_set[g_smem_count++] = SmemSetting{kernel, device, bytes};
+  if (g_smem_count < kMaxSmemSettings) g_smem_set[g_smem_count++] = SmemSetting{kernel, device, bytes};
   return CSA_OK;
 }
 
