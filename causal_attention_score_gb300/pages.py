@@ -81,6 +81,12 @@ def _list(t: torch.Tensor, name: str, n: int, dev: int) -> int:
     return t.data_ptr()
 
 
+def _entries(t: torch.Tensor, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    return t.numel()
+
+
 def _scratch(workspace, pages: KvPages, n: int, stream, dev: int):
     """(workspace, stream): the caller's workspace checked, or one of our own."""
     if workspace is None:
@@ -94,7 +100,7 @@ def kv_pages_extend(pages: KvPages, sequences: torch.Tensor, more: torch.Tensor,
     """Room for ``more[i]`` more tokens of sequence ``sequences[i]`` (int32 tensors): lengths grow,
     free pages are given to new blocks, lowest number first; see kv_pages_extend in
     include/csa.h."""
-    dev, n = _get_device(), sequences.numel()
+    dev, n = _get_device(), _entries(sequences, "sequences")
     ref = pages._pointer(dev)
     at, count = _list(sequences, "sequences", n, dev), _list(more, "more", n, dev)
     workspace, stream = _scratch(workspace, pages, n, stream, dev)
@@ -109,7 +115,7 @@ def kv_cache_fork(cache: KvCache, pages: KvPages, parents: torch.Tensor, childre
     """Place ``children[i]`` (of length 0) becomes a sequence of the first ``tokens[i]`` tokens of
     ``parents[i]`` (None: all of them): whole pages are shared, the written part of a last one is
     copied; see kv_cache_fork in include/csa.h."""
-    dev, n = _get_device(), children.numel()
+    dev, n = _get_device(), _entries(children, "children")
     ref, books = cache._pointer(dev), pages._pointer(dev)
     p, c = _list(parents, "parents", n, dev), _list(children, "children", n, dev)
     t = None if tokens is None else _list(tokens, "tokens", n, dev)
@@ -123,7 +129,7 @@ def kv_cache_fork(cache: KvCache, pages: KvPages, parents: torch.Tensor, childre
 def kv_pages_free(pages: KvPages, sequences: torch.Tensor, stream=None) -> None:
     """The sequences at ``sequences`` (int32) end: their lengths become 0, and pages that no other
     names are free; see kv_pages_free in include/csa.h."""
-    dev, n = _get_device(), sequences.numel()
+    dev, n = _get_device(), _entries(sequences, "sequences")
     rc = (_lib._lib or _lib.load()).kv_pages_free(
         pages._pointer(dev), _list(sequences, "sequences", n, dev), n, _stream_ptr(stream, dev))
     if rc:
@@ -134,7 +140,7 @@ def kv_cache_copy(to: KvCache, from_: KvCache, to_pages: torch.Tensor, from_page
                   stream=None) -> None:
     """Page ``to_pages[i]`` of cache ``to`` becomes a copy of page ``from_pages[i]`` of ``from_``
     (int32 tensors; the caches' pages are alike); see kv_cache_copy in include/csa.h."""
-    dev, n = _get_device(), to_pages.numel()
+    dev, n = _get_device(), _entries(to_pages, "to_pages")
     rc = (_lib._lib or _lib.load()).kv_cache_copy(
         to._pointer(dev), from_._pointer(dev), _list(to_pages, "to_pages", n, dev),
         _list(from_pages, "from_pages", n, dev), n, _stream_ptr(stream, dev))

@@ -386,8 +386,8 @@ def cache_attention_shared_forward(out: torch.Tensor, q: torch.Tensor, cache: Kv
     shape = (batch.rows, q_heads, cache.head_size)
     qt, qh = _rows(q, "q", shape, _HALF, dev)
     ot, oh = _rows(out, "out", shape, (dtype,), dev)
-    _need(shared, "shared", torch.int32, shared.numel())
-    G = shared.numel()
+    G = shared.numel() if isinstance(shared, torch.Tensor) else 0
+    _need(shared, "shared", torch.int32, G)
     _need(groups, "groups", torch.int32, G + 1)
     for name, t in (("groups", groups), ("shared", shared)):
         if t.get_device() != dev:

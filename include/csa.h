@@ -12,8 +12,12 @@
  * (trimul_forward_noalloc). For training on and answering with such layers: rotary
  * positions and their gradient (rotary_forward, rotary_backward), a paged 8-bit cache of
  * keys and values (kv_cache_write, kv_cache_read), and attention over that cache for single
- * tokens and whole prompts (cache_attention_forward). Each is documented at its
- * declaration below.
+ * tokens and whole prompts (cache_attention_forward). For several answers to one prompt: the
+ * books of such a cache (kv_pages_extend, kv_cache_fork, kv_pages_free, kv_cache_copy,
+ * kv_cache_compact), attention that reads what sequences share once
+ * (cache_attention_shared_forward), and log probabilities of tokens with their gradient
+ * (token_logprobs_forward, token_logprobs_backward). Each is documented at its declaration
+ * below.
  *
  *  trimul_forward  the causal triangular score product of
  *                  "llm.c dev/cuda/trimat_forward.cu" (the CPU referee
@@ -40,7 +44,7 @@
  *    trimul_forward_noalloc (plus the page-locked completion words below).
  *  - bf16 inputs are passed as `const void*` to raw 16-bit bfloat16 values.
  *  - Outputs are fp32 and fully overwritten (no read-modify-write), but for the rotary,
- *    cache and cache-attention calls, which name their types and what they leave.
+ *    cache, cache-attention, pages and logits calls, which name their types and what they leave.
  *  - `stream` is a cudaStream_t passed as void*; NULL is the legacy default
  *    stream. Calls are asynchronous on that stream; argument errors are
  *    returned synchronously before anything is launched.
@@ -329,10 +333,11 @@ csa_status csa_dense_tiling(int M, int H, int sms, int* bn, int* pairs);
  * disjoint SMs, as long as the first is launched first (clusters need whole pairs
  * of SMs). max_sms = 0 removes the limit; a limit above the device's SM count has
  * no effect. Results are the same bits under any limit, but for cache_attention_forward,
- * whose sums are split by it. The rotary and cache calls and the second, short kernel of
- * cache_attention_forward have small CTAs, of which a limit allows in proportion (8 to 48
- * for each of max_sms): it bounds their share of the memory system, not the SMs they are
- * on. Limits are keyed by the
+ * cache_attention_shared_forward and token_logprobs_forward, whose sums are split by it. The
+ * rotary, cache, pages and logits calls and the last, short kernels of the attention calls have
+ * small CTAs, of which a limit allows in proportion (2 to 48 for each of max_sms;
+ * kv_pages_extend, kv_cache_fork and kv_pages_free take some for each entry): it bounds their
+ * share of the memory system, not the SMs they are on. Limits are keyed by the
  * stream's handle value, process-wide, for at most 64 streams at once (then
  * CSA_ERR_BUSY); a stream destroyed with a limit set should have it removed
  * first, since a new stream may reuse the handle. Returns CSA_OK, CSA_ERR_SHAPE
@@ -612,8 +617,8 @@ csa_status cache_attention_shared_forward(void* out, const void* q, int dtype, i
  * csa_get_status reports CSA_ERR_INDEX: a place outside [0, sequences), a length outside
  * [0, table_width * page_tokens] before or after, a page outside [0, pages) (skipped), a place
  * that an earlier entry of the call extends or forks into. Free pages are given out lowest number
- * first, in the order of the entries; an entry whose pages are no longer there, all entries before
- * it served, is left as it was, reported as CSA_ERR_PAGES.
+ * first, in the order of the entries; an entry for which too few are left, as if all entries before
+ * it had got theirs, is left as it was and reported as CSA_ERR_PAGES.
  *
  * kv_pages_extend -- room for more[i] >= 0 more tokens of sequences[i]: its length grows by them
  * and pages are given to the blocks that it had none for (a place of length 0 begins a sequence).
@@ -622,7 +627,9 @@ csa_status cache_attention_shared_forward(void* out, const void* q, int dtype, i
  * kv_cache_fork -- children[i], a place of length 0, becomes a sequence of the first tokens[i]
  * tokens of parents[i] (tokens NULL: of all of them). Whole pages are shared, their refs grow; where
  * the last one is whole only in part, its written slots and its scales are copied to a page of the
- * child's own. A parent may have any number of children; a place is not both in one call.
+ * child's own. A parent may have any number of children; a place is not both in one call. (A
+ * sequence is shortened by forking its first tokens and ending it: a length alone must not be
+ * lowered into a page that others share.)
  *
  * kv_pages_free -- sequences[i] ends: its length becomes 0 and the refs of its pages go down by
  * one each; those that reach 0 are free. A place named twice, or of length 0, has nothing to end.
@@ -741,11 +748,11 @@ const char* csa_version(void);
  * csa_debug_inject -- when nonzero, the next kernel launch (any entry point)
  *   withholds one hand-off in every CTA: the first operand load (score
  *   products, the softmax's first Q tile, the dense layer's TMA form, the first codes of
- *   attention over prompts) or the first stage arrival (the dense layer's loader-warp
+ *   attention over prompts and over a shared part) or the first stage arrival (the dense layer's loader-warp
  *   forms), so a bounded wait
  *   downstream runs out; the kernel records CSA_ERR_TIMEOUT and returns with its
  *   output incomplete. Consumed by that launch (kernels without such waits, those of
- *   the rotary and cache calls and of attention for few rows, leave it set).
+ *   the rotary, cache, pages and logits calls and of attention for few rows, leave it set).
  */
 void csa_set_wait_limit_ns(uint64_t ns);
 uint64_t csa_get_wait_limit_ns(void);

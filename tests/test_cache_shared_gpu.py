@@ -275,6 +275,23 @@ def test_a_wait_that_runs_out_is_reported(sms):
     assert csa.get_status() == 0 and torch.equal(out, good)
 
 
+def test_one_sm(sms):
+    b = ref.SharedBatch([1, 2, 1, 40], [7, 90, 0, 3], [(0, 3, 160), (3, 4, 64)], 2, 64, 32, "int8", seed=13)
+    q = b.rows_of(8, torch.bfloat16)
+    cache, batch = b.device(csa)
+    st = torch.cuda.Stream()
+    csa.set_stream_sm_limit(st, 1)
+    try:
+        out = torch.full((b.rows, 8, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+        x = q.cuda()
+        torch.cuda.synchronize()
+        csa.cache_attention_shared_forward(out, x, cache, batch, *b.lists(), stream=st)
+        assert csa.get_status(st) == 0
+    finally:
+        csa.set_stream_sm_limit(st, 0)
+    check(b, q, out)
+
+
 def test_same_bits_every_time():
     b = ref.SharedBatch([1] * 30, [(i * 17) % 90 for i in range(30)], [(0, 30, 1600)], 2, 64, 32, "int8", seed=12)
     _, want = run(b, 8, torch.bfloat16)
@@ -283,9 +300,9 @@ def test_same_bits_every_time():
         assert torch.equal(got, want)
 
 
-def test_many_sequences_and_groups_share_where_it_pays(sms):
-    """As many as the plan's threads take in several rounds; one long shared part among short ones."""
-    S, G = 1300, 60
+@pytest.mark.parametrize("S,G", [(1300, 60), (270, 100), (200, 3)])
+def test_many_sequences_and_groups(sms, S, G):
+    """More than the plan's threads take at once, or keep to themselves."""
     bounds = [S * g // G for g in range(G + 1)]
     groups = [(bounds[g], bounds[g + 1], 16 * (g % 4)) for g in range(G)]
     b = ref.SharedBatch([1] * S, [i % 3 for i in range(S)], groups, 1, 16, 16, "int8", seed=14)

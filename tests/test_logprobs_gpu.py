@@ -254,6 +254,31 @@ def test_streams_graph_and_sm_limit():
         close(few[i], ref_want[name], bound[name], name)
 
 
+def test_past_2_to_the_31():
+    """Rows that lie more than 2^31 elements and 2^32 bytes into the logits."""
+    rows, V = 45000, 50257
+    x = torch.empty((rows, V), dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(2)
+    at = [0, 20000, 42731, 44999]
+    x.fill_(-1.5)
+    for r in at:
+        x[r] = torch.randn((V,), generator=g, device="cuda") * 3
+    tokens = torch.full((rows,), -1, dtype=torch.int32, device="cuda")
+    tokens[at] = torch.tensor([5, 50256, 777, 31000], dtype=torch.int32, device="cuda")
+    got = csa.token_logprobs(x, tokens, 3)
+    want, bound = ref.forward(x[at].cpu(), tokens[at].cpu(), 1.0, 3)
+    assert torch.equal(got[4][at].cpu().long(), want["top_token"])
+    close(got[0][at], want["logprob"], bound["logprob"], "logprob")
+    d = torch.ones((rows,), device="cuda")
+    wd, bd = ref.backward(x[at].cpu(), tokens[at].cpu(), 1.0, d[at].cpu())
+    csa.token_logprobs_backward(x, x, tokens, got[2], got[1], d)
+    assert csa.get_status() == 0
+    close(x[at], wd, bd, "in place", torch.bfloat16)
+    left_out = torch.ones((rows,), dtype=torch.bool, device="cuda")
+    left_out[at] = False
+    assert not x[left_out].any()
+
+
 def test_from_a_dense_layer():
     """Logits as a dense layer writes them, then the gradient by that layer's input."""
     g = torch.Generator().manual_seed(1)

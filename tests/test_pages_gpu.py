@@ -183,6 +183,32 @@ def test_large_pages_are_copied_whole():
     want.check(books, pools)
 
 
+def test_pages_past_2_to_the_32():
+    """Pages whose codes begin more than 2^32 bytes into the cache."""
+    cache = csa.KvCache.empty(34000, 8, 128, 128)  # 131072 bytes a page, 4.5 GB each of K and V
+    for t in (cache.k, cache.v):
+        t[0], t[33999], t[33000] = 1, 3, 4
+    cache.k_scale.fill_(0.5)
+    refs = torch.zeros((34000,), dtype=torch.int32, device="cuda")
+    refs[33000] = refs[33999] = 1
+    table = torch.tensor([[33000, 33999], [0, 0], [0, 0]], dtype=torch.int32, device="cuda")
+    books = csa.KvPages(refs, ints([200, 0, 0]), table, 128)
+    refs[:33990] += 1
+    refs[33000] -= 1
+    csa.kv_cache_fork(cache, books, ints([0]), ints([1]))  # its last page: 33990
+    assert csa.get_status() == 0 and books.table[1].tolist() == [33000, 33990]
+    assert bool((cache.k[33990, :, :72] == 3).all()) and bool((cache.v[33990, :, :72] == 3).all())
+    csa.kv_cache_copy(cache, cache, ints([33998]), ints([33000]))
+    assert bool((cache.k[33998] == 4).all()) and bool((cache.v[33998] == 4).all())
+    refs[:100] = 0
+    moves, used = ints([0] * 34000), ints([0])
+    csa.kv_cache_compact(cache, books, moves, used)
+    assert csa.get_status() == 0 and used.item() == 33892
+    end = moves[33999].item()
+    assert end == 99 and bool((cache.k[end] == 3).all()) and books.table[0].tolist() == [33000, 99]
+    assert bool((cache.v[books.table[1, 1].item(), :, :72] == 3).all())
+
+
 @pytest.mark.parametrize("pages", [1, 31, 33, 1024, 1025, 1024 * 1024 + 3, 2500000])
 def test_number_of_pages(pages):
     """Free pages are found at any number of pages, wherever they are."""
