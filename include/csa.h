@@ -615,7 +615,7 @@ csa_status cache_attention_shared_forward(void* out, const void* q, int dtype, i
  * All of these run on the device, asynchronous on `stream`, and may be captured; none allocates.
  * Lists of entries are device int32 arrays of n >= 1. An entry that breaks a rule is left out and
  * csa_get_status reports CSA_ERR_INDEX: a place outside [0, sequences), a length outside
- * [0, table_width * page_tokens] before or after, a page outside [0, pages) (skipped), a place
+ * [0, table_width * page_tokens] or past 2^31 - 1 before or after, a page outside [0, pages) (skipped), a place
  * that an earlier entry of the call extends or forks into. Free pages are given out lowest number
  * first, in the order of the entries; an entry for which too few are left, as if all entries before
  * it had got theirs, is left as it was and reported as CSA_ERR_PAGES.

@@ -265,6 +265,20 @@ def test_many_entries(pages, n):
     want.check(books)
 
 
+def test_length_past_31_bits():
+    """A table with room for more tokens than a length can say: the entry is left out."""
+    width = 2 ** 24 + 2
+    refs, table = torch.zeros(8, dtype=torch.int32, device="cuda"), torch.zeros((2, width), dtype=torch.int32, device="cuda")
+    lengths = ints([2 ** 31 - 100, 0])
+    books = csa.KvPages(refs, lengths, table, 128)
+    csa.kv_pages_extend(books, ints([0, 1]), ints([200, 130]))
+    assert csa.get_status() == INDEX
+    assert lengths.tolist() == [2 ** 31 - 100, 130] and refs.tolist() == [1, 1] + [0] * 6
+    csa.kv_pages_extend(books, ints([0]), ints([99]))
+    assert csa.get_status() == 0 and lengths.tolist() == [2 ** 31 - 1, 130]
+    assert not table[0].any() and table[1, :3].tolist() == [0, 1, 0]
+
+
 def test_captured_and_on_other_streams():
     """A turn (end, fork, extend, compact) captured once and replayed from other books; two caches on
     two streams with workspaces of their own."""
