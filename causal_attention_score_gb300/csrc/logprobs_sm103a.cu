@@ -21,9 +21,16 @@
 //
 // Bound: HBM, one read of the logits (and one write of the gradient). A CTA of 256 threads takes
 // a row and four 16-byte loads a thread at once; six such CTAs an SM, so that some load while
-// others rank. 8192 x 50257 in fp32 with two alternatives: 255 us (6.5 TB/s, 0.96 of the copy
-// rate; five CTAs 261, four 283, two of 512 threads 323). Few rows are split over a cluster of up
-// to eight CTAs, whose results meet in the first one's shared memory.
+// others rank. 8192 x 50257 in fp32 with two alternatives: 244 us (6.75 TB/s, the copy rate; five
+// CTAs 253, four 270); in bf16 with the gradient behind it, of five CTAs an SM, 380 us (four 380,
+// six 384; a read of the logits beside the gradient's write goes at 6.5 TB/s). Few rows are split
+// over a cluster of up to eight CTAs, whose results meet in the first one's shared memory: 48 x
+// 50257 in fp32 with five alternatives 8.8 us, a chain of loads, bound, second look and barriers.
+//
+// A token nearly certain has log p = -log S with S next to 1: right to fp32's half step of 1,
+// which is what the sum is held to, not to a part of itself. Leaving the largest element out of
+// the sum and log1p of the rest would give that, and cost 8 % of the time with the gradient and
+// 15 % of a few rows'.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
