@@ -134,6 +134,7 @@ void apply_stream_sm_limit(DeviceInfo& info, cudaStream_t stream) {
   std::lock_guard<std::mutex> lock(g_limit_mu);
   for (int i = 0; i < g_limit_count; ++i)
     if (g_limits[i].stream == stream) {
+      info.limited = g_limits[i].sms < info.sm_count;
       info.sm_count = std::max(1, std::min(info.sm_count, g_limits[i].sms));
       return;
     }

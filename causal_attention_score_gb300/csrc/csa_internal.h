@@ -15,6 +15,7 @@ namespace csa {
 struct DeviceInfo {
   int device = -1;
   int sm_count = 0;
+  bool limited = false;  // sm_count is the stream's limit, not the device's
   int cc = 0;              // major * 10 + minor
   int max_smem_optin = 0;  // bytes of dynamic shared memory a block may opt into
   int* status_word = nullptr;  // device address of the [code, site] status pair

@@ -22,8 +22,8 @@
 // Bound: HBM, one read of the logits (and one write of the gradient). A CTA of 256 threads takes
 // a row and four 16-byte loads a thread at once; six such CTAs an SM, so that some load while
 // others rank. 8192 x 50257 in fp32 with two alternatives: 244 us (6.75 TB/s, the copy rate; five
-// CTAs 253, four 270); in bf16 with the gradient behind it, of five CTAs an SM, 380 us (four 380,
-// six 384; a read of the logits beside the gradient's write goes at 6.5 TB/s). Few rows are split
+// CTAs 253, four 270); in bf16 with the gradient behind it, of five CTAs an SM, 351 us (four 360,
+// six 350; a read of the logits beside the gradient's write goes at 6.7 TB/s). Few rows are split
 // over a cluster of up to eight CTAs, whose results meet in the first one's shared memory: 48 x
 // 50257 in fp32 with five alternatives 8.8 us, a chain of loads, bound, second look and barriers.
 //
@@ -50,6 +50,13 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kForwardPerSm = 6, kBackwardPerSm = 5;  // CTAs an SM
+// Rows (or parts of them) of so many bytes have a CTA each, given to an SM when a place is free
+// there: rows left out then keep no place. Shorter ones are taken in turn by as many CTAs as there
+// are places for (8192 x 50257 in bf16, a tenth left out: forward 117 us, 134 in turn, backward 232
+// and 253; 32768 x 8000 in bf16 122 and 136, 192 and 183; 131072 x 2000 in fp32 356 and 339, 576
+// and 492).
+constexpr long long kForwardRowBytes = 16000, kBackwardRowBytes = 32000;
+constexpr long long kMostCtas = 1LL << 30;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxTop = 32;
 constexpr int kMaxCluster = 8;
@@ -704,7 +711,9 @@ cudaError_t launch_forward(ForwardArgs a, const DeviceInfo& dev, cudaStream_t st
          bytes / (2 * a.cluster) >= 8192)
     a.cluster *= 2;
   const int per_sm = a.cluster > 1 ? 2 : kForwardPerSm;
-  const long long most = std::max(per_sm * dev.sm_count / a.cluster, 1);
+  const long long most = a.cluster == 1 && bytes >= kForwardRowBytes && !dev.limited
+                             ? kMostCtas
+                             : std::max(per_sm * dev.sm_count / a.cluster, 1);
   const unsigned grid = static_cast<unsigned>(std::min(a.rows, most) * a.cluster);
   if (a.cluster > 1)
     return launch_programmatic_cluster(a.top > 0 ? logprobs_forward_sm103a_kernel<T, true, true>
@@ -722,7 +731,8 @@ cudaError_t launch_backward(BackwardArgs a, const DeviceInfo& dev, cudaStream_t 
   a.parts = 1;
   const long long most = static_cast<long long>(kBackwardPerSm) * dev.sm_count;
   while (a.rows * a.parts < most && bytes / (2 * a.parts) >= 8192) a.parts *= 2;
-  const unsigned grid = static_cast<unsigned>(std::min(a.rows * a.parts, most));
+  const unsigned grid = static_cast<unsigned>(std::min(
+      a.rows * a.parts, bytes / a.parts >= kBackwardRowBytes && !dev.limited ? kMostCtas : most));
   const bool vector =
       reinterpret_cast<uintptr_t>(a.logits) % 16 == reinterpret_cast<uintptr_t>(a.dlogits) % 16 &&
       (a.rows == 1 || (a.stride - a.d_stride) * static_cast<long long>(sizeof(T)) % 16 == 0);
