@@ -19,7 +19,8 @@
 // reaches the bound is ranked by counting. Where many threads' maxima tie at the bound, the
 // index of their first such element tells them apart.
 //
-// Bound: HBM, one read of the logits (and one write of the gradient). A CTA of 256 threads takes
+// Bound: HBM, one read of the logits (and one write of the gradient). Short rows have a warp each,
+// without barriers (figures below). Else a CTA of 256 threads takes
 // a row and four 16-byte loads a thread at once; six such CTAs an SM, so that some load while
 // others rank. 8192 x 50257 in fp32 with two alternatives: 244 us (6.75 TB/s, the copy rate; five
 // CTAs 253, four 270); in bf16 with the gradient behind it, of five CTAs an SM, 351 us (four 360,
@@ -50,13 +51,26 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kForwardPerSm = 6, kBackwardPerSm = 5;  // CTAs an SM
-// Rows (or parts of them) of so many bytes have a CTA each, given to an SM when a place is free
-// there: rows left out then keep no place. Shorter ones are taken in turn by as many CTAs as there
-// are places for (8192 x 50257 in bf16, a tenth left out: forward 117 us, 134 in turn, backward 232
-// and 253; 32768 x 8000 in bf16 122 and 136, 192 and 183; 131072 x 2000 in fp32 356 and 339, 576
-// and 492).
-constexpr long long kForwardRowBytes = 16000, kBackwardRowBytes = 32000;
+// Each row, or part of one, has a CTA, given to an SM when a place is free there: rows left out
+// then keep no place (8192 x 50257 in bf16, a tenth left out: forward 117 us, 134 with rows taken in
+// turn by as many CTAs as there are places; backward 232 and 253).
 constexpr long long kMostCtas = 1LL << 30;
+// A row of so few bytes has a warp: always, or where there are more than kManyRounds rows for every
+// place of a CTA. us with a warp / a CTA a row, forward; forward with four alternatives; backward:
+//   524288 x 64 bf16     126 / 936     401 / 3666    207 / 1401
+//   65536 x 2000 fp32    74 / 172      139 / 330     152 / 248
+//   16384 x 8000 bf16    44 / 63       103 / 101     81 / 93
+//   16384 x 8000 fp32    73 / 77       181 / 110     154 / 152
+//   2000 x 2000 bf16     3.6 / 6.1     8.5 / 14.0    4.7 / 7.6
+//   2000 x 8000 bf16     8.0 / 8.9     22.8 / 15.4   10.8 / 10.6
+//   100 x 500 fp32       2.1 / 2.3     4.2 / 4.6     2.9 / 2.5
+//   1 x 2000 fp32        3.1 / 2.3     6.0 / 4.2     4.4 / 2.5
+// Five CTAs of them an SM (524288 x 64 and 16384 x 8000 in bf16, forward: four 137 and 47, six 130
+// and 46).
+constexpr long long kShortAlways = 2048;  // forward
+constexpr long long kShortPlain = 16384, kShortTop = 8192, kShortBackward = 16384;
+constexpr int kManyRounds = 2, kShortPerSm = 5;
+constexpr long long kShortRounds = 8;  // CTAs in turn, that rows left out keep few places
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxTop = 32;
 constexpr int kMaxCluster = 8;
@@ -575,6 +589,151 @@ __global__ void __launch_bounds__(kThreads, kCluster ? 2 : kForwardPerSm)
   }
 }
 
+constexpr int kShortCandidates = 256;  // (a row whose chunks leave a lane without has no more)
+
+struct alignas(16) ShortShared {
+  uint32_t key[kShortCandidates];
+  int index[kShortCandidates];
+  int found;
+};
+
+// The k first elements of a short row, by one warp: lane i has the i-th's key and index (key 0: the
+// row has fewer). `top` is the lane's largest.
+template <typename T>
+__device__ void select_short(const Run<T>& run, float top, int k, ShortShared& sh, uint32_t& my_key,
+                             int& my_index) {
+  constexpr int V = Logit<T>::kVec;
+  const int lane = threadIdx.x & 31;
+  const bool any = lane < run.chunks || lane < run.head + run.tail;
+  const uint32_t mine = any ? order_key(top) : 0u;
+  // k lanes reach the k-th largest of the lanes' maxima (0: fewer than k hold elements)
+  uint32_t bound = __reduce_min_sync(0xFFFFFFFFu, mine), most = __reduce_max_sync(0xFFFFFFFFu, mine);
+  while (bound < most) {
+    const uint32_t mid = most - (most - bound) / 2;
+    const int n = __popc(__ballot_sync(0xFFFFFFFFu, mine >= mid));
+    if (n >= k) bound = mid;
+    else most = mid - 1;
+    if (n == k) break;
+  }
+  bound = max(bound, 1u);
+  auto for_elements = [&](bool in, auto f) {
+    if (in) {
+      if (lane < run.head + run.tail) {
+        const int e = run.loose(lane);
+        f(Logit<T>::get(run.row[e]), e);
+      }
+      for (int c = lane; c < run.chunks; c += 32) {
+        float x[V];
+        Logit<T>::unpack(__ldg(run.body + c), x);
+#pragma unroll
+        for (int e = 0; e < V; ++e) f(x[e], run.begin + run.head + c * V + e);
+      }
+    }
+    __syncwarp();
+  };
+  if (lane == 0) sh.found = 0;
+  __syncwarp();
+  for_elements(mine >= bound, [&](float x, int index) {
+    const uint32_t key = order_key(x);
+    if (key >= bound) {
+      const int at = atomicAdd(&sh.found, 1);
+      if (at < kShortCandidates) sh.key[at] = key, sh.index[at] = index;
+    }
+  });
+  const int found = sh.found;
+  my_key = 0;
+  my_index = -1;
+  uint32_t key = 0;  // the lane's first that is left
+  int index = 0x7FFFFFFF;
+  uint32_t last_key = 0xFFFFFFFFu;
+  int last_index = -1;
+  auto look = [&](uint32_t q, int at) {
+    if (before(last_key, last_index, q, at) && before(q, at, key, index)) key = q, index = at;
+  };
+  for (int n = 0; n < k; ++n) {
+    if (n == 0 || (key == last_key && index == last_index)) {
+      key = 0, index = 0x7FFFFFFF;
+      if (found <= kShortCandidates)
+        for (int i = lane; i < found; i += 32) look(sh.key[i], sh.index[i]);
+    }
+    __syncwarp();
+    // (rare: ties at the bound, or few lanes hold very many of the largest) the row once more
+    if (found > kShortCandidates) {
+      key = 0, index = 0x7FFFFFFF;
+      for_elements(mine >= bound, [&](float x, int at) { look(order_key(x), at); });
+    }
+    last_key = __reduce_max_sync(0xFFFFFFFFu, key);
+    last_index = static_cast<int>(__reduce_min_sync(
+        0xFFFFFFFFu, key == last_key ? static_cast<unsigned>(index) : 0x7FFFFFFFu));
+    if (lane == n) my_key = last_key, my_index = last_key == 0 ? -1 : last_index;
+  }
+}
+
+// A warp a row.
+template <typename T, bool kTop>
+__global__ void __launch_bounds__(kThreads, kShortPerSm)
+    logprobs_forward_short_sm103a_kernel(const ForwardArgs a) {
+  __shared__ ShortShared sh[kTop ? kWarps : 1];
+  constexpr int V = Logit<T>::kVec;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const float c = a.scale * kLog2e;
+  grid_dependency_wait();
+  for (long long r = static_cast<long long>(blockIdx.x) * kWarps + warp; r < a.rows;
+       r += static_cast<long long>(gridDim.x) * kWarps) {
+    const int token = __shfl_sync(0xFFFFFFFFu, a.tokens[r], 0);  // (one for all lanes)
+    const T* row = static_cast<const T*>(a.logits) + r * a.stride;
+    const bool out = token < 0 || token >= a.vocab;
+    const Run<T> run(row, 0, out ? 0 : a.vocab);
+    const float given = out ? 0.0f : Logit<T>::get(row[token]);
+    Partial p;
+    for (int i = lane; i < run.chunks; i += kLoads * 32) {
+      uint4 w[kLoads];
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k)
+        if (k == 0 || i + k * 32 < run.chunks) w[k] = __ldg(run.body + i + k * 32);
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k) {
+        if (k > 0 && i + k * 32 >= run.chunks) break;
+        float x[V];
+        Logit<T>::unpack(w[k], x);
+        p.add(x, c);
+      }
+    }
+    if (lane < run.head + run.tail) p.add_one(Logit<T>::get(row[run.loose(lane)]), c);
+    __syncwarp();
+    float m = p.m;
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+    if (m > p.m) p.raise(m, c);
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) {
+      p.s += __shfl_xor_sync(0xFFFFFFFFu, p.s, d);
+      p.t += __shfl_xor_sync(0xFFFFFFFFu, p.t, d);
+    }
+    const bool none = p.s == 0.0f;  // every logit is -inf
+    const float log_s = none ? 0.0f : logf(p.s);
+    if (lane == 0) {
+      if (token >= a.vocab) report_index(a.status, kIndexToken);
+      a.stats[r] = out ? make_float2(0.0f, 0.0f) : make_float2(none ? -INFINITY : m, log_s);
+      a.logprob[r] = out ? 0.0f : none ? -INFINITY : fmaf(given - m, a.scale, -log_s);
+      a.entropy[r] = none ? 0.0f : log_s - kLn2 * (p.t / p.s);
+    }
+    __syncwarp();
+    if constexpr (kTop) {
+      uint32_t key = 0;
+      int index = -1;
+      if (!out) select_short(run, p.top, a.top, sh[warp], key, index);
+      if (lane < a.top && (out || key != 0)) {
+        a.top_logprob[r * a.top + lane] = out    ? 0.0f
+                                          : none ? -INFINITY
+                                                 : fmaf(key_value(key) - m, a.scale, -log_s);
+        a.top_token[r * a.top + lane] = index;
+      }
+      __syncwarp();
+    }
+  }
+}
+
 struct BackwardArgs {
   const void* logits;
   void* dlogits;
@@ -702,16 +861,138 @@ __global__ void __launch_bounds__(kThreads, kBackwardPerSm)
   }
 }
 
+// A warp a row.
+template <typename T, bool kVector>
+__global__ void __launch_bounds__(kThreads, kShortPerSm)
+    logprobs_backward_short_sm103a_kernel(const BackwardArgs a) {
+  __shared__ int s_at[kWarps][kMaxTop + 1];  // the token and the alternatives
+  __shared__ float s_g[kWarps][kMaxTop + 1];
+  constexpr int V = Logit<T>::kVec;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int k = a.d_top ? a.top : 0;
+  int* const at = s_at[warp];
+  float* const own = s_g[warp];
+  grid_dependency_wait();
+  for (long long r = static_cast<long long>(blockIdx.x) * kWarps + warp; r < a.rows;
+       r += static_cast<long long>(gridDim.x) * kWarps) {
+    const T* row = static_cast<const T*>(a.logits) + r * a.stride;
+    T* drow = static_cast<T*>(a.dlogits) + r * a.d_stride;
+    const Run<T> run(row, 0, a.vocab);
+    const int token = __shfl_sync(0xFFFFFFFFu, a.tokens[r], 0);
+    const float2 st = a.stats[r];
+    const bool out = token < 0 || token >= a.vocab;
+    const bool zero = out || st.x == -INFINITY;  // left out, or no logit above -inf
+    if (out && token >= 0 && lane == 0) report_index(a.status, kIndexToken);
+    for (int i = lane; i <= k; i += 32) {
+      int t = token;
+      float g = 0.0f;
+      if (i == 0) {
+        if (a.d_logprob) g = a.d_logprob[r];
+      } else {
+        t = a.top_token[r * a.top + i - 1];
+        g = a.d_top[r * a.top + i - 1];
+        if (!out && (t < 0 || t >= a.vocab)) {
+          report_index(a.status, kIndexToken);
+          g = 0.0f;
+        }
+      }
+      at[i] = t;
+      own[i] = g;
+    }
+    __syncwarp();
+    float g = 0.0f;
+    for (int i = 0; i <= k; ++i) g += own[i];
+    const float h = a.d_entropy ? a.d_entropy[r] : 0.0f;
+    Slope f;
+    f.m = st.x;
+    f.c = a.scale * kLog2e;
+    f.log2_s = st.y * kLog2e;
+    f.A = -a.scale * fmaf(h, h != 0.0f ? a.entropy[r] : 0.0f, g);
+    f.B = -a.scale * h * kLn2;
+    // The elements with a weight of their own, as above: lane i the i-th, lane 0 the last of 33 too.
+    int where[2] = {-1, -1};
+    float special[2] = {0.0f, 0.0f};
+    if (!zero) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int n = lane + 32 * j;
+        if (n > k) continue;
+        const int e = at[n];
+        bool first = e >= 0 && e < a.vocab;
+        float sum = 0.0f;
+        for (int i = 0; i <= k; ++i)
+          if (at[i] == e) {
+            if (i < n) first = false;
+            sum += own[i];
+          }
+        if (first) {
+          where[j] = e;
+          special[j] = fmaf(a.scale, sum, f(Logit<T>::get(row[e])));
+        }
+      }
+    }
+    __syncwarp();  // (before the gradient takes the logits' place)
+    if constexpr (kVector) {
+      uint4* to_body = reinterpret_cast<uint4*>(drow + (reinterpret_cast<const T*>(run.body) - row));
+      for (int i = lane; i < run.chunks; i += kLoads * 32) {
+        uint4 w[kLoads];
+#pragma unroll
+        for (int n = 0; n < kLoads; ++n)
+          if (!zero && i + n * 32 < run.chunks) w[n] = run.body[i + n * 32];
+#pragma unroll
+        for (int n = 0; n < kLoads; ++n) {
+          if (i + n * 32 >= run.chunks) break;
+          if (zero) {
+            to_body[i + n * 32] = make_uint4(0, 0, 0, 0);
+          } else {
+            float x[V];
+            Logit<T>::unpack(w[n], x);
+#pragma unroll
+            for (int e = 0; e < V; ++e) x[e] = f(x[e]);
+            to_body[i + n * 32] = Logit<T>::pack(x);
+          }
+        }
+      }
+      if (lane < run.head + run.tail) {
+        const int e = run.loose(lane);
+        drow[e] = Logit<T>::put(zero ? 0.0f : f(Logit<T>::get(row[e])));
+      }
+    } else {
+      for (int e = lane; e < a.vocab; e += 32)
+        drow[e] = Logit<T>::put(zero ? 0.0f : f(Logit<T>::get(row[e])));
+    }
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (where[j] >= 0) drow[where[j]] = Logit<T>::put(special[j]);
+    __syncwarp();
+  }
+}
+
+bool many_rows(long long rows, const DeviceInfo& dev) {
+  return rows > static_cast<long long>(kManyRounds) * kForwardPerSm * dev.sm_count;
+}
+unsigned short_grid(long long rows, const DeviceInfo& dev) {
+  const long long most = static_cast<long long>(kShortPerSm) * dev.sm_count;
+  return static_cast<unsigned>(
+      std::min((rows + kWarps - 1) / kWarps, dev.limited ? most : kShortRounds * most));
+}
+
 template <typename T>
 cudaError_t launch_forward(ForwardArgs a, const DeviceInfo& dev, cudaStream_t stream) {
-  // CTAs of a row: as many as leave each 16 KB of it, while there are SMs without work.
   const long long bytes = static_cast<long long>(a.vocab) * static_cast<long long>(sizeof(T));
+  if (bytes <= kShortAlways ||
+      (bytes <= (a.top > 0 ? kShortTop : kShortPlain) && many_rows(a.rows, dev)))
+    return launch_programmatic(a.top > 0 ? logprobs_forward_short_sm103a_kernel<T, true>
+                                         : logprobs_forward_short_sm103a_kernel<T, false>,
+                               dim3(short_grid(a.rows, dev)), kThreads, 0, stream, a);
+  // CTAs of a row: as many as leave each 16 KB of it, while there are SMs without work.
   a.cluster = 1;
   while (a.cluster < kMaxCluster && a.rows * a.cluster < dev.sm_count &&
          bytes / (2 * a.cluster) >= 8192)
     a.cluster *= 2;
   const int per_sm = a.cluster > 1 ? 2 : kForwardPerSm;
-  const long long most = a.cluster == 1 && bytes >= kForwardRowBytes && !dev.limited
+  const long long most = a.cluster == 1 && !dev.limited
                              ? kMostCtas
                              : std::max(per_sm * dev.sm_count / a.cluster, 1);
   const unsigned grid = static_cast<unsigned>(std::min(a.rows, most) * a.cluster);
@@ -728,14 +1009,18 @@ cudaError_t launch_forward(ForwardArgs a, const DeviceInfo& dev, cudaStream_t st
 template <typename T>
 cudaError_t launch_backward(BackwardArgs a, const DeviceInfo& dev, cudaStream_t stream) {
   const long long bytes = static_cast<long long>(a.vocab) * static_cast<long long>(sizeof(T));
-  a.parts = 1;
-  const long long most = static_cast<long long>(kBackwardPerSm) * dev.sm_count;
-  while (a.rows * a.parts < most && bytes / (2 * a.parts) >= 8192) a.parts *= 2;
-  const unsigned grid = static_cast<unsigned>(std::min(
-      a.rows * a.parts, bytes / a.parts >= kBackwardRowBytes && !dev.limited ? kMostCtas : most));
   const bool vector =
       reinterpret_cast<uintptr_t>(a.logits) % 16 == reinterpret_cast<uintptr_t>(a.dlogits) % 16 &&
       (a.rows == 1 || (a.stride - a.d_stride) * static_cast<long long>(sizeof(T)) % 16 == 0);
+  if (bytes <= kShortBackward && many_rows(a.rows, dev))
+    return launch_programmatic(vector ? logprobs_backward_short_sm103a_kernel<T, true>
+                                      : logprobs_backward_short_sm103a_kernel<T, false>,
+                               dim3(short_grid(a.rows, dev)), kThreads, 0, stream, a);
+  a.parts = 1;
+  const long long most = static_cast<long long>(kBackwardPerSm) * dev.sm_count;
+  while (a.rows * a.parts < most && bytes / (2 * a.parts) >= 8192) a.parts *= 2;
+  const unsigned grid =
+      static_cast<unsigned>(std::min(a.rows * a.parts, dev.limited ? most : kMostCtas));
   const auto kernel = vector ? logprobs_backward_sm103a_kernel<T, true>
                              : logprobs_backward_sm103a_kernel<T, false>;
   return launch_programmatic(kernel, dim3(grid), kThreads, 0, stream, a);

@@ -6,6 +6,7 @@ import torch
 
 import causal_attention_score_gb300 as csa
 import logprobs_ref as ref
+from causal_attention_score_gb300 import _lib
 from serving_ref import half_step
 
 pytestmark = pytest.mark.gpu
@@ -162,6 +163,87 @@ def test_backward(kind, rows, vocab, pitch, d_pitch, shift, top, scale, terms, d
         assert torch.equal(x.cpu(), dx.cpu()), "in place"
     close(x, want, bound + 2.0 ** -25 * (dtype == torch.float16), "in place", dtype)
     assert before.shape == x.shape and csa.get_status() == 0
+
+
+# Rows so short and so many that a warp takes each (16384 and, with alternatives, 8192 bytes; more
+# than 12 rows an SM), and their neighbours that a CTA takes. One after the other a lane of a warp
+# adds up vocab / 256 chunks of 8 elements, 6 terms in the last of them and 6 of the lanes and what
+# belongs to no chunk: at 8192 elements 44, and the bound counts vocab / 512 + 32 = 48. In fp32
+# vocab / 128 chunks of 4 and 9 terms more: at 3900 elements 39.5 of 39.6.
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("kind,rows,vocab,pitch,shift,top,scale", [
+    ("normal", 2000, 1, 0, 0, 1, 1.0),
+    ("normal", 40000, 64, 0, 0, 4, 1.0),
+    ("normal", 1825, 255, 1, 1, 32, 2.0),
+    ("equal", 1900, 300, 0, 0, 20, 1.0),     # more candidates than are kept
+    ("equal", 9, 1023, 1, 0, 32, 1.0),
+    ("masked", 1900, 257, 0, 5, 32, 1.0),
+    ("few", 2100, 1500, 0, 0, 32, 1.0),
+    ("zeros", 2000, 2048, 0, 0, 3, 1.0),
+    ("rising", 2000, 2047, 0, 1, 32, 1.0),
+    ("columns", 1900, 2048, 0, 0, 32, 1.0),
+    ("lowest", 2000, 700, 4, 0, 5, 1.0),
+    ("normal", 2000, 3900, 0, 0, 0, 0.7),
+    ("far", 1900, 3899, 1, 3, 0, 1.0),
+    ("normal", 2000, 8192, 0, 0, 0, 1.0),
+    ("normal", 1824, 700, 0, 0, 6, 1.0),
+])
+def test_many_short_rows(kind, rows, vocab, pitch, shift, top, scale, dtype):
+    test_forward(kind, rows, vocab, pitch, shift, top, scale, dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("kind,rows,vocab,pitch,d_pitch,shift,top,scale,terms", [
+    ("normal", 2000, 1, 0, 0, 0, 1, 1.0, "leh"),
+    ("normal", 30000, 64, 0, 0, 0, 4, 1.0, "leh"),
+    ("normal", 1900, 333, 0, 3, 1, 32, 1.5, "leh"),
+    ("masked", 2000, 1001, 7, 7, 3, 32, 1.0, "leh"),
+    ("equal", 1900, 256, 0, 0, 0, 32, 0.7, "lh"),
+    ("peaked", 2000, 3900, 0, 0, 0, 0, 1.0, "le"),
+    ("normal", 1824, 700, 0, 0, 0, 6, 1.0, "leh"),
+])
+def test_gradient_of_many_short_rows(kind, rows, vocab, pitch, d_pitch, shift, top, scale, terms, dtype):
+    test_backward(kind, rows, vocab, pitch, d_pitch, shift, top, scale, terms, dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_short_rows_without_numbers(dtype):
+    """NaN, +inf and nothing but -inf in some of many short rows, tokens out of range and left out:
+    their results, and the others' as if each were the only row."""
+    rows, V, top = 2400, 200, 5
+    x = torch.randn((rows, V), generator=torch.Generator().manual_seed(8)).to(dtype)
+    tokens = torch.arange(rows, dtype=torch.int32) % V
+    x[7, 150] = math.nan
+    x[9, 3] = math.inf
+    x[11] = -math.inf
+    x[13, 4:] = -math.inf  # fewer than top are left
+    tokens[15], tokens[17] = -5, V
+    logprob, entropy, stats, top_logprob, top_token = (
+        t.cpu() for t in csa.token_logprobs(x.cuda(), tokens.cuda(), top))
+    assert csa.get_status() == _lib.CSA_ERR_INDEX
+    for r in (7, 9):
+        assert logprob[r].isnan() and entropy[r].isnan() and top_logprob[r].isnan().all()
+    assert logprob[11] == -math.inf and entropy[11] == 0 and stats[11].tolist() == [-math.inf, 0]
+    assert top_token[11].tolist() == [0, 1, 2, 3, 4] and (top_logprob[11] == -math.inf).all()
+    assert sorted(top_token[13, :4].tolist()) == [0, 1, 2, 3] and top_token[13, 4] == 4
+    assert top_logprob[13, 4] == -math.inf and top_logprob[13, :4].isfinite().all()
+    for r in (15, 17):
+        assert logprob[r] == 0 and entropy[r] == 0 and not stats[r].any()
+        assert (top_token[r] == -1).all() and not top_logprob[r].any()
+    odd = [7, 9, 11, 13, 15, 17]
+    keep = torch.ones(rows, dtype=torch.bool)
+    keep[odd] = False
+    clean, at = x.clone(), tokens.clone()
+    clean[odd], at[odd] = 0, 0
+    again = [t.cpu() for t in csa.token_logprobs(clean.cuda(), at.cuda(), top)]
+    for got, want in zip((logprob, entropy, stats, top_logprob, top_token), again):
+        assert torch.equal(got[keep], want[keep])
+    g = torch.ones(rows, device="cuda")
+    dx = torch.full_like(x, 3.0).cuda()
+    csa.token_logprobs_backward(dx, x.cuda(), tokens.cuda(), stats.cuda(), entropy.cuda(), g)
+    assert csa.get_status() == _lib.CSA_ERR_INDEX
+    assert not dx[[11, 15, 17]].any() and dx[7].isnan().any() and dx[9].isnan().any()
+    assert dx[keep.cuda()].isfinite().all()
 
 
 def test_repeated_alternatives_and_the_token_among_them():
