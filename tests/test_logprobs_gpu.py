@@ -336,6 +336,32 @@ def test_streams_graph_and_sm_limit():
         close(few[i], ref_want[name], bound[name], name)
 
 
+@pytest.mark.parametrize("sms", [1, 5])
+@pytest.mark.parametrize("rows,vocab,top", [(300, 5000, 4), (3000, 300, 7), (3000, 1900, 0), (40, 30000, 3)])
+def test_rows_in_turn_under_a_limit(rows, vocab, top, sms):
+    """Few SMs: CTAs, clusters and warps that take several rows, forwards and backwards."""
+    g = torch.Generator().manual_seed(rows + sms)
+    x = torch.randn((rows, vocab), generator=g) * 3
+    tokens = torch.randint(-vocab // 9, vocab, (rows,), generator=g, dtype=torch.int32)
+    d = {"d_logprob": torch.randn((rows,), generator=g), "d_entropy": torch.randn((rows,), generator=g)}
+    stream = torch.cuda.current_stream()
+    csa.set_stream_sm_limit(stream, sms)
+    try:
+        got = csa.token_logprobs(x.cuda(), tokens.cuda(), top)
+        dx = torch.full_like(x, 9.0).cuda()
+        csa.token_logprobs_backward(dx, x.cuda(), tokens.cuda(), got[2], got[1],
+                                    **{k: v.cuda() for k, v in d.items()})
+        assert csa.get_status() == 0
+    finally:
+        csa.set_stream_sm_limit(stream, 0)
+    want, bound = ref.forward(x, tokens, 1.0, top)
+    assert torch.equal(got[4].cpu().long(), want["top_token"].long())
+    for i, name in enumerate(("logprob", "entropy", "stats", "top_logprob")):
+        close(got[i], want[name], bound[name], name)
+    wd, bd = ref.backward(x, tokens, 1.0, **d)
+    close(dx, wd, bd, "gradient")
+
+
 def test_past_2_to_the_31():
     """Rows that lie more than 2^31 elements and 2^32 bytes into the logits."""
     rows, V = 45000, 50257
