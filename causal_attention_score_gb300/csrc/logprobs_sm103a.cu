@@ -57,18 +57,18 @@ constexpr int kForwardPerSm = 6, kBackwardPerSm = 5;  // CTAs an SM
 constexpr long long kMostCtas = 1LL << 30;
 // A row of so few bytes has a warp: always, or where there are more than kManyRounds rows for every
 // place of a CTA. us with a warp / a CTA a row, forward; forward with four alternatives; backward:
-//   524288 x 64 bf16     126 / 936     401 / 3666    207 / 1401
-//   65536 x 2000 fp32    74 / 172      139 / 330     152 / 248
-//   16384 x 8000 bf16    44 / 63       103 / 101     81 / 93
-//   16384 x 8000 fp32    73 / 77       181 / 110     154 / 152
-//   2000 x 2000 bf16     3.6 / 6.1     8.5 / 14.0    4.7 / 7.6
-//   2000 x 8000 bf16     8.0 / 8.9     22.8 / 15.4   10.8 / 10.6
+//   524288 x 64 bf16     126 / 936     456 / 3666    207 / 1401
+//   65536 x 2000 fp32    74 / 172      114 / 330     152 / 248
+//   16384 x 8000 bf16    44 / 63       70 / 100      81 / 93
+//   16384 x 8000 fp32    73 / 77       118 / 109     154 / 152
+//   2000 x 2000 bf16     3.6 / 6.1     7.8 / 14.0    4.7 / 7.6
+//   2000 x 8000 bf16     8.0 / 8.9     15.4 / 15.2   10.8 / 10.6
 //   100 x 500 fp32       2.1 / 2.3     4.2 / 4.6     2.9 / 2.5
 //   1 x 2000 fp32        3.1 / 2.3     6.0 / 4.2     4.4 / 2.5
 // Five CTAs of them an SM (524288 x 64 and 16384 x 8000 in bf16, forward: four 137 and 47, six 130
 // and 46).
 constexpr long long kShortAlways = 2048;  // forward
-constexpr long long kShortPlain = 16384, kShortTop = 8192, kShortBackward = 16384;
+constexpr long long kShortOfMany = 16384;
 constexpr int kManyRounds = 2, kShortPerSm = 5;
 constexpr long long kShortRounds = 8;  // CTAs in turn, that rows left out keep few places
 constexpr int kWarps = kThreads / 32;
@@ -594,6 +594,7 @@ constexpr int kShortCandidates = 256;  // (a row whose chunks leave a lane witho
 struct alignas(16) ShortShared {
   uint32_t key[kShortCandidates];
   int index[kShortCandidates];
+  int columns[32];  // lanes whose elements are looked at again
   int found;
 };
 
@@ -616,24 +617,31 @@ __device__ void select_short(const Run<T>& run, float top, int k, ShortShared& s
     if (n == k) break;
   }
   bound = max(bound, 1u);
-  auto for_elements = [&](bool in, auto f) {
-    if (in) {
-      if (lane < run.head + run.tail) {
-        const int e = run.loose(lane);
-        f(Logit<T>::get(run.row[e]), e);
-      }
-      for (int c = lane; c < run.chunks; c += 32) {
+  // Their elements, dealt out to all lanes: an item is a 16-byte chunk of one, or its loose element.
+  const uint32_t holds = __ballot_sync(0xFFFFFFFFu, mine >= bound);
+  if (holds >> lane & 1u) sh.columns[__popc(holds & ((1u << lane) - 1))] = lane;
+  const int per = (run.chunks + 31) / 32 + 1, items = __popc(holds) * per;
+  auto for_elements = [&](auto f) {
+#pragma unroll 2
+    for (int i = lane; i < items; i += 32) {
+      const int column = sh.columns[i / per], n = i % per - 1;
+      if (n < 0) {
+        if (column < run.head + run.tail) {
+          const int e = run.loose(column);
+          f(Logit<T>::get(run.row[e]), e);
+        }
+      } else if (column + n * 32 < run.chunks) {
         float x[V];
-        Logit<T>::unpack(__ldg(run.body + c), x);
+        Logit<T>::unpack(__ldg(run.body + column + n * 32), x);
 #pragma unroll
-        for (int e = 0; e < V; ++e) f(x[e], run.begin + run.head + c * V + e);
+        for (int e = 0; e < V; ++e) f(x[e], run.begin + run.head + (column + n * 32) * V + e);
       }
     }
     __syncwarp();
   };
   if (lane == 0) sh.found = 0;
   __syncwarp();
-  for_elements(mine >= bound, [&](float x, int index) {
+  for_elements([&](float x, int index) {
     const uint32_t key = order_key(x);
     if (key >= bound) {
       const int at = atomicAdd(&sh.found, 1);
@@ -660,7 +668,7 @@ __device__ void select_short(const Run<T>& run, float top, int k, ShortShared& s
     // (rare: ties at the bound, or few lanes hold very many of the largest) the row once more
     if (found > kShortCandidates) {
       key = 0, index = 0x7FFFFFFF;
-      for_elements(mine >= bound, [&](float x, int at) { look(order_key(x), at); });
+      for_elements([&](float x, int at) { look(order_key(x), at); });
     }
     last_key = __reduce_max_sync(0xFFFFFFFFu, key);
     last_index = static_cast<int>(__reduce_min_sync(
@@ -981,8 +989,7 @@ unsigned short_grid(long long rows, const DeviceInfo& dev) {
 template <typename T>
 cudaError_t launch_forward(ForwardArgs a, const DeviceInfo& dev, cudaStream_t stream) {
   const long long bytes = static_cast<long long>(a.vocab) * static_cast<long long>(sizeof(T));
-  if (bytes <= kShortAlways ||
-      (bytes <= (a.top > 0 ? kShortTop : kShortPlain) && many_rows(a.rows, dev)))
+  if (bytes <= kShortAlways || (bytes <= kShortOfMany && many_rows(a.rows, dev)))
     return launch_programmatic(a.top > 0 ? logprobs_forward_short_sm103a_kernel<T, true>
                                          : logprobs_forward_short_sm103a_kernel<T, false>,
                                dim3(short_grid(a.rows, dev)), kThreads, 0, stream, a);
@@ -1012,7 +1019,7 @@ cudaError_t launch_backward(BackwardArgs a, const DeviceInfo& dev, cudaStream_t 
   const bool vector =
       reinterpret_cast<uintptr_t>(a.logits) % 16 == reinterpret_cast<uintptr_t>(a.dlogits) % 16 &&
       (a.rows == 1 || (a.stride - a.d_stride) * static_cast<long long>(sizeof(T)) % 16 == 0);
-  if (bytes <= kShortBackward && many_rows(a.rows, dev))
+  if (bytes <= kShortOfMany && many_rows(a.rows, dev))
     return launch_programmatic(vector ? logprobs_backward_short_sm103a_kernel<T, true>
                                       : logprobs_backward_short_sm103a_kernel<T, false>,
                                dim3(short_grid(a.rows, dev)), kThreads, 0, stream, a);

@@ -165,8 +165,7 @@ def test_backward(kind, rows, vocab, pitch, d_pitch, shift, top, scale, terms, d
     assert before.shape == x.shape and csa.get_status() == 0
 
 
-# Rows so short and so many that a warp takes each (16384 and, with alternatives, 8192 bytes; more
-# than 12 rows an SM), and their neighbours that a CTA takes. One after the other a lane of a warp
+# Rows so short and so many that a warp takes each (up to 16384 bytes; more than 12 rows an SM), and their neighbours that a CTA takes. One after the other a lane of a warp
 # adds up vocab / 256 chunks of 8 elements, 6 terms in the last of them and 6 of the lanes and what
 # belongs to no chunk: at 8192 elements 44, and the bound counts vocab / 512 + 32 = 48. In fp32
 # vocab / 128 chunks of 4 and 9 terms more: at 3900 elements 39.5 of 39.6.
@@ -186,6 +185,8 @@ def test_backward(kind, rows, vocab, pitch, d_pitch, shift, top, scale, terms, d
     ("normal", 2000, 3900, 0, 0, 0, 0.7),
     ("far", 1900, 3899, 1, 3, 0, 1.0),
     ("normal", 2000, 8192, 0, 0, 0, 1.0),
+    ("normal", 1900, 8001, 3, 0, 20, 1.0),
+    ("rising", 1900, 3900, 0, 0, 32, 1.0),
     ("normal", 1824, 700, 0, 0, 6, 1.0),
 ])
 def test_many_short_rows(kind, rows, vocab, pitch, shift, top, scale, dtype):
