@@ -22,9 +22,9 @@
 // Bound: HBM, one read of the logits (and one write of the gradient). Short rows have a warp each,
 // without barriers (figures below). Else a CTA of 256 threads takes
 // a row and four 16-byte loads a thread at once; six such CTAs an SM, so that some load while
-// others rank. 8192 x 50257 in fp32 with two alternatives: 244 us (6.75 TB/s, the copy rate; five
+// others rank. 8192 x 50257 in fp32 with two alternatives: 244 us (6.6 TB/s, 0.97 of the copy rate; five
 // CTAs 253, four 270); in bf16 with the gradient behind it, of five CTAs an SM, 351 us (four 360,
-// six 350; a read of the logits beside the gradient's write goes at 6.7 TB/s). Few rows are split
+// six 350; a read of the logits beside the gradient's write goes at 6.6 TB/s). Few rows are split
 // over a cluster of up to eight CTAs, whose results meet in the first one's shared memory: 48 x
 // 50257 in fp32 with five alternatives 8.8 us, a chain of loads, bound, second look and barriers.
 //
