@@ -16,7 +16,7 @@
 // its moves in the second launch and makes them in the third.
 //
 // Bound: the copies by HBM (a job is 16 KB of one page, four 16-byte loads a thread, eight CTAs
-// an SM; 275 MB that compacting moves take 94 us, 5.9 TB/s of reads and writes), the rest by
+// an SM, given out one by one; 280 MB that compacting moves take 90 us, 6.2 TB/s), the rest by
 // launches and dependent loads: 24 sequences' end, 256 forks of 32 prompts and room for 352 more
 // are five launches and 21 us. One launch of one CTA for calls of few entries, and a second launch
 // begun before the first one's end, took no less.
@@ -64,7 +64,8 @@ struct Entry {
 struct Scan {
   uint32_t* bits;  // [words]: a set bit is a free page
   int* free_in;    // [chunks]
-  int* wanted;     // pages that all entries want (saturated)
+  int* wanted;     // compact: the number of moves
+  unsigned long long* taken;  // compact: jobs that CTAs have taken beside their first ones
   int* claims;     // [sequences]
   Entry* entries;
   int* movers;     // [pages] compact: the pages that move, in order
@@ -414,6 +415,7 @@ struct CopyArgs {
   const int* targets;  // [count], or by source where `moves`
   const int* moves;    // compact: a page's new number
   const int* counted;  // compact: the number of moves, on the device
+  unsigned long long* taken;  // compact: the next job's number, or nullptr: jobs in turn
   int count;
   int from_pages, to_pages;
   int heads, block_bytes;  // of a page's K
@@ -438,6 +440,7 @@ __global__ void __launch_bounds__(kThreads)
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     *in_use = used;
     *s.wanted = s_holes;
+    *s.taken = 0;
   }
   const int warps = static_cast<int>(gridDim.x) * kWarps, words = s.chunk_pages / 32;
   const int last = (b.pages + 31) / 32;
@@ -466,9 +469,50 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// Copies pages (a job: 16 KB of one's K or V); compact: and renames the table's entries.
+// A job: 16 KB of a page's K or V.
+template <bool kCompact>
+__device__ __forceinline__ void copy_job(const CopyArgs& a, long long job) {
+  const int tid = threadIdx.x;
+  const int i = static_cast<int>(job / a.jobs), part = static_cast<int>(job - static_cast<long long>(i) * a.jobs);
+  const int source = a.sources[i];
+  if (source < 0 || source >= a.from_pages) {
+    if (tid == 0 && part == 0) report_index(a.b.status, kIndexPage);
+    return;
+  }
+  const int target = kCompact ? a.moves[source] : a.targets[i];
+  if (target < 0 || target >= a.to_pages) {
+    if (tid == 0 && part == 0) report_index(a.b.status, kIndexPage);
+    return;
+  }
+  const int half = a.jobs / 2, which = part >= half, at = (part - which * half) * kJobBytes;
+  const uint4* from = reinterpret_cast<const uint4*>(
+      a.from.codes[which] + static_cast<long long>(source) * a.block_bytes + at);
+  uint4* to = reinterpret_cast<uint4*>(a.to.codes[which] +
+                                       static_cast<long long>(target) * a.block_bytes + at);
+  const int units = min(kJobBytes, a.block_bytes - at) / 16;
+  constexpr int kLoads = kJobBytes / 16 / kThreads;
+  uint4 x[kLoads];
+#pragma unroll
+  for (int k = 0; k < kLoads; ++k)
+    if (tid + k * kThreads < units) x[k] = from[tid + k * kThreads];
+#pragma unroll
+  for (int k = 0; k < kLoads; ++k)
+    if (tid + k * kThreads < units) to[tid + k * kThreads] = x[k];
+  if (at == 0) {
+    for (int h = tid; h < a.heads; h += kThreads)
+      a.to.scale[which][static_cast<long long>(target) * a.heads + h] =
+          a.from.scale[which][static_cast<long long>(source) * a.heads + h];
+    if (kCompact && tid == 0 && which == 0) {
+      a.b.refs[target] = a.b.refs[source];
+      a.b.refs[source] = 0;
+    }
+  }
+}
+
+// Copies pages; compact: and renames the table's entries.
 template <bool kCompact>
 __global__ void __launch_bounds__(kThreads, kCopyPerSm) cache_copy_sm103a_kernel(const CopyArgs a) {
+  __shared__ long long s_next[2];
   grid_dependency_wait();
   const int tid = threadIdx.x;
   if (kCompact && static_cast<int>(blockIdx.x) < a.table_ctas) {
@@ -493,41 +537,18 @@ __global__ void __launch_bounds__(kThreads, kCopyPerSm) cache_copy_sm103a_kernel
   const int skip = kCompact ? a.table_ctas : 0;
   const int count = kCompact ? min(*a.counted, a.b.pages) : a.count;
   const long long jobs = static_cast<long long>(count) * a.jobs;
-  for (long long job = static_cast<int>(blockIdx.x) - skip; job < jobs;
-       job += static_cast<int>(gridDim.x) - skip) {
-    const int i = static_cast<int>(job / a.jobs), part = static_cast<int>(job - static_cast<long long>(i) * a.jobs);
-    const int source = a.sources[i];
-    if (source < 0 || source >= a.from_pages) {
-      if (tid == 0 && part == 0) report_index(a.b.status, kIndexPage);
-      continue;
-    }
-    const int target = kCompact ? a.moves[source] : a.targets[i];
-    if (target < 0 || target >= a.to_pages) {
-      if (tid == 0 && part == 0) report_index(a.b.status, kIndexPage);
-      continue;
-    }
-    const int half = a.jobs / 2, which = part >= half, at = (part - which * half) * kJobBytes;
-    const uint4* from = reinterpret_cast<const uint4*>(
-        a.from.codes[which] + static_cast<long long>(source) * a.block_bytes + at);
-    uint4* to = reinterpret_cast<uint4*>(a.to.codes[which] +
-                                         static_cast<long long>(target) * a.block_bytes + at);
-    const int units = min(kJobBytes, a.block_bytes - at) / 16;
-    constexpr int kLoads = kJobBytes / 16 / kThreads;
-    uint4 x[kLoads];
-#pragma unroll
-    for (int k = 0; k < kLoads; ++k)
-      if (tid + k * kThreads < units) x[k] = from[tid + k * kThreads];
-#pragma unroll
-    for (int k = 0; k < kLoads; ++k)
-      if (tid + k * kThreads < units) to[tid + k * kThreads] = x[k];
-    if (at == 0) {
-      for (int h = tid; h < a.heads; h += kThreads)
-        a.to.scale[which][static_cast<long long>(target) * a.heads + h] =
-            a.from.scale[which][static_cast<long long>(source) * a.heads + h];
-      if (kCompact && tid == 0 && which == 0) {
-        a.b.refs[target] = a.b.refs[source];
-        a.b.refs[source] = 0;
-      }
+  const int step = static_cast<int>(gridDim.x) - skip;
+  long long job = static_cast<int>(blockIdx.x) - skip;
+  for (int turn = 0; job < jobs; turn ^= 1) {
+    // (asked for while the job is under way; two places, so one barrier a job is enough)
+    if (kCompact && a.taken && tid == 0) s_next[turn] = static_cast<long long>(atomicAdd(a.taken, 1ull));
+    copy_job<kCompact>(a, job);
+    if (kCompact && a.taken) {
+      __syncwarp();
+      __syncthreads();
+      job = step + s_next[turn];
+    } else {
+      job += step;
     }
   }
 }
@@ -567,6 +588,7 @@ size_t lay_out(const csa_kv_pages& p, int entries, void* workspace, Scan& s) {
   };
   s.free_in = reinterpret_cast<int*>(take(kMaxChunks * sizeof(int)));
   s.wanted = reinterpret_cast<int*>(take(sizeof(int)));
+  s.taken = reinterpret_cast<unsigned long long*>(take(sizeof(unsigned long long)));
   s.bits = reinterpret_cast<uint32_t*>(
       take(static_cast<size_t>(s.chunks) * (s.chunk_pages / 32) * sizeof(uint32_t)));
   s.movers = reinterpret_cast<int*>(take(static_cast<size_t>(p.pages) * sizeof(int)));
@@ -657,6 +679,11 @@ CopyArgs copy_args(const csa_kv_cache& to, const csa_kv_cache& from) {
   return a;
 }
 
+// Whether jobs are large enough to be given out one by one, which evens out how long SMs take:
+// 4095 pages of 2 x 64 KB 158 us (6.8 TB/s) and 179 in turn, but 16383 of 2 x 8 KB 92 and 83;
+// compacting a cache of 1 GB, with sequences copied out of it before, 119 us and 135 in turn.
+bool whole_jobs(const CopyArgs& a) { return a.block_bytes >= kJobBytes; }
+
 }  // namespace
 
 int kv_cache_copy_launch(const csa_kv_cache& to, const csa_kv_cache& from, const int* to_pages,
@@ -667,8 +694,10 @@ int kv_cache_copy_launch(const csa_kv_cache& to, const csa_kv_cache& from, const
   a.targets = to_pages;
   a.count = n;
   a.b.status = dev.status_word;
-  const unsigned grid = static_cast<unsigned>(
-      std::min<long long>(static_cast<long long>(n) * a.jobs, kCopyPerSm * dev.sm_count));
+  // A CTA a job, as places are free; jobs in turn where they are smaller ones.
+  const long long most = whole_jobs(a) && !dev.limited ? 1LL << 30 : kCopyPerSm * dev.sm_count;
+  const unsigned grid =
+      static_cast<unsigned>(std::min<long long>(static_cast<long long>(n) * a.jobs, most));
   return launched("kv_cache_copy",
                   launch_programmatic(cache_copy_sm103a_kernel<false>, dim3(grid), kThreads, 0,
                                       stream, a),
@@ -685,6 +714,7 @@ int kv_cache_compact_launch(const csa_kv_cache& cache, const csa_kv_pages& pages
   a.sources = scan.s.movers;
   a.moves = moves;
   a.counted = scan.s.wanted;
+  a.taken = whole_jobs(a) ? scan.s.taken : nullptr;
   a.b = scan.b;
   a.in_use = in_use;
   const int most = kCopyPerSm * dev.sm_count;
