@@ -77,7 +77,7 @@ struct PlanArgs {
 // CTA 0 plans, the others clear the marks of the rows.
 __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_sm103a_kernel(const PlanArgs a) {
   __shared__ int s_bad, s_most, s_chunk, s_sms;
-  __shared__ unsigned long long s_saved, s_blocks, s_tiles, s_own, s_key[kPlanThreads / 32];
+  __shared__ unsigned long long s_saved, s_blocks, s_tiles, s_own, s_long, s_key[kPlanThreads / 32];
   // (what fits is kept here until the end)
   __shared__ SharedGroup s_groups[kPlanGroups];
   __shared__ SharedSequence s_sequences[kPlanSequences];
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_sm103a_kernel(con
       reinterpret_cast<int4*>(plan.own_there)[i] = make_int4(0, 0, 0, 0);
     return;
   }
-  if (tid == 0) s_bad = s_most = 0, s_saved = s_blocks = s_tiles = s_own = 0;
+  if (tid == 0) s_bad = s_most = 0, s_saved = s_blocks = s_tiles = s_own = s_long = 0;
   __syncthreads();
 
   // The groups: bounds in order, whole pages.
@@ -114,8 +114,9 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_sm103a_kernel(con
   const bool bad = s_bad != 0;  // then nothing is computed
   if (bad && tid == 0) report_index(v.status, kIndexSequence);
 
-  // The sequences, each with its group (found by its bounds); and what their own parts take.
-  long long own = 0;
+  // The sequences, each with its group (found by its bounds); and what their own parts take, those
+  // of more rows than kRowLimit apart: another kernel's, if there are blocks enough of them.
+  long long own = 0, own_long = 0;
   for (int s = tid; s < S; s += kPlanThreads) {
     SharedSequence r{};
     r.q = kv_sequence(v, s);
@@ -141,16 +142,25 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_sm103a_kernel(con
       }
     }
     const long long rows = static_cast<long long>(r.q.n) * a.group_heads;
-    if (a.prompt_blocks > 0 && rows > kRowLimit)
-      atomicAdd(&s_blocks, static_cast<unsigned long long>((rows + 15) / 16 * v.heads));
-    else if (rows > 0)
-      own += (rows + a.own_rows - 1) / a.own_rows *
-             (max((r.q.length - r.lead + a.own_tile - 1) / a.own_tile, 1) + a.own_start);
+    if (rows > 0) {
+      const long long work = (rows + a.own_rows - 1) / a.own_rows *
+                             (max((r.q.length - r.lead + a.own_tile - 1) / a.own_tile, 1) + a.own_start);
+      if (a.prompt_blocks > 0 && rows > kRowLimit) {
+        atomicAdd(&s_blocks, static_cast<unsigned long long>((rows + 15) / 16 * v.heads));
+        own_long += work;
+      } else {
+        own += work;
+      }
+    }
     sequences[s] = r;
   }
 #pragma unroll
-  for (int d = 16; d > 0; d /= 2) own += __shfl_xor_sync(0xFFFFFFFFu, own, d);
+  for (int d = 16; d > 0; d /= 2) {
+    own += __shfl_xor_sync(0xFFFFFFFFu, own, d);
+    own_long += __shfl_xor_sync(0xFFFFFFFFu, own_long, d);
+  }
   if (lane == 0 && own > 0) atomicAdd(&s_own, static_cast<unsigned long long>(own));
+  if (lane == 0 && own_long > 0) atomicAdd(&s_long, static_cast<unsigned long long>(own_long));
   __syncthreads();
 
   // The groups' rows: from the first to the last of their sequences that have any; and what a
@@ -215,12 +225,15 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_sm103a_kernel(con
   }
   __syncthreads();
   const bool worth = static_cast<long long>(s_saved) * v.heads >= a.worth;
+  const bool prompts = static_cast<long long>(s_blocks) > a.prompt_blocks;
   // How many SMs take the shared part, and the longest run of tiles of a unit there (the longest
   // group's cut into 1, 2, ... pieces): what takes the least time, the shared part as rounds of
   // equal units and in parts, the own ones beside it, and has room. Numbers of SMs around those
   // that the two parts' work is in proportion to.
   {
-    const float own_us = static_cast<float>(s_own) * a.own_us;
+    // (12 x 9 tokens of 4 heads over 8192 shared and 3000 own, too few blocks for the kernel of prompts:
+    // 124 us; 1620 when their own parts were not counted and got one SM)
+    const float own_us = static_cast<float>(s_own + (prompts ? 0 : s_long)) * a.own_us;
     const float shared_us = static_cast<float>(s_tiles) * a.tile_us / static_cast<float>(a.per_sm);
     const float middle = static_cast<float>(a.sms) * (shared_us / (shared_us + own_us + 1e-6f));
     const int sms = min(max(static_cast<int>(middle + static_cast<float>(a.sms * ((tid & 15) - 7)) / 32.0f + 0.5f), 1),
@@ -294,8 +307,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) shared_plan_sm103a_kernel(con
       plan.head->shared_sms = s_sms;
       plan.head->own_sms = max(a.sms - s_sms, 1);
       plan.head->shared = PromptList{0u, 0};
-      plan.head->own = PromptList{
-          0u, static_cast<long long>(s_blocks) > a.prompt_blocks ? kRowLimit : kNoRowLimit};
+      plan.head->own = PromptList{0u, prompts ? kRowLimit : kNoRowLimit};
       if (!room) report_index(v.status, kIndexRows);
       s_bad = room ? 0 : 1;
     }
