@@ -975,7 +975,9 @@ __global__ void __launch_bounds__(128 * kGroups<HSP, NB>, 1)
     group_sync(gi);  // sm is reused
   }
   if (!kShared && !left_open && gtid == 0) header[kHeadPieces] = 0;
-  if (kShared && a.beside) grid_dependency_wait();
+  // (one CTA that waits is enough for this kernel to end behind the shared part's; the others, and
+  // those without work first of all, keep no SM: the call holds as many as its two parts work on)
+  if (kShared && a.beside && blockIdx.x == 0) grid_dependency_wait();
 }
 
 // Joins the pieces of each unit that was split: row blockIdx.y of the unit that the

@@ -337,8 +337,10 @@ csa_status csa_dense_tiling(int M, int H, int sms, int* bn, int* pairs);
  * rotary, cache, pages and logits calls and the last, short kernels of the attention calls have
  * small CTAs, of which a limit allows in proportion (2 to 48 for each of max_sms;
  * kv_pages_extend, kv_cache_fork and kv_pages_free take some for each entry): it bounds their
- * share of the memory system, not the SMs they are on. Limits are keyed by the
- * stream's handle value, process-wide, for at most 64 streams at once (then
+ * share of the memory system, not the SMs they are on. The two parts of
+ * cache_attention_shared_forward run side by side on max_sms SMs between them; each begins as
+ * max_sms CTAs, of which those that the division leaves without work end as soon as they have read
+ * it. Limits are keyed by the stream's handle value, process-wide, for at most 64 streams at once (then
  * CSA_ERR_BUSY); a stream destroyed with a limit set should have it removed
  * first, since a new stream may reuse the handle. Returns CSA_OK, CSA_ERR_SHAPE
  * for max_sms < 0, or CSA_ERR_BUSY.

@@ -1,4 +1,5 @@
-"""How cache_attention_shared_forward shares the SMs out between its two parts (GPU)."""
+"""How cache_attention_shared_forward shares the SMs out: between its two parts, and with calls on
+other streams (GPU)."""
 import pytest
 import torch
 
@@ -90,3 +91,51 @@ def test_middling_rows_against_definition(mode):
         check(b, q, out)
     finally:
         csa.set_shared_part(csa.SHARED_AUTO)
+
+
+def test_a_limited_call_leaves_the_other_sms_to_a_call_beside_it():
+    """Two streams limited to half the SMs each: a short call that begins while a long shared one runs
+    does not wait for the latter's end."""
+    half = torch.cuda.get_device_properties(0).multi_processor_count // 2
+    long = Large([1] * 128, [100] * 128, 65536)
+    short = Large([1] * 8, [2048] * 8, 64, seed=1)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        csa.set_stream_sm_limit(s, half)
+    try:
+        def timed(beside):
+            gate = torch.cuda.Event()
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            z = torch.cuda.Event(enable_timing=True)
+            torch.cuda.synchronize()
+            torch.cuda._sleep(1_000_000)  # until everything is launched
+            z.record()
+            gate.record()
+            for s in streams:
+                s.wait_event(gate)
+            if beside:
+                long.call(streams[0])
+            end = torch.cuda.Event(enable_timing=True)
+            end.record(streams[0])
+            with torch.cuda.stream(streams[1]):
+                torch.cuda._sleep(200_000)  # the long call's own parts are done
+            a.record(streams[1])
+            short.plain(streams[1])
+            b.record(streams[1])
+            torch.cuda.synchronize()
+            return a.elapsed_time(b) * 1e3, z.elapsed_time(end) * 1e3
+
+        for _ in range(2):
+            timed(True), timed(False)
+        want_long, want_short = long.out.clone(), short.out.clone()
+        alone = min(timed(False)[0] for _ in range(5))
+        runs = [timed(True) for _ in range(5)]
+        assert csa.get_status() == 0
+        assert torch.equal(long.out, want_long) and torch.equal(short.out, want_short)
+        beside, took = min(r[0] for r in runs), min(r[1] for r in runs)
+        assert took > 200, took  # (the long call is still under way when the short one begins)
+        assert beside < alone + 0.25 * took, (alone, beside, took)
+    finally:
+        torch.cuda.synchronize()
+        for s in streams:
+            csa.set_stream_sm_limit(s, 0)
