@@ -9,7 +9,9 @@
 // One pass over the logits: a thread keeps the maximum of what it has seen and S and T
 // relative to it, rescaled when the maximum grows (T' = r (T - D S), S' = r S, r = exp(-D)).
 // Exponents are worked out as (x - m) c with c = s log2(e), the difference first, which is
-// exact near the maximum. All sums are fp32 over at most a few hundred terms a thread, then a
+// exact near the maximum. All sums are fp32: a thread adds up its chunks' sums (of 4 or 8 weights)
+// one after the other, at most 512 of them (a row of 524288 words in fp32; 49 at 50257), which then
+// go to a sum of such runs, and the threads' sums make a
 // tree. A forbidden word's -inf has weight 0 and adds 0 to T (its d is clamped for the
 // product); a NaN or +inf makes its row's results NaN.
 //
@@ -41,6 +43,7 @@
 #include <cmath>
 #include <cstdint>
 #include <string>
+#include <type_traits>
 
 #include "csa_internal.h"
 #include "kv_cache.cuh"
@@ -76,6 +79,10 @@ constexpr int kMaxTop = 32;
 constexpr int kMaxCluster = 8;
 static_assert(kWarps >= kMaxCluster, "a warp for each CTA's list");
 constexpr int kLoads = 4;         // 16-byte loads that a thread has in flight
+// Chunks of a run: what a thread adds up of them, kRunLoads loads' sums one after the other, goes to a
+// sum of runs then.
+constexpr int kRunLoads = 512;
+constexpr int kRunChunks = kRunLoads * kThreads;
 constexpr int kCandidates = 1024; // elements that reach the bound
 constexpr int kColumns = 4 * kMaxTop;  // threads whose elements are looked at again
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -211,6 +218,13 @@ struct Partial {
     unpack_f32x2(t2, a, b);
     t += a + b;
   }
+  // This and another's S and T.
+  __device__ __forceinline__ void join(Partial q, float c) {
+    if (q.m > m) raise(q.m, c);
+    else if (m > q.m) q.raise(m, c);
+    s += q.s;
+    t += q.t;
+  }
   __device__ __forceinline__ void add_one(float x, float c) {
     if (x > m) raise(x, c);
     top = fmaxf(top, x);
@@ -258,7 +272,10 @@ struct alignas(16) Shared {
   int all_index[kMaxCluster][kMaxTop];
   uint32_t best_key[kWarps];
   int best_index[kWarps];
-  uint32_t cand_key[kCandidates];
+  union {
+    float3 runs[kThreads];  // long rows: what a thread's runs before this one came to
+    uint32_t cand_key[kCandidates];  // (once all sums are done)
+  };
   int cand_index[kCandidates];
 };
 
@@ -438,8 +455,9 @@ __device__ void select_top(const Run<T>& run, float top, int k, Shared& sh) {
   }
 }
 
-// kCluster: a row's CTAs are a cluster of a.cluster (else 1).
-template <typename T, bool kTop, bool kCluster>
+// kCluster: a row's CTAs are a cluster of a.cluster (else 1). kLong: a CTA's part of a row may be
+// more than a run (of 2 MB; apart, as the loop costs others 0.5 %).
+template <typename T, bool kTop, bool kCluster, bool kLong>
 __global__ void __launch_bounds__(kThreads, kCluster ? 2 : kForwardPerSm)
     logprobs_forward_sm103a_kernel(const ForwardArgs a) {
   __shared__ Shared sh;
@@ -469,21 +487,35 @@ __global__ void __launch_bounds__(kThreads, kCluster ? 2 : kForwardPerSm)
     }
     const float given = out ? 0.0f : Logit<T>::get(row[token]);
     Partial p;
-    for (int i = tid; i < run.chunks; i += kLoads * kThreads) {
-      uint4 w[kLoads];
+    int i = tid;
+    for (int end = kLong ? min(run.chunks, kRunChunks) : run.chunks;;
+         end = min(run.chunks, end + kRunChunks)) {
+      for (; i < end; i += kLoads * kThreads) {
+        uint4 w[kLoads];
 #pragma unroll
-      for (int k = 0; k < kLoads; ++k) {
-        if (k > 0 && i + k * kThreads >= run.chunks) continue;
-        if (kCluster && i == tid) w[k] = early[kCluster ? k : 0];
-        else w[k] = __ldg(run.body + i + k * kThreads);
-      }
+        for (int k = 0; k < kLoads; ++k) {
+          if (k > 0 && i + k * kThreads >= end) continue;
+          if (kCluster && i == tid) w[k] = early[kCluster ? k : 0];
+          else w[k] = __ldg(run.body + i + k * kThreads);
+        }
 #pragma unroll
-      for (int k = 0; k < kLoads; ++k) {
-        if (k > 0 && i + k * kThreads >= run.chunks) break;
-        float x[V];
-        Logit<T>::unpack(w[k], x);
-        p.add(x, c);
+        for (int k = 0; k < kLoads; ++k) {
+          if (k > 0 && i + k * kThreads >= end) break;
+          float x[V];
+          Logit<T>::unpack(w[k], x);
+          p.add(x, c);
+        }
       }
+      if (!kLong || run.chunks <= kRunChunks) break;
+      if (end > kRunChunks) {  // with the runs before
+        const float3 q = sh.runs[tid];
+        Partial before;
+        before.m = q.x, before.s = q.y, before.t = q.z;
+        p.join(before, c);
+      }
+      if (end == run.chunks) break;
+      sh.runs[tid] = make_float3(p.m, p.s, p.t);
+      p.s = p.t = 0.0f;
     }
     if (tid < run.head + run.tail) p.add_one(Logit<T>::get(row[run.loose(tid)]), c);
     __syncwarp();
@@ -1003,14 +1035,19 @@ cudaError_t launch_forward(ForwardArgs a, const DeviceInfo& dev, cudaStream_t st
                              ? kMostCtas
                              : std::max(per_sm * dev.sm_count / a.cluster, 1);
   const unsigned grid = static_cast<unsigned>(std::min(a.rows, most) * a.cluster);
-  if (a.cluster > 1)
-    return launch_programmatic_cluster(a.top > 0 ? logprobs_forward_sm103a_kernel<T, true, true>
-                                                 : logprobs_forward_sm103a_kernel<T, false, true>,
-                                       grid, kThreads, 0, stream,
-                                       static_cast<unsigned>(a.cluster), a);
-  return launch_programmatic(a.top > 0 ? logprobs_forward_sm103a_kernel<T, true, false>
-                                       : logprobs_forward_sm103a_kernel<T, false, false>,
-                             dim3(grid), kThreads, 0, stream, a);
+  const bool is_long = bytes / a.cluster >= 16LL * kRunChunks;
+  auto launch = [&](auto top, auto l) {
+    constexpr bool kTop = decltype(top)::value, kLong = decltype(l)::value;
+    return a.cluster > 1
+               ? launch_programmatic_cluster(logprobs_forward_sm103a_kernel<T, kTop, true, kLong>, grid,
+                                             kThreads, 0, stream, static_cast<unsigned>(a.cluster), a)
+               : launch_programmatic(logprobs_forward_sm103a_kernel<T, kTop, false, kLong>, dim3(grid),
+                                     kThreads, 0, stream, a);
+  };
+  using Yes = std::true_type;
+  using No = std::false_type;
+  return a.top > 0 ? is_long ? launch(Yes{}, Yes{}) : launch(Yes{}, No{})
+                   : is_long ? launch(No{}, Yes{}) : launch(No{}, No{});
 }
 
 template <typename T>

@@ -692,7 +692,8 @@ csa_status kv_cache_compact(const csa_kv_cache* cache, const csa_kv_pages* pages
  *   top          0 .. min(32, vocab); top_logprob fp32 and top_token int32, [rows][top] (unused
  *                and may be NULL with top = 0).
  * Computed in fp32 (the difference to m first, so that log p near 0 is exact to fp32's
- * 2^-24 of the sum, not of m). A logit of -inf is a forbidden token: p = 0, nothing added to the
+ * 2^-24 of the sum, not of m; the sums in runs of at most 512 16-byte groups of words and a sum of
+ * such runs, whatever the vocabulary: their roundings are below 2^-14 of them at 2^27 words). A logit of -inf is a forbidden token: p = 0, nothing added to the
  * entropy. Where every logit of a row is -inf, log p is -inf, the entropy 0 and stats (-inf, 0).
  * A NaN or +inf makes its row's logprob, entropy and top_logprob NaN; among the top tokens a NaN
  * counts as -inf. Outputs must not overlap the inputs or each other. Asynchronous on `stream`;
