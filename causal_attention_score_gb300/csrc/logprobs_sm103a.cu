@@ -621,7 +621,8 @@ __global__ void __launch_bounds__(kThreads, kCluster ? 2 : kForwardPerSm)
   }
 }
 
-constexpr int kShortCandidates = 256;  // (a row whose chunks leave a lane without has no more)
+// (as many as a row has whose chunks leave a lane without: 31 of 8 words and 14 loose ones are 262)
+constexpr int kShortCandidates = 288;
 
 struct alignas(16) ShortShared {
   uint32_t key[kShortCandidates];

@@ -1,9 +1,9 @@
-"""What token_logprobs_forward and _backward leave as it was (GPU)."""
+"""What token_logprobs_forward and _backward leave as it was, and rows at the kernels' borders (GPU)."""
 import pytest
 import torch
 
 import causal_attention_score_gb300 as csa
-from test_logprobs_gpu import TYPES, rows_of
+from test_logprobs_gpu import TYPES, rows_of, test_forward as check_forward
 
 pytestmark = pytest.mark.gpu
 
@@ -48,3 +48,10 @@ def test_the_gradient_writes_its_rows_alone(rows, vocab, pitch, d_pitch, shift, 
     csa.token_logprobs_backward(x, x, t, stats, entropy, d, d, d_top, top_token)
     only_inside(x, held, "in place")
     assert csa.get_status() == 0
+
+
+@pytest.mark.parametrize("kind", ["normal", "rising", "equal"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_short_rows_of_31_chunks_and_14_loose_words(dtype, kind):
+    """The most words that a lane without a chunk leaves in a row: with 32 alternatives all are candidates."""
+    check_forward(kind, 1900, 262, 2, 1, 32, 1.0, dtype)
