@@ -18,6 +18,12 @@ class _KvPagesStruct(ctypes.Structure):
                 ("table_width", ctypes.c_int), ("page_tokens", ctypes.c_int)]
 
 
+def _meet(tensors) -> bool:
+    """Whether any of these contiguous int32 tensors share elements."""
+    spans = sorted((t.data_ptr(), t.data_ptr() + 4 * t.numel()) for t in tensors)
+    return any(a[1] > b[0] for a, b in zip(spans, spans[1:]))
+
+
 class KvPages(_Marshalled):
     """The books of a cache (csa_kv_pages in include/csa.h): int32 tensors ``refs`` [pages] (how
     many table entries name a page; 0: free), ``lengths`` [S] (tokens of each place's sequence; 0:
@@ -40,6 +46,8 @@ class KvPages(_Marshalled):
         self.page_tokens = int(page_tokens)
         self._tensors = (refs, lengths, table)
         self._ptrs = [t.data_ptr() for t in self._tensors]
+        if _meet(self._tensors):
+            raise ValueError("refs, lengths and table must not overlap")
         self._device = refs.get_device()
         self._struct = _KvPagesStruct(*self._ptrs, refs.numel(), S, width, self.page_tokens)
         self._ref = ctypes.addressof(self._struct)
@@ -156,6 +164,8 @@ def kv_cache_compact(cache: KvCache, pages: KvPages, moves: torch.Tensor, in_use
     dev = _get_device()
     ref, books = cache._pointer(dev), pages._pointer(dev)
     m, u = _list(moves, "moves", pages.refs.numel(), dev), _list(in_use, "in_use", 1, dev)
+    if _meet((*pages._tensors, moves, in_use)):
+        raise ValueError("moves and in_use must not overlap the books or each other")
     workspace, stream = _scratch(workspace, pages, 0, stream, dev)
     rc = (_lib._lib or _lib.load()).kv_cache_compact(
         ref, books, m, u, workspace.data_ptr(), workspace.nbytes, _stream_ptr(stream, dev))

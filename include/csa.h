@@ -645,7 +645,7 @@ csa_status cache_attention_shared_forward(void* out, const void* q, int dtype, i
  * below n, both in ascending order: codes, scales and refs, and every sequence's table entries.
  * Afterwards pages 0 .. n - 1 are in use and the rest free.
  *   moves    device, int32 [pages]: each page's new number, -1 for those that were free;
- *   in_use   device, int32 [1]: n.
+ *   in_use   device, int32 [1]: n. They overlap neither the books nor each other.
  *
  * kv_pages_workspace_size -- bytes of workspace that kv_pages_extend and kv_cache_fork with up to
  * n entries and kv_cache_compact need, into *bytes (host only; n >= 0). The workspace: device,
@@ -707,7 +707,8 @@ csa_status kv_cache_compact(const csa_kv_cache* cache, const csa_kv_pages* pages
  *   d_logprob, d_entropy [rows], d_top [rows][top]   device, fp32; any may be NULL (no such
  *                term; top_token is read with d_top only);
  *   dlogits      device, of the logits' type, rows d_stride apart; the logits themselves with
- *                equal strides (in place), or apart from them (CSA_ERR_UNSUPPORTED otherwise).
+ *                equal strides (in place), or apart from them (CSA_ERR_UNSUPPORTED otherwise);
+ *                apart from the other arrays.
  * Every element of dlogits is written: 0 in rows left out and in rows with every logit -inf.
  * The choice of the alternatives has no gradient. Asynchronous on `stream`.
  */
