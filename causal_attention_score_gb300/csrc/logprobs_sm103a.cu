@@ -60,12 +60,12 @@ constexpr int kForwardPerSm = 6, kBackwardPerSm = 5;  // CTAs an SM
 constexpr long long kMostCtas = 1LL << 30;
 // A row of so few bytes has a warp: always, or where there are more than kManyRounds rows for every
 // place of a CTA. us with a warp / a CTA a row, forward; forward with four alternatives; backward:
-//   524288 x 64 bf16     126 / 936     456 / 3666    207 / 1401
-//   65536 x 2000 fp32    74 / 172      114 / 330     152 / 248
-//   16384 x 8000 bf16    44 / 63       70 / 100      81 / 93
-//   16384 x 8000 fp32    73 / 77       118 / 109     154 / 152
-//   2000 x 2000 bf16     3.6 / 6.1     7.8 / 14.0    4.7 / 7.6
-//   2000 x 8000 bf16     8.0 / 8.9     15.4 / 15.2   10.8 / 10.6
+//   524288 x 64 bf16     126 / 936     416 / 3666    207 / 1401
+//   65536 x 2000 fp32    74 / 172      108 / 330     152 / 248
+//   16384 x 8000 bf16    44 / 63       67 / 100      81 / 93
+//   16384 x 8000 fp32    73 / 77       110 / 109     154 / 152
+//   2000 x 2000 bf16     3.6 / 6.1     7.6 / 14.0    4.7 / 7.6
+//   2000 x 8000 bf16     8.0 / 8.9     14.7 / 15.2   10.8 / 10.6
 //   100 x 500 fp32       2.1 / 2.3     4.2 / 4.6     2.9 / 2.5
 //   1 x 2000 fp32        3.1 / 2.3     6.0 / 4.2     4.4 / 2.5
 // Five CTAs of them an SM (524288 x 64 and 16384 x 8000 in bf16, forward: four 137 and 47, six 130
@@ -655,6 +655,22 @@ __device__ void select_short(const Run<T>& run, float top, int k, ShortShared& s
   if (holds >> lane & 1u) sh.columns[__popc(holds & ((1u << lane) - 1))] = lane;
   const int per = (run.chunks + 31) / 32 + 1, items = __popc(holds) * per;
   auto for_elements = [&](auto f) {
+    if (run.chunks <= 32) {  // (no lane has two: each its own, 416 us of 524288 x 64 bf16; dealt 457)
+      if (mine >= bound) {
+        if (lane < run.head + run.tail) {
+          const int e = run.loose(lane);
+          f(Logit<T>::get(run.row[e]), e);
+        }
+        if (lane < run.chunks) {
+          float x[V];
+          Logit<T>::unpack(__ldg(run.body + lane), x);
+#pragma unroll
+          for (int e = 0; e < V; ++e) f(x[e], run.begin + run.head + lane * V + e);
+        }
+      }
+      __syncwarp();
+      return;
+    }
 #pragma unroll 2
     for (int i = lane; i < items; i += 32) {
       const int column = sh.columns[i / per], n = i % per - 1;
