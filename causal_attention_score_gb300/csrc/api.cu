@@ -849,6 +849,15 @@ Range range_of(const void* p, int esize, long long span) {
 }
 bool ranges_meet(const Range& a, const Range& b) { return a.from < b.to && b.from < a.to; }
 
+// Whether a range shares bytes with rows of `row` bytes, `pitch` apart, whose range is `m`: it may
+// lie between two of them.
+bool meets_rows(const Range& a, const Range& m, uintptr_t row, uintptr_t pitch) {
+  if (!ranges_meet(a, m)) return false;
+  if (a.from < m.from) return true;
+  const uintptr_t off = (a.from - m.from) % pitch;
+  return off < row || off + (a.to - a.from) > pitch;
+}
+
 // One of two tensors of [tokens][heads][size] rows.
 struct Rows {
   const void* p;
@@ -1325,6 +1334,22 @@ csa_status token_logprobs_forward(float* logprob, float* entropy, float* stats, 
     if (!aligned(logprob, 4) || !aligned(entropy, 4) || !aligned(stats, 8) ||
         (top > 0 && (!aligned(top_logprob, 4) || !aligned(top_token, 4))))
       return set_error(CSA_ERR_ALIGN, w + ": a pointer breaks its type's alignment");
+    const int esize = dtype == CSA_F32 ? 4 : 2;
+    if (rows == 1) stride = vocab;
+    const Range in = range_of(logits, esize, span_of(rows, 1, vocab, stride, 0));
+    const Range all[] = {range_of(tokens, 4, rows),        range_of(logprob, 4, rows),
+                         range_of(entropy, 4, rows),       range_of(stats, 8, rows),
+                         range_of(top_logprob, 4, rows * top), range_of(top_token, 4, rows * top)};
+    // (the alternatives against logprob and each other: the binding's to check)
+    const int arrays = top > 0 ? 6 : 4;
+    for (int i = 1; i < arrays; ++i) {
+      bool meet = meets_rows(all[i], in, static_cast<uintptr_t>(vocab) * esize,
+                             static_cast<uintptr_t>(stride) * esize);
+      for (int j = 0; j < std::min(i, 4); ++j) meet |= !(i > 3 && j == 1) && ranges_meet(all[i], all[j]);
+      if (meet)
+        return set_error(CSA_ERR_UNSUPPORTED,
+                         w + ": outputs overlap each other, the logits or the tokens");
+    }
     return on_device(stream, [&](const DeviceInfo& dev, cudaStream_t st, std::string& err) {
       return logprobs_forward_launch({logits, dtype, stride, rows, vocab, top, tokens, scale,
                                       logprob, entropy, stats, top_logprob, top_token},
@@ -1361,6 +1386,18 @@ csa_status token_logprobs_backward(void* dlogits, const void* logits, int dtype,
     } else if (rows_meet({logits, stride, 0}, {dlogits, d_stride, 0}, rows, 1, vocab, esize)) {
       return set_error(CSA_ERR_UNSUPPORTED, w + ": logits and gradient overlap in part");
     }
+    const Range out = range_of(dlogits, esize, span_of(rows, 1, vocab, d_stride, 0));
+    const Range others[] = {range_of(tokens, 4, rows),
+                            range_of(stats, 8, rows),
+                            range_of(entropy, 4, rows),
+                            range_of(d_logprob, 4, d_logprob ? rows : 0),
+                            range_of(d_entropy, 4, d_entropy ? rows : 0),
+                            range_of(d_top, 4, with_top ? rows * top : 0),
+                            range_of(top_token, 4, with_top ? rows * top : 0)};
+    for (const Range& r : others)
+      if (meets_rows(r, out, static_cast<uintptr_t>(vocab) * esize,
+                     static_cast<uintptr_t>(d_stride) * esize))
+        return set_error(CSA_ERR_UNSUPPORTED, w + ": gradient and another input overlap");
     return on_device(stream, [&](const DeviceInfo& dev, cudaStream_t st, std::string& err) {
       return logprobs_backward_launch(
           {logits, dlogits, dtype, stride, d_stride, rows, vocab, with_top ? top : 0, tokens, scale,

@@ -47,23 +47,6 @@ def _array(t: torch.Tensor, name: str, dtype: torch.dtype, shape, dev: int) -> i
     return t.data_ptr()
 
 
-def _apart(spans) -> bool:
-    """Whether no two of ``spans`` [(begin, end)] meet."""
-    last = 0
-    for begin, end in sorted(spans):
-        if begin < last:
-            return False
-        last = end
-    return True
-
-
-def _between(spans, base: int, row: int, pitch: int, end: int) -> bool:
-    """Whether ``spans`` lie outside the rows, of ``row`` bytes and ``pitch`` apart, of a matrix in
-    [base, end): before, behind or between them."""
-    return all(z <= base or a >= end or ((a - base) % pitch >= row and (a - base) % pitch + z - a <= pitch)
-               for a, z in spans)
-
-
 def token_logprobs_forward(logprob: torch.Tensor, entropy: torch.Tensor, stats: torch.Tensor,
                            logits: torch.Tensor, tokens: torch.Tensor, scale: float = 1.0,
                            top_logprob: torch.Tensor | None = None,
@@ -87,22 +70,17 @@ def token_logprobs_forward(logprob: torch.Tensor, entropy: torch.Tensor, stats: 
     p_log = _array(logprob, "logprob", f32, (rows,), dev)
     p_ent = _array(entropy, "entropy", f32, (rows,), dev)
     p_stats = _array(stats, "stats", f32, (rows, 2), dev)
-    p_tok, p_in, n = _array(tokens, "tokens", torch.int32, (rows,), dev), logits.data_ptr(), 4 * rows
+    p_tok = _array(tokens, "tokens", torch.int32, (rows,), dev)
     p_top = p_index = None
-    spans = [(p_log, p_log + n), (p_ent, p_ent + n), (p_stats, p_stats + 2 * n)]
     if top_token is not None:
         p_top = _array(top_logprob, "top_logprob", f32, (rows, top), dev)
         p_index = _array(top_token, "top_token", torch.int32, (rows, top), dev)
-        if top:
-            spans += [(p_top, p_top + top * n), (p_index, p_index + top * n)]
-    size, one = logits.element_size(), (p_tok, p_tok + n)
-    end = p_in + ((rows - 1) * stride + vocab) * size
-    if rows and not _apart([*spans, one, (p_in, end)]) and not (
-            _apart([*spans, one]) and _between(spans, p_in, vocab * size, stride * size or 1, end)):
-        raise ValueError("the outputs must not overlap each other, the logits or the tokens")
+        n, k = 4 * rows, 4 * rows * top  # (what the library does not check)
+        if k and (-k < p_top - p_index < k or -k < p_top - p_log < n or -k < p_index - p_log < n):
+            raise ValueError("top_logprob, top_token and logprob must not overlap")
     rc = (_lib._lib or _lib.load()).token_logprobs_forward(
-        p_log, p_ent, p_stats, p_in, _DTYPE[logits.dtype], rows, vocab, stride, p_tok, scale, top,
-        p_top, p_index, _stream_ptr(stream, dev))
+        p_log, p_ent, p_stats, logits.data_ptr(), _DTYPE[logits.dtype], rows, vocab, stride, p_tok,
+        scale, top, p_top, p_index, _stream_ptr(stream, dev))
     if rc:
         _lib.check(rc, "token_logprobs_forward")
 
@@ -133,22 +111,14 @@ def token_logprobs_backward(dlogits: torch.Tensor, logits: torch.Tensor, tokens:
     def given(t, name, dtype, shape):
         return None if t is None else _array(t, name, dtype, shape, dev)
 
-    p_out, n, size = dlogits.data_ptr(), 4 * rows, logits.element_size()
-    p_tok = _array(tokens, "tokens", torch.int32, (rows,), dev)
-    p_stats = _array(stats, "stats", f32, (rows, 2), dev)
-    p_ent = _array(entropy, "entropy", f32, (rows,), dev)
-    p_dlog = given(d_logprob, "d_logprob", f32, (rows,))
-    p_dent = given(d_entropy, "d_entropy", f32, (rows,))
-    p_dtop = given(d_top, "d_top", f32, (rows, top))
-    p_index = given(top_token if d_top is not None else None, "top_token", torch.int32, (rows, top))
-    end = p_out + ((rows - 1) * d_stride + vocab) * size
-    for p, k in ((p_tok, 1), (p_stats, 2), (p_ent, 1), (p_dlog, 1), (p_dent, 1), (p_dtop, top), (p_index, top)):
-        if p and p < end and p + k * n > p_out and not _between([(p, p + k * n)], p_out, vocab * size,
-                                                                d_stride * size or 1, end):
-            raise ValueError("dlogits must not overlap the other inputs")
     rc = (_lib._lib or _lib.load()).token_logprobs_backward(
-        p_out, logits.data_ptr(), _DTYPE[logits.dtype], rows, vocab, d_stride, stride, p_tok, scale,
-        p_stats, p_ent, p_dlog, p_dent, top, p_dtop, p_index, _stream_ptr(stream, dev))
+        dlogits.data_ptr(), logits.data_ptr(), _DTYPE[logits.dtype], rows, vocab, d_stride, stride,
+        _array(tokens, "tokens", torch.int32, (rows,), dev), scale,
+        _array(stats, "stats", f32, (rows, 2), dev), _array(entropy, "entropy", f32, (rows,), dev),
+        given(d_logprob, "d_logprob", f32, (rows,)), given(d_entropy, "d_entropy", f32, (rows,)),
+        top, given(d_top, "d_top", f32, (rows, top)),
+        given(top_token if d_top is not None else None, "top_token", torch.int32, (rows, top)),
+        _stream_ptr(stream, dev))
     if rc:
         _lib.check(rc, "token_logprobs_backward")
 

@@ -18,10 +18,14 @@ class _KvPagesStruct(ctypes.Structure):
                 ("table_width", ctypes.c_int), ("page_tokens", ctypes.c_int)]
 
 
-def _meet(tensors) -> bool:
-    """Whether any of these contiguous int32 tensors share elements."""
-    spans = sorted((t.data_ptr(), t.data_ptr() + 4 * t.numel()) for t in tensors)
-    return any(a[1] > b[0] for a, b in zip(spans, spans[1:]))
+def _apart(spans) -> bool:
+    """Whether no two of ``spans`` [(begin, end)] meet."""
+    last = 0
+    for begin, end in sorted(spans):
+        if begin < last:
+            return False
+        last = end
+    return True
 
 
 class KvPages(_Marshalled):
@@ -46,7 +50,8 @@ class KvPages(_Marshalled):
         self.page_tokens = int(page_tokens)
         self._tensors = (refs, lengths, table)
         self._ptrs = [t.data_ptr() for t in self._tensors]
-        if _meet(self._tensors):
+        self._spans = [(p, p + 4 * t.numel()) for p, t in zip(self._ptrs, self._tensors)]
+        if not _apart(self._spans):
             raise ValueError("refs, lengths and table must not overlap")
         self._device = refs.get_device()
         self._struct = _KvPagesStruct(*self._ptrs, refs.numel(), S, width, self.page_tokens)
@@ -164,7 +169,7 @@ def kv_cache_compact(cache: KvCache, pages: KvPages, moves: torch.Tensor, in_use
     dev = _get_device()
     ref, books = cache._pointer(dev), pages._pointer(dev)
     m, u = _list(moves, "moves", pages.refs.numel(), dev), _list(in_use, "in_use", 1, dev)
-    if _meet((*pages._tensors, moves, in_use)):
+    if not _apart([*pages._spans, (m, m + 4 * pages.refs.numel()), (u, u + 4)]):
         raise ValueError("moves and in_use must not overlap the books or each other")
     workspace, stream = _scratch(workspace, pages, 0, stream, dev)
     rc = (_lib._lib or _lib.load()).kv_cache_compact(

@@ -696,7 +696,8 @@ csa_status kv_cache_compact(const csa_kv_cache* cache, const csa_kv_pages* pages
  * such runs, whatever the vocabulary: their roundings are below 2^-14 of them at 2^27 words). A logit of -inf is a forbidden token: p = 0, nothing added to the
  * entropy. Where every logit of a row is -inf, log p is -inf, the entropy 0 and stats (-inf, 0).
  * A NaN or +inf makes its row's logprob, entropy and top_logprob NaN; among the top tokens a NaN
- * counts as -inf. Outputs must not overlap the inputs or each other. Asynchronous on `stream`;
+ * counts as -inf. Outputs must not overlap the inputs or each other (CSA_ERR_UNSUPPORTED; that
+ * logprob and the alternatives' two are apart is not checked). Asynchronous on `stream`;
  * results do not depend on an SM limit beyond the order in which fp32 sums are taken.
  *
  * token_logprobs_backward -- the gradient of sum_r d_logprob[r] logprob[r] + d_entropy[r]
@@ -708,7 +709,7 @@ csa_status kv_cache_compact(const csa_kv_cache* cache, const csa_kv_pages* pages
  *                term; top_token is read with d_top only);
  *   dlogits      device, of the logits' type, rows d_stride apart; the logits themselves with
  *                equal strides (in place), or apart from them (CSA_ERR_UNSUPPORTED otherwise);
- *                apart from the other arrays.
+ *                apart from the other arrays (the same).
  * Every element of dlogits is written: 0 in rows left out and in rows with every logit -inf.
  * The choice of the alternatives has no gradient. Asynchronous on `stream`.
  */

@@ -1,5 +1,5 @@
-"""The binding refuses arrays that overlap where the pages and logits calls forbid it (GPU); what lies side
-by side is taken."""
+"""The pages and logits calls refuse arrays that overlap where the header forbids it (GPU); what lies side by
+side is taken."""
 import pytest
 import torch
 
@@ -28,7 +28,7 @@ def arrays():
 def test_forward(change):
     a = arrays()
     change(a)
-    with pytest.raises(ValueError, match="overlap"):
+    with pytest.raises((ValueError, csa.CsaError), match="overlap"):
         csa.token_logprobs_forward(a["logprob"], a["entropy"], a["stats"], a["logits"], a["tokens"], 1.0,
                                    a["top_logprob"], a["top_token"])
 
@@ -62,7 +62,7 @@ def test_backward():
                 dict(d_top=flat[:ROWS * TOP].view(ROWS, TOP)),
                 dict(top_token=flat[:ROWS * TOP].view(torch.int32).view(ROWS, TOP))):
         given = dict(tokens=a["tokens"], stats=f[2], entropy=f[1], d_logprob=d, d_entropy=d, d_top=f[3], top_token=f[4])
-        with pytest.raises(ValueError, match="overlap"):
+        with pytest.raises(csa.CsaError, match="overlap"):
             csa.token_logprobs_backward(dx, a["logits"], **{**given, **bad})
     csa.token_logprobs_backward(dx, a["logits"], **given)  # (two inputs that are one array are fine)
     assert csa.get_status() == 0 and bool(dx.any())
