@@ -22,7 +22,7 @@
 // masks) where the groups have rows enough, to the kernel of few rows otherwise.
 //
 // Bound: for long shared parts the tcgen05 kernel's step (1.3 us for 256 rows x 64 keys of 128
-// elements, 6.5 of 12.4 TFLOP/s an SM; 64 x 1 token over 65536 shared: 102 us, 1050 with every
+// elements, 6.5 of 12.4 TFLOP/s an SM; 64 x 1 token over 65536 shared: 106 us, 1060 with every
 // sequence reading them), for short ones the launches (17 us for 2 sequences over 1024 tokens) and
 // the own units' beginnings and ends.
 #include <cuda_runtime.h>
@@ -48,9 +48,17 @@ constexpr int kPlanGroups = 64, kPlanSequences = 256;
 // 65 and 87 here, 64 rows 89 there and 150 here; over 4 groups of 8192 32 rows take 66 there, 60 here.
 constexpr int kPrefixFrom = 33;
 // Below so many bytes of codes that it would keep from being read again (by all SMs), the shared
-// part is not worth its launches and sequences read it for themselves: with 66 MB (64 x 1 token
-// over 512) it takes 28 us with a shared part and 32 without, with 33 MB (over 256) 27 and 28, with
-// 30 MB (20 over 5008, 2 heads of 80) 28 and 25, with 16 MB (64 over 128) 27 and 25.
+// part is not worth its launches and sequences read it for themselves. us with a shared part,
+// without one in this call, and with cache_attention_forward (8 kv heads of 128 but for the last;
+// 100 own tokens each):
+//   64 x 1 token over 1024 (132 MB)  29 / -  / 34      16 x 1 over 1024 (31 MB)   21 / 27 / 17
+//   64 x 1 over 512 (66 MB)          28 / -  / 25      8 x 1 over 2048 (29 MB)    22 / 21 / 16
+//   64 x 1 over 256 (33 MB)          28 / 32 / 21      4 x 1 over 4096 (25 MB)    22 / 22 / 16
+//   64 x 1 over 192 (25 MB)          28 / 31 / 20      128 x 1 over 128 (33 MB)   33 / 35 / 26
+//   64 x 1 over 128 (17 MB)          28 / 25 / 18      20 x 1 over 5008 (30 MB)   27 / 25 / 20
+// Without one the kernel of the shared part is launched for nothing (5 us of those of 25 to 33 MB),
+// unless the host sees that the tables have no room for so much (the 25 us over 128): a bound that
+// fits both, and what the plan itself and the joining take (6 us where nothing is shared), is left.
 constexpr long long kWorthBytes = 32LL << 20;
 // Room for parts beyond one for each row and head: what cutting along the tokens may take.
 constexpr long long kSpareParts = 2LL * kMaxSms * kPrefixRows;
